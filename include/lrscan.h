@@ -71,8 +71,10 @@ enum {
     LRSCAN_ERR_ALGO = -7,      /* unknown algorithm */
     LRSCAN_ERR_CAPTURE = -8,   /* the stream is capturing a graph and its library workspace is
                                   missing or too small (see "Graph capture" above) */
-    LRSCAN_ERR_TOO_BIG = -9    /* scan_fwd_noalloc: the call needs more scratch than its static
+    LRSCAN_ERR_TOO_BIG = -9,   /* scan_fwd_noalloc: the call needs more scratch than its static
                                   buffer holds */
+    LRSCAN_ERR_ARG = -10       /* a scale, stride, tap count, activation or id size is outside
+                                  what the call takes (gated scan, convolution, embedding) */
 };
 
 /* Bytes of the static device scratch of scan_fwd_noalloc (per device). */
@@ -281,6 +283,117 @@ LRSCAN_API int scan_samu_bwd(const void* eta, const void* delta, const float* nu
 /* Bytes of caller workspace a fused-transition call needs (0 for invalid arguments). */
 LRSCAN_API size_t scan_samu_workspace_bytes(int64_t B, int64_t T, int64_t M, int dtype,
                                             const lrscan_opts* opts);
+
+/* ------------------------------------------------------------------------
+ * Gated scan: the real scan with its transition and input made in the kernels
+ * from two gates and a decay rate for each channel,
+ *   r = sigmoid(gate_r),  i = sigmoid(gate_i),
+ *   a = exp(-scale softplus(decay[d]) r),
+ *   h_t = a_t h_{t-1} + sqrt(1 - a_t^2) i_t x_t.
+ * At a reset step (opts->reset) a = 0: the state that enters it is dropped,
+ * whatever it holds (an infinity or NaN of one segment does not reach the
+ * next), and h_t = i_t x_t.  The backward is the gradient of
+ * <grad_out, out> + <grad_last, last>, with lambda_t = grad_out_t +
+ * a_{t+1} lambda_{t+1} and P_t = lambda_t a_t y_t (h_{t-1} - a_t i_t x_t / beta_t),
+ * y = log a, beta = sqrt(1 - a^2):
+ *   grad_x = lambda beta i,            grad_i = grad_x x (1 - i),
+ *   grad_r = P (1 - r),                grad_h0 = a_0 lambda_0,
+ *   grad_decay[d] = sigmoid(decay) / softplus(decay) sum_{b,t} P   (fp32);
+ * P is 0 at a reset step, and where 1 - a^2 is 0 (or below 2^-126) the term
+ * with beta takes its limit, 0.
+ *
+ * scale is finite and > 0.  `strides` (a host array, or NULL for contiguous
+ * [B, T, D]) holds two numbers for each strided operand, in elements: from one
+ * batch row to the next, and from one step to the next (the gates may be
+ * halves of one [B, T, 2 D] projection).  None is negative; an input's may be
+ * 0 (a broadcast row); rows that are written do not overlap.  out and grad_out
+ * are contiguous.
+ * opts: algo AUTO or SEQ (a per-lane walk) with chunk and width 0; h0,
+ * grad_h0, reset, polls and workspace as for the real scan.
+ * ------------------------------------------------------------------------ */
+/*   x, gate_r, gate_i [B,T,D] dtype and decay [D] fp32 read.  out [B,T,D]
+ *   (NULL: state only, then last is required) and last [B,D] fp32 written.
+ *   strides: x, gate_r, gate_i. */
+LRSCAN_API int scan_gated_fwd(const void* x, const void* gate_r, const void* gate_i,
+                              const float* decay, float scale, void* out, float* last, int64_t B,
+                              int64_t T, int64_t D, int dtype, const int64_t* strides, void* stream,
+                              const lrscan_opts* opts);
+/*   out: the forward's output.  grad_x, grad_r, grad_i [B,T,D] dtype written;
+ *   grad_decay [D] fp32 or NULL.  strides: x, gate_r, gate_i, grad_x, grad_r,
+ *   grad_i. */
+LRSCAN_API int scan_gated_bwd(const void* x, const void* gate_r, const void* gate_i,
+                              const float* decay, float scale, const void* out, const void* grad_out,
+                              const float* grad_last, void* grad_x, void* grad_r, void* grad_i,
+                              float* grad_decay, int64_t B, int64_t T, int64_t D, int dtype,
+                              const int64_t* strides, void* stream, const lrscan_opts* opts);
+/*   One step on [B, D]; state_in (NULL: zero), reset ([B] or NULL), out and
+ *   state_out (may equal state_in) as for scan_step.  strides: the batch strides
+ *   of x, gate_r and gate_i, or NULL.  Chained steps give the states of
+ *   scan_gated_fwd with LRSCAN_ALGO_SEQ bit for bit. */
+LRSCAN_API int scan_gated_step(const void* x, const void* gate_r, const void* gate_i,
+                               const float* decay, float scale, const float* state_in,
+                               const uint8_t* reset, void* out, float* state_out, int64_t B,
+                               int64_t D, int dtype, const int64_t* strides, void* stream);
+/* Bytes of caller workspace a gated call of either direction needs (0 if none,
+ * or for invalid arguments). */
+LRSCAN_API size_t scan_gated_workspace_bytes(int64_t B, int64_t T, int64_t D, int dtype,
+                                             const lrscan_opts* opts);
+
+/* ------------------------------------------------------------------------
+ * Short causal convolution over tokens, one filter of K taps (2 to 4) for each
+ * channel:
+ *   z_t = bias + sum_{j<K} weight[j] x_{t-K+1+j},
+ *   out_t = z_t (activation 0)  or  z_t sigmoid(z_t) (activation 1).
+ * Tokens before the first come from `state` [B, K-1, D] (oldest first; NULL:
+ * zeros), and a tap that would reach across a reset step counts as zero,
+ * whatever the token holds.  `last` is the state after the call: its last K-1
+ * tokens, those of an earlier segment zero.
+ * weight [K, D] and bias [D] (or NULL) are fp32; state, last and their
+ * gradients have x's type.  `strides` as for the gated scan.
+ * ------------------------------------------------------------------------ */
+/*   out [B,T,D] written, last [B,K-1,D] written or NULL.  strides: x. */
+LRSCAN_API int scan_conv_fwd(const void* x, const float* weight, const float* bias, const void* state,
+                             const uint8_t* reset, int activation, void* out, void* last, int64_t B,
+                             int64_t T, int64_t D, int64_t K, int dtype, const int64_t* strides,
+                             void* stream);
+/*   Gradients of <grad_out, out> + <grad_last, last>.  grad_last may be NULL.
+ *   grad_x [B,T,D] written; grad_weight [K,D] and grad_bias [D] fp32 and
+ *   grad_state [B,K-1,D] written unless NULL.  strides: x, grad_x.  opts: only
+ *   the workspace is used (for the parameter gradients). */
+LRSCAN_API int scan_conv_bwd(const void* x, const float* weight, const float* bias, const void* state,
+                             const uint8_t* reset, int activation, const void* grad_out,
+                             const void* grad_last, void* grad_x, float* grad_weight, float* grad_bias,
+                             void* grad_state, int64_t B, int64_t T, int64_t D, int64_t K, int dtype,
+                             const int64_t* strides, void* stream, const lrscan_opts* opts);
+/*   One token on [B, D]: state_in [B,K-1,D] (NULL: zeros) to state_out (written;
+ *   may equal state_in), reset [B] or NULL.  strides: x's batch stride, or NULL.
+ *   Chained steps give scan_conv_fwd's outputs bit for bit. */
+LRSCAN_API int scan_conv_step(const void* x, const float* weight, const float* bias, const void* state_in,
+                              const uint8_t* reset, int activation, void* out, void* state_out, int64_t B,
+                              int64_t D, int64_t K, int dtype, const int64_t* strides, void* stream);
+/* Bytes of caller workspace a backward with parameter gradients needs (0 for
+ * invalid arguments). */
+LRSCAN_API size_t scan_conv_workspace_bytes(int64_t B, int64_t T, int64_t D, int64_t K, int dtype);
+
+/* ------------------------------------------------------------------------
+ * Embedding lookup with scaling, out[n] = scale weight[ids[n]], and its gradient
+ * grad_weight[v] = scale sum_{n: ids[n] = v} grad_out[n].  An id outside [0, V)
+ * names no row: the lookup gives zeros for it and the gradient leaves it out.
+ * ids: N whole numbers of id_bytes (4 or 8).  weight [V, D], out and grad_out
+ * [N, D] of `dtype`, contiguous.  scale is finite.
+ * ------------------------------------------------------------------------ */
+LRSCAN_API int scan_embed_fwd(const void* ids, int id_bytes, const void* weight, float scale, void* out,
+                              int64_t N, int64_t V, int64_t D, int dtype, void* stream);
+/*   grad_weight [V, D] of grad_dtype (`dtype`, or LRSCAN_F32 for either): every
+ *   row is written (zeros where no token names it), or with accumulate != 0
+ *   rows that tokens name are added to and the others not touched.  A row's
+ *   tokens are added in the order that N, V and ids alone fix, in fp32, and
+ *   rounded once.  opts: only the workspace is used. */
+LRSCAN_API int scan_embed_bwd(const void* ids, int id_bytes, const void* grad_out, float scale,
+                              void* grad_weight, int grad_dtype, int accumulate, int64_t N, int64_t V,
+                              int64_t D, int dtype, void* stream, const lrscan_opts* opts);
+/* Bytes of caller workspace the gradient needs (0 for invalid arguments). */
+LRSCAN_API size_t scan_embed_workspace_bytes(int64_t N, int64_t V, int64_t D, int dtype);
 
 /* Bytes of workspace the call with these arguments needs (0 if none).
  * Returns 0 for invalid arguments. */

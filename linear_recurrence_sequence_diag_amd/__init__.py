@@ -26,7 +26,7 @@ ALGOS = {"auto": ALGO_AUTO, "seq": ALGO_SEQ, "chunked": ALGO_CHUNKED, "fused": A
 STATUS = {
     0: "LRSCAN_OK", -1: "LRSCAN_ERR_NULL", -2: "LRSCAN_ERR_DIM", -3: "LRSCAN_ERR_DTYPE",
     -4: "LRSCAN_ERR_CHUNK", -5: "LRSCAN_ERR_WORKSPACE", -6: "LRSCAN_ERR_HIP", -7: "LRSCAN_ERR_ALGO",
-    -8: "LRSCAN_ERR_CAPTURE", -9: "LRSCAN_ERR_TOO_BIG",
+    -8: "LRSCAN_ERR_CAPTURE", -9: "LRSCAN_ERR_TOO_BIG", -10: "LRSCAN_ERR_ARG",
 }
 
 
@@ -54,6 +54,7 @@ class Opts(ctypes.Structure):
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _INT = ctypes.c_int
+_F32 = ctypes.c_float
 _SIGS = {
     "scan_fwd": ([_P, _P, _P, _P, _I64, _I64, _I64, _INT, _P], _INT),
     "scan_bwd": ([_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _INT, _P], _INT),
@@ -71,6 +72,22 @@ _SIGS = {
                                   ctypes.c_size_t),
     "scan_complex_workspace_bytes": ([_I64, _I64, _I64, _INT, ctypes.POINTER(Opts)],
                                      ctypes.c_size_t),
+    "scan_gated_fwd": ([_P] * 4 + [_F32, _P, _P, _I64, _I64, _I64, _INT, _P, _P,
+                                   ctypes.POINTER(Opts)], _INT),
+    "scan_gated_bwd": ([_P] * 4 + [_F32] + [_P] * 7 + [_I64, _I64, _I64, _INT, _P, _P,
+                                                       ctypes.POINTER(Opts)], _INT),
+    "scan_gated_step": ([_P] * 4 + [_F32] + [_P] * 4 + [_I64, _I64, _INT, _P, _P], _INT),
+    "scan_gated_workspace_bytes": ([_I64, _I64, _I64, _INT, ctypes.POINTER(Opts)],
+                                   ctypes.c_size_t),
+    "scan_conv_fwd": ([_P] * 5 + [_INT, _P, _P, _I64, _I64, _I64, _I64, _INT, _P, _P], _INT),
+    "scan_conv_bwd": ([_P] * 5 + [_INT] + [_P] * 6 + [_I64, _I64, _I64, _I64, _INT, _P, _P,
+                                                      ctypes.POINTER(Opts)], _INT),
+    "scan_conv_step": ([_P] * 5 + [_INT, _P, _P, _I64, _I64, _I64, _INT, _P, _P], _INT),
+    "scan_conv_workspace_bytes": ([_I64, _I64, _I64, _I64, _INT], ctypes.c_size_t),
+    "scan_embed_fwd": ([_P, _INT, _P, _F32, _P, _I64, _I64, _I64, _INT, _P], _INT),
+    "scan_embed_bwd": ([_P, _INT, _P, _F32, _P, _INT, _INT, _I64, _I64, _I64, _INT, _P,
+                        ctypes.POINTER(Opts)], _INT),
+    "scan_embed_workspace_bytes": ([_I64, _I64, _I64, _INT], ctypes.c_size_t),
     "scan_auto_algo": ([_I64, _I64, _I64, _INT, _INT, ctypes.POINTER(_INT), ctypes.POINTER(_INT)],
                        _INT),
     "scan_chunk_summary": ([_P, _P, _P, _P, _I64, _I64, _I64, _INT, _INT, _P], _INT),
@@ -247,6 +264,83 @@ def scan_reverse_chunk_replay(a, out, grad_out, future, h0, grad_a, grad_b, B, T
     return _check(library().scan_reverse_chunk_replay(a, out, grad_out, future, h0, grad_a, grad_b,
                                                       B, T, D, chunk, dtype, stream),
                   "scan_reverse_chunk_replay")
+
+
+def _opts(opts):
+    return ctypes.byref(opts) if opts is not None else None
+
+
+def _i64s(values):
+    """A host array of int64 (None: NULL)."""
+    return None if values is None else (_I64 * len(values))(*values)
+
+
+def scan_gated_fwd(x, gate_r, gate_i, decay, scale, out, last, B, T, D, dtype, strides, stream,
+                   opts):
+    return _check(library().scan_gated_fwd(x, gate_r, gate_i, decay, scale, out, last, B, T, D,
+                                           dtype, _i64s(strides), stream, _opts(opts)),
+                  "scan_gated_fwd")
+
+
+def scan_gated_bwd(x, gate_r, gate_i, decay, scale, out, grad_out, grad_last, grad_x, grad_r,
+                   grad_i, grad_decay, B, T, D, dtype, strides, stream, opts):
+    return _check(library().scan_gated_bwd(x, gate_r, gate_i, decay, scale, out, grad_out,
+                                           grad_last, grad_x, grad_r, grad_i, grad_decay, B, T, D,
+                                           dtype, _i64s(strides), stream, _opts(opts)),
+                  "scan_gated_bwd")
+
+
+def scan_gated_step(x, gate_r, gate_i, decay, scale, state_in, reset, out, state_out, B, D, dtype,
+                    strides, stream):
+    return _check(library().scan_gated_step(x, gate_r, gate_i, decay, scale, state_in, reset, out,
+                                            state_out, B, D, dtype, _i64s(strides), stream),
+                  "scan_gated_step")
+
+
+def scan_gated_workspace_bytes(B, T, D, dtype, opts=None):
+    return library().scan_gated_workspace_bytes(B, T, D, dtype, _opts(opts))
+
+
+def scan_conv_fwd(x, weight, bias, state, reset, activation, out, last, B, T, D, K, dtype, strides,
+                  stream):
+    return _check(library().scan_conv_fwd(x, weight, bias, state, reset, activation, out, last, B,
+                                          T, D, K, dtype, _i64s(strides), stream),
+                  "scan_conv_fwd")
+
+
+def scan_conv_bwd(x, weight, bias, state, reset, activation, grad_out, grad_last, grad_x,
+                  grad_weight, grad_bias, grad_state, B, T, D, K, dtype, strides, stream, opts):
+    return _check(library().scan_conv_bwd(x, weight, bias, state, reset, activation, grad_out,
+                                          grad_last, grad_x, grad_weight, grad_bias, grad_state, B,
+                                          T, D, K, dtype, _i64s(strides), stream, _opts(opts)),
+                  "scan_conv_bwd")
+
+
+def scan_conv_step(x, weight, bias, state_in, reset, activation, out, state_out, B, D, K, dtype,
+                   strides, stream):
+    return _check(library().scan_conv_step(x, weight, bias, state_in, reset, activation, out,
+                                           state_out, B, D, K, dtype, _i64s(strides), stream),
+                  "scan_conv_step")
+
+
+def scan_conv_workspace_bytes(B, T, D, K, dtype):
+    return library().scan_conv_workspace_bytes(B, T, D, K, dtype)
+
+
+def scan_embed_fwd(ids, id_bytes, weight, scale, out, N, V, D, dtype, stream):
+    return _check(library().scan_embed_fwd(ids, id_bytes, weight, scale, out, N, V, D, dtype,
+                                           stream), "scan_embed_fwd")
+
+
+def scan_embed_bwd(ids, id_bytes, grad_out, scale, grad_weight, grad_dtype, accumulate, N, V, D,
+                   dtype, stream, opts):
+    return _check(library().scan_embed_bwd(ids, id_bytes, grad_out, scale, grad_weight, grad_dtype,
+                                           accumulate, N, V, D, dtype, stream, _opts(opts)),
+                  "scan_embed_bwd")
+
+
+def scan_embed_workspace_bytes(N, V, D, dtype):
+    return library().scan_embed_workspace_bytes(N, V, D, dtype)
 
 
 # ---------------------------------------------------------------------------
@@ -533,6 +627,293 @@ def samu_scan_backward(eta, delta, nu_log, theta_log, out_r, out_i, grad_out_r, 
     return ge, gd, gn, gt, gbr, gbi, gh0
 
 
+# ---- gated scan, short causal convolution, embedding ----
+def _check_rows(name, t, ref, dims):
+    """An operand whose rows may be strided: contiguous along the last dimension."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA (HIP) tensor")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must be [{'B, T, D' if dims == 3 else 'B, D'}]")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous along its last dimension")
+    if t is not ref and (t.shape != ref.shape or t.dtype != ref.dtype or t.device != ref.device):
+        raise ValueError(f"{name} must match x in shape, dtype and device")
+
+
+def _strides(*tensors):
+    """(batch, step) strides of [B, T, D] tensors, or batch strides of [B, D]
+    ones, for the C ABI; a dimension of one takes the contiguous value (torch
+    leaves it arbitrary)."""
+    out = []
+    for t in tensors:
+        width = t.shape[-1]
+        if t.dim() == 2:
+            out.append(t.stride(0) if t.shape[0] > 1 else width)
+            continue
+        out.append(t.stride(0) if t.shape[0] > 1 else t.shape[1] * width)
+        out.append(t.stride(1) if t.shape[1] > 1 else width)
+    return out
+
+
+def _check_param(name, t, shape, ref):
+    """A float32 parameter on x's device."""
+    torch = _torch()
+    if (not isinstance(t, torch.Tensor) or tuple(t.shape) != tuple(shape)
+            or t.dtype != torch.float32 or t.device != ref.device or not t.is_contiguous()):
+        dims = ", ".join(str(n) for n in shape)
+        raise ValueError(f"{name} must be a contiguous float32 [{dims}] tensor on x's device")
+
+
+def _check_step_mask(reset, ref):
+    torch = _torch()
+    if reset is not None and (reset.shape != ref.shape[:1]
+                              or reset.dtype not in (torch.bool, torch.uint8)
+                              or reset.device != ref.device or not reset.is_contiguous()):
+        raise ValueError("reset must be a contiguous bool or uint8 [B] tensor on x's device")
+
+
+def gated_scan(x, gate_r, gate_i, decay, scale=8.0, h0=None, reset=None, algo="auto",
+               with_last=True, with_out=True, polls=0, workspace=None):
+    """Gated scan h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(gate_i) x_t with
+    a_t = exp(-scale softplus(decay) sigmoid(gate_r)).  x, gate_r, gate_i:
+    [B, T, D], contiguous along D (the gates may be halves of one projection);
+    decay: float32 [D]; ``reset`` ([B, T] bool/uint8) starts segments.
+    Returns (out, last); parts not asked for are None."""
+    torch = _torch()
+    _check_rows("x", x, x, 3)
+    _check_rows("gate_r", gate_r, x, 3)
+    _check_rows("gate_i", gate_i, x, 3)
+    B, T, D = x.shape
+    _check_param("decay", decay, (D,), x)
+    _check_mask(reset, x)
+    _check_state("h0", h0, x)
+    if not (with_out or with_last):
+        raise ValueError("a forward needs out or last")
+    out = torch.empty((B, T, D), device=x.device, dtype=x.dtype) if with_out else None
+    last = torch.empty((B, D), device=x.device, dtype=torch.float32) if with_last else None
+    with torch.cuda.device(x.device):
+        scan_gated_fwd(x.data_ptr(), gate_r.data_ptr(), gate_i.data_ptr(), decay.data_ptr(), scale,
+                       _ptr(out), _ptr(last), B, T, D, dtype_code(x.dtype),
+                       _strides(x, gate_r, gate_i), _stream(x),
+                       make_opts(algo, h0=h0, reset=reset, polls=polls, workspace=workspace))
+    return out, last
+
+
+def gated_scan_backward(x, gate_r, gate_i, decay, out, grad_out, scale=8.0, grad_last=None,
+                        h0=None, need_grad_h0=False, reset=None, algo="auto", polls=0,
+                        workspace=None, grads=None):
+    """Adjoint of gated_scan.  Returns (grad_x, grad_r, grad_i, grad_decay, grad_h0
+    or None); grad_decay is float32 [D].  ``grads``: a triple of tensors like x,
+    contiguous along D, that receive the first three (so that the gates'
+    gradients can be halves of one projection's)."""
+    torch = _torch()
+    _check_rows("x", x, x, 3)
+    _check_rows("gate_r", gate_r, x, 3)
+    _check_rows("gate_i", gate_i, x, 3)
+    B, T, D = x.shape
+    _check_param("decay", decay, (D,), x)
+    for name, t in (("out", out), ("grad_out", grad_out)):
+        _check_rows(name, t, x, 3)
+        _check_seq(name, t)
+    _check_mask(reset, x)
+    _check_state("grad_last", grad_last, x)
+    _check_state("h0", h0, x)
+    if grads is None:
+        grads = [torch.empty((B, T, D), device=x.device, dtype=x.dtype) for _ in range(3)]
+    for name, t in zip(("grad_x", "grad_r", "grad_i"), grads):
+        _check_rows(name, t, x, 3)
+    gx, gr, gi = grads
+    gd = torch.empty((D,), device=x.device, dtype=torch.float32)
+    gh0 = torch.empty((B, D), device=x.device, dtype=torch.float32) if need_grad_h0 else None
+    with torch.cuda.device(x.device):
+        scan_gated_bwd(x.data_ptr(), gate_r.data_ptr(), gate_i.data_ptr(), decay.data_ptr(), scale,
+                       out.data_ptr(), grad_out.data_ptr(), _ptr(grad_last), gx.data_ptr(),
+                       gr.data_ptr(), gi.data_ptr(), gd.data_ptr(), B, T, D, dtype_code(x.dtype),
+                       _strides(x, gate_r, gate_i, gx, gr, gi), _stream(x),
+                       make_opts(algo, h0=h0, grad_h0=gh0, reset=reset, polls=polls,
+                                 workspace=workspace))
+    return gx, gr, gi, gd, gh0
+
+
+def gated_step(x, gate_r, gate_i, decay, state=None, scale=8.0, reset=None, with_out=True,
+               out_state=None):
+    """One decoding step of gated_scan on [B, D] from a float32 state (None:
+    zero; rows with reset set start anew).  Returns (out in x's dtype or None,
+    the new float32 state).  ``out_state`` may be ``state`` (in place)."""
+    torch = _torch()
+    _check_rows("x", x, x, 2)
+    _check_rows("gate_r", gate_r, x, 2)
+    _check_rows("gate_i", gate_i, x, 2)
+    B, D = x.shape
+    _check_param("decay", decay, (D,), x)
+    for name, t in (("state", state), ("out_state", out_state)):
+        if t is not None:
+            _check_param(name, t, (B, D), x)
+    _check_step_mask(reset, x)
+    out = torch.empty((B, D), device=x.device, dtype=x.dtype) if with_out else None
+    new = out_state if out_state is not None else torch.empty((B, D), device=x.device,
+                                                              dtype=torch.float32)
+    with torch.cuda.device(x.device):
+        scan_gated_step(x.data_ptr(), gate_r.data_ptr(), gate_i.data_ptr(), decay.data_ptr(), scale,
+                        _ptr(state), _ptr(reset), _ptr(out), new.data_ptr(), B, D,
+                        dtype_code(x.dtype), _strides(x, gate_r, gate_i), _stream(x))
+    return out, new
+
+
+ACTIVATIONS = {None: 0, "silu": 1}
+
+
+def _activation(name):
+    if name not in ACTIVATIONS:
+        raise ValueError(f"activation must be None or 'silu', not {name!r}")
+    return ACTIVATIONS[name]
+
+
+def _check_conv(x, weight, bias, dims):
+    torch = _torch()
+    _check_rows("x", x, x, dims)
+    D = x.shape[-1]
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("weight must be [K, D]")
+    _check_param("weight", weight, (weight.shape[0], D), x)
+    if bias is not None:
+        _check_param("bias", bias, (D,), x)
+    return weight.shape[0]
+
+
+def _check_taps_state(name, t, x, K):
+    torch = _torch()
+    if t is None:
+        return
+    if (not isinstance(t, torch.Tensor) or t.shape != (x.shape[0], K - 1, x.shape[-1])
+            or t.dtype != x.dtype or t.device != x.device or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous [B, K - 1, D] tensor of x's dtype and device")
+
+
+def short_conv(x, weight, bias=None, state=None, reset=None, activation=None, with_last=True):
+    """Causal convolution over tokens, one filter a channel: z_t = bias +
+    sum_j weight[j] x_{t-K+1+j}; activation None or "silu" (z sigmoid(z)).
+    x: [B, T, D], contiguous along D; weight: float32 [K, D], K = 2 .. 4, the
+    last tap the current token's; bias: float32 [D] or None; ``state``
+    [B, K-1, D]: the tokens before the first (None: zeros); no tap reaches
+    across a ``reset`` ([B, T] bool/uint8).  Returns (out, last): ``last`` is
+    the state to go on from, or None."""
+    torch = _torch()
+    K = _check_conv(x, weight, bias, 3)
+    B, T, D = x.shape
+    _check_taps_state("state", state, x, K)
+    _check_mask(reset, x)
+    out = torch.empty((B, T, D), device=x.device, dtype=x.dtype)
+    last = (torch.empty((B, max(K - 1, 0), D), device=x.device, dtype=x.dtype) if with_last
+            else None)
+    with torch.cuda.device(x.device):
+        scan_conv_fwd(x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(state), _ptr(reset),
+                      _activation(activation), out.data_ptr(), _ptr(last), B, T, D, K,
+                      dtype_code(x.dtype), _strides(x), _stream(x))
+    return out, last
+
+
+def short_conv_backward(x, weight, bias, grad_out, state=None, grad_last=None, reset=None,
+                        activation=None, need_grad_state=False, workspace=None, grad_x=None):
+    """Adjoint of short_conv.  Returns (grad_x, grad_weight, grad_bias, grad_state or
+    None); grad_weight [K, D] and grad_bias [D] are float32 (grad_bias is None
+    where bias is).  ``grad_x``: a tensor like x that receives it."""
+    torch = _torch()
+    K = _check_conv(x, weight, bias, 3)
+    B, T, D = x.shape
+    _check_rows("grad_out", grad_out, x, 3)
+    _check_seq("grad_out", grad_out)
+    _check_taps_state("state", state, x, K)
+    _check_taps_state("grad_last", grad_last, x, K)
+    _check_mask(reset, x)
+    gx = grad_x if grad_x is not None else torch.empty((B, T, D), device=x.device, dtype=x.dtype)
+    _check_rows("grad_x", gx, x, 3)
+    gw = torch.empty_like(weight)
+    gb = torch.empty_like(bias) if bias is not None else None
+    gs = (torch.empty((B, max(K - 1, 0), D), device=x.device, dtype=x.dtype) if need_grad_state
+          else None)
+    opts = make_opts(workspace=workspace)
+    with torch.cuda.device(x.device):
+        scan_conv_bwd(x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(state), _ptr(reset),
+                      _activation(activation), grad_out.data_ptr(), _ptr(grad_last), gx.data_ptr(),
+                      gw.data_ptr(), _ptr(gb), _ptr(gs), B, T, D, K, dtype_code(x.dtype),
+                      _strides(x, gx), _stream(x), opts)
+    return gx, gw, gb, gs
+
+
+def short_conv_step(x, weight, bias=None, state=None, reset=None, activation=None,
+                    out_state=None):
+    """One decoding step of short_conv on [B, D].  Returns (out, the new state
+    [B, K-1, D]); ``out_state`` may be ``state`` (in place)."""
+    torch = _torch()
+    K = _check_conv(x, weight, bias, 2)
+    B, D = x.shape
+    _check_taps_state("state", state, x, K)
+    _check_taps_state("out_state", out_state, x, K)
+    _check_step_mask(reset, x)
+    out = torch.empty((B, D), device=x.device, dtype=x.dtype)
+    new = (out_state if out_state is not None
+           else torch.empty((B, max(K - 1, 0), D), device=x.device, dtype=x.dtype))
+    with torch.cuda.device(x.device):
+        scan_conv_step(x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(state), _ptr(reset),
+                       _activation(activation), out.data_ptr(), new.data_ptr(), B, D, K,
+                       dtype_code(x.dtype), _strides(x), _stream(x))
+    return out, new
+
+
+def _check_ids(ids, ref):
+    torch = _torch()
+    if (not isinstance(ids, torch.Tensor) or ids.dtype not in (torch.int32, torch.int64)
+            or ids.device != ref.device or not ids.is_contiguous()):
+        raise ValueError("ids must be a contiguous int32 or int64 tensor on the same device")
+    return 4 if ids.dtype == torch.int32 else 8
+
+
+def embed(ids, weight, scale=1.0):
+    """Rows ``scale * weight[ids]`` of a [V, D] table, shaped ids.shape + [D];
+    zeros for an id outside [0, V)."""
+    torch = _torch()
+    if (not isinstance(weight, torch.Tensor) or not weight.is_cuda or weight.dim() != 2
+            or not weight.is_contiguous()):
+        raise ValueError("weight must be a contiguous CUDA (HIP) [V, D] tensor")
+    id_bytes = _check_ids(ids, weight)
+    V, D = weight.shape
+    out = torch.empty((*ids.shape, D), device=weight.device, dtype=weight.dtype)
+    with torch.cuda.device(weight.device):
+        scan_embed_fwd(ids.data_ptr(), id_bytes, weight.data_ptr(), scale, out.data_ptr(),
+                       ids.numel(), V, D, dtype_code(weight.dtype), _stream(weight))
+    return out
+
+
+def embed_backward(ids, grad_out, rows, scale=1.0, grad_weight=None, workspace=None):
+    """Gradient of ``embed`` for its table of ``rows`` rows: [rows, D] in
+    grad_out's dtype, each row the fp32 sum of its tokens' gradients in a
+    fixed order.  ``grad_weight`` (that shape; grad_out's dtype or float32):
+    the sums are added to it instead, and it is returned."""
+    torch = _torch()
+    if (not isinstance(grad_out, torch.Tensor) or not grad_out.is_cuda or grad_out.dim() < 1
+            or not grad_out.is_contiguous() or not isinstance(ids, torch.Tensor)
+            or grad_out.shape[:-1] != ids.shape):
+        raise ValueError("grad_out must be a contiguous CUDA (HIP) tensor of shape ids.shape + [D]")
+    id_bytes = _check_ids(ids, grad_out)
+    D = grad_out.shape[-1]
+    add = grad_weight is not None
+    if add and (grad_weight.shape != (rows, D) or grad_weight.device != grad_out.device
+                or grad_weight.dtype not in (grad_out.dtype, torch.float32)
+                or not grad_weight.is_contiguous()):
+        raise ValueError("grad_weight must be a contiguous [rows, D] tensor of grad_out's dtype or "
+                         "float32 on its device")
+    gw = grad_weight if add else torch.empty((rows, D), device=grad_out.device,
+                                             dtype=grad_out.dtype)
+    with torch.cuda.device(grad_out.device):
+        scan_embed_bwd(ids.data_ptr(), id_bytes, grad_out.data_ptr(), scale, gw.data_ptr(),
+                       dtype_code(gw.dtype), int(add), ids.numel(), rows, D,
+                       dtype_code(grad_out.dtype), _stream(grad_out),
+                       make_opts(workspace=workspace))
+    return gw
+
+
 def n_chunks(T, chunk):
     return (T + chunk - 1) // chunk
 
@@ -683,3 +1064,88 @@ def complex_diagonal_scan(ar, ai, br, bi, reset=None):
 def samu_diagonal_scan(eta, delta, nu_log, theta_log, br, bi, reset=None):
     """Differentiable fused-transition scan (torch autograd); returns (out_r, out_i)."""
     return _function("samu").apply(reset, eta, delta, nu_log, theta_log, br, bi)
+
+
+def _rows_contiguous(t):
+    """``t`` as the strided operands take it."""
+    return t if t.shape[-1] <= 1 or t.stride(-1) == 1 else t.contiguous()
+
+
+_model_functions = {}
+
+
+def _model_function(name):
+    """The torch.autograd.Function of one of the operators below (made once;
+    torch is imported on the first use)."""
+    if name in _model_functions:
+        return _model_functions[name]
+    torch = _torch()
+
+    class GatedScanFunction(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, gate_r, gate_i, decay, scale, reset):
+            x, gate_r, gate_i = (_rows_contiguous(t) for t in (x, gate_r, gate_i))
+            decay = decay.contiguous()
+            out, _ = gated_scan(x, gate_r, gate_i, decay, scale, reset=reset, with_last=False)
+            ctx.save_for_backward(x, gate_r, gate_i, decay, out)
+            ctx.scale, ctx.reset = scale, reset
+            return out
+
+        @staticmethod
+        def backward(ctx, grad):
+            x, gate_r, gate_i, decay, out = ctx.saved_tensors
+            gx, gr, gi, gd, _ = gated_scan_backward(x, gate_r, gate_i, decay, out,
+                                                    grad.contiguous(), ctx.scale,
+                                                    reset=ctx.reset)
+            return gx, gr, gi, gd, None, None
+
+    class ShortConvFunction(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, weight, bias, reset, activation):
+            x, weight = _rows_contiguous(x), weight.contiguous()
+            bias = None if bias is None else bias.contiguous()
+            out, _ = short_conv(x, weight, bias, reset=reset, activation=activation,
+                                with_last=False)
+            ctx.save_for_backward(x, weight, bias)
+            ctx.reset, ctx.activation = reset, activation
+            return out
+
+        @staticmethod
+        def backward(ctx, grad):
+            x, weight, bias = ctx.saved_tensors
+            gx, gw, gb, _ = short_conv_backward(x, weight, bias, grad.contiguous(),
+                                                reset=ctx.reset, activation=ctx.activation)
+            return gx, gw, gb, None, None
+
+    class EmbeddingFunction(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, ids, weight, scale):
+            ids = ids.contiguous()
+            ctx.save_for_backward(ids)
+            ctx.rows, ctx.scale = weight.shape[0], scale
+            return embed(ids, weight.contiguous(), scale)
+
+        @staticmethod
+        def backward(ctx, grad):
+            ids, = ctx.saved_tensors
+            return None, embed_backward(ids, grad.contiguous(), ctx.rows, ctx.scale), None
+
+    _model_functions.update(gated=GatedScanFunction, conv=ShortConvFunction,
+                            embedding=EmbeddingFunction)
+    return _model_functions[name]
+
+
+def gated_diagonal_scan(x, gate_r, gate_i, decay, scale=8.0, reset=None):
+    """Differentiable gated scan (torch autograd) returning every state; ``reset``
+    ([B, T] bool/uint8, not differentiated) starts new segments."""
+    return _model_function("gated").apply(x, gate_r, gate_i, decay, scale, reset)
+
+
+def short_convolution(x, weight, bias=None, reset=None, activation=None):
+    """Differentiable short_conv (torch autograd) from a zero state."""
+    return _model_function("conv").apply(x, weight, bias, reset, activation)
+
+
+def embedding(ids, weight, scale=1.0):
+    """Differentiable embed (torch autograd); the gradient is a dense [V, D] table."""
+    return _model_function("embedding").apply(ids, weight, scale)

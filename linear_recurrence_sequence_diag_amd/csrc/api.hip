@@ -3,6 +3,7 @@
 // the kernel launchers.  No torch type crosses this boundary.
 #include <hip/hip_runtime.h>
 
+#include <cmath>
 #include <map>
 #include <mutex>
 #include <tuple>
@@ -10,7 +11,10 @@
 #include <vector>
 
 #include "../../include/lrscan.h"
+#include "conv.hpp"
 #include "device.hpp"
+#include "embed.hpp"
+#include "gated.hpp"
 #include "launch.hpp"
 
 using namespace lrscan;
@@ -37,8 +41,10 @@ size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 // ---- library-owned workspaces, one per (device, stream, kind) ----------------
 // Kind 0 holds the chunked form's P, Q and entering states; kind 1 holds the
 // fused form's self-cleaning scratch, which must not be shared with anything
-// else and is initialised once per allocation; kind 2 holds the
-// fused-transition scan's factor tables and partial sums.
+// else and is initialised once per allocation; kind 2 holds what a call
+// rewrites before it reads it: the fused-transition scan's factor tables and
+// partial sums, the partial sums of the gated scan and of the convolution, and
+// the sorted tokens of the embedding's gradient.
 //
 // Graph capture.  A call captured into a HIP graph bakes the workspace
 // address into the graph's kernel arguments, and every replay uses it.  So
@@ -403,6 +409,83 @@ int samu_workspace(const Shape& s, const lrscan_opts* o, hipStream_t st, Workspa
     return LRSCAN_OK;
 }
 
+// ---- gated scan, convolution and embedding helpers ----
+
+int64_t elem_bytes(int dtype) { return dtype == LRSCAN_F32 ? 4 : 2; }
+
+// Operand `i` of a call: its strides (elements; batch row, step) from the
+// caller's table, or those of contiguous [B, T, D].
+Rows rows_of(const void* p, const int64_t* strides, int i, int64_t T, int64_t D, int dtype) {
+    const int64_t sb = strides ? strides[2 * i] : T * D;
+    const int64_t st = strides ? strides[2 * i + 1] : D;
+    return Rows{static_cast<char*>(const_cast<void*>(p)), (size_t)(sb * elem_bytes(dtype)),
+                (size_t)(st * elem_bytes(dtype))};
+}
+
+// Strides of `n` operands: none negative, and every row within a size that
+// keeps byte offsets exact.
+bool strides_ok(const int64_t* strides, int n, int64_t B, int64_t T) {
+    if (!strides) return true;
+    for (int i = 0; i < n; ++i) {
+        const int64_t sb = strides[2 * i], st = strides[2 * i + 1];
+        if (sb < 0 || st < 0 || sb > kMaxElems || st > kMaxElems) return false;
+        if ((B > 1 && sb > 4 * kMaxElems / B) || (T > 1 && st > 4 * kMaxElems / T)) return false;
+    }
+    return true;
+}
+
+// Rows that are written must not overlap.
+bool written_rows_ok(const int64_t* strides, int i, int64_t B, int64_t T, int64_t D) {
+    if (!strides) return true;
+    const int64_t sb = strides[2 * i], st = strides[2 * i + 1];
+    if (T > 1 && st < D) return false;
+    if (B == 1) return true;
+    if (T == 1) return sb >= D;
+    return sb >= (T - 1) * st + D || (sb >= D && st >= (B - 1) * sb + D);
+}
+
+// The part of a call's scratch that lives in a kind-2 buffer: the caller's
+// workspace, or the library's.
+int plain_workspace(size_t need, const lrscan_opts* o, hipStream_t st, void** out) {
+    *out = nullptr;
+    if (need == 0) return LRSCAN_OK;
+    if (o && o->workspace) {
+        if (o->workspace_bytes < need) return LRSCAN_ERR_WORKSPACE;
+        if (reinterpret_cast<uintptr_t>(o->workspace) % 256 != 0) return LRSCAN_ERR_WORKSPACE;
+        *out = o->workspace;
+        return LRSCAN_OK;
+    }
+    Workspace w;
+    const int rc = library_workspace(need, 2, st, &w);
+    *out = w.ptr;
+    return rc;
+}
+
+bool scale_ok(float scale) { return std::isfinite(scale) && scale > 0.0f; }
+
+// AUTO or SEQ.
+int gated_algo(const GatedShape& s, const lrscan_opts* o, int* algo) {
+    const int a = o ? o->algo : LRSCAN_ALGO_AUTO;
+    if (a != LRSCAN_ALGO_AUTO && a != LRSCAN_ALGO_SEQ) return LRSCAN_ERR_ALGO;
+    if (o && (o->chunk != 0 || o->width != 0)) return LRSCAN_ERR_CHUNK;
+    *algo = LRSCAN_ALGO_SEQ;
+    return gated_walk_fits(s) ? LRSCAN_OK : LRSCAN_ERR_DIM;
+}
+
+// Rows of partial sums of the decay gradient, and the bytes of them and of
+// their reduction's scratch.
+int64_t gated_part_rows(const GatedShape& s) { return s.B; }
+size_t gated_sum_bytes(const GatedShape& s) {
+    const int64_t rows = gated_part_rows(s);
+    return align_up((size_t)rows * (size_t)s.D * 4, 256) + gated_decay_scratch(rows, s.D);
+}
+
+bool conv_args_ok(int64_t K, int activation) {
+    return K >= kMinTaps && K <= kMaxTaps && (activation == 0 || activation == 1);
+}
+
+size_t conv_bytes(const ConvShape& s) { return align_up(conv_part_bytes(s), 256) + conv_sum_scratch(s); }
+
 // ---- the forward, shared by scan_fwd_ex and scan_fwd_noalloc ----
 
 struct FwdCall {
@@ -499,6 +582,8 @@ LRSCAN_API const char* scan_status_string(int status) {
         case LRSCAN_ERR_TOO_BIG:
             return "the call needs more scratch than the static buffer of scan_fwd_noalloc "
                    "(LRSCAN_NOALLOC_SCRATCH_BYTES) holds";
+        case LRSCAN_ERR_ARG:
+            return "a scale, stride, tap count, activation or id size is outside what the call takes";
         case LRSCAN_ERR_CAPTURE:
             return "the stream is capturing a graph and has no library workspace of this size yet "
                    "(make one eager call of at least this size on the stream first, or pass "
@@ -784,6 +869,187 @@ LRSCAN_API size_t scan_samu_workspace_bytes(int64_t B, int64_t T, int64_t M, int
     // the walk uses the same buffer (its tables and partial sums in the part
     // after the fused scratch), so the need is the same for every algorithm
     return samu_supported(s) ? samu_need(s) : 0;
+}
+
+// ---- gated scan -----------------------------------------------------------------------
+
+LRSCAN_API int scan_gated_fwd(const void* x, const void* gate_r, const void* gate_i,
+                              const float* decay, float scale, void* out, float* last, int64_t B,
+                              int64_t T, int64_t D, int dtype, const int64_t* strides, void* stream,
+                              const lrscan_opts* opts) {
+    if (!x || !gate_r || !gate_i || !decay || (!out && !last)) return LRSCAN_ERR_NULL;
+    if (!dims_ok(B, T, D)) return LRSCAN_ERR_DIM;
+    if (!dtype_ok(dtype)) return LRSCAN_ERR_DTYPE;
+    if (!scale_ok(scale) || !strides_ok(strides, 3, B, T)) return LRSCAN_ERR_ARG;
+    const GatedShape s{B, T, D, dtype};
+    int algo = 0;
+    const int rc = gated_algo(s, opts, &algo);
+    if (rc != LRSCAN_OK) return rc;
+    const GatedFwd p{rows_of(x, strides, 0, T, D, dtype),
+                     rows_of(gate_r, strides, 1, T, D, dtype),
+                     rows_of(gate_i, strides, 2, T, D, dtype),
+                     decay, scale, out, last,
+                     opts ? opts->h0 : nullptr, opts ? opts->reset : nullptr};
+    return hip_status(launch_gated_walk_fwd(s, p, static_cast<hipStream_t>(stream)));
+}
+
+LRSCAN_API int scan_gated_bwd(const void* x, const void* gate_r, const void* gate_i,
+                              const float* decay, float scale, const void* out, const void* grad_out,
+                              const float* grad_last, void* grad_x, void* grad_r, void* grad_i,
+                              float* grad_decay, int64_t B, int64_t T, int64_t D, int dtype,
+                              const int64_t* strides, void* stream, const lrscan_opts* opts) {
+    if (!x || !gate_r || !gate_i || !decay || !out || !grad_out || !grad_x || !grad_r || !grad_i)
+        return LRSCAN_ERR_NULL;
+    if (!dims_ok(B, T, D)) return LRSCAN_ERR_DIM;
+    if (!dtype_ok(dtype)) return LRSCAN_ERR_DTYPE;
+    if (!scale_ok(scale) || !strides_ok(strides, 6, B, T)) return LRSCAN_ERR_ARG;
+    for (int i = 3; i < 6; ++i)
+        if (!written_rows_ok(strides, i, B, T, D)) return LRSCAN_ERR_ARG;
+    const GatedShape s{B, T, D, dtype};
+    int algo = 0;
+    int rc = gated_algo(s, opts, &algo);
+    if (rc != LRSCAN_OK) return rc;
+    const GatedBwd p{rows_of(x, strides, 0, T, D, dtype),
+                     rows_of(gate_r, strides, 1, T, D, dtype),
+                     rows_of(gate_i, strides, 2, T, D, dtype),
+                     decay, scale, out, grad_out, grad_last,
+                     opts ? opts->h0 : nullptr, opts ? opts->reset : nullptr,
+                     rows_of(grad_x, strides, 3, T, D, dtype),
+                     rows_of(grad_r, strides, 4, T, D, dtype),
+                     rows_of(grad_i, strides, 5, T, D, dtype),
+                     opts ? opts->grad_h0 : nullptr};
+    hipStream_t hs = static_cast<hipStream_t>(stream);
+    void* part = nullptr;
+    if (grad_decay) {
+        rc = plain_workspace(gated_sum_bytes(s), opts, hs, &part);
+        if (rc != LRSCAN_OK) return rc;
+    }
+    const hipError_t e = launch_gated_walk_bwd(s, p, static_cast<float*>(part), hs);
+    if (e != hipSuccess || !grad_decay) return hip_status(e);
+    const int64_t rows = gated_part_rows(s);
+    float* scratch = reinterpret_cast<float*>(static_cast<char*>(part) + align_up((size_t)rows * D * 4, 256));
+    return hip_status(launch_gated_decay(static_cast<float*>(part), rows, D, scratch, decay, grad_decay, hs));
+}
+
+LRSCAN_API int scan_gated_step(const void* x, const void* gate_r, const void* gate_i,
+                               const float* decay, float scale, const float* state_in,
+                               const uint8_t* reset, void* out, float* state_out, int64_t B,
+                               int64_t D, int dtype, const int64_t* strides, void* stream) {
+    if (!x || !gate_r || !gate_i || !decay || (!out && !state_out)) return LRSCAN_ERR_NULL;
+    if (!dims_ok(B, 1, D)) return LRSCAN_ERR_DIM;
+    if (!dtype_ok(dtype)) return LRSCAN_ERR_DTYPE;
+    int64_t rows[6];
+    for (int i = 0; i < 3; ++i) {
+        rows[2 * i] = strides ? strides[i] : D;
+        rows[2 * i + 1] = D;
+    }
+    if (!scale_ok(scale) || !strides_ok(rows, 3, B, 1)) return LRSCAN_ERR_ARG;
+    const GatedShape s{B, 1, D, dtype};
+    if (!gated_walk_fits(s)) return LRSCAN_ERR_DIM;
+    const GatedFwd p{rows_of(x, rows, 0, 1, D, dtype), rows_of(gate_r, rows, 1, 1, D, dtype),
+                     rows_of(gate_i, rows, 2, 1, D, dtype), decay, scale, out, state_out, state_in, reset};
+    return hip_status(launch_gated_walk_fwd(s, p, static_cast<hipStream_t>(stream)));
+}
+
+LRSCAN_API size_t scan_gated_workspace_bytes(int64_t B, int64_t T, int64_t D, int dtype,
+                                             const lrscan_opts* opts) {
+    if (!dims_ok(B, T, D) || !dtype_ok(dtype)) return 0;
+    const GatedShape s{B, T, D, dtype};
+    int algo = 0;
+    if (gated_algo(s, opts, &algo) != LRSCAN_OK) return 0;
+    return gated_sum_bytes(s);
+}
+
+// ---- short causal convolution -------------------------------------------------------------
+
+LRSCAN_API int scan_conv_fwd(const void* x, const float* weight, const float* bias, const void* state,
+                             const uint8_t* reset, int activation, void* out, void* last, int64_t B,
+                             int64_t T, int64_t D, int64_t K, int dtype, const int64_t* strides,
+                             void* stream) {
+    if (!x || !weight || !out) return LRSCAN_ERR_NULL;
+    if (!dims_ok(B, T, D)) return LRSCAN_ERR_DIM;
+    if (!dtype_ok(dtype)) return LRSCAN_ERR_DTYPE;
+    if (!conv_args_ok(K, activation) || !strides_ok(strides, 1, B, T)) return LRSCAN_ERR_ARG;
+    const ConvShape s{B, T, D, (int)K, dtype, activation};
+    if (!conv_fits(s)) return LRSCAN_ERR_DIM;
+    const ConvFwd p{rows_of(x, strides, 0, T, D, dtype), weight, bias, state, reset, out, last};
+    return hip_status(launch_conv_fwd(s, p, static_cast<hipStream_t>(stream)));
+}
+
+LRSCAN_API int scan_conv_bwd(const void* x, const float* weight, const float* bias, const void* state,
+                             const uint8_t* reset, int activation, const void* grad_out,
+                             const void* grad_last, void* grad_x, float* grad_weight, float* grad_bias,
+                             void* grad_state, int64_t B, int64_t T, int64_t D, int64_t K, int dtype,
+                             const int64_t* strides, void* stream, const lrscan_opts* opts) {
+    if (!x || !weight || !grad_out || !grad_x) return LRSCAN_ERR_NULL;
+    if (!dims_ok(B, T, D)) return LRSCAN_ERR_DIM;
+    if (!dtype_ok(dtype)) return LRSCAN_ERR_DTYPE;
+    if (!conv_args_ok(K, activation) || !strides_ok(strides, 2, B, T) || !written_rows_ok(strides, 1, B, T, D))
+        return LRSCAN_ERR_ARG;
+    const ConvShape s{B, T, D, (int)K, dtype, activation};
+    if (!conv_fits(s)) return LRSCAN_ERR_DIM;
+    const ConvBwd p{rows_of(x, strides, 0, T, D, dtype), weight, bias, state, reset, grad_out, grad_last,
+                    rows_of(grad_x, strides, 1, T, D, dtype), grad_state};
+    hipStream_t hs = static_cast<hipStream_t>(stream);
+    void* part = nullptr;
+    if (grad_weight || grad_bias) {
+        const int rc = plain_workspace(conv_bytes(s), opts, hs, &part);
+        if (rc != LRSCAN_OK) return rc;
+    }
+    float* scratch = part ? reinterpret_cast<float*>(static_cast<char*>(part) + align_up(conv_part_bytes(s), 256))
+                          : nullptr;
+    return hip_status(launch_conv_bwd(s, p, static_cast<float*>(part), scratch, grad_weight, grad_bias, hs));
+}
+
+LRSCAN_API int scan_conv_step(const void* x, const float* weight, const float* bias, const void* state_in,
+                              const uint8_t* reset, int activation, void* out, void* state_out, int64_t B,
+                              int64_t D, int64_t K, int dtype, const int64_t* strides, void* stream) {
+    if (!state_out) return LRSCAN_ERR_NULL;
+    const int64_t rows[2] = {strides ? strides[0] : D, D};
+    return scan_conv_fwd(x, weight, bias, state_in, reset, activation, out, state_out, B, 1, D, K, dtype,
+                         rows, stream);
+}
+
+LRSCAN_API size_t scan_conv_workspace_bytes(int64_t B, int64_t T, int64_t D, int64_t K, int dtype) {
+    if (!dims_ok(B, T, D) || !dtype_ok(dtype) || !conv_args_ok(K, 0)) return 0;
+    const ConvShape s{B, T, D, (int)K, dtype, 0};
+    return conv_fits(s) ? conv_bytes(s) : 0;
+}
+
+// ---- embedding ------------------------------------------------------------------------------
+
+LRSCAN_API int scan_embed_fwd(const void* ids, int id_bytes, const void* weight, float scale, void* out,
+                              int64_t N, int64_t V, int64_t D, int dtype, void* stream) {
+    if (!ids || !weight || !out) return LRSCAN_ERR_NULL;
+    if (!dims_ok(N, 1, D) || !dims_ok(V, 1, D)) return LRSCAN_ERR_DIM;
+    if (!dtype_ok(dtype)) return LRSCAN_ERR_DTYPE;
+    if ((id_bytes != 4 && id_bytes != 8) || !std::isfinite(scale)) return LRSCAN_ERR_ARG;
+    const EmbedShape s{N, V, D, id_bytes, dtype};
+    if (!embed_fits(s)) return LRSCAN_ERR_DIM;
+    return hip_status(launch_embed_fwd(s, ids, weight, scale, out, static_cast<hipStream_t>(stream)));
+}
+
+LRSCAN_API int scan_embed_bwd(const void* ids, int id_bytes, const void* grad_out, float scale,
+                              void* grad_weight, int grad_dtype, int accumulate, int64_t N, int64_t V,
+                              int64_t D, int dtype, void* stream, const lrscan_opts* opts) {
+    if (!ids || !grad_out || !grad_weight) return LRSCAN_ERR_NULL;
+    if (!dims_ok(N, 1, D) || !dims_ok(V, 1, D)) return LRSCAN_ERR_DIM;
+    if (!dtype_ok(dtype) || !dtype_ok(grad_dtype)) return LRSCAN_ERR_DTYPE;
+    if (grad_dtype != dtype && grad_dtype != LRSCAN_F32) return LRSCAN_ERR_DTYPE;
+    if ((id_bytes != 4 && id_bytes != 8) || !std::isfinite(scale)) return LRSCAN_ERR_ARG;
+    const EmbedShape s{N, V, D, id_bytes, dtype};
+    if (!embed_fits(s)) return LRSCAN_ERR_DIM;
+    hipStream_t hs = static_cast<hipStream_t>(stream);
+    void* ws = nullptr;
+    const int rc = plain_workspace(embed_ws_bytes(s), opts, hs, &ws);
+    if (rc != LRSCAN_OK) return rc;
+    return hip_status(launch_embed_bwd(s, ids, grad_out, scale, grad_weight, grad_dtype, accumulate != 0, ws, hs));
+}
+
+LRSCAN_API size_t scan_embed_workspace_bytes(int64_t N, int64_t V, int64_t D, int dtype) {
+    if (!dims_ok(N, 1, D) || !dims_ok(V, 1, D) || !dtype_ok(dtype)) return 0;
+    const EmbedShape s{N, V, D, 8, dtype};
+    return embed_fits(s) ? embed_ws_bytes(s) : 0;
 }
 
 // ---- the chunked form, step by step ---------------------------------------------

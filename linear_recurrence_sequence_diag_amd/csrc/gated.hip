@@ -1,0 +1,256 @@
+// gated.hip -- the gated scan, one thread to V adjacent lanes of a batch row
+// (the per-lane walk), its decode step, and the reduction of the decay
+// gradient's partial sums.
+//
+//   h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(gate_i) x_t,
+//   a_t = exp(-scale softplus(decay) sigmoid(gate_r))
+//
+// (mathematics and gradients in gated_math.hpp).  The transition and the input
+// term are formed in registers from x and the two gate pre-activations, so a
+// forward reads three arrays and writes one; formed by separate passes they
+// would cost five more.  A reset step drops the state by a select, not by a
+// product with 0, so an infinity or NaN in one segment does not reach the
+// next.
+//
+// The walk is the form for sequences too short for tiles, for one decode step
+// (T = 1) and for shapes past the tiles' index limits.
+#include "column_sum.hpp"
+#include "gated.hpp"
+#include "gated_math.hpp"
+#include "launch.hpp"
+
+namespace lrscan {
+
+namespace {
+
+constexpr int kBlock = 256;
+constexpr int kRowsAhead = 4;  // rows of every operand loaded together
+
+template <int DT, bool ALIGNED>
+__device__ __forceinline__ RowVec<DT> load_at(const char* row, int64_t d0, int nvalid, float fill) {
+    return load_row<DT, ALIGNED>(row, (size_t)d0, nvalid, fill);
+}
+
+struct WalkArgs {
+    GatedShape s;
+    int64_t vpr;  // vectors of V lanes in a row
+};
+
+// U rows are loaded ahead of the arithmetic; U = 1 is the decode step.
+template <int DT, bool ALIGNED, int U>
+__global__ __launch_bounds__(kBlock) void gated_walk_fwd_kernel(GatedFwd p, WalkArgs w) {
+    constexpr int V = Elem<DT>::V;
+    const int64_t B = w.s.B, T = w.s.T, D = w.s.D;
+    const int64_t gid = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    const int64_t bi = gid / w.vpr;
+    if (bi >= B) return;
+    const int64_t d0 = (gid - bi * w.vpr) * V;
+    const int nvalid = (int)((D - d0) < V ? (D - d0) : V);
+
+    float rate[V], h[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        rate[j] = j < nvalid ? gate_rate(p.decay[d0 + j], p.scale) : 0.0f;
+        h[j] = (p.h0 && j < nvalid) ? p.h0[bi * D + d0 + j] : 0.0f;
+    }
+    for (int64_t t0 = 0; t0 < T; t0 += U) {
+        RowVec<DT> x[U], gr[U], gi[U];
+        bool start[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t t = t0 + u < T ? t0 + u : T - 1;
+            x[u] = load_at<DT, ALIGNED>(p.x.row(bi, t), d0, nvalid, 0.0f);
+            gr[u] = load_at<DT, ALIGNED>(p.gr.row(bi, t), d0, nvalid, 0.0f);
+            gi[u] = load_at<DT, ALIGNED>(p.gi.row(bi, t), d0, nvalid, 0.0f);
+            start[u] = p.reset && p.reset[bi * T + t];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (t0 + u < T) {
+                RowOut<DT> o;
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const GatedStep g = gated_step_of(x[u].get(j), gr[u].get(j), gi[u].get(j), rate[j]);
+                    const GatedStep f = gated_start_of(x[u].get(j), gi[u].get(j));
+                    h[j] = start[u] ? f.b : fmaf(g.a, h[j], g.b);
+                    o.v[j] = h[j];
+                }
+                if (p.out) store_row<DT, ALIGNED>(p.out, (size_t)((bi * T + t0 + u) * D + d0), nvalid, o);
+            }
+        }
+    }
+    if (p.last) {
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            if (j < nvalid) p.last[bi * D + d0 + j] = h[j];
+    }
+}
+
+// Compensated running sum (Neumaier): a channel's decay gradient may run over
+// millions of steps in one thread.
+struct Compensated {
+    float s = 0.0f, c = 0.0f;
+    __device__ __forceinline__ void add(float x) {
+        const float t = s + x;
+        c += fabsf(s) >= fabsf(x) ? (s - t) + x : (x - t) + s;
+        s = t;
+    }
+};
+
+template <int DT, bool ALIGNED, int U>
+__global__ __launch_bounds__(kBlock) void gated_walk_bwd_kernel(GatedBwd p, WalkArgs w, float* part) {
+    constexpr int V = Elem<DT>::V;
+    const int64_t B = w.s.B, T = w.s.T, D = w.s.D;
+    const int64_t gid = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    const int64_t bi = gid / w.vpr;
+    if (bi >= B) return;
+    const int64_t d0 = (gid - bi * w.vpr) * V;
+    const int nvalid = (int)((D - d0) < V ? (D - d0) : V);
+
+    float rate[V], carry[V];
+    Compensated sum[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        rate[j] = j < nvalid ? gate_rate(p.decay[d0 + j], p.scale) : 0.0f;
+        carry[j] = (p.grad_last && j < nvalid) ? p.grad_last[bi * D + d0 + j] : 0.0f;
+    }
+    for (int64_t t1 = T; t1 > 0; t1 -= U) {  // rows t1 - 1, ..., t1 - U
+        RowVec<DT> x[U], gr[U], gi[U], g[U], hp[U];
+        bool start[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t t = t1 - 1 - u >= 0 ? t1 - 1 - u : 0;
+            const int64_t tp = t > 0 ? t - 1 : 0;
+            x[u] = load_at<DT, ALIGNED>(p.x.row(bi, t), d0, nvalid, 0.0f);
+            gr[u] = load_at<DT, ALIGNED>(p.gr.row(bi, t), d0, nvalid, 0.0f);
+            gi[u] = load_at<DT, ALIGNED>(p.gi.row(bi, t), d0, nvalid, 0.0f);
+            g[u] = load_row<DT, ALIGNED>(p.g, (size_t)((bi * T + t) * D + d0), nvalid, 0.0f);
+            hp[u] = load_row<DT, ALIGNED>(p.out, (size_t)((bi * T + tp) * D + d0), nvalid, 0.0f);
+            start[u] = p.reset && p.reset[bi * T + t];
+        }
+        float block_sum[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) block_sum[j] = 0.0f;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t t = t1 - 1 - u;
+            if (t >= 0) {
+                RowOut<DT> ox, orr, oi;
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    float prev = hp[u].get(j);
+                    if (t == 0) prev = (p.h0 && j < nvalid) ? p.h0[bi * D + d0 + j] : 0.0f;
+                    const float lam = carry[j] + g[u].get(j);
+                    const float xv = x[u].get(j), rv = gr[u].get(j), iv = gi[u].get(j);
+                    const GatedGrad q = start[u] ? gated_start_grad_of(xv, iv, lam)
+                                                 : gated_grad_of(xv, rv, iv, rate[j], prev, lam);
+                    carry[j] = start[u] ? 0.0f : gated_a_of(rv, rate[j]) * lam;
+                    ox.v[j] = q.dx;
+                    orr.v[j] = q.dgr;
+                    oi.v[j] = q.dgi;
+                    block_sum[j] += q.p;
+                }
+                store_row<DT, ALIGNED>(p.gx.row(bi, t), (size_t)d0, nvalid, ox);
+                store_row<DT, ALIGNED>(p.ggr.row(bi, t), (size_t)d0, nvalid, orr);
+                store_row<DT, ALIGNED>(p.ggi.row(bi, t), (size_t)d0, nvalid, oi);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j) sum[j].add(block_sum[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        if (j < nvalid) {
+            if (p.grad_h0) p.grad_h0[bi * D + d0 + j] = carry[j];
+            if (part) part[bi * D + d0 + j] = sum[j].s + sum[j].c;
+        }
+    }
+}
+
+template <int DT>
+dim3 walk_grid(const GatedShape& s, int block, WalkArgs* w) {
+    w->s = s;
+    w->vpr = (s.D + Elem<DT>::V - 1) / Elem<DT>::V;
+    return dim3((unsigned)((s.B * w->vpr + block - 1) / block));
+}
+
+template <int DT>
+hipError_t walk_fwd_t(const GatedShape& s, const GatedFwd& p, hipStream_t st) {
+    WalkArgs w;
+    // one step: workgroups of one wavefront, to spread a small batch over the CUs
+    const int block = s.T == 1 ? kWave : kBlock;
+    const dim3 grid = walk_grid<DT>(s, block, &w);
+    const bool al = gated_fwd_aligned(s, p);
+    if (s.T == 1) {
+        if (al) hipLaunchKernelGGL((gated_walk_fwd_kernel<DT, true, 1>), grid, dim3(block), 0, st, p, w);
+        else hipLaunchKernelGGL((gated_walk_fwd_kernel<DT, false, 1>), grid, dim3(block), 0, st, p, w);
+    } else {
+        if (al) hipLaunchKernelGGL((gated_walk_fwd_kernel<DT, true, kRowsAhead>), grid, dim3(block), 0, st, p, w);
+        else hipLaunchKernelGGL((gated_walk_fwd_kernel<DT, false, kRowsAhead>), grid, dim3(block), 0, st, p, w);
+    }
+    return hipGetLastError();
+}
+
+template <int DT>
+hipError_t walk_bwd_t(const GatedShape& s, const GatedBwd& p, float* part, hipStream_t st) {
+    WalkArgs w;
+    const dim3 grid = walk_grid<DT>(s, kBlock, &w);
+    if (gated_bwd_aligned(s, p))
+        hipLaunchKernelGGL((gated_walk_bwd_kernel<DT, true, kRowsAhead>), grid, dim3(kBlock), 0, st, p, w, part);
+    else
+        hipLaunchKernelGGL((gated_walk_bwd_kernel<DT, false, kRowsAhead>), grid, dim3(kBlock), 0, st, p, w, part);
+    return hipGetLastError();
+}
+
+// grad_decay = slope(decay) * sum of the partial rows.
+struct WriteDecay {
+    const float* decay;
+    float* grad;
+    __device__ __forceinline__ void put(int64_t, int64_t c, float sum) const {
+        grad[c] = decay_slope(decay[c]) * sum;
+    }
+};
+
+}  // namespace
+
+bool operand_aligned(int64_t B, int64_t T, const Rows& r) {
+    if (reinterpret_cast<uintptr_t>(r.p) % 16 != 0) return false;
+    return (T == 1 || r.st % 16 == 0) && (B == 1 || r.sb % 16 == 0);
+}
+
+bool gated_fwd_aligned(const GatedShape& s, const GatedFwd& p) {
+    const Shape c{s.B, s.T, s.D, s.dtype};
+    const void* ptrs[1] = {p.out};
+    return rows_aligned(c, ptrs, 1) && operand_aligned(s.B, s.T, p.x) && operand_aligned(s.B, s.T, p.gr) &&
+           operand_aligned(s.B, s.T, p.gi);
+}
+
+bool gated_bwd_aligned(const GatedShape& s, const GatedBwd& p) {
+    const Shape c{s.B, s.T, s.D, s.dtype};
+    const void* ptrs[2] = {p.out, p.g};
+    return rows_aligned(c, ptrs, 2) && operand_aligned(s.B, s.T, p.x) && operand_aligned(s.B, s.T, p.gr) &&
+           operand_aligned(s.B, s.T, p.gi) && operand_aligned(s.B, s.T, p.gx) && operand_aligned(s.B, s.T, p.ggr) &&
+           operand_aligned(s.B, s.T, p.ggi);
+}
+
+bool gated_walk_fits(const GatedShape& s) {
+    const int64_t v = s.dtype == DT_F32 ? Elem<DT_F32>::V : Elem<DT_BF16>::V;
+    return s.B * ((s.D + v - 1) / v) < ((int64_t)1 << 32) - kBlock;  // work-items of the grid
+}
+
+hipError_t launch_gated_walk_fwd(const GatedShape& s, const GatedFwd& p, hipStream_t st) {
+    return s.dtype == DT_F32 ? walk_fwd_t<DT_F32>(s, p, st) : walk_fwd_t<DT_BF16>(s, p, st);
+}
+
+hipError_t launch_gated_walk_bwd(const GatedShape& s, const GatedBwd& p, float* part, hipStream_t st) {
+    return s.dtype == DT_F32 ? walk_bwd_t<DT_F32>(s, p, part, st) : walk_bwd_t<DT_BF16>(s, p, part, st);
+}
+
+size_t gated_decay_scratch(int64_t rows, int64_t D) { return column_sum_scratch(rows, D); }
+
+hipError_t launch_gated_decay(const float* part, int64_t rows, int64_t D, float* scratch,
+                              const float* decay, float* grad_decay, hipStream_t st) {
+    return launch_column_sum(part, rows, D, scratch, WriteDecay{decay, grad_decay}, st);
+}
+
+}  // namespace lrscan

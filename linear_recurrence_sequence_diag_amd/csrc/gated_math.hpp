@@ -1,0 +1,126 @@
+// gated_math.hpp -- the gated scan's per-element mathematics, shared by its
+// per-lane walk (gated.hip) and its tiled form (gated_fused.hip).
+//
+//   r = sigmoid(gate_r),  i = sigmoid(gate_i),  y = -scale softplus(decay) r,
+//   a = e^y,  beta = sqrt(1 - a^2),  u = i x,      h_t = a_t h_{t-1} + beta_t u_t
+//
+// Everything is fp32 with the hardware exp2, reciprocal and square root (one
+// ulp each), so a costs one exp2 and one reciprocal more than a stored
+// transition would cost a load.
+#pragma once
+
+#include "device.hpp"
+
+namespace lrscan {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+// softplus(x) = max(x, 0) + log(1 + e^-|x|), once per channel.
+__device__ __forceinline__ float softplus_f(float x) {
+    return fmaxf(x, 0.0f) + log1pf(expf(-fabsf(x)));
+}
+
+// sigmoid(x) / softplus(x): the factor that takes sum P to grad_decay.  Below
+// -16 the quotient is 1 - e^x / 2, which is 1 in fp32, while its numerator and
+// denominator both go to zero.
+__device__ __forceinline__ float decay_slope(float x) {
+    return x < -16.0f ? 1.0f : 1.0f / ((1.0f + expf(-x)) * softplus_f(x));
+}
+
+// -scale softplus(decay) log2(e): y in units of log 2 is this times r.
+__device__ __forceinline__ float gate_rate(float decay, float scale) {
+    return -(scale * softplus_f(decay)) * kLog2e;
+}
+
+// sigmoid(x).  e^-x may overflow to infinity (x < -88); its reciprocal is then
+// the 0 that the sigmoid rounds to.
+__device__ __forceinline__ float sigmoid_f(float x) {
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -kLog2e));
+}
+
+// sigmoid(x) with its complement, 1 - sigmoid(x) = e^-x sigmoid(x), which keeps
+// its digits where the sigmoid is near 1.  The exponent is capped at 126 so
+// that the product never is infinity times zero (at x = -87.3, where the
+// sigmoid is 1e-38); written as a comparison, which a NaN passes through.
+struct Sigmoid {
+    float s, c;
+};
+__device__ __forceinline__ Sigmoid sigmoid_pair(float x) {
+    const float t = x * -kLog2e;
+    const float e = __builtin_amdgcn_exp2f(t > 126.0f ? 126.0f : t);
+    const float s = __builtin_amdgcn_rcpf(1.0f + e);
+    return Sigmoid{s, e * s};
+}
+
+// 1 - a^2 for a = 2^y2, y2 <= 0.  Near a = 1 the difference would cancel (a
+// slow channel's 1 - a^2 of 2e-4 would keep 3 digits), so there it is
+// -2 a sinh(y) by the odd series of sinh, whose next term is below 2^-24 of
+// the sum for |y| < 1/4; further away the difference itself loses at most
+// two bits.
+__device__ __forceinline__ float one_minus_sq(float a, float y2) {
+    constexpr float c0 = -2.0f * kLn2;
+    constexpr float c1 = c0 * kLn2 * kLn2 / 6.0f;
+    constexpr float c2 = c1 * kLn2 * kLn2 / 20.0f;
+    const float s = y2 * y2;
+    const float near_one = (a * y2) * fmaf(s, fmaf(s, c2, c1), c0);
+    return y2 > -0.36f ? near_one : fmaf(-a, a, 1.0f);
+}
+
+// The transition and the input term of one step.
+struct GatedStep {
+    float a, b;
+};
+__device__ __forceinline__ GatedStep gated_step_of(float x, float gr, float gi, float rate) {
+    const float y2 = rate * sigmoid_f(gr);
+    const float a = __builtin_amdgcn_exp2f(y2);
+    const float beta = __builtin_amdgcn_sqrtf(one_minus_sq(a, y2));
+    return GatedStep{a, beta * (sigmoid_f(gi) * x)};
+}
+// ... of a step that starts a segment: a = 0, beta = 1.
+__device__ __forceinline__ GatedStep gated_start_of(float x, float gi) {
+    return GatedStep{0.0f, sigmoid_f(gi) * x};
+}
+
+// The transition alone (the adjoint's map needs no input term).
+__device__ __forceinline__ float gated_a_of(float gr, float rate) {
+    return __builtin_amdgcn_exp2f(rate * sigmoid_f(gr));
+}
+
+// Gradients of one step from its adjoint lam and the state before it:
+//   du = lam beta,  dx = du i,  dgi = dx x (1 - i),
+//   P = y dL/dy = lam a y (h_prev - a u / beta),  dgr = P (1 - r),
+// and sum P gives grad_decay.  y / beta is finite down to beta = 0 (y and
+// beta^2 vanish together), so P is formed from a y2 and y2 / beta.
+struct GatedGrad {
+    float dx, dgr, dgi, p;
+};
+__device__ __forceinline__ GatedGrad gated_grad_of(float x, float gr, float gi, float rate,
+                                                   float h_prev, float lam) {
+    const Sigmoid r = sigmoid_pair(gr);
+    const Sigmoid ig = sigmoid_pair(gi);
+    const float y2 = rate * r.s;
+    const float a = __builtin_amdgcn_exp2f(y2);
+    const float v = one_minus_sq(a, y2);
+    // 1 / beta; 0 where beta is 0 or below 1e-19 (the reciprocal root of a
+    // denormal would be infinite), so that y / beta takes its limit there
+    const float inv = v < 0x1p-126f ? 0.0f : __builtin_amdgcn_rsqf(v);
+    GatedGrad o;
+    o.dx = (lam * (v * inv)) * ig.s;
+    o.dgi = (o.dx * x) * ig.c;
+    const float ay = a * y2;
+    o.p = (lam * kLn2) * (ay * h_prev - (a * ay) * (inv * (ig.s * x)));
+    o.dgr = o.p * r.c;
+    return o;
+}
+__device__ __forceinline__ GatedGrad gated_start_grad_of(float x, float gi, float lam) {
+    const Sigmoid ig = sigmoid_pair(gi);
+    GatedGrad o;
+    o.dx = lam * ig.s;
+    o.dgi = (o.dx * x) * ig.c;
+    o.p = 0.0f;
+    o.dgr = 0.0f;
+    return o;
+}
+
+}  // namespace lrscan
