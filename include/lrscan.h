@@ -308,8 +308,10 @@ LRSCAN_API size_t scan_samu_workspace_bytes(int64_t B, int64_t T, int64_t M, int
  * halves of one [B, T, 2 D] projection).  None is negative; an input's may be
  * 0 (a broadcast row); rows that are written do not overlap.  out and grad_out
  * are contiguous.
- * opts: algo AUTO or SEQ (a per-lane walk) with chunk and width 0; h0,
- * grad_h0, reset, polls and workspace as for the real scan.
+ * opts: algo AUTO, FUSED (one tiled launch) or SEQ (a per-lane walk) with
+ * chunk and width 0 (else LRSCAN_ERR_CHUNK; so for FUSED on rows too far apart
+ * for a tile's 32-bit offsets, which AUTO walks); h0, grad_h0, reset, polls
+ * and workspace as for the real scan.
  * ------------------------------------------------------------------------ */
 /*   x, gate_r, gate_i [B,T,D] dtype and decay [D] fp32 read.  out [B,T,D]
  *   (NULL: state only, then last is required) and last [B,D] fp32 written.

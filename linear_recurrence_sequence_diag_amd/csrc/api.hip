@@ -463,21 +463,58 @@ int plain_workspace(size_t need, const lrscan_opts* o, hipStream_t st, void** ou
 
 bool scale_ok(float scale) { return std::isfinite(scale) && scale > 0.0f; }
 
-// AUTO or SEQ.
-int gated_algo(const GatedShape& s, const lrscan_opts* o, int* algo) {
+// The per-lane walk for sequences of a few steps, whose tiles would be mostly
+// idle rows.
+bool gated_prefer_seq(const GatedShape& s) { return s.T <= 8; }
+
+// AUTO, FUSED (the library's tile shapes) or SEQ; AUTO walks short sequences
+// and what the tiles' index limits leave out.  `rows`: byte strides of the
+// steps of the call's strided operands.
+int gated_algo(const GatedShape& s, int dir, const size_t* rows, int n, const lrscan_opts* o, int* algo) {
     const int a = o ? o->algo : LRSCAN_ALGO_AUTO;
-    if (a != LRSCAN_ALGO_AUTO && a != LRSCAN_ALGO_SEQ) return LRSCAN_ERR_ALGO;
+    if (a != LRSCAN_ALGO_AUTO && a != LRSCAN_ALGO_FUSED && a != LRSCAN_ALGO_SEQ) return LRSCAN_ERR_ALGO;
     if (o && (o->chunk != 0 || o->width != 0)) return LRSCAN_ERR_CHUNK;
-    *algo = LRSCAN_ALGO_SEQ;
-    return gated_walk_fits(s) ? LRSCAN_OK : LRSCAN_ERR_DIM;
+    const bool fits = gated_fused_fits(s, dir, rows, n);
+    if (a == LRSCAN_ALGO_FUSED && !fits) return LRSCAN_ERR_CHUNK;
+    const bool seq = a == LRSCAN_ALGO_SEQ || (a == LRSCAN_ALGO_AUTO && (gated_prefer_seq(s) || !fits));
+    if (seq && !gated_walk_fits(s)) return LRSCAN_ERR_DIM;
+    *algo = seq ? LRSCAN_ALGO_SEQ : LRSCAN_ALGO_FUSED;
+    return LRSCAN_OK;
 }
 
 // Rows of partial sums of the decay gradient, and the bytes of them and of
 // their reduction's scratch.
-int64_t gated_part_rows(const GatedShape& s) { return s.B; }
-size_t gated_sum_bytes(const GatedShape& s) {
-    const int64_t rows = gated_part_rows(s);
+int64_t gated_part_rows(const GatedShape& s, int algo) {
+    return algo == LRSCAN_ALGO_SEQ ? s.B : gated_fused_part_rows(s);
+}
+size_t gated_sum_bytes(const GatedShape& s, int algo) {
+    const int64_t rows = gated_part_rows(s, algo);
     return align_up((size_t)rows * (size_t)s.D * 4, 256) + gated_decay_scratch(rows, s.D);
+}
+
+// The tiles' scratch (library kind 1, or the head of the caller's buffer) where
+// the call is tiled, and the partial sums (kind 2, or after it) where it has
+// any.
+int gated_workspace(const GatedShape& s, int algo, bool sums, const lrscan_opts* o, hipStream_t st,
+                    Workspace* ws, void** part) {
+    *ws = Workspace{};
+    *part = nullptr;
+    const size_t head = algo == LRSCAN_ALGO_FUSED ? align_up(gated_fused_bytes(s), 256) : 0;
+    const size_t tail = sums ? gated_sum_bytes(s, algo) : 0;
+    if (o && o->workspace && head + tail > 0) {
+        if (o->workspace_bytes < head + tail) return LRSCAN_ERR_WORKSPACE;
+        if (reinterpret_cast<uintptr_t>(o->workspace) % 256 != 0) return LRSCAN_ERR_WORKSPACE;
+        ws->ptr = o->workspace;
+        ws->bytes = head;
+        ws->init = true;
+        if (sums) *part = static_cast<char*>(o->workspace) + head;
+        return LRSCAN_OK;
+    }
+    if (head > 0) {
+        const int rc = library_workspace(head, 1, st, ws);
+        if (rc != LRSCAN_OK) return rc;
+    }
+    return plain_workspace(tail, nullptr, st, part);
 }
 
 bool conv_args_ok(int64_t K, int activation) {
@@ -882,15 +919,23 @@ LRSCAN_API int scan_gated_fwd(const void* x, const void* gate_r, const void* gat
     if (!dtype_ok(dtype)) return LRSCAN_ERR_DTYPE;
     if (!scale_ok(scale) || !strides_ok(strides, 3, B, T)) return LRSCAN_ERR_ARG;
     const GatedShape s{B, T, D, dtype};
-    int algo = 0;
-    const int rc = gated_algo(s, opts, &algo);
-    if (rc != LRSCAN_OK) return rc;
     const GatedFwd p{rows_of(x, strides, 0, T, D, dtype),
                      rows_of(gate_r, strides, 1, T, D, dtype),
                      rows_of(gate_i, strides, 2, T, D, dtype),
                      decay, scale, out, last,
                      opts ? opts->h0 : nullptr, opts ? opts->reset : nullptr};
-    return hip_status(launch_gated_walk_fwd(s, p, static_cast<hipStream_t>(stream)));
+    const size_t rows[3] = {p.x.st, p.gr.st, p.gi.st};
+    int algo = 0;
+    int rc = gated_algo(s, 0, rows, 3, opts, &algo);
+    if (rc != LRSCAN_OK) return rc;
+    hipStream_t hs = static_cast<hipStream_t>(stream);
+    if (algo == LRSCAN_ALGO_SEQ) return hip_status(launch_gated_walk_fwd(s, p, hs));
+    Workspace ws;
+    void* part = nullptr;
+    rc = gated_workspace(s, algo, false, opts, hs, &ws, &part);
+    if (rc != LRSCAN_OK) return rc;
+    return fused_status(launch_gated_fused_fwd(s, p, ws.ptr, ws.bytes, ws.init, opts ? opts->polls : 0, hs),
+                        ws, hs);
 }
 
 LRSCAN_API int scan_gated_bwd(const void* x, const void* gate_r, const void* gate_i,
@@ -906,9 +951,6 @@ LRSCAN_API int scan_gated_bwd(const void* x, const void* gate_r, const void* gat
     for (int i = 3; i < 6; ++i)
         if (!written_rows_ok(strides, i, B, T, D)) return LRSCAN_ERR_ARG;
     const GatedShape s{B, T, D, dtype};
-    int algo = 0;
-    int rc = gated_algo(s, opts, &algo);
-    if (rc != LRSCAN_OK) return rc;
     const GatedBwd p{rows_of(x, strides, 0, T, D, dtype),
                      rows_of(gate_r, strides, 1, T, D, dtype),
                      rows_of(gate_i, strides, 2, T, D, dtype),
@@ -918,17 +960,25 @@ LRSCAN_API int scan_gated_bwd(const void* x, const void* gate_r, const void* gat
                      rows_of(grad_r, strides, 4, T, D, dtype),
                      rows_of(grad_i, strides, 5, T, D, dtype),
                      opts ? opts->grad_h0 : nullptr};
+    const size_t rows[6] = {p.x.st, p.gr.st, p.gi.st, p.gx.st, p.ggr.st, p.ggi.st};
+    int algo = 0;
+    int rc = gated_algo(s, 1, rows, 6, opts, &algo);
+    if (rc != LRSCAN_OK) return rc;
     hipStream_t hs = static_cast<hipStream_t>(stream);
+    Workspace ws;
     void* part = nullptr;
-    if (grad_decay) {
-        rc = plain_workspace(gated_sum_bytes(s), opts, hs, &part);
-        if (rc != LRSCAN_OK) return rc;
-    }
-    const hipError_t e = launch_gated_walk_bwd(s, p, static_cast<float*>(part), hs);
-    if (e != hipSuccess || !grad_decay) return hip_status(e);
-    const int64_t rows = gated_part_rows(s);
-    float* scratch = reinterpret_cast<float*>(static_cast<char*>(part) + align_up((size_t)rows * D * 4, 256));
-    return hip_status(launch_gated_decay(static_cast<float*>(part), rows, D, scratch, decay, grad_decay, hs));
+    rc = gated_workspace(s, algo, grad_decay != nullptr, opts, hs, &ws, &part);
+    if (rc != LRSCAN_OK) return rc;
+    if (algo == LRSCAN_ALGO_SEQ)
+        rc = hip_status(launch_gated_walk_bwd(s, p, static_cast<float*>(part), hs));
+    else
+        rc = fused_status(launch_gated_fused_bwd(s, p, static_cast<float*>(part), ws.ptr, ws.bytes, ws.init,
+                                                 opts ? opts->polls : 0, hs),
+                          ws, hs);
+    if (rc != LRSCAN_OK || !grad_decay) return rc;
+    const int64_t sums = gated_part_rows(s, algo);
+    float* scratch = reinterpret_cast<float*>(static_cast<char*>(part) + align_up((size_t)sums * D * 4, 256));
+    return hip_status(launch_gated_decay(static_cast<float*>(part), sums, D, scratch, decay, grad_decay, hs));
 }
 
 LRSCAN_API int scan_gated_step(const void* x, const void* gate_r, const void* gate_i,
@@ -955,9 +1005,16 @@ LRSCAN_API size_t scan_gated_workspace_bytes(int64_t B, int64_t T, int64_t D, in
                                              const lrscan_opts* opts) {
     if (!dims_ok(B, T, D) || !dtype_ok(dtype)) return 0;
     const GatedShape s{B, T, D, dtype};
-    int algo = 0;
-    if (gated_algo(s, opts, &algo) != LRSCAN_OK) return 0;
-    return gated_sum_bytes(s);
+    // contiguous rows take tiles wherever strided ones do, and a walk needs no more
+    size_t need = 0;
+    for (int dir = 0; dir < 2; ++dir) {
+        int algo = 0;
+        if (gated_algo(s, dir, nullptr, 0, opts, &algo) != LRSCAN_OK) return 0;
+        size_t n = dir == 1 ? gated_sum_bytes(s, algo) : 0;
+        if (algo == LRSCAN_ALGO_FUSED) n += align_up(gated_fused_bytes(s), 256);
+        need = n > need ? n : need;
+    }
+    return need;
 }
 
 // ---- short causal convolution -------------------------------------------------------------

@@ -55,6 +55,18 @@ bool gated_walk_fits(const GatedShape& s);
 hipError_t launch_gated_walk_fwd(const GatedShape& s, const GatedFwd& p, hipStream_t st);
 hipError_t launch_gated_walk_bwd(const GatedShape& s, const GatedBwd& p, float* part, hipStream_t st);
 
+// The tiled single-launch form (scratch conventions of the fused form).  It
+// takes a shape whose tiles' byte offsets stay in 32 bits, `row_strides` the
+// bytes between the steps of its strided operands.  The backward's `part` (or
+// NULL) receives gated_fused_part_rows rows of D partial sums of P.
+bool gated_fused_fits(const GatedShape& s, int dir, const size_t* row_strides, int n);
+size_t gated_fused_bytes(const GatedShape& s);
+int64_t gated_fused_part_rows(const GatedShape& s);
+hipError_t launch_gated_fused_fwd(const GatedShape& s, const GatedFwd& p, void* ws, size_t ws_bytes,
+                                  bool init, int polls, hipStream_t st);
+hipError_t launch_gated_fused_bwd(const GatedShape& s, const GatedBwd& p, float* part, void* ws,
+                                  size_t ws_bytes, bool init, int polls, hipStream_t st);
+
 // grad_decay from `rows` rows of D partial sums; `scratch` holds
 // gated_decay_scratch bytes.
 size_t gated_decay_scratch(int64_t rows, int64_t D);

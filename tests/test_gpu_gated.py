@@ -78,7 +78,7 @@ class Case:
         return out, last
 
 
-ALGOS = ["auto", "seq"]
+ALGOS = ["auto", "seq", "fused"]
 SHAPES = [(1, 1, 1), (2, 3, 5), (3, 17, 8), (2, 64, 64), (1, 65, 131), (2, 257, 130), (1, 300, 72), (5, 129, 520),
           (2, 700, 33), (3, 513, 256), (70, 5, 100), (1, 2100, 24)]
 
@@ -220,6 +220,22 @@ def test_steps_give_the_rows(D, dtype):
     assert torch.equal(a, b)
     none, s = lr.gated_step(c.x[:, 0], c.gr[:, 0], c.gi[:, 0], c.decay, with_out=False)
     assert none is None and s.shape == (B, D)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("reset", [None, "some"])
+def test_tiles_that_do_not_wait(reset, dtype):
+    """With one poll a tile derives the maps it misses: the same bits."""
+    for B, T, D in ((1, 3000, 40), (2, 1500, 257), (1, 20000, 64)):
+        log(f"{B} {T} {D}")
+        c = Case(B, T, D, dtype, reset=reset, states=True) if T < 5000 else Case(B, T, D, dtype, reset=reset)
+        out, last = c.forward(algo="fused")
+        grads = c.backward(out, algo="fused")
+        for _ in range(2):
+            out1, last1 = c.forward(algo="fused", polls=1)
+            assert torch.equal(out, out1) and torch.equal(last, last1)
+            for a, b in zip(grads, c.backward(out, algo="fused", polls=1)):
+                assert a is b or torch.equal(a, b)
 
 
 def test_autograd_and_repeatability():
