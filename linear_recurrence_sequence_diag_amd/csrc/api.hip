@@ -464,8 +464,16 @@ int plain_workspace(size_t need, const lrscan_opts* o, hipStream_t st, void** ou
 bool scale_ok(float scale) { return std::isfinite(scale) && scale > 0.0f; }
 
 // The per-lane walk for sequences of a few steps, whose tiles would be mostly
-// idle rows.
-bool gated_prefer_seq(const GatedShape& s) { return s.T <= 8; }
+// idle rows.  Measured on MI355X (caches flushed, us forward / reverse, 32-row
+// tiles against the walk): bf16 [4096,4,1024] 187 / 316 against 47 / 93,
+// [2048,8,2560] 234 / 404 against 86 / 180, [1024,16,2560] 125 / 234 against
+// 86 / 179, [512,32,2560] 75 / 145 against 92 / 198, [16,16,2560] 8 / 14
+// against 18 / 37; fp32 [1024,16,2560] 144 / 296 against 159 / 302.
+bool gated_prefer_seq(const GatedShape& s) {
+    const int64_t lanes = s.B * s.D;
+    return s.T <= 2 || (s.T <= 8 && lanes >= ((int64_t)1 << 18)) ||
+           (s.T <= 16 && s.dtype == LRSCAN_BF16 && lanes >= ((int64_t)1 << 20));
+}
 
 // AUTO, FUSED (the library's tile shapes) or SEQ; AUTO walks short sequences
 // and what the tiles' index limits leave out.  `rows`: byte strides of the

@@ -144,7 +144,7 @@ __global__ __launch_bounds__(kBlock) void gated_walk_bwd_kernel(GatedBwd p, Walk
                     const float xv = x[u].get(j), rv = gr[u].get(j), iv = gi[u].get(j);
                     const GatedGrad q = start[u] ? gated_start_grad_of(xv, iv, lam)
                                                  : gated_grad_of(xv, rv, iv, rate[j], prev, lam);
-                    carry[j] = start[u] ? 0.0f : gated_a_of(rv, rate[j]) * lam;
+                    carry[j] = start[u] ? 0.0f : q.a * lam;
                     ox.v[j] = q.dx;
                     orr.v[j] = q.dgr;
                     oi.v[j] = q.dgi;
@@ -202,12 +202,12 @@ hipError_t walk_bwd_t(const GatedShape& s, const GatedBwd& p, float* part, hipSt
     return hipGetLastError();
 }
 
-// grad_decay = slope(decay) * sum of the partial rows.
+// grad_decay = slope(decay) * sum of the partial rows (of P / ln 2).
 struct WriteDecay {
     const float* decay;
     float* grad;
     __device__ __forceinline__ void put(int64_t, int64_t c, float sum) const {
-        grad[c] = decay_slope(decay[c]) * sum;
+        grad[c] = decay_slope(decay[c]) * (kLn2 * sum);
     }
 };
 

@@ -15,6 +15,8 @@
 // is >= +0 and a reset enters compositions by selects, so the sign tells a
 // drop from a product that underflowed, whose argument still counts where it
 // is an infinity or NaN.
+#include <type_traits>
+
 #include "fused_common.hpp"
 #include "gated.hpp"
 #include "gated_math.hpp"
@@ -196,6 +198,37 @@ __device__ __forceinline__ void tile_rates(float (&s_rate)[C::W], const float* d
     __syncthreads();
 }
 
+// Segment starts among this thread's rows that exist, bit i for row i.
+template <class C>
+__device__ __forceinline__ uint32_t start_bits(const uint8_t* reset, const Geo& g, int T) {
+    static_assert(C::NR % 4 == 0 || C::NR < 4, "whole words of mask bytes");
+    uint32_t bits = 0;
+    if (C::NR % 4 == 0 && g.nrows == C::NR) {
+        const uint8_t* p = reset + (size_t)g.bi * T + g.row0;
+#pragma unroll
+        for (int w = 0; w < C::NR / 4; ++w) {
+            uint32_t four;
+            __builtin_memcpy(&four, p + 4 * w, 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) bits |= ((four >> (8 * i)) & 0xffu ? 1u : 0u) << (4 * w + i);
+        }
+        return bits;
+    }
+#pragma unroll
+    for (int i = 0; i < C::NR; ++i)
+        if (i < g.nrows && reset_byte(reset, g, i, T)) bits |= 1u << i;
+    return bits;
+}
+
+// Different empty statements at the top of the two versions of a loop: without
+// them the compiler hoists their common start above the branch and keeps its
+// registers alive into both, which spilled.
+template <bool PLAIN>
+__device__ __forceinline__ void path_marker() {
+    if constexpr (PLAIN) asm volatile("; plain rows");
+    else asm volatile("; any rows");
+}
+
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
@@ -224,26 +257,21 @@ void gated_fwd_kernel(GatedFwdArgs x) {
     char* po = static_cast<char*>(x.p.out) + g.tbase;
     const uint32_t rowbytes = (uint32_t)d.D * C::EB;
 
-    uint32_t rbits = 0;
-    if constexpr (RST) {
-#pragma unroll
-        for (int i = 0; i < NR; ++i) rbits |= (reset_byte(x.p.reset, g, i, d.T) ? 1u : 0u) << i;
-    }
+    const uint32_t rbits = RST ? start_bits<C>(x.p.reset, g, d.T) : 0u;
     RowVec<C::DT> rx[NR], rr[NR], ri[NR];
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
         const int row = g.row0 + i;
-        rr[i] = load_vec<C::DT, ALIGNED, false>(pr.p, pr.off(g, row, d.T), g.nvalid, 0.0f);
-        ri[i] = load_vec<C::DT, ALIGNED, false>(pi.p, pi.off(g, row, d.T), g.nvalid, 0.0f);
-        rx[i] = load_vec<C::DT, ALIGNED, false>(px.p, px.off(g, row, d.T), g.nvalid, 0.0f);
+        rr[i] = load_vec<C::DT, ALIGNED, true>(pr.p, pr.off(g, row, d.T), g.nvalid, 0.0f);
+        ri[i] = load_vec<C::DT, ALIGNED, true>(pi.p, pi.off(g, row, d.T), g.nvalid, 0.0f);
+        rx[i] = load_vec<C::DT, ALIGNED, true>(px.p, px.off(g, row, d.T), g.nvalid, 0.0f);
     }
     tile_rates<C>(s_rate, x.p.decay, x.p.scale, g, d.D);
     float rate[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) rate[j] = s_rate[cg * V + j];
 
-    // coefficients and summary, row by row; rows past T (and every row of a
-    // thread whose lanes lie past D) become identity steps
+    // coefficients and summary, row by row
     const bool full = g.trow0 + C::CT <= d.T && g.dcol0 + W <= d.D;
     float ca[NR][V], cb[NR][V];
     Aff m[V];
@@ -251,14 +279,42 @@ void gated_fwd_kernel(GatedFwdArgs x) {
     for (int j = 0; j < V; ++j) m[j] = aff_identity();
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
-        const bool start = RST && ((rbits >> i) & 1u) && (full || i < g.nrows);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            GatedStep s = gated_coef<RST>(rx[i].get(j), rr[i].get(j), ri[i].get(j), rate[j], start);
-            if (!full && i >= g.nrows) s = GatedStep{1.0f, 0.0f};
+            const GatedStep s = gated_step_of(rx[i].get(j), rr[i].get(j), ri[i].get(j), rate[j]);
             ca[i][j] = s.a;
             cb[i][j] = s.b;
-            fold_fwd<RST>(m[j], s, start);
+            fold_fwd<false>(m[j], s, false);
+        }
+    }
+    // A wavefront that holds a segment start or a row that does not exist puts
+    // those rows right (a start's input term from its reloaded row) and folds
+    // again, rather than every element paying for selects: few wavefronts do
+    // ([8, 2048, 2560] bf16 with a start every 512 tokens: 85 -> 80 us).
+    const bool plain = __all(full && rbits == 0);
+    if (!plain) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) m[j] = aff_identity();
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+            const bool start = RST && ((rbits >> i) & 1u), gone = i >= g.nrows;
+            if (RST && __any(start)) {
+                const int row = g.row0 + i;
+                const RowVec<C::DT> xs = load_vec<C::DT, ALIGNED>(px.p, px.off(g, row, d.T), g.nvalid, 0.0f);
+                const RowVec<C::DT> is = load_vec<C::DT, ALIGNED>(pi.p, pi.off(g, row, d.T), g.nvalid, 0.0f);
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const GatedStep s = gated_start_of(xs.get(j), is.get(j));
+                    ca[i][j] = start ? s.a : ca[i][j];
+                    cb[i][j] = start ? s.b : cb[i][j];
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                ca[i][j] = gone ? 1.0f : ca[i][j];
+                cb[i][j] = gone ? 0.0f : cb[i][j];
+                fold_fwd<RST>(m[j], GatedStep{ca[i][j], cb[i][j]}, start);
+            }
         }
     }
     const int seg = wave * RG + rg;
@@ -313,21 +369,27 @@ void gated_fwd_kernel(GatedFwdArgs x) {
     for (int j = 0; j < V; ++j)
         h[j] = gated_apply<RST>(s_seg[seg][cg * V + j],
                                 gated_apply<RST>(s_wav[wave][cg * V + j], s_hin[cg * V + j]));
+    const auto replay = [&](auto plain) {
+        constexpr bool PLAIN = decltype(plain)::value;
+        path_marker<PLAIN>();
 #pragma unroll
-    for (int i = 0; i < NR; ++i) {
-        if (full || i < g.nrows) {
-            const bool start = RST && ((rbits >> i) & 1u);
-            RowOut<C::DT> o;
+        for (int i = 0; i < NR; ++i) {
+            if (PLAIN || i < g.nrows) {
+                const bool start = !PLAIN && RST && ((rbits >> i) & 1u);
+                RowOut<C::DT> o;
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float n = fmaf(ca[i][j], h[j], cb[i][j]);
-                h[j] = start ? cb[i][j] : n;
-                o.v[j] = h[j];
+                for (int j = 0; j < V; ++j) {
+                    const float n = fmaf(ca[i][j], h[j], cb[i][j]);
+                    h[j] = start ? cb[i][j] : n;
+                    o.v[j] = h[j];
+                }
+                if constexpr (OUT)
+                    store_vec<C::DT, ALIGNED>(po, row_off(g, g.row0 + i, d.T, rowbytes), g.nvalid, o);
             }
-            if constexpr (OUT)
-                store_vec<C::DT, ALIGNED>(po, row_off(g, g.row0 + i, d.T, rowbytes), g.nvalid, o);
         }
-    }
+    };
+    if (plain) replay(std::true_type{});
+    else replay(std::false_type{});
     if (x.p.last && ends) {
 #pragma unroll
         for (int j = 0; j < V; ++j)
@@ -366,11 +428,7 @@ void gated_bwd_kernel(GatedBwdArgs x) {
     const int hrow0 = g.trow0 > 0 ? g.trow0 - 1 : 0;  // h_{t-1} is row t-1 of `out`
     const char* ph = static_cast<const char*>(x.p.out) + g.tbase - (size_t)(g.trow0 - hrow0) * rowbytes;
 
-    uint32_t rbits = 0;
-    if constexpr (RST) {
-#pragma unroll
-        for (int i = 0; i < NR; ++i) rbits |= (reset_byte(x.p.reset, g, i, d.T) ? 1u : 0u) << i;
-    }
+    const uint32_t rbits = RST ? start_bits<C>(x.p.reset, g, d.T) : 0u;
     // what the summary uses first, in its order, then the replay's rows
     RowVec<C::DT> rr[NR], rg_[NR], rx[NR], ri[NR], rh[NR];
 #pragma unroll
@@ -402,17 +460,26 @@ void gated_bwd_kernel(GatedBwdArgs x) {
 #pragma unroll
     for (int j = 0; j < V; ++j) m[j] = aff_identity();
 #pragma unroll
-    for (int i = NR - 1; i >= 0; --i) {
-        const bool ok = full || i < g.nrows;
-        const bool start = RST && ((rbits >> i) & 1u) && ok;
+    for (int i = NR - 1; i >= 0; --i)
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            float a = gated_a_of(rr[i].get(j), rate[j]), gt = rg_[i].get(j);
-            if (!ok) {
-                a = 1.0f;
-                gt = 0.0f;
+        for (int j = 0; j < V; ++j)
+            fold_rev<false>(m[j], gated_a_of(rr[i].get(j), rate[j]), rg_[i].get(j), false);
+    // with a segment start or a row that does not exist: folded again, as in
+    // the forward
+    const bool plain = __all(full && rbits == 0);
+    if (!plain) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) m[j] = aff_identity();
+#pragma unroll
+        for (int i = NR - 1; i >= 0; --i) {
+            opaque(rr[i]);
+            opaque(rg_[i]);
+            const bool start = RST && ((rbits >> i) & 1u), gone = i >= g.nrows;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float a = gated_a_of(rr[i].get(j), rate[j]), gt = rg_[i].get(j);
+                fold_rev<RST>(m[j], gone ? 1.0f : a, gone ? 0.0f : gt, start);
             }
-            fold_rev<RST>(m[j], a, gt, start);
         }
     }
     const int seg = wave * RG + rg;
@@ -469,33 +536,39 @@ void gated_bwd_kernel(GatedBwdArgs x) {
                                     gated_apply<RST>(s_wav[wave][cg * V + j], s_cin[cg * V + j]));
         sum[j] = 0.0f;
     }
+    // one row; STARTS: some thread of the wavefront has a segment start there
+    const auto replay = [&](int i, auto starts) {
+        constexpr bool STARTS = decltype(starts)::value;
+        const int row = g.row0 + i;
+        const bool start = STARTS && ((rbits >> i) & 1u);
+        RowOut<C::DT> ox, orr, oi;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const float lam = carry[j] + rg_[i].get(j);
+            float hp = rh[i].get(j);
+            if (i == 0 && g.row0 == 0)  // row 0: h0, or 0
+                hp = (x.p.h0 && j < g.nvalid) ? x.p.h0[(size_t)g.bi * d.D + g.d0 + j] : 0.0f;
+            const float xv = rx[i].get(j), iv = ri[i].get(j), rv = rr[i].get(j);
+            GatedGrad q = gated_grad_of(xv, rv, iv, rate[j], hp, lam);
+            carry[j] = q.a * lam;
+            if (start) {
+                q = gated_start_grad_of(xv, iv, lam);
+                carry[j] = 0.0f;
+            }
+            ox.v[j] = q.dx;
+            orr.v[j] = q.dgr;
+            oi.v[j] = q.dgi;
+            sum[j] += q.p;
+        }
+        store_vec<C::DT, ALIGNED>(qx.p, qx.off(g, row, d.T), g.nvalid, ox);
+        store_vec<C::DT, ALIGNED>(qr.p, qr.off(g, row, d.T), g.nvalid, orr);
+        store_vec<C::DT, ALIGNED>(qi.p, qi.off(g, row, d.T), g.nvalid, oi);
+    };
 #pragma unroll
     for (int i = NR - 1; i >= 0; --i) {
         if (full || i < g.nrows) {
-            const int row = g.row0 + i;
-            const bool start = RST && ((rbits >> i) & 1u);
-            RowOut<C::DT> ox, orr, oi;
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float lam = carry[j] + rg_[i].get(j);
-                float hp = rh[i].get(j);
-                if (i == 0 && g.row0 == 0)  // row 0: h0, or 0
-                    hp = (x.p.h0 && j < g.nvalid) ? x.p.h0[(size_t)g.bi * d.D + g.d0 + j] : 0.0f;
-                const float xv = rx[i].get(j), iv = ri[i].get(j), rv = rr[i].get(j);
-                GatedGrad q = gated_grad_of(xv, rv, iv, rate[j], hp, lam);
-                carry[j] = gated_a_of(rv, rate[j]) * lam;
-                if (start) {
-                    q = gated_start_grad_of(xv, iv, lam);
-                    carry[j] = 0.0f;
-                }
-                ox.v[j] = q.dx;
-                orr.v[j] = q.dgr;
-                oi.v[j] = q.dgi;
-                sum[j] += q.p;
-            }
-            store_vec<C::DT, ALIGNED>(qx.p, qx.off(g, row, d.T), g.nvalid, ox);
-            store_vec<C::DT, ALIGNED>(qr.p, qr.off(g, row, d.T), g.nvalid, orr);
-            store_vec<C::DT, ALIGNED>(qi.p, qi.off(g, row, d.T), g.nvalid, oi);
+            if (RST && __any((rbits >> i) & 1u)) replay(i, std::true_type{});
+            else replay(i, std::false_type{});
         }
     }
     if (x.p.grad_h0 && g.nrows > 0 && g.row0 == 0) {
@@ -535,20 +608,49 @@ void gated_bwd_kernel(GatedBwdArgs x) {
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-template <int DT, int TPR, int NR, int WAVES, int LB, int OF, int OB>
-struct GCfg : Cfg<DT, TPR, NR, WAVES, LB> {
+// OCC_F, OCC_G: wavefronts a SIMD is to hold, forward and reverse (their
+// registers fit without spilling, or with under 40 bytes).
+template <int DT, int TPR, int NR, int LB, int OF, int OB>
+struct GCfg : Cfg<DT, TPR, NR, 4, LB> {
     static constexpr int OCC_F = OF, OCC_G = OB;
 };
+template <int DT> using Tile16x32 = GCfg<DT, 16, 2, 4, 5, 4>;
+template <int DT> using Tile16x64 = GCfg<DT, 16, 4, 4, 3, 3>;
+template <int DT> using Tile8x128 = GCfg<DT, 8, 4, 8, 3, 3>;
+template <int DT> using Tile8x256 = GCfg<DT, 8, 8, 8, 2, 2>;
 
+// Tile of a shape: `width` threads of 16 bytes along a row, `tile` rows.
+//
+// Measured on MI355X (us forward / reverse, caches flushed; 16x32, 16x64,
+// 8x128, 8x256):
+//   bf16 [512,32,2560]   75/145  104/217  201/370  388/709
+//   bf16 [256,64,2560]   77/154   68/142  112/211  203/367
+//   bf16 [64,200,2560]   67/130   66/134   68/134   70/127
+//   bf16 [8,2048,2560]     -      74/153   75/151   77/151
+//   bf16 [1,131072,1024]   -     572/ -   251/ -   236/ -
+//   bf16 [1,131072,256]    -      - /503    - /212   - /152
+//   bf16 [1,4096,2560]   49/62    35/57    30/57    34/61
+//   f32  [4,2048,4096]     -      97/214   95/194   93/193
+// So a tile is no taller than a short sequence.  Otherwise few chains of tall
+// tiles: a chain hands its state on about every 0.28 us, so 64-row tiles want
+// some 64 chains of them to keep the memory busy, and tall ones enough tiles
+// (2048) to fill the GPU evenly.  With many chains the bf16 forward is fastest
+// in wide tiles: its arithmetic is as long as its loads, and 64 rows leave
+// registers for a third wavefront to overlap them.
 struct GatedTile {
     int width, tile;
 };
-GatedTile gated_tile(const Shape&, int) { return GatedTile{8, 256}; }
-
-template <int DT, int NR, int WAVES>
-using FwdCfg = GCfg<DT, 8, NR, WAVES, 8, 2, 2>;
-template <int DT>
-using BwdCfg = GCfg<DT, 8, 4, 8, 8, 2, 2>;
+GatedTile gated_tile(const Shape& s, int dir) {
+    const int64_t row = s.D * (s.dtype == DT_F32 ? 4 : 2);
+    const int64_t chains16 = s.B * ((row + 255) / 256), chains8 = s.B * ((row + 127) / 128);
+    const bool wide = row > 128;
+    if (s.T <= 32 && wide) return GatedTile{16, 32};
+    if (s.T <= 64 && wide) return GatedTile{16, 64};
+    if (dir == 0 && s.dtype == DT_BF16 && wide && chains16 >= 64) return GatedTile{16, 64};
+    const int64_t tall = (s.T + 255) / 256;
+    if (chains8 * tall >= 2048 && tall * 256 <= s.T + s.T / 4) return GatedTile{8, 256};
+    return GatedTile{8, 128};
+}
 
 template <class C, bool AL>
 void fwd_cfg(const GatedFwdArgs& x, hipStream_t st) {
@@ -569,17 +671,19 @@ void bwd_cfg(const GatedBwdArgs& x, hipStream_t st) {
     else hipLaunchKernelGGL((gated_bwd_kernel<C, AL, false>), grid, block, 0, st, x);
 }
 
-template <int DT>
-void fwd_t(bool al, const GatedFwdArgs& x, hipStream_t st) {
-    using C = FwdCfg<DT, 8, 4>;
-    if (al) fwd_cfg<C, true>(x, st);
-    else fwd_cfg<C, false>(x, st);
+template <int DT, bool AL>
+void fwd_t(const GatedTile& t, const GatedFwdArgs& x, hipStream_t st) {
+    if (t.tile == 32) fwd_cfg<Tile16x32<DT>, AL>(x, st);
+    else if (t.tile == 64) fwd_cfg<Tile16x64<DT>, AL>(x, st);
+    else if (t.tile == 128) fwd_cfg<Tile8x128<DT>, AL>(x, st);
+    else fwd_cfg<Tile8x256<DT>, AL>(x, st);
 }
-template <int DT>
-void bwd_t(bool al, const GatedBwdArgs& x, hipStream_t st) {
-    using C = BwdCfg<DT>;
-    if (al) bwd_cfg<C, true>(x, st);
-    else bwd_cfg<C, false>(x, st);
+template <int DT, bool AL>
+void bwd_t(const GatedTile& t, const GatedBwdArgs& x, hipStream_t st) {
+    if (t.tile == 32) bwd_cfg<Tile16x32<DT>, AL>(x, st);
+    else if (t.tile == 64) bwd_cfg<Tile16x64<DT>, AL>(x, st);
+    else if (t.tile == 128) bwd_cfg<Tile8x128<DT>, AL>(x, st);
+    else bwd_cfg<Tile8x256<DT>, AL>(x, st);
 }
 
 Layout gated_layout(const GatedShape& s, int dir) {
@@ -608,7 +712,7 @@ bool gated_fused_fits(const GatedShape& s, int dir, const size_t* row_strides, i
     if ((unsigned long long)((s.T + t.tile - 1) / t.tile) * (unsigned long long)(s.B * ((s.D + L.W - 1) / L.W)) >=
         0xffffffffull)
         return false;
-    return grid_fits(L, 1024);
+    return grid_fits(L, 4 * kWave);
 }
 
 size_t gated_fused_bytes(const GatedShape& s) {
@@ -630,8 +734,9 @@ hipError_t launch_gated_fused_fwd(const GatedShape& s, const GatedFwd& p, void* 
     x.d = Dims{(int)s.T, (int)s.D, L.nW, L.nS, L.NK};
     x.polls = polls > 0 ? (uint32_t)polls : kDefaultPolls;
     const bool al = gated_fwd_aligned(s, p);
-    if (s.dtype == DT_F32) fwd_t<DT_F32>(al, x, st);
-    else fwd_t<DT_BF16>(al, x, st);
+    const GatedTile t = gated_tile(Shape{s.B, s.T, s.D, s.dtype}, 0);
+    if (s.dtype == DT_F32) al ? fwd_t<DT_F32, true>(t, x, st) : fwd_t<DT_F32, false>(t, x, st);
+    else al ? fwd_t<DT_BF16, true>(t, x, st) : fwd_t<DT_BF16, false>(t, x, st);
     return hipGetLastError();
 }
 
@@ -646,8 +751,9 @@ hipError_t launch_gated_fused_bwd(const GatedShape& s, const GatedBwd& p, float*
     x.d = Dims{(int)s.T, (int)s.D, L.nW, L.nS, L.NK};
     x.polls = polls > 0 ? (uint32_t)polls : kDefaultPolls;
     const bool al = gated_bwd_aligned(s, p);
-    if (s.dtype == DT_F32) bwd_t<DT_F32>(al, x, st);
-    else bwd_t<DT_BF16>(al, x, st);
+    const GatedTile t = gated_tile(Shape{s.B, s.T, s.D, s.dtype}, 1);
+    if (s.dtype == DT_F32) al ? bwd_t<DT_F32, true>(t, x, st) : bwd_t<DT_F32, false>(t, x, st);
+    else al ? bwd_t<DT_BF16, true>(t, x, st) : bwd_t<DT_BF16, false>(t, x, st);
     return hipGetLastError();
 }
 

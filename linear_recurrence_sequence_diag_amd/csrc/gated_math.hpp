@@ -40,17 +40,16 @@ __device__ __forceinline__ float sigmoid_f(float x) {
 }
 
 // sigmoid(x) with its complement, 1 - sigmoid(x) = e^-x sigmoid(x), which keeps
-// its digits where the sigmoid is near 1.  The exponent is capped at 126 so
-// that the product never is infinity times zero (at x = -87.3, where the
-// sigmoid is 1e-38); written as a comparison, which a NaN passes through.
+// its digits where the sigmoid is near 1.  Below x = -88 the product is
+// infinity times zero; the minimum with 1 takes the 1 there.  (It takes the 1
+// for a NaN too, which the sigmoid itself still carries.)
 struct Sigmoid {
     float s, c;
 };
 __device__ __forceinline__ Sigmoid sigmoid_pair(float x) {
-    const float t = x * -kLog2e;
-    const float e = __builtin_amdgcn_exp2f(t > 126.0f ? 126.0f : t);
+    const float e = __builtin_amdgcn_exp2f(x * -kLog2e);
     const float s = __builtin_amdgcn_rcpf(1.0f + e);
-    return Sigmoid{s, e * s};
+    return Sigmoid{s, fminf(e * s, 1.0f)};
 }
 
 // 1 - a^2 for a = 2^y2, y2 <= 0.  Near a = 1 the difference would cancel (a
@@ -90,10 +89,11 @@ __device__ __forceinline__ float gated_a_of(float gr, float rate) {
 // Gradients of one step from its adjoint lam and the state before it:
 //   du = lam beta,  dx = du i,  dgi = dx x (1 - i),
 //   P = y dL/dy = lam a y (h_prev - a u / beta),  dgr = P (1 - r),
-// and sum P gives grad_decay.  y / beta is finite down to beta = 0 (y and
+// and sum P gives grad_decay (times ln 2 for a y in units of log 2).  y / beta is finite down to beta = 0 (y and
 // beta^2 vanish together), so P is formed from a y2 and y2 / beta.
+// a is the transition, and p is P / ln 2 (its sum takes the factor once).
 struct GatedGrad {
-    float dx, dgr, dgi, p;
+    float dx, dgr, dgi, p, a;
 };
 __device__ __forceinline__ GatedGrad gated_grad_of(float x, float gr, float gi, float rate,
                                                    float h_prev, float lam) {
@@ -109,8 +109,9 @@ __device__ __forceinline__ GatedGrad gated_grad_of(float x, float gr, float gi, 
     o.dx = (lam * (v * inv)) * ig.s;
     o.dgi = (o.dx * x) * ig.c;
     const float ay = a * y2;
-    o.p = (lam * kLn2) * (ay * h_prev - (a * ay) * (inv * (ig.s * x)));
-    o.dgr = o.p * r.c;
+    o.p = lam * (ay * fmaf(-a, inv * (ig.s * x), h_prev));
+    o.dgr = o.p * (kLn2 * r.c);
+    o.a = a;
     return o;
 }
 __device__ __forceinline__ GatedGrad gated_start_grad_of(float x, float gi, float lam) {
@@ -120,6 +121,7 @@ __device__ __forceinline__ GatedGrad gated_start_grad_of(float x, float gi, floa
     o.dgi = (o.dx * x) * ig.c;
     o.p = 0.0f;
     o.dgr = 0.0f;
+    o.a = 0.0f;
     return o;
 }
 

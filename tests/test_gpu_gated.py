@@ -80,7 +80,8 @@ class Case:
 
 ALGOS = ["auto", "seq", "fused"]
 SHAPES = [(1, 1, 1), (2, 3, 5), (3, 17, 8), (2, 64, 64), (1, 65, 131), (2, 257, 130), (1, 300, 72), (5, 129, 520),
-          (2, 700, 33), (3, 513, 256), (70, 5, 100), (1, 2100, 24)]
+          (2, 700, 33), (3, 513, 256), (70, 5, 100), (1, 2100, 24),
+          (64, 130, 256), (700, 700, 5)]  # wide tiles over many chains; tall tiles, many of them
 
 
 @pytest.mark.parametrize("algo", ALGOS)
