@@ -105,6 +105,8 @@ _lib = None
 def library():
     """The loaded liblrscan (ctypes.CDLL).  Raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -270,9 +272,12 @@ def _opts(opts):
     return ctypes.byref(opts) if opts is not None else None
 
 
+_I64_ARRAYS = [_I64 * n for n in range(13)]
+
+
 def _i64s(values):
     """A host array of int64 (None: NULL)."""
-    return None if values is None else (_I64 * len(values))(*values)
+    return None if values is None else _I64_ARRAYS[len(values)](*values)
 
 
 def scan_gated_fwd(x, gate_r, gate_i, decay, scale, out, last, B, T, D, dtype, strides, stream,
@@ -628,39 +633,54 @@ def samu_scan_backward(eta, delta, nu_log, theta_log, out_r, out_i, grad_out_r, 
 
 
 # ---- gated scan, short causal convolution, embedding ----
+# A decode step's launch takes the GPU a few microseconds, so these helpers look
+# at each tensor once and switch devices only where they have to.
+def _enqueue(ref, call, *args):
+    """call(*args, stream) with ref's device current; the current stream there."""
+    torch = _torch()
+    index = ref.device.index
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if index == torch.cuda.current_device():
+        return call(*args, stream)
+    with torch.cuda.device(index):
+        return call(*args, stream)
+
+
 def _check_rows(name, t, ref, dims):
     """An operand whose rows may be strided: contiguous along the last dimension."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, _torch().Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA (HIP) tensor")
-    if t.dim() != dims:
-        raise ValueError(f"{name} must be [{'B, T, D' if dims == 3 else 'B, D'}]")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name} must be contiguous along its last dimension")
     if t is not ref and (t.shape != ref.shape or t.dtype != ref.dtype or t.device != ref.device):
         raise ValueError(f"{name} must match x in shape, dtype and device")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must be [{'B, T, D' if dims == 3 else 'B, D'}]")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name} must be contiguous along its last dimension")
 
 
 def _strides(*tensors):
     """(batch, step) strides of [B, T, D] tensors, or batch strides of [B, D]
-    ones, for the C ABI; a dimension of one takes the contiguous value (torch
-    leaves it arbitrary)."""
+    ones, for the C ABI, or None where all are contiguous; a dimension of one
+    takes the contiguous value (torch leaves it arbitrary)."""
+    if all(t.is_contiguous() for t in tensors):
+        return None
     out = []
     for t in tensors:
-        width = t.shape[-1]
-        if t.dim() == 2:
-            out.append(t.stride(0) if t.shape[0] > 1 else width)
+        shape, stride = t.shape, t.stride()
+        width = shape[-1]
+        if len(shape) == 2:
+            out.append(stride[0] if shape[0] > 1 else width)
             continue
-        out.append(t.stride(0) if t.shape[0] > 1 else t.shape[1] * width)
-        out.append(t.stride(1) if t.shape[1] > 1 else width)
+        out.append(stride[0] if shape[0] > 1 else shape[1] * width)
+        out.append(stride[1] if shape[1] > 1 else width)
     return out
 
 
 def _check_param(name, t, shape, ref):
     """A float32 parameter on x's device."""
     torch = _torch()
-    if (not isinstance(t, torch.Tensor) or tuple(t.shape) != tuple(shape)
-            or t.dtype != torch.float32 or t.device != ref.device or not t.is_contiguous()):
+    if (not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype != torch.float32
+            or t.device != ref.device or not t.is_contiguous()):
         dims = ", ".join(str(n) for n in shape)
         raise ValueError(f"{name} must be a contiguous float32 [{dims}] tensor on x's device")
 
@@ -692,11 +712,10 @@ def gated_scan(x, gate_r, gate_i, decay, scale=8.0, h0=None, reset=None, algo="a
         raise ValueError("a forward needs out or last")
     out = torch.empty((B, T, D), device=x.device, dtype=x.dtype) if with_out else None
     last = torch.empty((B, D), device=x.device, dtype=torch.float32) if with_last else None
-    with torch.cuda.device(x.device):
-        scan_gated_fwd(x.data_ptr(), gate_r.data_ptr(), gate_i.data_ptr(), decay.data_ptr(), scale,
-                       _ptr(out), _ptr(last), B, T, D, dtype_code(x.dtype),
-                       _strides(x, gate_r, gate_i), _stream(x),
-                       make_opts(algo, h0=h0, reset=reset, polls=polls, workspace=workspace))
+    opts = make_opts(algo, h0=h0, reset=reset, polls=polls, workspace=workspace)
+    _enqueue(x, lambda *a: scan_gated_fwd(*a, opts), x.data_ptr(), gate_r.data_ptr(),
+             gate_i.data_ptr(), decay.data_ptr(), scale, _ptr(out), _ptr(last), B, T, D,
+             dtype_code(x.dtype), _strides(x, gate_r, gate_i))
     return out, last
 
 
@@ -726,13 +745,11 @@ def gated_scan_backward(x, gate_r, gate_i, decay, out, grad_out, scale=8.0, grad
     gx, gr, gi = grads
     gd = torch.empty((D,), device=x.device, dtype=torch.float32)
     gh0 = torch.empty((B, D), device=x.device, dtype=torch.float32) if need_grad_h0 else None
-    with torch.cuda.device(x.device):
-        scan_gated_bwd(x.data_ptr(), gate_r.data_ptr(), gate_i.data_ptr(), decay.data_ptr(), scale,
-                       out.data_ptr(), grad_out.data_ptr(), _ptr(grad_last), gx.data_ptr(),
-                       gr.data_ptr(), gi.data_ptr(), gd.data_ptr(), B, T, D, dtype_code(x.dtype),
-                       _strides(x, gate_r, gate_i, gx, gr, gi), _stream(x),
-                       make_opts(algo, h0=h0, grad_h0=gh0, reset=reset, polls=polls,
-                                 workspace=workspace))
+    opts = make_opts(algo, h0=h0, grad_h0=gh0, reset=reset, polls=polls, workspace=workspace)
+    _enqueue(x, lambda *a: scan_gated_bwd(*a, opts), x.data_ptr(), gate_r.data_ptr(),
+             gate_i.data_ptr(), decay.data_ptr(), scale, out.data_ptr(), grad_out.data_ptr(),
+             _ptr(grad_last), gx.data_ptr(), gr.data_ptr(), gi.data_ptr(), gd.data_ptr(), B, T, D,
+             dtype_code(x.dtype), _strides(x, gate_r, gate_i, gx, gr, gi))
     return gx, gr, gi, gd, gh0
 
 
@@ -754,10 +771,9 @@ def gated_step(x, gate_r, gate_i, decay, state=None, scale=8.0, reset=None, with
     out = torch.empty((B, D), device=x.device, dtype=x.dtype) if with_out else None
     new = out_state if out_state is not None else torch.empty((B, D), device=x.device,
                                                               dtype=torch.float32)
-    with torch.cuda.device(x.device):
-        scan_gated_step(x.data_ptr(), gate_r.data_ptr(), gate_i.data_ptr(), decay.data_ptr(), scale,
-                        _ptr(state), _ptr(reset), _ptr(out), new.data_ptr(), B, D,
-                        dtype_code(x.dtype), _strides(x, gate_r, gate_i), _stream(x))
+    _enqueue(x, scan_gated_step, x.data_ptr(), gate_r.data_ptr(), gate_i.data_ptr(),
+             decay.data_ptr(), scale, _ptr(state), _ptr(reset), _ptr(out), new.data_ptr(), B, D,
+             dtype_code(x.dtype), _strides(x, gate_r, gate_i))
     return out, new
 
 
@@ -807,10 +823,9 @@ def short_conv(x, weight, bias=None, state=None, reset=None, activation=None, wi
     out = torch.empty((B, T, D), device=x.device, dtype=x.dtype)
     last = (torch.empty((B, max(K - 1, 0), D), device=x.device, dtype=x.dtype) if with_last
             else None)
-    with torch.cuda.device(x.device):
-        scan_conv_fwd(x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(state), _ptr(reset),
-                      _activation(activation), out.data_ptr(), _ptr(last), B, T, D, K,
-                      dtype_code(x.dtype), _strides(x), _stream(x))
+    _enqueue(x, scan_conv_fwd, x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(state),
+             _ptr(reset), _activation(activation), out.data_ptr(), _ptr(last), B, T, D, K,
+             dtype_code(x.dtype), _strides(x))
     return out, last
 
 
@@ -834,11 +849,10 @@ def short_conv_backward(x, weight, bias, grad_out, state=None, grad_last=None, r
     gs = (torch.empty((B, max(K - 1, 0), D), device=x.device, dtype=x.dtype) if need_grad_state
           else None)
     opts = make_opts(workspace=workspace)
-    with torch.cuda.device(x.device):
-        scan_conv_bwd(x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(state), _ptr(reset),
-                      _activation(activation), grad_out.data_ptr(), _ptr(grad_last), gx.data_ptr(),
-                      gw.data_ptr(), _ptr(gb), _ptr(gs), B, T, D, K, dtype_code(x.dtype),
-                      _strides(x, gx), _stream(x), opts)
+    _enqueue(x, lambda *a: scan_conv_bwd(*a, opts), x.data_ptr(), weight.data_ptr(), _ptr(bias),
+             _ptr(state), _ptr(reset), _activation(activation), grad_out.data_ptr(),
+             _ptr(grad_last), gx.data_ptr(), gw.data_ptr(), _ptr(gb), _ptr(gs), B, T, D, K,
+             dtype_code(x.dtype), _strides(x, gx))
     return gx, gw, gb, gs
 
 
@@ -855,10 +869,9 @@ def short_conv_step(x, weight, bias=None, state=None, reset=None, activation=Non
     out = torch.empty((B, D), device=x.device, dtype=x.dtype)
     new = (out_state if out_state is not None
            else torch.empty((B, max(K - 1, 0), D), device=x.device, dtype=x.dtype))
-    with torch.cuda.device(x.device):
-        scan_conv_step(x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(state), _ptr(reset),
-                       _activation(activation), out.data_ptr(), new.data_ptr(), B, D, K,
-                       dtype_code(x.dtype), _strides(x), _stream(x))
+    _enqueue(x, scan_conv_step, x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(state),
+             _ptr(reset), _activation(activation), out.data_ptr(), new.data_ptr(), B, D, K,
+             dtype_code(x.dtype), _strides(x))
     return out, new
 
 
@@ -880,9 +893,8 @@ def embed(ids, weight, scale=1.0):
     id_bytes = _check_ids(ids, weight)
     V, D = weight.shape
     out = torch.empty((*ids.shape, D), device=weight.device, dtype=weight.dtype)
-    with torch.cuda.device(weight.device):
-        scan_embed_fwd(ids.data_ptr(), id_bytes, weight.data_ptr(), scale, out.data_ptr(),
-                       ids.numel(), V, D, dtype_code(weight.dtype), _stream(weight))
+    _enqueue(weight, scan_embed_fwd, ids.data_ptr(), id_bytes, weight.data_ptr(), scale,
+             out.data_ptr(), ids.numel(), V, D, dtype_code(weight.dtype))
     return out
 
 
@@ -906,11 +918,10 @@ def embed_backward(ids, grad_out, rows, scale=1.0, grad_weight=None, workspace=N
                          "float32 on its device")
     gw = grad_weight if add else torch.empty((rows, D), device=grad_out.device,
                                              dtype=grad_out.dtype)
-    with torch.cuda.device(grad_out.device):
-        scan_embed_bwd(ids.data_ptr(), id_bytes, grad_out.data_ptr(), scale, gw.data_ptr(),
-                       dtype_code(gw.dtype), int(add), ids.numel(), rows, D,
-                       dtype_code(grad_out.dtype), _stream(grad_out),
-                       make_opts(workspace=workspace))
+    opts = make_opts(workspace=workspace)
+    _enqueue(grad_out, lambda *a: scan_embed_bwd(*a, opts), ids.data_ptr(), id_bytes,
+             grad_out.data_ptr(), scale, gw.data_ptr(), dtype_code(gw.dtype), int(add),
+             ids.numel(), rows, D, dtype_code(grad_out.dtype))
     return gw
 
 

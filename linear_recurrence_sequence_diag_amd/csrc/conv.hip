@@ -8,15 +8,23 @@
 // Inputs before the first come from `state` (the K - 1 inputs before it) or are
 // zero, and a tap that would reach across a reset counts as zero.
 //
-// A thread owns V adjacent channels (16 bytes) of a chunk of consecutive
-// tokens.  The last K - 1 inputs stay in registers, so a chunk re-reads only
-// K - 1 rows of its neighbour; a reset clears them, which drops an infinity or
-// NaN of the segment before.  The backward walks the chunk in the same order,
-// recomputes z, and keeps the K - 1 input gradients that still wait for later
-// gz in registers.  The parameter gradients are summed over the chunk in
-// registers, over a workgroup's chunks through LDS, and over workgroups by
-// column_sum, each in a fixed order.
+// A thread owns four adjacent channels of a chunk of consecutive
+// tokens and walks it in groups of four, whose rows are loaded together.  The
+// last K - 1 inputs stay in registers, so a chunk re-reads only K - 1 rows of
+// its neighbour; a reset clears them, which drops an infinity or NaN of the
+// segment before.  The backward walks in the same order, recomputes z, and
+// keeps the K - 1 input gradients that still wait for later gz in registers.
+// The parameter gradients are summed over the chunk in registers, over a
+// workgroup's chunks through LDS, and over workgroups by column_sum, each in a
+// fixed order.
+//
+// Resets and the ends of a row are rare, so what they need runs under
+// wavefront-wide branches; everything else is straight-line code, in which the
+// moving window costs no instruction.  (With a test of every thread at every
+// row the window was moved through copies, a quarter of all instructions.)
 #include "conv.hpp"
+
+#include <type_traits>
 
 #include "column_sum.hpp"
 #include "gated_math.hpp"
@@ -27,15 +35,85 @@ namespace lrscan {
 namespace {
 
 constexpr int kBlock = 256;
-constexpr int kFwdRows = 16;  // tokens of a chunk
-constexpr int kBwdRows = 32;
+// Tokens whose rows are loaded together: a multiple of K - 1, so that the
+// window's and the waiting gradients' places in their rings are constants.
+constexpr int group_of(int K) { return K == 4 ? 6 : 4; }
+
+constexpr int V = 4;       // channels of a thread
+
+// Four adjacent channels of a row as they are stored.  (A thread with all
+// eight bf16 channels of 16 bytes held about 180 registers in the backward,
+// which left two wavefronts a SIMD.)  FULL: rows are whole quads; then a quad
+// is one access, whatever its address is aligned to, else the last one of a
+// row goes channel by channel.
+template <int DT>
+struct Quad {
+    static constexpr int S = Elem<DT>::bytes;
+    static constexpr int W = DT == DT_F32 ? 4 : 2;  // dwords
+    typedef unsigned int Raw __attribute__((ext_vector_type(W), aligned(S)));
+    Raw w;
+    __device__ __forceinline__ static Quad zero() {
+        Quad q;
+#pragma unroll
+        for (int i = 0; i < W; ++i) q.w[i] = 0u;
+        return q;
+    }
+    __device__ __forceinline__ float get(int j) const {
+        if constexpr (DT == DT_F32) return __uint_as_float(w[j]);
+        else return (j & 1) ? __uint_as_float(w[j >> 1] & 0xffff0000u) : __uint_as_float(w[j >> 1] << 16);
+    }
+    __device__ __forceinline__ void set(const float (&v)[V]) {
+        if constexpr (DT == DT_F32) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) w[j] = __float_as_uint(v[j]);
+        } else {
+            w[0] = pack_bf16x2(v[0], v[1]);
+            w[1] = pack_bf16x2(v[2], v[3]);
+        }
+    }
+    template <bool FULL>
+    __device__ __forceinline__ static Quad load(const char* p, int nvalid) {
+        Quad q = zero();
+        if (FULL || nvalid == V) {
+            q.w = __builtin_nontemporal_load(reinterpret_cast<const Raw*>(p));
+        } else {
+            float v[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) v[j] = j < nvalid ? Elem<DT>::load1(p, j) : 0.0f;
+            q.set(v);
+        }
+        return q;
+    }
+    template <bool FULL>
+    __device__ __forceinline__ void store(char* p, int nvalid) const {
+        if (FULL || nvalid == V) {
+            __builtin_nontemporal_store(w, reinterpret_cast<Raw*>(p));
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (j < nvalid) Elem<DT>::store1(p, j, get(j));
+        }
+    }
+};
+
+// Tokens of a chunk.  The backward's walk goes K - 1 tokens past its chunk, so
+// that walk is what is a whole number of groups.
+//
+// Long chunks re-read less, short ones make more wavefronts: the longest of five
+// lengths that leaves ten wavefronts for each of the 256 CUs (bf16, K = 4,
+// reverse: [8, 2048, 2560] 72 us in chunks of 57 tokens, 96 in 15; [1, 2048,
+// 1024] 40 in 57, 17 in 9).  A thread of four channels beats one of eight there
+// (72 against 85; forward 43 against 48): its state leaves four wavefronts a SIMD
+// in the reverse walk and eight in the forward one.
+int fwd_rows(const ConvShape& s);
+int bwd_rows(const ConvShape& s);
 
 // Workgroup blockIdx.x covers lane block blockIdx.x % ncb and `groups`
 // consecutive chunks (a chunk: `rows` tokens of one batch row).
 struct ConvGrid {
     uint32_t tpr;      // threads along a row (a power of two, at most 64)
     uint32_t groups;   // kBlock / tpr chunks side by side
-    uint32_t vpr;      // vectors in a row
+    uint32_t vpr;      // quads in a row
     uint32_t ncb;      // lane blocks
     uint32_t nchunks;  // chunks of a batch row
     uint32_t chunks;   // B * nchunks
@@ -46,10 +124,9 @@ struct ConvGrid {
 int64_t chunks_of(const ConvShape& s, int rows) { return s.B * ((s.T + rows - 1) / rows); }
 
 ConvGrid conv_grid(const ConvShape& s, int rows) {
-    const int v = s.dtype == DT_F32 ? Elem<DT_F32>::V : Elem<DT_BF16>::V;
     ConvGrid g;
     g.rows = rows;
-    g.vpr = (uint32_t)((s.D + v - 1) / v);
+    g.vpr = (uint32_t)((s.D + V - 1) / V);
     g.tpr = 1;
     while (g.tpr < 64 && g.tpr < g.vpr) g.tpr *= 2;
     g.groups = kBlock / g.tpr;
@@ -60,59 +137,53 @@ ConvGrid conv_grid(const ConvShape& s, int rows) {
     return g;
 }
 
+int chunk_groups(const ConvShape& s) {
+    const int u = group_of(s.K);
+    const int64_t per = (s.D + V * 64 - 1) / (V * 64);  // wavefronts to a row
+    for (const int n : {60 / u, 30 / u, 3, 2})
+        if (s.B * ((s.T + n * u - 1) / (n * u)) * per >= 2560) return n;
+    return 1;
+}
+int fwd_rows(const ConvShape& s) { return chunk_groups(s) * group_of(s.K); }
+int bwd_rows(const ConvShape& s) {
+    const int n = chunk_groups(s);
+    return (n > 1 ? n : 2) * group_of(s.K) - (s.K - 1);
+}
+
 struct ConvPos {
     int64_t bi, t0, t1, d0;  // batch row, tokens [t0, t1), first channel
-    int nvalid;              // channels of the vector that exist; 0: an idle thread
+    int nvalid;              // channels of the quad that exist; 0: an idle thread
 };
 
-template <int V>
+// UNI: a wavefront lies in one chunk (rows of more than 32 quads), so chunk,
+// tokens and row addresses are scalars.
+template <bool UNI>
 __device__ __forceinline__ ConvPos conv_pos(const ConvGrid& g, int64_t T, int64_t D) {
     const uint32_t cb = blockIdx.x % g.ncb, rb = blockIdx.x / g.ncb;
-    const uint32_t lane = threadIdx.x & (g.tpr - 1), grp = threadIdx.x / g.tpr;
+    const uint32_t lane = threadIdx.x & (g.tpr - 1);
+    const uint32_t grp = UNI ? uniform((int)(threadIdx.x / kWave)) : threadIdx.x / g.tpr;
     const uint32_t chunk = rb * g.groups + grp, vec = cb * g.tpr + lane;
     ConvPos p;
     p.nvalid = 0;
     p.bi = p.t0 = p.t1 = p.d0 = 0;
-    if (chunk >= g.chunks || vec >= g.vpr) return p;
+    if (chunk >= g.chunks) return p;
     const uint32_t b = chunk / g.nchunks;
     p.bi = b;
     p.t0 = (int64_t)(chunk - b * g.nchunks) * g.rows;
     p.t1 = p.t0 + g.rows < T ? p.t0 + g.rows : T;
     p.d0 = (int64_t)vec * V;
-    p.nvalid = (int)((D - p.d0) < V ? (D - p.d0) : V);
+    p.nvalid = vec >= g.vpr ? 0 : (int)((D - p.d0) < V ? (D - p.d0) : V);
     return p;
 }
 
-// The K - 1 inputs before token t0, oldest first, those of an earlier segment
-// cleared.
-template <int DT, bool ALIGNED, int K>
-__device__ __forceinline__ void conv_warm(RowVec<DT> (&win)[K - 1], const Rows& x, const void* state,
-                                          const uint8_t* reset, const ConvPos& p, int64_t T, int64_t D) {
-#pragma unroll
-    for (int j = 0; j < K - 1; ++j) {
-        const int64_t t = p.t0 - (K - 1) + j;
-        if (t >= 0)
-            win[j] = load_row<DT, ALIGNED>(x.row(p.bi, t), (size_t)p.d0, p.nvalid, 0.0f);
-        else if (state)
-            win[j] = load_row<DT, ALIGNED>(state, (size_t)((p.bi * (K - 1) + t + K - 1) * D + p.d0),
-                                           p.nvalid, 0.0f);
-        else
-            win[j] = RowVec<DT>::splat(0.0f);
-        if (reset && t >= 0 && reset[p.bi * T + t]) {
-#pragma unroll
-            for (int i = 0; i < j; ++i) win[i] = RowVec<DT>::splat(0.0f);
-        }
-    }
+// Whether a condition on the chunk holds for some thread of the wavefront.
+template <bool UNI>
+__device__ __forceinline__ bool some(bool c) {
+    if constexpr (UNI) return c;
+    else return __any(c);
 }
 
-template <int DT, int K>
-__device__ __forceinline__ void conv_push(RowVec<DT> (&win)[K - 1], const RowVec<DT>& x) {
-#pragma unroll
-    for (int j = 0; j + 1 < K - 1; ++j) win[j] = win[j + 1];
-    win[K - 2] = x;
-}
-
-template <int V, int K>
+template <int K>
 struct Taps {
     float w[K][V], bias[V];
     __device__ __forceinline__ void load(const float* wp, const float* bp, const ConvPos& p, int64_t D) {
@@ -123,68 +194,156 @@ struct Taps {
             bias[j] = (bp && j < p.nvalid) ? bp[p.d0 + j] : 0.0f;
         }
     }
+    // The window is a ring whose oldest token is at place `u` modulo K - 1.
     template <int DT>
-    __device__ __forceinline__ float z(const RowVec<DT> (&win)[K - 1], const RowVec<DT>& x, int j) const {
+    __device__ __forceinline__ float z(const Quad<DT> (&win)[K - 1], const Quad<DT>& x, int u, int j) const {
         float z = bias[j];
 #pragma unroll
-        for (int k = 0; k < K - 1; ++k) z = fmaf(w[k][j], win[k].get(j), z);
+        for (int k = 0; k < K - 1; ++k) z = fmaf(w[k][j], win[(u + k) % (K - 1)].get(j), z);
         return fmaf(w[K - 1][j], x.get(j), z);
     }
 };
 
-template <int DT, bool ALIGNED, int K, bool SILU>
-__global__ __launch_bounds__(kBlock) void conv_fwd_kernel(ConvFwd a, ConvGrid g, int64_t T, int64_t D) {
-    constexpr int V = Elem<DT>::V, U = 4;
-    const ConvPos p = conv_pos<V>(g, T, D);
-    if (p.nvalid == 0) return;
-    Taps<V, K> tp;
-    tp.load(a.w, a.bias, p, D);
-    RowVec<DT> win[K - 1];
-    conv_warm<DT, ALIGNED, K>(win, a.x, a.state, a.reset, p, T, D);
-    for (int64_t t = p.t0; t < p.t1; t += U) {
-        RowVec<DT> x[U];
-        bool start[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t tu = t + u < p.t1 ? t + u : p.t1 - 1;
-            x[u] = load_row<DT, ALIGNED>(a.x.row(p.bi, tu), (size_t)p.d0, p.nvalid, 0.0f);
-            start[u] = a.reset && a.reset[p.bi * T + tu];
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (t + u < p.t1) {
-                if (start[u]) {
-#pragma unroll
-                    for (int j = 0; j < K - 1; ++j) win[j] = RowVec<DT>::splat(0.0f);
-                }
-                RowOut<DT> o;
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float z = tp.z(win, x[u], j);
-                    o.v[j] = SILU ? z * sigmoid_f(z) : z;
-                }
-                store_row<DT, ALIGNED>(a.out, (size_t)((p.bi * T + t + u) * D + p.d0), p.nvalid, o);
-                conv_push<DT, K>(win, x[u]);
+// Segment starts of a chunk.  A wavefront in one chunk reads the mask of the
+// whole walk (the window before it too, at most 63 tokens) with one load, a
+// token to a lane, and keeps it as a scalar; otherwise each thread reads its
+// group's bytes.
+template <bool UNI, int K>
+struct Starts {
+    const uint8_t* row;  // mask of the batch row, or NULL
+    int64_t t0, T;
+    unsigned long long bits;  // UNI: bit i for token t0 - (K - 1) + i
+    __device__ __forceinline__ void init(const uint8_t* reset, int64_t bi, int64_t from, int64_t len) {
+        row = reset ? reset + bi * len : nullptr;
+        t0 = from;
+        T = len;
+        if constexpr (UNI) {
+            bits = 0;
+            if (reset) {
+                const int64_t t = t0 - (K - 1) + (int64_t)(threadIdx.x % kWave);
+                bits = __ballot(t >= 0 && t < T && row[t < 0 ? 0 : (t < T ? t : T - 1)] != 0);
             }
         }
     }
-    if (a.last && p.t1 == T) {
+    __device__ __forceinline__ bool at(int64_t t) const {  // for the window
+        if constexpr (UNI) return (bits >> (int)(t - t0 + K - 1)) & 1u;
+        else return row && t >= 0 && row[t];
+    }
+    // tokens t .. t + U - 1, bit u for token t + u
+    template <int U>
+    __device__ __forceinline__ uint32_t group(int64_t t) const {
+        if constexpr (UNI) return (uint32_t)(bits >> (int)(t - t0 + K - 1)) & ((1u << U) - 1u);
+        if (!row) return 0;
+        uint32_t m = 0;
 #pragma unroll
-        for (int j = 0; j < K - 1; ++j) {
-            RowOut<DT> o;
+        for (int u = 0; u < U; ++u)
+            if (t + u < T && row[t + u]) m |= 1u << u;
+        return m;
+    }
+};
+
+// The K - 1 inputs before token t0, oldest first, those of an earlier segment
+// cleared.
+template <int DT, bool FULL, bool UNI, int K>
+__device__ __forceinline__ void conv_warm(Quad<DT> (&win)[K - 1], const Rows& x, const void* state,
+                                          const Starts<UNI, K>& starts, const ConvPos& p, int64_t D,
+                                          uint32_t lo) {
+    constexpr int S = Elem<DT>::bytes;
 #pragma unroll
-            for (int v = 0; v < V; ++v) o.v[v] = win[j].get(v);
-            store_row<DT, ALIGNED>(a.last, (size_t)((p.bi * (K - 1) + j) * D + p.d0), p.nvalid, o);
+    for (int j = 0; j < K - 1; ++j) {
+        const int64_t t = p.t0 - (K - 1) + j;
+        if (t >= 0)
+            win[j] = Quad<DT>::template load<FULL>(x.row(p.bi, t) + lo, p.nvalid);
+        else if (state)
+            win[j] = Quad<DT>::template load<FULL>(
+                static_cast<const char*>(state) + (size_t)((p.bi * (K - 1) + t + K - 1) * D) * S + lo,
+                p.nvalid);
+        else
+            win[j] = Quad<DT>::zero();
+        if (starts.at(t)) {
+#pragma unroll
+            for (int i = 0; i < j; ++i) win[i] = Quad<DT>::zero();
         }
     }
 }
 
-template <int DT, bool ALIGNED, int K, bool SILU>
-__global__ __launch_bounds__(kBlock) void conv_bwd_kernel(ConvBwd a, ConvGrid g, int64_t T, int64_t D,
+// The rows of a group; those past token T - 1 (ANY: there may be some) are that
+// token's.
+template <int DT, bool FULL, bool ANY, int U>
+__device__ __forceinline__ void load_group(Quad<DT> (&r)[U], const char* p, size_t st, uint32_t lo, int64_t t,
+                                           int64_t T, int nvalid) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        int64_t d = u;
+        if (ANY && t + u >= T) d = T - 1 - t;  // may lie before the group
+        r[u] = Quad<DT>::template load<FULL>(p + (ptrdiff_t)st * d + lo, nvalid);
+    }
+}
+
+template <int DT, bool FULL, bool UNI, int K, bool SILU>
+__global__ __launch_bounds__(kBlock) void conv_fwd_kernel(ConvFwd a, ConvGrid g, int64_t T, int64_t D) {
+    constexpr int S = Elem<DT>::bytes, U = group_of(K);
+    const ConvPos p = conv_pos<UNI>(g, T, D);
+    const uint32_t lo = (uint32_t)p.d0 * S;  // this thread's bytes into a row
+    Starts<UNI, K> st;
+    st.init(a.reset, p.bi, p.t0, T);  // with every lane, idle ones too
+    if (p.nvalid == 0) return;
+    Taps<K> tp;
+    tp.load(a.w, a.bias, p, D);
+    Quad<DT> win[K - 1];
+    conv_warm<DT, FULL, UNI, K>(win, a.x, a.state, st, p, D, lo);
+    const char* px = a.x.row(p.bi, p.t0);
+    const size_t so = (size_t)D * S;
+    char* po = static_cast<char*>(a.out) + (size_t)(p.bi * T + p.t0) * so;
+    int head = 0;  // the ring's oldest token
+    for (int64_t t = p.t0; t < p.t1; t += U) {
+        const uint32_t starts = st.template group<U>(t);
+        Quad<DT> x[U];
+        if (some<UNI>(t + U > T)) load_group<DT, FULL, true>(x, px, a.x.st, lo, t, T, p.nvalid);
+        else load_group<DT, FULL, false>(x, px, a.x.st, lo, t, T, p.nvalid);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (some<UNI>(((starts >> u) & 1u) && t + u < p.t1)) {
+#pragma unroll
+                for (int j = 0; j < K - 1; ++j)
+                    if (((starts >> u) & 1u) && t + u < p.t1) win[j] = Quad<DT>::zero();
+            }
+            float y[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float z = tp.z(win, x[u], u, j);
+                y[j] = SILU ? z * sigmoid_f(z) : z;
+            }
+            Quad<DT> o;
+            o.set(y);
+            if (t + u < p.t1) {
+                o.template store<FULL>(po + so * u + lo, p.nvalid);
+                win[u % (K - 1)] = x[u];
+                head = (u + 1) % (K - 1);
+            }
+        }
+        px += a.x.st * U;
+        po += so * U;
+    }
+    if (a.last && p.t1 == T) {
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) {
+            const int back = j >= head ? j - head : j - head + K - 1;  // place in the window, oldest first
+            win[j].template store<FULL>(
+                static_cast<char*>(a.last) + (size_t)((p.bi * (K - 1) + back) * D) * S + lo, p.nvalid);
+        }
+    }
+}
+
+template <int DT, bool FULL, bool UNI, int K, bool SILU>
+__global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(UNI ? 4 : 2))) void conv_bwd_kernel(ConvBwd a, ConvGrid g, int64_t T, int64_t D,
                                                           float* part) {
-    constexpr int V = Elem<DT>::V, U = 4;
+    constexpr int S = Elem<DT>::bytes, U = group_of(K);
     __shared__ float s_part[kBlock * V];
-    const ConvPos p = conv_pos<V>(g, T, D);
+    const ConvPos p = conv_pos<UNI>(g, T, D);
+    const uint32_t lo = (uint32_t)p.d0 * S;  // this thread's bytes into a row
+    Starts<UNI, K> st;
+    st.init(a.reset, p.bi, p.t0, T);  // with every lane, idle ones too
     float dw[K][V], db[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -193,82 +352,107 @@ __global__ __launch_bounds__(kBlock) void conv_bwd_kernel(ConvBwd a, ConvGrid g,
         for (int k = 0; k < K; ++k) dw[k][j] = 0.0f;
     }
     if (p.nvalid > 0) {
-        Taps<V, K> tp;
+        Taps<K> tp;
         tp.load(a.w, a.bias, p, D);
-        RowVec<DT> win[K - 1];
-        conv_warm<DT, ALIGNED, K>(win, a.x, a.state, a.reset, p, T, D);
-        float acc[K - 1][V];  // input gradients of tokens t - K + 1 .. t - 1
+        Quad<DT> win[K - 1];
+        conv_warm<DT, FULL, UNI, K>(win, a.x, a.state, st, p, D, lo);
+        float acc[K - 1][V];  // input gradients of tokens t - K + 1 .. t - 1, in the window's ring
 #pragma unroll
         for (int i = 0; i < K - 1; ++i)
 #pragma unroll
             for (int j = 0; j < V; ++j) acc[i][j] = 0.0f;
         int age = K - 1;  // tokens back that still lie in the segment (capped)
-        const int64_t end = p.t0 + g.rows;  // one past the chunk's last token, which may lie past T
+        const size_t so = (size_t)D * S;
+        const char* px = a.x.row(p.bi, p.t0);
+        const char* pg = static_cast<const char*>(a.g) + (size_t)(p.bi * T + p.t0) * so;
+        // of token t - K + 1, which for the first tokens is not there (nor written)
+        char* pq = a.gx.row(p.bi, p.t0) - a.gx.st * (K - 1);
+            const int64_t end = p.t0 + g.rows;  // one past the chunk's last token, which may lie past T
+
         for (int64_t t = p.t0; t < end + K - 1; t += U) {
-            RowVec<DT> x[U], gr[U];
-            bool start[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int64_t tu = t + u < T ? t + u : T - 1;
-                x[u] = load_row<DT, ALIGNED>(a.x.row(p.bi, tu), (size_t)p.d0, p.nvalid, 0.0f);
-                gr[u] = load_row<DT, ALIGNED>(a.g, (size_t)((p.bi * T + tu) * D + p.d0), p.nvalid, 0.0f);
-                start[u] = a.reset && a.reset[p.bi * T + tu];
+            const uint32_t starts = st.template group<U>(t);
+            Quad<DT> x[U], gr[U];
+            if (some<UNI>(t + U > T)) {
+                load_group<DT, FULL, true>(x, px, a.x.st, lo, t, T, p.nvalid);
+                load_group<DT, FULL, true>(gr, pg, so, lo, t, T, p.nvalid);
+            } else {
+                load_group<DT, FULL, false>(x, px, a.x.st, lo, t, T, p.nvalid);
+                load_group<DT, FULL, false>(gr, pg, so, lo, t, T, p.nvalid);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
+                // token tu enters, and s = tu - K + 1 gets its last contribution
                 const int64_t tu = t + u, s = tu - (K - 1);
-                if (tu >= end + K - 1) break;
-                const bool live = tu < T;
-                if (live) {
-                    age = start[u] ? 0 : (age < K - 1 ? age + 1 : K - 1);
-                    if (start[u]) {
+                const bool start = (starts >> u) & 1u;
+                if (tu < T) age = start ? 0 : (age < K - 1 ? age + 1 : K - 1);
+                if (some<UNI>(start)) {
 #pragma unroll
-                        for (int j = 0; j < K - 1; ++j) win[j] = RowVec<DT>::splat(0.0f);
-                    }
+                    for (int j = 0; j < K - 1; ++j)
+                        if (start) win[j] = Quad<DT>::zero();
                 }
-                RowOut<DT> o;
+                float gz[V], dx[V];
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
-                    float gz = 0.0f;
-                    if (live) {
-                        gz = gr[u].get(j);
-                        if constexpr (SILU) {
-                            const float z = tp.z(win, x[u], j);
-                            const Sigmoid q = sigmoid_pair(z);
-                            gz *= q.s * fmaf(z, q.c, 1.0f);
-                        }
-                        if (tu < end) {
-                            db[j] += gz;
-                            dw[K - 1][j] = fmaf(gz, x[u].get(j), dw[K - 1][j]);
-#pragma unroll
-                            for (int k = 0; k < K - 1; ++k) dw[k][j] = fmaf(gz, win[k].get(j), dw[k][j]);
-                        }
-#pragma unroll
-                        for (int i = 0; i < K - 1; ++i)
-                            if (K - 1 - i <= age) acc[i][j] = fmaf(tp.w[i][j], gz, acc[i][j]);
+                    gz[j] = gr[u].get(j);
+                    if constexpr (SILU) {  // dy/dz = q (1 + z (1 - q)), q = sigmoid(z)
+                        const float z = tp.z(win, x[u], u, j);
+                        const float q = sigmoid_f(z);
+                        gz[j] *= q * fmaf(z, 1.0f - q, 1.0f);
                     }
-                    o.v[j] = acc[0][j];
-#pragma unroll
-                    for (int i = 0; i + 1 < K - 1; ++i) acc[i][j] = acc[i + 1][j];
-                    acc[K - 2][j] = tp.w[K - 1][j] * gz;
                 }
-                if (live) conv_push<DT, K>(win, x[u]);
-                // token s is complete: it is the chunk's, or one of the state's
-                if (s < T && (s >= p.t0 || (s < 0 && p.t0 == 0 && a.grad_state))) {
-                    const int64_t back = T - 1 - s;  // its place in `last`, from the end
-                    if (a.grad_last && back < K - 1 && back <= age) {
-                        const RowVec<DT> gl = load_row<DT, ALIGNED>(
-                            a.grad_last, (size_t)((p.bi * (K - 1) + K - 2 - back) * D + p.d0), p.nvalid, 0.0f);
+                if (some<UNI>(tu >= T)) {
 #pragma unroll
-                        for (int j = 0; j < V; ++j) o.v[j] += gl.get(j);
+                    for (int j = 0; j < V; ++j) gz[j] = tu < T ? gz[j] : 0.0f;
+                }
+                if (some<UNI>(tu < end)) {  // the walk's last K - 1 tokens are the next chunk's
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        const float gm = tu < end ? gz[j] : 0.0f;
+                        db[j] += gm;
+                        dw[K - 1][j] = fmaf(gm, x[u].get(j), dw[K - 1][j]);
+#pragma unroll
+                        for (int k = 0; k < K - 1; ++k) dw[k][j] = fmaf(gm, win[(u + k) % (K - 1)].get(j), dw[k][j]);
                     }
-                    if (s >= 0)
-                        store_row<DT, ALIGNED>(a.gx.row(p.bi, s), (size_t)p.d0, p.nvalid, o);
-                    else
-                        store_row<DT, ALIGNED>(a.grad_state,
-                                               (size_t)((p.bi * (K - 1) + s + K - 1) * D + p.d0), p.nvalid, o);
                 }
+                if (some<UNI>(age < K - 1)) {
+#pragma unroll
+                    for (int i = 0; i < K - 1; ++i)
+#pragma unroll
+                        for (int j = 0; j < V; ++j)
+                            if (K - 1 - i <= age) acc[(u + i) % (K - 1)][j] = fmaf(tp.w[i][j], gz[j], acc[(u + i) % (K - 1)][j]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < K - 1; ++i)
+#pragma unroll
+                        for (int j = 0; j < V; ++j)
+                            acc[(u + i) % (K - 1)][j] = fmaf(tp.w[i][j], gz[j], acc[(u + i) % (K - 1)][j]);
+                }
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    dx[j] = acc[u % (K - 1)][j];
+                    acc[u % (K - 1)][j] = tp.w[K - 1][j] * gz[j];
+                }
+                win[u % (K - 1)] = x[u];
+                if (a.grad_last && s < T && T - 1 - s < K - 1 && T - 1 - s <= age) {
+                    const Quad<DT> gl = Quad<DT>::template load<FULL>(
+                        static_cast<const char*>(a.grad_last) +
+                            (size_t)((p.bi * (K - 1) + K - 1 - (T - s)) * D) * S + lo,
+                        p.nvalid);
+#pragma unroll
+                    for (int j = 0; j < V; ++j) dx[j] += gl.get(j);
+                }
+                Quad<DT> o;
+                o.set(dx);
+                if (s >= p.t0 && s < T && s < end)
+                    o.template store<FULL>(pq + a.gx.st * u + lo, p.nvalid);
+                if (a.grad_state && s < 0)  // a token of the state (p.t0 is 0)
+                    o.template store<FULL>(static_cast<char*>(a.grad_state) +
+                                               (size_t)((p.bi * (K - 1) + s + K - 1) * D) * S + lo,
+                                           p.nvalid);
             }
+            px += a.x.st * U;
+            pg += so * U;
+            pq += a.gx.st * U;
         }
     }
     if (!part) return;
@@ -305,49 +489,55 @@ struct WriteParams {
     }
 };
 
-bool conv_aligned(const ConvShape& s, const void* const* ptrs, int n, const Rows* const* rows, int nr) {
-    const Shape c{s.B, s.T, s.D, s.dtype};
-    if (!rows_aligned(c, ptrs, n)) return false;
-    for (int i = 0; i < nr; ++i)
-        if (!operand_aligned(s.B, s.T, *rows[i])) return false;
-    return true;
-}
-
-template <int DT, bool AL, int K>
+template <int DT, bool FULL, bool UNI, int K>
 void fwd_launch(const ConvShape& s, const ConvFwd& p, const ConvGrid& g, hipStream_t st) {
     const dim3 grid(g.ncb * g.blocks), block(kBlock);
-    if (s.silu) hipLaunchKernelGGL((conv_fwd_kernel<DT, AL, K, true>), grid, block, 0, st, p, g, s.T, s.D);
-    else hipLaunchKernelGGL((conv_fwd_kernel<DT, AL, K, false>), grid, block, 0, st, p, g, s.T, s.D);
+    if (s.silu) hipLaunchKernelGGL((conv_fwd_kernel<DT, FULL, UNI, K, true>), grid, block, 0, st, p, g, s.T, s.D);
+    else hipLaunchKernelGGL((conv_fwd_kernel<DT, FULL, UNI, K, false>), grid, block, 0, st, p, g, s.T, s.D);
 }
 
-template <int DT, bool AL, int K>
+template <int DT, bool FULL, bool UNI, int K>
 void bwd_launch(const ConvShape& s, const ConvBwd& p, const ConvGrid& g, float* part, hipStream_t st) {
     const dim3 grid(g.ncb * g.blocks), block(kBlock);
     if (s.silu)
-        hipLaunchKernelGGL((conv_bwd_kernel<DT, AL, K, true>), grid, block, 0, st, p, g, s.T, s.D, part);
+        hipLaunchKernelGGL((conv_bwd_kernel<DT, FULL, UNI, K, true>), grid, block, 0, st, p, g, s.T, s.D, part);
     else
-        hipLaunchKernelGGL((conv_bwd_kernel<DT, AL, K, false>), grid, block, 0, st, p, g, s.T, s.D, part);
+        hipLaunchKernelGGL((conv_bwd_kernel<DT, FULL, UNI, K, false>), grid, block, 0, st, p, g, s.T, s.D, part);
 }
 
-template <int DT, bool AL>
+template <int DT, bool FULL, bool UNI>
 void fwd_taps(const ConvShape& s, const ConvFwd& p, const ConvGrid& g, hipStream_t st) {
-    if (s.K == 2) fwd_launch<DT, AL, 2>(s, p, g, st);
-    else if (s.K == 3) fwd_launch<DT, AL, 3>(s, p, g, st);
-    else fwd_launch<DT, AL, 4>(s, p, g, st);
+    if (s.K == 2) fwd_launch<DT, FULL, UNI, 2>(s, p, g, st);
+    else if (s.K == 3) fwd_launch<DT, FULL, UNI, 3>(s, p, g, st);
+    else fwd_launch<DT, FULL, UNI, 4>(s, p, g, st);
 }
 
-template <int DT, bool AL>
+template <int DT, bool FULL, bool UNI>
 void bwd_taps(const ConvShape& s, const ConvBwd& p, const ConvGrid& g, float* part, hipStream_t st) {
-    if (s.K == 2) bwd_launch<DT, AL, 2>(s, p, g, part, st);
-    else if (s.K == 3) bwd_launch<DT, AL, 3>(s, p, g, part, st);
-    else bwd_launch<DT, AL, 4>(s, p, g, part, st);
+    if (s.K == 2) bwd_launch<DT, FULL, UNI, 2>(s, p, g, part, st);
+    else if (s.K == 3) bwd_launch<DT, FULL, UNI, 3>(s, p, g, part, st);
+    else bwd_launch<DT, FULL, UNI, 4>(s, p, g, part, st);
+}
+
+template <int DT>
+void fwd_rows_kind(const ConvShape& s, const ConvFwd& p, const ConvGrid& g, hipStream_t st) {
+    if (g.tpr == kWave) s.D % V == 0 ? fwd_taps<DT, true, true>(s, p, g, st) : fwd_taps<DT, false, true>(s, p, g, st);
+    else s.D % V == 0 ? fwd_taps<DT, true, false>(s, p, g, st) : fwd_taps<DT, false, false>(s, p, g, st);
+}
+
+template <int DT>
+void bwd_rows_kind(const ConvShape& s, const ConvBwd& p, const ConvGrid& g, float* part, hipStream_t st) {
+    if (g.tpr == kWave)
+        s.D % V == 0 ? bwd_taps<DT, true, true>(s, p, g, part, st) : bwd_taps<DT, false, true>(s, p, g, part, st);
+    else
+        s.D % V == 0 ? bwd_taps<DT, true, false>(s, p, g, part, st) : bwd_taps<DT, false, false>(s, p, g, part, st);
 }
 
 }  // namespace
 
 bool conv_fits(const ConvShape& s) {
     if (s.D >= ((int64_t)1 << 31)) return false;
-    for (const int rows : {kFwdRows, kBwdRows}) {
+    for (const int rows : {fwd_rows(s), bwd_rows(s)}) {
         const int64_t chunks = chunks_of(s, rows);
         if (chunks >= ((int64_t)1 << 31)) return false;
         const ConvGrid g = conv_grid(s, rows);
@@ -358,33 +548,25 @@ bool conv_fits(const ConvShape& s) {
 }
 
 size_t conv_part_bytes(const ConvShape& s) {
-    return (size_t)conv_grid(s, kBwdRows).blocks * (size_t)(s.K + 1) * (size_t)s.D * 4;
+    return (size_t)conv_grid(s, bwd_rows(s)).blocks * (size_t)(s.K + 1) * (size_t)s.D * 4;
 }
 
 size_t conv_sum_scratch(const ConvShape& s) {
-    return column_sum_scratch(conv_grid(s, kBwdRows).blocks, (s.K + 1) * s.D);
+    return column_sum_scratch(conv_grid(s, bwd_rows(s)).blocks, (s.K + 1) * s.D);
 }
 
 hipError_t launch_conv_fwd(const ConvShape& s, const ConvFwd& p, hipStream_t st) {
-    const ConvGrid g = conv_grid(s, kFwdRows);
-    const void* ptrs[3] = {p.out, p.state, p.last};
-    const Rows* rows[1] = {&p.x};
-    const bool al = conv_aligned(s, ptrs, 3, rows, 1);
-    if (s.dtype == DT_F32) al ? fwd_taps<DT_F32, true>(s, p, g, st) : fwd_taps<DT_F32, false>(s, p, g, st);
-    else al ? fwd_taps<DT_BF16, true>(s, p, g, st) : fwd_taps<DT_BF16, false>(s, p, g, st);
+    const ConvGrid g = conv_grid(s, fwd_rows(s));
+    if (s.dtype == DT_F32) fwd_rows_kind<DT_F32>(s, p, g, st);
+    else fwd_rows_kind<DT_BF16>(s, p, g, st);
     return hipGetLastError();
 }
 
 hipError_t launch_conv_bwd(const ConvShape& s, const ConvBwd& p, float* part, float* scratch,
                            float* grad_w, float* grad_bias, hipStream_t st) {
-    const ConvGrid g = conv_grid(s, kBwdRows);
-    const void* ptrs[4] = {p.state, p.g, p.grad_last, p.grad_state};
-    const Rows* rows[2] = {&p.x, &p.gx};
-    const bool al = conv_aligned(s, ptrs, 4, rows, 2);
-    if (s.dtype == DT_F32)
-        al ? bwd_taps<DT_F32, true>(s, p, g, part, st) : bwd_taps<DT_F32, false>(s, p, g, part, st);
-    else
-        al ? bwd_taps<DT_BF16, true>(s, p, g, part, st) : bwd_taps<DT_BF16, false>(s, p, g, part, st);
+    const ConvGrid g = conv_grid(s, bwd_rows(s));
+    if (s.dtype == DT_F32) bwd_rows_kind<DT_F32>(s, p, g, part, st);
+    else bwd_rows_kind<DT_BF16>(s, p, g, part, st);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !part) return e;
     return launch_column_sum(part, (int64_t)g.blocks, (int64_t)(s.K + 1) * s.D, scratch,
