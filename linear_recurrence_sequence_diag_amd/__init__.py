@@ -351,9 +351,15 @@ def scan_embed_workspace_bytes(N, V, D, dtype):
 # ---------------------------------------------------------------------------
 # torch tensor helpers (allocation + marshalling only)
 # ---------------------------------------------------------------------------
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def dtype_code(dt) -> int:
@@ -650,7 +656,8 @@ def _check_rows(name, t, ref, dims):
     """An operand whose rows may be strided: contiguous along the last dimension."""
     if not isinstance(t, _torch().Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA (HIP) tensor")
-    if t is not ref and (t.shape != ref.shape or t.dtype != ref.dtype or t.device != ref.device):
+    if t is not ref and (t.shape != ref.shape or t.dtype != ref.dtype
+                         or t.get_device() != ref.get_device()):
         raise ValueError(f"{name} must match x in shape, dtype and device")
     if t.dim() != dims:
         raise ValueError(f"{name} must be [{'B, T, D' if dims == 3 else 'B, D'}]")
@@ -662,17 +669,19 @@ def _strides(*tensors):
     """(batch, step) strides of [B, T, D] tensors, or batch strides of [B, D]
     ones, for the C ABI, or None where all are contiguous; a dimension of one
     takes the contiguous value (torch leaves it arbitrary)."""
-    if all(t.is_contiguous() for t in tensors):
+    for t in tensors:
+        if not t.is_contiguous():
+            break
+    else:
         return None
+    shape = tensors[0].shape
+    width = shape[-1]
+    if len(shape) == 2:
+        return [t.stride(0) if shape[0] > 1 else width for t in tensors]
     out = []
     for t in tensors:
-        shape, stride = t.shape, t.stride()
-        width = shape[-1]
-        if len(shape) == 2:
-            out.append(stride[0] if shape[0] > 1 else width)
-            continue
-        out.append(stride[0] if shape[0] > 1 else shape[1] * width)
-        out.append(stride[1] if shape[1] > 1 else width)
+        out.append(t.stride(0) if shape[0] > 1 else shape[1] * width)
+        out.append(t.stride(1) if shape[1] > 1 else width)
     return out
 
 
@@ -680,9 +689,17 @@ def _check_param(name, t, shape, ref):
     """A float32 parameter on x's device."""
     torch = _torch()
     if (not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype != torch.float32
-            or t.device != ref.device or not t.is_contiguous()):
+            or t.get_device() != ref.get_device() or not t.is_contiguous()):
         dims = ", ".join(str(n) for n in shape)
         raise ValueError(f"{name} must be a contiguous float32 [{dims}] tensor on x's device")
+
+
+def _rows_like(x):
+    """An uninitialised contiguous tensor of x's shape, dtype and device."""
+    torch = _torch()
+    if x.is_contiguous():
+        return torch.empty_like(x)
+    return torch.empty(x.shape, device=x.device, dtype=x.dtype)
 
 
 def _check_step_mask(reset, ref):
@@ -710,7 +727,7 @@ def gated_scan(x, gate_r, gate_i, decay, scale=8.0, h0=None, reset=None, algo="a
     _check_state("h0", h0, x)
     if not (with_out or with_last):
         raise ValueError("a forward needs out or last")
-    out = torch.empty((B, T, D), device=x.device, dtype=x.dtype) if with_out else None
+    out = _rows_like(x) if with_out else None
     last = torch.empty((B, D), device=x.device, dtype=torch.float32) if with_last else None
     opts = make_opts(algo, h0=h0, reset=reset, polls=polls, workspace=workspace)
     _enqueue(x, lambda *a: scan_gated_fwd(*a, opts), x.data_ptr(), gate_r.data_ptr(),
@@ -739,7 +756,7 @@ def gated_scan_backward(x, gate_r, gate_i, decay, out, grad_out, scale=8.0, grad
     _check_state("grad_last", grad_last, x)
     _check_state("h0", h0, x)
     if grads is None:
-        grads = [torch.empty((B, T, D), device=x.device, dtype=x.dtype) for _ in range(3)]
+        grads = [_rows_like(x) for _ in range(3)]
     for name, t in zip(("grad_x", "grad_r", "grad_i"), grads):
         _check_rows(name, t, x, 3)
     gx, gr, gi = grads
@@ -768,7 +785,7 @@ def gated_step(x, gate_r, gate_i, decay, state=None, scale=8.0, reset=None, with
         if t is not None:
             _check_param(name, t, (B, D), x)
     _check_step_mask(reset, x)
-    out = torch.empty((B, D), device=x.device, dtype=x.dtype) if with_out else None
+    out = _rows_like(x) if with_out else None
     new = out_state if out_state is not None else torch.empty((B, D), device=x.device,
                                                               dtype=torch.float32)
     _enqueue(x, scan_gated_step, x.data_ptr(), gate_r.data_ptr(), gate_i.data_ptr(),
@@ -820,7 +837,7 @@ def short_conv(x, weight, bias=None, state=None, reset=None, activation=None, wi
     B, T, D = x.shape
     _check_taps_state("state", state, x, K)
     _check_mask(reset, x)
-    out = torch.empty((B, T, D), device=x.device, dtype=x.dtype)
+    out = _rows_like(x)
     last = (torch.empty((B, max(K - 1, 0), D), device=x.device, dtype=x.dtype) if with_last
             else None)
     _enqueue(x, scan_conv_fwd, x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(state),
@@ -842,7 +859,7 @@ def short_conv_backward(x, weight, bias, grad_out, state=None, grad_last=None, r
     _check_taps_state("state", state, x, K)
     _check_taps_state("grad_last", grad_last, x, K)
     _check_mask(reset, x)
-    gx = grad_x if grad_x is not None else torch.empty((B, T, D), device=x.device, dtype=x.dtype)
+    gx = grad_x if grad_x is not None else _rows_like(x)
     _check_rows("grad_x", gx, x, 3)
     gw = torch.empty_like(weight)
     gb = torch.empty_like(bias) if bias is not None else None
@@ -866,7 +883,7 @@ def short_conv_step(x, weight, bias=None, state=None, reset=None, activation=Non
     _check_taps_state("state", state, x, K)
     _check_taps_state("out_state", out_state, x, K)
     _check_step_mask(reset, x)
-    out = torch.empty((B, D), device=x.device, dtype=x.dtype)
+    out = _rows_like(x)
     new = (out_state if out_state is not None
            else torch.empty((B, max(K - 1, 0), D), device=x.device, dtype=x.dtype))
     _enqueue(x, scan_conv_step, x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(state),

@@ -29,6 +29,7 @@
 #include "column_sum.hpp"
 #include "gated_math.hpp"
 #include "launch.hpp"
+#include "quad.hpp"
 
 namespace lrscan {
 
@@ -39,62 +40,7 @@ constexpr int kBlock = 256;
 // window's and the waiting gradients' places in their rings are constants.
 constexpr int group_of(int K) { return K == 4 ? 6 : 4; }
 
-constexpr int V = 4;       // channels of a thread
-
-// Four adjacent channels of a row as they are stored.  (A thread with all
-// eight bf16 channels of 16 bytes held about 180 registers in the backward,
-// which left two wavefronts a SIMD.)  FULL: rows are whole quads; then a quad
-// is one access, whatever its address is aligned to, else the last one of a
-// row goes channel by channel.
-template <int DT>
-struct Quad {
-    static constexpr int S = Elem<DT>::bytes;
-    static constexpr int W = DT == DT_F32 ? 4 : 2;  // dwords
-    typedef unsigned int Raw __attribute__((ext_vector_type(W), aligned(S)));
-    Raw w;
-    __device__ __forceinline__ static Quad zero() {
-        Quad q;
-#pragma unroll
-        for (int i = 0; i < W; ++i) q.w[i] = 0u;
-        return q;
-    }
-    __device__ __forceinline__ float get(int j) const {
-        if constexpr (DT == DT_F32) return __uint_as_float(w[j]);
-        else return (j & 1) ? __uint_as_float(w[j >> 1] & 0xffff0000u) : __uint_as_float(w[j >> 1] << 16);
-    }
-    __device__ __forceinline__ void set(const float (&v)[V]) {
-        if constexpr (DT == DT_F32) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) w[j] = __float_as_uint(v[j]);
-        } else {
-            w[0] = pack_bf16x2(v[0], v[1]);
-            w[1] = pack_bf16x2(v[2], v[3]);
-        }
-    }
-    template <bool FULL>
-    __device__ __forceinline__ static Quad load(const char* p, int nvalid) {
-        Quad q = zero();
-        if (FULL || nvalid == V) {
-            q.w = __builtin_nontemporal_load(reinterpret_cast<const Raw*>(p));
-        } else {
-            float v[V];
-#pragma unroll
-            for (int j = 0; j < V; ++j) v[j] = j < nvalid ? Elem<DT>::load1(p, j) : 0.0f;
-            q.set(v);
-        }
-        return q;
-    }
-    template <bool FULL>
-    __device__ __forceinline__ void store(char* p, int nvalid) const {
-        if (FULL || nvalid == V) {
-            __builtin_nontemporal_store(w, reinterpret_cast<Raw*>(p));
-        } else {
-#pragma unroll
-            for (int j = 0; j < V; ++j)
-                if (j < nvalid) Elem<DT>::store1(p, j, get(j));
-        }
-    }
-};
+constexpr int V = kQuad;  // channels of a thread
 
 // Tokens of a chunk.  The backward's walk goes K - 1 tokens past its chunk, so
 // that walk is what is a whole number of groups.
@@ -185,14 +131,16 @@ __device__ __forceinline__ bool some(bool c) {
 
 template <int K>
 struct Taps {
-    float w[K][V], bias[V];
+    float w[K][V], bias[V] = {0.0f, 0.0f, 0.0f, 0.0f};
+    __device__ __forceinline__ static void row(const float* p, int nvalid, float (&v)[V]) {
+        const Quad<DT_F32> q = Quad<DT_F32>::load<false>(reinterpret_cast<const char*>(p), nvalid);
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] = q.get(j);
+    }
     __device__ __forceinline__ void load(const float* wp, const float* bp, const ConvPos& p, int64_t D) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-#pragma unroll
-            for (int k = 0; k < K; ++k) w[k][j] = j < p.nvalid ? wp[k * D + p.d0 + j] : 0.0f;
-            bias[j] = (bp && j < p.nvalid) ? bp[p.d0 + j] : 0.0f;
-        }
+        for (int k = 0; k < K; ++k) row(wp + k * D + p.d0, p.nvalid, w[k]);
+        if (bp) row(bp + p.d0, p.nvalid, bias);
     }
     // The window is a ring whose oldest token is at place `u` modulo K - 1.
     template <int DT>
@@ -476,6 +424,51 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(UNI ? 4 
     }
 }
 
+// One token: the taps' state read, used and moved on by one (a thread's own
+// channels only, so the state may be updated in place).
+template <int DT, bool FULL, int K, bool SILU>
+__global__ __launch_bounds__(kBlock) void conv_step_kernel(ConvFwd a, int64_t B, int64_t D, uint32_t vpr) {
+    constexpr int S = Elem<DT>::bytes;
+    const uint32_t vec = blockIdx.x * blockDim.x + threadIdx.x;
+    const int64_t bi = blockIdx.y;
+    if (vec >= vpr) return;
+    ConvPos p;
+    p.bi = bi;
+    p.t0 = 0;
+    p.t1 = 1;
+    p.d0 = (int64_t)vec * V;
+    p.nvalid = (int)((D - p.d0) < V ? (D - p.d0) : V);
+    const size_t lo = (size_t)p.d0 * S, so = (size_t)D * S;
+    const size_t state = (size_t)bi * (K - 1) * so + lo;
+    Quad<DT> win[K - 1];
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j)
+        win[j] = a.state ? Quad<DT>::template load<FULL>(static_cast<const char*>(a.state) + state + j * so, p.nvalid)
+                         : Quad<DT>::zero();
+    const Quad<DT> x = Quad<DT>::template load<FULL>(a.x.row(bi, 0) + lo, p.nvalid);
+    Taps<K> tp;
+    tp.load(a.w, a.bias, p, D);
+    if (a.reset && a.reset[bi]) {
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) win[j] = Quad<DT>::zero();
+    }
+    float y[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const float z = tp.z(win, x, 0, j);
+        y[j] = SILU ? z * sigmoid_f(z) : z;
+    }
+    Quad<DT> o;
+    o.set(y);
+    o.template store<FULL>(static_cast<char*>(a.out) + (size_t)bi * so + lo, p.nvalid);
+    if (a.last) {
+#pragma unroll
+        for (int j = 0; j + 1 < K - 1; ++j)
+            win[j + 1].template store<FULL>(static_cast<char*>(a.last) + state + j * so, p.nvalid);
+        x.template store<FULL>(static_cast<char*>(a.last) + state + (K - 2) * so, p.nvalid);
+    }
+}
+
 // Column c of the partial rows: tap c / D of channel c % D, the bias as tap K.
 struct WriteParams {
     float *w, *bias;
@@ -519,6 +512,28 @@ void bwd_taps(const ConvShape& s, const ConvBwd& p, const ConvGrid& g, float* pa
     else bwd_launch<DT, FULL, UNI, 4>(s, p, g, part, st);
 }
 
+// Wavefront-sized workgroups, to spread a small batch over the CUs.
+template <int DT, bool FULL, int K>
+void step_launch(const ConvShape& s, const ConvFwd& p, hipStream_t st) {
+    const uint32_t vpr = (uint32_t)((s.D + V - 1) / V);
+    const dim3 grid((vpr + kWave - 1) / kWave, (unsigned)s.B), block(kWave);
+    if (s.silu) hipLaunchKernelGGL((conv_step_kernel<DT, FULL, K, true>), grid, block, 0, st, p, s.B, s.D, vpr);
+    else hipLaunchKernelGGL((conv_step_kernel<DT, FULL, K, false>), grid, block, 0, st, p, s.B, s.D, vpr);
+}
+
+template <int DT, bool FULL>
+void step_taps(const ConvShape& s, const ConvFwd& p, hipStream_t st) {
+    if (s.K == 2) step_launch<DT, FULL, 2>(s, p, st);
+    else if (s.K == 3) step_launch<DT, FULL, 3>(s, p, st);
+    else step_launch<DT, FULL, 4>(s, p, st);
+}
+
+template <int DT>
+void step_kind(const ConvShape& s, const ConvFwd& p, hipStream_t st) {
+    if (s.D % V == 0) step_taps<DT, true>(s, p, st);
+    else step_taps<DT, false>(s, p, st);
+}
+
 template <int DT>
 void fwd_rows_kind(const ConvShape& s, const ConvFwd& p, const ConvGrid& g, hipStream_t st) {
     if (g.tpr == kWave) s.D % V == 0 ? fwd_taps<DT, true, true>(s, p, g, st) : fwd_taps<DT, false, true>(s, p, g, st);
@@ -556,6 +571,11 @@ size_t conv_sum_scratch(const ConvShape& s) {
 }
 
 hipError_t launch_conv_fwd(const ConvShape& s, const ConvFwd& p, hipStream_t st) {
+    if (s.T == 1 && s.B <= 65535) {
+        if (s.dtype == DT_F32) step_kind<DT_F32>(s, p, st);
+        else step_kind<DT_BF16>(s, p, st);
+        return hipGetLastError();
+    }
     const ConvGrid g = conv_grid(s, fwd_rows(s));
     if (s.dtype == DT_F32) fwd_rows_kind<DT_F32>(s, p, g, st);
     else fwd_rows_kind<DT_BF16>(s, p, g, st);

@@ -18,6 +18,7 @@
 #include "gated.hpp"
 #include "gated_math.hpp"
 #include "launch.hpp"
+#include "quad.hpp"
 
 namespace lrscan {
 
@@ -36,7 +37,7 @@ struct WalkArgs {
     int64_t vpr;  // vectors of V lanes in a row
 };
 
-// U rows are loaded ahead of the arithmetic; U = 1 is the decode step.
+// U rows are loaded ahead of the arithmetic.
 template <int DT, bool ALIGNED, int U>
 __global__ __launch_bounds__(kBlock) void gated_walk_fwd_kernel(GatedFwd p, WalkArgs w) {
     constexpr int V = Elem<DT>::V;
@@ -83,6 +84,57 @@ __global__ __launch_bounds__(kBlock) void gated_walk_fwd_kernel(GatedFwd p, Walk
 #pragma unroll
         for (int j = 0; j < V; ++j)
             if (j < nvalid) p.last[bi * D + d0 + j] = h[j];
+    }
+}
+
+// One step (T = 1): four channels of R batch rows to a thread, all their loads
+// before the arithmetic; h0 may be last itself.  A channel's rate costs about
+// as much as a step, so R rows share it where rows are many.
+template <int DT, bool FULL, int R>
+__global__ __launch_bounds__(kBlock) void gated_step_kernel(GatedFwd p, int64_t B, int64_t D, uint32_t vpr) {
+    constexpr int S = Elem<DT>::bytes;
+    const uint32_t vec = blockIdx.x * blockDim.x + threadIdx.x;
+    if (vec >= vpr) return;
+    const int64_t d0 = (int64_t)vec * kQuad, b0 = (int64_t)blockIdx.y * R;
+    const int nvalid = (int)((D - d0) < kQuad ? (D - d0) : kQuad);
+    const size_t lo = (size_t)d0 * S;
+    Quad<DT> x[R], gr[R], gi[R];
+    Quad<DT_F32> h[R];
+    bool start[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int64_t b = b0 + r < B ? b0 + r : B - 1;
+        x[r] = Quad<DT>::template load<FULL>(p.x.row(b, 0) + lo, nvalid);
+        gr[r] = Quad<DT>::template load<FULL>(p.gr.row(b, 0) + lo, nvalid);
+        gi[r] = Quad<DT>::template load<FULL>(p.gi.row(b, 0) + lo, nvalid);
+        h[r] = p.h0 ? Quad<DT_F32>::template load<FULL>(reinterpret_cast<const char*>(p.h0 + b * D + d0), nvalid)
+                    : Quad<DT_F32>::zero();
+        start[r] = p.reset && p.reset[b];
+    }
+    const Quad<DT_F32> dc = Quad<DT_F32>::template load<FULL>(reinterpret_cast<const char*>(p.decay + d0), nvalid);
+    float rate[kQuad];
+#pragma unroll
+    for (int j = 0; j < kQuad; ++j) rate[j] = gate_rate(dc.get(j), p.scale);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        if (b0 + r >= B) break;
+        float v[kQuad];
+#pragma unroll
+        for (int j = 0; j < kQuad; ++j) {
+            const GatedStep g = gated_step_of(x[r].get(j), gr[r].get(j), gi[r].get(j), rate[j]);
+            const GatedStep f = gated_start_of(x[r].get(j), gi[r].get(j));
+            v[j] = start[r] ? f.b : fmaf(g.a, h[r].get(j), g.b);
+        }
+        if (p.out) {
+            Quad<DT> o;
+            o.set(v);
+            o.template store<FULL>(static_cast<char*>(p.out) + (size_t)(b0 + r) * D * S + lo, nvalid);
+        }
+        if (p.last) {
+            Quad<DT_F32> o;
+            o.set(v);
+            o.template store<FULL>(reinterpret_cast<char*>(p.last + (b0 + r) * D + d0), nvalid);
+        }
     }
 }
 
@@ -177,17 +229,26 @@ dim3 walk_grid(const GatedShape& s, int block, WalkArgs* w) {
 template <int DT>
 hipError_t walk_fwd_t(const GatedShape& s, const GatedFwd& p, hipStream_t st) {
     WalkArgs w;
-    // one step: workgroups of one wavefront, to spread a small batch over the CUs
-    const int block = s.T == 1 ? kWave : kBlock;
-    const dim3 grid = walk_grid<DT>(s, block, &w);
-    const bool al = gated_fwd_aligned(s, p);
-    if (s.T == 1) {
-        if (al) hipLaunchKernelGGL((gated_walk_fwd_kernel<DT, true, 1>), grid, dim3(block), 0, st, p, w);
-        else hipLaunchKernelGGL((gated_walk_fwd_kernel<DT, false, 1>), grid, dim3(block), 0, st, p, w);
-    } else {
-        if (al) hipLaunchKernelGGL((gated_walk_fwd_kernel<DT, true, kRowsAhead>), grid, dim3(block), 0, st, p, w);
-        else hipLaunchKernelGGL((gated_walk_fwd_kernel<DT, false, kRowsAhead>), grid, dim3(block), 0, st, p, w);
-    }
+    const dim3 grid = walk_grid<DT>(s, kBlock, &w);
+    if (gated_fwd_aligned(s, p))
+        hipLaunchKernelGGL((gated_walk_fwd_kernel<DT, true, kRowsAhead>), grid, dim3(kBlock), 0, st, p, w);
+    else
+        hipLaunchKernelGGL((gated_walk_fwd_kernel<DT, false, kRowsAhead>), grid, dim3(kBlock), 0, st, p, w);
+    return hipGetLastError();
+}
+
+// Workgroups of one wavefront spread a small batch over the CUs; rows are
+// shared by fours once that leaves eight wavefronts to a CU.
+template <int DT, bool FULL>
+hipError_t step_t(const GatedShape& s, const GatedFwd& p, hipStream_t st) {
+    const uint32_t vpr = (uint32_t)((s.D + kQuad - 1) / kQuad);
+    const unsigned gx = (vpr + kWave - 1) / kWave;
+    if ((int64_t)gx * s.B >= 4 * 2048)
+        hipLaunchKernelGGL((gated_step_kernel<DT, FULL, 4>), dim3(gx, (unsigned)((s.B + 3) / 4)), dim3(kWave), 0, st,
+                           p, s.B, s.D, vpr);
+    else
+        hipLaunchKernelGGL((gated_step_kernel<DT, FULL, 1>), dim3(gx, (unsigned)s.B), dim3(kWave), 0, st, p, s.B, s.D,
+                           vpr);
     return hipGetLastError();
 }
 
@@ -239,6 +300,11 @@ bool gated_walk_fits(const GatedShape& s) {
 }
 
 hipError_t launch_gated_walk_fwd(const GatedShape& s, const GatedFwd& p, hipStream_t st) {
+    if (s.T == 1 && s.B <= 65535 && s.D < ((int64_t)1 << 31)) {
+        const bool full = s.D % kQuad == 0;
+        if (s.dtype == DT_F32) return full ? step_t<DT_F32, true>(s, p, st) : step_t<DT_F32, false>(s, p, st);
+        return full ? step_t<DT_BF16, true>(s, p, st) : step_t<DT_BF16, false>(s, p, st);
+    }
     return s.dtype == DT_F32 ? walk_fwd_t<DT_F32>(s, p, st) : walk_fwd_t<DT_BF16>(s, p, st);
 }
 
