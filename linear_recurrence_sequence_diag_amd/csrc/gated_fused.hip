@@ -88,14 +88,69 @@ struct GatedBwdArgs {
     uint32_t polls;
 };
 
+// How rows lie.  kWhole: at least one vector long, but not made of aligned
+// vectors.  Its last, partial vector is moved back to start at D - V, so that
+// every access is one of 16 bytes; the columns it shares with its neighbour
+// are computed twice, to the same bits.  (With the partial vector tested for at
+// every access instead, fp32 [5, 777, 1023] took 28.8 us forward and 46.5
+// reverse, against 19.2 and 33.3 for rows of 1024.)  kNarrow: shorter than a
+// vector, element by element.
+enum RowKind { kAligned, kWhole, kNarrow };
+
+template <class C, int RK, bool REV>
+__device__ __forceinline__ Geo gated_geo(uint32_t ticket, const Dims& d, int wave, int rg, int cg) {
+    Geo g = tile_geo<C, REV>(ticket, d, wave, rg, cg);
+    if constexpr (RK == kWhole) {
+        // bases are taken 16 bytes before the tile, so that offsets stay positive
+        g.tbase -= 16;
+        g.coff += 16;
+        if (g.nvalid > 0 && g.nvalid < C::V) {
+            const int back = C::V - g.nvalid;
+            g.d0 -= back;
+            g.coff -= (uint32_t)(back * C::EB);
+            g.nvalid = C::V;
+        }
+    }
+    return g;
+}
+
+// The column of a tile's slot c (D or more: none).
+template <class C, int RK>
+__device__ __forceinline__ int slot_column(const Geo& g, int c, int D) {
+    const int d0 = g.dcol0 + c / C::V * C::V;
+    return (RK == kWhole && d0 < D && d0 + C::V > D ? D - C::V : d0) + c % C::V;
+}
+
+template <class C, int RK>
+__device__ __forceinline__ RowVec<C::DT> load_tile(const char* base, uint32_t off, int nvalid) {
+    if constexpr (RK == kWhole) {
+        RowVec<C::DT> r;
+        r.w = load16_any(base + off);
+        return r;
+    } else {
+        return load_vec<C::DT, RK == kAligned, true>(base, off, nvalid, 0.0f);
+    }
+}
+template <class C, int RK>
+__device__ __forceinline__ void store_tile(char* base, uint32_t off, int nvalid, const RowOut<C::DT>& o) {
+    if constexpr (RK == kWhole) store16_any(base + off, o.pack());
+    else store_vec<C::DT, RK == kAligned>(base, off, nvalid, o);
+}
+
+// Whether every row of the tile and some column of every vector exist.
+template <class C>
+__device__ __forceinline__ bool tile_full(const Geo& g, const Dims& d) {
+    return g.trow0 + C::CT <= d.T && g.dcol0 + (C::TPR - 1) * C::V < d.D;
+}
+
 // One operand's rows of a tile: base of (batch row, first row, first lane) and
 // the bytes between rows, 32-bit inside a tile.
 struct TileRows {
     char* p;
     uint32_t st;
-    template <class C>
+    template <class C, int RK>
     __device__ __forceinline__ static TileRows of(const Rows& r, const Geo& g) {
-        return TileRows{r.row(g.bi, g.trow0) + (size_t)g.dcol0 * C::EB, (uint32_t)r.st};
+        return TileRows{r.row(g.bi, g.trow0) + (size_t)g.dcol0 * C::EB - (RK == kWhole ? 16 : 0), (uint32_t)r.st};
     }
     __device__ __forceinline__ uint32_t off(const Geo& g, int row, int T) const {
         return row_off(g, row, T, st);
@@ -188,11 +243,11 @@ __device__ Aff gated_bwd_tile_map(const GatedBwdArgs& x, int j, int bi, int col)
 }
 
 // Rates of the tile's lanes (lanes past D take the last one's; never used).
-template <class C>
+template <class C, int RK>
 __device__ __forceinline__ void tile_rates(float (&s_rate)[C::W], const float* decay, float scale,
                                            const Geo& g, int D) {
     if (threadIdx.x < C::W) {
-        const int c = g.dcol0 + (int)threadIdx.x;
+        const int c = slot_column<C, RK>(g, (int)threadIdx.x, D);
         s_rate[threadIdx.x] = gate_rate(decay[c < D ? c : D - 1], scale);
     }
     __syncthreads();
@@ -233,7 +288,7 @@ __device__ __forceinline__ void path_marker() {
 // forward
 // ---------------------------------------------------------------------------
 // OUT = false: state-only forward: only the thread holding row T-1 replays.
-template <class C, bool ALIGNED, bool RST, bool OUT>
+template <class C, int RK, bool RST, bool OUT>
 __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::OCC_F)))
 void gated_fwd_kernel(GatedFwdArgs x) {
     constexpr int V = C::V, W = C::W, RG = C::RG, NR = C::NR, TPR = C::TPR;
@@ -251,9 +306,9 @@ void gated_fwd_kernel(GatedFwdArgs x) {
     const int rg = l / TPR;
     const int cg = l % TPR;
     const Ticket tk = take_ticket(x.sc);
-    const Geo g = tile_geo<C, false>(tk.ticket, d, wave, rg, cg);
-    const TileRows px = TileRows::of<C>(x.p.x, g), pr = TileRows::of<C>(x.p.gr, g),
-                   pi = TileRows::of<C>(x.p.gi, g);
+    const Geo g = gated_geo<C, RK, false>(tk.ticket, d, wave, rg, cg);
+    const TileRows px = TileRows::of<C, RK>(x.p.x, g), pr = TileRows::of<C, RK>(x.p.gr, g),
+                   pi = TileRows::of<C, RK>(x.p.gi, g);
     char* po = static_cast<char*>(x.p.out) + g.tbase;
     const uint32_t rowbytes = (uint32_t)d.D * C::EB;
 
@@ -262,17 +317,17 @@ void gated_fwd_kernel(GatedFwdArgs x) {
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
         const int row = g.row0 + i;
-        rr[i] = load_vec<C::DT, ALIGNED, true>(pr.p, pr.off(g, row, d.T), g.nvalid, 0.0f);
-        ri[i] = load_vec<C::DT, ALIGNED, true>(pi.p, pi.off(g, row, d.T), g.nvalid, 0.0f);
-        rx[i] = load_vec<C::DT, ALIGNED, true>(px.p, px.off(g, row, d.T), g.nvalid, 0.0f);
+        rr[i] = load_tile<C, RK>(pr.p, pr.off(g, row, d.T), g.nvalid);
+        ri[i] = load_tile<C, RK>(pi.p, pi.off(g, row, d.T), g.nvalid);
+        rx[i] = load_tile<C, RK>(px.p, px.off(g, row, d.T), g.nvalid);
     }
-    tile_rates<C>(s_rate, x.p.decay, x.p.scale, g, d.D);
+    tile_rates<C, RK>(s_rate, x.p.decay, x.p.scale, g, d.D);
     float rate[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) rate[j] = s_rate[cg * V + j];
 
     // coefficients and summary, row by row
-    const bool full = g.trow0 + C::CT <= d.T && g.dcol0 + W <= d.D;
+    const bool full = tile_full<C>(g, d);
     float ca[NR][V], cb[NR][V];
     Aff m[V];
 #pragma unroll
@@ -300,8 +355,8 @@ void gated_fwd_kernel(GatedFwdArgs x) {
             const bool start = RST && ((rbits >> i) & 1u), gone = i >= g.nrows;
             if (RST && __any(start)) {
                 const int row = g.row0 + i;
-                const RowVec<C::DT> xs = load_vec<C::DT, ALIGNED>(px.p, px.off(g, row, d.T), g.nvalid, 0.0f);
-                const RowVec<C::DT> is = load_vec<C::DT, ALIGNED>(pi.p, pi.off(g, row, d.T), g.nvalid, 0.0f);
+                const RowVec<C::DT> xs = load_tile<C, RK>(px.p, px.off(g, row, d.T), g.nvalid);
+                const RowVec<C::DT> is = load_tile<C, RK>(pi.p, pi.off(g, row, d.T), g.nvalid);
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     const GatedStep s = gated_start_of(xs.get(j), is.get(j));
@@ -346,7 +401,7 @@ void gated_fwd_kernel(GatedFwdArgs x) {
         const size_t o = ((size_t)g.k * (size_t)d.nS + (size_t)g.s) * W + c;
         const bool more = g.k + 1 < d.NK;
         if (more) publish_u64(const_cast<unsigned long long*>(pqs) + o, pack_map(A));
-        const int dl = g.dcol0 + c;
+        const int dl = slot_column<C, RK>(g, c, d.D);
         const float base0 = (x.p.h0 && dl < d.D) ? x.p.h0[(size_t)g.bi * d.D + dl] : 0.0f;
         const Link lk{hs, pqs, d.nS, g.s, W, c};
         float hin;
@@ -384,7 +439,7 @@ void gated_fwd_kernel(GatedFwdArgs x) {
                     o.v[j] = h[j];
                 }
                 if constexpr (OUT)
-                    store_vec<C::DT, ALIGNED>(po, row_off(g, g.row0 + i, d.T, rowbytes), g.nvalid, o);
+                    store_tile<C, RK>(po, row_off(g, g.row0 + i, d.T, rowbytes), g.nvalid, o);
             }
         }
     };
@@ -400,7 +455,7 @@ void gated_fwd_kernel(GatedFwdArgs x) {
 // ---------------------------------------------------------------------------
 // reverse time
 // ---------------------------------------------------------------------------
-template <class C, bool ALIGNED, bool RST>
+template <class C, int RK, bool RST>
 __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::OCC_G)))
 void gated_bwd_kernel(GatedBwdArgs x) {
     constexpr int V = C::V, W = C::W, RG = C::RG, NR = C::NR, TPR = C::TPR;
@@ -418,12 +473,12 @@ void gated_bwd_kernel(GatedBwdArgs x) {
     const int rg = l / TPR;
     const int cg = l % TPR;
     const Ticket tk = take_ticket(x.sc);
-    const Geo g = tile_geo<C, true>(tk.ticket, d, wave, rg, cg);
+    const Geo g = gated_geo<C, RK, true>(tk.ticket, d, wave, rg, cg);
     const uint32_t rowbytes = (uint32_t)d.D * C::EB;
-    const TileRows px = TileRows::of<C>(x.p.x, g), pr = TileRows::of<C>(x.p.gr, g),
-                   pi = TileRows::of<C>(x.p.gi, g);
-    const TileRows qx = TileRows::of<C>(x.p.gx, g), qr = TileRows::of<C>(x.p.ggr, g),
-                   qi = TileRows::of<C>(x.p.ggi, g);
+    const TileRows px = TileRows::of<C, RK>(x.p.x, g), pr = TileRows::of<C, RK>(x.p.gr, g),
+                   pi = TileRows::of<C, RK>(x.p.gi, g);
+    const TileRows qx = TileRows::of<C, RK>(x.p.gx, g), qr = TileRows::of<C, RK>(x.p.ggr, g),
+                   qi = TileRows::of<C, RK>(x.p.ggi, g);
     const char* pg = static_cast<const char*>(x.p.g) + g.tbase;
     const int hrow0 = g.trow0 > 0 ? g.trow0 - 1 : 0;  // h_{t-1} is row t-1 of `out`
     const char* ph = static_cast<const char*>(x.p.out) + g.tbase - (size_t)(g.trow0 - hrow0) * rowbytes;
@@ -434,8 +489,8 @@ void gated_bwd_kernel(GatedBwdArgs x) {
 #pragma unroll
     for (int i = NR - 1; i >= 0; --i) {
         const int row = g.row0 + i;
-        rr[i] = load_vec<C::DT, ALIGNED, true>(pr.p, pr.off(g, row, d.T), g.nvalid, 0.0f);
-        rg_[i] = load_vec<C::DT, ALIGNED, true>(pg, row_off(g, row, d.T, rowbytes), g.nvalid, 0.0f);
+        rr[i] = load_tile<C, RK>(pr.p, pr.off(g, row, d.T), g.nvalid);
+        rg_[i] = load_tile<C, RK>(pg, row_off(g, row, d.T, rowbytes), g.nvalid);
     }
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -443,19 +498,19 @@ void gated_bwd_kernel(GatedBwdArgs x) {
         const int row = g.row0 + i;
         const int rc = row < d.T ? row : d.T - 1;
         const int hr = rc >= 1 ? rc - 1 : 0;
-        rh[i] = load_vec<C::DT, ALIGNED, true>(ph, (uint32_t)(hr - hrow0) * rowbytes + g.coff, g.nvalid, 0.0f);
-        rx[i] = load_vec<C::DT, ALIGNED, true>(px.p, px.off(g, row, d.T), g.nvalid, 0.0f);
-        ri[i] = load_vec<C::DT, ALIGNED, true>(pi.p, pi.off(g, row, d.T), g.nvalid, 0.0f);
+        rh[i] = load_tile<C, RK>(ph, (uint32_t)(hr - hrow0) * rowbytes + g.coff, g.nvalid);
+        rx[i] = load_tile<C, RK>(px.p, px.off(g, row, d.T), g.nvalid);
+        ri[i] = load_tile<C, RK>(pi.p, pi.off(g, row, d.T), g.nvalid);
     }
     __builtin_amdgcn_sched_barrier(0);
-    tile_rates<C>(s_rate, x.p.decay, x.p.scale, g, d.D);
+    tile_rates<C, RK>(s_rate, x.p.decay, x.p.scale, g, d.D);
     float rate[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) rate[j] = s_rate[cg * V + j];
 
     // reverse summary: the map from the carry entering the segment on the
     // right to the carry a_s lambda_s leaving its first row s
-    const bool full = g.trow0 + C::CT <= d.T && g.dcol0 + W <= d.D;
+    const bool full = tile_full<C>(g, d);
     Aff m[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) m[j] = aff_identity();
@@ -515,7 +570,7 @@ void gated_bwd_kernel(GatedBwdArgs x) {
         const size_t o = ((size_t)g.k * (size_t)d.nS + (size_t)g.s) * W + c;
         const bool more = g.k > 0;
         if (more) publish_u64(const_cast<unsigned long long*>(pqs) + o, pack_map(A));
-        const int dl = g.dcol0 + c;
+        const int dl = slot_column<C, RK>(g, c, d.D);
         const float base0 = (x.p.grad_last && dl < d.D) ? x.p.grad_last[(size_t)g.bi * d.D + dl] : 0.0f;
         const Link lk{hs, pqs, d.nS, g.s, W, c};
         float cin;
@@ -560,9 +615,9 @@ void gated_bwd_kernel(GatedBwdArgs x) {
             oi.v[j] = q.dgi;
             sum[j] += q.p;
         }
-        store_vec<C::DT, ALIGNED>(qx.p, qx.off(g, row, d.T), g.nvalid, ox);
-        store_vec<C::DT, ALIGNED>(qr.p, qr.off(g, row, d.T), g.nvalid, orr);
-        store_vec<C::DT, ALIGNED>(qi.p, qi.off(g, row, d.T), g.nvalid, oi);
+        store_tile<C, RK>(qx.p, qx.off(g, row, d.T), g.nvalid, ox);
+        store_tile<C, RK>(qr.p, qr.off(g, row, d.T), g.nvalid, orr);
+        store_tile<C, RK>(qi.p, qi.off(g, row, d.T), g.nvalid, oi);
     };
 #pragma unroll
     for (int i = NR - 1; i >= 0; --i) {
@@ -596,12 +651,13 @@ void gated_bwd_kernel(GatedBwdArgs x) {
         s_wav[wave][c].p = t;
     }
     __syncthreads();
-    if (tid < W && g.dcol0 + tid < d.D) {
+    const int dt = tid < W ? slot_column<C, RK>(g, tid, d.D) : d.D;
+    if (dt < d.D) {
         float t = 0.0f;
 #pragma unroll
         for (int w = 0; w < C::WAVES; ++w) t += s_wav[w][tid].p;
         const int nB = d.nS / d.nW;
-        x.part[((size_t)g.k * nB + g.bi) * (size_t)d.D + g.dcol0 + tid] = t;
+        x.part[((size_t)g.k * nB + g.bi) * (size_t)d.D + dt] = t;
     }
 }
 
@@ -644,6 +700,7 @@ GatedTile gated_tile(const Shape& s, int dir) {
     const int64_t row = s.D * (s.dtype == DT_F32 ? 4 : 2);
     const int64_t chains16 = s.B * ((row + 255) / 256), chains8 = s.B * ((row + 127) / 128);
     const bool wide = row > 128;
+    if (s.D < (s.dtype == DT_F32 ? Elem<DT_F32>::V : Elem<DT_BF16>::V)) return GatedTile{8, 128};  // kNarrow
     if (s.T <= 32 && wide) return GatedTile{16, 32};
     if (s.T <= 64 && wide) return GatedTile{16, 64};
     if (dir == 0 && s.dtype == DT_BF16 && wide && chains16 >= 64) return GatedTile{16, 64};
@@ -652,38 +709,50 @@ GatedTile gated_tile(const Shape& s, int dir) {
     return GatedTile{8, 128};
 }
 
-template <class C, bool AL>
+template <class C, int RK>
 void fwd_cfg(const GatedFwdArgs& x, hipStream_t st) {
     const dim3 grid(x.sc.total_tiles), block(C::NT);
     if (x.p.out) {
-        if (x.p.reset) hipLaunchKernelGGL((gated_fwd_kernel<C, AL, true, true>), grid, block, 0, st, x);
-        else hipLaunchKernelGGL((gated_fwd_kernel<C, AL, false, true>), grid, block, 0, st, x);
+        if (x.p.reset) hipLaunchKernelGGL((gated_fwd_kernel<C, RK, true, true>), grid, block, 0, st, x);
+        else hipLaunchKernelGGL((gated_fwd_kernel<C, RK, false, true>), grid, block, 0, st, x);
     } else {
-        if (x.p.reset) hipLaunchKernelGGL((gated_fwd_kernel<C, AL, true, false>), grid, block, 0, st, x);
-        else hipLaunchKernelGGL((gated_fwd_kernel<C, AL, false, false>), grid, block, 0, st, x);
+        if (x.p.reset) hipLaunchKernelGGL((gated_fwd_kernel<C, RK, true, false>), grid, block, 0, st, x);
+        else hipLaunchKernelGGL((gated_fwd_kernel<C, RK, false, false>), grid, block, 0, st, x);
     }
 }
 
-template <class C, bool AL>
+template <class C, int RK>
 void bwd_cfg(const GatedBwdArgs& x, hipStream_t st) {
     const dim3 grid(x.sc.total_tiles), block(C::NT);
-    if (x.p.reset) hipLaunchKernelGGL((gated_bwd_kernel<C, AL, true>), grid, block, 0, st, x);
-    else hipLaunchKernelGGL((gated_bwd_kernel<C, AL, false>), grid, block, 0, st, x);
+    if (x.p.reset) hipLaunchKernelGGL((gated_bwd_kernel<C, RK, true>), grid, block, 0, st, x);
+    else hipLaunchKernelGGL((gated_bwd_kernel<C, RK, false>), grid, block, 0, st, x);
 }
 
-template <int DT, bool AL>
-void fwd_t(const GatedTile& t, const GatedFwdArgs& x, hipStream_t st) {
-    if (t.tile == 32) fwd_cfg<Tile16x32<DT>, AL>(x, st);
-    else if (t.tile == 64) fwd_cfg<Tile16x64<DT>, AL>(x, st);
-    else if (t.tile == 128) fwd_cfg<Tile8x128<DT>, AL>(x, st);
-    else fwd_cfg<Tile8x256<DT>, AL>(x, st);
+template <int DT, int RK>
+void fwd_rk(const GatedTile& t, const GatedFwdArgs& x, hipStream_t st) {
+    if (t.tile == 32) fwd_cfg<Tile16x32<DT>, RK>(x, st);
+    else if (t.tile == 64) fwd_cfg<Tile16x64<DT>, RK>(x, st);
+    else if (t.tile == 128) fwd_cfg<Tile8x128<DT>, RK>(x, st);
+    else fwd_cfg<Tile8x256<DT>, RK>(x, st);
 }
-template <int DT, bool AL>
-void bwd_t(const GatedTile& t, const GatedBwdArgs& x, hipStream_t st) {
-    if (t.tile == 32) bwd_cfg<Tile16x32<DT>, AL>(x, st);
-    else if (t.tile == 64) bwd_cfg<Tile16x64<DT>, AL>(x, st);
-    else if (t.tile == 128) bwd_cfg<Tile8x128<DT>, AL>(x, st);
-    else bwd_cfg<Tile8x256<DT>, AL>(x, st);
+template <int DT, int RK>
+void bwd_rk(const GatedTile& t, const GatedBwdArgs& x, hipStream_t st) {
+    if (t.tile == 32) bwd_cfg<Tile16x32<DT>, RK>(x, st);
+    else if (t.tile == 64) bwd_cfg<Tile16x64<DT>, RK>(x, st);
+    else if (t.tile == 128) bwd_cfg<Tile8x128<DT>, RK>(x, st);
+    else bwd_cfg<Tile8x256<DT>, RK>(x, st);
+}
+template <int DT>
+void fwd_t(const GatedTile& t, bool al, const GatedFwdArgs& x, hipStream_t st) {
+    if (al) fwd_rk<DT, kAligned>(t, x, st);
+    else if (x.d.D >= Elem<DT>::V) fwd_rk<DT, kWhole>(t, x, st);
+    else fwd_cfg<Tile8x128<DT>, kNarrow>(x, st);
+}
+template <int DT>
+void bwd_t(const GatedTile& t, bool al, const GatedBwdArgs& x, hipStream_t st) {
+    if (al) bwd_rk<DT, kAligned>(t, x, st);
+    else if (x.d.D >= Elem<DT>::V) bwd_rk<DT, kWhole>(t, x, st);
+    else bwd_cfg<Tile8x128<DT>, kNarrow>(x, st);
 }
 
 Layout gated_layout(const GatedShape& s, int dir) {
@@ -735,8 +804,8 @@ hipError_t launch_gated_fused_fwd(const GatedShape& s, const GatedFwd& p, void* 
     x.polls = polls > 0 ? (uint32_t)polls : kDefaultPolls;
     const bool al = gated_fwd_aligned(s, p);
     const GatedTile t = gated_tile(Shape{s.B, s.T, s.D, s.dtype}, 0);
-    if (s.dtype == DT_F32) al ? fwd_t<DT_F32, true>(t, x, st) : fwd_t<DT_F32, false>(t, x, st);
-    else al ? fwd_t<DT_BF16, true>(t, x, st) : fwd_t<DT_BF16, false>(t, x, st);
+    if (s.dtype == DT_F32) fwd_t<DT_F32>(t, al, x, st);
+    else fwd_t<DT_BF16>(t, al, x, st);
     return hipGetLastError();
 }
 
@@ -752,8 +821,8 @@ hipError_t launch_gated_fused_bwd(const GatedShape& s, const GatedBwd& p, float*
     x.polls = polls > 0 ? (uint32_t)polls : kDefaultPolls;
     const bool al = gated_bwd_aligned(s, p);
     const GatedTile t = gated_tile(Shape{s.B, s.T, s.D, s.dtype}, 1);
-    if (s.dtype == DT_F32) al ? bwd_t<DT_F32, true>(t, x, st) : bwd_t<DT_F32, false>(t, x, st);
-    else al ? bwd_t<DT_BF16, true>(t, x, st) : bwd_t<DT_BF16, false>(t, x, st);
+    if (s.dtype == DT_F32) bwd_t<DT_F32>(t, al, x, st);
+    else bwd_t<DT_BF16>(t, al, x, st);
     return hipGetLastError();
 }
 
