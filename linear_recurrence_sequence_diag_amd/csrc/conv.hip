@@ -551,7 +551,7 @@ void bwd_rows_kind(const ConvShape& s, const ConvBwd& p, const ConvGrid& g, floa
 }  // namespace
 
 bool conv_fits(const ConvShape& s) {
-    if (s.D >= ((int64_t)1 << 31)) return false;
+    if (s.D > ((int64_t)1 << 29)) return false;  // a row's bytes in 32 bits
     for (const int rows : {fwd_rows(s), bwd_rows(s)}) {
         const int64_t chunks = chunks_of(s, rows);
         if (chunks >= ((int64_t)1 << 31)) return false;

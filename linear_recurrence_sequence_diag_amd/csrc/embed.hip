@@ -734,7 +734,7 @@ hipError_t sums_t(const Sorted& x, uint32_t chunks, const void* g, void* grad, h
 }  // namespace
 
 bool embed_fits(const EmbedShape& s) {
-    // 32-bit positions, keys and grid sizes; a row's vectors, 64 at a time, along
+    // 32-bit positions, keys and grid sizes (N below 2^26); a row's vectors, 64 at a time, along
     // the grid's second dimension (at most 65535)
     return s.N < ((int64_t)1 << 31) && s.V < ((int64_t)1 << 31) - 2 && s.D <= ((int64_t)1 << 23) &&
            (s.N + kWaves) / kWaves < ((int64_t)1 << 32) / kBlock;

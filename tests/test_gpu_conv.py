@@ -181,3 +181,23 @@ def test_refusals():
                 lambda: lr.short_conv_backward(c.x, c.w, c.b, c.g, workspace=torch.zeros(4, device="cuda"))):
         with pytest.raises(lr.LRScanError):
             bad()
+
+
+def test_offsets_past_32_bits():
+    B, T, D, n = 2, 150000, 8192, 40
+    x = torch.zeros(B, T, D, device="cuda", dtype=torch.bfloat16)
+    r = np.random.default_rng(0)
+    part, gp = (put(r.standard_normal((1, n, D)), "bf16") for _ in range(2))
+    x[-1, -n:] = part[0]
+    w = put(r.normal(0, 0.6, (4, D)), "f32")
+    g = torch.zeros_like(x)
+    g[-1, -n:] = gp[0]
+    out, last = lr.short_conv(x, w, activation="silu")
+    c = ref.Conv(host(part), host(w), None, True)
+    close("out", out[-1:, -n:], (c.out, c.E), "bf16")
+    assert np.array_equal(host(last[-1:]), c.last) and not out[:, :-n].any()
+    gx, gw, _, _ = lr.short_conv_backward(x, w, None, g, activation="silu")
+    want = c.grad(host(gp))
+    close("grad_x", gx[-1:, -n:], want["grad_x"], "bf16")
+    close("grad_weight", gw, want["grad_weight"], "f32")
+    assert not gx[:, :-n - 3].any()

@@ -315,3 +315,32 @@ def test_refusals():
     with pytest.raises(lr.LRScanError):
         lr.gated_scan_backward(c.x, c.gr, c.gi, c.decay, c.x, c.g,
                                workspace=torch.zeros(4, device="cuda"))
+
+
+def test_offsets_past_32_bits():
+    """Tensors of more than 2^32 bytes: the last segment of the last row, which
+    stands for itself, against the reference."""
+    B, T, D, n = 2, 150000, 8192, 200
+    bf = torch.bfloat16
+    x = torch.zeros(B, T, D, device="cuda", dtype=bf)
+    gr, gi = torch.zeros_like(x), torch.zeros_like(x)
+    r = np.random.default_rng(0)
+    small = [put(r.standard_normal((1, n, D)), "bf16") for _ in range(4)]
+    for t, v in zip((x, gr, gi), small):
+        t[-1, -n:] = v[0]
+    decay = put(r.normal(-4, 0.5, D), "f32")
+    m = torch.zeros(B, T, dtype=torch.bool, device="cuda")
+    m[-1, -n] = True
+    out, last = lr.gated_scan(x, gr, gi, decay, reset=m)
+    cols = np.r_[0:16, D - 16:D]
+    f = ref.Gated(*(host(t[..., cols]) for t in small[:3]), host(decay[cols]), 8.0, np.arange(n)[None] == 0)
+    close("out", out[-1:, -n:, cols], (f.h, f.E), "bf16")
+    close("last", last[-1:, cols], (f.h[:, -1], f.E[:, -1]), "f32")
+    g = torch.zeros_like(x)
+    g[-1, -n:] = small[3][0]
+    grads = lr.gated_scan_backward(x, gr, gi, decay, out, g, reset=m)
+    want = f.grad(host(out[-1:, -n:, cols]), host(small[3][..., cols]))
+    for name, got in zip(("grad_x", "grad_r", "grad_i"), grads):
+        close(name, got[-1:, -n:, cols], want[name], "bf16")
+        assert not got[0].any() and not got[1, :-n - 1].any()
+    close("grad_decay", grads[3][cols], want["grad_decay"], "f32")
