@@ -16,6 +16,8 @@
 //    of the work.  It needs no sort, so the sort's launches do it: after the
 //    few workgroups that sort come many that clear a share of the table, and
 //    the sort's own time is hidden behind them.
+//    (Up to 256 tokens are not sorted at all: each looks for its own row's
+//    other tokens among them, and a row's first token adds them.)
 //  * The sorted tokens are cut into chunks of equal length, whatever rows they
 //    name.  A wavefront adds its chunk's tokens row by row in fp32 and writes
 //    every row that lies inside the chunk.  A row that crosses a chunk's end
@@ -460,7 +462,7 @@ __device__ __forceinline__ void put_row(const Sorted& s, void* grad, uint32_t ro
 // One wavefront: one chunk, 64 vectors of the rows.
 template <int DT, int GDT>
 __global__ __launch_bounds__(kWave) void chunk_sum_kernel(Sorted s, const void* g, void* grad) {
-    constexpr int V = Elem<DT>::V, U = 8;
+    constexpr int V = Elem<DT>::V, U = 16;
     const uint32_t c = blockIdx.x, lane = threadIdx.x;
     const Columns<DT> col(((int64_t)blockIdx.y * kWave + lane) * V, s.D, s.blocks);
     const uint32_t p0 = c * s.chunk, p1 = s.N - p0 > s.chunk ? p0 + s.chunk : s.N;
@@ -521,6 +523,60 @@ __global__ __launch_bounds__(kWave) void chunk_sum_kernel(Sorted s, const void* 
     else if (after == cur) col.store_floats(s.tail + (size_t)c * s.D, sum, false);
     else put_row<DT, GDT>(s, grad, cur, col, sum);
 }
+
+// Up to kDirectTokens tokens, unsorted: one wavefront to a token and 64 vectors.
+// The token's row is summed by its first token, in the order of positions.
+constexpr uint32_t kDirectTokens = 256;
+template <int DT, int GDT, class Src>
+__global__ __launch_bounds__(kWave) void direct_sum_kernel(Sorted s, Src src, const void* g, void* grad) {
+    constexpr int V = Elem<DT>::V, U = 8, Q = kDirectTokens / kWave;
+    const uint32_t n = blockIdx.x, lane = threadIdx.x;
+    uint32_t key[Q];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+        const uint32_t t = q * kWave + lane;
+        key[q] = t < s.N ? src.key(t) : s.V;
+    }
+    const uint32_t mine = uniform(src.key(n));
+    if (mine >= s.V) return;
+    unsigned long long same[Q];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) same[q] = __ballot(key[q] == mine);
+    uint32_t first = 0;
+#pragma unroll
+    for (int q = Q - 1; q >= 0; --q)
+        if (same[q]) first = q * kWave + (uint32_t)__builtin_ctzll(same[q]);
+    if (first != n) return;
+    const Columns<DT> col(((int64_t)blockIdx.y * kWave + lane) * V, s.D, s.blocks);
+    float sum[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) sum[j] = 0.0f;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+        while (same[q]) {  // eight rows at a time, the last one again in place of none
+            RowVec<DT> r[U];
+            uint32_t have = 0, at = 0;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (same[q]) {
+                    at = q * kWave + (uint32_t)__builtin_ctzll(same[q]);
+                    same[q] &= same[q] - 1;
+                    have = u + 1;
+                }
+                r[u] = col.load(g, at, s.D);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if ((uint32_t)u < have) {
+#pragma unroll
+                    for (int j = 0; j < V; ++j) sum[j] += r[u].get(j);
+                }
+        }
+    }
+    put_row<DT, GDT>(s, grad, mine, col, sum);
+}
+
+__global__ __launch_bounds__(kBlock) void clear_kernel(Clear c) { clear_share(c, 0); }
 
 // A row that starts in chunk c and goes on past it: the chunk's tail, then the
 // heads of the chunks it runs through, a fourth of them to each wavefront.
@@ -731,6 +787,31 @@ hipError_t sums_t(const Sorted& x, uint32_t chunks, const void* g, void* grad, h
     return hipGetLastError();
 }
 
+// Without a sort: the table cleared, then the rows summed.
+template <int DT, int GDT, class Src>
+hipError_t direct_t(const Sorted& x, Src src, const void* g, void* grad, uint64_t bytes, hipStream_t st) {
+    Clearing clearing{static_cast<char*>(grad), bytes, 1};
+    unsigned groups = 0;
+    const Clear c = clearing.next(&groups);
+    if (groups > 0) {
+        hipLaunchKernelGGL(clear_kernel, dim3(groups), dim3(kBlock), 0, st, c);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    const int64_t lanes = (int64_t)kWave * Elem<DT>::V;
+    hipLaunchKernelGGL((direct_sum_kernel<DT, GDT, Src>), dim3(x.N, (uint32_t)((x.D + lanes - 1) / lanes)),
+                       dim3(kWave), 0, st, x, src, g, grad);
+    return hipGetLastError();
+}
+
+template <class Src>
+hipError_t direct(const EmbedShape& s, const Sorted& x, Src src, const void* g, void* grad, int grad_dtype,
+                  uint64_t bytes, hipStream_t st) {
+    if (s.dtype == DT_F32) return direct_t<DT_F32, DT_F32>(x, src, g, grad, bytes, st);
+    if (grad_dtype == DT_F32) return direct_t<DT_BF16, DT_F32>(x, src, g, grad, bytes, st);
+    return direct_t<DT_BF16, DT_BF16>(x, src, g, grad, bytes, st);
+}
+
 }  // namespace
 
 bool embed_fits(const EmbedShape& s) {
@@ -762,6 +843,12 @@ hipError_t launch_embed_bwd(const EmbedShape& s, const void* ids, const void* g,
     const uint64_t row = (uint64_t)s.D * (grad_dtype == DT_F32 ? 4 : 2);
     const uint64_t bytes = add ? 0 : (uint64_t)s.V * row;
     char* table = static_cast<char*>(grad);
+    if (s.N <= kDirectTokens) {
+        const Sorted x{nullptr, nullptr, (uint32_t)s.N, (uint32_t)s.V, 0, nullptr, nullptr, scale, add, s.D,
+                       whole_blocks(s, grad)};
+        return s.id_bytes == 8 ? direct(s, x, KeysFromIds<8>{ids, s.V}, g, grad, grad_dtype, bytes, st)
+                               : direct(s, x, KeysFromIds<4>{ids, s.V}, g, grad, grad_dtype, bytes, st);
+    }
     int at = 0;
     const hipError_t e =
         s.id_bytes == 8

@@ -58,8 +58,8 @@ def run(ids, V, D, dtype, idt=torch.int64, scale=1.25, seed=1):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("kind", ["uniform", "zipf", "one", "none", "descending"])
-@pytest.mark.parametrize("n,V,D", [(1, 1, 1), (3, 7, 5), (70, 300, 64), (2500, 900, 33), (5000, 2000, 16),
-                                   (4100, 5, 130)])
+@pytest.mark.parametrize("n,V,D", [(1, 1, 1), (3, 7, 5), (70, 300, 64), (256, 40, 20), (257, 40, 20),
+                                   (2500, 900, 33), (5000, 2000, 16), (4100, 5, 130), (8193, 300, 12)])
 def test_gradient(n, V, D, kind, dtype):
     log(f"{n} {V} {D} {kind} {dtype}")
     run(make_ids(kind, n, V), V, D, dtype)
