@@ -244,14 +244,22 @@ __global__ __launch_bounds__(kBlock) void sort_scatter_kernel(Src src, SortPass 
     const uint32_t d = tid * 4;
     uint32_t total[4] = {0, 0, 0, 0}, before[4] = {0, 0, 0, 0};
     if (d < digits) {
-#pragma unroll 4
-        for (uint32_t b = 0; b < p.blocks; ++b) {
-            const uint4 c = *reinterpret_cast<const uint4*>(counts + (size_t)b * digits + d);
-            const uint32_t cq[4] = {c.x, c.y, c.z, c.w};
+        constexpr uint32_t U = 16;  // loads in flight (64 workgroups, 8-bit digits: 13 -> 11 us)
+        for (uint32_t b0 = 0; b0 < p.blocks; b0 += U) {
+            uint4 c[U];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                before[q] += b < blockIdx.x ? cq[q] : 0u;
-                total[q] += cq[q];
+            for (uint32_t u = 0; u < U; ++u)
+                c[u] = *reinterpret_cast<const uint4*>(
+                    counts + (size_t)(b0 + u < p.blocks ? b0 + u : p.blocks - 1) * digits + d);
+#pragma unroll
+            for (uint32_t u = 0; u < U; ++u) {
+                const uint32_t cq[4] = {c[u].x, c[u].y, c[u].z, c[u].w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint32_t n = b0 + u < p.blocks ? cq[q] : 0u;
+                    before[q] += b0 + u < blockIdx.x ? n : 0u;
+                    total[q] += n;
+                }
             }
         }
     }
@@ -462,7 +470,7 @@ __device__ __forceinline__ void put_row(const Sorted& s, void* grad, uint32_t ro
 // One wavefront: one chunk, 64 vectors of the rows.
 template <int DT, int GDT>
 __global__ __launch_bounds__(kWave) void chunk_sum_kernel(Sorted s, const void* g, void* grad) {
-    constexpr int V = Elem<DT>::V, U = 16;
+    constexpr int V = Elem<DT>::V, U = 8;
     const uint32_t c = blockIdx.x, lane = threadIdx.x;
     const Columns<DT> col(((int64_t)blockIdx.y * kWave + lane) * V, s.D, s.blocks);
     const uint32_t p0 = c * s.chunk, p1 = s.N - p0 > s.chunk ? p0 + s.chunk : s.N;
