@@ -9,7 +9,7 @@
 // zero, and a tap that would reach across a reset counts as zero.
 //
 // A thread owns four adjacent channels of a chunk of consecutive
-// tokens and walks it in groups of four, whose rows are loaded together.  The
+// tokens and walks it in groups of tokens whose rows are loaded together.  The
 // last K - 1 inputs stay in registers, so a chunk re-reads only K - 1 rows of
 // its neighbour; a reset clears them, which drops an infinity or NaN of the
 // segment before.  The backward walks in the same order, recomputes z, and
@@ -45,19 +45,26 @@ constexpr int V = kQuad;  // channels of a thread
 // Tokens of a chunk.  The backward's walk goes K - 1 tokens past its chunk, so
 // that walk is what is a whole number of groups.
 //
-// Long chunks re-read less, short ones make more wavefronts: the longest of five
-// lengths that leaves ten wavefronts for each of the 256 CUs (bf16, K = 4,
-// reverse: [8, 2048, 2560] 72 us in chunks of 57 tokens, 96 in 15; [1, 2048,
-// 1024] 40 in 57, 17 in 9).  A thread of four channels beats one of eight there
-// (72 against 85; forward 43 against 48): its state leaves four wavefronts a SIMD
-// in the reverse walk and eight in the forward one.
+// Long chunks re-read less, short ones make more wavefronts: the longest of
+// some lengths that leaves six wavefronts for each of the 256 CUs (reverse,
+// bf16, K = 4: [8, 2048, 2560] 69 us in chunks of 57 tokens, 96 in 15; [8, 2048,
+// 1024] 39 in 27, 50 in 57; [1, 2048, 1024] 16 in 9, 40 in 57).  The forward,
+// with no sums to carry, takes at most 18 tokens, its four wavefronts side by
+// side along the rows, so that the rows in flight lie together ([16, 4096,
+// 2560] bf16 135 us, 146 in chunks of 60 one after the other).
+//
+// A thread of four channels beats one of eight (reverse 72 against 85, forward
+// 43 against 48, [8, 2048, 2560] bf16): its state leaves four wavefronts a SIMD in
+// the reverse walk and eight in the forward one.
+constexpr uint32_t kFwdWidth = 256, kBwdWidth = 64;  // threads along a row, at most
+constexpr int kFwdTokens = 18, kBwdTokens = 60;      // of a walk, at most
 int fwd_rows(const ConvShape& s);
 int bwd_rows(const ConvShape& s);
 
 // Workgroup blockIdx.x covers lane block blockIdx.x % ncb and `groups`
 // consecutive chunks (a chunk: `rows` tokens of one batch row).
 struct ConvGrid {
-    uint32_t tpr;      // threads along a row (a power of two, at most 64)
+    uint32_t tpr;      // threads along a row (a power of two, at most kBlock)
     uint32_t groups;   // kBlock / tpr chunks side by side
     uint32_t vpr;      // quads in a row
     uint32_t ncb;      // lane blocks
@@ -69,12 +76,12 @@ struct ConvGrid {
 
 int64_t chunks_of(const ConvShape& s, int rows) { return s.B * ((s.T + rows - 1) / rows); }
 
-ConvGrid conv_grid(const ConvShape& s, int rows) {
+ConvGrid conv_grid(const ConvShape& s, int rows, uint32_t widest) {
     ConvGrid g;
     g.rows = rows;
     g.vpr = (uint32_t)((s.D + V - 1) / V);
     g.tpr = 1;
-    while (g.tpr < 64 && g.tpr < g.vpr) g.tpr *= 2;
+    while (g.tpr < widest && g.tpr < g.vpr) g.tpr *= 2;
     g.groups = kBlock / g.tpr;
     g.ncb = (g.vpr + g.tpr - 1) / g.tpr;
     g.nchunks = (uint32_t)((s.T + rows - 1) / rows);
@@ -83,16 +90,16 @@ ConvGrid conv_grid(const ConvShape& s, int rows) {
     return g;
 }
 
-int chunk_groups(const ConvShape& s) {
+int chunk_groups(const ConvShape& s, int most) {
     const int u = group_of(s.K);
     const int64_t per = (s.D + V * 64 - 1) / (V * 64);  // wavefronts to a row
     for (const int n : {60 / u, 30 / u, 3, 2})
-        if (s.B * ((s.T + n * u - 1) / (n * u)) * per >= 2560) return n;
+        if (n * u <= most && s.B * ((s.T + n * u - 1) / (n * u)) * per >= 1536) return n;
     return 1;
 }
-int fwd_rows(const ConvShape& s) { return chunk_groups(s) * group_of(s.K); }
+int fwd_rows(const ConvShape& s) { return chunk_groups(s, kFwdTokens) * group_of(s.K); }
 int bwd_rows(const ConvShape& s) {
-    const int n = chunk_groups(s);
+    const int n = chunk_groups(s, kBwdTokens);
     return (n > 1 ? n : 2) * group_of(s.K) - (s.K - 1);
 }
 
@@ -107,7 +114,7 @@ template <bool UNI>
 __device__ __forceinline__ ConvPos conv_pos(const ConvGrid& g, int64_t T, int64_t D) {
     const uint32_t cb = blockIdx.x % g.ncb, rb = blockIdx.x / g.ncb;
     const uint32_t lane = threadIdx.x & (g.tpr - 1);
-    const uint32_t grp = UNI ? uniform((int)(threadIdx.x / kWave)) : threadIdx.x / g.tpr;
+    const uint32_t grp = UNI ? uniform((int)(threadIdx.x / g.tpr)) : threadIdx.x / g.tpr;
     const uint32_t chunk = rb * g.groups + grp, vec = cb * g.tpr + lane;
     ConvPos p;
     p.nvalid = 0;
@@ -536,13 +543,13 @@ void step_kind(const ConvShape& s, const ConvFwd& p, hipStream_t st) {
 
 template <int DT>
 void fwd_rows_kind(const ConvShape& s, const ConvFwd& p, const ConvGrid& g, hipStream_t st) {
-    if (g.tpr == kWave) s.D % V == 0 ? fwd_taps<DT, true, true>(s, p, g, st) : fwd_taps<DT, false, true>(s, p, g, st);
+    if (g.tpr >= kWave) s.D % V == 0 ? fwd_taps<DT, true, true>(s, p, g, st) : fwd_taps<DT, false, true>(s, p, g, st);
     else s.D % V == 0 ? fwd_taps<DT, true, false>(s, p, g, st) : fwd_taps<DT, false, false>(s, p, g, st);
 }
 
 template <int DT>
 void bwd_rows_kind(const ConvShape& s, const ConvBwd& p, const ConvGrid& g, float* part, hipStream_t st) {
-    if (g.tpr == kWave)
+    if (g.tpr >= kWave)
         s.D % V == 0 ? bwd_taps<DT, true, true>(s, p, g, part, st) : bwd_taps<DT, false, true>(s, p, g, part, st);
     else
         s.D % V == 0 ? bwd_taps<DT, true, false>(s, p, g, part, st) : bwd_taps<DT, false, false>(s, p, g, part, st);
@@ -552,10 +559,10 @@ void bwd_rows_kind(const ConvShape& s, const ConvBwd& p, const ConvGrid& g, floa
 
 bool conv_fits(const ConvShape& s) {
     if (s.D > ((int64_t)1 << 29)) return false;  // a row's bytes in 32 bits
-    for (const int rows : {fwd_rows(s), bwd_rows(s)}) {
-        const int64_t chunks = chunks_of(s, rows);
-        if (chunks >= ((int64_t)1 << 31)) return false;
-        const ConvGrid g = conv_grid(s, rows);
+    for (int dir = 0; dir < 2; ++dir) {
+        const int rows = dir == 0 ? fwd_rows(s) : bwd_rows(s);
+        if (chunks_of(s, rows) >= ((int64_t)1 << 31)) return false;
+        const ConvGrid g = conv_grid(s, rows, dir == 0 ? kFwdWidth : kBwdWidth);
         // work-items of the grid in 32 bits
         if ((uint64_t)g.ncb * g.blocks >= ((uint64_t)1 << 32) / kBlock) return false;
     }
@@ -563,11 +570,11 @@ bool conv_fits(const ConvShape& s) {
 }
 
 size_t conv_part_bytes(const ConvShape& s) {
-    return (size_t)conv_grid(s, bwd_rows(s)).blocks * (size_t)(s.K + 1) * (size_t)s.D * 4;
+    return (size_t)conv_grid(s, bwd_rows(s), kBwdWidth).blocks * (size_t)(s.K + 1) * (size_t)s.D * 4;
 }
 
 size_t conv_sum_scratch(const ConvShape& s) {
-    return column_sum_scratch(conv_grid(s, bwd_rows(s)).blocks, (s.K + 1) * s.D);
+    return column_sum_scratch(conv_grid(s, bwd_rows(s), kBwdWidth).blocks, (s.K + 1) * s.D);
 }
 
 hipError_t launch_conv_fwd(const ConvShape& s, const ConvFwd& p, hipStream_t st) {
@@ -576,7 +583,7 @@ hipError_t launch_conv_fwd(const ConvShape& s, const ConvFwd& p, hipStream_t st)
         else step_kind<DT_BF16>(s, p, st);
         return hipGetLastError();
     }
-    const ConvGrid g = conv_grid(s, fwd_rows(s));
+    const ConvGrid g = conv_grid(s, fwd_rows(s), kFwdWidth);
     if (s.dtype == DT_F32) fwd_rows_kind<DT_F32>(s, p, g, st);
     else fwd_rows_kind<DT_BF16>(s, p, g, st);
     return hipGetLastError();
@@ -584,7 +591,7 @@ hipError_t launch_conv_fwd(const ConvShape& s, const ConvFwd& p, hipStream_t st)
 
 hipError_t launch_conv_bwd(const ConvShape& s, const ConvBwd& p, float* part, float* scratch,
                            float* grad_w, float* grad_bias, hipStream_t st) {
-    const ConvGrid g = conv_grid(s, bwd_rows(s));
+    const ConvGrid g = conv_grid(s, bwd_rows(s), kBwdWidth);
     if (s.dtype == DT_F32) bwd_rows_kind<DT_F32>(s, p, g, part, st);
     else bwd_rows_kind<DT_BF16>(s, p, g, part, st);
     const hipError_t e = hipGetLastError();
