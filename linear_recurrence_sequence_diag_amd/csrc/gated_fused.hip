@@ -275,15 +275,6 @@ __device__ __forceinline__ uint32_t start_bits(const uint8_t* reset, const Geo& 
     return bits;
 }
 
-// Different empty statements at the top of the two versions of a loop: without
-// them the compiler hoists their common start above the branch and keeps its
-// registers alive into both, which spilled.
-template <bool PLAIN>
-__device__ __forceinline__ void path_marker() {
-    if constexpr (PLAIN) asm volatile("; plain rows");
-    else asm volatile("; any rows");
-}
-
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
@@ -326,7 +317,10 @@ void gated_fwd_kernel(GatedFwdArgs x) {
 #pragma unroll
     for (int j = 0; j < V; ++j) rate[j] = s_rate[cg * V + j];
 
-    // coefficients and summary, row by row
+    // Coefficients and summary, row by row.  Segment starts and rows that do not
+    // exist are put right under wavefront-wide branches, as few rows have them,
+    // rather than by selects for every element ([8, 2048, 2560] bf16 with a start
+    // every 512 tokens: 85 -> 74 us; folding such a wavefront's rows twice: 76).
     const bool full = tile_full<C>(g, d);
     float ca[NR][V], cb[NR][V];
     Aff m[V];
@@ -334,42 +328,37 @@ void gated_fwd_kernel(GatedFwdArgs x) {
     for (int j = 0; j < V; ++j) m[j] = aff_identity();
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
+        const bool start = RST && ((rbits >> i) & 1u), gone = i >= g.nrows;
+        const bool starts = RST && __any(start);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const GatedStep s = gated_step_of(rx[i].get(j), rr[i].get(j), ri[i].get(j), rate[j]);
             ca[i][j] = s.a;
             cb[i][j] = s.b;
-            fold_fwd<false>(m[j], s, false);
         }
-    }
-    // A wavefront that holds a segment start or a row that does not exist puts
-    // those rows right (a start's input term from its reloaded row) and folds
-    // again, rather than every element paying for selects: few wavefronts do
-    // ([8, 2048, 2560] bf16 with a start every 512 tokens: 85 -> 80 us).
-    const bool plain = __all(full && rbits == 0);
-    if (!plain) {
+        if (starts) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) m[j] = aff_identity();
-#pragma unroll
-        for (int i = 0; i < NR; ++i) {
-            const bool start = RST && ((rbits >> i) & 1u), gone = i >= g.nrows;
-            if (RST && __any(start)) {
-                const int row = g.row0 + i;
-                const RowVec<C::DT> xs = load_tile<C, RK>(px.p, px.off(g, row, d.T), g.nvalid);
-                const RowVec<C::DT> is = load_tile<C, RK>(pi.p, pi.off(g, row, d.T), g.nvalid);
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const GatedStep s = gated_start_of(xs.get(j), is.get(j));
-                    ca[i][j] = start ? s.a : ca[i][j];
-                    cb[i][j] = start ? s.b : cb[i][j];
-                }
+            for (int j = 0; j < V; ++j) {
+                const GatedStep s = gated_start_of(rx[i].get(j), ri[i].get(j));
+                ca[i][j] = start ? s.a : ca[i][j];
+                cb[i][j] = start ? s.b : cb[i][j];
             }
+        }
+        if (!full) {
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 ca[i][j] = gone ? 1.0f : ca[i][j];
                 cb[i][j] = gone ? 0.0f : cb[i][j];
-                fold_fwd<RST>(m[j], GatedStep{ca[i][j], cb[i][j]}, start);
             }
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            m[j].p = ca[i][j] * m[j].p;
+            m[j].q = fmaf(ca[i][j], m[j].q, cb[i][j]);
+        }
+        if (starts) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) m[j] = start ? Aff{-0.0f, cb[i][j]} : m[j];
         }
     }
     const int seg = wave * RG + rg;
@@ -424,27 +413,25 @@ void gated_fwd_kernel(GatedFwdArgs x) {
     for (int j = 0; j < V; ++j)
         h[j] = gated_apply<RST>(s_seg[seg][cg * V + j],
                                 gated_apply<RST>(s_wav[wave][cg * V + j], s_hin[cg * V + j]));
-    const auto replay = [&](auto plain) {
-        constexpr bool PLAIN = decltype(plain)::value;
-        path_marker<PLAIN>();
 #pragma unroll
-        for (int i = 0; i < NR; ++i) {
-            if (PLAIN || i < g.nrows) {
-                const bool start = !PLAIN && RST && ((rbits >> i) & 1u);
-                RowOut<C::DT> o;
+    for (int i = 0; i < NR; ++i) {
+        const bool start = RST && ((rbits >> i) & 1u);
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float n = fmaf(ca[i][j], h[j], cb[i][j]);
-                    h[j] = start ? cb[i][j] : n;
-                    o.v[j] = h[j];
-                }
-                if constexpr (OUT)
-                    store_tile<C, RK>(po, row_off(g, g.row0 + i, d.T, rowbytes), g.nvalid, o);
-            }
+        for (int j = 0; j < V; ++j) {
+            const float n = fmaf(ca[i][j], h[j], cb[i][j]);  // (of a row that does not exist: h itself)
+            h[j] = n;
         }
-    };
-    if (plain) replay(std::true_type{});
-    else replay(std::false_type{});
+        if (RST && __any(start)) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) h[j] = start ? cb[i][j] : h[j];
+        }
+        if (OUT && (full || i < g.nrows)) {
+            RowOut<C::DT> o;
+#pragma unroll
+            for (int j = 0; j < V; ++j) o.v[j] = h[j];
+            store_tile<C, RK>(po, row_off(g, g.row0 + i, d.T, rowbytes), g.nvalid, o);
+        }
+    }
     if (x.p.last && ends) {
 #pragma unroll
         for (int j = 0; j < V; ++j)
@@ -515,14 +502,17 @@ void gated_bwd_kernel(GatedBwdArgs x) {
 #pragma unroll
     for (int j = 0; j < V; ++j) m[j] = aff_identity();
 #pragma unroll
-    for (int i = NR - 1; i >= 0; --i)
+    for (int i = NR - 1; i >= 0; --i) {
+        const bool start = RST && ((rbits >> i) & 1u);
 #pragma unroll
         for (int j = 0; j < V; ++j)
             fold_rev<false>(m[j], gated_a_of(rr[i].get(j), rate[j]), rg_[i].get(j), false);
-    // with a segment start or a row that does not exist: folded again, as in
-    // the forward
-    const bool plain = __all(full && rbits == 0);
-    if (!plain) {
+        if (RST && __any(start)) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) m[j] = start ? Aff{-0.0f, 0.0f} : m[j];
+        }
+    }
+    if (!full) {  // folded again, without the rows that do not exist
 #pragma unroll
         for (int j = 0; j < V; ++j) m[j] = aff_identity();
 #pragma unroll
@@ -591,7 +581,9 @@ void gated_bwd_kernel(GatedBwdArgs x) {
                                     gated_apply<RST>(s_wav[wave][cg * V + j], s_cin[cg * V + j]));
         sum[j] = 0.0f;
     }
-    // one row; STARTS: some thread of the wavefront has a segment start there
+    // One row; STARTS: some thread of the wavefront has a segment start there (as
+    // a version of its own: the selects under a branch in one version spilled,
+    // 166 against 158 us).
     const auto replay = [&](int i, auto starts) {
         constexpr bool STARTS = decltype(starts)::value;
         const int row = g.row0 + i;

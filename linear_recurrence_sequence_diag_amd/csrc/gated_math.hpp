@@ -15,6 +15,7 @@ namespace lrscan {
 
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kLog2Ln2 = -0.52876637294489770f;  // log2(ln 2)
 
 // softplus(x) = max(x, 0) + log(1 + e), e = e^-|x|, once per channel.  The
 // logarithm is 2 artanh(t) with t = e / (2 + e) <= 1/3, by its series; the first
@@ -108,20 +109,22 @@ struct GatedGrad {
 };
 __device__ __forceinline__ GatedGrad gated_grad_of(float x, float gr, float gi, float rate,
                                                    float h_prev, float lam) {
-    const Sigmoid r = sigmoid_pair(gr);
+    // r with ln 2 (1 - r): the factor comes with the exponential
+    const float er = __builtin_amdgcn_exp2f(fmaf(gr, -kLog2e, kLog2Ln2));
+    const float r = __builtin_amdgcn_rcpf(fmaf(er, kLog2e, 1.0f));
+    const float cr = fminf(er * r, kLn2);
     const Sigmoid ig = sigmoid_pair(gi);
-    const float y2 = rate * r.s;
+    const float y2 = rate * r;
     const float a = __builtin_amdgcn_exp2f(y2);
     const float v = one_minus_sq(a, y2);
-    // 1 / beta; 0 where beta is 0 or below 1e-19 (the reciprocal root of a
-    // denormal would be infinite), so that y / beta takes its limit there
-    const float inv = v < 0x1p-126f ? 0.0f : __builtin_amdgcn_rsqf(v);
+    // i / beta; below 2^-126, where the reciprocal root of a denormal would be
+    // infinite, beta counts as 1e-19: y / beta is near its limit 0 then anyway
+    const float w = __builtin_amdgcn_rsqf(fmaxf(v, 0x1p-126f)) * ig.s;
     GatedGrad o;
-    o.dx = (lam * (v * inv)) * ig.s;
+    o.dx = lam * (v * w);
     o.dgi = (o.dx * x) * ig.c;
-    const float ay = a * y2;
-    o.p = lam * (ay * fmaf(-a, inv * (ig.s * x), h_prev));
-    o.dgr = o.p * (kLn2 * r.c);
+    o.p = lam * ((a * y2) * fmaf(-a, w * x, h_prev));
+    o.dgr = o.p * cr;
     o.a = a;
     return o;
 }
