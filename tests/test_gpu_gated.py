@@ -101,6 +101,24 @@ def test_resets_states_and_projected_gates(reset, shape, dtype, algo):
     Case(*shape, dtype, reset=reset, states=True, proj=True).check(algo=algo)
 
 
+@pytest.mark.parametrize("reset", [None, "some"])
+@pytest.mark.parametrize("algo", ["seq", "fused"])
+@pytest.mark.parametrize("shape", [(1051, 7, 1999), (1051, 32, 500)])
+def test_the_last_states_gradient_may_cancel_the_last_rows(shape, algo, reset):
+    """Among this many channels some where both, and the sum of the row before, are nearly nothing."""
+    log(f"{shape} {algo} {reset}")
+    Case(*shape, "f32", reset=reset, states=True).check(algo=algo)
+
+
+@pytest.mark.parametrize("algo", ["auto", "seq"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(2101, 3, 1000), (2101, 2, 1001), (4203, 4, 500), (1051, 7, 1999)])
+def test_short_sequences_that_share_a_channels_rate(shape, dtype, algo):
+    """Several batch rows to a thread, the last thread's fewer; states and resets of each row its own."""
+    log(f"{shape} {dtype} {algo}")
+    Case(*shape, dtype, reset="some", states=True).check(algo=algo)
+
+
 @pytest.mark.parametrize("algo", ALGOS)
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_strided_operands(dtype, algo):
