@@ -464,15 +464,24 @@ int plain_workspace(size_t need, const lrscan_opts* o, hipStream_t st, void** ou
 bool scale_ok(float scale) { return std::isfinite(scale) && scale > 0.0f; }
 
 // The per-lane walk for sequences of a few steps, whose tiles would be mostly
-// idle rows.  Measured on MI355X (caches flushed, us forward / reverse, 32-row
-// tiles against the walk): bf16 [4096,4,1024] 187 / 316 against 47 / 93,
-// [2048,8,2560] 234 / 404 against 86 / 180, [1024,16,2560] 125 / 234 against
-// 86 / 179, [512,32,2560] 75 / 145 against 92 / 198, [16,16,2560] 8 / 14
-// against 18 / 37; fp32 [1024,16,2560] 144 / 296 against 159 / 302.
+// idle rows; rows that are no whole vectors gain less.  Measured on MI355X
+// (caches flushed, us forward / reverse, tiles against the walk):
+//   bf16 [128,4,1024]   9.8 /  17 against 8.6 /  16   fp32  10 /  18 against 6.6 /  13
+//        [256,8,1024]    16 /  29         12 /  24           17 /  32         11 /  23
+//        [256,16,1024]   17 /  32         18 /  37           19 /  36         17 /  37
+//        [512,16,1024]   29 /  55         21 /  45           32 /  64         27 /  58
+//        [4096,4,1024]  176 / 304         37 /  63          186 / 373         53 / 108
+//        [1024,32,2560] 135 / 270        137 / 264          213 / 448        252 / 505
+//        [256,2,1023]    19 /  32         13 /  22           17 /  32         11 /  20
+//        [1024,4,1023]   61 / 103         26 /  71           55 / 111         38 /  67
+//        [512,8,1023]    36 /  62         36 /  67           33 /  66         39 /  69
 bool gated_prefer_seq(const GatedShape& s) {
     const int64_t lanes = s.B * s.D;
-    return s.T <= 2 || (s.T <= 8 && lanes >= ((int64_t)1 << 18)) ||
-           (s.T <= 16 && s.dtype == LRSCAN_BF16 && lanes >= ((int64_t)1 << 20));
+    if (s.T <= 2) return true;
+    if (s.T <= 4) return lanes >= ((int64_t)1 << 17);
+    const bool whole = s.D % 8 == 0;
+    if (s.T <= 8) return whole && lanes >= ((int64_t)1 << 18);
+    return whole && s.T <= 16 && lanes >= ((int64_t)1 << 19);
 }
 
 // AUTO, FUSED (the library's tile shapes) or SEQ; AUTO walks short sequences
@@ -493,7 +502,9 @@ int gated_algo(const GatedShape& s, int dir, const size_t* rows, int n, const lr
 // Rows of partial sums of the decay gradient, and the bytes of them and of
 // their reduction's scratch.
 int64_t gated_part_rows(const GatedShape& s, int algo) {
-    return algo == LRSCAN_ALGO_SEQ ? s.B : gated_fused_part_rows(s);
+    if (algo == LRSCAN_ALGO_FUSED) return gated_fused_part_rows(s);
+    const int64_t rows = gated_walk_rows(s);
+    return (s.B + rows - 1) / rows;
 }
 size_t gated_sum_bytes(const GatedShape& s, int algo) {
     const int64_t rows = gated_part_rows(s, algo);

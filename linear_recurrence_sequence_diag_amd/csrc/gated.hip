@@ -25,16 +25,22 @@ namespace lrscan {
 namespace {
 
 constexpr int kBlock = 256;
-constexpr int kRowsAhead = 4;  // rows of every operand loaded together
+// Rows of every operand loaded together, 2 for sequences of two.  Measured (us
+// forward / reverse, bf16, 2 / 4 / 8 rows): [4096,2,1024] 28.8 / 43.2,
+// 29.7 / 50.5, 35.5 / 79.5; [2048,8,2560] 77 / 154, 81 / 149, 79 / 212;
+// [1024,16,2560] 74 / 155, 79 / 149, 71 / 209: 8 spill in the reverse walk.
+constexpr int kRowsAhead = 4;
 
+// Non-temporal, as every row is read once.
 template <int DT, bool ALIGNED>
-__device__ __forceinline__ RowVec<DT> load_at(const char* row, int64_t d0, int nvalid, float fill) {
-    return load_row<DT, ALIGNED>(row, (size_t)d0, nvalid, fill);
+__device__ __forceinline__ RowVec<DT> load_at(const char* row, int64_t d0, int nvalid) {
+    return load_vec<DT, ALIGNED, true>(row + (size_t)d0 * Elem<DT>::bytes, 0, nvalid, 0.0f);
 }
 
 struct WalkArgs {
     GatedShape s;
-    int64_t vpr;  // vectors of V lanes in a row
+    int64_t vpr;   // vectors of V lanes in a row
+    int64_t rows;  // batch rows a thread walks, one after the other
 };
 
 // U rows are loaded ahead of the arithmetic.
@@ -43,47 +49,49 @@ __global__ __launch_bounds__(kBlock) void gated_walk_fwd_kernel(GatedFwd p, Walk
     constexpr int V = Elem<DT>::V;
     const int64_t B = w.s.B, T = w.s.T, D = w.s.D;
     const int64_t gid = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    const int64_t bi = gid / w.vpr;
-    if (bi >= B) return;
-    const int64_t d0 = (gid - bi * w.vpr) * V;
+    const int64_t group = gid / w.vpr;
+    if (group * w.rows >= B) return;
+    const int64_t d0 = (gid - group * w.vpr) * V;
     const int nvalid = (int)((D - d0) < V ? (D - d0) : V);
 
     float rate[V], h[V];
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        rate[j] = j < nvalid ? gate_rate(p.decay[d0 + j], p.scale) : 0.0f;
-        h[j] = (p.h0 && j < nvalid) ? p.h0[bi * D + d0 + j] : 0.0f;
-    }
-    for (int64_t t0 = 0; t0 < T; t0 += U) {
-        RowVec<DT> x[U], gr[U], gi[U];
-        bool start[U];
+    for (int j = 0; j < V; ++j) rate[j] = j < nvalid ? gate_rate(p.decay[d0 + j], p.scale) : 0.0f;
+    const int64_t end = (group + 1) * w.rows < B ? (group + 1) * w.rows : B;
+    for (int64_t bi = group * w.rows; bi < end; ++bi) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t t = t0 + u < T ? t0 + u : T - 1;
-            x[u] = load_at<DT, ALIGNED>(p.x.row(bi, t), d0, nvalid, 0.0f);
-            gr[u] = load_at<DT, ALIGNED>(p.gr.row(bi, t), d0, nvalid, 0.0f);
-            gi[u] = load_at<DT, ALIGNED>(p.gi.row(bi, t), d0, nvalid, 0.0f);
-            start[u] = p.reset && p.reset[bi * T + t];
-        }
+        for (int j = 0; j < V; ++j) h[j] = (p.h0 && j < nvalid) ? p.h0[bi * D + d0 + j] : 0.0f;
+        for (int64_t t0 = 0; t0 < T; t0 += U) {
+            RowVec<DT> x[U], gr[U], gi[U];
+            bool start[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (t0 + u < T) {
-                RowOut<DT> o;
+            for (int u = 0; u < U; ++u) {
+                const int64_t t = t0 + u < T ? t0 + u : T - 1;
+                x[u] = load_at<DT, ALIGNED>(p.x.row(bi, t), d0, nvalid);
+                gr[u] = load_at<DT, ALIGNED>(p.gr.row(bi, t), d0, nvalid);
+                gi[u] = load_at<DT, ALIGNED>(p.gi.row(bi, t), d0, nvalid);
+                start[u] = p.reset && p.reset[bi * T + t];
+            }
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const GatedStep g = gated_step_of(x[u].get(j), gr[u].get(j), gi[u].get(j), rate[j]);
-                    const GatedStep f = gated_start_of(x[u].get(j), gi[u].get(j));
-                    h[j] = start[u] ? f.b : fmaf(g.a, h[j], g.b);
-                    o.v[j] = h[j];
+            for (int u = 0; u < U; ++u) {
+                if (t0 + u < T) {
+                    RowOut<DT> o;
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        const GatedStep g = gated_step_of(x[u].get(j), gr[u].get(j), gi[u].get(j), rate[j]);
+                        const GatedStep f = gated_start_of(x[u].get(j), gi[u].get(j));
+                        h[j] = start[u] ? f.b : fmaf(g.a, h[j], g.b);
+                        o.v[j] = h[j];
+                    }
+                    if (p.out) store_row<DT, ALIGNED>(p.out, (size_t)((bi * T + t0 + u) * D + d0), nvalid, o);
                 }
-                if (p.out) store_row<DT, ALIGNED>(p.out, (size_t)((bi * T + t0 + u) * D + d0), nvalid, o);
             }
         }
-    }
-    if (p.last) {
+        if (p.last) {
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-            if (j < nvalid) p.last[bi * D + d0 + j] = h[j];
+            for (int j = 0; j < V; ++j)
+                if (j < nvalid) p.last[bi * D + d0 + j] = h[j];
+        }
     }
 }
 
@@ -154,68 +162,75 @@ __global__ __launch_bounds__(kBlock) void gated_walk_bwd_kernel(GatedBwd p, Walk
     constexpr int V = Elem<DT>::V;
     const int64_t B = w.s.B, T = w.s.T, D = w.s.D;
     const int64_t gid = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    const int64_t bi = gid / w.vpr;
-    if (bi >= B) return;
-    const int64_t d0 = (gid - bi * w.vpr) * V;
+    const int64_t group = gid / w.vpr;
+    if (group * w.rows >= B) return;
+    const int64_t d0 = (gid - group * w.vpr) * V;
     const int nvalid = (int)((D - d0) < V ? (D - d0) : V);
 
     float rate[V], carry[V];
     Compensated sum[V];
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        rate[j] = j < nvalid ? gate_rate(p.decay[d0 + j], p.scale) : 0.0f;
-        carry[j] = (p.grad_last && j < nvalid) ? p.grad_last[bi * D + d0 + j] : 0.0f;
-    }
-    for (int64_t t1 = T; t1 > 0; t1 -= U) {  // rows t1 - 1, ..., t1 - U
-        RowVec<DT> x[U], gr[U], gi[U], g[U], hp[U];
-        bool start[U];
+    for (int j = 0; j < V; ++j) rate[j] = j < nvalid ? gate_rate(p.decay[d0 + j], p.scale) : 0.0f;
+    const int64_t end = (group + 1) * w.rows < B ? (group + 1) * w.rows : B;
+    for (int64_t bi = group * w.rows; bi < end; ++bi) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t t = t1 - 1 - u >= 0 ? t1 - 1 - u : 0;
-            const int64_t tp = t > 0 ? t - 1 : 0;
-            x[u] = load_at<DT, ALIGNED>(p.x.row(bi, t), d0, nvalid, 0.0f);
-            gr[u] = load_at<DT, ALIGNED>(p.gr.row(bi, t), d0, nvalid, 0.0f);
-            gi[u] = load_at<DT, ALIGNED>(p.gi.row(bi, t), d0, nvalid, 0.0f);
-            g[u] = load_row<DT, ALIGNED>(p.g, (size_t)((bi * T + t) * D + d0), nvalid, 0.0f);
-            hp[u] = load_row<DT, ALIGNED>(p.out, (size_t)((bi * T + tp) * D + d0), nvalid, 0.0f);
-            start[u] = p.reset && p.reset[bi * T + t];
-        }
-        float block_sum[V];
+        for (int j = 0; j < V; ++j) carry[j] = (p.grad_last && j < nvalid) ? p.grad_last[bi * D + d0 + j] : 0.0f;
+        for (int64_t t1 = T; t1 > 0; t1 -= U) {  // rows t1 - 1, ..., t1 - U
+            RowVec<DT> x[U], gr[U], gi[U], g[U], hp[U];
+            bool start[U];
 #pragma unroll
-        for (int j = 0; j < V; ++j) block_sum[j] = 0.0f;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t t = t1 - 1 - u;
-            if (t >= 0) {
-                RowOut<DT> ox, orr, oi;
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    float prev = hp[u].get(j);
-                    if (t == 0) prev = (p.h0 && j < nvalid) ? p.h0[bi * D + d0 + j] : 0.0f;
-                    const float lam = carry[j] + g[u].get(j);
-                    const float xv = x[u].get(j), rv = gr[u].get(j), iv = gi[u].get(j);
-                    const GatedGrad q = start[u] ? gated_start_grad_of(xv, iv, lam)
-                                                 : gated_grad_of(xv, rv, iv, rate[j], prev, lam);
-                    carry[j] = start[u] ? 0.0f : q.a * lam;
-                    ox.v[j] = q.dx;
-                    orr.v[j] = q.dgr;
-                    oi.v[j] = q.dgi;
-                    block_sum[j] += q.p;
-                }
-                store_row<DT, ALIGNED>(p.gx.row(bi, t), (size_t)d0, nvalid, ox);
-                store_row<DT, ALIGNED>(p.ggr.row(bi, t), (size_t)d0, nvalid, orr);
-                store_row<DT, ALIGNED>(p.ggi.row(bi, t), (size_t)d0, nvalid, oi);
+            for (int u = 0; u < U; ++u) {
+                const int64_t t = t1 - 1 - u >= 0 ? t1 - 1 - u : 0;
+                const int64_t tp = t > 0 ? t - 1 : 0;
+                x[u] = load_at<DT, ALIGNED>(p.x.row(bi, t), d0, nvalid);
+                gr[u] = load_at<DT, ALIGNED>(p.gr.row(bi, t), d0, nvalid);
+                gi[u] = load_at<DT, ALIGNED>(p.gi.row(bi, t), d0, nvalid);
+                g[u] = load_at<DT, ALIGNED>(static_cast<const char*>(p.g) + (size_t)((bi * T + t) * D) * Elem<DT>::bytes, d0,
+                                            nvalid);
+                hp[u] = load_at<DT, ALIGNED>(static_cast<const char*>(p.out) + (size_t)((bi * T + tp) * D) * Elem<DT>::bytes, d0,
+                                             nvalid);
+                start[u] = p.reset && p.reset[bi * T + t];
             }
-        }
+            float block_sum[V];
 #pragma unroll
-        for (int j = 0; j < V; ++j) sum[j].add(block_sum[j]);
+            for (int j = 0; j < V; ++j) block_sum[j] = 0.0f;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t t = t1 - 1 - u;
+                if (t >= 0) {
+                    RowOut<DT> ox, orr, oi;
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        float prev = hp[u].get(j);
+                        if (t == 0) prev = (p.h0 && j < nvalid) ? p.h0[bi * D + d0 + j] : 0.0f;
+                        const float lam = carry[j] + g[u].get(j);
+                        const float xv = x[u].get(j), rv = gr[u].get(j), iv = gi[u].get(j);
+                        const GatedGrad q = start[u] ? gated_start_grad_of(xv, iv, lam)
+                                                     : gated_grad_of(xv, rv, iv, rate[j], prev, lam);
+                        carry[j] = start[u] ? 0.0f : q.a * lam;
+                        ox.v[j] = q.dx;
+                        orr.v[j] = q.dgr;
+                        oi.v[j] = q.dgi;
+                        block_sum[j] += q.p;
+                    }
+                    store_row<DT, ALIGNED>(p.gx.row(bi, t), (size_t)d0, nvalid, ox);
+                    store_row<DT, ALIGNED>(p.ggr.row(bi, t), (size_t)d0, nvalid, orr);
+                    store_row<DT, ALIGNED>(p.ggi.row(bi, t), (size_t)d0, nvalid, oi);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < V; ++j) sum[j].add(block_sum[j]);
+        }
+        if (p.grad_h0) {
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (j < nvalid) p.grad_h0[bi * D + d0 + j] = carry[j];
+        }
     }
+    if (part) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        if (j < nvalid) {
-            if (p.grad_h0) p.grad_h0[bi * D + d0 + j] = carry[j];
-            if (part) part[bi * D + d0 + j] = sum[j].s + sum[j].c;
-        }
+        for (int j = 0; j < V; ++j)
+            if (j < nvalid) part[group * D + d0 + j] = sum[j].s + sum[j].c;
     }
 }
 
@@ -223,17 +238,23 @@ template <int DT>
 dim3 walk_grid(const GatedShape& s, int block, WalkArgs* w) {
     w->s = s;
     w->vpr = (s.D + Elem<DT>::V - 1) / Elem<DT>::V;
-    return dim3((unsigned)((s.B * w->vpr + block - 1) / block));
+    w->rows = gated_walk_rows(s);
+    const int64_t groups = (s.B + w->rows - 1) / w->rows;
+    return dim3((unsigned)((groups * w->vpr + block - 1) / block));
 }
 
 template <int DT>
 hipError_t walk_fwd_t(const GatedShape& s, const GatedFwd& p, hipStream_t st) {
     WalkArgs w;
     const dim3 grid = walk_grid<DT>(s, kBlock, &w);
-    if (gated_fwd_aligned(s, p))
-        hipLaunchKernelGGL((gated_walk_fwd_kernel<DT, true, kRowsAhead>), grid, dim3(kBlock), 0, st, p, w);
-    else
-        hipLaunchKernelGGL((gated_walk_fwd_kernel<DT, false, kRowsAhead>), grid, dim3(kBlock), 0, st, p, w);
+    const bool al = gated_fwd_aligned(s, p);
+    if (s.T <= 2) {
+        if (al) hipLaunchKernelGGL((gated_walk_fwd_kernel<DT, true, 2>), grid, dim3(kBlock), 0, st, p, w);
+        else hipLaunchKernelGGL((gated_walk_fwd_kernel<DT, false, 2>), grid, dim3(kBlock), 0, st, p, w);
+    } else {
+        if (al) hipLaunchKernelGGL((gated_walk_fwd_kernel<DT, true, kRowsAhead>), grid, dim3(kBlock), 0, st, p, w);
+        else hipLaunchKernelGGL((gated_walk_fwd_kernel<DT, false, kRowsAhead>), grid, dim3(kBlock), 0, st, p, w);
+    }
     return hipGetLastError();
 }
 
@@ -256,10 +277,14 @@ template <int DT>
 hipError_t walk_bwd_t(const GatedShape& s, const GatedBwd& p, float* part, hipStream_t st) {
     WalkArgs w;
     const dim3 grid = walk_grid<DT>(s, kBlock, &w);
-    if (gated_bwd_aligned(s, p))
-        hipLaunchKernelGGL((gated_walk_bwd_kernel<DT, true, kRowsAhead>), grid, dim3(kBlock), 0, st, p, w, part);
-    else
-        hipLaunchKernelGGL((gated_walk_bwd_kernel<DT, false, kRowsAhead>), grid, dim3(kBlock), 0, st, p, w, part);
+    const bool al = gated_bwd_aligned(s, p);
+    if (s.T <= 2) {
+        if (al) hipLaunchKernelGGL((gated_walk_bwd_kernel<DT, true, 2>), grid, dim3(kBlock), 0, st, p, w, part);
+        else hipLaunchKernelGGL((gated_walk_bwd_kernel<DT, false, 2>), grid, dim3(kBlock), 0, st, p, w, part);
+    } else {
+        if (al) hipLaunchKernelGGL((gated_walk_bwd_kernel<DT, true, kRowsAhead>), grid, dim3(kBlock), 0, st, p, w, part);
+        else hipLaunchKernelGGL((gated_walk_bwd_kernel<DT, false, kRowsAhead>), grid, dim3(kBlock), 0, st, p, w, part);
+    }
     return hipGetLastError();
 }
 
@@ -292,6 +317,18 @@ bool gated_bwd_aligned(const GatedShape& s, const GatedBwd& p) {
     return rows_aligned(c, ptrs, 2) && operand_aligned(s.B, s.T, p.x) && operand_aligned(s.B, s.T, p.gr) &&
            operand_aligned(s.B, s.T, p.gi) && operand_aligned(s.B, s.T, p.gx) && operand_aligned(s.B, s.T, p.ggr) &&
            operand_aligned(s.B, s.T, p.ggi);
+}
+
+// A channel's rate costs a thread about as much as two steps, so short
+// sequences share it (and one partial row of the decay gradient) among up to
+// 16 steps' worth of batch rows, as long as that leaves eight wavefronts to
+// a CU.  WALKNOTE
+int64_t gated_walk_rows(const GatedShape& s) {
+    const int64_t v = s.dtype == DT_F32 ? Elem<DT_F32>::V : Elem<DT_BF16>::V;
+    const int64_t threads = s.B * ((s.D + v - 1) / v);
+    int64_t rows = 1;
+    while (rows * 2 * s.T <= 16 && threads / (rows * 2) >= ((int64_t)1 << 17)) rows *= 2;
+    return rows;
 }
 
 bool gated_walk_fits(const GatedShape& s) {

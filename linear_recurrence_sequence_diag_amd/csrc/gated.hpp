@@ -49,8 +49,9 @@ bool operand_aligned(int64_t B, int64_t T, const Rows& r);
 bool gated_fwd_aligned(const GatedShape& s, const GatedFwd& p);
 bool gated_bwd_aligned(const GatedShape& s, const GatedBwd& p);
 
-// The per-lane walk.  The backward's `part` (or NULL) receives B rows of D
-// partial sums of P.
+// The per-lane walk.  A thread walks gated_walk_rows batch rows; the backward's
+// `part` (or NULL) receives a row of D partial sums of P from each such group.
+int64_t gated_walk_rows(const GatedShape& s);
 bool gated_walk_fits(const GatedShape& s);
 hipError_t launch_gated_walk_fwd(const GatedShape& s, const GatedFwd& p, hipStream_t st);
 hipError_t launch_gated_walk_bwd(const GatedShape& s, const GatedBwd& p, float* part, hipStream_t st);
