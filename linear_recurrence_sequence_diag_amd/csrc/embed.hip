@@ -23,6 +23,14 @@
 //    every row that lies inside the chunk.  A row that crosses a chunk's end
 //    leaves partial sums, which one more launch adds in the chunks' order, so
 //    a token that half the batch consists of costs no more than others.
+//
+// Bound (MI355X, caches flushed): bytes.  Lookup, 16384 tokens of bf16 rows of
+// 2560: 20 us, 84 MB written at 4.2 TB/s and a table's rows read as the caches
+// hold them.  Gradient of as many tokens into bf16 [262144, 2560]: 264 us, of
+// which 208 to 215 are the four sort launches that write 1.34 GB of zeros on
+// the side (6.3 TB/s; a fill reaches 6.9) and 51 the sums.  A small table's
+// gradient is its launches: 6007 tokens into fp32 [4001, 1023] 14 us of sort,
+// 10 of sums, 4 of crossing rows.
 #include "embed.hpp"
 
 #include <algorithm>

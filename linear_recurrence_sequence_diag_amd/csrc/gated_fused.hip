@@ -10,6 +10,13 @@
 // would not fit beside them) and writes the three gradients; the tile's sum
 // of P for the decay gradient goes to one partial row for each tile.
 //
+// Bound (MI355X, bf16 [8, 2048, 2560] with resets, caches flushed): forward
+// 74 us for 336 MB (4.5 TB/s; a copy reaches 4.95), with the vector units busy
+// for 46 of them, 37 instructions an element of which 6 are transcendental;
+// reverse 152 us for 671 MB (4.4 TB/s), 78 of them busy, 64 instructions an
+// element.  fp32, with half the elements to a byte, runs at the memory's rate:
+// reverse [4, 2048, 4096] 195 us for 1.07 GB (5.5 TB/s).
+//
 // A reset step is a map that drops its argument.  It is carried as the map
 // (p, q) with p = -0: a product of transitions is never -0, because each
 // is >= +0 and a reset enters compositions by selects, so the sign tells a
