@@ -51,19 +51,17 @@ constexpr int V = kQuad;  // channels of a thread
 // Tokens of a chunk.  The backward's walk goes K - 1 tokens past its chunk, so
 // that walk is what is a whole number of groups.
 //
-// Long chunks re-read less, short ones make more wavefronts: the longest of
-// some lengths that leaves six wavefronts for each of the 256 CUs (reverse,
-// bf16, K = 4: [8, 2048, 2560] 69 us in chunks of 57 tokens, 96 in 15; [8, 2048,
-// 1024] 39 in 27, 50 in 57; [1, 2048, 1024] 16 in 9, 40 in 57).  The forward,
-// with no sums to carry, takes at most 18 tokens, its four wavefronts side by
-// side along the rows, so that the rows in flight lie together ([16, 4096,
-// 2560] bf16 135 us, 146 in chunks of 60 one after the other).
+// Long chunks re-read less, short ones make more wavefronts.  The forward takes
+// the longest of some lengths that leaves six wavefronts for each of the 256
+// CUs, and at most 18 tokens, its four wavefronts side by side along the rows,
+// so that the rows in flight lie together ([16, 4096, 2560] bf16 135 us, 146 in
+// chunks of 60 one after the other).  For the reverse see bwd_rows.
 //
 // A thread of four channels beats one of eight (reverse 72 against 85, forward
 // 43 against 48, [8, 2048, 2560] bf16): its state leaves four wavefronts a SIMD in
 // the reverse walk and eight in the forward one.
 constexpr uint32_t kFwdWidth = 256, kBwdWidth = 64;  // threads along a row, at most
-constexpr int kFwdTokens = 18, kBwdTokens = 60;      // of a walk, at most
+constexpr int kFwdGroups = 3, kBwdGroups = 14;       // of tokens in a walk, at most
 int fwd_rows(const ConvShape& s);
 int bwd_rows(const ConvShape& s);
 
@@ -96,17 +94,37 @@ ConvGrid conv_grid(const ConvShape& s, int rows, uint32_t widest) {
     return g;
 }
 
-int chunk_groups(const ConvShape& s, int most) {
+int fwd_rows(const ConvShape& s) {
     const int u = group_of(s.K);
     const int64_t per = (s.D + V * 64 - 1) / (V * 64);  // wavefronts to a row
-    for (const int n : {60 / u, 30 / u, 3, 2})
-        if (n * u <= most && s.B * ((s.T + n * u - 1) / (n * u)) * per >= 1536) return n;
-    return 1;
+    for (int n = kFwdGroups; n > 1; --n)
+        if (s.B * ((s.T + n * u - 1) / (n * u)) * per >= 1536) return n * u;
+    return u;
 }
-int fwd_rows(const ConvShape& s) { return chunk_groups(s, kFwdTokens) * group_of(s.K); }
+
+// The reverse's chunks are few and long, so what counts is how they fill the
+// GPU.  A CU holds four workgroups; c of them side by side take a time of about
+// (c + 2) (walk + 3 tokens), and the launch that of its fullest CU.  The walk
+// with the least is taken.  Measured on MI355X (us, K = 4, in walks of 24, 36,
+// 48, 60 and 72 tokens; the one taken in brackets):
+//   bf16 [8,2048,2560]    74    75   [69]   70    76
+//        [16,4096,2560]  242   230   227   225   226  [221 in 84]
+//        [8,2048,1024]    38   [38]   43    50    49
+//        [16,2048,1024]   62   [58]   57    64    62
+//   fp32 [4,2048,4096]    91   [86]   86    91    81
+// (By the longest walk that left six wavefronts a CU: [64,2048,128] 50, now 37;
+// [1,32768,1024] 64, now 56.)
 int bwd_rows(const ConvShape& s) {
-    const int n = chunk_groups(s, kBwdTokens);
-    return (n > 1 ? n : 2) * group_of(s.K) - (s.K - 1);
+    const int u = group_of(s.K);
+    int best = 2;
+    int64_t least = 0;
+    for (int n = 2; n <= kBwdGroups; ++n) {
+        const ConvGrid g = conv_grid(s, n * u - (s.K - 1), kBwdWidth);
+        const int64_t all = (int64_t)g.ncb * g.blocks, left = (all % 1024 + 255) / 256;
+        const int64_t cost = (n * u + 3) * (all / 1024 * 6 + (left ? left + 2 : 0));
+        if (n == 2 || cost < least) best = n, least = cost;
+    }
+    return best * u - (s.K - 1);
 }
 
 struct ConvPos {
