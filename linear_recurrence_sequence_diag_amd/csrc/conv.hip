@@ -52,16 +52,21 @@ constexpr int V = kQuad;  // channels of a thread
 // that walk is what is a whole number of groups.
 //
 // Long chunks re-read less, short ones make more wavefronts.  The forward takes
-// the longest of some lengths that leaves six wavefronts for each of the 256
-// CUs, and at most 18 tokens, its four wavefronts side by side along the rows,
-// so that the rows in flight lie together ([16, 4096, 2560] bf16 135 us, 146 in
-// chunks of 60 one after the other).  For the reverse see bwd_rows.
+// two groups of tokens, three of rows that a wavefront holds several of, as
+// long as that leaves six wavefronts for each of the 256 CUs, and else one: its
+// wavefronts lie side by side along the rows in pairs, so that the rows in
+// flight lie together.  Measured on MI355X (bf16, us, K = 4, in chunks of 6, 12,
+// 18 and 48 tokens, four wavefronts side by side): [16, 4096, 2560] 148, 135, 135,
+// 143; [16, 2048, 1024] 34, 32, 33, 32; [64, 2048, 128] 21, 21, 18, 25; [1, 2048,
+// 1024] 7, 8, 10, 17.  Pairs take up to 10% less ([32, 1024, 1536] 45 against 50),
+// single ones 6% more on long rows (142 against 134).  For the reverse see
+// bwd_rows.
 //
 // A thread of four channels beats one of eight (reverse 72 against 85, forward
 // 43 against 48, [8, 2048, 2560] bf16): its state leaves four wavefronts a SIMD in
 // the reverse walk and eight in the forward one.
-constexpr uint32_t kFwdWidth = 256, kBwdWidth = 64;  // threads along a row, at most
-constexpr int kFwdGroups = 3, kBwdGroups = 14;       // of tokens in a walk, at most
+constexpr uint32_t kFwdWidth = 128, kBwdWidth = 64;  // threads along a row, at most
+constexpr int kBwdGroups = 14;                       // of tokens in a reverse walk, at most
 int fwd_rows(const ConvShape& s);
 int bwd_rows(const ConvShape& s);
 
@@ -97,7 +102,7 @@ ConvGrid conv_grid(const ConvShape& s, int rows, uint32_t widest) {
 int fwd_rows(const ConvShape& s) {
     const int u = group_of(s.K);
     const int64_t per = (s.D + V * 64 - 1) / (V * 64);  // wavefronts to a row
-    for (int n = kFwdGroups; n > 1; --n)
+    for (int n = s.D > 32 * V ? 2 : 3; n > 1; --n)
         if (s.B * ((s.T + n * u - 1) / (n * u)) * per >= 1536) return n * u;
     return u;
 }
