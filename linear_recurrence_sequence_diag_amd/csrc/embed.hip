@@ -26,9 +26,9 @@
 //
 // Bound (MI355X, caches flushed): bytes.  Lookup, 16384 tokens of bf16 rows of
 // 2560: 20 us, 84 MB written at 4.2 TB/s and a table's rows read as the caches
-// hold them.  Gradient of as many tokens into bf16 [262144, 2560]: 264 us, of
-// which 208 to 215 are the four sort launches that write 1.34 GB of zeros on
-// the side (6.3 TB/s; a fill reaches 6.9) and 51 the sums.  A small table's
+// hold them.  Gradient of as many tokens into bf16 [262144, 2560]: 254 us, of
+// which some 203 are the four sort launches that write 1.34 GB of zeros on the
+// side (6.6 TB/s; a fill reaches 6.9) and 51 the sums.  A small table's
 // gradient is its launches: 6007 tokens into fp32 [4001, 1023] 14 us of sort,
 // 10 of sums, 4 of crossing rows.
 #include "embed.hpp"
@@ -166,13 +166,17 @@ struct Clear {
     uint32_t nhead, ntail;
 };
 
-// The workgroups of a launch past the first `first` clear, side by side: 64K
-// threads writing one stretch of memory at a time (6.6 TB/s over 1.3 GB; 256K
-// or 512K threads 4.6, non-temporal 6.3).
-constexpr unsigned kClearThreads = 65536;
+// The workgroups of a launch past the first `first` clear, side by side, with
+// their first kBlock threads each: half a workgroup's worth for every CU,
+// writing one stretch of memory at a time.  Measured on MI355X, the gradient of
+// 16384 tokens into bf16 [262144, 2560] with 16K, 32K, 48K, 64K and 128K threads:
+// 255, 255, 267, 267 and 283 us; of 4000 into [262144, 1024]: 96, 94, 101, 97 and
+// 109 (1.3 GB by 256K or 512K threads: 4.6 TB/s; non-temporal 6.3).
+constexpr unsigned kClearThreads = 32768;
 __device__ __forceinline__ void clear_share(const Clear& c, uint32_t first) {
-    const uint64_t threads = (uint64_t)(gridDim.x - first) * blockDim.x;
-    const uint64_t me = (uint64_t)(blockIdx.x - first) * blockDim.x + threadIdx.x;
+    if (threadIdx.x >= kBlock) return;
+    const uint64_t threads = (uint64_t)(gridDim.x - first) * kBlock;
+    const uint64_t me = (uint64_t)(blockIdx.x - first) * kBlock + threadIdx.x;
     for (uint64_t i = c.from + me; i < c.to; i += threads)
         reinterpret_cast<uint4*>(c.p)[i] = make_uint4(0u, 0u, 0u, 0u);
     if (me < c.nhead) c.head[me] = 0;
@@ -334,18 +338,19 @@ struct SmallSort {
     uint32_t N;
     int pos_bits, passes, bits;
 };
-template <class Src>
+template <class Src, int BITS>
 __global__ __launch_bounds__(kSmallWaves* kWave) void sort_small_kernel(Src src, SmallSort p, uint32_t* keys,
                                                                         uint32_t* poss, Clear clear) {
+    static_assert((1 << BITS) % kWave == 0, "the digits' places are whole wavefronts' work");
     constexpr int E = kSmallTokens / (kSmallWaves * kWave);
     __shared__ uint32_t s_word[kSmallTokens];
-    __shared__ uint32_t s_at[kSmallWaves][1 << kSmallBits];
+    __shared__ uint32_t s_at[kSmallWaves][1 << BITS];
     __shared__ uint32_t s_wave[4];
     if (blockIdx.x >= 1) {
         clear_share(clear, 1);
         return;
     }
-    const uint32_t digits = 1u << p.bits;
+    constexpr uint32_t digits = 1u << BITS;
     const uint32_t tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave;
     // this thread's words: w0 + 64 e, e < rounds (whole rounds, shared evenly)
     const uint32_t rounds = (p.N + kSmallWaves * kWave - 1) / (kSmallWaves * kWave);
@@ -357,37 +362,41 @@ __global__ __launch_bounds__(kSmallWaves* kWave) void sort_small_kernel(Src src,
         v[e] = (uint32_t)e < rounds && n < p.N ? (src.key(n) << p.pos_bits) | n : 0u;
     }
     for (int pass = 0; pass < p.passes; ++pass) {
-        const int shift = p.pos_bits + pass * p.bits;
+        const int shift = p.pos_bits + pass * BITS;
         for (uint32_t d = lane; d < digits; d += kWave) s_at[wave][d] = 0;
         // how many of the wavefront's words before this one have its digit
         uint32_t rank[E];
+        unsigned long long same[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             if ((uint32_t)e >= rounds) break;
-            const bool have = w0 + e * kWave < p.N;
-            const uint32_t d = (v[e] >> shift) & (digits - 1);
-            unsigned long long same = __ballot(have);
-            for (int b = 0; b < p.bits; ++b) {
+            const uint32_t d = v[e] >> shift;
+            same[e] = __ballot(w0 + e * kWave < p.N);
+#pragma unroll
+            for (int b = 0; b < BITS; ++b) {
                 const unsigned long long one = __ballot((d >> b) & 1u);
-                same &= (d >> b) & 1u ? one : ~one;
+                same[e] &= (d >> b) & 1u ? one : ~one;
             }
-            const unsigned long long below = same & ((1ull << lane) - 1);
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            if ((uint32_t)e >= rounds) break;
+            const uint32_t d = (v[e] >> shift) & (digits - 1);
+            const unsigned long long below = same[e] & ((1ull << lane) - 1);
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             __builtin_amdgcn_wave_barrier();
             const uint32_t so_far = s_at[wave][d];
             rank[e] = so_far + (uint32_t)__popcll(below);
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             __builtin_amdgcn_wave_barrier();
-            if (have && below == 0) s_at[wave][d] = so_far + (uint32_t)__popcll(same);
+            if (w0 + e * kWave < p.N && below == 0) s_at[wave][d] = so_far + (uint32_t)__popcll(same[e]);
         }
         __syncthreads();
-        // places of the digits, one to each of the first 256 threads
+        // places of the digits, one to a thread
         uint32_t sum = 0, upto = 0;
-        if (tid < (1u << kSmallBits)) {
-            if (tid < digits) {
+        if (tid < digits) {
 #pragma unroll
-                for (int w = 0; w < kSmallWaves; ++w) sum += s_at[w][tid];
-            }
+            for (int w = 0; w < kSmallWaves; ++w) sum += s_at[w][tid];
             upto = sum;
 #pragma unroll
             for (int o = 1; o < kWave; o <<= 1) {
@@ -720,7 +729,7 @@ struct Clearing {
     char* table;
     uint64_t bytes;
     int n, done = 0;
-    Clear next(unsigned* groups, unsigned threads = kBlock) {
+    Clear next(unsigned* groups) {
         const uintptr_t at = reinterpret_cast<uintptr_t>(table);
         const uint64_t nhead = std::min<uint64_t>((16 - at % 16) % 16, bytes);
         const uint64_t blocks = (bytes - nhead) / 16;
@@ -733,8 +742,8 @@ struct Clearing {
         c.tail = c.p + blocks * 16;
         c.ntail = done == 0 ? (uint32_t)(bytes - nhead - blocks * 16) : 0u;
         ++done;
-        const uint64_t want = (c.to - c.from + threads - 1) / threads + (done == 1 ? 1 : 0);
-        *groups = (unsigned)std::min<uint64_t>(want, kClearThreads / threads);
+        const uint64_t want = (c.to - c.from + kBlock - 1) / kBlock + (done == 1 ? 1 : 0);
+        *groups = (unsigned)std::min<uint64_t>(want, kClearThreads / kBlock);
         if (bytes == 0) *groups = 0;
         return c;
     }
@@ -760,8 +769,12 @@ hipError_t sort_small(Src src, const SmallSort& p, uint32_t* keys, uint32_t* pos
                       hipStream_t st) {
     constexpr unsigned threads = kSmallWaves * kWave;
     unsigned more = 0;
-    const Clear c = clearing->next(&more, threads);
-    hipLaunchKernelGGL((sort_small_kernel<Src>), dim3(1 + more), dim3(threads), 0, st, src, p, keys, poss, c);
+    const Clear c = clearing->next(&more);
+    if (p.bits <= 6)
+        hipLaunchKernelGGL((sort_small_kernel<Src, 6>), dim3(1 + more), dim3(threads), 0, st, src, p, keys, poss, c);
+    else
+        hipLaunchKernelGGL((sort_small_kernel<Src, kSmallBits>), dim3(1 + more), dim3(threads), 0, st, src, p, keys,
+                           poss, c);
     return hipGetLastError();
 }
 
