@@ -1108,6 +1108,7 @@ def _model_function(name):
     if name in _model_functions:
         return _model_functions[name]
     torch = _torch()
+    once_differentiable = torch.autograd.function.once_differentiable
 
     class GatedScanFunction(torch.autograd.Function):
         @staticmethod
@@ -1120,6 +1121,7 @@ def _model_function(name):
             return out
 
         @staticmethod
+        @once_differentiable
         def backward(ctx, grad):
             x, gate_r, gate_i, decay, out = ctx.saved_tensors
             gx, gr, gi, gd, _ = gated_scan_backward(x, gate_r, gate_i, decay, out,
@@ -1139,6 +1141,7 @@ def _model_function(name):
             return out
 
         @staticmethod
+        @once_differentiable
         def backward(ctx, grad):
             x, weight, bias = ctx.saved_tensors
             gx, gw, gb, _ = short_conv_backward(x, weight, bias, grad.contiguous(),
@@ -1154,6 +1157,7 @@ def _model_function(name):
             return embed(ids, weight.contiguous(), scale)
 
         @staticmethod
+        @once_differentiable
         def backward(ctx, grad):
             ids, = ctx.saved_tensors
             return None, embed_backward(ids, grad.contiguous(), ctx.rows, ctx.scale), None

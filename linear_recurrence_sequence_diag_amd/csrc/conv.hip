@@ -24,7 +24,7 @@
 // row the window was moved through copies, a quarter of all instructions.)
 //
 // Bound (MI355X, bf16 [8, 2048, 2560], K = 4, with resets and activation,
-// caches flushed): forward 39 us for 168 MB (4.3 TB/s), the vector units busy
+// caches flushed): forward 37 us for 168 MB (4.5 TB/s), the vector units busy
 // for 21; reverse 62 us and 5 for the parameters' sums, 252 MB (4.0 TB/s), the
 // vector units busy for 40: four wavefronts a SIMD, each with a group of rows in
 // flight, cover neither wholly.

@@ -273,6 +273,20 @@ def test_autograd_and_repeatability():
         assert torch.equal(a, b)
 
 
+def test_a_second_derivative_is_refused():
+    """Of each differentiable operator: an error, and no gradient without its graph."""
+    x = torch.randn(2, 5, 8, device="cuda", requires_grad=True)
+    ones = torch.ones(8, device="cuda")
+    table = torch.randn(4, 8, device="cuda", requires_grad=True)
+    ids = torch.tensor([0, 3, 3], device="cuda")
+    for leaf, out in ((x, lr.gated_diagonal_scan(x, x, x, ones)),
+                      (x, lr.short_convolution(x, torch.ones(4, 8, device="cuda"), activation="silu")),
+                      (table, lr.embedding(ids, table))):
+        g, = torch.autograd.grad((out * out).sum(), leaf, create_graph=True)
+        with pytest.raises(RuntimeError):
+            g.sum().backward()
+
+
 def test_workspace_streams_and_capture():
     """A caller's workspace gives the library's results; so does a captured call,
     replayed between eager calls; and a call on another stream after its inputs."""
