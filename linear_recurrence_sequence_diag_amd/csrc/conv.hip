@@ -66,7 +66,7 @@ constexpr int V = kQuad;  // channels of a thread
 // 43 against 48, [8, 2048, 2560] bf16): its state leaves four wavefronts a SIMD in
 // the reverse walk and eight in the forward one.
 constexpr uint32_t kFwdWidth = 128, kBwdWidth = 64;  // threads along a row, at most
-constexpr int kBwdGroups = 14;                       // of tokens in a reverse walk, at most
+constexpr int kFwdGroups = 3, kBwdGroups = 14;       // of tokens in a walk, at most
 int fwd_rows(const ConvShape& s);
 int bwd_rows(const ConvShape& s);
 
@@ -102,7 +102,7 @@ ConvGrid conv_grid(const ConvShape& s, int rows, uint32_t widest) {
 int fwd_rows(const ConvShape& s) {
     const int u = group_of(s.K);
     const int64_t per = (s.D + V * 64 - 1) / (V * 64);  // wavefronts to a row
-    for (int n = s.D > 32 * V ? 2 : 3; n > 1; --n)
+    for (int n = s.D > 32 * V ? 2 : kFwdGroups; n > 1; --n)
         if (s.B * ((s.T + n * u - 1) / (n * u)) * per >= 1536) return n * u;
     return u;
 }
@@ -188,35 +188,47 @@ struct Taps {
     }
 };
 
-// Segment starts of a chunk.  A wavefront in one chunk reads the mask of the
-// whole walk (the window before it too, at most 63 tokens) with one load, a
-// token to a lane, and keeps it as a scalar; otherwise each thread reads its
-// group's bytes.
-template <bool UNI, int K>
+// Segment starts of a chunk whose walk has up to WALK tokens.  A wavefront in
+// one chunk reads the mask of the whole walk (the window before it too) with
+// one load for every 64 tokens, a token to a lane, and keeps it as scalars;
+// otherwise each thread reads its group's bytes.  (With one word for walks of
+// 84 tokens the starts past token 60 were lost.)
+template <bool UNI, int K, int WALK>
 struct Starts {
+    static constexpr int kWords = (WALK + K - 1 + kWave - 1) / kWave;
+    static_assert(kWords <= 2, "a group is taken from at most two words");
     const uint8_t* row;  // mask of the batch row, or NULL
     int64_t t0, T;
-    unsigned long long bits;  // UNI: bit i for token t0 - (K - 1) + i
+    unsigned long long bits[kWords];  // UNI: bit i of word w for token t0 - (K - 1) + 64 w + i
     __device__ __forceinline__ void init(const uint8_t* reset, int64_t bi, int64_t from, int64_t len) {
         row = reset ? reset + bi * len : nullptr;
         t0 = from;
         T = len;
         if constexpr (UNI) {
-            bits = 0;
-            if (reset) {
-                const int64_t t = t0 - (K - 1) + (int64_t)(threadIdx.x % kWave);
-                bits = __ballot(t >= 0 && t < T && row[t < 0 ? 0 : (t < T ? t : T - 1)] != 0);
+#pragma unroll
+            for (int w = 0; w < kWords; ++w) {
+                bits[w] = 0;
+                if (reset) {
+                    const int64_t t = t0 - (K - 1) + w * kWave + (int64_t)(threadIdx.x % kWave);
+                    bits[w] = __ballot(t >= 0 && t < T && row[t < 0 ? 0 : (t < T ? t : T - 1)] != 0);
+                }
             }
         }
     }
     __device__ __forceinline__ bool at(int64_t t) const {  // for the window
-        if constexpr (UNI) return (bits >> (int)(t - t0 + K - 1)) & 1u;
+        if constexpr (UNI) return (bits[0] >> (int)(t - t0 + K - 1)) & 1u;
         else return row && t >= 0 && row[t];
     }
-    // tokens t .. t + U - 1, bit u for token t + u
+    // tokens t .. t + U - 1 of the walk, bit u for token t + u
     template <int U>
     __device__ __forceinline__ uint32_t group(int64_t t) const {
-        if constexpr (UNI) return (uint32_t)(bits >> (int)(t - t0 + K - 1)) & ((1u << U) - 1u);
+        if constexpr (UNI) {
+            const int at = (int)(t - t0) + K - 1;  // 1 or more
+            unsigned long long w = bits[0];
+            if constexpr (kWords == 1) w >>= at;
+            else w = at < kWave ? (w >> at) | (bits[1] << (kWave - at)) : bits[1] >> (at - kWave);
+            return (uint32_t)w & ((1u << U) - 1u);
+        }
         if (!row) return 0;
         uint32_t m = 0;
 #pragma unroll
@@ -228,9 +240,9 @@ struct Starts {
 
 // The K - 1 inputs before token t0, oldest first, those of an earlier segment
 // cleared.
-template <int DT, bool FULL, bool UNI, int K>
+template <int DT, bool FULL, bool UNI, int K, int WALK>
 __device__ __forceinline__ void conv_warm(Quad<DT> (&win)[K - 1], const Rows& x, const void* state,
-                                          const Starts<UNI, K>& starts, const ConvPos& p, int64_t D,
+                                          const Starts<UNI, K, WALK>& starts, const ConvPos& p, int64_t D,
                                           uint32_t lo) {
     constexpr int S = Elem<DT>::bytes;
 #pragma unroll
@@ -269,7 +281,7 @@ __global__ __launch_bounds__(kBlock) void conv_fwd_kernel(ConvFwd a, ConvGrid g,
     constexpr int S = Elem<DT>::bytes, U = group_of(K);
     const ConvPos p = conv_pos<UNI>(g, T, D);
     const uint32_t lo = (uint32_t)p.d0 * S;  // this thread's bytes into a row
-    Starts<UNI, K> st;
+    Starts<UNI, K, kFwdGroups * U> st;
     st.init(a.reset, p.bi, p.t0, T);  // with every lane, idle ones too
     if (p.nvalid == 0) return;
     Taps<K> tp;
@@ -326,7 +338,7 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(UNI ? 4 
     __shared__ float s_part[kBlock * V];
     const ConvPos p = conv_pos<UNI>(g, T, D);
     const uint32_t lo = (uint32_t)p.d0 * S;  // this thread's bytes into a row
-    Starts<UNI, K> st;
+    Starts<UNI, K, kBwdGroups * U> st;
     st.init(a.reset, p.bi, p.t0, T);  // with every lane, idle ones too
     float dw[K][V], db[V];
 #pragma unroll

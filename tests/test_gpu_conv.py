@@ -201,3 +201,47 @@ def test_offsets_past_32_bits():
     close("grad_x", gx[-1:, -n:], want["grad_x"], "bf16")
     close("grad_weight", gw, want["grad_weight"], "f32")
     assert not gx[:, :-n - 3].any()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("K", [2, 3, 4])
+@pytest.mark.parametrize("D", [132, 260, 1031])
+@pytest.mark.parametrize("reset", ["some", "all"])
+def test_resets_of_wide_rows(reset, D, K, dtype):
+    """Rows that a wavefront walks alone, several chunks long: starts on every place of a chunk."""
+    log(f"{D} {K} {dtype} {reset}")
+    Case(2, 203, D, K, dtype, reset=reset, state=True).check()
+
+
+# Whose reverse walks are the longest, in groups of six tokens: 14 of them, 12, 11 and 12; 14 of four with three taps.
+LONG_WALKS = [(8, 4096, 2560, 4, "bf16"), (8, 2048, 4096, 4, "f32"), (42, 2938, 277, 4, "bf16"),
+              (4, 32768, 289, 4, "f32"), (8, 4096, 2560, 3, "bf16")]
+
+
+@pytest.mark.parametrize("shape", LONG_WALKS)
+def test_resets_in_long_walks(shape):
+    """Starts at every distance from a chunk's first token, against the 64-bit form on some columns."""
+    B, T, D, K, dtype = shape
+    log(f"{shape}")
+    gen = torch.Generator(device="cuda").manual_seed(D + K)
+    x, g = (torch.randn(B, T, D, generator=gen, device="cuda").to(DT[dtype]) for _ in range(2))
+    w, b = torch.randn(K, D, generator=gen, device="cuda") * 0.6, torch.randn(D, generator=gen, device="cuda")
+    m = torch.rand(B, T, generator=gen, device="cuda") < 0.04
+    cols = np.r_[0:8, D // 2:D // 2 + 4, D - 8:D]
+    c = ref.Conv(host(x[..., cols]), host(w[:, cols]), host(b[cols]), True, host(m).astype(bool))
+    out, last = lr.short_conv(x, w, b, reset=m, activation="silu")
+    close("out", out[..., cols], (c.out, c.E), dtype)
+    assert np.array_equal(host(last[..., cols]), c.last)
+    want = c.grad(host(g[..., cols]))
+    gx, gw, gb, _ = lr.short_conv_backward(x, w, b, g, reset=m, activation="silu")
+    close("grad_x", gx[..., cols], want["grad_x"], dtype)
+    close("grad_weight", gw[:, cols], want["grad_weight"], "f32")
+    close("grad_bias", gb[cols], want["grad_bias"], "f32")
+    # an infinity and a NaN stay in their segment: of the other tokens every bit stays
+    t = torch.arange(T, device="cuda")
+    m[:, (t % 97 == 5) | (t % 97 == 70)] = True
+    gx = lr.short_conv_backward(x, w, b, g, reset=m, activation="silu")[0]
+    bad = (t % 97 >= 5) & (t % 97 < 70)
+    x[:, t % 97 == 68], x[:, t % 97 == 69], g[:, t % 97 == 5] = float("inf"), float("nan"), float("nan")
+    gx2 = lr.short_conv_backward(x, w, b, g, reset=m, activation="silu")[0]
+    assert torch.equal(gx[:, ~bad], gx2[:, ~bad])
