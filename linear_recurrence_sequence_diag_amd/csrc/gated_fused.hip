@@ -26,6 +26,7 @@
 
 #include "fused_common.hpp"
 #include "gated.hpp"
+#include "gated_geo.hpp"
 #include "gated_math.hpp"
 
 namespace lrscan {
@@ -94,39 +95,6 @@ struct GatedBwdArgs {
     Dims d;
     uint32_t polls;
 };
-
-// How rows lie.  kWhole: at least one vector long, but not made of aligned
-// vectors.  Its last, partial vector is moved back to start at D - V, so that
-// every access is one of 16 bytes; the columns it shares with its neighbour
-// are computed twice, to the same bits.  (With the partial vector tested for at
-// every access instead, fp32 [5, 777, 1023] took 28.8 us forward and 46.5
-// reverse, against 19.2 and 33.3 for rows of 1024.)  kNarrow: shorter than a
-// vector, element by element.
-enum RowKind { kAligned, kWhole, kNarrow };
-
-template <class C, int RK, bool REV>
-__device__ __forceinline__ Geo gated_geo(uint32_t ticket, const Dims& d, int wave, int rg, int cg) {
-    Geo g = tile_geo<C, REV>(ticket, d, wave, rg, cg);
-    if constexpr (RK == kWhole) {
-        // bases are taken 16 bytes before the tile, so that offsets stay positive
-        g.tbase -= 16;
-        g.coff += 16;
-        if (g.nvalid > 0 && g.nvalid < C::V) {
-            const int back = C::V - g.nvalid;
-            g.d0 -= back;
-            g.coff -= (uint32_t)(back * C::EB);
-            g.nvalid = C::V;
-        }
-    }
-    return g;
-}
-
-// The column of a tile's slot c (D or more: none).
-template <class C, int RK>
-__device__ __forceinline__ int slot_column(const Geo& g, int c, int D) {
-    const int d0 = g.dcol0 + c / C::V * C::V;
-    return (RK == kWhole && d0 < D && d0 + C::V > D ? D - C::V : d0) + c % C::V;
-}
 
 template <class C, int RK>
 __device__ __forceinline__ RowVec<C::DT> load_tile(const char* base, uint32_t off, int nvalid) {
