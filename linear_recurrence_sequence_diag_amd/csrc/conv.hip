@@ -332,8 +332,8 @@ __global__ __launch_bounds__(kBlock) void conv_fwd_kernel(ConvFwd a, ConvGrid g,
 }
 
 template <int DT, bool FULL, bool UNI, int K, bool SILU>
-__global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(UNI ? 4 : 2))) void conv_bwd_kernel(ConvBwd a, ConvGrid g, int64_t T, int64_t D,
-                                                          float* part) {
+__global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(UNI ? 4 : 2)))
+void conv_bwd_kernel(ConvBwd a, ConvGrid g, int64_t T, int64_t D, float* part) {
     constexpr int S = Elem<DT>::bytes, U = group_of(K);
     __shared__ float s_part[kBlock * V];
     const ConvPos p = conv_pos<UNI>(g, T, D);
@@ -363,8 +363,7 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(UNI ? 4 
         const char* pg = static_cast<const char*>(a.g) + (size_t)(p.bi * T + p.t0) * so;
         // of token t - K + 1, which for the first tokens is not there (nor written)
         char* pq = a.gx.row(p.bi, p.t0) - a.gx.st * (K - 1);
-            const int64_t end = p.t0 + g.rows;  // one past the chunk's last token, which may lie past T
-
+        const int64_t end = p.t0 + g.rows;  // one past the chunk's last token, which may lie past T
         for (int64_t t = p.t0; t < end + K - 1; t += U) {
             const uint32_t starts = st.template group<U>(t);
             Quad<DT> x[U], gr[U];
@@ -381,6 +380,8 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(UNI ? 4 
                 const int64_t tu = t + u, s = tu - (K - 1);
                 const bool start = (starts >> u) & 1u;
                 if (tu < T) age = start ? 0 : (age < K - 1 ? age + 1 : K - 1);
+                // tokens back whose gradient it adds to: past the last token, none
+                const int reach = tu < T ? age : -1;
                 if (some<UNI>(start)) {
 #pragma unroll
                     for (int j = 0; j < K - 1; ++j)
@@ -396,26 +397,23 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(UNI ? 4 
                         gz[j] *= q * fmaf(z, 1.0f - q, 1.0f);
                     }
                 }
-                if (some<UNI>(tu >= T)) {
-#pragma unroll
-                    for (int j = 0; j < V; ++j) gz[j] = tu < T ? gz[j] : 0.0f;
-                }
-                if (some<UNI>(tu < end)) {  // the walk's last K - 1 tokens are the next chunk's
+                // the walk's last K - 1 tokens are the next chunk's, or past the last
+                // one (skipped and not multiplied by 0: an infinity may be there)
+                if (tu < p.t1) {
 #pragma unroll
                     for (int j = 0; j < V; ++j) {
-                        const float gm = tu < end ? gz[j] : 0.0f;
-                        db[j] += gm;
-                        dw[K - 1][j] = fmaf(gm, x[u].get(j), dw[K - 1][j]);
+                        db[j] += gz[j];
+                        dw[K - 1][j] = fmaf(gz[j], x[u].get(j), dw[K - 1][j]);
 #pragma unroll
-                        for (int k = 0; k < K - 1; ++k) dw[k][j] = fmaf(gm, win[(u + k) % (K - 1)].get(j), dw[k][j]);
+                        for (int k = 0; k < K - 1; ++k) dw[k][j] = fmaf(gz[j], win[(u + k) % (K - 1)].get(j), dw[k][j]);
                     }
                 }
-                if (some<UNI>(age < K - 1)) {
+                if (some<UNI>(reach < K - 1)) {
 #pragma unroll
                     for (int i = 0; i < K - 1; ++i)
 #pragma unroll
                         for (int j = 0; j < V; ++j)
-                            if (K - 1 - i <= age) acc[(u + i) % (K - 1)][j] = fmaf(tp.w[i][j], gz[j], acc[(u + i) % (K - 1)][j]);
+                            if (K - 1 - i <= reach) acc[(u + i) % (K - 1)][j] = fmaf(tp.w[i][j], gz[j], acc[(u + i) % (K - 1)][j]);
                 } else {
 #pragma unroll
                     for (int i = 0; i < K - 1; ++i)

@@ -245,3 +245,22 @@ def test_resets_in_long_walks(shape):
     x[:, t % 97 == 68], x[:, t % 97 == 69], g[:, t % 97 == 5] = float("inf"), float("nan"), float("nan")
     gx2 = lr.short_conv_backward(x, w, b, g, reset=m, activation="silu")[0]
     assert torch.equal(gx[:, ~bad], gx2[:, ~bad])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [24, 260])
+@pytest.mark.parametrize("K", [2, 3, 4])
+def test_no_token_past_the_last_takes_part(K, D, dtype):
+    """The last input belongs to the last tap's gradient alone, an early tap to no gradient of the last token: an
+    infinity in one leaves the others as they are, bit for bit."""
+    for T in (50, 64, 203):
+        c = Case(2, T, D, K, dtype, act=None)
+        grads = c.backward()
+        c.x = c.x.clone()
+        c.x[:, -1] = float("inf")
+        got = c.backward()
+        assert torch.equal(got[0], grads[0]) and torch.equal(got[2], grads[2])
+        assert torch.equal(got[1][:-1], grads[1][:-1]) and not torch.isfinite(got[1][-1]).any()
+        c.w = c.w.clone()
+        c.w[0] = float("inf")
+        assert torch.equal(c.backward()[0][:, T - K + 1:], grads[0][:, T - K + 1:])
