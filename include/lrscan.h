@@ -390,7 +390,8 @@ LRSCAN_API int scan_embed_fwd(const void* ids, int id_bytes, const void* weight,
  *   row is written (zeros where no token names it), or with accumulate != 0
  *   rows that tokens name are added to and the others not touched.  A row's
  *   tokens are added in the order that N, V and ids alone fix, in fp32, and
- *   rounded once.  opts: only the workspace is used. */
+ *   rounded once.  opts: only the workspace is used (and of up to 256 tokens
+ *   not even that: such a call may be the first of a stream in capture). */
 LRSCAN_API int scan_embed_bwd(const void* ids, int id_bytes, const void* grad_out, float scale,
                               void* grad_weight, int grad_dtype, int accumulate, int64_t N, int64_t V,
                               int64_t D, int dtype, void* stream, const lrscan_opts* opts);

@@ -1117,7 +1117,9 @@ LRSCAN_API int scan_embed_bwd(const void* ids, int id_bytes, const void* grad_ou
     if (!embed_fits(s)) return LRSCAN_ERR_DIM;
     hipStream_t hs = static_cast<hipStream_t>(stream);
     void* ws = nullptr;
-    const int rc = plain_workspace(embed_ws_bytes(s), opts, hs, &ws);
+    // a buffer that is given is checked whether or not the call will use it
+    const bool given = opts && opts->workspace;
+    const int rc = plain_workspace(given || embed_sorts(s) ? embed_ws_bytes(s) : 0, opts, hs, &ws);
     if (rc != LRSCAN_OK) return rc;
     return hip_status(launch_embed_bwd(s, ids, grad_out, scale, grad_weight, grad_dtype, accumulate != 0, ws, hs));
 }

@@ -859,6 +859,8 @@ hipError_t launch_embed_fwd(const EmbedShape& s, const void* ids, const void* w,
                            : embed_fwd_t<DT_BF16, 4>(s, ids, w, scale, out, st);
 }
 
+bool embed_sorts(const EmbedShape& s) { return s.N > kDirectTokens; }
+
 size_t embed_ws_bytes(const EmbedShape& s) {
     EmbedWs w;
     return ws_layout(s, nullptr, &w);
@@ -866,18 +868,18 @@ size_t embed_ws_bytes(const EmbedShape& s) {
 
 hipError_t launch_embed_bwd(const EmbedShape& s, const void* ids, const void* g, float scale, void* grad,
                             int grad_dtype, bool add, void* ws, hipStream_t st) {
-    EmbedWs w;
-    ws_layout(s, ws, &w);
-    const SortPlan plan = sort_plan(s);
     const uint64_t row = (uint64_t)s.D * (grad_dtype == DT_F32 ? 4 : 2);
     const uint64_t bytes = add ? 0 : (uint64_t)s.V * row;
     char* table = static_cast<char*>(grad);
-    if (s.N <= kDirectTokens) {
+    if (!embed_sorts(s)) {
         const Sorted x{nullptr, nullptr, (uint32_t)s.N, (uint32_t)s.V, 0, nullptr, nullptr, scale, add, s.D,
                        whole_blocks(s, grad)};
         return s.id_bytes == 8 ? direct(s, x, KeysFromIds<8>{ids, s.V}, g, grad, grad_dtype, bytes, st)
                                : direct(s, x, KeysFromIds<4>{ids, s.V}, g, grad, grad_dtype, bytes, st);
     }
+    EmbedWs w;
+    ws_layout(s, ws, &w);
+    const SortPlan plan = sort_plan(s);
     int at = 0;
     const hipError_t e =
         s.id_bytes == 8

@@ -18,8 +18,12 @@ bool embed_fits(const EmbedShape& s);
 hipError_t launch_embed_fwd(const EmbedShape& s, const void* ids, const void* w, float scale, void* out,
                             hipStream_t st);
 
-// `ws` holds embed_ws_bytes (256-byte aligned).  `add`: rows that tokens name
-// are added to and the others left as they are; else every row is written.
+// Whether a gradient sorts its tokens; only then is its workspace used.
+bool embed_sorts(const EmbedShape& s);
+
+// `ws` holds embed_ws_bytes (256-byte aligned; NULL where nothing is sorted).
+// `add`: rows that tokens name are added to and the others left as they are;
+// else every row is written.
 size_t embed_ws_bytes(const EmbedShape& s);
 hipError_t launch_embed_bwd(const EmbedShape& s, const void* ids, const void* g, float scale,
                             void* grad, int grad_dtype, bool add, void* ws, hipStream_t st);

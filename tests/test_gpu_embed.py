@@ -173,3 +173,28 @@ def test_refusals():
                                           workspace=torch.zeros(4, device="cuda"))):
         with pytest.raises(lr.LRScanError):
             bad()
+
+
+@pytest.mark.parametrize("n", [1, 100, 256])
+def test_a_small_gradient_captures_on_a_stream_without_a_workspace(n):
+    """Nothing is sorted, so nothing has to be there; of one token more there has."""
+    from test_gpu_graphs_streams import fresh_stream
+    V, D = 300, 40
+    t = torch.from_numpy(make_ids("zipf", n, V)).cuda()
+    g = put(np.random.default_rng(n).standard_normal((n, D)), "bf16")
+    want = lr.embed_backward(t, g, V, 2.0)
+    more, gmore = torch.zeros(257, dtype=torch.int64, device="cuda"), torch.zeros(257, D, device="cuda")
+    st = fresh_stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=st):
+        cap = lr.embed_backward(t, g, V, 2.0)
+        with pytest.raises(lr.LRScanError) as err:
+            lr.embed_backward(more, gmore, V)
+    assert err.value.status == -8
+    for _ in range(3):
+        cap.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(cap, want)
+        assert torch.equal(lr.embed_backward(t, g, V, 2.0), want)
