@@ -1116,17 +1116,16 @@ def _model_function(name):
             x, gate_r, gate_i = (_rows_contiguous(t) for t in (x, gate_r, gate_i))
             decay = decay.contiguous()
             out, _ = gated_scan(x, gate_r, gate_i, decay, scale, reset=reset, with_last=False)
-            ctx.save_for_backward(x, gate_r, gate_i, decay, out)
-            ctx.scale, ctx.reset = scale, reset
+            ctx.save_for_backward(x, gate_r, gate_i, decay, out, reset)
+            ctx.scale = scale
             return out
 
         @staticmethod
         @once_differentiable
         def backward(ctx, grad):
-            x, gate_r, gate_i, decay, out = ctx.saved_tensors
+            x, gate_r, gate_i, decay, out, reset = ctx.saved_tensors
             gx, gr, gi, gd, _ = gated_scan_backward(x, gate_r, gate_i, decay, out,
-                                                    grad.contiguous(), ctx.scale,
-                                                    reset=ctx.reset)
+                                                    grad.contiguous(), ctx.scale, reset=reset)
             return gx, gr, gi, gd, None, None
 
     class ShortConvFunction(torch.autograd.Function):
@@ -1136,16 +1135,16 @@ def _model_function(name):
             bias = None if bias is None else bias.contiguous()
             out, _ = short_conv(x, weight, bias, reset=reset, activation=activation,
                                 with_last=False)
-            ctx.save_for_backward(x, weight, bias)
-            ctx.reset, ctx.activation = reset, activation
+            ctx.save_for_backward(x, weight, bias, reset)
+            ctx.activation = activation
             return out
 
         @staticmethod
         @once_differentiable
         def backward(ctx, grad):
-            x, weight, bias = ctx.saved_tensors
-            gx, gw, gb, _ = short_conv_backward(x, weight, bias, grad.contiguous(),
-                                                reset=ctx.reset, activation=ctx.activation)
+            x, weight, bias, reset = ctx.saved_tensors
+            gx, gw, gb, _ = short_conv_backward(x, weight, bias, grad.contiguous(), reset=reset,
+                                                activation=ctx.activation)
             return gx, gw, gb, None, None
 
     class EmbeddingFunction(torch.autograd.Function):

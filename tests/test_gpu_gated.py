@@ -376,3 +376,18 @@ def test_offsets_past_32_bits():
         close(name, got[-1:, -n:, cols], want[name], "bf16")
         assert not got[0].any() and not got[1, :-n - 1].any()
     close("grad_decay", grads[3][cols], want["grad_decay"], "f32")
+
+
+def test_a_mask_changed_before_the_backward_is_refused():
+    """As any operand changed in place is: an error, and no gradient of another mask's segments."""
+    x = torch.randn(2, 9, 8, device="cuda", requires_grad=True)
+    ones = torch.ones(8, device="cuda")
+    for call in (lambda m: lr.gated_diagonal_scan(x, x, x, ones, reset=m),
+                 lambda m: lr.short_convolution(x, torch.ones(4, 8, device="cuda"), reset=m)):
+        m = torch.zeros(2, 9, dtype=torch.bool, device="cuda")
+        m[:, 4] = True
+        torch.autograd.grad(call(m).sum(), x)
+        out = call(m).sum()
+        m[:, 4] = False
+        with pytest.raises(RuntimeError):
+            torch.autograd.grad(out, x)
