@@ -983,6 +983,7 @@ LRSCAN_API int scan_gated_bwd(const void* x, const void* gate_r, const void* gat
     int algo = 0;
     int rc = gated_algo(s, 1, rows, 6, opts, &algo);
     if (rc != LRSCAN_OK) return rc;
+    if (grad_decay && !gated_decay_fits(D)) return LRSCAN_ERR_DIM;
     hipStream_t hs = static_cast<hipStream_t>(stream);
     Workspace ws;
     void* part = nullptr;
@@ -1029,7 +1030,7 @@ LRSCAN_API size_t scan_gated_workspace_bytes(int64_t B, int64_t T, int64_t D, in
     for (int dir = 0; dir < 2; ++dir) {
         int algo = 0;
         if (gated_algo(s, dir, nullptr, 0, opts, &algo) != LRSCAN_OK) return 0;
-        size_t n = dir == 1 ? gated_sum_bytes(s, algo) : 0;
+        size_t n = dir == 1 && gated_decay_fits(D) ? gated_sum_bytes(s, algo) : 0;
         if (algo == LRSCAN_ALGO_FUSED) n += align_up(gated_fused_bytes(s), 256);
         need = n > need ? n : need;
     }
@@ -1069,6 +1070,7 @@ LRSCAN_API int scan_conv_bwd(const void* x, const float* weight, const float* bi
     hipStream_t hs = static_cast<hipStream_t>(stream);
     void* part = nullptr;
     if (grad_weight || grad_bias) {
+        if (!conv_sums_fit(s)) return LRSCAN_ERR_DIM;
         const int rc = plain_workspace(conv_bytes(s), opts, hs, &part);
         if (rc != LRSCAN_OK) return rc;
     }
@@ -1089,7 +1091,7 @@ LRSCAN_API int scan_conv_step(const void* x, const float* weight, const float* b
 LRSCAN_API size_t scan_conv_workspace_bytes(int64_t B, int64_t T, int64_t D, int64_t K, int dtype) {
     if (!dims_ok(B, T, D) || !dtype_ok(dtype) || !conv_args_ok(K, 0)) return 0;
     const ConvShape s{B, T, D, (int)K, dtype, 0};
-    return conv_fits(s) ? conv_bytes(s) : 0;
+    return conv_fits(s) && conv_sums_fit(s) ? conv_bytes(s) : 0;
 }
 
 // ---- embedding ------------------------------------------------------------------------------

@@ -60,6 +60,11 @@ int64_t column_sum_ranges(int64_t R) {
     return n < kSumRanges ? n : kSumRanges;
 }
 
+// Whether a launch's work-items along the columns stay in 32 bits.
+bool column_sum_fits(int64_t C) {
+    return (C + kWave - 1) / kWave < ((int64_t)1 << 32) / (kSumWaves * kWave);
+}
+
 // Bytes of `scratch` (0 if one launch does).
 size_t column_sum_scratch(int64_t R, int64_t C) {
     const int64_t n = column_sum_ranges(R);

@@ -609,6 +609,8 @@ bool conv_fits(const ConvShape& s) {
     return true;
 }
 
+bool conv_sums_fit(const ConvShape& s) { return column_sum_fits((s.K + 1) * s.D); }
+
 size_t conv_part_bytes(const ConvShape& s) {
     return (size_t)conv_grid(s, bwd_rows(s), kBwdWidth).blocks * (size_t)(s.K + 1) * (size_t)s.D * 4;
 }

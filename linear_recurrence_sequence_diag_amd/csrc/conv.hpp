@@ -38,8 +38,9 @@ struct ConvBwd {
     void* grad_state;  // [B, K - 1, D] or NULL
 };
 
-// Bytes of partial sums, and of their reduction's scratch, that a backward with
-// parameter gradients needs.
+// Whether a backward can have parameter gradients, and the bytes of their
+// partial sums and of the reduction's scratch.
+bool conv_sums_fit(const ConvShape& s);
 size_t conv_part_bytes(const ConvShape& s);
 size_t conv_sum_scratch(const ConvShape& s);
 bool conv_fits(const ConvShape& s);

@@ -353,6 +353,8 @@ hipError_t launch_gated_walk_bwd(const GatedShape& s, const GatedBwd& p, float* 
     return s.dtype == DT_F32 ? walk_bwd_t<DT_F32>(s, p, part, st) : walk_bwd_t<DT_BF16>(s, p, part, st);
 }
 
+bool gated_decay_fits(int64_t D) { return column_sum_fits(D); }
+
 size_t gated_decay_scratch(int64_t rows, int64_t D) { return column_sum_scratch(rows, D); }
 
 hipError_t launch_gated_decay(const float* part, int64_t rows, int64_t D, float* scratch,

@@ -70,6 +70,7 @@ hipError_t launch_gated_fused_bwd(const GatedShape& s, const GatedBwd& p, float*
 
 // grad_decay from `rows` rows of D partial sums; `scratch` holds
 // gated_decay_scratch bytes.
+bool gated_decay_fits(int64_t D);
 size_t gated_decay_scratch(int64_t rows, int64_t D);
 hipError_t launch_gated_decay(const float* part, int64_t rows, int64_t D, float* scratch,
                               const float* decay, float* grad_decay, hipStream_t st);

@@ -192,3 +192,21 @@ def test_refusals_of_the_tensor_helpers():
         lr.embed(torch.zeros(3, dtype=torch.int64), torch.zeros(5, 4))
     with pytest.raises(ValueError):
         lr.embed_backward(torch.zeros(3, dtype=torch.int64), torch.zeros(3, 4), 5)
+
+
+def test_sums_over_too_many_channels_are_refused():
+    """More columns than one launch's work-items can count: found before anything is enqueued."""
+    lr = _lib()
+    lib = lr.library()
+    p, D = 0x10000, 1 << 28  # never dereferenced
+
+    def gated(d):
+        return lib.scan_gated_bwd(p, p, p, p, 8.0, p, p, None, p, p, p, p, 1, 1, d, lr.F32, None, None, None)
+
+    def conv(d):
+        return lib.scan_conv_bwd(p, p, None, None, None, 0, p, None, p, p, p, None, 1, 1, d, 4, lr.F32, None, None, None)
+
+    assert gated(D) == -2 and conv(D // 5 + 64) == -2
+    assert lr.scan_gated_workspace_bytes(1, 1, D, lr.F32) == 0 < lr.scan_gated_workspace_bytes(1, 1, D - 64, lr.F32)
+    assert lr.scan_conv_workspace_bytes(1, 1, D // 5 + 64, 4, lr.F32) == 0
+    assert lr.scan_conv_workspace_bytes(1, 1, D // 5 - 64, 4, lr.F32) > 0
