@@ -45,3 +45,48 @@ def test_decoding_is_the_whole_row(lm):
     whole = model(ids)[:, 39:].detach()
     # two orders of the same fp32 sums over a width of 128
     assert (seen - whole).abs().max() <= 1e-4 * whole.abs().max()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_a_captured_step_replays_to_the_eager_chain(lm, dtype):
+    """Lookup, convolution step and gated step of one token in a graph on a stream that has no workspace, the states
+    moved on in place: every replay, with eager calls between, gives the eager chain's bits."""
+    from test_gpu_graphs_streams import fresh_stream
+    lr = lm.lr
+    B, V, D, K, steps = 5, 31, 136, 4, 6
+    table, gates = torch.randn(V, D, device="cuda").to(dtype), torch.randn(B, 2 * D, device="cuda").to(dtype)
+    taps, bias, decay = (torch.randn(*s, device="cuda") for s in ((K, D), (D,), (D,)))
+    tokens = torch.randint(0, V, (steps, B), device="cuda")
+    starts = torch.rand(steps, B, device="cuda") < 0.2
+    ids, reset = tokens[0].clone(), starts[0].clone()
+    window, state = torch.zeros(B, K - 1, D, device="cuda", dtype=dtype), torch.zeros(B, D, device="cuda")
+
+    def step():
+        c, _ = lr.short_conv_step(lr.embed(ids, table, 2.0), taps, bias, window, reset=reset, activation="silu",
+                                  out_state=window)
+        return c, lr.gated_step(c, gates[:, :D], gates[:, D:], decay, state, reset=reset, out_state=state)[0]
+
+    def chain(one):
+        window.zero_()
+        state.zero_()
+        rows = []
+        for k in range(steps):
+            ids.copy_(tokens[k])
+            reset.copy_(starts[k])
+            rows += [t.clone() for t in (*one(), window, state)]
+        return rows
+
+    want = chain(step)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=fresh_stream()):
+        out = step()
+
+    def replay():
+        graph.replay()
+        torch.cuda.synchronize()
+        return out
+
+    for _ in range(2):
+        assert all(torch.equal(a, b) for a, b in zip(chain(replay), want))
+        assert all(torch.equal(a, b) for a, b in zip(chain(step), want))
