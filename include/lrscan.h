@@ -32,7 +32,9 @@
  *  - Results are deterministic: the same call on the same data gives the same
  *    bits every time.
  *  - Calls that share one workspace (the library's own per-stream workspace,
- *    or one passed in opts) must be ordered on one stream.
+ *    or one passed in opts) must be ordered on one stream.  A call may be
+ *    several launches, so host threads that share a stream, and with it the
+ *    library's workspace, make their calls one after the other.
  *  - Graph capture.  While `stream` is capturing a HIP graph, the library
  *    allocates, frees and initialises nothing.  A call that needs the
  *    library's workspace (opts->workspace NULL) then uses the one this stream

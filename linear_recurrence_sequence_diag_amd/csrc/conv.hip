@@ -25,9 +25,11 @@
 //
 // Bound (MI355X, bf16 [8, 2048, 2560], K = 4, with resets and activation,
 // caches flushed): forward 37 us for 168 MB (4.5 TB/s), the vector units busy
-// for 21; reverse 62 us and 5 for the parameters' sums, 252 MB (4.0 TB/s), the
-// vector units busy for 40: four wavefronts a SIMD, each with a group of rows in
-// flight, cover neither wholly.
+// for 21; reverse 68 us, 5 of them the parameters' sums, for 252 MB (3.7 TB/s),
+// the vector units busy for 42: four wavefronts a SIMD, each with a group of
+// rows in flight, cover neither wholly.  Smaller calls leave a SIMD two
+// wavefronts (bf16 [8, 2048, 1024] 39 us for 101 MB), and rows that are not
+// whole quads take twice the time ([8, 2048, 1023] 90 us).
 #include "conv.hpp"
 
 #include <type_traits>
@@ -113,7 +115,7 @@ int fwd_rows(const ConvShape& s) {
 // with the least is taken.  Measured on MI355X (us, K = 4, in walks of 24, 36,
 // 48, 60 and 72 tokens; the one taken in brackets):
 //   bf16 [8,2048,2560]    74    75   [69]   70    76
-//        [16,4096,2560]  242   230   227   225   226  [221 in 84]
+//        [16,4096,2560]  242   230   227   225   226  [222 in 84]
 //        [8,2048,1024]    38   [38]   43    50    49
 //        [16,2048,1024]   62   [58]   57    64    62
 //   fp32 [4,2048,4096]    91   [86]   86    91    81

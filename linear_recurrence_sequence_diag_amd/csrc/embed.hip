@@ -21,8 +21,11 @@
 //  * The sorted tokens are cut into chunks of equal length, whatever rows they
 //    name.  A wavefront adds its chunk's tokens row by row in fp32 and writes
 //    every row that lies inside the chunk.  A row that crosses a chunk's end
-//    leaves partial sums, which one more launch adds in the chunks' order, so
-//    a token that half the batch consists of costs no more than others.
+//    leaves partial sums, which one more launch adds in the chunks' order, a
+//    fourth of them to a wavefront.  A token that the batch consists of to half
+//    or wholly is a long such row: 16384 tokens into bf16 [262144, 2560], whose
+//    most frequent holds 3% of them, 257 us, half of them one token 274, all of
+//    them 289.
 //
 // Bound (MI355X, caches flushed): bytes.  Lookup, 16384 tokens of bf16 rows of
 // 2560: 20 us, 84 MB written at 4.2 TB/s and a table's rows read as the caches

@@ -100,8 +100,9 @@ __global__ __launch_bounds__(kBlock) void gated_walk_fwd_kernel(GatedFwd p, Walk
 
 // One step (T = 1): four channels of R batch rows to a thread, all their loads
 // before the arithmetic; h0 may be last itself.  A decode step is one round of
-// loads and stores long: 3.1 us at bf16 [32, 2560], whose 1.4 MB are 0.3.  A channel's rate costs about
-// as much as a step, so R rows share it where rows are many.
+// loads and stores long: 3.1 us at bf16 [32, 2560], whose 1.4 MB are 0.3.  A
+// channel's rate costs about as much as a step, so R rows share it where rows
+// are many.
 template <int DT, bool FULL, int R>
 __global__ __launch_bounds__(kBlock) void gated_step_kernel(GatedFwd p, int64_t B, int64_t D, uint32_t vpr) {
     constexpr int S = Elem<DT>::bytes;
@@ -326,7 +327,14 @@ bool gated_bwd_aligned(const GatedShape& s, const GatedBwd& p) {
 // A channel's rate costs a thread about as much as two steps, so short
 // sequences share it (and one partial row of the decay gradient) among up to
 // 16 steps' worth of batch rows, as long as that leaves eight wavefronts to
-// a CU.  WALKNOTE
+// a CU.  Measured on MI355X (us forward / reverse; one row to a thread, up to 8,
+// 16 and 32 steps' worth):
+//   bf16 [8192,2,1024]  53 /  94    44 /  74    48 /  63    49 /  63
+//        [4096,4,1024]  39 /  82    38 /  77    37 /  67    37 /  67
+//        [2048,8,2560]  75 / 155    75 / 155    82 / 149    78 / 167
+//   f32  [2048,8,2560] 120 / 246   121 / 246   130 / 256   140 / 265
+// (half as many wavefronts to a CU: [1024,4,1024] 15 / 29 for 13 / 27; twice as
+// many: [4096,4,1024] 38 / 76 for 37 / 67).
 int64_t gated_walk_rows(const GatedShape& s) {
     const int64_t v = s.dtype == DT_F32 ? Elem<DT_F32>::V : Elem<DT_BF16>::V;
     const int64_t threads = s.B * ((s.D + v - 1) / v);

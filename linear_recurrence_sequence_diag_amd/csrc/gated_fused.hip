@@ -648,7 +648,7 @@ void gated_bwd_kernel(GatedBwdArgs x) {
 // host side
 // ---------------------------------------------------------------------------
 // OCC_F, OCC_G: wavefronts a SIMD is to hold, forward and reverse (their
-// registers fit without spilling, or with under 40 bytes).
+// registers fit without spilling, or with at most 56 bytes).
 template <int DT, int TPR, int NR, int LB, int OF, int OB>
 struct GCfg : Cfg<DT, TPR, NR, 4, LB> {
     static constexpr int OCC_F = OF, OCC_G = OB;

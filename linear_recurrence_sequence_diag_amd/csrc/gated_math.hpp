@@ -101,9 +101,10 @@ __device__ __forceinline__ float gated_a_of(float gr, float rate) {
 // Gradients of one step from its adjoint lam and the state before it:
 //   du = lam beta,  dx = du i,  dgi = dx x (1 - i),
 //   P = y dL/dy = lam a y (h_prev - a u / beta),  dgr = P (1 - r),
-// and sum P gives grad_decay (times ln 2 for a y in units of log 2).  y / beta is finite down to beta = 0 (y and
-// beta^2 vanish together), so P is formed from a y2 and y2 / beta.
-// a is the transition, and p is P / ln 2 (its sum takes the factor once).
+// and sum P gives grad_decay (times ln 2 for a y in units of log 2).  y / beta
+// is finite down to beta = 0 (y and beta^2 vanish together), so P is formed
+// from a y2 and y2 / beta.  a is the transition, and p is P / ln 2 (its sum
+// takes the factor once).
 struct GatedGrad {
     float dx, dgr, dgi, p, a;
 };

@@ -9,9 +9,8 @@ namespace lrscan {
 
 constexpr int kQuad = 4;
 
-// FULL: rows are whole quads; then a quad
-// is one access, whatever its address is aligned to, else the last one of a
-// row goes channel by channel.
+// FULL: rows are whole quads; then a quad is one access, whatever its address
+// is aligned to, else the last one of a row goes channel by channel.
 template <int DT>
 struct Quad {
     static constexpr int S = Elem<DT>::bytes;
