@@ -400,6 +400,62 @@ LRSCAN_API int scan_embed_bwd(const void* ids, int id_bytes, const void* grad_ou
 /* Bytes of caller workspace the gradient needs (0 for invalid arguments). */
 LRSCAN_API size_t scan_embed_workspace_bytes(int64_t N, int64_t V, int64_t D, int dtype);
 
+/* ------------------------------------------------------------------------
+ * Gated delta rule: a recurrence whose state is a matrix S [K, V] for each of H
+ * heads.  A token decays the state, reads what its key gives, and writes the
+ * difference to its value back under that key:
+ *   a_t = exp(log_decay_t),
+ *   S_t = a_t S_{t-1} + beta_t k_t (v_t - a_t S_{t-1}^T k_t)^T,
+ *   out_t = scale S_t^T q_t.
+ * q, k [B,T,HK,K] and v [B,T,H,V] of `dtype`; log_decay and beta [B,T,H] fp32;
+ * value head h reads query/key head h / (H / HK) (H a multiple of HK).  K is at
+ * most 256.  Queries and keys are taken as they are: with keys of norm 1 and
+ * beta in [0, 1] the state stays bounded.  A log_decay below -200 counts as
+ * -200 (a decay of 0 in fp32).
+ * At a reset step (opts->reset, [B,T]) the state that enters is dropped,
+ * whatever it holds, and log_decay is not used; nothing of one segment reaches
+ * another, be it an infinity or a NaN.  Within a segment an infinity may come
+ * out as a NaN.
+ * Tokens are taken in blocks of 64, whose products run on the matrix cores with
+ * the accuracy of fp32 (every operand as the exact sum of bf16 parts); all sums
+ * and states are fp32.
+ * `strides` (a host array, or NULL for contiguous) holds three numbers for each
+ * operand, in elements: from one batch row, one step and one head to the next
+ * (q, k and v may be parts of one projection).  None is negative; one may be 0.
+ * log_decay and beta are read element by element; rows of q, k and v are
+ * contiguous.  out, last and every gradient are contiguous.
+ * opts: algo AUTO with chunk and width 0; h0 and grad_h0 [B,H,K,V]; reset;
+ * workspace.
+ * ------------------------------------------------------------------------ */
+/*   out [B,T,H,V] dtype and last [B,H,K,V] fp32 written, one of them may be
+ *   NULL.  strides: q, k, v, log_decay, beta. */
+LRSCAN_API int scan_delta_fwd(const void* q, const void* k, const void* v, const float* log_decay,
+                              const float* beta, float scale, void* out, float* last, int64_t B, int64_t T,
+                              int64_t H, int64_t HK, int64_t K, int64_t V, int dtype, const int64_t* strides,
+                              void* stream, const lrscan_opts* opts);
+/*   Gradients of <grad_out, out> + <grad_last, last> (grad_last may be NULL):
+ *   grad_q, grad_k [B,T,HK,K] (summed over the heads that share a row, in order)
+ *   and grad_v [B,T,H,V] of dtype, grad_log_decay and grad_beta [B,T,H] fp32.
+ *   strides: as above. */
+LRSCAN_API int scan_delta_bwd(const void* q, const void* k, const void* v, const float* log_decay,
+                              const float* beta, float scale, const void* grad_out, const float* grad_last,
+                              void* grad_q, void* grad_k, void* grad_v, float* grad_log_decay,
+                              float* grad_beta, int64_t B, int64_t T, int64_t H, int64_t HK, int64_t K,
+                              int64_t V, int dtype, const int64_t* strides, void* stream,
+                              const lrscan_opts* opts);
+/*   One token on [B,HK,K], [B,H,V] and [B,H]: state_in [B,H,K,V] fp32 (NULL:
+ *   zero) to state_out (may equal state_in; may be NULL when out is given),
+ *   reset [B] or NULL.  strides: two numbers for each operand, batch row and head,
+ *   or NULL. */
+LRSCAN_API int scan_delta_step(const void* q, const void* k, const void* v, const float* log_decay,
+                               const float* beta, float scale, const float* state_in, const uint8_t* reset,
+                               void* out, float* state_out, int64_t B, int64_t H, int64_t HK, int64_t K,
+                               int64_t V, int dtype, const int64_t* strides, void* stream);
+/* Bytes of caller workspace that a call of these sizes needs, with resets or
+ * without (0 for invalid arguments). */
+LRSCAN_API size_t scan_delta_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t HK, int64_t K,
+                                             int64_t V, int dtype, int backward);
+
 /* Bytes of workspace the call with these arguments needs (0 if none).
  * Returns 0 for invalid arguments. */
 LRSCAN_API size_t scan_workspace_bytes(int64_t B, int64_t T, int64_t D, int dtype,

@@ -88,6 +88,12 @@ _SIGS = {
     "scan_embed_bwd": ([_P, _INT, _P, _F32, _P, _INT, _INT, _I64, _I64, _I64, _INT, _P,
                         ctypes.POINTER(Opts)], _INT),
     "scan_embed_workspace_bytes": ([_I64, _I64, _I64, _INT], ctypes.c_size_t),
+    "scan_delta_fwd": ([_P] * 5 + [_F32, _P, _P] + [_I64] * 6 + [_INT, _P, _P,
+                                                                ctypes.POINTER(Opts)], _INT),
+    "scan_delta_bwd": ([_P] * 5 + [_F32] + [_P] * 7 + [_I64] * 6 + [_INT, _P, _P,
+                                                                    ctypes.POINTER(Opts)], _INT),
+    "scan_delta_step": ([_P] * 5 + [_F32] + [_P] * 4 + [_I64] * 5 + [_INT, _P, _P], _INT),
+    "scan_delta_workspace_bytes": ([_I64] * 6 + [_INT, _INT], ctypes.c_size_t),
     "scan_auto_algo": ([_I64, _I64, _I64, _INT, _INT, ctypes.POINTER(_INT), ctypes.POINTER(_INT)],
                        _INT),
     "scan_chunk_summary": ([_P, _P, _P, _P, _I64, _I64, _I64, _INT, _INT, _P], _INT),
@@ -272,7 +278,7 @@ def _opts(opts):
     return ctypes.byref(opts) if opts is not None else None
 
 
-_I64_ARRAYS = [_I64 * n for n in range(13)]
+_I64_ARRAYS = [_I64 * n for n in range(16)]
 
 
 def _i64s(values):
@@ -346,6 +352,32 @@ def scan_embed_bwd(ids, id_bytes, grad_out, scale, grad_weight, grad_dtype, accu
 
 def scan_embed_workspace_bytes(N, V, D, dtype):
     return library().scan_embed_workspace_bytes(N, V, D, dtype)
+
+
+def scan_delta_fwd(q, k, v, log_decay, beta, scale, out, last, B, T, H, HK, K, V, dtype, strides,
+                   stream, opts):
+    return _check(library().scan_delta_fwd(q, k, v, log_decay, beta, scale, out, last, B, T, H, HK,
+                                           K, V, dtype, _i64s(strides), stream, _opts(opts)),
+                  "scan_delta_fwd")
+
+
+def scan_delta_bwd(q, k, v, log_decay, beta, scale, grad_out, grad_last, grad_q, grad_k, grad_v,
+                   grad_log_decay, grad_beta, B, T, H, HK, K, V, dtype, strides, stream, opts):
+    return _check(library().scan_delta_bwd(q, k, v, log_decay, beta, scale, grad_out, grad_last,
+                                           grad_q, grad_k, grad_v, grad_log_decay, grad_beta, B, T,
+                                           H, HK, K, V, dtype, _i64s(strides), stream,
+                                           _opts(opts)), "scan_delta_bwd")
+
+
+def scan_delta_step(q, k, v, log_decay, beta, scale, state_in, reset, out, state_out, B, H, HK, K,
+                    V, dtype, strides, stream):
+    return _check(library().scan_delta_step(q, k, v, log_decay, beta, scale, state_in, reset, out,
+                                            state_out, B, H, HK, K, V, dtype, _i64s(strides),
+                                            stream), "scan_delta_step")
+
+
+def scan_delta_workspace_bytes(B, T, H, HK, K, V, dtype, backward):
+    return library().scan_delta_workspace_bytes(B, T, H, HK, K, V, dtype, int(backward))
 
 
 # ---------------------------------------------------------------------------
@@ -942,6 +974,142 @@ def embed_backward(ids, grad_out, rows, scale=1.0, grad_weight=None, workspace=N
     return gw
 
 
+# ---- gated delta rule ----
+def _check_delta(q, k, v, log_decay, beta, lead):
+    """Shapes of a call whose operands have ``lead`` dimensions before the heads;
+    returns (H, HK, K, V)."""
+    torch = _torch()
+    names = "[B, T, " if lead == 2 else "[B, "
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != lead + 2:
+            raise ValueError(f"{name} must be a CUDA (HIP) {names}heads, width] tensor")
+        if t.stride(-1) != 1 and t.shape[-1] > 1:
+            raise ValueError(f"{name} must be contiguous along its last dimension")
+        if t.dtype != q.dtype or t.get_device() != q.get_device():
+            raise ValueError(f"{name} must match q in dtype and device")
+    HK, K = q.shape[-2:]
+    H, V = v.shape[-2:]
+    if k.shape != q.shape or v.shape[:lead] != q.shape[:lead]:
+        raise ValueError("k must have q's shape, and v q's batch and steps")
+    if HK < 1 or H % HK != 0:
+        raise ValueError("v's heads must be a multiple of q's and k's")
+    for name, t in (("log_decay", log_decay), ("beta", beta)):
+        if (not isinstance(t, torch.Tensor) or t.shape != v.shape[:-1] or t.dtype != torch.float32
+                or t.get_device() != q.get_device()):
+            raise ValueError(f"{name} must be a float32 {names}H] tensor on q's device")
+    return H, HK, K, V
+
+
+def _head_strides(*tensors):
+    """Strides of the operands, the last one of q, k and v left out, or None where
+    all are contiguous; a dimension of one takes 0 (torch leaves it arbitrary)."""
+    for t in tensors:
+        if not t.is_contiguous():
+            break
+    else:
+        return None
+    out = []
+    for i, t in enumerate(tensors):
+        n = t.dim() - (i < 3)
+        out += [t.stride(d) if t.shape[d] > 1 else 0 for d in range(n)]
+    return out
+
+
+def _check_matrix_state(name, t, shape, ref):
+    torch = _torch()
+    if t is not None and (not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype != torch.float32
+                          or t.get_device() != ref.get_device() or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous float32 [B, H, K, V] tensor on q's device")
+
+
+def _delta_reset(reset, q):
+    torch = _torch()
+    if reset is not None and (not isinstance(reset, torch.Tensor) or reset.shape != q.shape[:-2]
+                              or reset.dtype not in (torch.bool, torch.uint8)
+                              or reset.get_device() != q.get_device() or not reset.is_contiguous()):
+        dims = "[B, T]" if q.dim() == 4 else "[B]"
+        raise ValueError(f"reset must be a contiguous bool or uint8 {dims} tensor on q's device")
+
+
+def delta_scan(q, k, v, log_decay, beta, scale=None, h0=None, reset=None, with_last=True,
+               with_out=True, workspace=None):
+    """Gated delta rule S_t = a_t S_{t-1} + beta_t k_t (v_t - a_t S_{t-1}^T k_t)^T,
+    a_t = exp(log_decay_t), out_t = scale S_t^T q_t, with a state S [K, V] for each
+    head.  q, k: [B, T, HK, K]; v: [B, T, H, V], contiguous along the last
+    dimension (they may be parts of one projection); value head h reads query/key
+    head h // (H // HK); log_decay, beta: float32 [B, T, H]; K at most 256;
+    ``scale`` None: K ** -0.5; ``h0``: float32 [B, H, K, V]; ``reset`` ([B, T]
+    bool/uint8) starts segments.  Returns (out, last): [B, T, H, V] in q's dtype
+    and float32 [B, H, K, V]; parts not asked for are None."""
+    torch = _torch()
+    H, HK, K, V = _check_delta(q, k, v, log_decay, beta, 2)
+    B, T = q.shape[:2]
+    _check_matrix_state("h0", h0, (B, H, K, V), q)
+    _delta_reset(reset, q)
+    if not (with_out or with_last):
+        raise ValueError("a forward needs out or last")
+    out = torch.empty((B, T, H, V), device=q.device, dtype=q.dtype) if with_out else None
+    last = (torch.empty((B, H, K, V), device=q.device, dtype=torch.float32) if with_last
+            else None)
+    opts = make_opts(h0=h0, reset=reset, workspace=workspace)
+    _enqueue(q, lambda *a: scan_delta_fwd(*a, opts), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+             log_decay.data_ptr(), beta.data_ptr(), K ** -0.5 if scale is None else scale,
+             _ptr(out), _ptr(last), B, T, H, HK, K, V, dtype_code(q.dtype),
+             _head_strides(q, k, v, log_decay, beta))
+    return out, last
+
+
+def delta_scan_backward(q, k, v, log_decay, beta, grad_out, scale=None, grad_last=None, h0=None,
+                        need_grad_h0=False, reset=None, workspace=None):
+    """Adjoint of delta_scan.  Returns (grad_q, grad_k, grad_v, grad_log_decay,
+    grad_beta, grad_h0 or None), contiguous; the last three are float32.  A
+    query/key head's gradients are the sums over the value heads that read it."""
+    torch = _torch()
+    H, HK, K, V = _check_delta(q, k, v, log_decay, beta, 2)
+    B, T = q.shape[:2]
+    if (not isinstance(grad_out, torch.Tensor) or grad_out.shape != v.shape
+            or grad_out.dtype != q.dtype or grad_out.get_device() != q.get_device()
+            or not grad_out.is_contiguous()):
+        raise ValueError("grad_out must be a contiguous tensor of v's shape, dtype and device")
+    _check_matrix_state("h0", h0, (B, H, K, V), q)
+    _check_matrix_state("grad_last", grad_last, (B, H, K, V), q)
+    _delta_reset(reset, q)
+    gq, gk = (torch.empty((B, T, HK, K), device=q.device, dtype=q.dtype) for _ in range(2))
+    gv = torch.empty((B, T, H, V), device=q.device, dtype=q.dtype)
+    gg, gb = (torch.empty((B, T, H), device=q.device, dtype=torch.float32) for _ in range(2))
+    gh0 = (torch.empty((B, H, K, V), device=q.device, dtype=torch.float32) if need_grad_h0
+           else None)
+    opts = make_opts(h0=h0, grad_h0=gh0, reset=reset, workspace=workspace)
+    _enqueue(q, lambda *a: scan_delta_bwd(*a, opts), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+             log_decay.data_ptr(), beta.data_ptr(), K ** -0.5 if scale is None else scale,
+             grad_out.data_ptr(), _ptr(grad_last), gq.data_ptr(), gk.data_ptr(), gv.data_ptr(),
+             gg.data_ptr(), gb.data_ptr(), B, T, H, HK, K, V, dtype_code(q.dtype),
+             _head_strides(q, k, v, log_decay, beta))
+    return gq, gk, gv, gg, gb, gh0
+
+
+def delta_step(q, k, v, log_decay, beta, state=None, scale=None, reset=None, with_out=True,
+               out_state=None):
+    """One decoding step of delta_scan on [B, HK, K], [B, H, V] and [B, H] from a
+    float32 state [B, H, K, V] (None: zero; rows with reset set start anew).
+    Returns (out in q's dtype or None, the new state).  ``out_state`` may be
+    ``state`` (in place)."""
+    torch = _torch()
+    H, HK, K, V = _check_delta(q, k, v, log_decay, beta, 1)
+    B = q.shape[0]
+    _check_matrix_state("state", state, (B, H, K, V), q)
+    _check_matrix_state("out_state", out_state, (B, H, K, V), q)
+    _delta_reset(reset, q)
+    out = torch.empty((B, H, V), device=q.device, dtype=q.dtype) if with_out else None
+    new = (out_state if out_state is not None
+           else torch.empty((B, H, K, V), device=q.device, dtype=torch.float32))
+    _enqueue(q, scan_delta_step, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+             beta.data_ptr(), K ** -0.5 if scale is None else scale, _ptr(state), _ptr(reset),
+             _ptr(out), new.data_ptr(), B, H, HK, K, V, dtype_code(q.dtype),
+             _head_strides(q, k, v, log_decay, beta))
+    return out, new
+
+
 def n_chunks(T, chunk):
     return (T + chunk - 1) // chunk
 
@@ -1161,7 +1329,23 @@ def _model_function(name):
             ids, = ctx.saved_tensors
             return None, embed_backward(ids, grad.contiguous(), ctx.rows, ctx.scale), None
 
-    _model_functions.update(gated=GatedScanFunction, conv=ShortConvFunction,
+    class DeltaRuleFunction(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, q, k, v, log_decay, beta, scale, reset):
+            q, k, v = (_rows_contiguous(t) for t in (q, k, v))
+            out, _ = delta_scan(q, k, v, log_decay, beta, scale, reset=reset, with_last=False)
+            ctx.save_for_backward(q, k, v, log_decay, beta, reset)
+            ctx.scale = scale
+            return out
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, grad):
+            q, k, v, log_decay, beta, reset = ctx.saved_tensors
+            return (*delta_scan_backward(q, k, v, log_decay, beta, grad.contiguous(), ctx.scale,
+                                         reset=reset)[:5], None, None)
+
+    _model_functions.update(delta=DeltaRuleFunction, gated=GatedScanFunction, conv=ShortConvFunction,
                             embedding=EmbeddingFunction)
     return _model_functions[name]
 
@@ -1170,6 +1354,13 @@ def gated_diagonal_scan(x, gate_r, gate_i, decay, scale=8.0, reset=None):
     """Differentiable gated scan (torch autograd) returning every state; ``reset``
     ([B, T] bool/uint8, not differentiated) starts new segments."""
     return _model_function("gated").apply(x, gate_r, gate_i, decay, scale, reset)
+
+
+def gated_delta_rule(q, k, v, log_decay, beta, scale=None, reset=None):
+    """Differentiable delta_scan (torch autograd) from a zero state, returning the
+    outputs [B, T, H, V]; ``reset`` ([B, T] bool/uint8, not differentiated) starts
+    new segments."""
+    return _model_function("delta").apply(q, k, v, log_decay, beta, scale, reset)
 
 
 def short_convolution(x, weight, bias=None, reset=None, activation=None):

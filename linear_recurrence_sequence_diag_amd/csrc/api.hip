@@ -12,6 +12,7 @@
 
 #include "../../include/lrscan.h"
 #include "conv.hpp"
+#include "delta.hpp"
 #include "device.hpp"
 #include "embed.hpp"
 #include "gated.hpp"
@@ -43,8 +44,9 @@ size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 // fused form's self-cleaning scratch, which must not be shared with anything
 // else and is initialised once per allocation; kind 2 holds what a call
 // rewrites before it reads it: the fused-transition scan's factor tables and
-// partial sums, the partial sums of the gated scan and of the convolution, and
-// the sorted tokens of the embedding's gradient.
+// partial sums, the partial sums of the gated scan and of the convolution, the
+// sorted tokens of the embedding's gradient, and what the passes of the gated
+// delta rule hand on.
 //
 // Graph capture.  A call captured into a HIP graph bakes the workspace
 // address into the graph's kernel arguments, and every replay uses it.  So
@@ -459,6 +461,56 @@ int plain_workspace(size_t need, const lrscan_opts* o, hipStream_t st, void** ou
     const int rc = library_workspace(need, 2, st, &w);
     *out = w.ptr;
     return rc;
+}
+
+// ---- gated delta rule helpers ----
+
+// Operand `i` of a call with `heads` heads of `width` elements: its strides
+// (elements; batch row, step, head) from the caller's table, or those of a
+// contiguous [B, T, heads, width].
+HeadRows heads_of(const void* p, const int64_t* strides, int i, int64_t T, int64_t heads, int64_t width, int64_t bytes) {
+    const int64_t sb = strides ? strides[3 * i] : T * heads * width;
+    const int64_t st = strides ? strides[3 * i + 1] : heads * width;
+    const int64_t sh = strides ? strides[3 * i + 2] : width;
+    return HeadRows{static_cast<char*>(const_cast<void*>(p)), sb * bytes, st * bytes, sh * bytes};
+}
+
+// Strides of the five operands: none negative, every offset within a size that
+// keeps byte offsets exact.
+bool head_strides_ok(const int64_t* strides, const DeltaShape& s) {
+    if (!strides) return true;
+    for (int i = 0; i < 5; ++i) {
+        const int64_t n[3] = {s.B, s.T, i < 2 ? s.HK : s.H};
+        for (int j = 0; j < 3; ++j) {
+            const int64_t x = strides[3 * i + j];
+            if (x < 0 || x > kMaxElems || (n[j] > 1 && x > 4 * kMaxElems / n[j])) return false;
+        }
+    }
+    return true;
+}
+
+int delta_shape(int64_t B, int64_t T, int64_t H, int64_t HK, int64_t K, int64_t V, int dtype, DeltaShape* s) {
+    if (B < 1 || T < 1 || H < 1 || HK < 1 || K < 1 || V < 1) return LRSCAN_ERR_DIM;
+    if (H > kMaxElems || HK > H || H % HK != 0 || K > kDeltaMaxK || V > kMaxElems) return LRSCAN_ERR_DIM;
+    if (!dims_ok(B, T, H) || H * B * T > kMaxElems / (V > K ? V : K)) return LRSCAN_ERR_DIM;
+    if (!dtype_ok(dtype)) return LRSCAN_ERR_DTYPE;
+    if (H > 65536 || V > 65536) return LRSCAN_ERR_DIM;
+    *s = DeltaShape{B, T, (int)H, (int)HK, (int)K, (int)V, dtype};
+    return delta_fits(*s) ? LRSCAN_OK : LRSCAN_ERR_DIM;
+}
+
+int delta_opts_ok(const lrscan_opts* o) {
+    if (!o) return LRSCAN_OK;
+    if (o->algo != LRSCAN_ALGO_AUTO) return LRSCAN_ERR_ALGO;
+    return o->chunk != 0 || o->width != 0 ? LRSCAN_ERR_CHUNK : LRSCAN_OK;
+}
+
+DeltaIn delta_in(const DeltaShape& s, const void* q, const void* k, const void* v, const float* log_decay,
+                 const float* beta, float scale, const float* h0, const uint8_t* reset, const int64_t* strides) {
+    const int64_t e = elem_bytes(s.dtype);
+    return DeltaIn{heads_of(q, strides, 0, s.T, s.HK, s.K, e), heads_of(k, strides, 1, s.T, s.HK, s.K, e),
+                   heads_of(v, strides, 2, s.T, s.H, s.V, e),  heads_of(log_decay, strides, 3, s.T, s.H, 1, 4),
+                   heads_of(beta, strides, 4, s.T, s.H, 1, 4), scale, h0, reset};
 }
 
 bool scale_ok(float scale) { return std::isfinite(scale) && scale > 0.0f; }
@@ -1130,6 +1182,78 @@ LRSCAN_API size_t scan_embed_workspace_bytes(int64_t N, int64_t V, int64_t D, in
     if (!dims_ok(N, 1, D) || !dims_ok(V, 1, D) || !dtype_ok(dtype)) return 0;
     const EmbedShape s{N, V, D, 8, dtype};
     return embed_fits(s) ? embed_ws_bytes(s) : 0;
+}
+
+// ---- gated delta rule -------------------------------------------------------------------
+
+LRSCAN_API int scan_delta_fwd(const void* q, const void* k, const void* v, const float* log_decay, const float* beta,
+                              float scale, void* out, float* last, int64_t B, int64_t T, int64_t H, int64_t HK,
+                              int64_t K, int64_t V, int dtype, const int64_t* strides, void* stream,
+                              const lrscan_opts* opts) {
+    if (!q || !k || !v || !log_decay || !beta || (!out && !last)) return LRSCAN_ERR_NULL;
+    DeltaShape s;
+    int rc = delta_shape(B, T, H, HK, K, V, dtype, &s);
+    if (rc != LRSCAN_OK) return rc;
+    if (!std::isfinite(scale) || !head_strides_ok(strides, s)) return LRSCAN_ERR_ARG;
+    if ((rc = delta_opts_ok(opts)) != LRSCAN_OK) return rc;
+    const uint8_t* reset = opts ? opts->reset : nullptr;
+    hipStream_t hs = static_cast<hipStream_t>(stream);
+    void* ws = nullptr;
+    rc = plain_workspace(delta_ws_bytes(s, false, reset != nullptr), opts, hs, &ws);
+    if (rc != LRSCAN_OK) return rc;
+    const DeltaIn in = delta_in(s, q, k, v, log_decay, beta, scale, opts ? opts->h0 : nullptr, reset, strides);
+    return hip_status(launch_delta_fwd(s, in, DeltaFwd{out, last}, ws, hs));
+}
+
+LRSCAN_API int scan_delta_bwd(const void* q, const void* k, const void* v, const float* log_decay, const float* beta,
+                              float scale, const void* grad_out, const float* grad_last, void* grad_q, void* grad_k,
+                              void* grad_v, float* grad_log_decay, float* grad_beta, int64_t B, int64_t T, int64_t H,
+                              int64_t HK, int64_t K, int64_t V, int dtype, const int64_t* strides, void* stream,
+                              const lrscan_opts* opts) {
+    if (!q || !k || !v || !log_decay || !beta || !grad_out || !grad_q || !grad_k || !grad_v || !grad_log_decay ||
+        !grad_beta)
+        return LRSCAN_ERR_NULL;
+    DeltaShape s;
+    int rc = delta_shape(B, T, H, HK, K, V, dtype, &s);
+    if (rc != LRSCAN_OK) return rc;
+    if (!std::isfinite(scale) || !head_strides_ok(strides, s)) return LRSCAN_ERR_ARG;
+    if ((rc = delta_opts_ok(opts)) != LRSCAN_OK) return rc;
+    const uint8_t* reset = opts ? opts->reset : nullptr;
+    hipStream_t hs = static_cast<hipStream_t>(stream);
+    void* ws = nullptr;
+    rc = plain_workspace(delta_ws_bytes(s, true, reset != nullptr), opts, hs, &ws);
+    if (rc != LRSCAN_OK) return rc;
+    const DeltaIn in = delta_in(s, q, k, v, log_decay, beta, scale, opts ? opts->h0 : nullptr, reset, strides);
+    const DeltaBwd p{grad_out, grad_last, grad_q, grad_k, grad_v, grad_log_decay, grad_beta,
+                     opts ? opts->grad_h0 : nullptr};
+    return hip_status(launch_delta_bwd(s, in, p, ws, hs));
+}
+
+LRSCAN_API int scan_delta_step(const void* q, const void* k, const void* v, const float* log_decay, const float* beta,
+                               float scale, const float* state_in, const uint8_t* reset, void* out, float* state_out,
+                               int64_t B, int64_t H, int64_t HK, int64_t K, int64_t V, int dtype,
+                               const int64_t* strides, void* stream) {
+    if (!q || !k || !v || !log_decay || !beta || (!out && !state_out)) return LRSCAN_ERR_NULL;
+    DeltaShape s;
+    const int rc = delta_shape(B, 1, H, HK, K, V, dtype, &s);
+    if (rc != LRSCAN_OK) return rc;
+    int64_t rows[15];
+    for (int i = 0; strides && i < 5; ++i) {
+        rows[3 * i] = strides[2 * i];
+        rows[3 * i + 1] = 0;
+        rows[3 * i + 2] = strides[2 * i + 1];
+    }
+    const int64_t* table = strides ? rows : nullptr;
+    if (!std::isfinite(scale) || !head_strides_ok(table, s)) return LRSCAN_ERR_ARG;
+    const DeltaIn in = delta_in(s, q, k, v, log_decay, beta, scale, state_in, reset, table);
+    return hip_status(launch_delta_step(s, in, DeltaFwd{out, state_out}, static_cast<hipStream_t>(stream)));
+}
+
+LRSCAN_API size_t scan_delta_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t HK, int64_t K, int64_t V,
+                                             int dtype, int backward) {
+    DeltaShape s;
+    if (delta_shape(B, T, H, HK, K, V, dtype, &s) != LRSCAN_OK) return 0;
+    return delta_ws_bytes(s, backward != 0, true);
 }
 
 // ---- the chunked form, step by step ---------------------------------------------

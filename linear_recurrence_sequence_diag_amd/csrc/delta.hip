@@ -1,0 +1,171 @@
+// delta.hip -- gated delta rule: the passes of a call, and the step of one token.
+//
+// Forward: [blocks between resets], prep, walk.  Backward: the same with the
+// entering states kept, the walk back, and the gradients block by block.
+#include "delta_tile.hpp"
+#include "delta_ws.hpp"
+
+namespace lrscan {
+
+using namespace delta;
+
+bool delta_fits(const DeltaShape& s) {
+    if (s.K > kDeltaMaxK || s.V > 65536 || s.H > 65536 || s.T > ((int64_t)1 << 30)) return false;
+    const int64_t slots = (s.T + kC - 1) / kC, groups = (s.V + 15) / 16;
+    const int64_t heads = s.B * s.H;  // B * T * H * V is within 2^40
+    return heads <= ((int64_t)1 << 30) / groups && heads <= ((int64_t)1 << 30) / slots;
+}
+
+size_t delta_ws_bytes(const DeltaShape& s, bool backward, bool reset) { return Layout(s, backward, reset).total; }
+
+namespace {
+
+struct Pass {
+    Blocks blocks;
+    Prep prep;
+    Kept keep;
+};
+
+hipError_t begin(const DeltaShape& s, const DeltaIn& in, bool backward, void* ws, hipStream_t st, Pass* pass) {
+    const Layout l(s, backward, in.reset != nullptr);
+    char* base = static_cast<char*>(ws);
+    auto f = [&](size_t o) { return reinterpret_cast<float*>(base + o); };
+    int* starts = in.reset ? reinterpret_cast<int*>(base + l.starts) : nullptr;
+    int* counts = in.reset ? reinterpret_cast<int*>(base + l.counts) : nullptr;
+    pass->blocks = Blocks{starts, counts, (int)s.T};
+    pass->prep = Prep{f(l.enter), f(l.leave), f(l.gh), f(l.gl), f(l.inv), f(l.att), f(l.att_t), f(l.inv_t)};
+    pass->keep = Kept{f(l.x), f(l.r), f(l.s), f(l.ds), f(l.pq), f(l.pk)};
+    if (in.reset) {
+        const hipError_t e = run_blocks(s, in.reset, starts, counts, st);
+        if (e != hipSuccess) return e;
+    }
+    return run_prep(s, in, pass->blocks, pass->prep, backward, st);
+}
+
+}  // namespace
+
+hipError_t launch_delta_fwd(const DeltaShape& s, const DeltaIn& in, const DeltaFwd& p, void* ws, hipStream_t st) {
+    Pass pass;
+    const hipError_t e = begin(s, in, false, ws, st, &pass);
+    if (e != hipSuccess) return e;
+    return run_walk(s, in, pass.blocks, pass.prep, p, nullptr, st);
+}
+
+hipError_t launch_delta_bwd(const DeltaShape& s, const DeltaIn& in, const DeltaBwd& p, void* ws, hipStream_t st) {
+    Pass pass;
+    hipError_t e = begin(s, in, true, ws, st, &pass);
+    if (e != hipSuccess) return e;
+    e = run_walk(s, in, pass.blocks, pass.prep, DeltaFwd{nullptr, nullptr}, &pass.keep, st);
+    if (e != hipSuccess) return e;
+    e = run_walk_back(s, in, pass.blocks, pass.prep, p, pass.keep, st);
+    if (e != hipSuccess) return e;
+    return run_grads(s, in, pass.blocks, pass.prep, p, pass.keep, st);
+}
+
+// ---- one token ----
+//
+// S' = a S + k u^T with u = beta (v - a S^T k), o = scale S'^T q, of which
+// S^T k, S^T q and q.k are sums over one pass of S: o = scale (a S^T q + (q.k) u).
+// A workgroup has COLS columns of a head; its threads hold CV columns of every
+// RG-th row in registers between the sums and the update.  Bytes of the state
+// bound it.  Every thread writes the elements that it read, so the new state may
+// replace the old one.
+namespace delta {
+
+template <int DT, int COLS, int CV>
+__global__ void __launch_bounds__(kThreads) delta_step(DeltaShape s, DeltaIn in, DeltaFwd p, int groups) {
+    constexpr int CG = COLS / CV, RG = kThreads / CG, ROWS = kDeltaMaxK / RG;
+    __shared__ float qs[kDeltaMaxK], ks[kDeltaMaxK];
+    __shared__ float sk[RG][COLS], sq[RG][COLS];
+    __shared__ float dots[kThreads / 64];
+    const int64_t bh = blockIdx.x / groups, b = bh / s.H;
+    const int h = (int)(bh % s.H), hk = h / (s.H / s.HK);
+    const int cg = threadIdx.x % CG, rg = threadIdx.x / CG;
+    const int col = (int)(blockIdx.x % groups) * COLS + cg * CV;
+    const float* state = in.reset && in.reset[b] ? nullptr : in.h0;
+    typedef float vec __attribute__((ext_vector_type(CV)));
+    vec S[ROWS];
+    const int64_t base = bh * s.K * s.V + col;
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const int d = i * RG + rg;
+        S[i] = vec(0.0f);
+        if (state && d < s.K && col < s.V) S[i] = *reinterpret_cast<const vec*>(state + base + (int64_t)d * s.V);
+    }
+    float dot = 0.0f;
+    {
+        const int d = threadIdx.x;
+        float q = 0.0f, k = 0.0f;
+        if (d < s.K) q = load1<DT>(in.q.row(b, 0, hk), d), k = load1<DT>(in.k.row(b, 0, hk), d);
+        qs[d] = q, ks[d] = k;
+        dot = q * k;
+    }
+#pragma unroll
+    for (int m = 1; m < 64; m *= 2) dot += __shfl_xor(dot, m);
+    if ((threadIdx.x & 63) == 0) dots[threadIdx.x >> 6] = dot;
+    __syncthreads();
+    vec a = vec(0.0f), q = vec(0.0f);
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const int d = i * RG + rg;
+#pragma unroll
+        for (int c = 0; c < CV; ++c) {
+            a[c] = fmaf(ks[d], S[i][c], a[c]);
+            q[c] = fmaf(qs[d], S[i][c], q[c]);
+        }
+    }
+    *reinterpret_cast<vec*>(&sk[rg][cg * CV]) = a;
+    *reinterpret_cast<vec*>(&sq[rg][cg * CV]) = q;
+    __syncthreads();
+    a = q = vec(0.0f);
+    for (int r = 0; r < RG; ++r) {
+        a += *reinterpret_cast<const vec*>(&sk[r][cg * CV]);
+        if (p.out) q += *reinterpret_cast<const vec*>(&sq[r][cg * CV]);
+    }
+    if (col >= s.V) return;
+    const float decay = expf(*reinterpret_cast<const float*>(in.g.row(b, 0, h)));
+    const float beta = *reinterpret_cast<const float*>(in.beta.row(b, 0, h));
+    const float qk = (dots[0] + dots[1]) + (dots[2] + dots[3]);
+    vec u;
+#pragma unroll
+    for (int c = 0; c < CV; ++c) {
+        const float v = load1<DT>(in.v.row(b, 0, h), col + c);
+        // a state that a segment starts from is zero whatever the decay
+        u[c] = beta * (state ? fmaf(-decay, a[c], v) : v);
+        if (p.out && rg == 0) put1<DT>(p.out, bh * s.V + col + c, in.scale * (state ? fmaf(decay, q[c], qk * u[c]) : qk * u[c]));
+    }
+    if (p.last)
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            const int d = i * RG + rg;
+            if (d < s.K) {
+                vec y;
+#pragma unroll
+                for (int c = 0; c < CV; ++c) y[c] = state ? fmaf(ks[d], u[c], decay * S[i][c]) : ks[d] * u[c];
+                *reinterpret_cast<vec*>(p.last + base + (int64_t)d * s.V) = y;
+            }
+        }
+}
+
+template <int DT, int COLS, int CV>
+hipError_t step(const DeltaShape& s, const DeltaIn& in, const DeltaFwd& p, hipStream_t st) {
+    const int groups = (s.V + COLS - 1) / COLS;
+    delta_step<DT, COLS, CV><<<dim3((unsigned)(s.B * s.H * groups)), kThreads, 0, st>>>(s, in, p, groups);
+    return hipGetLastError();
+}
+
+template <int DT>
+hipError_t step_of(const DeltaShape& s, const DeltaIn& in, const DeltaFwd& p, hipStream_t st) {
+    const bool vec = (reinterpret_cast<uintptr_t>(in.h0) | reinterpret_cast<uintptr_t>(p.last) |
+                      (uintptr_t)(s.V * 4)) % 16 == 0;
+    if (!vec) return step<DT, 64, 1>(s, in, p, st);
+    return step<DT, 64, 4>(s, in, p, st);
+}
+
+}  // namespace delta
+
+hipError_t launch_delta_step(const DeltaShape& s, const DeltaIn& in, const DeltaFwd& p, hipStream_t st) {
+    return s.dtype == DT_BF16 ? step_of<DT_BF16>(s, in, p, st) : step_of<DT_F32>(s, in, p, st);
+}
+
+}  // namespace lrscan

@@ -1,0 +1,239 @@
+// delta_tile.hpp -- device building blocks of the gated delta rule's blocks of
+// tokens (gfx950).
+//
+// Products on the matrix cores.  A fp32 value is the exact sum of three bf16
+// values (8 leading bits of the significand each, cut off, not rounded), so a
+// product of two fp32 operands is six bf16 products of 16x16x32 with fp32 sums
+// (those whose weight is at least 2^-16 of the leading one; what is left out is
+// below 2^-23 of the product), and a product with a bf16 operand is three.  The
+// fp32 matrix instruction has a sixteenth of the bf16 rate, so six are 2.7
+// times as fast, three 5.3 times.  An infinity or NaN gives NaN.
+//
+// Layouts of v_mfma_f32_16x16x32_bf16, lane l, ln = l & 15, lg = l >> 4:
+//   A: row ln, k = 8 lg .. 8 lg + 7      B: column ln, the same k
+//   C: column ln, rows 4 lg .. 4 lg + 3
+// So four values of a lane of C are four consecutive k of a B operand's column:
+// results go to the next product through LDS arrays [column][k].
+#pragma once
+
+#include "device.hpp"
+#include "delta.hpp"
+
+namespace lrscan {
+namespace delta {
+
+constexpr int kC = 64;       // tokens of a block
+constexpr int kThreads = 256;
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+template <int NP>
+struct Frag {
+    u32x4 p[NP];
+};
+
+// bf16 planes that hold a stored element exactly
+template <int DT>
+constexpr int kPlanes = DT == DT_F32 ? 3 : 1;
+
+__device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
+                                                   0, 0, 0);
+}
+
+// c += a b, the small parts first
+template <int NA, int NB>
+__device__ __forceinline__ void mma(f32x4& c, const Frag<NA>& a, const Frag<NB>& b) {
+#pragma unroll
+    for (int s = 2; s >= 0; --s)
+#pragma unroll
+        for (int i = 0; i <= s; ++i)
+            if (i < NA && s - i < NB) c = mfma(a.p[i], b.p[s - i], c);
+}
+
+// the upper halves of two floats, as two bf16
+__device__ __forceinline__ uint32_t uppers(float x0, float x1) {
+    return __builtin_amdgcn_perm(__float_as_uint(x1), __float_as_uint(x0), 0x07060302);
+}
+
+// two floats as three pairs of bf16
+__device__ __forceinline__ void split2(float x0, float x1, uint32_t& h, uint32_t& m, uint32_t& l) {
+    h = uppers(x0, x1);
+    const float r0 = x0 - __uint_as_float(__float_as_uint(x0) & 0xffff0000u);
+    const float r1 = x1 - __uint_as_float(__float_as_uint(x1) & 0xffff0000u);
+    m = uppers(r0, r1);
+    l = uppers(r0 - __uint_as_float(__float_as_uint(r0) & 0xffff0000u),
+               r1 - __uint_as_float(__float_as_uint(r1) & 0xffff0000u));
+}
+
+__device__ __forceinline__ Frag<3> split8(f32x4 a, f32x4 b) {
+    Frag<3> f;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        uint32_t h, m, l;
+        split2(a[2 * j], a[2 * j + 1], h, m, l);
+        f.p[0][j] = h, f.p[1][j] = m, f.p[2][j] = l;
+        split2(b[2 * j], b[2 * j + 1], h, m, l);
+        f.p[0][2 + j] = h, f.p[1][2 + j] = m, f.p[2][2 + j] = l;
+    }
+    return f;
+}
+
+// Four consecutive k of a column, into planes `step` elements apart.
+__device__ __forceinline__ void store_planes(uint16_t* at, int step, f32x4 v) {
+    uint32_t h[2], m[2], l[2];
+    split2(v[0], v[1], h[0], m[0], l[0]);
+    split2(v[2], v[3], h[1], m[1], l[1]);
+    *reinterpret_cast<u32x2*>(at) = u32x2{h[0], h[1]};
+    *reinterpret_cast<u32x2*>(at + step) = u32x2{m[0], m[1]};
+    *reinterpret_cast<u32x2*>(at + 2 * step) = u32x2{l[0], l[1]};
+}
+
+// ---- eight consecutive elements of a row as they lie in memory ----
+template <int DT>
+struct Raw8;
+template <>
+struct Raw8<DT_BF16> {
+    u32x4 w;
+    __device__ __forceinline__ float get(int j) const {
+        return __uint_as_float(j & 1 ? w[j >> 1] & 0xffff0000u : w[j >> 1] << 16);
+    }
+    __device__ __forceinline__ Frag<1> frag() const { return Frag<1>{{w}}; }
+};
+template <>
+struct Raw8<DT_F32> {
+    f32x4 a, b;
+    __device__ __forceinline__ float get(int j) const { return j < 4 ? a[j & 3] : b[j & 3]; }
+    __device__ __forceinline__ Frag<3> frag() const { return split8(a, b); }
+};
+
+// Columns c .. c + 7 of a row of n, zeros past its end or where !ok.  vec: rows
+// are whole aligned vectors (16 bytes).
+__device__ __forceinline__ void load8(Raw8<DT_BF16>& r, const char* row, bool ok, int c, int n, bool vec) {
+    r.w = u32x4{0, 0, 0, 0};
+    if (!ok || c >= n) return;
+    if (vec) {
+        r.w = *reinterpret_cast<const u32x4*>(row + 2 * c);
+        return;
+    }
+    const uint16_t* p = reinterpret_cast<const uint16_t*>(row) + c;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (c + j < n) r.w[j >> 1] |= (uint32_t)p[j] << (16 * (j & 1));
+}
+__device__ __forceinline__ void load8(Raw8<DT_F32>& r, const char* row, bool ok, int c, int n, bool vec) {
+    r.a = r.b = f32x4{0, 0, 0, 0};
+    if (!ok || c >= n) return;
+    const float* p = reinterpret_cast<const float*>(row) + c;
+    if (vec) {
+        r.a = *reinterpret_cast<const f32x4*>(p);
+        if (c + 4 < n) r.b = *reinterpret_cast<const f32x4*>(p + 4);
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (c + j < n) r.a[j] = p[j];
+        if (c + 4 + j < n) r.b[j] = p[4 + j];
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ float load1(const char* row, int c) {
+    return Elem<DT>::load1(row, c);
+}
+
+// One element; neighbouring lanes' parts of a line meet in the L2.
+template <int DT>
+__device__ __forceinline__ void put1(void* base, int64_t i, float x) {
+    if constexpr (DT == DT_F32)
+        reinterpret_cast<float*>(base)[i] = x;
+    else
+        reinterpret_cast<uint16_t*>(base)[i] = f32_to_bf16_bits(x);
+}
+
+// ---- LDS tiles of bf16 planes [NP][rows][stride] ----
+// An A (or B) operand whose row (column) and k run as the tile's rows and columns.
+template <int NP>
+__device__ __forceinline__ Frag<NP> row_frag(const uint16_t* tile, int plane, int stride, int row0, int k0, int lane) {
+    Frag<NP> f;
+    const uint16_t* at = tile + (row0 + (lane & 15)) * stride + k0 + (lane >> 4) * 8;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) f.p[i] = *reinterpret_cast<const u32x4*>(at + i * plane);
+    return f;
+}
+
+// One whose k run down the tile's rows: element [k][row] of the tile, read with
+// the transposing LDS load, in which 16 lanes read four rows of 16 elements and
+// get four rows of one column each.
+template <int NP>
+__device__ __forceinline__ Frag<NP> col_frag(const uint16_t* tile, int plane, int stride, int k0, int col0, int lane) {
+    typedef __attribute__((address_space(3))) s16x4 lds4;
+    Frag<NP> f;
+    const uint16_t* at = tile + (k0 + (lane >> 4) * 8 + (lane >> 2 & 3)) * stride + col0 + (lane & 3) * 4;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(at + i * plane));
+        const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(at + i * plane + 4 * stride));
+        const u32x2 x = __builtin_bit_cast(u32x2, a), y = __builtin_bit_cast(u32x2, b);
+        f.p[i] = u32x4{x[0], x[1], y[0], y[1]};
+    }
+    return f;
+}
+
+template <int NP>
+__device__ __forceinline__ void store_frag(uint16_t* at, int plane, const Frag<NP>& f) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) *reinterpret_cast<u32x4*>(at + i * plane) = f.p[i];
+}
+
+// one element of a tile
+template <int NP>
+__device__ __forceinline__ float element(const uint16_t* at, int plane) {
+    float x = bf16_bits_to_f32(at[0]);
+    if constexpr (NP == 3) x += bf16_bits_to_f32(at[plane]) + bf16_bits_to_f32(at[2 * plane]);
+    return x;
+}
+
+// ---- the blocks of a batch row ----
+// Every block of up to kC tokens lies within one segment, so no product reaches
+// from one segment into another.  Without resets they start at multiples of kC.
+struct Blocks {
+    const int* starts;  // [B][T + 1], the last one T; NULL without resets
+    const int* counts;  // [B]
+    int T;
+    __device__ __forceinline__ int count(int64_t b) const { return starts ? counts[b] : (T + kC - 1) / kC; }
+    __device__ __forceinline__ void at(int64_t b, int c, int& start, int& len) const {
+        if (starts) {
+            const int* p = starts + b * ((int64_t)T + 1) + c;
+            start = p[0];
+            len = p[1] - start;
+        } else {
+            start = c * kC;
+            len = min(kC, T - start);
+        }
+    }
+};
+
+// What prepares the blocks for the walk over them, by token: [B, H, T] and rows of kC.
+struct Prep {
+    float *enter, *leave;  // exp(G_i), exp(G_end - G_i), G the running sum of log_decay in the block
+    float *gh, *gl;        // G in two floats (backward)
+    float *inv, *att;      // rows of (I + N)^-1, N_ij = decay_ij k_i.k_j beta_j (i > j); of decay_ij q_i.k_j
+    float *att_t, *inv_t;  // backward: columns of decay_ij q_i.k_j, and of (I + diag(beta) M)^-1, M = N / beta_j
+};
+
+// the matrix-core product of two small fp32 LDS matrices: one 16x16 tile of A B, depth k
+__device__ __forceinline__ f32x4 mm16(const float* A, int sa, const float* B, int sb, int k, int lane) {
+    f32x4 c = {0, 0, 0, 0};
+    const int ln = lane & 15, lg = lane >> 4;
+    for (int i = 0; i < k; i += 4)
+        c = __builtin_amdgcn_mfma_f32_16x16x4f32(A[ln * sa + i + lg], B[(i + lg) * sb + ln], c, 0, 0, 0);
+    return c;
+}
+
+}  // namespace delta
+}  // namespace lrscan

@@ -1,0 +1,77 @@
+// delta_ws.hpp -- the gated delta rule's scratch and the passes over it
+// (internal to the delta_*.hip files).
+#pragma once
+
+#include "delta_tile.hpp"
+
+namespace lrscan {
+namespace delta {
+
+// States at the blocks' starts: a block that a segment does not start begins 64
+// tokens behind another of its segment, so start / 64 is its own slot; one more
+// for the sequence's end.
+__host__ __device__ __forceinline__ int64_t state_slots(int64_t T) { return T / kC + 2; }
+
+// Byte offsets into a call's workspace.
+struct Layout {
+    size_t starts, counts, enter, leave, gh, gl, inv, att, att_t, inv_t, x, r, s, ds, pq, pk, total;
+    Layout(const DeltaShape& d, bool backward, bool reset) {
+        const size_t tokens = (size_t)d.B * d.H * d.T;
+        size_t at = 0;
+        auto take = [&](size_t& o, size_t bytes, bool wanted) {
+            o = at;
+            if (wanted) at += (bytes + 255) / 256 * 256;
+        };
+        take(starts, (size_t)d.B * (d.T + 1) * 4, reset);
+        take(counts, (size_t)d.B * 4, reset);
+        take(enter, tokens * 4, true);
+        take(leave, tokens * 4, true);
+        take(gh, tokens * 4, backward);
+        take(gl, tokens * 4, backward);
+        take(inv, tokens * kC * 4, true);
+        take(att, tokens * kC * 4, !backward);
+        take(att_t, tokens * kC * 4, backward);
+        take(inv_t, tokens * kC * 4, backward);
+        take(x, tokens * d.V * 4, backward);
+        take(r, tokens * d.V * 4, backward);
+        const size_t state = (size_t)d.B * d.H * state_slots(d.T) * d.K * d.V * 4;
+        take(s, state, backward);
+        take(ds, state, backward);
+        const size_t part = (size_t)d.B * d.T * d.HK * d.K * 4;
+        take(pq, part, backward && d.H > d.HK);
+        take(pk, part, backward && d.H > d.HK);
+        total = at;
+    }
+};
+
+// What the backward keeps between its passes, in fp32.
+struct Kept {
+    float *x, *r;    // [B, H, T, V]: x of the forward, and the gradient of beta (x's right side)
+    float *s, *ds;   // [B, H, slots, K, V]: states that enter blocks, gradients that leave them
+    float *pq, *pk;  // [B, T, HK, K]: sums over the heads that share a query/key head so far
+};
+
+inline bool rows_whole(const HeadRows& r, int width, int bytes) {
+    return (reinterpret_cast<uintptr_t>(r.p) | (uintptr_t)r.sb | (uintptr_t)r.st | (uintptr_t)r.sh |
+            (uintptr_t)(width * bytes)) % 16 == 0;
+}
+inline bool rows_vec(const DeltaShape& s, const DeltaIn& in) {
+    const int bytes = s.dtype == DT_F32 ? 4 : 2;
+    return rows_whole(in.q, s.K, bytes) && rows_whole(in.k, s.K, bytes);
+}
+
+hipError_t run_blocks(const DeltaShape& s, const uint8_t* reset, int* starts, int* counts, hipStream_t st);
+hipError_t run_prep(const DeltaShape& s, const DeltaIn& in, const Blocks& blocks, const Prep& prep, bool backward,
+                    hipStream_t st);
+// The walk over the blocks: outputs and the last state, or (keep) x and the entering states.
+hipError_t run_walk(const DeltaShape& s, const DeltaIn& in, const Blocks& blocks, const Prep& prep,
+                    const DeltaFwd& out, const Kept* keep, hipStream_t st);
+// The walk back: r, grad_v, the gradients that leave blocks, and grad_h0.
+hipError_t run_walk_back(const DeltaShape& s, const DeltaIn& in, const Blocks& blocks, const Prep& prep,
+                         const DeltaBwd& p, const Kept& keep, hipStream_t st);
+// The other gradients, every block by itself.
+hipError_t run_grads(const DeltaShape& s, const DeltaIn& in, const Blocks& blocks, const Prep& prep,
+                     const DeltaBwd& p, const Kept& keep, hipStream_t st);
+
+}  // namespace delta
+}  // namespace lrscan
