@@ -76,7 +76,8 @@ enum {
     LRSCAN_ERR_TOO_BIG = -9,   /* scan_fwd_noalloc: the call needs more scratch than its static
                                   buffer holds */
     LRSCAN_ERR_ARG = -10       /* a scale, stride, tap count, activation or id size is outside
-                                  what the call takes (gated scan, convolution, embedding) */
+                                  what the call takes (gated scan, convolution, embedding, delta
+                                  rule, AdamW, logits) */
 };
 
 /* Bytes of the static device scratch of scan_fwd_noalloc (per device). */
@@ -455,6 +456,63 @@ LRSCAN_API int scan_delta_step(const void* q, const void* k, const void* v, cons
  * without (0 for invalid arguments). */
 LRSCAN_API size_t scan_delta_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t HK, int64_t K,
                                              int64_t V, int dtype, int backward);
+
+/* ------------------------------------------------------------------------
+ * AdamW update of many tensors in place, in few launches:
+ *   g = grad_scale grad,  m <- beta1 m + (1 - beta1) g,  v <- beta2 v + (1 - beta2) g^2,
+ *   w <- w (1 - rate weight_decay)
+ *          - rate / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps).
+ * param and grad hold n elements of `dtype`; the update is in fp32 and rounded
+ * once.  master (of all tensors or of none) holds the weights in fp32: it is
+ * updated and param becomes its rounding.
+ * state_bits 32: exp_avg and exp_avg_sq are m and v in fp32.  state_bits 8: they
+ * are e4m3 codes (OCP, 1 byte) of m and of sqrt(v), for each 256 consecutive
+ * elements times a scale (exp_avg_scale, exp_avg_sq_scale: ceil(n / 256) floats)
+ * that takes the largest magnitude to 448; a root above zero is held as at least
+ * the smallest code above zero.  All zero is a valid first state.  A gradient
+ * that is not finite makes states of its group of 256 not finite.
+ * Tensors lie 16-byte aligned for the fast path, and do not overlap.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+    void* param;
+    const void* grad;
+    float* master;
+    void* exp_avg;
+    void* exp_avg_sq;
+    float* exp_avg_scale;    /* state_bits 8 */
+    float* exp_avg_sq_scale; /* state_bits 8 */
+    int64_t n;
+} lrscan_adamw_tensor;
+/*   tensors: a host array of count descriptors, read before the call returns.
+ *   step: the update's number t, from 1, or with step_dev (device) not NULL what
+ *   that holds when the update runs.  grad_scale: one float on the device, or
+ *   NULL for 1. */
+LRSCAN_API int scan_adamw(const lrscan_adamw_tensor* tensors, int64_t count, int state_bits, double rate,
+                          double beta1, double beta2, double eps, double weight_decay, int64_t step,
+                          const int64_t* step_dev, const float* grad_scale, int dtype, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Adjustment of logits [B, V] before a token is chosen, in this order, in fp32
+ * and rounded once:
+ *   z > 0: z / repetition, else z repetition, for tokens in the row's history;
+ *   z - frequency n - presence, for tokens that occur n > 0 times in its
+ *   answered part;  z + bias for tokens in the row's list (added in order where
+ *   a token stands there twice);  -inf where the token's bit of `allowed` is 0
+ *   (bit v % 32 of word v / 32; a row without any bit set is -inf throughout).
+ * A row's history are the first lengths[b] of its L tokens (NULL: all), of which
+ * the first prompts[b] are the prompt (NULL: none); both are cut to [0, L].
+ * Tokens and list entries outside [0, V) name nothing.
+ * tokens, lengths, prompts and bias_ids are whole numbers of id_bytes (4 or 8).
+ * repetition, presence, frequency [B], bias [B,K] fp32.  Each of the rules may
+ * be NULL.  in_stride, out_stride, token_stride: elements between rows.  out may
+ * be logits itself (with the same stride).
+ * ------------------------------------------------------------------------ */
+LRSCAN_API int scan_logits(const void* logits, int64_t in_stride, void* out, int64_t out_stride,
+                           const void* tokens, int64_t token_stride, int64_t L, const void* lengths,
+                           const void* prompts, const float* repetition, const float* presence,
+                           const float* frequency, const void* bias_ids, const float* bias, int64_t K,
+                           const uint32_t* allowed, int id_bytes, int64_t B, int64_t V, int dtype,
+                           void* stream);
 
 /* Bytes of workspace the call with these arguments needs (0 if none).
  * Returns 0 for invalid arguments. */

@@ -94,6 +94,9 @@ _SIGS = {
                                                                     ctypes.POINTER(Opts)], _INT),
     "scan_delta_step": ([_P] * 5 + [_F32] + [_P] * 4 + [_I64] * 5 + [_INT, _P, _P], _INT),
     "scan_delta_workspace_bytes": ([_I64] * 6 + [_INT, _INT], ctypes.c_size_t),
+    "scan_adamw": ([_P, _I64, _INT] + [ctypes.c_double] * 5 + [_I64, _P, _P, _INT, _P], _INT),
+    "scan_logits": ([_P, _I64, _P, _I64, _P, _I64, _I64] + [_P] * 7 + [_I64, _P, _INT, _I64, _I64,
+                                                                     _INT, _P], _INT),
     "scan_auto_algo": ([_I64, _I64, _I64, _INT, _INT, ctypes.POINTER(_INT), ctypes.POINTER(_INT)],
                        _INT),
     "scan_chunk_summary": ([_P, _P, _P, _P, _I64, _I64, _I64, _INT, _INT, _P], _INT),
@@ -378,6 +381,24 @@ def scan_delta_step(q, k, v, log_decay, beta, scale, state_in, reset, out, state
 
 def scan_delta_workspace_bytes(B, T, H, HK, K, V, dtype, backward):
     return library().scan_delta_workspace_bytes(B, T, H, HK, K, V, dtype, int(backward))
+
+
+def scan_adamw(tensors, count, state_bits, rate, beta1, beta2, eps, weight_decay, step, step_dev,
+               grad_scale, dtype, stream):
+    """``tensors``: address of ``count`` descriptors (lrscan_adamw_tensor: seven
+    pointers and the number of elements, eight bytes each)."""
+    return _check(library().scan_adamw(tensors, count, state_bits, rate, beta1, beta2, eps,
+                                       weight_decay, step, step_dev, grad_scale, dtype, stream),
+                  "scan_adamw")
+
+
+def scan_logits(logits, in_stride, out, out_stride, tokens, token_stride, L, lengths, prompts,
+                repetition, presence, frequency, bias_ids, bias, K, allowed, id_bytes, B, V, dtype,
+                stream):
+    return _check(library().scan_logits(logits, in_stride, out, out_stride, tokens, token_stride, L,
+                                        lengths, prompts, repetition, presence, frequency, bias_ids,
+                                        bias, K, allowed, id_bytes, B, V, dtype, stream),
+                  "scan_logits")
 
 
 # ---------------------------------------------------------------------------
@@ -1108,6 +1129,224 @@ def delta_step(q, k, v, log_decay, beta, state=None, scale=None, reset=None, wit
              _ptr(out), new.data_ptr(), B, H, HK, K, V, dtype_code(q.dtype),
              _head_strides(q, k, v, log_decay, beta))
     return out, new
+
+
+# ---- AdamW ----
+ADAMW_GROUP = 256  # consecutive elements that share the scale of an 8-bit state
+
+
+def adamw_update(params, grads, exp_avgs, exp_avg_sqs, step, rate=1e-3, betas=(0.9, 0.999),
+                 eps=1e-8, weight_decay=1e-2, masters=None, exp_avg_scales=None,
+                 exp_avg_sq_scales=None, grad_scale=None):
+    """AdamW update number ``step`` (an int from 1, or an int64 CUDA tensor of one
+    element) of lists of tensors, in place and in few launches; all tensors are
+    contiguous and on one device, and no two overlap.  Params and grads share one
+    dtype; the update is in float32.  ``masters``: float32 weights that are updated
+    instead, params then being their rounding.  The states are float32 tensors like
+    the params, or float8_e4m3fn ones with ``exp_avg_scales`` and
+    ``exp_avg_sq_scales`` (float32, one for each ADAMW_GROUP elements); the second
+    then holds the root of the mean square.  ``grad_scale``: a float32 CUDA tensor
+    of one element that multiplies the gradients."""
+    torch = _torch()
+    count = len(params)
+    small = exp_avg_scales is not None
+    if count == 0:
+        raise ValueError("params must hold at least one tensor")
+    if small != (exp_avg_sq_scales is not None):
+        raise ValueError("exp_avg_scales and exp_avg_sq_scales go together")
+    lists = [("params", params), ("grads", grads), ("masters", masters), ("exp_avgs", exp_avgs),
+             ("exp_avg_sqs", exp_avg_sqs), ("exp_avg_scales", exp_avg_scales),
+             ("exp_avg_sq_scales", exp_avg_sq_scales)]
+    ref = params[0]
+    if not isinstance(ref, torch.Tensor) or not ref.is_cuda:
+        raise ValueError("params must be CUDA (HIP) tensors")
+    dtype, device = ref.dtype, ref.get_device()
+    state = torch.float8_e4m3fn if small else torch.float32
+    kinds = (dtype, dtype, torch.float32, state, state, torch.float32, torch.float32)
+    flat = [0] * (8 * count)
+    flat[7::8] = sizes = [t.numel() for t in params]
+    groups = [-(-n // ADAMW_GROUP) for n in sizes] if small else sizes
+    for at, ((name, ts), kind) in enumerate(zip(lists, kinds)):
+        if ts is None:
+            continue
+        if len(ts) != count:
+            raise ValueError(f"{name} must hold a tensor for each param")
+        for t, n in zip(ts, groups if at >= 5 else sizes):
+            if t.dtype != kind or t.numel() != n or t.get_device() != device or not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous {kind} tensors of the params' sizes on "
+                                 "their device" + (f" (a scale for each {ADAMW_GROUP} elements)"
+                                                   if at >= 5 else ""))
+        flat[at::8] = ptrs = [t.data_ptr() for t in ts]
+        if at != 1 and len(set(ptrs)) != count:
+            raise ValueError(f"{name} holds a tensor twice")
+    for name, t, kind in (("step", step, torch.int64), ("grad_scale", grad_scale, torch.float32)):
+        if isinstance(t, torch.Tensor) and (t.dtype != kind or t.numel() != 1
+                                            or t.get_device() != device):
+            raise ValueError(f"{name} must be a {kind} tensor of one element on the params' device")
+    on_device = isinstance(step, torch.Tensor)
+    if grad_scale is not None and not isinstance(grad_scale, torch.Tensor):
+        raise ValueError("grad_scale must be a float32 CUDA (HIP) tensor of one element")
+    table = (_I64 * len(flat))(*flat)
+    _enqueue(ref, scan_adamw, ctypes.addressof(table), count, 8 if small else 32, rate, betas[0],
+             betas[1], eps, weight_decay, 0 if on_device else step,
+             step.data_ptr() if on_device else None, _ptr(grad_scale), dtype_code(dtype))
+
+
+def _adamw_class():
+    torch = _torch()
+
+    class AdamW(torch.optim.Optimizer):
+        """AdamW (decoupled weight decay) whose step is ``adamw_update`` on all params of
+        a group that have a gradient.  ``state_bits`` 8 holds the states as e4m3 codes
+        with a scale for each ADAMW_GROUP elements; ``master`` holds float32 weights
+        beside bfloat16 params.  ``step(grad_scale=...)`` multiplies the gradients."""
+
+        def __init__(self, params, rate=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2,
+                     state_bits=32, master=False):
+            if state_bits not in (8, 32):
+                raise ValueError("state_bits must be 8 or 32")
+            super().__init__(params, dict(lr=rate, betas=tuple(betas), eps=eps,
+                                          weight_decay=weight_decay, state_bits=state_bits,
+                                          master=bool(master)))
+
+        def _begin(self, p, group):
+            s = self.state[p]
+            s["step"] = 0
+            if group["state_bits"] == 8:
+                groups = -(-p.numel() // ADAMW_GROUP)
+                for name in ("exp_avg", "exp_avg_sq"):
+                    s[name] = torch.zeros(p.shape, dtype=torch.uint8, device=p.device).view(
+                        torch.float8_e4m3fn)
+                    s[name + "_scale"] = torch.zeros(groups, device=p.device)
+            else:
+                for name in ("exp_avg", "exp_avg_sq"):
+                    s[name] = torch.zeros(p.shape, dtype=torch.float32, device=p.device)
+            if group["master"] and p.dtype != torch.float32:
+                s["master"] = p.detach().float()
+
+        @torch.no_grad()
+        def step(self, closure=None, grad_scale=None):
+            loss = None
+            if closure is not None:
+                with torch.enable_grad():
+                    loss = closure()
+            for group in self.param_groups:
+                alike = {}  # one update takes tensors of one device, dtype and step
+                for p in group["params"]:
+                    if p.grad is None or p.numel() == 0:
+                        continue
+                    if not p.is_contiguous() or p.grad.is_sparse:
+                        raise ValueError("params must be contiguous and their gradients dense")
+                    if not self.state[p]:
+                        self._begin(p, group)
+                    s = self.state[p]
+                    s["step"] += 1
+                    alike.setdefault((p.device, p.dtype, s["step"]), []).append(p)
+                for (_, _, at), ps in alike.items():
+                    states = [self.state[p] for p in ps]
+
+                    def kept(name):
+                        return [s[name] for s in states] if name in states[0] else None
+
+                    adamw_update([p.detach() for p in ps], [p.grad.contiguous() for p in ps],
+                                 kept("exp_avg"), kept("exp_avg_sq"), at, rate=group["lr"],
+                                 betas=group["betas"], eps=group["eps"],
+                                 weight_decay=group["weight_decay"], masters=kept("master"),
+                                 exp_avg_scales=kept("exp_avg_scale"),
+                                 exp_avg_sq_scales=kept("exp_avg_sq_scale"), grad_scale=grad_scale)
+            return loss
+
+        def load_state_dict(self, state_dict):
+            # torch's own casts every state to its param's dtype; these keep theirs
+            super().load_state_dict(state_dict)
+            saved = [i for g in state_dict["param_groups"] for i in g["params"]]
+            for i, p in zip(saved, (p for g in self.param_groups for p in g["params"])):
+                for name, t in state_dict["state"].get(i, {}).items():
+                    if isinstance(t, torch.Tensor):
+                        self.state[p][name] = t.detach().to(p.device, copy=True)
+
+    AdamW.__module__, AdamW.__qualname__ = __name__, "AdamW"
+    return AdamW
+
+
+def __getattr__(name):
+    # the optimizer's class derives from torch's, so it is made on the first use
+    if name == "AdamW":
+        globals()[name] = made = _adamw_class()
+        return made
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
+# ---- logits ----
+def adjust_logits(logits, tokens=None, lengths=None, prompt_lengths=None, repetition=None,
+                  presence=None, frequency=None, bias_ids=None, bias=None, allowed=None, out=None):
+    """Logits [B, V] (rows may be strided) with penalties, biases and a grammar's
+    mask, in this order: tokens of a row's history become z / repetition where
+    z > 0 and z * repetition elsewhere; those in its answered part lose frequency
+    for each time and presence once; tokens in ``bias_ids`` gain ``bias``; tokens
+    whose bit in ``allowed`` is clear become -inf.
+    tokens: int32 or int64 [B, L], a row's history its first ``lengths`` [B]
+    (None: all), the first ``prompt_lengths`` [B] of them the prompt (None: none);
+    repetition, presence, frequency: float32 [B]; bias_ids [B, K] with bias
+    float32 [B, K]; all whole numbers of one type; ids outside [0, V) name
+    nothing.  allowed: int32 [B, ceil(V / 32)], bit v % 32 of word v // 32.
+    ``out``: a tensor like logits that receives the result (may be logits)."""
+    torch = _torch()
+    if (not isinstance(logits, torch.Tensor) or not logits.is_cuda or logits.dim() != 2
+            or (logits.stride(1) != 1 and logits.shape[1] > 1)):
+        raise ValueError("logits must be a CUDA (HIP) [B, V] tensor, contiguous along V")
+    B, V = logits.shape
+    device = logits.get_device()
+
+    def check(name, t, shape, kinds, rows=False):
+        if t is None:
+            return
+        if (not isinstance(t, torch.Tensor) or tuple(t.shape) != shape or t.dtype not in kinds
+                or t.get_device() != device
+                or not (t.is_contiguous() or rows and (t.stride(1) == 1 or shape[1] <= 1))):
+            raise ValueError(f"{name} must be a contiguous {list(shape)} tensor of "
+                             f"{' or '.join(str(k) for k in kinds)} on logits' device")
+
+    whole = (torch.int32, torch.int64)
+    kind = None
+    L = K = 0
+    if tokens is not None:
+        L = tokens.shape[-1] if isinstance(tokens, torch.Tensor) and tokens.dim() == 2 else 0
+        check("tokens", tokens, (B, L), whole, rows=True)
+        kind = tokens.dtype
+    elif any(t is not None for t in (lengths, prompt_lengths, repetition, presence, frequency)):
+        raise ValueError("lengths and penalties need tokens")
+    if (bias_ids is None) != (bias is None):
+        raise ValueError("bias_ids and bias go together")
+    if bias is not None:
+        K = bias.shape[-1] if isinstance(bias, torch.Tensor) and bias.dim() == 2 else 0
+        check("bias_ids", bias_ids, (B, K), whole if kind is None else (kind,))
+        check("bias", bias, (B, K), (torch.float32,))
+        kind = bias_ids.dtype
+    if kind is not None:
+        check("lengths", lengths, (B,), (kind,))
+        check("prompt_lengths", prompt_lengths, (B,), (kind,))
+    for name, t in (("repetition", repetition), ("presence", presence), ("frequency", frequency)):
+        check(name, t, (B,), (torch.float32,))
+    check("allowed", allowed, (B, -(-V // 32)), (torch.int32,))
+    if out is None:
+        out = torch.empty((B, V), device=logits.device, dtype=logits.dtype)
+    else:
+        check("out", out, (B, V), (logits.dtype,), rows=True)
+    if L == 0:
+        tokens = lengths = prompt_lengths = repetition = presence = frequency = None
+    if K == 0:
+        bias_ids = bias = None
+
+    def rows(t):
+        return t.stride(0) if B > 1 else t.shape[1]
+
+    _enqueue(logits, scan_logits, logits.data_ptr(), rows(logits), out.data_ptr(), rows(out),
+             _ptr(tokens), 0 if tokens is None else rows(tokens), L, _ptr(lengths),
+             _ptr(prompt_lengths), _ptr(repetition), _ptr(presence), _ptr(frequency),
+             _ptr(bias_ids), _ptr(bias), K, _ptr(allowed), 4 if kind == torch.int32 else 8, B, V,
+             dtype_code(logits.dtype))
+    return out
 
 
 def n_chunks(T, chunk):

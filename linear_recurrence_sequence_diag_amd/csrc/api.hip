@@ -11,12 +11,14 @@
 #include <vector>
 
 #include "../../include/lrscan.h"
+#include "adamw.hpp"
 #include "conv.hpp"
 #include "delta.hpp"
 #include "device.hpp"
 #include "embed.hpp"
 #include "gated.hpp"
 #include "launch.hpp"
+#include "logits.hpp"
 
 using namespace lrscan;
 
@@ -1254,6 +1256,52 @@ LRSCAN_API size_t scan_delta_workspace_bytes(int64_t B, int64_t T, int64_t H, in
     DeltaShape s;
     if (delta_shape(B, T, H, HK, K, V, dtype, &s) != LRSCAN_OK) return 0;
     return delta_ws_bytes(s, backward != 0, true);
+}
+
+// ---- AdamW ------------------------------------------------------------------------------
+
+LRSCAN_API int scan_adamw(const lrscan_adamw_tensor* tensors, int64_t count, int state_bits, double rate, double beta1,
+                          double beta2, double eps, double weight_decay, int64_t step, const int64_t* step_dev,
+                          const float* grad_scale, int dtype, void* stream) {
+    if (!tensors) return LRSCAN_ERR_NULL;
+    if (count < 1) return LRSCAN_ERR_DIM;
+    if (!dtype_ok(dtype)) return LRSCAN_ERR_DTYPE;
+    if (state_bits != 8 && state_bits != 32) return LRSCAN_ERR_ARG;
+    const bool masters = tensors[0].master != nullptr;
+    for (int64_t i = 0; i < count; ++i) {
+        const lrscan_adamw_tensor& t = tensors[i];
+        if (!t.param || !t.grad || !t.exp_avg || !t.exp_avg_sq || (t.master != nullptr) != masters)
+            return LRSCAN_ERR_NULL;
+        if (state_bits == 8 && (!t.exp_avg_scale || !t.exp_avg_sq_scale)) return LRSCAN_ERR_NULL;
+        if (t.n < 1 || t.n > kMaxElems) return LRSCAN_ERR_DIM;
+    }
+    if (!std::isfinite(rate) || !std::isfinite(weight_decay) || !(eps >= 0.0) || !std::isfinite(eps) ||
+        !(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || (!step_dev && step < 1))
+        return LRSCAN_ERR_ARG;
+    const AdamwArgs a{rate, beta1, beta2, eps, weight_decay, step, step_dev, grad_scale};
+    return hip_status(launch_adamw(tensors, count, dtype, state_bits, masters, a, static_cast<hipStream_t>(stream)));
+}
+
+// ---- logits -----------------------------------------------------------------------------
+
+LRSCAN_API int scan_logits(const void* logits, int64_t in_stride, void* out, int64_t out_stride, const void* tokens,
+                           int64_t token_stride, int64_t L, const void* lengths, const void* prompts,
+                           const float* repetition, const float* presence, const float* frequency,
+                           const void* bias_ids, const float* bias, int64_t K, const uint32_t* allowed, int id_bytes,
+                           int64_t B, int64_t V, int dtype, void* stream) {
+    if (!logits || !out || (bias_ids != nullptr) != (bias != nullptr)) return LRSCAN_ERR_NULL;
+    if (!tokens && (lengths || prompts || repetition || presence || frequency)) return LRSCAN_ERR_NULL;
+    if (!dims_ok(B, 1, V) || (tokens && !dims_ok(B, 1, L)) || (bias && !dims_ok(B, 1, K))) return LRSCAN_ERR_DIM;
+    if (!dtype_ok(dtype)) return LRSCAN_ERR_DTYPE;
+    if ((id_bytes != 4 && id_bytes != 8) || (out == logits && in_stride != out_stride)) return LRSCAN_ERR_ARG;
+    const int64_t strides[3] = {in_stride, out_stride, tokens ? token_stride : 0};
+    for (int i = 0; i < 3; ++i)
+        if (strides[i] < 0 || strides[i] > kMaxElems || (B > 1 && strides[i] > 4 * kMaxElems / B)) return LRSCAN_ERR_ARG;
+    if (B > 1 && out_stride < V) return LRSCAN_ERR_ARG;
+    const LogitsArgs a{logits, out, B, V, in_stride, out_stride, dtype, id_bytes, tokens, tokens ? L : 0, token_stride,
+                       lengths, prompts, repetition, presence, frequency, bias_ids, bias, bias ? K : 0, allowed};
+    if (!logits_fits(a)) return LRSCAN_ERR_DIM;
+    return hip_status(launch_logits(a, static_cast<hipStream_t>(stream)));
 }
 
 // ---- the chunked form, step by step ---------------------------------------------
