@@ -472,7 +472,7 @@ int plain_workspace(size_t need, const lrscan_opts* o, hipStream_t st, void** ou
 // contiguous [B, T, heads, width].
 HeadRows heads_of(const void* p, const int64_t* strides, int i, int64_t T, int64_t heads, int64_t width, int64_t bytes) {
     const int64_t sb = strides ? strides[3 * i] : T * heads * width;
-    const int64_t st = strides ? strides[3 * i + 1] : heads * width;
+    const int64_t st = strides && T > 1 ? strides[3 * i + 1] : heads * width;  // of one step there is no distance
     const int64_t sh = strides ? strides[3 * i + 2] : width;
     return HeadRows{static_cast<char*>(const_cast<void*>(p)), sb * bytes, st * bytes, sh * bytes};
 }
@@ -1200,10 +1200,10 @@ LRSCAN_API int scan_delta_fwd(const void* q, const void* k, const void* v, const
     if ((rc = delta_opts_ok(opts)) != LRSCAN_OK) return rc;
     const uint8_t* reset = opts ? opts->reset : nullptr;
     hipStream_t hs = static_cast<hipStream_t>(stream);
-    void* ws = nullptr;
-    rc = plain_workspace(delta_ws_bytes(s, false, reset != nullptr), opts, hs, &ws);
-    if (rc != LRSCAN_OK) return rc;
     const DeltaIn in = delta_in(s, q, k, v, log_decay, beta, scale, opts ? opts->h0 : nullptr, reset, strides);
+    void* ws = nullptr;
+    rc = plain_workspace(delta_ws_bytes(s, &in, nullptr, false), opts, hs, &ws);
+    if (rc != LRSCAN_OK) return rc;
     return hip_status(launch_delta_fwd(s, in, DeltaFwd{out, last}, ws, hs));
 }
 
@@ -1222,10 +1222,10 @@ LRSCAN_API int scan_delta_bwd(const void* q, const void* k, const void* v, const
     if ((rc = delta_opts_ok(opts)) != LRSCAN_OK) return rc;
     const uint8_t* reset = opts ? opts->reset : nullptr;
     hipStream_t hs = static_cast<hipStream_t>(stream);
-    void* ws = nullptr;
-    rc = plain_workspace(delta_ws_bytes(s, true, reset != nullptr), opts, hs, &ws);
-    if (rc != LRSCAN_OK) return rc;
     const DeltaIn in = delta_in(s, q, k, v, log_decay, beta, scale, opts ? opts->h0 : nullptr, reset, strides);
+    void* ws = nullptr;
+    rc = plain_workspace(delta_ws_bytes(s, &in, grad_out, true), opts, hs, &ws);
+    if (rc != LRSCAN_OK) return rc;
     const DeltaBwd p{grad_out, grad_last, grad_q, grad_k, grad_v, grad_log_decay, grad_beta,
                      opts ? opts->grad_h0 : nullptr};
     return hip_status(launch_delta_bwd(s, in, p, ws, hs));
@@ -1255,7 +1255,7 @@ LRSCAN_API size_t scan_delta_workspace_bytes(int64_t B, int64_t T, int64_t H, in
                                              int dtype, int backward) {
     DeltaShape s;
     if (delta_shape(B, T, H, HK, K, V, dtype, &s) != LRSCAN_OK) return 0;
-    return delta_ws_bytes(s, backward != 0, true);
+    return delta_ws_bytes(s, nullptr, nullptr, backward != 0);
 }
 
 // ---- AdamW ------------------------------------------------------------------------------

@@ -9,6 +9,21 @@ namespace lrscan {
 
 using namespace delta;
 
+namespace {
+
+HeadRows contiguous(const DeltaShape& s, const void* p, int64_t heads, int width) {
+    const int64_t sh = (int64_t)width * (s.dtype == DT_F32 ? 4 : 2);
+    return HeadRows{static_cast<char*>(const_cast<void*>(p)), s.T * heads * sh, heads * sh, sh};
+}
+
+Copies copies(const DeltaShape& s, const DeltaIn& in, const void* grad_out) {
+    const int e = s.dtype == DT_F32 ? 4 : 2;
+    return Copies{!rows_whole(in.q, s.K, e), !rows_whole(in.k, s.K, e), !rows_whole(in.v, s.V, e),
+                  grad_out && !rows_whole(contiguous(s, grad_out, s.H, s.V), s.V, e)};
+}
+
+}  // namespace
+
 bool delta_fits(const DeltaShape& s) {
     if (s.K > kDeltaMaxK || s.V > 65536 || s.H > 65536 || s.T > ((int64_t)1 << 30)) return false;
     const int64_t slots = (s.T + kC - 1) / kC, groups = (s.V + 15) / 16;
@@ -16,51 +31,98 @@ bool delta_fits(const DeltaShape& s) {
     return heads <= ((int64_t)1 << 30) / groups && heads <= ((int64_t)1 << 30) / slots;
 }
 
-size_t delta_ws_bytes(const DeltaShape& s, bool backward, bool reset) { return Layout(s, backward, reset).total; }
+size_t delta_ws_bytes(const DeltaShape& s, const DeltaIn* in, const void* grad_out, bool backward) {
+    if (!in) return Layout(s, backward, true, Copies{true, true, true, true}).total;
+    return Layout(s, backward, in->reset != nullptr, copies(s, *in, grad_out)).total;
+}
 
 namespace {
 
 struct Pass {
+    DeltaIn in;
+    HeadRows go;
     Blocks blocks;
     Prep prep;
     Kept keep;
 };
 
-hipError_t begin(const DeltaShape& s, const DeltaIn& in, bool backward, void* ws, hipStream_t st, Pass* pass) {
-    const Layout l(s, backward, in.reset != nullptr);
+hipError_t begin(const DeltaShape& s, const DeltaIn& in, const void* grad_out, void* ws, hipStream_t st, Pass* pass) {
+    const bool backward = grad_out != nullptr;
+    const Copies copy = copies(s, in, grad_out);
+    const Layout l(s, backward, in.reset != nullptr, copy);
     char* base = static_cast<char*>(ws);
     auto f = [&](size_t o) { return reinterpret_cast<float*>(base + o); };
+    auto planes = [&](size_t o) { return reinterpret_cast<uint16_t*>(base + o); };
     int* starts = in.reset ? reinterpret_cast<int*>(base + l.starts) : nullptr;
     int* counts = in.reset ? reinterpret_cast<int*>(base + l.counts) : nullptr;
+    pass->in = in;
     pass->blocks = Blocks{starts, counts, (int)s.T};
-    pass->prep = Prep{f(l.enter), f(l.leave), f(l.gh), f(l.gl), f(l.inv), f(l.att), f(l.att_t), f(l.inv_t)};
+    pass->prep = Prep{f(l.enter), f(l.leave), f(l.gh), f(l.gl), planes(l.inv), planes(l.att), planes(l.att_t),
+                      planes(l.inv_t)};
     pass->keep = Kept{f(l.x), f(l.r), f(l.s), f(l.ds), f(l.pq), f(l.pk)};
-    if (in.reset) {
-        const hipError_t e = run_blocks(s, in.reset, starts, counts, st);
-        if (e != hipSuccess) return e;
+    auto whole = [&](HeadRows* rows, bool wanted, size_t o, int64_t heads, int n) {
+        if (!wanted) return hipSuccess;
+        const hipError_t e = run_copy(*rows, base + o, s.B, s.T, heads, n, s.dtype, st);
+        *rows = contiguous(s, base + o, heads, row_width(n, s.dtype));
+        return e;
+    };
+    hipError_t e = whole(&pass->in.q, copy.q, l.q, s.HK, s.K);
+    if (e == hipSuccess) e = whole(&pass->in.k, copy.k, l.k, s.HK, s.K);
+    if (e == hipSuccess) e = whole(&pass->in.v, copy.v, l.v, s.H, s.V);
+    if (backward) {
+        pass->go = contiguous(s, grad_out, s.H, s.V);
+        if (e == hipSuccess) e = whole(&pass->go, copy.go, l.go, s.H, s.V);
     }
-    return run_prep(s, in, pass->blocks, pass->prep, backward, st);
+    if (e == hipSuccess && in.reset) e = run_blocks(s, in.reset, starts, counts, st);
+    if (e != hipSuccess) return e;
+    return run_prep(s, pass->in, pass->blocks, pass->prep, backward, st);
 }
 
 }  // namespace
 
 hipError_t launch_delta_fwd(const DeltaShape& s, const DeltaIn& in, const DeltaFwd& p, void* ws, hipStream_t st) {
     Pass pass;
-    const hipError_t e = begin(s, in, false, ws, st, &pass);
+    const hipError_t e = begin(s, in, nullptr, ws, st, &pass);
     if (e != hipSuccess) return e;
-    return run_walk(s, in, pass.blocks, pass.prep, p, nullptr, st);
+    return run_walk(s, pass.in, pass.blocks, pass.prep, p, nullptr, st);
 }
 
 hipError_t launch_delta_bwd(const DeltaShape& s, const DeltaIn& in, const DeltaBwd& p, void* ws, hipStream_t st) {
     Pass pass;
-    hipError_t e = begin(s, in, true, ws, st, &pass);
+    hipError_t e = begin(s, in, p.grad_out, ws, st, &pass);
     if (e != hipSuccess) return e;
-    e = run_walk(s, in, pass.blocks, pass.prep, DeltaFwd{nullptr, nullptr}, &pass.keep, st);
+    e = run_walk(s, pass.in, pass.blocks, pass.prep, DeltaFwd{nullptr, nullptr}, &pass.keep, st);
     if (e != hipSuccess) return e;
-    e = run_walk_back(s, in, pass.blocks, pass.prep, p, pass.keep, st);
+    e = run_walk_back(s, pass.in, pass.blocks, pass.prep, p, pass.go, pass.keep, st);
     if (e != hipSuccess) return e;
-    return run_grads(s, in, pass.blocks, pass.prep, p, pass.keep, st);
+    return run_grads(s, pass.in, pass.blocks, pass.prep, p, pass.go, pass.keep, st);
 }
+
+namespace delta {
+
+template <class E>
+__global__ void __launch_bounds__(kThreads) delta_copy(HeadRows from, E* to, int64_t T, int64_t heads, int n, int width,
+                                                       int64_t total) {
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThreads) {
+        const int64_t row = i / width;
+        const int c = (int)(i - row * width);
+        const int64_t h = row % heads, t = row / heads % T, b = row / heads / T;
+        to[i] = c < n ? reinterpret_cast<const E*>(from.row(b, t, h))[c] : E(0);
+    }
+}
+
+hipError_t run_copy(const HeadRows& from, void* to, int64_t B, int64_t T, int64_t heads, int n, int dtype, hipStream_t st) {
+    const int width = row_width(n, dtype);
+    const int64_t total = B * T * heads * width, blocks = (total + kThreads - 1) / kThreads;
+    const dim3 grid((unsigned)(blocks < 16384 ? blocks : 16384));
+    if (dtype == DT_F32)
+        delta_copy<uint32_t><<<grid, kThreads, 0, st>>>(from, static_cast<uint32_t*>(to), T, heads, n, width, total);
+    else
+        delta_copy<uint16_t><<<grid, kThreads, 0, st>>>(from, static_cast<uint16_t*>(to), T, heads, n, width, total);
+    return hipGetLastError();
+}
+
+}  // namespace delta
 
 // ---- one token ----
 //

@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(kScanThreads) delta_blocks(const uint8_t* rese
         int at = carry[1] + total - n;
 #pragma unroll
         for (int j = 0; j < kScanTokens; ++j)
-            if (first >> j & 1) starts[at++] = (int)(mine + j);
+            if (first >> j & 1) starts[at++] = (int)(mine + j) | (marks >> j & 1 ? kCut : 0);
         __syncthreads();
         if (threadIdx.x == kScanThreads - 1) {
             carry[0] = max(carry[0], upto);
@@ -86,18 +86,26 @@ __global__ void __launch_bounds__(kScanThreads) delta_blocks(const uint8_t* rese
 constexpr int kS = kC + 4;  // floats of an LDS row
 
 template <int DT, bool BWD>
-__global__ void __launch_bounds__(kThreads) delta_prep(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, bool vec,
-                                                       int slots) {
+__global__ void __launch_bounds__(kThreads) delta_prep(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, int slots,
+                                                       int width) {
     constexpr int NP = kPlanes<DT>;
-    __shared__ __attribute__((aligned(16))) float N[kC * kS], M[BWD ? kC * kS : 4], Ti[kC * kS], tmp[32 * kS];
+    // 128 columns (fp32: 64) of K and Q at a time, then the block's matrices
+    constexpr int kW = DT == DT_F32 ? 64 : 128, kKS = kW + 8, kPlane = kC * kKS;
+    constexpr int kTile = 2 * NP * kPlane * 2, kMats = 3 * kC * kS * 4;
+    __shared__ __attribute__((aligned(16))) char lds[kTile > kMats ? kTile : kMats];
     __shared__ float gh[kC], gl[kC], bt[kC];
+    uint16_t* const tile = reinterpret_cast<uint16_t*>(lds);
+    float* const N = reinterpret_cast<float*>(lds);
+    float *const M = N + kC * kS, *const Ti = M + kC * kS;  // M: the outputs' weights, forward
+    float* const tmp = Ti + 32;  // the inverse's upper right quarter, which nothing reads
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, ln = lane & 15, lg = lane >> 4;
     const int64_t bh = blockIdx.x / slots, b = bh / s.H;
     const int h = (int)(bh % s.H), hk = h / (s.H / s.HK);
     const int n = blocks.count(b);
     for (int c = blockIdx.x % slots; c < n; c += slots) {
         int start, len;
-        blocks.at(b, c, start, len);
+        bool cut;
+        blocks.at(b, c, start, len, cut);
         __syncthreads();  // the last block's LDS is read
         if (w == 0) {
             const bool ok = lane < len;
@@ -120,30 +128,42 @@ __global__ void __launch_bounds__(kThreads) delta_prep(DeltaShape s, DeltaIn in,
                 if (BWD) prep.gh[at] = hi, prep.gl[at] = lo;
             }
         }
-        for (int i = threadIdx.x; i < kC * kS; i += kThreads) Ti[i] = 0.0f;
-
+        const Buffer krows = block_rows(in.k, b, hk, start, len), qrows = block_rows(in.q, b, hk, start, len);
         // K K^T and Q K^T: a wavefront's 16 rows against the tokens up to them
         f32x4 kk[4], qk[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) kk[j] = qk[j] = f32x4{0, 0, 0, 0};
-        const int row = w * 16 + ln;
-        for (int k0 = 0; k0 < s.K; k0 += 32) {
-            Raw8<DT> ka, qa;
-            load8(ka, in.k.row(b, start + row, hk), row < len, k0 + lg * 8, s.K, vec);
-            load8(qa, in.q.row(b, start + row, hk), row < len, k0 + lg * 8, s.K, vec);
-            const Frag<NP> kf = ka.frag(), qf = qa.frag();
+        for (int k0 = 0; k0 < s.K; k0 += kW) {
+            Raw8<DT> ka[kW / 32], qa[kW / 32];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (j <= w) {
-                    Raw8<DT> kb;
-                    const int r = j * 16 + ln;
-                    load8(kb, in.k.row(b, start + r, hk), r < len, k0 + lg * 8, s.K, vec);
-                    const Frag<NP> bf = kb.frag();
-                    mma(kk[j], kf, bf);
-                    mma(qk[j], qf, bf);
-                }
+            for (int i = 0; i < kW / 32; ++i) {
+                const int o = i * kThreads + threadIdx.x, r = o / (kW / 8), q = k0 + o % (kW / 8) * 8;
+                ka[i].load(krows, r * (int)in.k.st, q, width);
+                qa[i].load(qrows, r * (int)in.q.st, q, width);
+            }
+            if (k0) __syncthreads();
+#pragma unroll
+            for (int i = 0; i < kW / 32; ++i) {
+                const int o = i * kThreads + threadIdx.x, at = o / (kW / 8) * kKS + o % (kW / 8) * 8;
+                store_frag(tile + at, kPlane, ka[i].frag());
+                store_frag(tile + NP * kPlane + at, kPlane, qa[i].frag());
+            }
+            __syncthreads();
+#pragma unroll
+            for (int ks = 0; ks < kW; ks += 32) {
+                const Frag<NP> kf = row_frag<NP>(tile, kPlane, kKS, w * 16, ks, lane);
+                const Frag<NP> qf = row_frag<NP>(tile + NP * kPlane, kPlane, kKS, w * 16, ks, lane);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (j <= w) {
+                        const Frag<NP> bf = row_frag<NP>(tile, kPlane, kKS, j * 16, ks, lane);
+                        mma(kk[j], kf, bf);
+                        mma(qk[j], qf, bf);
+                    }
+            }
         }
-        __syncthreads();
+        __syncthreads();  // the tiles are read
+        for (int i = threadIdx.x; i < kC * kS; i += kThreads) Ti[i] = 0.0f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int col = j * 16 + ln;
@@ -160,11 +180,15 @@ __global__ void __launch_bounds__(kThreads) delta_prep(DeltaShape s, DeltaIn in,
                 N[i * kS + col] = m * bt[col];
                 if (BWD) M[i * kS + col] = m;
                 back[r] = a;
-                // rows 0 .. 31 are read up to column 31
-                if (!BWD && i < len && (j < 2 || w >= 2)) prep.att[(bh * s.T + start + i) * kC + col] = a;
             }
-            if (BWD && col < len && (j < 2 || w >= 2))
-                *reinterpret_cast<f32x4*>(prep.att_t + (bh * s.T + start + col) * kC + w * 16 + lg * 4) = back;
+            // rows (columns of the transposed ones) 0 .. 31 have nothing to read beyond (before) 32
+            if (BWD) {
+                if (col < len && (j < 2 || w >= 2))
+                    store_planes<3>(prep.att_t + ((bh * s.T + start + col) * 3) * kC + w * 16 + lg * 4, kC, back);
+            } else {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) M[(w * 16 + lg * 4 + r) * kS + col] = back[r];
+            }
         }
         __syncthreads();
 
@@ -212,12 +236,23 @@ __global__ void __launch_bounds__(kThreads) delta_prep(DeltaShape s, DeltaIn in,
         }
         __syncthreads();
 
-        // rows of the inverse
-        for (int i = threadIdx.x; i < kC * 16; i += kThreads) {
-            const int r = i >> 4, q = (i & 15) * 4;
-            if (r < len && (r >= 32 || q < 32))
-                *reinterpret_cast<f32x4*>(prep.inv + (bh * s.T + start + r) * kC + q) =
-                    *reinterpret_cast<const f32x4*>(Ti + r * kS + q);
+        // rows of the inverse and of the outputs' weights
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int o = i * kThreads + threadIdx.x, r = o >> 3, q = (o & 7) * 8;
+            if (r < len && (r >= 32 || q < 32)) {
+                const float* at = Ti + r * kS + q;
+                store_frag(prep.inv + (bh * s.T + start + r) * 3 * kC + q, kC,
+                           split8(*reinterpret_cast<const f32x4*>(at), *reinterpret_cast<const f32x4*>(at + 4)));
+                if (!BWD) {
+                    constexpr int NA = kAttPlanes<DT>;
+                    at = M + r * kS + q;
+                    const Frag<3> f = split8(*reinterpret_cast<const f32x4*>(at), *reinterpret_cast<const f32x4*>(at + 4));
+#pragma unroll
+                    for (int n_ = 0; n_ < NA; ++n_)
+                        *reinterpret_cast<u32x4*>(prep.att + ((bh * s.T + start + r) * NA + n_) * kC + q) = f.p[n_];
+                }
+            }
         }
         if (BWD) {
             // (I + diag(beta) M)^-1 = I - diag(beta) (I + N)^-1 M, its columns
@@ -232,7 +267,7 @@ __global__ void __launch_bounds__(kThreads) delta_prep(DeltaShape s, DeltaIn in,
                     y[r] = (i == col ? 1.0f : 0.0f) - bt[i] * y[r];
                 }
                 if (col < len && (j < 2 || w >= 2))
-                    *reinterpret_cast<f32x4*>(prep.inv_t + (bh * s.T + start + col) * kC + w * 16 + lg * 4) = y;
+                    store_planes<3>(prep.inv_t + (bh * s.T + start + col) * 3 * kC + w * 16 + lg * 4, kC, y);
             }
         }
     }
@@ -247,17 +282,17 @@ hipError_t run_prep(const DeltaShape& s, const DeltaIn& in, const Blocks& blocks
                     hipStream_t st) {
     const int slots = (int)((s.T + kC - 1) / kC);
     const dim3 grid((unsigned)(s.B * s.H * slots)), block(kThreads);
-    const bool vec = rows_vec(s, in);
+    const int width = row_width(s.K, s.dtype);
     if (s.dtype == DT_BF16) {
         if (backward)
-            delta_prep<DT_BF16, true><<<grid, block, 0, st>>>(s, in, blocks, prep, vec, slots);
+            delta_prep<DT_BF16, true><<<grid, block, 0, st>>>(s, in, blocks, prep, slots, width);
         else
-            delta_prep<DT_BF16, false><<<grid, block, 0, st>>>(s, in, blocks, prep, vec, slots);
+            delta_prep<DT_BF16, false><<<grid, block, 0, st>>>(s, in, blocks, prep, slots, width);
     } else {
         if (backward)
-            delta_prep<DT_F32, true><<<grid, block, 0, st>>>(s, in, blocks, prep, vec, slots);
+            delta_prep<DT_F32, true><<<grid, block, 0, st>>>(s, in, blocks, prep, slots, width);
         else
-            delta_prep<DT_F32, false><<<grid, block, 0, st>>>(s, in, blocks, prep, vec, slots);
+            delta_prep<DT_F32, false><<<grid, block, 0, st>>>(s, in, blocks, prep, slots, width);
     }
     return hipGetLastError();
 }

@@ -24,6 +24,7 @@ namespace delta {
 
 constexpr int kC = 64;       // tokens of a block
 constexpr int kThreads = 256;
+constexpr int kCut = (int)0x80000000;
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -83,63 +84,63 @@ __device__ __forceinline__ Frag<3> split8(f32x4 a, f32x4 b) {
     return f;
 }
 
-// Four consecutive k of a column, into planes `step` elements apart.
+// Four consecutive k of a column, into N planes `step` elements apart.
+template <int N = 3>
 __device__ __forceinline__ void store_planes(uint16_t* at, int step, f32x4 v) {
     uint32_t h[2], m[2], l[2];
     split2(v[0], v[1], h[0], m[0], l[0]);
     split2(v[2], v[3], h[1], m[1], l[1]);
     *reinterpret_cast<u32x2*>(at) = u32x2{h[0], h[1]};
     *reinterpret_cast<u32x2*>(at + step) = u32x2{m[0], m[1]};
-    *reinterpret_cast<u32x2*>(at + 2 * step) = u32x2{l[0], l[1]};
+    if (N == 3) *reinterpret_cast<u32x2*>(at + 2 * step) = u32x2{l[0], l[1]};
 }
 
-// ---- eight consecutive elements of a row as they lie in memory ----
+// ---- rows in memory ----
+// A buffer descriptor of `bytes` from p on (p and bytes uniform): loads past the
+// end give zeros and stores past it do nothing, which is how a block's missing
+// tokens, and columns past a row's end (offset kNowhere), are left out.
+typedef __amdgpu_buffer_rsrc_t Buffer;
+constexpr uint32_t kNowhere = 0x80000000u;
+__device__ __forceinline__ Buffer buffer(const void* p, int64_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00020000);
+}
+__device__ __forceinline__ u32x4 load16(Buffer r, uint32_t at, uint32_t more = 0) {
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, at, more, 0));
+}
+__device__ __forceinline__ float load4(Buffer r, uint32_t at, uint32_t more = 0) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, at, more, 0));
+}
+__device__ __forceinline__ void store4(Buffer r, uint32_t at, uint32_t more, float x) {
+    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, x), r, at, more, 0);
+}
+
+// The rows of one head of an operand that belong to a block.  Rows are whole
+// aligned vectors of 16 bytes (others were copied into such).
+__device__ __forceinline__ Buffer block_rows(const HeadRows& rows, int64_t b, int64_t head, int start, int len) {
+    return buffer(rows.row(b, start, head), len * rows.st);
+}
+
+// ---- eight consecutive elements of a row ----
 template <int DT>
 struct Raw8;
 template <>
 struct Raw8<DT_BF16> {
     u32x4 w;
-    __device__ __forceinline__ float get(int j) const {
-        return __uint_as_float(j & 1 ? w[j >> 1] & 0xffff0000u : w[j >> 1] << 16);
-    }
     __device__ __forceinline__ Frag<1> frag() const { return Frag<1>{{w}}; }
+    // columns c .. c + 7 of a row of n at byte `row`
+    __device__ __forceinline__ void load(Buffer r, uint32_t row, int c, int n) {
+        w = load16(r, c < n ? row + 2 * c : kNowhere);
+    }
 };
 template <>
 struct Raw8<DT_F32> {
     f32x4 a, b;
-    __device__ __forceinline__ float get(int j) const { return j < 4 ? a[j & 3] : b[j & 3]; }
     __device__ __forceinline__ Frag<3> frag() const { return split8(a, b); }
+    __device__ __forceinline__ void load(Buffer r, uint32_t row, int c, int n) {
+        a = __builtin_bit_cast(f32x4, load16(r, c < n ? row + 4 * c : kNowhere));
+        b = __builtin_bit_cast(f32x4, load16(r, c + 4 < n ? row + 4 * c + 16 : kNowhere));
+    }
 };
-
-// Columns c .. c + 7 of a row of n, zeros past its end or where !ok.  vec: rows
-// are whole aligned vectors (16 bytes).
-__device__ __forceinline__ void load8(Raw8<DT_BF16>& r, const char* row, bool ok, int c, int n, bool vec) {
-    r.w = u32x4{0, 0, 0, 0};
-    if (!ok || c >= n) return;
-    if (vec) {
-        r.w = *reinterpret_cast<const u32x4*>(row + 2 * c);
-        return;
-    }
-    const uint16_t* p = reinterpret_cast<const uint16_t*>(row) + c;
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        if (c + j < n) r.w[j >> 1] |= (uint32_t)p[j] << (16 * (j & 1));
-}
-__device__ __forceinline__ void load8(Raw8<DT_F32>& r, const char* row, bool ok, int c, int n, bool vec) {
-    r.a = r.b = f32x4{0, 0, 0, 0};
-    if (!ok || c >= n) return;
-    const float* p = reinterpret_cast<const float*>(row) + c;
-    if (vec) {
-        r.a = *reinterpret_cast<const f32x4*>(p);
-        if (c + 4 < n) r.b = *reinterpret_cast<const f32x4*>(p + 4);
-        return;
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        if (c + j < n) r.a[j] = p[j];
-        if (c + 4 + j < n) r.b[j] = p[4 + j];
-    }
-}
 
 template <int DT>
 __device__ __forceinline__ float load1(const char* row, int c) {
@@ -202,18 +203,21 @@ __device__ __forceinline__ float element(const uint16_t* at, int plane) {
 // Every block of up to kC tokens lies within one segment, so no product reaches
 // from one segment into another.  Without resets they start at multiples of kC.
 struct Blocks {
-    const int* starts;  // [B][T + 1], the last one T; NULL without resets
+    const int* starts;  // [B][T + 1], kCut set where a segment starts, the last one T; NULL without resets
     const int* counts;  // [B]
     int T;
     __device__ __forceinline__ int count(int64_t b) const { return starts ? counts[b] : (T + kC - 1) / kC; }
-    __device__ __forceinline__ void at(int64_t b, int c, int& start, int& len) const {
+    // block c, and whether a reset starts it
+    __device__ __forceinline__ void at(int64_t b, int c, int& start, int& len, bool& cut) const {
         if (starts) {
             const int* p = starts + b * ((int64_t)T + 1) + c;
-            start = p[0];
-            len = p[1] - start;
+            cut = p[0] < 0;
+            start = p[0] & ~kCut;
+            len = (p[1] & ~kCut) - start;
         } else {
             start = c * kC;
             len = min(kC, T - start);
+            cut = false;
         }
     }
 };
@@ -222,9 +226,28 @@ struct Blocks {
 struct Prep {
     float *enter, *leave;  // exp(G_i), exp(G_end - G_i), G the running sum of log_decay in the block
     float *gh, *gl;        // G in two floats (backward)
-    float *inv, *att;      // rows of (I + N)^-1, N_ij = decay_ij k_i.k_j beta_j (i > j); of decay_ij q_i.k_j
-    float *att_t, *inv_t;  // backward: columns of decay_ij q_i.k_j, and of (I + diag(beta) M)^-1, M = N / beta_j
+    // rows of kC as bf16 planes, [B, H, T][plane][kC]:
+    uint16_t *inv, *att;      // (I + N)^-1, N_ij = decay_ij k_i.k_j beta_j (i > j); decay_ij q_i.k_j
+    uint16_t *att_t, *inv_t;  // backward: columns of decay_ij q_i.k_j, and of (I + diag(beta) M)^-1, M = N / beta_j
 };
+
+// Planes of the outputs' weights: what goes into a bf16 output is off by 2^-16
+// with two, a hundredth of its rounding.
+template <int DT>
+constexpr int kAttPlanes = DT == DT_F32 ? 3 : 2;
+
+// A fragment of such rows: row r of the block's NP planes each, columns c .. c + 7.
+template <int NP>
+__device__ __forceinline__ Frag<NP> plane_frag(Buffer rows, int r, int c) {
+    Frag<NP> f;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) f.p[i] = load16(rows, r * (NP * kC * 2) + c * 2 + i * (kC * 2));
+    return f;
+}
+template <int NP>
+__device__ __forceinline__ Buffer plane_rows(const uint16_t* p, int64_t t0, int len) {
+    return buffer(p + t0 * (NP * kC), len * (NP * kC * 2));
+}
 
 // the matrix-core product of two small fp32 LDS matrices: one 16x16 tile of A B, depth k
 __device__ __forceinline__ f32x4 mm16(const float* A, int sa, const float* B, int sb, int k, int lane) {

@@ -12,15 +12,34 @@ namespace delta {
 // for the sequence's end.
 __host__ __device__ __forceinline__ int64_t state_slots(int64_t T) { return T / kC + 2; }
 
+// Elements of a row of n that is whole vectors of 16 bytes.
+inline int row_width(int n, int dtype) {
+    const int per = dtype == DT_F32 ? 4 : 8;
+    return (n + per - 1) / per * per;
+}
+// Columns of the scratch rows that the backward keeps.
+__host__ __device__ __forceinline__ int kept_width(int V) { return (V + 7) / 8 * 8; }
+
+// Operands whose rows are not whole aligned vectors, or lie too far apart for
+// 32-bit offsets within a block, are copied into rows that are.
+struct Copies {
+    bool q, k, v, go;
+};
+inline bool rows_whole(const HeadRows& r, int width, int bytes) {
+    return (reinterpret_cast<uintptr_t>(r.p) | (uintptr_t)r.sb | (uintptr_t)r.st | (uintptr_t)r.sh |
+            (uintptr_t)(width * bytes)) % 16 == 0 &&
+           r.st >= width * bytes && r.st <= (1 << 24);
+}
+
 // Byte offsets into a call's workspace.
 struct Layout {
-    size_t starts, counts, enter, leave, gh, gl, inv, att, att_t, inv_t, x, r, s, ds, pq, pk, total;
-    Layout(const DeltaShape& d, bool backward, bool reset) {
-        const size_t tokens = (size_t)d.B * d.H * d.T;
+    size_t starts, counts, enter, leave, gh, gl, inv, att, att_t, inv_t, x, r, s, ds, pq, pk, q, k, v, go, total;
+    Layout(const DeltaShape& d, bool backward, bool reset, const Copies& copy) {
+        const size_t tokens = (size_t)d.B * d.H * d.T, bytes = d.dtype == DT_F32 ? 4 : 2;
         size_t at = 0;
-        auto take = [&](size_t& o, size_t bytes, bool wanted) {
+        auto take = [&](size_t& o, size_t n, bool wanted) {
             o = at;
-            if (wanted) at += (bytes + 255) / 256 * 256;
+            if (wanted) at += (n + 255) / 256 * 256;
         };
         take(starts, (size_t)d.B * (d.T + 1) * 4, reset);
         take(counts, (size_t)d.B * 4, reset);
@@ -28,38 +47,36 @@ struct Layout {
         take(leave, tokens * 4, true);
         take(gh, tokens * 4, backward);
         take(gl, tokens * 4, backward);
-        take(inv, tokens * kC * 4, true);
-        take(att, tokens * kC * 4, !backward);
-        take(att_t, tokens * kC * 4, backward);
-        take(inv_t, tokens * kC * 4, backward);
-        take(x, tokens * d.V * 4, backward);
-        take(r, tokens * d.V * 4, backward);
-        const size_t state = (size_t)d.B * d.H * state_slots(d.T) * d.K * d.V * 4;
+        take(inv, tokens * kC * 6, true);
+        take(att, tokens * kC * (d.dtype == DT_F32 ? 6 : 4), !backward);
+        take(att_t, tokens * kC * 6, backward);
+        take(inv_t, tokens * kC * 6, backward);
+        take(x, tokens * kept_width(d.V) * 4, backward);
+        take(r, tokens * kept_width(d.V) * 4, backward);
+        const size_t state = (size_t)d.B * d.H * state_slots(d.T) * d.K * kept_width(d.V) * 4;
         take(s, state, backward);
         take(ds, state, backward);
         const size_t part = (size_t)d.B * d.T * d.HK * d.K * 4;
         take(pq, part, backward && d.H > d.HK);
         take(pk, part, backward && d.H > d.HK);
+        const size_t kr = (size_t)d.B * d.T * d.HK * row_width(d.K, d.dtype) * bytes, vr = tokens * row_width(d.V, d.dtype) * bytes;
+        take(q, kr, copy.q);
+        take(k, kr, copy.k);
+        take(v, vr, copy.v);
+        take(go, vr, backward && copy.go);
         total = at;
     }
 };
 
-// What the backward keeps between its passes, in fp32.
+// What the backward keeps between its passes, in fp32, in rows of kept_width(V).
 struct Kept {
-    float *x, *r;    // [B, H, T, V]: x of the forward, and the gradient of beta (x's right side)
-    float *s, *ds;   // [B, H, slots, K, V]: states that enter blocks, gradients that leave them
+    float *x, *r;    // [B, H, T]: x of the forward, and the gradient of beta (x's right side)
+    float *s, *ds;   // [B, H, slots, K]: states that enter blocks, gradients that leave them
     float *pq, *pk;  // [B, T, HK, K]: sums over the heads that share a query/key head so far
 };
 
-inline bool rows_whole(const HeadRows& r, int width, int bytes) {
-    return (reinterpret_cast<uintptr_t>(r.p) | (uintptr_t)r.sb | (uintptr_t)r.st | (uintptr_t)r.sh |
-            (uintptr_t)(width * bytes)) % 16 == 0;
-}
-inline bool rows_vec(const DeltaShape& s, const DeltaIn& in) {
-    const int bytes = s.dtype == DT_F32 ? 4 : 2;
-    return rows_whole(in.q, s.K, bytes) && rows_whole(in.k, s.K, bytes);
-}
-
+// Copies rows [B, T, heads, n] into contiguous ones of row_width(n), zeros behind.
+hipError_t run_copy(const HeadRows& from, void* to, int64_t B, int64_t T, int64_t heads, int n, int dtype, hipStream_t st);
 hipError_t run_blocks(const DeltaShape& s, const uint8_t* reset, int* starts, int* counts, hipStream_t st);
 hipError_t run_prep(const DeltaShape& s, const DeltaIn& in, const Blocks& blocks, const Prep& prep, bool backward,
                     hipStream_t st);
@@ -68,10 +85,10 @@ hipError_t run_walk(const DeltaShape& s, const DeltaIn& in, const Blocks& blocks
                     const DeltaFwd& out, const Kept* keep, hipStream_t st);
 // The walk back: r, grad_v, the gradients that leave blocks, and grad_h0.
 hipError_t run_walk_back(const DeltaShape& s, const DeltaIn& in, const Blocks& blocks, const Prep& prep,
-                         const DeltaBwd& p, const Kept& keep, hipStream_t st);
+                         const DeltaBwd& p, const HeadRows& go, const Kept& keep, hipStream_t st);
 // The other gradients, every block by itself.
 hipError_t run_grads(const DeltaShape& s, const DeltaIn& in, const Blocks& blocks, const Prep& prep,
-                     const DeltaBwd& p, const Kept& keep, hipStream_t st);
+                     const DeltaBwd& p, const HeadRows& go, const Kept& keep, hipStream_t st);
 
 }  // namespace delta
 }  // namespace lrscan
