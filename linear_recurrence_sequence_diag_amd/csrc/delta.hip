@@ -26,6 +26,7 @@ Copies copies(const DeltaShape& s, const DeltaIn& in, const void* grad_out) {
 
 bool delta_fits(const DeltaShape& s) {
     if (s.K > kDeltaMaxK || s.V > 65536 || s.H > 65536 || s.T > ((int64_t)1 << 30)) return false;
+    if ((int64_t)s.H * s.V > (1 << 22) || (int64_t)s.HK * s.K > (1 << 22)) return false;  // 32-bit offsets in a block's rows
     const int64_t slots = (s.T + kC - 1) / kC, groups = (s.V + 15) / 16;
     const int64_t heads = s.B * s.H;  // B * T * H * V is within 2^40
     return heads <= ((int64_t)1 << 30) / groups && heads <= ((int64_t)1 << 30) / slots;
@@ -57,7 +58,7 @@ hipError_t begin(const DeltaShape& s, const DeltaIn& in, const void* grad_out, v
     int* counts = in.reset ? reinterpret_cast<int*>(base + l.counts) : nullptr;
     pass->in = in;
     pass->blocks = Blocks{starts, counts, (int)s.T};
-    pass->prep = Prep{f(l.enter), f(l.leave), f(l.gh), f(l.gl), planes(l.inv), planes(l.att), planes(l.att_t),
+    pass->prep = Prep{reinterpret_cast<f32x4*>(base + l.gates), f(l.gl), planes(l.inv), planes(l.att), planes(l.att_t),
                       planes(l.inv_t)};
     pass->keep = Kept{f(l.x), f(l.r), f(l.s), f(l.ds), f(l.pq), f(l.pk)};
     auto whole = [&](HeadRows* rows, bool wanted, size_t o, int64_t heads, int n) {

@@ -37,7 +37,7 @@ __global__ void __launch_bounds__(kWide) delta_grads(DeltaShape s, DeltaIn in, B
     __shared__ __attribute__((aligned(16))) float enter[kC], leave[kC], beta[kC], gh[kC], gl[kC], dg[2 * kC];
     __shared__ float ends[kWide / 64];
     uint16_t *const st = ops, *const dt = ops + 3 * kVPlane, *const kb = ops, *const qb = ops + NP * kTPlane;
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, ln = lane & 15, lg = lane >> 4;
+    const int lane = threadIdx.x & 63, w = wave_number(), ln = lane & 15, lg = lane >> 4;
     const int wt = w & 3, wh = w >> 2;
     const int64_t bk = blockIdx.x / slots, b = bk / s.HK;
     const int hk = (int)(bk % s.HK), share = s.H / s.HK;
@@ -82,13 +82,9 @@ __global__ void __launch_bounds__(kWide) delta_grads(DeltaShape s, DeltaIn in, B
             r.load(rrows, row * kw * 4, lg * 8, kw);
             __syncthreads();
             if (threadIdx.x < kC) {
-                const bool in_ = threadIdx.x < len;
-                const int64_t at = t0 + threadIdx.x;
-                enter[threadIdx.x] = in_ ? prep.enter[at] : 0.0f;
-                leave[threadIdx.x] = in_ ? prep.leave[at] : 0.0f;
-                gh[threadIdx.x] = in_ ? prep.gh[at] : 0.0f;
-                gl[threadIdx.x] = in_ ? prep.gl[at] : 0.0f;
-                beta[threadIdx.x] = in_ ? *reinterpret_cast<const float*>(in.beta.row(b, start + threadIdx.x, h)) : 0.0f;
+                const f32x4 g = __builtin_bit_cast(f32x4, load16(buffer(prep.gates + t0, len * 16), threadIdx.x * 16));
+                enter[threadIdx.x] = g[0], leave[threadIdx.x] = g[1], beta[threadIdx.x] = g[2], gh[threadIdx.x] = g[3];
+                gl[threadIdx.x] = load4(buffer(prep.gl + t0, len * 4), threadIdx.x * 4);
             }
             for (int v0 = 0; v0 < s.V; v0 += 32) {
                 store_planes(st + sr * kVS + sc, kVPlane, xs);

@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kThreads) delta_prep(DeltaShape s, DeltaIn in,
     float* const N = reinterpret_cast<float*>(lds);
     float *const M = N + kC * kS, *const Ti = M + kC * kS;  // M: the outputs' weights, forward
     float* const tmp = Ti + 32;  // the inverse's upper right quarter, which nothing reads
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, ln = lane & 15, lg = lane >> 4;
+    const int lane = threadIdx.x & 63, w = wave_number(), ln = lane & 15, lg = lane >> 4;
     const int64_t bh = blockIdx.x / slots, b = bh / s.H;
     const int h = (int)(bh % s.H), hk = h / (s.H / s.HK);
     const int n = blocks.count(b);
@@ -123,9 +123,8 @@ __global__ void __launch_bounds__(kThreads) delta_prep(DeltaShape s, DeltaIn in,
             gh[lane] = hi, gl[lane] = lo, bt[lane] = beta;
             if (ok) {
                 const int64_t at = bh * s.T + start + lane;
-                prep.enter[at] = expf((float)G);
-                prep.leave[at] = expf((float)(end - G));
-                if (BWD) prep.gh[at] = hi, prep.gl[at] = lo;
+                prep.gates[at] = f32x4{expf((float)G), expf((float)(end - G)), beta, hi};
+                if (BWD) prep.gl[at] = lo;
             }
         }
         const Buffer krows = block_rows(in.k, b, hk, start, len), qrows = block_rows(in.q, b, hk, start, len);

@@ -56,6 +56,18 @@ __device__ __forceinline__ void mma(f32x4& c, const Frag<NA>& a, const Frag<NB>&
             if (i < NA && s - i < NB) c = mfma(a.p[i], b.p[s - i], c);
 }
 
+// c[j] += a b[j], the sums in turn: a product does not wait for the one before
+template <int NA, int NB, int M>
+__device__ __forceinline__ void mma(f32x4 (&c)[M], const Frag<NA>& a, const Frag<NB> (&b)[M]) {
+#pragma unroll
+    for (int s = 2; s >= 0; --s)
+#pragma unroll
+        for (int i = 0; i <= s; ++i)
+            if (i < NA && s - i < NB)
+#pragma unroll
+                for (int j = 0; j < M; ++j) c[j] = mfma(a.p[i], b[j].p[s - i], c[j]);
+}
+
 // the upper halves of two floats, as two bf16
 __device__ __forceinline__ uint32_t uppers(float x0, float x1) {
     return __builtin_amdgcn_perm(__float_as_uint(x1), __float_as_uint(x0), 0x07060302);
@@ -113,6 +125,9 @@ __device__ __forceinline__ float load4(Buffer r, uint32_t at, uint32_t more = 0)
 __device__ __forceinline__ void store4(Buffer r, uint32_t at, uint32_t more, float x) {
     __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, x), r, at, more, 0);
 }
+
+// The wavefront's number in its workgroup, as a scalar.
+__device__ __forceinline__ int wave_number() { return __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)); }
 
 // The rows of one head of an operand that belong to a block.  Rows are whole
 // aligned vectors of 16 bytes (others were copied into such).
@@ -224,8 +239,10 @@ struct Blocks {
 
 // What prepares the blocks for the walk over them, by token: [B, H, T] and rows of kC.
 struct Prep {
-    float *enter, *leave;  // exp(G_i), exp(G_end - G_i), G the running sum of log_decay in the block
-    float *gh, *gl;        // G in two floats (backward)
+    // of a token, with G the running sum of log_decay in the block: exp(G_i), exp(G_end - G_i), beta and
+    // the upper float of G; the lower one (backward)
+    f32x4* gates;
+    float* gl;
     // rows of kC as bf16 planes, [B, H, T][plane][kC]:
     uint16_t *inv, *att;      // (I + N)^-1, N_ij = decay_ij k_i.k_j beta_j (i > j); decay_ij q_i.k_j
     uint16_t *att_t, *inv_t;  // backward: columns of decay_ij q_i.k_j, and of (I + diag(beta) M)^-1, M = N / beta_j
@@ -241,7 +258,7 @@ template <int NP>
 __device__ __forceinline__ Frag<NP> plane_frag(Buffer rows, int r, int c) {
     Frag<NP> f;
 #pragma unroll
-    for (int i = 0; i < NP; ++i) f.p[i] = load16(rows, r * (NP * kC * 2) + c * 2 + i * (kC * 2));
+    for (int i = 0; i < NP; ++i) f.p[i] = load16(rows, r * (NP * kC * 2) + c * 2, i * (kC * 2));
     return f;
 }
 template <int NP>

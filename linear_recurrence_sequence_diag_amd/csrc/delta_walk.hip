@@ -2,14 +2,12 @@
 // carries a head's state, forward and back.
 //
 // One workgroup carries CT * 16 columns of one head's state [K, V] through all
-// blocks of its batch row; the columns are independent.  Its four wavefronts
-// share the columns' tiles of 16 and, of those, the state's rows (held in
-// accumulators) and the block's tokens.  A block's products follow one another,
+// blocks of its batch row; the columns are independent.  A block's products follow
+// one another,
 //   K S -> X = (I + N)^-1 (V - enter K S) -> S' = end S + K^T (leave beta X),
 // and each result becomes the next one's operand through LDS, cut into bf16
-// planes there.  Q S and the outputs' product with U fill in beside them.  What
-// the next block reads from memory is loaded into registers a block ahead, each
-// operand as soon as this block's is used.
+// planes there.  Four wavefronts do nothing but this chain; four more load the
+// operands a block ahead, and take Q S and the outputs' product with U off it.
 #include "delta_tile.hpp"
 #include "delta_ws.hpp"
 
@@ -29,90 +27,135 @@ __device__ __forceinline__ bool my_head(const DeltaShape& s, int groups, int64_t
     return bh < s.B * s.H;
 }
 
-// What a workgroup's wavefronts have of a block: of W columns the tile wc, of the
-// tokens NT tiles of 16 from wr NT on, of the state's rows ND from wr ND on.
+// Eight wavefronts: `chain` ones (0 .. 3) carry the state, `side` ones (4 .. 7)
+// bring the operands into LDS and do what does not wait for the state.  Of a
+// block each has 16 tokens, of the state a chain wavefront 16 ND rows, all W columns.
+constexpr int kWalkThreads = 512;
 template <int RT, int CT>
 struct Share {
-    static constexpr int WR = 4 / CT, NT = 4 / WR, ND = 4 * RT / WR;
+    static constexpr int ND = RT;
     static constexpr int KP = 64 * RT, KS = KP + 8, W = CT * 16, VS = W + 8;
     static constexpr int kKPlane = kC * KS, kSPlane = W * KS, kTPlane = W * kTS;
 };
 
-// The block's gates, [3][kC] in LDS; a thread of the first 64 loads its token's.
+// The block's gates, [3][kC] in LDS, brought by the first 64 side threads.
 struct Gates {
-    float enter, leave, beta;
-    __device__ __forceinline__ void load(const DeltaIn& in, const Prep& prep, int64_t b, int64_t h, int64_t t0, int start,
-                                         int len) {
-        enter = leave = beta = 0.0f;
-        const int i = threadIdx.x;
-        if (i < len) {
-            enter = prep.enter[t0 + i];
-            leave = prep.leave[t0 + i];
-            beta = *reinterpret_cast<const float*>(in.beta.row(b, start + i, h));
-        }
+    f32x4 x;
+    __device__ __forceinline__ void load(const Prep& prep, int64_t t0, int len) {
+        const uint32_t i = threadIdx.x & 255;
+        x = __builtin_bit_cast(f32x4, load16(buffer(prep.gates + t0, len * 16), i < kC ? i * 16 : kNowhere));
     }
     __device__ __forceinline__ void store(float* lds) const {
-        if (threadIdx.x < kC) lds[threadIdx.x] = enter, lds[kC + threadIdx.x] = leave, lds[2 * kC + threadIdx.x] = beta;
+        const int i = threadIdx.x & 255;
+        if (i < kC) lds[i] = x[0], lds[kC + i] = x[1], lds[2 * kC + i] = x[2];
     }
 };
 
-// A tile of a block's kC rows and COLS columns, 8 columns a thread at a time.
+// A tile of a block's kC rows and COLS columns, 8 columns a side thread at a time.
 template <int DT, int COLS>
 struct Tile {
-    static constexpr int N = kC * COLS / 8, PER = (N + kThreads - 1) / kThreads;
+    static constexpr int N = kC * COLS / 8, PER = (N + 255) / 256;
     Raw8<DT> x[PER];
     __device__ __forceinline__ void load(Buffer rows, int64_t st, int c0, int n) {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int o = i * kThreads + threadIdx.x;
+            const int o = i * 256 + (threadIdx.x & 255);
             x[i].load(rows, o / (COLS / 8) * (int)st, c0 + o % (COLS / 8) * 8, n);
         }
     }
     __device__ __forceinline__ void store(uint16_t* tile, int plane, int stride) const {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int o = i * kThreads + threadIdx.x;
-            if (N % kThreads == 0 || o < N) store_frag(tile + o / (COLS / 8) * stride + o % (COLS / 8) * 8, plane, x[i].frag());
+            const int o = i * 256 + (threadIdx.x & 255);
+            if (N % 256 == 0 || o < N) store_frag(tile + o / (COLS / 8) * stride + o % (COLS / 8) * 8, plane, x[i].frag());
         }
     }
 };
 
-// Rows of an [.., H, V] output from LDS elements [kC][stride], 8 columns a thread.
-template <int DT, int COLS>
-__device__ __forceinline__ void store_rows(void* out, const char* lds, int stride, const DeltaShape& s, int64_t b, int h,
-                                           int start, int len, int v0, bool vec) {
-    constexpr int N = kC * COLS / 8, E = Elem<DT>::bytes;
-    for (int o = threadIdx.x; o < N; o += kThreads) {
-        const int r = o / (COLS / 8), q = o % (COLS / 8) * 8;
-        if (r >= len || v0 + q >= s.V) continue;
-        const char* from = lds + (r * stride + q) * E;
-        char* to = static_cast<char*>(out) + (((b * s.T + start + r) * s.H + h) * (int64_t)s.V + v0 + q) * E;
-        if (vec) {
-            *reinterpret_cast<u32x4*>(to) = *reinterpret_cast<const u32x4*>(from);
-            if (E == 4 && v0 + q + 4 < s.V) *reinterpret_cast<u32x4*>(to + 16) = *reinterpret_cast<const u32x4*>(from + 16);
-        } else {
-            for (int j = 0; j < 8 && v0 + q + j < s.V; ++j) {
-                if (E == 4)
-                    reinterpret_cast<uint32_t*>(to)[j] = reinterpret_cast<const uint32_t*>(from)[j];
-                else
-                    reinterpret_cast<uint16_t*>(to)[j] = reinterpret_cast<const uint16_t*>(from)[j];
-            }
-        }
+// A wavefront's 16 rows of a contiguous [B, T, H, V] output, of which this
+// workgroup has COLS columns: from accumulators through `lds` (the wavefront's
+// own, 16 rows of COLS + 8 elements), in whole vectors or element by element.
+template <int DT, int CT, bool WHOLE>
+__device__ __forceinline__ void store_rows(void* out, char* lds, const DeltaShape& s, int64_t b, int h, int start, int len,
+                                           int row0, int v0, const f32x4 (&x)[CT]) {
+    constexpr int E = Elem<DT>::bytes, COLS = CT * 16, ROW = COLS + 8, PER = WHOLE ? 16 / E : 1, N = 16 * COLS / PER;
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int j = 0; j < CT; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) put1<DT>(lds, ((lane >> 4) * 4 + r) * ROW + j * 16 + (lane & 15), x[j][r]);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // one wavefront's LDS accesses keep their order
+    const int64_t step = (int64_t)s.H * s.V * E;
+    const Buffer rows = buffer(static_cast<char*>(out) + (b * s.T + start) * step + (int64_t)h * s.V * E, len * step);
+#pragma unroll
+    for (int i = 0; i < (N + 63) / 64; ++i) {
+        const int o = i * 64 + lane, r = o / (COLS / PER), q = o % (COLS / PER) * PER;
+        const bool ok = N % 64 == 0 || o < N;
+        const uint32_t at = ok && v0 + q < s.V ? (row0 + r) * (int)step + (v0 + q) * E : kNowhere;
+        const char* from = lds + ((ok ? r : 0) * ROW + q) * E;
+        if constexpr (WHOLE)
+            __builtin_amdgcn_raw_buffer_store_b128(*reinterpret_cast<const u32x4*>(from), rows, at, 0, 0);
+        else if constexpr (E == 4)
+            __builtin_amdgcn_raw_buffer_store_b32(*reinterpret_cast<const uint32_t*>(from), rows, at, 0, 0);
+        else
+            __builtin_amdgcn_raw_buffer_store_b16(*reinterpret_cast<const uint16_t*>(from), rows, at, 0, 0);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+}
+
+// A chain wavefront's rows of a state scratch (rows of kw columns), and its
+// tokens' rows of a token scratch; what lies past the rows or columns is left out.
+template <int ND, int CT>
+__device__ __forceinline__ void keep_state(float* to, const DeltaShape& s, int kw, int row0, int v0, int lane,
+                                           const f32x4 (&x)[ND][CT]) {
+    const Buffer rows = buffer(to, (int64_t)s.K * kw * 4);
+#pragma unroll
+    for (int j = 0; j < CT; ++j) {
+        const int col = v0 + j * 16 + (lane & 15);
+        const uint32_t at = col < kw ? (uint32_t)(((row0 + (lane >> 4) * 4) * kw + col) * 4) : kNowhere;
+#pragma unroll
+        for (int i = 0; i < ND; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) store4(rows, at, (i * 16 + r) * kw * 4, x[i][j][r]);
+    }
+}
+template <int CT>
+__device__ __forceinline__ void keep_tokens(float* to, int kw, int len, int row0, int v0, int lane, const f32x4 (&x)[CT]) {
+    const Buffer rows = buffer(to, (int64_t)len * kw * 4);
+#pragma unroll
+    for (int j = 0; j < CT; ++j) {
+        const int col = v0 + j * 16 + (lane & 15);
+        const uint32_t at = col < kw ? (uint32_t)(((row0 + (lane >> 4) * 4) * kw + col) * 4) : kNowhere;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) store4(rows, at, r * kw * 4, x[j][r]);
     }
 }
 
-// Elements of the operands' rows of K and of V, and whether rows of the output are whole vectors.
+// A state [K, V] in or out of accumulators.
+template <int ND, int CT, class F>
+__device__ __forceinline__ void each_state(const DeltaShape& s, int64_t bh, int row0, int v0, int lane, F f) {
+#pragma unroll
+    for (int i = 0; i < ND; ++i)
+#pragma unroll
+        for (int j = 0; j < CT; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int d = row0 + i * 16 + (lane >> 4) * 4 + r, col = v0 + j * 16 + (lane & 15);
+                f(i, j, r, d < s.K && col < s.V, (bh * s.K + d) * s.V + col);
+            }
+}
+
+// Elements of the operands' rows of K and of V.
 struct Widths {
     int k, v;
-    bool out;
 };
 
-template <int DT, int RT, int CT, bool KEEP>
-__global__ void __launch_bounds__(kThreads, DT == DT_BF16 && RT <= 2 ? 2 : 1)
+template <int DT, int RT, int CT, bool KEEP, bool WHOLE>
+__global__ void __launch_bounds__(kWalkThreads, DT == DT_BF16 && RT <= 2 ? 4 : 2)
 delta_walk(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaFwd p, Kept keep, int groups, Widths wd) {
     using Sh = Share<RT, CT>;
     constexpr int NP = kPlanes<DT>, NA = kAttPlanes<DT>;
-    constexpr int NT = Sh::NT, ND = Sh::ND, KP = Sh::KP, KS = Sh::KS, W = Sh::W, VS = Sh::VS;
+    constexpr int ND = Sh::ND, KP = Sh::KP, KS = Sh::KS, W = Sh::W, VS = Sh::VS;
     constexpr int kKPlane = Sh::kKPlane, kSPlane = Sh::kSPlane, kTPlane = Sh::kTPlane;
     constexpr int kU = KEEP ? 0 : NA;  // planes of u beside the three of leave u
     constexpr int kWide = 3 * kSPlane > (kU + 3) * kTPlane ? 3 * kSPlane : (kU + 3) * kTPlane;
@@ -129,203 +172,197 @@ delta_walk(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaFwd p, Kept 
     if (!my_head(s, groups, bh, group)) return;
     const int64_t b = bh / s.H;
     const int h = (int)(bh % s.H), hk = h / (s.H / s.HK);
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, ln = lane & 15, lg = lane >> 4;
-    const int wc = w % CT, wr = w / CT;
-    const int v0 = group * W, col = v0 + wc * 16 + ln;
-
-    f32x4 S[ND];
-#pragma unroll
-    for (int i = 0; i < ND; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int d = (wr * ND + i) * 16 + lg * 4 + r;
-            S[i][r] = in.h0 && d < s.K && col < s.V ? in.h0[(bh * s.K + d) * s.V + col] : 0.0f;
-        }
-
-    // rows of kw columns, of which this lane has one; what lies past the state's rows or columns is left out
-    const int kw = kept_width(s.V);
-    const uint32_t kept_at = col < kw ? (uint32_t)(((wr * ND * 16 + lg * 4) * kw + col) * 4) : kNowhere;
-    auto keep_state = [&](float* to, const f32x4 (&x)[ND]) {
-        const Buffer rows = buffer(to, (int64_t)s.K * kw * 4);
-#pragma unroll
-        for (int i = 0; i < ND; ++i)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) store4(rows, kept_at, (i * 16 + r) * kw * 4, x[i][r]);
-    };
-    const uint32_t kept_x = col < kw ? (uint32_t)(((wr * NT * 16 + lg * 4) * kw + col) * 4) : kNowhere;
-    auto keep_tokens = [&](float* to, int start, int len, const f32x4 (&x)[NT]) {
-        const Buffer rows = buffer(to + (bh * s.T + start) * kw, (int64_t)len * kw * 4);
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) store4(rows, kept_x, (i * 16 + r) * kw * 4, x[i][r]);
-    };
-
-    Tile<DT, KP> kn;
-    Tile<DT, W> vn;
-    Raw8<DT> qn[NT][KP / 32];
-    Frag<3> ti[NT][2];
-    Frag<NA> at[NT][2];
-    Gates gn;
-    auto token = [&](int i) { return (wr * NT + i) * 16 + ln; };
-    auto load_q = [&](int start, int len) {
-        const Buffer rows = block_rows(in.q, b, hk, start, len);
-        if (!KEEP)
-#pragma unroll
-            for (int i = 0; i < NT; ++i)
-#pragma unroll
-                for (int k = 0; k < KP / 32; ++k)
-                    qn[i][k].load(rows, token(i) * (int)in.q.st, k * 32 + lg * 8, wd.k);
-    };
-    // tokens of the lower half of a block reach its first 32 only
-    auto load_inv = [&](int start, int len) {
-        const Buffer rows = plane_rows<3>(prep.inv, bh * s.T + start, len);
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-                if (k == 0 || wr * NT + i >= 2) ti[i][k] = plane_frag<3>(rows, token(i), k * 32 + lg * 8);
-    };
-    auto load_att = [&](int start, int len) {
-        const Buffer rows = plane_rows<NA>(prep.att, bh * s.T + start, len);
-        if (!KEEP)
-#pragma unroll
-            for (int i = 0; i < NT; ++i)
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-                    if (k == 0 || wr * NT + i >= 2) at[i][k] = plane_frag<NA>(rows, token(i), k * 32 + lg * 8);
-    };
-
+    const int lane = threadIdx.x & 63, w = wave_number(), ln = lane & 15, lg = lane >> 4;
+    const int v0 = group * W, wr = w & 3;
+    const int row0 = wr * 16, r0 = row0 + lg * 4;  // tokens of the wavefront, and of the lane in a tile of results
     const int n = blocks.count(b);
     int start, len;
     bool cut;
     blocks.at(b, 0, start, len, cut);
-    kn.load(block_rows(in.k, b, hk, start, len), in.k.st, 0, wd.k);
-    vn.load(block_rows(in.v, b, h, start, len), in.v.st, v0, wd.v);
-    gn.load(in, prep, b, h, bh * s.T + start, start, len);
-    load_q(start, len);
-    load_inv(start, len);
-    load_att(start, len);
-    for (int c = 0; c < n; ++c) {
-        // the next block; past the last one, one without tokens
-        int next = s.T, nlen = 0;
-        bool ncut = false;
-        if (c + 1 < n) blocks.at(b, c + 1, next, nlen, ncut);
-        if (cut) {
+
+    if (w < 4) {
+        const int d0 = wr * ND * 16, kw = kept_width(s.V);
+        f32x4 S[ND][CT];
+        each_state<ND, CT>(s, bh, d0, v0, lane,
+                           [&](int i, int j, int r, bool ok, int64_t at) { S[i][j][r] = in.h0 && ok ? in.h0[at] : 0.0f; });
+        Frag<3> ti[2];
+        // tokens of the lower half of a block reach its first 32 only
+        auto load_inv = [&](int start, int len) {
+            const Buffer rows = plane_rows<3>(prep.inv, bh * s.T + start, len);
+            ti[0] = plane_frag<3>(rows, row0 + ln, lg * 8);
+            if (wr >= 2) ti[1] = plane_frag<3>(rows, row0 + ln, 32 + lg * 8);
+        };
+        load_inv(start, len);
+        for (int c = 0; c < n; ++c) {
+            // the next block; past the last one, one without tokens
+            int next = s.T, nlen = 0;
+            bool ncut = false;
+            if (c + 1 < n) blocks.at(b, c + 1, next, nlen, ncut);
+            if (cut) {
 #pragma unroll
-            for (int i = 0; i < ND; ++i) S[i] = f32x4{0, 0, 0, 0};
-        } else if (KEEP) {
-            keep_state(keep.s + (bh * state_slots(s.T) + start / kC) * s.K * kw, S);
+                for (int i = 0; i < ND; ++i)
+#pragma unroll
+                    for (int j = 0; j < CT; ++j) S[i][j] = f32x4{0, 0, 0, 0};
+            } else if (KEEP) {
+                keep_state<ND, CT>(keep.s + (bh * state_slots(s.T) + start / kC) * s.K * kw, s, kw, d0, v0, lane, S);
+            }
+#pragma unroll
+            for (int i = 0; i < ND; ++i)
+#pragma unroll
+                for (int j = 0; j < CT; ++j)
+                    store_planes(wide + (j * 16 + ln) * KS + d0 + i * 16 + lg * 4, kSPlane, S[i][j]);
+            __syncthreads();  // the operands and the state are in LDS
+
+            f32x4 ks[CT];
+#pragma unroll
+            for (int j = 0; j < CT; ++j) ks[j] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int k = 0; k < KP; k += 32) {
+                Frag<3> sf[CT];
+#pragma unroll
+                for (int j = 0; j < CT; ++j) sf[j] = row_frag<3>(wide, kSPlane, KS, j * 16, k, lane);
+                mma(ks, row_frag<NP>(kt, kKPlane, KS, row0, k, lane), sf);
+            }
+            const f32x4 en = *reinterpret_cast<const f32x4*>(gates + r0);
+            const f32x4 le = *reinterpret_cast<const f32x4*>(gates + kC + r0);
+            const f32x4 be = *reinterpret_cast<const f32x4*>(gates + 2 * kC + r0);
+            const float end = gates[len - 1];
+#pragma unroll
+            for (int j = 0; j < CT; ++j) {
+                f32x4 y;
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    y[r] = fmaf(-en[r], ks[j][r], element<NP>(vt + (r0 + r) * VS + j * 16 + ln, kC * VS));
+                store_planes(rt + (j * 16 + ln) * kTS + r0, kTPlane, y);
+            }
+            __syncthreads();  // the right sides are
+
+            f32x4 x[CT];
+            Frag<3> f[CT];
+#pragma unroll
+            for (int j = 0; j < CT; ++j) {
+                x[j] = f32x4{0, 0, 0, 0};
+                f[j] = row_frag<3>(rt, kTPlane, kTS, j * 16, 0, lane);
+            }
+            mma(x, ti[0], f);
+            if (wr >= 2) {
+#pragma unroll
+                for (int j = 0; j < CT; ++j) f[j] = row_frag<3>(rt, kTPlane, kTS, j * 16, 32, lane);
+                mma(x, ti[1], f);
+            }
+            load_inv(next, nlen);
+#pragma unroll
+            for (int j = 0; j < CT; ++j) {
+                f32x4 u, l;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    u[r] = be[r] * x[j][r];
+                    l[r] = le[r] * u[r];
+                }
+                const int o = (j * 16 + ln) * kTS + r0;
+                if (!KEEP) store_planes<NA>(ut + o, kTPlane, u);
+                store_planes(lt + o, kTPlane, l);
+            }
+            __syncthreads();  // u is
+
+            if (KEEP) keep_tokens<CT>(keep.x + (bh * s.T + start) * kw, kw, len, row0, v0, lane, x);
+#pragma unroll
+            for (int i = 0; i < ND; ++i)
+#pragma unroll
+                for (int j = 0; j < CT; ++j)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) S[i][j][r] *= end;
+#pragma unroll
+            for (int k = 0; k < kC; k += 32) {
+#pragma unroll
+                for (int j = 0; j < CT; ++j) f[j] = row_frag<3>(lt, kTPlane, kTS, j * 16, k, lane);
+#pragma unroll
+                for (int i = 0; i < ND; ++i) mma(S[i], col_frag<NP>(kt, kKPlane, KS, k, d0 + i * 16, lane), f);
+            }
+            __syncthreads();  // and all of it is read
+            start = next, len = nlen, cut = ncut;
         }
+        if (!KEEP && p.last)
+            each_state<ND, CT>(s, bh, d0, v0, lane, [&](int i, int j, int r, bool ok, int64_t at) {
+                if (ok) p.last[at] = S[i][j][r];
+            });
+        return;
+    }
+
+    Tile<DT, KP> kn;
+    Tile<DT, W> vn;
+    Gates gn;
+    Raw8<DT> qn[KP / 32];
+    Frag<NA> at[2];
+    auto load = [&](int start, int len) {
+        kn.load(block_rows(in.k, b, hk, start, len), in.k.st, 0, wd.k);
+        vn.load(block_rows(in.v, b, h, start, len), in.v.st, v0, wd.v);
+        gn.load(prep, bh * s.T + start, len);
+    };
+    auto load_q = [&](int start, int len) {
+        const Buffer rows = block_rows(in.q, b, hk, start, len);
+#pragma unroll
+        for (int k = 0; k < KP / 32; ++k) qn[k].load(rows, (row0 + ln) * (int)in.q.st, k * 32 + lg * 8, wd.k);
+    };
+    auto load_att = [&](int start, int len) {
+        const Buffer rows = plane_rows<NA>(prep.att, bh * s.T + start, len);
+        at[0] = plane_frag<NA>(rows, row0 + ln, lg * 8);
+        if (wr >= 2) at[1] = plane_frag<NA>(rows, row0 + ln, 32 + lg * 8);
+    };
+    load(start, len);
+    if (!KEEP) {
+        load_q(start, len);
+        load_att(start, len);
+    }
+    for (int c = 0; c < n; ++c) {
+        int next = s.T, nlen = 0;
+        if (c + 1 < n) blocks.at(b, c + 1, next, nlen, cut);
         kn.store(kt, kKPlane, KS);
         vn.store(vt, kC * VS, VS);
         gn.store(gates);
-#pragma unroll
-        for (int i = 0; i < ND; ++i)
-            store_planes(wide + (wc * 16 + ln) * KS + (wr * ND + i) * 16 + lg * 4, kSPlane, S[i]);
         __syncthreads();
-        kn.load(block_rows(in.k, b, hk, next, nlen), in.k.st, 0, wd.k);
-        vn.load(block_rows(in.v, b, h, next, nlen), in.v.st, v0, wd.v);
-        gn.load(in, prep, b, h, bh * s.T + next, next, nlen);
-
-        f32x4 ks_[NT], qs[NT];
+        load(next, nlen);
+        f32x4 qs[CT], o[CT];
+        if (!KEEP) {
 #pragma unroll
-        for (int i = 0; i < NT; ++i) ks_[i] = qs[i] = f32x4{0, 0, 0, 0};
+            for (int j = 0; j < CT; ++j) qs[j] = o[j] = f32x4{0, 0, 0, 0};
 #pragma unroll
-        for (int k = 0; k < KP / 32; ++k) {
-            const Frag<3> sf = row_frag<3>(wide, kSPlane, KS, wc * 16, k * 32, lane);
-            Frag<NA> sa;
+            for (int k = 0; k < KP / 32; ++k) {
+                Frag<NA> sf[CT];
 #pragma unroll
-            for (int i = 0; i < NA; ++i) sa.p[i] = sf.p[i];
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                mma(ks_[i], row_frag<NP>(kt, kKPlane, KS, (wr * NT + i) * 16, k * 32, lane), sf);
-                if (!KEEP) mma(qs[i], qn[i][k].frag(), sa);
+                for (int j = 0; j < CT; ++j) sf[j] = row_frag<NA>(wide, kSPlane, KS, j * 16, k * 32, lane);
+                mma(qs, qn[k].frag(), sf);
             }
-        }
-        load_q(next, nlen);
-        f32x4 en[NT], le[NT], be[NT];
+            load_q(next, nlen);
+            const f32x4 en = *reinterpret_cast<const f32x4*>(gates + r0);
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            const int r0 = (wr * NT + i) * 16 + lg * 4;
-            en[i] = *reinterpret_cast<const f32x4*>(gates + r0);
-            le[i] = *reinterpret_cast<const f32x4*>(gates + kC + r0);
-            be[i] = *reinterpret_cast<const f32x4*>(gates + 2 * kC + r0);
-            f32x4 y;
+            for (int j = 0; j < CT; ++j)
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                y[r] = fmaf(-en[i][r], ks_[i][r], element<NP>(vt + (r0 + r) * VS + wc * 16 + ln, kC * VS));
-            store_planes(rt + (wc * 16 + ln) * kTS + r0, kTPlane, y);
-        }
-        const float end = gates[len - 1];
-        __syncthreads();
-
-        f32x4 x[NT];
-        {
-            const Frag<3> y0 = row_frag<3>(rt, kTPlane, kTS, wc * 16, 0, lane);
-            const Frag<3> y1 = row_frag<3>(rt, kTPlane, kTS, wc * 16, 32, lane);
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                x[i] = f32x4{0, 0, 0, 0};
-                mma(x[i], ti[i][0], y0);
-                if (wr * NT + i >= 2) mma(x[i], ti[i][1], y1);
-            }
-        }
-        load_inv(next, nlen);
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            const int at_ = (wc * 16 + ln) * kTS + (wr * NT + i) * 16 + lg * 4;
-            f32x4 u, l;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                u[r] = be[i][r] * x[i][r];
-                l[r] = le[i][r] * u[r];
-            }
-            if (!KEEP) store_planes<NA>(ut + at_, kTPlane, u);
-            store_planes(lt + at_, kTPlane, l);
+                for (int r = 0; r < 4; ++r) qs[j][r] *= en[r];
         }
         __syncthreads();
-
-        if (KEEP) {
-            keep_tokens(keep.x, start, len, x);
-        } else {
-            const Frag<NA> u0 = row_frag<NA>(ut, kTPlane, kTS, wc * 16, 0, lane);
-            const Frag<NA> u1 = row_frag<NA>(ut, kTPlane, kTS, wc * 16, 32, lane);
+        __syncthreads();
+        if (!KEEP) {
+            Frag<NA> f[CT];
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                f32x4 o = {0, 0, 0, 0};
-                mma(o, at[i][0], u0);
-                if (wr * NT + i >= 2) mma(o, at[i][1], u1);
+            for (int j = 0; j < CT; ++j) f[j] = row_frag<NA>(ut, kTPlane, kTS, j * 16, 0, lane);
+            mma(o, at[0], f);
+            if (wr >= 2) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    put1<DT>(ot, ((wr * NT + i) * 16 + lg * 4 + r) * VS + wc * 16 + ln,
-                             in.scale * fmaf(en[i][r], qs[i][r], o[r]));
+                for (int j = 0; j < CT; ++j) f[j] = row_frag<NA>(ut, kTPlane, kTS, j * 16, 32, lane);
+                mma(o, at[1], f);
             }
-        }
-        load_att(next, nlen);
-        {
-            const Frag<3> l0 = row_frag<3>(lt, kTPlane, kTS, wc * 16, 0, lane);
-            const Frag<3> l1 = row_frag<3>(lt, kTPlane, kTS, wc * 16, 32, lane);
+            load_att(next, nlen);
 #pragma unroll
-            for (int i = 0; i < ND; ++i) {
+            for (int j = 0; j < CT; ++j)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) S[i][r] *= end;
-                mma(S[i], col_frag<NP>(kt, kKPlane, KS, 0, (wr * ND + i) * 16, lane), l0);
-                mma(S[i], col_frag<NP>(kt, kKPlane, KS, 32, (wr * ND + i) * 16, lane), l1);
-            }
+                for (int r = 0; r < 4; ++r) o[j][r] = in.scale * (qs[j][r] + o[j][r]);
+            if (p.out)
+                store_rows<DT, CT, WHOLE>(p.out, ot + row0 * VS * Elem<DT>::bytes, s, b, h, start, len, row0, v0, o);
         }
         __syncthreads();
-        if (!KEEP && p.out) store_rows<DT, W>(p.out, ot, VS, s, b, h, start, len, v0, wd.out);
-        start = next, len = nlen, cut = ncut;
+        start = next, len = nlen;
     }
-    if (!KEEP && p.last)
-#pragma unroll
-        for (int i = 0; i < ND; ++i)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int d = (wr * ND + i) * 16 + lg * 4 + r;
-                if (d < s.K && col < s.V) p.last[(bh * s.K + d) * s.V + col] = S[i][r];
-            }
 }
 
 // The walk back.  With P the outputs' weights, dS the gradient of the state
@@ -333,13 +370,13 @@ delta_walk(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaFwd p, Kept 
 //   dU = scale P^T dO + leave K dS,  R = (I + diag(beta) M)^-T dU  (the gradient
 //   of beta (V - enter K S)),  dV = beta R,
 //   dS' = end dS + Q^T (scale enter dO) - K^T (beta enter R).
-template <int DT, int RT, int CT>
-__global__ void __launch_bounds__(kThreads, DT == DT_BF16 && RT == 1 ? 2 : 1)
-delta_walk_back(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaBwd p, HeadRows go, Kept keep,
-                int groups, Widths wd) {
+template <int DT, int RT, int CT, bool WHOLE>
+__global__ void __launch_bounds__(kWalkThreads, DT == DT_BF16 && RT == 1 ? 4 : 2)
+delta_walk_back(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaBwd p, HeadRows go, Kept keep, int groups,
+                Widths wd) {
     using Sh = Share<RT, CT>;
     constexpr int NP = kPlanes<DT>;
-    constexpr int NT = Sh::NT, ND = Sh::ND, KP = Sh::KP, KS = Sh::KS, W = Sh::W, VS = Sh::VS;
+    constexpr int ND = Sh::ND, KP = Sh::KP, KS = Sh::KS, W = Sh::W, VS = Sh::VS;
     constexpr int kKPlane = Sh::kKPlane, kSPlane = Sh::kSPlane, kTPlane = Sh::kTPlane, kOPlane = kC * VS;
     constexpr int kWide = 3 * (kSPlane > 2 * kTPlane ? kSPlane : 2 * kTPlane);
     // fp32 tiles of K and Q together pass the LDS from 65 rows on: Q then takes K's place
@@ -359,192 +396,184 @@ delta_walk_back(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaBwd p, 
     if (!my_head(s, groups, bh, group)) return;
     const int64_t b = bh / s.H;
     const int h = (int)(bh % s.H), hk = h / (s.H / s.HK);
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, ln = lane & 15, lg = lane >> 4;
-    const int wc = w % CT, wr = w / CT;
-    const int v0 = group * W, col = v0 + wc * 16 + ln;
+    const int lane = threadIdx.x & 63, w = wave_number(), ln = lane & 15, lg = lane >> 4;
+    const int v0 = group * W, wr = w & 3;
+    const int row0 = wr * 16, r0 = row0 + lg * 4;
     const int64_t slots = state_slots(s.T);
-
-    f32x4 S[ND];
-#pragma unroll
-    for (int i = 0; i < ND; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int d = (wr * ND + i) * 16 + lg * 4 + r;
-            S[i][r] = p.grad_last && d < s.K && col < s.V ? p.grad_last[(bh * s.K + d) * s.V + col] : 0.0f;
-        }
-
-    // rows of kw columns, of which this lane has one; what lies past the state's rows or columns is left out
-    const int kw = kept_width(s.V);
-    const uint32_t kept_at = col < kw ? (uint32_t)(((wr * ND * 16 + lg * 4) * kw + col) * 4) : kNowhere;
-    auto keep_state = [&](float* to, const f32x4 (&x)[ND]) {
-        const Buffer rows = buffer(to, (int64_t)s.K * kw * 4);
-#pragma unroll
-        for (int i = 0; i < ND; ++i)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) store4(rows, kept_at, (i * 16 + r) * kw * 4, x[i][r]);
-    };
-    const uint32_t kept_x = col < kw ? (uint32_t)(((wr * NT * 16 + lg * 4) * kw + col) * 4) : kNowhere;
-    auto keep_tokens = [&](float* to, int start, int len, const f32x4 (&x)[NT]) {
-        const Buffer rows = buffer(to + (bh * s.T + start) * kw, (int64_t)len * kw * 4);
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) store4(rows, kept_x, (i * 16 + r) * kw * 4, x[i][r]);
-    };
-
-    Tile<DT, KP> kn, qn;
-    Tile<DT, W> on;
-    Frag<3> ti[NT][2], at[NT][2];  // columns of the inverse and of the weights: tokens from a row's own on
-    Gates gn;
-    auto load_cols = [&](Frag<3> (&f)[NT][2], const uint16_t* p, int start, int len) {
-        const Buffer rows = plane_rows<3>(p, bh * s.T + start, len);
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-                if (k == 1 || wr * NT + i < 2) f[i][k] = plane_frag<3>(rows, (wr * NT + i) * 16 + ln, k * 32 + lg * 8);
-    };
-
     const int n = blocks.count(b);
     int start, len;
     bool first;  // whether a segment starts with the block
     blocks.at(b, n - 1, start, len, first);
-    kn.load(block_rows(in.k, b, hk, start, len), in.k.st, 0, wd.k);
-    if (!kShare) qn.load(block_rows(in.q, b, hk, start, len), in.q.st, 0, wd.k);
-    on.load(block_rows(go, b, h, start, len), go.st, v0, wd.v);
-    gn.load(in, prep, b, h, bh * s.T + start, start, len);
-    load_cols(at, prep.att_t, start, len);
-    load_cols(ti, prep.inv_t, start, len);
-    // what leaves a block enters the one behind it, unless a segment starts there
-    bool cut = false;
-    for (int c = n - 1; c >= 0; --c) {
-        const int behind = start + len;
-        int prev = 0, plen = 0;
-        bool pfirst = false;
-        if (c > 0) blocks.at(b, c - 1, prev, plen, pfirst);
-        if (cut) {
+
+    if (w < 4) {
+        const int d0 = wr * ND * 16, kw = kept_width(s.V);
+        f32x4 S[ND][CT];
+        each_state<ND, CT>(s, bh, d0, v0, lane, [&](int i, int j, int r, bool ok, int64_t at) {
+            S[i][j][r] = p.grad_last && ok ? p.grad_last[at] : 0.0f;
+        });
+        Frag<3> ti[2], at[2];  // columns of the inverse and of the weights: tokens from a row's own on
+        auto load_cols = [&](Frag<3> (&f)[2], const uint16_t* p, int start, int len) {
+            const Buffer rows = plane_rows<3>(p, bh * s.T + start, len);
+            if (wr < 2) f[0] = plane_frag<3>(rows, row0 + ln, lg * 8);
+            f[1] = plane_frag<3>(rows, row0 + ln, 32 + lg * 8);
+        };
+        load_cols(at, prep.att_t, start, len);
+        load_cols(ti, prep.inv_t, start, len);
+        // what leaves a block enters the one behind it, unless a segment starts there
+        bool cut = false;
+        for (int c = n - 1; c >= 0; --c) {
+            const int behind = start + len;
+            int prev = 0, plen = 0;
+            bool pfirst = false;
+            if (c > 0) blocks.at(b, c - 1, prev, plen, pfirst);
+            if (cut) {
 #pragma unroll
-            for (int i = 0; i < ND; ++i) S[i] = f32x4{0, 0, 0, 0};
-        } else {
-            keep_state(keep.ds + (bh * slots + (behind < s.T ? behind / kC : slots - 1)) * s.K * kw, S);
+                for (int i = 0; i < ND; ++i)
+#pragma unroll
+                    for (int j = 0; j < CT; ++j) S[i][j] = f32x4{0, 0, 0, 0};
+            } else {
+                keep_state<ND, CT>(keep.ds + (bh * slots + (behind < s.T ? behind / kC : slots - 1)) * s.K * kw, s, kw, d0,
+                                   v0, lane, S);
+            }
+#pragma unroll
+            for (int i = 0; i < ND; ++i)
+#pragma unroll
+                for (int j = 0; j < CT; ++j)
+                    store_planes(wide + (j * 16 + ln) * KS + d0 + i * 16 + lg * 4, kSPlane, S[i][j]);
+            __syncthreads();  // the operands and dS are in LDS
+
+            f32x4 kd[CT], po[CT];
+            Frag<NP> of[CT];
+#pragma unroll
+            for (int j = 0; j < CT; ++j) kd[j] = po[j] = f32x4{0, 0, 0, 0};
+            if (wr < 2) {
+#pragma unroll
+                for (int j = 0; j < CT; ++j) of[j] = col_frag<NP>(ot, kOPlane, VS, 0, j * 16, lane);
+                mma(po, at[0], of);
+            }
+#pragma unroll
+            for (int j = 0; j < CT; ++j) of[j] = col_frag<NP>(ot, kOPlane, VS, 32, j * 16, lane);
+            mma(po, at[1], of);
+            load_cols(at, prep.att_t, prev, plen);
+            Frag<3> f[CT];
+#pragma unroll
+            for (int k = 0; k < KP; k += 32) {
+#pragma unroll
+                for (int j = 0; j < CT; ++j) f[j] = row_frag<3>(wide, kSPlane, KS, j * 16, k, lane);
+                mma(kd, row_frag<NP>(kt, kKPlane, KS, row0, k, lane), f);
+            }
+            const f32x4 en = *reinterpret_cast<const f32x4*>(gates + r0);
+            const f32x4 le = *reinterpret_cast<const f32x4*>(gates + kC + r0);
+            const f32x4 be = *reinterpret_cast<const f32x4*>(gates + 2 * kC + r0);
+            const float end = gates[len - 1];
+#pragma unroll
+            for (int j = 0; j < CT; ++j) {
+                f32x4 y;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) y[r] = fmaf(le[r], kd[j][r], in.scale * po[j][r]);
+                store_planes(rt + (j * 16 + ln) * kTS + r0, kTPlane, y);
+            }
+            __syncthreads();  // dU is
+
+            f32x4 x[CT];
+#pragma unroll
+            for (int j = 0; j < CT; ++j) x[j] = f32x4{0, 0, 0, 0};
+            if (wr < 2) {
+#pragma unroll
+                for (int j = 0; j < CT; ++j) f[j] = row_frag<3>(rt, kTPlane, kTS, j * 16, 0, lane);
+                mma(x, ti[0], f);
+            }
+#pragma unroll
+            for (int j = 0; j < CT; ++j) f[j] = row_frag<3>(rt, kTPlane, kTS, j * 16, 32, lane);
+            mma(x, ti[1], f);
+            load_cols(ti, prep.inv_t, prev, plen);
+            f32x4 dv[CT];
+#pragma unroll
+            for (int j = 0; j < CT; ++j) {
+                f32x4 l;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    dv[j][r] = be[r] * x[j][r];
+                    l[r] = -en[r] * dv[j][r];
+                }
+                store_planes(lt + (j * 16 + ln) * kTS + r0, kTPlane, l);
+            }
+            __syncthreads();  // what goes into K^T and Q^T is
+
+            keep_tokens<CT>(keep.r + (bh * s.T + start) * kw, kw, len, row0, v0, lane, x);
+            store_rows<DT, CT, WHOLE>(p.grad_v, gt + row0 * VS * Elem<DT>::bytes, s, b, h, start, len, row0, v0, dv);
+#pragma unroll
+            for (int i = 0; i < ND; ++i)
+#pragma unroll
+                for (int j = 0; j < CT; ++j)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) S[i][j][r] *= end;
+#pragma unroll
+            for (int k = 0; k < kC; k += 32) {
+#pragma unroll
+                for (int j = 0; j < CT; ++j) f[j] = row_frag<3>(lt, kTPlane, kTS, j * 16, k, lane);
+#pragma unroll
+                for (int i = 0; i < ND; ++i) mma(S[i], col_frag<NP>(kt, kKPlane, KS, k, d0 + i * 16, lane), f);
+            }
+            if (kShare) {
+                __syncthreads();  // K is read
+                __syncthreads();  // Q is in its place
+            }
+#pragma unroll
+            for (int k = 0; k < kC; k += 32) {
+#pragma unroll
+                for (int j = 0; j < CT; ++j) f[j] = row_frag<3>(et, kTPlane, kTS, j * 16, k, lane);
+#pragma unroll
+                for (int i = 0; i < ND; ++i) mma(S[i], col_frag<NP>(qt, kKPlane, KS, k, d0 + i * 16, lane), f);
+            }
+            __syncthreads();  // and all of it is read
+            start = prev, len = plen, cut = first, first = pfirst;
         }
+        if (p.grad_h0)
+            each_state<ND, CT>(s, bh, d0, v0, lane, [&](int i, int j, int r, bool ok, int64_t at) {
+                if (ok) p.grad_h0[at] = cut ? 0.0f : S[i][j][r];
+            });
+        return;
+    }
+
+    Tile<DT, KP> kn, qn;
+    Tile<DT, W> on;
+    Gates gn;
+    auto load = [&](int start, int len) {
+        kn.load(block_rows(in.k, b, hk, start, len), in.k.st, 0, wd.k);
+        if (!kShare) qn.load(block_rows(in.q, b, hk, start, len), in.q.st, 0, wd.k);
+        on.load(block_rows(go, b, h, start, len), go.st, v0, wd.v);
+        gn.load(prep, bh * s.T + start, len);
+    };
+    load(start, len);
+    for (int c = n - 1; c >= 0; --c) {
+        int prev = 0, plen = 0;
+        if (c > 0) blocks.at(b, c - 1, prev, plen, first);
         kn.store(kt, kKPlane, KS);
         if (!kShare) qn.store(qt, kKPlane, KS);
         on.store(ot, kOPlane, VS);
         gn.store(gates);
-#pragma unroll
-        for (int i = 0; i < ND; ++i)
-            store_planes(wide + (wc * 16 + ln) * KS + (wr * ND + i) * 16 + lg * 4, kSPlane, S[i]);
         __syncthreads();
-        kn.load(block_rows(in.k, b, hk, prev, plen), in.k.st, 0, wd.k);
-        if (kShare)
-            qn.load(block_rows(in.q, b, hk, start, len), in.q.st, 0, wd.k);
-        else
-            qn.load(block_rows(in.q, b, hk, prev, plen), in.q.st, 0, wd.k);
-        on.load(block_rows(go, b, h, prev, plen), go.st, v0, wd.v);
-        gn.load(in, prep, b, h, bh * s.T + prev, prev, plen);
-
-        f32x4 kd[NT], po[NT];
-#pragma unroll
-        for (int i = 0; i < NT; ++i) kd[i] = po[i] = f32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int k = 0; k < KP / 32; ++k) {
-            const Frag<3> sf = row_frag<3>(wide, kSPlane, KS, wc * 16, k * 32, lane);
-#pragma unroll
-            for (int i = 0; i < NT; ++i) mma(kd[i], row_frag<NP>(kt, kKPlane, KS, (wr * NT + i) * 16, k * 32, lane), sf);
-        }
-        {
-            const Frag<NP> o0 = col_frag<NP>(ot, kOPlane, VS, 0, wc * 16, lane);
-            const Frag<NP> o1 = col_frag<NP>(ot, kOPlane, VS, 32, wc * 16, lane);
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                if (wr * NT + i < 2) mma(po[i], at[i][0], o0);
-                mma(po[i], at[i][1], o1);
-            }
-        }
-        load_cols(at, prep.att_t, prev, plen);
-        f32x4 en[NT], be[NT];
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            const int r0 = (wr * NT + i) * 16 + lg * 4;
-            en[i] = *reinterpret_cast<const f32x4*>(gates + r0);
-            be[i] = *reinterpret_cast<const f32x4*>(gates + 2 * kC + r0);
-            const f32x4 le = *reinterpret_cast<const f32x4*>(gates + kC + r0);
-            f32x4 y;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) y[r] = fmaf(le[r], kd[i][r], in.scale * po[i][r]);
-            store_planes(rt + (wc * 16 + ln) * kTS + r0, kTPlane, y);
-        }
-        const float end = gates[len - 1];
+        if (kShare) qn.load(block_rows(in.q, b, hk, start, len), in.q.st, 0, wd.k);
+        load(prev, plen);
+        const f32x4 en = *reinterpret_cast<const f32x4*>(gates + r0);
         __syncthreads();
-
-        f32x4 x[NT];
-        {
-            const Frag<3> y0 = row_frag<3>(rt, kTPlane, kTS, wc * 16, 0, lane);
-            const Frag<3> y1 = row_frag<3>(rt, kTPlane, kTS, wc * 16, 32, lane);
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                x[i] = f32x4{0, 0, 0, 0};
-                if (wr * NT + i < 2) mma(x[i], ti[i][0], y0);
-                mma(x[i], ti[i][1], y1);
-            }
-        }
-        load_cols(ti, prep.inv_t, prev, plen);
-        keep_tokens(keep.r, start, len, x);
+        for (int j = 0; j < CT; ++j) {
+            f32x4 e;
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            const int r0 = (wr * NT + i) * 16 + lg * 4;
-            uint16_t* o = lt + (wc * 16 + ln) * kTS + r0;
-            f32x4 l, e;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const float dv = be[i][r] * x[i][r];
-                l[r] = -en[i][r] * dv;
-                e[r] = in.scale * en[i][r] * element<NP>(ot + (r0 + r) * VS + wc * 16 + ln, kOPlane);
-                put1<DT>(gt, (r0 + r) * VS + wc * 16 + ln, dv);
-            }
-            store_planes(o, kTPlane, l);
-            store_planes(o + 3 * kTPlane, kTPlane, e);
+            for (int r = 0; r < 4; ++r) e[r] = in.scale * en[r] * element<NP>(ot + (r0 + r) * VS + j * 16 + ln, kOPlane);
+            store_planes(et + (j * 16 + ln) * kTS + r0, kTPlane, e);
         }
         __syncthreads();
-        store_rows<DT, W>(p.grad_v, gt, VS, s, b, h, start, len, v0, wd.out);
-
-        {
-            const Frag<3> l0 = row_frag<3>(lt, kTPlane, kTS, wc * 16, 0, lane);
-            const Frag<3> l1 = row_frag<3>(lt, kTPlane, kTS, wc * 16, 32, lane);
-#pragma unroll
-            for (int i = 0; i < ND; ++i) {
-#pragma unroll
-                for (int r = 0; r < 4; ++r) S[i][r] *= end;
-                mma(S[i], col_frag<NP>(kt, kKPlane, KS, 0, (wr * ND + i) * 16, lane), l0);
-                mma(S[i], col_frag<NP>(kt, kKPlane, KS, 32, (wr * ND + i) * 16, lane), l1);
-            }
-        }
         if (kShare) {
             __syncthreads();
             qn.store(qt, kKPlane, KS);
             __syncthreads();
         }
-        {
-            const Frag<3> e0 = row_frag<3>(et, kTPlane, kTS, wc * 16, 0, lane);
-            const Frag<3> e1 = row_frag<3>(et, kTPlane, kTS, wc * 16, 32, lane);
-#pragma unroll
-            for (int i = 0; i < ND; ++i) {
-                mma(S[i], col_frag<NP>(qt, kKPlane, KS, 0, (wr * ND + i) * 16, lane), e0);
-                mma(S[i], col_frag<NP>(qt, kKPlane, KS, 32, (wr * ND + i) * 16, lane), e1);
-            }
-        }
         __syncthreads();
-        start = prev, len = plen, cut = first, first = pfirst;
+        start = prev, len = plen;
     }
-    if (p.grad_h0)
-#pragma unroll
-        for (int i = 0; i < ND; ++i)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int d = (wr * ND + i) * 16 + lg * 4 + r;
-                if (d < s.K && col < s.V) p.grad_h0[(bh * s.K + d) * s.V + col] = cut ? 0.0f : S[i][r];
-            }
 }
 
 // Columns of a workgroup: 32, or 16 where fp32 tiles of K leave no room for
@@ -562,19 +591,25 @@ hipError_t by_rows(const DeltaShape& s, F f) {
     }
 }
 
-// Contiguous rows of `bytes` that are whole aligned vectors.
-bool whole(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) | (uintptr_t)bytes) % 16 == 0; }
+// Whether rows of a [B, T, H, V] output are whole aligned vectors.
+bool whole(const DeltaShape& s, const void* p, int dtype) {
+    return (reinterpret_cast<uintptr_t>(p) | (uintptr_t)(s.V * (dtype == DT_F32 ? 4 : 2))) % 16 == 0;
+}
 
 dim3 walk_grid(const DeltaShape& s, int groups) { return dim3((unsigned)((s.B * s.H + 7) / 8 * 8 * groups)); }
 
 template <int DT, bool KEEP>
 hipError_t walk(const DeltaShape& s, const DeltaIn& in, const Blocks& blocks, const Prep& prep, const DeltaFwd& out,
                 const Kept& keep, hipStream_t st) {
-    const Widths wd{row_width(s.K, DT), row_width(s.V, DT), whole(out.out, s.V * Elem<DT>::bytes)};
+    const Widths wd{row_width(s.K, DT), row_width(s.V, DT)};
+    const bool rows = whole(s, out.out, DT);
     return by_rows(s, [&](auto rt) {
         constexpr int RT = decltype(rt)::value, CT = kMaxCT<DT, RT>;
         const int groups = (s.V + CT * 16 - 1) / (CT * 16);
-        delta_walk<DT, RT, CT, KEEP><<<walk_grid(s, groups), kThreads, 0, st>>>(s, in, blocks, prep, out, keep, groups, wd);
+        if (KEEP || rows)
+            delta_walk<DT, RT, CT, KEEP, true><<<walk_grid(s, groups), kWalkThreads, 0, st>>>(s, in, blocks, prep, out, keep, groups, wd);
+        else
+            delta_walk<DT, RT, CT, KEEP, KEEP><<<walk_grid(s, groups), kWalkThreads, 0, st>>>(s, in, blocks, prep, out, keep, groups, wd);
         return hipGetLastError();
     });
 }
@@ -591,11 +626,15 @@ hipError_t run_walk(const DeltaShape& s, const DeltaIn& in, const Blocks& blocks
 template <int DT>
 hipError_t walk_back(const DeltaShape& s, const DeltaIn& in, const Blocks& blocks, const Prep& prep, const DeltaBwd& p,
                      const HeadRows& go, const Kept& keep, hipStream_t st) {
-    const Widths wd{row_width(s.K, DT), row_width(s.V, DT), whole(p.grad_v, s.V * Elem<DT>::bytes)};
+    const Widths wd{row_width(s.K, DT), row_width(s.V, DT)};
+    const bool rows = whole(s, p.grad_v, DT);
     return by_rows(s, [&](auto rt) {
         constexpr int RT = decltype(rt)::value, CT = kMaxCT<DT, RT>;
         const int groups = (s.V + CT * 16 - 1) / (CT * 16);
-        delta_walk_back<DT, RT, CT><<<walk_grid(s, groups), kThreads, 0, st>>>(s, in, blocks, prep, p, go, keep, groups, wd);
+        if (rows)
+            delta_walk_back<DT, RT, CT, true><<<walk_grid(s, groups), kWalkThreads, 0, st>>>(s, in, blocks, prep, p, go, keep, groups, wd);
+        else
+            delta_walk_back<DT, RT, CT, false><<<walk_grid(s, groups), kWalkThreads, 0, st>>>(s, in, blocks, prep, p, go, keep, groups, wd);
         return hipGetLastError();
     });
 }

@@ -33,7 +33,7 @@ inline bool rows_whole(const HeadRows& r, int width, int bytes) {
 
 // Byte offsets into a call's workspace.
 struct Layout {
-    size_t starts, counts, enter, leave, gh, gl, inv, att, att_t, inv_t, x, r, s, ds, pq, pk, q, k, v, go, total;
+    size_t starts, counts, gates, gl, inv, att, att_t, inv_t, x, r, s, ds, pq, pk, q, k, v, go, total;
     Layout(const DeltaShape& d, bool backward, bool reset, const Copies& copy) {
         const size_t tokens = (size_t)d.B * d.H * d.T, bytes = d.dtype == DT_F32 ? 4 : 2;
         size_t at = 0;
@@ -43,9 +43,7 @@ struct Layout {
         };
         take(starts, (size_t)d.B * (d.T + 1) * 4, reset);
         take(counts, (size_t)d.B * 4, reset);
-        take(enter, tokens * 4, true);
-        take(leave, tokens * 4, true);
-        take(gh, tokens * 4, backward);
+        take(gates, tokens * 16, true);
         take(gl, tokens * 4, backward);
         take(inv, tokens * kC * 6, true);
         take(att, tokens * kC * (d.dtype == DT_F32 ? 6 : 4), !backward);
