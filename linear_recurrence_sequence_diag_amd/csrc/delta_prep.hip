@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kScanThreads) delta_blocks(const uint8_t* rese
 
 constexpr int kS = kC + 4;  // floats of an LDS row
 
-template <int DT, bool BWD>
+template <int DT, bool BWD, int NS>
 __global__ void __launch_bounds__(kThreads) delta_prep(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, int slots,
                                                        int width) {
     constexpr int NP = kPlanes<DT>;
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kThreads) delta_prep(DeltaShape s, DeltaIn in,
             // rows (columns of the transposed ones) 0 .. 31 have nothing to read beyond (before) 32
             if (BWD) {
                 if (col < len && (j < 2 || w >= 2))
-                    store_planes<3>(prep.att_t + ((bh * s.T + start + col) * 3) * kC + w * 16 + lg * 4, kC, back);
+                    store_planes<3>(prep.att_t + ((bh * s.T + start + col) * 3) * kC + place(w * 16 + lg * 4), kC, back);
             } else {
 #pragma unroll
                 for (int r = 0; r < 4; ++r) M[(w * 16 + lg * 4 + r) * kS + col] = back[r];
@@ -240,17 +240,14 @@ __global__ void __launch_bounds__(kThreads) delta_prep(DeltaShape s, DeltaIn in,
         for (int i = 0; i < 2; ++i) {
             const int o = i * kThreads + threadIdx.x, r = o >> 3, q = (o & 7) * 8;
             if (r < len && (r >= 32 || q < 32)) {
-                const float* at = Ti + r * kS + q;
-                store_frag(prep.inv + (bh * s.T + start + r) * 3 * kC + q, kC,
-                           split8(*reinterpret_cast<const f32x4*>(at), *reinterpret_cast<const f32x4*>(at + 4)));
-                if (!BWD) {
-                    constexpr int NA = kAttPlanes<DT>;
-                    at = M + r * kS + q;
-                    const Frag<3> f = split8(*reinterpret_cast<const f32x4*>(at), *reinterpret_cast<const f32x4*>(at + 4));
-#pragma unroll
-                    for (int n_ = 0; n_ < NA; ++n_)
-                        *reinterpret_cast<u32x4*>(prep.att + ((bh * s.T + start + r) * NA + n_) * kC + q) = f.p[n_];
-                }
+                // the eight elements that stand at q .. q + 7
+                const int e = r * kS + (q & 32) + (q & 24) / 2;
+                const int64_t to = (bh * s.T + start + r) * NS * kC + q;
+                store_frag(prep.inv + to, kC,
+                           split8<NS>(*reinterpret_cast<const f32x4*>(Ti + e), *reinterpret_cast<const f32x4*>(Ti + e + 16)));
+                if (!BWD)
+                    store_frag(prep.att + to, kC,
+                               split8<NS>(*reinterpret_cast<const f32x4*>(M + e), *reinterpret_cast<const f32x4*>(M + e + 16)));
             }
         }
         if (BWD) {
@@ -266,7 +263,7 @@ __global__ void __launch_bounds__(kThreads) delta_prep(DeltaShape s, DeltaIn in,
                     y[r] = (i == col ? 1.0f : 0.0f) - bt[i] * y[r];
                 }
                 if (col < len && (j < 2 || w >= 2))
-                    store_planes<3>(prep.inv_t + (bh * s.T + start + col) * 3 * kC + w * 16 + lg * 4, kC, y);
+                    store_planes<3>(prep.inv_t + (bh * s.T + start + col) * 3 * kC + place(w * 16 + lg * 4), kC, y);
             }
         }
     }
@@ -277,23 +274,21 @@ hipError_t run_blocks(const DeltaShape& s, const uint8_t* reset, int* starts, in
     return hipGetLastError();
 }
 
-hipError_t run_prep(const DeltaShape& s, const DeltaIn& in, const Blocks& blocks, const Prep& prep, bool backward,
-                    hipStream_t st) {
+template <int DT, bool BWD, int NS>
+hipError_t prep_of(const DeltaShape& s, const DeltaIn& in, const Blocks& blocks, const Prep& prep, hipStream_t st) {
     const int slots = (int)((s.T + kC - 1) / kC);
-    const dim3 grid((unsigned)(s.B * s.H * slots)), block(kThreads);
-    const int width = row_width(s.K, s.dtype);
-    if (s.dtype == DT_BF16) {
-        if (backward)
-            delta_prep<DT_BF16, true><<<grid, block, 0, st>>>(s, in, blocks, prep, slots, width);
-        else
-            delta_prep<DT_BF16, false><<<grid, block, 0, st>>>(s, in, blocks, prep, slots, width);
-    } else {
-        if (backward)
-            delta_prep<DT_F32, true><<<grid, block, 0, st>>>(s, in, blocks, prep, slots, width);
-        else
-            delta_prep<DT_F32, false><<<grid, block, 0, st>>>(s, in, blocks, prep, slots, width);
-    }
+    delta_prep<DT, BWD, NS><<<dim3((unsigned)(s.B * s.H * slots)), kThreads, 0, st>>>(s, in, blocks, prep, slots,
+                                                                                   row_width(s.K, DT));
     return hipGetLastError();
+}
+
+hipError_t run_prep(const DeltaShape& s, const DeltaIn& in, const Blocks& blocks, const Prep& prep, bool backward,
+                    int planes, hipStream_t st) {
+    if (s.dtype == DT_F32)
+        return backward ? prep_of<DT_F32, true, 3>(s, in, blocks, prep, st) : prep_of<DT_F32, false, 3>(s, in, blocks, prep, st);
+    if (backward) return prep_of<DT_BF16, true, 3>(s, in, blocks, prep, st);
+    return planes == 2 ? prep_of<DT_BF16, false, 2>(s, in, blocks, prep, st)
+                       : prep_of<DT_BF16, false, 3>(s, in, blocks, prep, st);
 }
 
 }  // namespace delta

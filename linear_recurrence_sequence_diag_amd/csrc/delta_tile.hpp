@@ -1,19 +1,23 @@
 // delta_tile.hpp -- device building blocks of the gated delta rule's blocks of
 // tokens (gfx950).
 //
-// Products on the matrix cores.  A fp32 value is the exact sum of three bf16
-// values (8 leading bits of the significand each, cut off, not rounded), so a
+// Products on the matrix cores.  A fp32 value is the sum of three bf16 values,
+// each the rest of those before it, rounded (what is left is below 2^-26), so a
 // product of two fp32 operands is six bf16 products of 16x16x32 with fp32 sums
-// (those whose weight is at least 2^-16 of the leading one; what is left out is
-// below 2^-23 of the product), and a product with a bf16 operand is three.  The
-// fp32 matrix instruction has a sixteenth of the bf16 rate, so six are 2.7
-// times as fast, three 5.3 times.  An infinity or NaN gives NaN.
+// (those left out are below 2^-26 of it), and a product with a bf16 operand is
+// three.  The fp32 matrix instruction has a sixteenth of the bf16 rate, so six
+// are 2.7 times as fast, three 5.3 times.  Two values hold 17 bits (what is left
+// is at most 2^-18): enough for what ends in a bf16 output, whose rounding is 512
+// times as large.  An infinity or NaN gives NaN.
 //
 // Layouts of v_mfma_f32_16x16x32_bf16, lane l, ln = l & 15, lg = l >> 4:
 //   A: row ln, k = 8 lg .. 8 lg + 7      B: column ln, the same k
 //   C: column ln, rows 4 lg .. 4 lg + 3
-// So four values of a lane of C are four consecutive k of a B operand's column:
-// results go to the next product through LDS arrays [column][k].
+// The order of k is free as long as A and B agree.  Where a lane's eight k are
+// 4 lg .. 4 lg + 3 of one tile of 16 and the same of the next one, two tiles of C
+// are, as they stand in their registers, a B operand with their rows as k: a
+// chain of products needs no exchange between lanes.  place() is where an index
+// stands in rows that hold their k in that order.
 #pragma once
 
 #include "device.hpp"
@@ -32,6 +36,11 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
+// Where index i stands in rows of that order (groups of 32).
+__host__ __device__ __forceinline__ constexpr int place(int i) {
+    return (i & ~31) + (i >> 2 & 3) * 8 + (i >> 4 & 1) * 4 + (i & 3);
+}
+
 template <int NP>
 struct Frag {
     u32x4 p[NP];
@@ -46,65 +55,75 @@ __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
                                                    0, 0, 0);
 }
 
+// the products of parts i and j with i + j up to this are taken
+template <int NA, int NB>
+constexpr int kLast = NA == 3 || NB == 3 ? 2 : 1;
+
 // c += a b, the small parts first
 template <int NA, int NB>
 __device__ __forceinline__ void mma(f32x4& c, const Frag<NA>& a, const Frag<NB>& b) {
 #pragma unroll
-    for (int s = 2; s >= 0; --s)
+    for (int s = kLast<NA, NB>; s >= 0; --s)
 #pragma unroll
         for (int i = 0; i <= s; ++i)
             if (i < NA && s - i < NB) c = mfma(a.p[i], b.p[s - i], c);
 }
 
-// c[j] += a b[j], the sums in turn: a product does not wait for the one before
+// c[j] += a[j] b, the sums in turn: a product does not wait for the one before
 template <int NA, int NB, int M>
-__device__ __forceinline__ void mma(f32x4 (&c)[M], const Frag<NA>& a, const Frag<NB> (&b)[M]) {
+__device__ __forceinline__ void mma(f32x4 (&c)[M], const Frag<NA> (&a)[M], const Frag<NB>& b) {
 #pragma unroll
-    for (int s = 2; s >= 0; --s)
+    for (int s = kLast<NA, NB>; s >= 0; --s)
 #pragma unroll
         for (int i = 0; i <= s; ++i)
             if (i < NA && s - i < NB)
 #pragma unroll
-                for (int j = 0; j < M; ++j) c[j] = mfma(a.p[i], b[j].p[s - i], c[j]);
+                for (int j = 0; j < M; ++j) c[j] = mfma(a[j].p[i], b.p[s - i], c[j]);
 }
 
-// the upper halves of two floats, as two bf16
-__device__ __forceinline__ uint32_t uppers(float x0, float x1) {
-    return __builtin_amdgcn_perm(__float_as_uint(x1), __float_as_uint(x0), 0x07060302);
+// two floats as N pairs of bf16, each the rounded rest of those before it
+template <int N>
+__device__ __forceinline__ void split2(float x0, float x1, uint32_t (&p)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        p[i] = pack_bf16x2(x0, x1);
+        if (i + 1 < N) {
+            x0 -= __uint_as_float(p[i] << 16);
+            x1 -= __uint_as_float(p[i] & 0xffff0000u);
+        }
+    }
 }
 
-// two floats as three pairs of bf16
-__device__ __forceinline__ void split2(float x0, float x1, uint32_t& h, uint32_t& m, uint32_t& l) {
-    h = uppers(x0, x1);
-    const float r0 = x0 - __uint_as_float(__float_as_uint(x0) & 0xffff0000u);
-    const float r1 = x1 - __uint_as_float(__float_as_uint(x1) & 0xffff0000u);
-    m = uppers(r0, r1);
-    l = uppers(r0 - __uint_as_float(__float_as_uint(r0) & 0xffff0000u),
-               r1 - __uint_as_float(__float_as_uint(r1) & 0xffff0000u));
-}
-
-__device__ __forceinline__ Frag<3> split8(f32x4 a, f32x4 b) {
-    Frag<3> f;
+template <int N = 3>
+__device__ __forceinline__ Frag<N> split8(f32x4 a, f32x4 b) {
+    Frag<N> f;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        uint32_t h, m, l;
-        split2(a[2 * j], a[2 * j + 1], h, m, l);
-        f.p[0][j] = h, f.p[1][j] = m, f.p[2][j] = l;
-        split2(b[2 * j], b[2 * j + 1], h, m, l);
-        f.p[0][2 + j] = h, f.p[1][2 + j] = m, f.p[2][2 + j] = l;
+        uint32_t p[N], q[N];
+        split2<N>(a[2 * j], a[2 * j + 1], p);
+        split2<N>(b[2 * j], b[2 * j + 1], q);
+#pragma unroll
+        for (int i = 0; i < N; ++i) f.p[i][j] = p[i], f.p[i][2 + j] = q[i];
     }
     return f;
+}
+
+template <int N>
+__device__ __forceinline__ Frag<N> planes(const Frag<3>& f) {
+    Frag<N> x;
+#pragma unroll
+    for (int i = 0; i < N; ++i) x.p[i] = f.p[i];
+    return x;
 }
 
 // Four consecutive k of a column, into N planes `step` elements apart.
 template <int N = 3>
 __device__ __forceinline__ void store_planes(uint16_t* at, int step, f32x4 v) {
-    uint32_t h[2], m[2], l[2];
-    split2(v[0], v[1], h[0], m[0], l[0]);
-    split2(v[2], v[3], h[1], m[1], l[1]);
-    *reinterpret_cast<u32x2*>(at) = u32x2{h[0], h[1]};
-    *reinterpret_cast<u32x2*>(at + step) = u32x2{m[0], m[1]};
-    if (N == 3) *reinterpret_cast<u32x2*>(at + 2 * step) = u32x2{l[0], l[1]};
+    uint32_t p[N], q[N];
+    split2<N>(v[0], v[1], p);
+    split2<N>(v[2], v[3], q);
+#pragma unroll
+    for (int i = 0; i < N; ++i) *reinterpret_cast<u32x2*>(at + i * step) = u32x2{p[i], q[i]};
 }
 
 // ---- rows in memory ----
@@ -200,6 +219,53 @@ __device__ __forceinline__ Frag<NP> col_frag(const uint16_t* tile, int plane, in
     return f;
 }
 
+// Four rows of a tile in a lane's column: rows row0 + 4 lg .. 4 lg + 3, columns
+// col0 + (lane & 3) * step .. of four lanes each.
+template <int NP>
+__device__ __forceinline__ void read_rows(u32x2 (&x)[NP], const uint16_t* tile, int plane, int stride, int row0, int col0,
+                                          int step, int lane) {
+    typedef __attribute__((address_space(3))) s16x4 lds4;
+    const uint16_t* at = tile + (row0 + (lane >> 4) * 4 + (lane >> 2 & 3)) * stride + col0 + (lane & 3) * step;
+#pragma unroll
+    for (int i = 0; i < NP; ++i)
+        x[i] = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(at + i * plane)));
+}
+// An operand with the tile's rows k0 .. k0 + 31 as k, and 16 of its columns.
+template <int NP>
+__device__ __forceinline__ Frag<NP> rows_frag(const uint16_t* tile, int plane, int stride, int k0, int col0, int step,
+                                              int lane) {
+    u32x2 x[NP], y[NP];
+    read_rows<NP>(x, tile, plane, stride, k0, col0, step, lane);
+    read_rows<NP>(y, tile, plane, stride, k0 + 16, col0, step, lane);
+    Frag<NP> f;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) f.p[i] = u32x4{x[i][0], x[i][1], y[i][0], y[i][1]};
+    return f;
+}
+// The same where the tile's columns stand in place().
+template <int NP>
+__device__ __forceinline__ Frag<NP> placed_rows_frag(const uint16_t* tile, int plane, int stride, int k0, int col_tile,
+                                                     int lane) {
+    return rows_frag<NP>(tile, plane, stride, k0, (col_tile >> 1) * 32 + (col_tile & 1) * 4, 8, lane);
+}
+// Four values of a column as floats.
+template <int NP>
+__device__ __forceinline__ f32x4 read_values(const uint16_t* tile, int plane, int stride, int row0, int col0, int lane) {
+    u32x2 x[NP];
+    read_rows<NP>(x, tile, plane, stride, row0, col0, 4, lane);
+    f32x4 v;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        v[j] = __uint_as_float(j & 1 ? x[0][j >> 1] & 0xffff0000u : x[0][j >> 1] << 16);
+        if constexpr (NP == 3) {
+            const float m = __uint_as_float(j & 1 ? x[1][j >> 1] & 0xffff0000u : x[1][j >> 1] << 16);
+            const float l = __uint_as_float(j & 1 ? x[2][j >> 1] & 0xffff0000u : x[2][j >> 1] << 16);
+            v[j] += m + l;
+        }
+    }
+    return v;
+}
+
 template <int NP>
 __device__ __forceinline__ void store_frag(uint16_t* at, int plane, const Frag<NP>& f) {
 #pragma unroll
@@ -243,28 +309,14 @@ struct Prep {
     // the upper float of G; the lower one (backward)
     f32x4* gates;
     float* gl;
-    // rows of kC as bf16 planes, [B, H, T][plane][kC]:
+    // rows of kC as bf16 planes, [B, H, T][plane][kC], their columns in place():
     uint16_t *inv, *att;      // (I + N)^-1, N_ij = decay_ij k_i.k_j beta_j (i > j); decay_ij q_i.k_j
     uint16_t *att_t, *inv_t;  // backward: columns of decay_ij q_i.k_j, and of (I + diag(beta) M)^-1, M = N / beta_j
 };
 
-// Planes of the outputs' weights: what goes into a bf16 output is off by 2^-16
-// with two, a hundredth of its rounding.
-template <int DT>
-constexpr int kAttPlanes = DT == DT_F32 ? 3 : 2;
-
-// A fragment of such rows: row r of the block's NP planes each, columns c .. c + 7.
-template <int NP>
-__device__ __forceinline__ Frag<NP> plane_frag(Buffer rows, int r, int c) {
-    Frag<NP> f;
-#pragma unroll
-    for (int i = 0; i < NP; ++i) f.p[i] = load16(rows, r * (NP * kC * 2) + c * 2, i * (kC * 2));
-    return f;
-}
-template <int NP>
-__device__ __forceinline__ Buffer plane_rows(const uint16_t* p, int64_t t0, int len) {
-    return buffer(p + t0 * (NP * kC), len * (NP * kC * 2));
-}
+// Planes of a call's fp32 operands: two where all that it gives are bf16 outputs;
+// three where a state or gradient in fp32 leaves it.
+inline int operand_planes(const DeltaShape& s, bool fp32_results) { return s.dtype == DT_F32 || fp32_results ? 3 : 2; }
 
 // the matrix-core product of two small fp32 LDS matrices: one 16x16 tile of A B, depth k
 __device__ __forceinline__ f32x4 mm16(const float* A, int sa, const float* B, int sb, int k, int lane) {

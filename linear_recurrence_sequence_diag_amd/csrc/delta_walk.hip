@@ -1,13 +1,17 @@
 // delta_walk.hip -- gated delta rule: the walk over a sequence's blocks that
 // carries a head's state, forward and back.
 //
-// One workgroup carries CT * 16 columns of one head's state [K, V] through all
-// blocks of its batch row; the columns are independent.  A block's products follow
-// one another,
+// One wavefront carries 16 columns of one head's state [K, V] through all blocks of
+// its batch row; the columns are independent.  With S of a block's start, a block's
+// products follow one another,
 //   K S -> X = (I + N)^-1 (V - enter K S) -> S' = end S + K^T (leave beta X),
-// and each result becomes the next one's operand through LDS, cut into bf16
-// planes there.  Four wavefronts do nothing but this chain; four more load the
-// operands a block ahead, and take Q S and the outputs' product with U off it.
+// and O = scale (enter Q S + P beta X).  In the order of k described in
+// delta_tile.hpp each result is the next product's operand where it stands, cut
+// into bf16 planes in registers, so a wavefront waits for no other within a block.
+// What does not depend on the columns (K, Q, rows of the inverse and of P) lies in
+// LDS, shared by the up to eight wavefronts of a head that make up a workgroup; a
+// block's is loaded into registers while the block before is at work.  Wavefronts
+// beyond the columns only load.
 #include "delta_tile.hpp"
 #include "delta_ws.hpp"
 
@@ -16,10 +20,12 @@
 namespace lrscan {
 namespace delta {
 
-constexpr int kTS = kC + 8;  // elements of an LDS column of 64 tokens
+constexpr int kWalkThreads = 512;
+constexpr int kTS = kC + 8;          // elements of an LDS row of 64
+constexpr int kTPlane = kC * kTS;
 
-// Workgroups of one head lie on one XCD, so its q, k and rows of the inverse are
-// read from memory once: bh % 8 is the workgroup's number % 8.
+// Workgroups of one head lie on one XCD, so its operands are read from memory
+// once: bh % 8 is the workgroup's number % 8.
 __device__ __forceinline__ bool my_head(const DeltaShape& s, int groups, int64_t& bh, int& group) {
     const int64_t r = blockIdx.x >> 3;
     group = (int)(r % groups);
@@ -27,122 +33,152 @@ __device__ __forceinline__ bool my_head(const DeltaShape& s, int groups, int64_t
     return bh < s.B * s.H;
 }
 
-// Eight wavefronts: `chain` ones (0 .. 3) carry the state, `side` ones (4 .. 7)
-// bring the operands into LDS and do what does not wait for the state.  Of a
-// block each has 16 tokens, of the state a chain wavefront 16 ND rows, all W columns.
-constexpr int kWalkThreads = 512;
-template <int RT, int CT>
-struct Share {
-    static constexpr int ND = RT;
-    static constexpr int KP = 64 * RT, KS = KP + 8, W = CT * 16, VS = W + 8;
-    static constexpr int kKPlane = kC * KS, kSPlane = W * KS, kTPlane = W * kTS;
-};
-
-// The block's gates, [3][kC] in LDS, brought by the first 64 side threads.
+// A block's gates, [3][kC] in LDS.
 struct Gates {
     f32x4 x;
     __device__ __forceinline__ void load(const Prep& prep, int64_t t0, int len) {
-        const uint32_t i = threadIdx.x & 255;
-        x = __builtin_bit_cast(f32x4, load16(buffer(prep.gates + t0, len * 16), i < kC ? i * 16 : kNowhere));
+        x = __builtin_bit_cast(f32x4, load16(buffer(prep.gates + t0, len * 16), threadIdx.x < kC ? threadIdx.x * 16 : kNowhere));
     }
     __device__ __forceinline__ void store(float* lds) const {
-        const int i = threadIdx.x & 255;
+        const int i = threadIdx.x;
         if (i < kC) lds[i] = x[0], lds[kC + i] = x[1], lds[2 * kC + i] = x[2];
     }
 };
 
-// A tile of a block's kC rows and COLS columns, 8 columns a side thread at a time.
-template <int DT, int COLS>
+// A tile of a block's kC rows and up to COLS columns (uniform `cols` of them, a
+// multiple of 8), 8 columns a thread at a time; PLACED: columns stand in place().
+template <int DT, int COLS, bool PLACED>
 struct Tile {
-    static constexpr int N = kC * COLS / 8, PER = (N + 255) / 256;
+    static constexpr int PER = kC * COLS / 8 / kWalkThreads;
     Raw8<DT> x[PER];
-    __device__ __forceinline__ void load(Buffer rows, int64_t st, int c0, int n) {
+    __device__ __forceinline__ void load(Buffer rows, int64_t st, int c0, int cols, int n) {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int o = i * 256 + (threadIdx.x & 255);
-            x[i].load(rows, o / (COLS / 8) * (int)st, c0 + o % (COLS / 8) * 8, n);
+            const int o = i * kWalkThreads + threadIdx.x, q = o % (COLS / 8) * 8;
+            x[i].load(rows, o / (COLS / 8) * (int)st, q < cols ? c0 + q : n, n);
         }
     }
     __device__ __forceinline__ void store(uint16_t* tile, int plane, int stride) const {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int o = i * 256 + (threadIdx.x & 255);
-            if (N % 256 == 0 || o < N) store_frag(tile + o / (COLS / 8) * stride + o % (COLS / 8) * 8, plane, x[i].frag());
+            const int o = i * kWalkThreads + threadIdx.x, q = o % (COLS / 8) * 8;
+            uint16_t* row = tile + o / (COLS / 8) * stride;
+            const auto f = x[i].frag();
+            if constexpr (PLACED) {
+#pragma unroll
+                for (int p = 0; p < kPlanes<DT>; ++p) {
+                    *reinterpret_cast<u32x2*>(row + p * plane + place(q)) = u32x2{f.p[p][0], f.p[p][1]};
+                    *reinterpret_cast<u32x2*>(row + p * plane + place(q + 4)) = u32x2{f.p[p][2], f.p[p][3]};
+                }
+            } else {
+                store_frag(row + q, plane, f);
+            }
         }
     }
 };
 
-// A wavefront's 16 rows of a contiguous [B, T, H, V] output, of which this
-// workgroup has COLS columns: from accumulators through `lds` (the wavefront's
-// own, 16 rows of COLS + 8 elements), in whole vectors or element by element.
-template <int DT, int CT, bool WHOLE>
-__device__ __forceinline__ void store_rows(void* out, char* lds, const DeltaShape& s, int64_t b, int h, int start, int len,
-                                           int row0, int v0, const f32x4 (&x)[CT]) {
-    constexpr int E = Elem<DT>::bytes, COLS = CT * 16, ROW = COLS + 8, PER = WHOLE ? 16 / E : 1, N = 16 * COLS / PER;
-    const int lane = threadIdx.x & 63;
+// A block's rows of kC in NP planes.
+template <int NP>
+struct Rows64 {
+    u32x4 x[NP];
+    __device__ __forceinline__ void load(const uint16_t* p, int64_t t0, int len) {
+        const Buffer rows = buffer(p + t0 * (NP * kC), len * (NP * kC * 2));
 #pragma unroll
-    for (int j = 0; j < CT; ++j)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) put1<DT>(lds, ((lane >> 4) * 4 + r) * ROW + j * 16 + (lane & 15), x[j][r]);
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // one wavefront's LDS accesses keep their order
-    const int64_t step = (int64_t)s.H * s.V * E;
-    const Buffer rows = buffer(static_cast<char*>(out) + (b * s.T + start) * step + (int64_t)h * s.V * E, len * step);
-#pragma unroll
-    for (int i = 0; i < (N + 63) / 64; ++i) {
-        const int o = i * 64 + lane, r = o / (COLS / PER), q = o % (COLS / PER) * PER;
-        const bool ok = N % 64 == 0 || o < N;
-        const uint32_t at = ok && v0 + q < s.V ? (row0 + r) * (int)step + (v0 + q) * E : kNowhere;
-        const char* from = lds + ((ok ? r : 0) * ROW + q) * E;
-        if constexpr (WHOLE)
-            __builtin_amdgcn_raw_buffer_store_b128(*reinterpret_cast<const u32x4*>(from), rows, at, 0, 0);
-        else if constexpr (E == 4)
-            __builtin_amdgcn_raw_buffer_store_b32(*reinterpret_cast<const uint32_t*>(from), rows, at, 0, 0);
-        else
-            __builtin_amdgcn_raw_buffer_store_b16(*reinterpret_cast<const uint16_t*>(from), rows, at, 0, 0);
+        for (int i = 0; i < NP; ++i) x[i] = load16(rows, (i * kWalkThreads + threadIdx.x) * 16);
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-}
+    __device__ __forceinline__ void store(uint16_t* tile) const {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const int o = i * kWalkThreads + threadIdx.x, r = o / (8 * NP), q = o % (8 * NP);
+            *reinterpret_cast<u32x4*>(tile + q / 8 * kTPlane + r * kTS + q % 8 * 8) = x[i];
+        }
+    }
+};
 
-// A chain wavefront's rows of a state scratch (rows of kw columns), and its
-// tokens' rows of a token scratch; what lies past the rows or columns is left out.
-template <int ND, int CT>
-__device__ __forceinline__ void keep_state(float* to, const DeltaShape& s, int kw, int row0, int v0, int lane,
-                                           const f32x4 (&x)[ND][CT]) {
-    const Buffer rows = buffer(to, (int64_t)s.K * kw * 4);
-#pragma unroll
-    for (int j = 0; j < CT; ++j) {
-        const int col = v0 + j * 16 + (lane & 15);
-        const uint32_t at = col < kw ? (uint32_t)(((row0 + (lane >> 4) * 4) * kw + col) * 4) : kNowhere;
-#pragma unroll
-        for (int i = 0; i < ND; ++i)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) store4(rows, at, (i * 16 + r) * kw * 4, x[i][j][r]);
-    }
-}
-template <int CT>
-__device__ __forceinline__ void keep_tokens(float* to, int kw, int len, int row0, int v0, int lane, const f32x4 (&x)[CT]) {
+// A lane's tokens of a column of a token scratch (rows of kw columns), of a state
+// scratch, and of a [tokens, heads, V] output; what lies past rows or columns is
+// left out.
+__device__ __forceinline__ void keep_tokens(float* to, int kw, int len, int col, int lane, const f32x4 (&x)[4]) {
     const Buffer rows = buffer(to, (int64_t)len * kw * 4);
+    const uint32_t at = col < kw ? (uint32_t)(((lane >> 4) * 4 * kw + col) * 4) : kNowhere;
 #pragma unroll
-    for (int j = 0; j < CT; ++j) {
-        const int col = v0 + j * 16 + (lane & 15);
-        const uint32_t at = col < kw ? (uint32_t)(((row0 + (lane >> 4) * 4) * kw + col) * 4) : kNowhere;
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) store4(rows, at, r * kw * 4, x[j][r]);
-    }
+        for (int r = 0; r < 4; ++r) store4(rows, at, (i * 16 + r) * kw * 4, x[i][r]);
 }
-
-// A state [K, V] in or out of accumulators.
-template <int ND, int CT, class F>
-__device__ __forceinline__ void each_state(const DeltaShape& s, int64_t bh, int row0, int v0, int lane, F f) {
+template <int ND>
+__device__ __forceinline__ void keep_state(float* to, int K, int kw, int col, int lane, const f32x4 (&x)[ND]) {
+    const Buffer rows = buffer(to, (int64_t)K * kw * 4);
+    const uint32_t at = col < kw ? (uint32_t)(((lane >> 4) * 4 * kw + col) * 4) : kNowhere;
 #pragma unroll
     for (int i = 0; i < ND; ++i)
 #pragma unroll
-        for (int j = 0; j < CT; ++j)
+        for (int r = 0; r < 4; ++r) store4(rows, at, (i * 16 + r) * kw * 4, x[i][r]);
+}
+template <int DT>
+__device__ __forceinline__ void store_tokens(void* out, const DeltaShape& s, int64_t t0, int len, int h, int col, int lane,
+                                             const f32x4 (&x)[4]) {
+    constexpr int E = Elem<DT>::bytes;
+    const int64_t step = (int64_t)s.H * s.V * E;
+    const Buffer rows = buffer(static_cast<char*>(out) + t0 * step + (int64_t)h * s.V * E, len * step);
+    const uint32_t at = col < s.V ? (lane >> 4) * 4 * (int)step + col * E : kNowhere;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int d = row0 + i * 16 + (lane >> 4) * 4 + r, col = v0 + j * 16 + (lane & 15);
-                f(i, j, r, d < s.K && col < s.V, (bh * s.K + d) * s.V + col);
-            }
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            if constexpr (DT == DT_F32)
+                store4(rows, at, (i * 16 + r) * (int)step, x[i][r]);
+            else
+                __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16_bits(x[i][r]), rows, at, (i * 16 + r) * (int)step, 0);
+        }
+}
+
+// A column of a state [K, V] in or out of accumulators.
+template <int ND, class F>
+__device__ __forceinline__ void each_state(const DeltaShape& s, int64_t bh, int col, int lane, F f) {
+#pragma unroll
+    for (int i = 0; i < ND; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int d = i * 16 + (lane >> 4) * 4 + r;
+            f(i, r, d < s.K && col < s.V, (bh * s.K + d) * s.V + col);
+        }
+}
+
+// S = end S + K^T l (or Q^T l), l the tokens' two operands of 32.
+template <int NP, int ND, int NS>
+__device__ __forceinline__ void add_tokens(f32x4 (&S)[ND], const uint16_t* tile, int plane, int stride, const Frag<NS>& l0,
+                                           const Frag<NS>& l1, int lane) {
+#pragma unroll
+    for (int i = 0; i < ND; i += 2) {
+        f32x4 c[2] = {S[i], S[i + 1]};
+        const Frag<NP> a[2] = {placed_rows_frag<NP>(tile, plane, stride, 0, i, lane),
+                               placed_rows_frag<NP>(tile, plane, stride, 0, i + 1, lane)};
+        const Frag<NP> b[2] = {placed_rows_frag<NP>(tile, plane, stride, 32, i, lane),
+                               placed_rows_frag<NP>(tile, plane, stride, 32, i + 1, lane)};
+        mma(c, a, l0);
+        mma(c, b, l1);
+        S[i] = c[0], S[i + 1] = c[1];
+    }
+}
+
+// x += A y over a block's tokens, A's rows in NA planes in LDS, y the tokens' two
+// operands of 32; LOWER: rows reach the tokens up to their own, else from there on.
+template <int NA, bool LOWER, int NB>
+__device__ __forceinline__ void triangle(f32x4 (&x)[4], const uint16_t* rows, const Frag<NB>& y0, const Frag<NB>& y1,
+                                         int lane) {
+    f32x4 c[2] = {x[LOWER ? 2 : 0], x[LOWER ? 3 : 1]}, d[2] = {x[LOWER ? 0 : 2], x[LOWER ? 1 : 3]};
+    const int full = LOWER ? 2 : 0, half = LOWER ? 0 : 2;  // tiles of rows with both operands, and with one
+    const Frag<NA> a[2] = {row_frag<NA>(rows, kTPlane, kTS, full * 16, 0, lane),
+                           row_frag<NA>(rows, kTPlane, kTS, (full + 1) * 16, 0, lane)};
+    const Frag<NA> b[2] = {row_frag<NA>(rows, kTPlane, kTS, full * 16, 32, lane),
+                           row_frag<NA>(rows, kTPlane, kTS, (full + 1) * 16, 32, lane)};
+    const Frag<NA> e[2] = {row_frag<NA>(rows, kTPlane, kTS, half * 16, LOWER ? 0 : 32, lane),
+                           row_frag<NA>(rows, kTPlane, kTS, (half + 1) * 16, LOWER ? 0 : 32, lane)};
+    mma(d, e, LOWER ? y0 : y1);
+    mma(c, a, y0);
+    mma(c, b, y1);
+    x[full] = c[0], x[full + 1] = c[1], x[half] = d[0], x[half + 1] = d[1];
 }
 
 // Elements of the operands' rows of K and of V.
@@ -150,22 +186,23 @@ struct Widths {
     int k, v;
 };
 
-template <int DT, int RT, int CT, bool KEEP, bool WHOLE>
-__global__ void __launch_bounds__(kWalkThreads, DT == DT_BF16 && RT <= 2 ? 4 : 2)
-delta_walk(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaFwd p, Kept keep, int groups, Widths wd) {
-    using Sh = Share<RT, CT>;
-    constexpr int NP = kPlanes<DT>, NA = kAttPlanes<DT>;
-    constexpr int ND = Sh::ND, KP = Sh::KP, KS = Sh::KS, W = Sh::W, VS = Sh::VS;
-    constexpr int kKPlane = Sh::kKPlane, kSPlane = Sh::kSPlane, kTPlane = Sh::kTPlane;
-    constexpr int kU = KEEP ? 0 : NA;  // planes of u beside the three of leave u
-    constexpr int kWide = 3 * kSPlane > (kU + 3) * kTPlane ? 3 * kSPlane : (kU + 3) * kTPlane;
-    __shared__ __attribute__((aligned(16))) uint16_t kt[NP * kKPlane];  // K of the block [token][row]
-    __shared__ __attribute__((aligned(16))) uint16_t wide[kWide];       // the state, then u and leave u
-    __shared__ __attribute__((aligned(16))) uint16_t rt[3 * kTPlane];   // right sides of the triangular system
-    __shared__ __attribute__((aligned(16))) uint16_t vt[NP * kC * VS];  // V [token][column]
-    __shared__ __attribute__((aligned(16))) char ot[KEEP ? 16 : kC * VS * Elem<DT>::bytes];  // the outputs, as stored
+// NC: wavefronts with columns, at most; the launch says how many.  NS: planes of
+// fp32 operands.
+template <int DT, int RT, int NC, bool KEEP, int NS>
+__global__ void __launch_bounds__(kWalkThreads, 2)
+delta_walk(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaFwd p, Kept keep, int groups, int waves, Widths wd) {
+    constexpr int NP = kPlanes<DT>;
+    constexpr int ND = 4 * RT, KP = 64 * RT, KS = KP + 8, VS = 16 * NC + 8;
+    constexpr int kKPlane = kC * KS, kVPlane = kC * VS;
+    // fp32 tiles take three planes each: Q lies where K will, the inverse where P will
+    constexpr bool kShare = DT == DT_F32;
+    __shared__ __attribute__((aligned(16))) uint16_t kt[NP * kKPlane];
+    __shared__ __attribute__((aligned(16))) uint16_t qt_[KEEP || kShare ? 8 : NP * kKPlane];
+    __shared__ __attribute__((aligned(16))) uint16_t it[NS * kTPlane];
+    __shared__ __attribute__((aligned(16))) uint16_t at_[KEEP || kShare ? 8 : NS * kTPlane];
+    __shared__ __attribute__((aligned(16))) uint16_t vt[NP * kVPlane];  // V [token][column]
     __shared__ __attribute__((aligned(16))) float gates[3 * kC];
-    uint16_t *const ut = wide, *const lt = wide + kU * kTPlane;
+    uint16_t *const qt = kShare ? kt : qt_, *const at = kShare ? it : at_;
 
     int64_t bh;
     int group;
@@ -173,196 +210,142 @@ delta_walk(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaFwd p, Kept 
     const int64_t b = bh / s.H;
     const int h = (int)(bh % s.H), hk = h / (s.H / s.HK);
     const int lane = threadIdx.x & 63, w = wave_number(), ln = lane & 15, lg = lane >> 4;
-    const int v0 = group * W, wr = w & 3;
-    const int row0 = wr * 16, r0 = row0 + lg * 4;  // tokens of the wavefront, and of the lane in a tile of results
+    const int v0 = group * waves * 16, col = v0 + w * 16 + ln, kw = kept_width(s.V);
+    const bool works = w < waves;
+
+    f32x4 S[ND];
+    each_state<ND>(s, bh, col, lane, [&](int i, int r, bool ok, int64_t at) { S[i][r] = works && in.h0 && ok ? in.h0[at] : 0.0f; });
+
+    Tile<DT, KP, true> kn, qn;
+    Tile<DT, NC * 16, false> vn;
+    Rows64<NS> tn, an;
+    Gates gn;
+    auto load = [&](int start, int len) {
+        gn.load(prep, bh * s.T + start, len);
+        if (!KEEP) qn.load(block_rows(in.q, b, hk, start, len), in.q.st, 0, KP, wd.k);
+        kn.load(block_rows(in.k, b, hk, start, len), in.k.st, 0, KP, wd.k);
+        vn.load(block_rows(in.v, b, h, start, len), in.v.st, v0, waves * 16, wd.v);
+        tn.load(prep.inv, bh * s.T + start, len);
+        if (!KEEP) an.load(prep.att, bh * s.T + start, len);
+    };
     const int n = blocks.count(b);
     int start, len;
     bool cut;
     blocks.at(b, 0, start, len, cut);
+    load(start, len);
+    for (int c = 0; c < n; ++c) {
+        // the next block; past the last one, one without tokens
+        int next = s.T, nlen = 0;
+        bool ncut = false;
+        if (c + 1 < n) blocks.at(b, c + 1, next, nlen, ncut);
+        gn.store(gates);
+        if (!KEEP) qn.store(qt, kKPlane, KS);
+        if (KEEP || !kShare) kn.store(kt, kKPlane, KS);
+        vn.store(vt, kVPlane, VS);
+        tn.store(it);
+        if (!KEEP && !kShare) an.store(at);
+        __syncthreads();
+        if (KEEP || !kShare) load(next, nlen);
 
-    if (w < 4) {
-        const int d0 = wr * ND * 16, kw = kept_width(s.V);
-        f32x4 S[ND][CT];
-        each_state<ND, CT>(s, bh, d0, v0, lane,
-                           [&](int i, int j, int r, bool ok, int64_t at) { S[i][j][r] = in.h0 && ok ? in.h0[at] : 0.0f; });
-        Frag<3> ti[2];
-        // tokens of the lower half of a block reach its first 32 only
-        auto load_inv = [&](int start, int len) {
-            const Buffer rows = plane_rows<3>(prep.inv, bh * s.T + start, len);
-            ti[0] = plane_frag<3>(rows, row0 + ln, lg * 8);
-            if (wr >= 2) ti[1] = plane_frag<3>(rows, row0 + ln, 32 + lg * 8);
-        };
-        load_inv(start, len);
-        for (int c = 0; c < n; ++c) {
-            // the next block; past the last one, one without tokens
-            int next = s.T, nlen = 0;
-            bool ncut = false;
-            if (c + 1 < n) blocks.at(b, c + 1, next, nlen, ncut);
+        f32x4 qs[4], ks[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) qs[i] = ks[i] = f32x4{0, 0, 0, 0};
+        if (works) {
             if (cut) {
 #pragma unroll
-                for (int i = 0; i < ND; ++i)
-#pragma unroll
-                    for (int j = 0; j < CT; ++j) S[i][j] = f32x4{0, 0, 0, 0};
+                for (int i = 0; i < ND; ++i) S[i] = f32x4{0, 0, 0, 0};
             } else if (KEEP) {
-                keep_state<ND, CT>(keep.s + (bh * state_slots(s.T) + start / kC) * s.K * kw, s, kw, d0, v0, lane, S);
+                keep_state<ND>(keep.s + (bh * state_slots(s.T) + start / kC) * s.K * kw, s.K, kw, col, lane, S);
             }
+        }
+        // x += A S for rows A in LDS
+        auto times_state = [&](f32x4 (&x)[4], const uint16_t* tile, const auto& sf, int g) {
+            Frag<NP> a[4];
 #pragma unroll
-            for (int i = 0; i < ND; ++i)
+            for (int i = 0; i < 4; ++i) a[i] = row_frag<NP>(tile, kKPlane, KS, i * 16, g * 32, lane);
+            mma(x, a, sf);
+        };
+        if (works) {
 #pragma unroll
-                for (int j = 0; j < CT; ++j)
-                    store_planes(wide + (j * 16 + ln) * KS + d0 + i * 16 + lg * 4, kSPlane, S[i][j]);
-            __syncthreads();  // the operands and the state are in LDS
-
-            f32x4 ks[CT];
-#pragma unroll
-            for (int j = 0; j < CT; ++j) ks[j] = f32x4{0, 0, 0, 0};
-#pragma unroll
-            for (int k = 0; k < KP; k += 32) {
-                Frag<3> sf[CT];
-#pragma unroll
-                for (int j = 0; j < CT; ++j) sf[j] = row_frag<3>(wide, kSPlane, KS, j * 16, k, lane);
-                mma(ks, row_frag<NP>(kt, kKPlane, KS, row0, k, lane), sf);
+            for (int g = 0; g < KP / 32; ++g) {
+                const Frag<NS> sf = split8<NS>(S[2 * g], S[2 * g + 1]);
+                if (!KEEP) times_state(qs, qt, sf, g);
+                if (KEEP || !kShare) times_state(ks, kt, sf, g);
             }
-            const f32x4 en = *reinterpret_cast<const f32x4*>(gates + r0);
-            const f32x4 le = *reinterpret_cast<const f32x4*>(gates + kC + r0);
-            const f32x4 be = *reinterpret_cast<const f32x4*>(gates + 2 * kC + r0);
-            const float end = gates[len - 1];
+        }
+        if (!KEEP && kShare) {
+            __syncthreads();  // Q is read
+            kn.store(kt, kKPlane, KS);
+            __syncthreads();
+            if (works)
 #pragma unroll
-            for (int j = 0; j < CT; ++j) {
-                f32x4 y;
+                for (int g = 0; g < KP / 32; ++g) {
+                    times_state(ks, kt, split8<NS>(S[2 * g], S[2 * g + 1]), g);
+                }
+        }
+        f32x4 en[4];
+        Frag<NS> l0, l1, u0, u1;
+        float end = 0.0f;
+        if (works) {
+            end = gates[len - 1];
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    y[r] = fmaf(-en[r], ks[j][r], element<NP>(vt + (r0 + r) * VS + j * 16 + ln, kC * VS));
-                store_planes(rt + (j * 16 + ln) * kTS + r0, kTPlane, y);
+            for (int i = 0; i < 4; ++i) {
+                en[i] = *reinterpret_cast<const f32x4*>(gates + i * 16 + lg * 4);
+                const f32x4 v = read_values<NP>(vt, kVPlane, VS, i * 16, w * 16, lane);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) ks[i][r] = fmaf(-en[i][r], ks[i][r], v[r]);
             }
-            __syncthreads();  // the right sides are
-
-            f32x4 x[CT];
-            Frag<3> f[CT];
+            f32x4 x[4];
 #pragma unroll
-            for (int j = 0; j < CT; ++j) {
-                x[j] = f32x4{0, 0, 0, 0};
-                f[j] = row_frag<3>(rt, kTPlane, kTS, j * 16, 0, lane);
-            }
-            mma(x, ti[0], f);
-            if (wr >= 2) {
+            for (int i = 0; i < 4; ++i) x[i] = f32x4{0, 0, 0, 0};
+            triangle<NS, true>(x, it, split8<NS>(ks[0], ks[1]), split8<NS>(ks[2], ks[3]), lane);
+            if (KEEP) keep_tokens(keep.x + (bh * s.T + start) * kw, kw, len, col, lane, x);
+            f32x4 l[4];
 #pragma unroll
-                for (int j = 0; j < CT; ++j) f[j] = row_frag<3>(rt, kTPlane, kTS, j * 16, 32, lane);
-                mma(x, ti[1], f);
-            }
-            load_inv(next, nlen);
-#pragma unroll
-            for (int j = 0; j < CT; ++j) {
-                f32x4 u, l;
+            for (int i = 0; i < 4; ++i) {
+                const f32x4 le = *reinterpret_cast<const f32x4*>(gates + kC + i * 16 + lg * 4);
+                const f32x4 be = *reinterpret_cast<const f32x4*>(gates + 2 * kC + i * 16 + lg * 4);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    u[r] = be[r] * x[j][r];
-                    l[r] = le[r] * u[r];
+                    x[i][r] *= be[r];
+                    l[i][r] = le[r] * x[i][r];
                 }
-                const int o = (j * 16 + ln) * kTS + r0;
-                if (!KEEP) store_planes<NA>(ut + o, kTPlane, u);
-                store_planes(lt + o, kTPlane, l);
             }
-            __syncthreads();  // u is
-
-            if (KEEP) keep_tokens<CT>(keep.x + (bh * s.T + start) * kw, kw, len, row0, v0, lane, x);
+            u0 = split8<NS>(x[0], x[1]), u1 = split8<NS>(x[2], x[3]);
+            l0 = split8<NS>(l[0], l[1]), l1 = split8<NS>(l[2], l[3]);
+        }
+        if (!KEEP && kShare) {
+            __syncthreads();  // the inverse is read
+            an.store(at);
+            __syncthreads();
+            load(next, nlen);
+        }
+        if (works) {
+            if (!KEEP && p.out) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) qs[i][r] *= en[i][r];
+                triangle<NS, true>(qs, at, u0, u1, lane);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) qs[i][r] *= in.scale;
+                store_tokens<DT>(p.out, s, b * s.T + start, len, h, col, lane, qs);
+            }
 #pragma unroll
             for (int i = 0; i < ND; ++i)
 #pragma unroll
-                for (int j = 0; j < CT; ++j)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) S[i][j][r] *= end;
-#pragma unroll
-            for (int k = 0; k < kC; k += 32) {
-#pragma unroll
-                for (int j = 0; j < CT; ++j) f[j] = row_frag<3>(lt, kTPlane, kTS, j * 16, k, lane);
-#pragma unroll
-                for (int i = 0; i < ND; ++i) mma(S[i], col_frag<NP>(kt, kKPlane, KS, k, d0 + i * 16, lane), f);
-            }
-            __syncthreads();  // and all of it is read
-            start = next, len = nlen, cut = ncut;
+                for (int r = 0; r < 4; ++r) S[i][r] *= end;
+            add_tokens<NP>(S, kt, kKPlane, KS, l0, l1, lane);
         }
-        if (!KEEP && p.last)
-            each_state<ND, CT>(s, bh, d0, v0, lane, [&](int i, int j, int r, bool ok, int64_t at) {
-                if (ok) p.last[at] = S[i][j][r];
-            });
-        return;
+        __syncthreads();  // all of the block is read
+        start = next, len = nlen, cut = ncut;
     }
-
-    Tile<DT, KP> kn;
-    Tile<DT, W> vn;
-    Gates gn;
-    Raw8<DT> qn[KP / 32];
-    Frag<NA> at[2];
-    auto load = [&](int start, int len) {
-        kn.load(block_rows(in.k, b, hk, start, len), in.k.st, 0, wd.k);
-        vn.load(block_rows(in.v, b, h, start, len), in.v.st, v0, wd.v);
-        gn.load(prep, bh * s.T + start, len);
-    };
-    auto load_q = [&](int start, int len) {
-        const Buffer rows = block_rows(in.q, b, hk, start, len);
-#pragma unroll
-        for (int k = 0; k < KP / 32; ++k) qn[k].load(rows, (row0 + ln) * (int)in.q.st, k * 32 + lg * 8, wd.k);
-    };
-    auto load_att = [&](int start, int len) {
-        const Buffer rows = plane_rows<NA>(prep.att, bh * s.T + start, len);
-        at[0] = plane_frag<NA>(rows, row0 + ln, lg * 8);
-        if (wr >= 2) at[1] = plane_frag<NA>(rows, row0 + ln, 32 + lg * 8);
-    };
-    load(start, len);
-    if (!KEEP) {
-        load_q(start, len);
-        load_att(start, len);
-    }
-    for (int c = 0; c < n; ++c) {
-        int next = s.T, nlen = 0;
-        if (c + 1 < n) blocks.at(b, c + 1, next, nlen, cut);
-        kn.store(kt, kKPlane, KS);
-        vn.store(vt, kC * VS, VS);
-        gn.store(gates);
-        __syncthreads();
-        load(next, nlen);
-        f32x4 qs[CT], o[CT];
-        if (!KEEP) {
-#pragma unroll
-            for (int j = 0; j < CT; ++j) qs[j] = o[j] = f32x4{0, 0, 0, 0};
-#pragma unroll
-            for (int k = 0; k < KP / 32; ++k) {
-                Frag<NA> sf[CT];
-#pragma unroll
-                for (int j = 0; j < CT; ++j) sf[j] = row_frag<NA>(wide, kSPlane, KS, j * 16, k * 32, lane);
-                mma(qs, qn[k].frag(), sf);
-            }
-            load_q(next, nlen);
-            const f32x4 en = *reinterpret_cast<const f32x4*>(gates + r0);
-#pragma unroll
-            for (int j = 0; j < CT; ++j)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) qs[j][r] *= en[r];
-        }
-        __syncthreads();
-        __syncthreads();
-        if (!KEEP) {
-            Frag<NA> f[CT];
-#pragma unroll
-            for (int j = 0; j < CT; ++j) f[j] = row_frag<NA>(ut, kTPlane, kTS, j * 16, 0, lane);
-            mma(o, at[0], f);
-            if (wr >= 2) {
-#pragma unroll
-                for (int j = 0; j < CT; ++j) f[j] = row_frag<NA>(ut, kTPlane, kTS, j * 16, 32, lane);
-                mma(o, at[1], f);
-            }
-            load_att(next, nlen);
-#pragma unroll
-            for (int j = 0; j < CT; ++j)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) o[j][r] = in.scale * (qs[j][r] + o[j][r]);
-            if (p.out)
-                store_rows<DT, CT, WHOLE>(p.out, ot + row0 * VS * Elem<DT>::bytes, s, b, h, start, len, row0, v0, o);
-        }
-        __syncthreads();
-        start = next, len = nlen;
-    }
+    if (!KEEP && p.last && works)
+        each_state<ND>(s, bh, col, lane, [&](int i, int r, bool ok, int64_t at) {
+            if (ok) p.last[at] = S[i][r];
+        });
 }
 
 // The walk back.  With P the outputs' weights, dS the gradient of the state
@@ -370,26 +353,22 @@ delta_walk(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaFwd p, Kept 
 //   dU = scale P^T dO + leave K dS,  R = (I + diag(beta) M)^-T dU  (the gradient
 //   of beta (V - enter K S)),  dV = beta R,
 //   dS' = end dS + Q^T (scale enter dO) - K^T (beta enter R).
-template <int DT, int RT, int CT, bool WHOLE>
-__global__ void __launch_bounds__(kWalkThreads, DT == DT_BF16 && RT == 1 ? 4 : 2)
+template <int DT, int RT, int NC>
+__global__ void __launch_bounds__(kWalkThreads, 2)
 delta_walk_back(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaBwd p, HeadRows go, Kept keep, int groups,
-                Widths wd) {
-    using Sh = Share<RT, CT>;
+                int waves, Widths wd) {
     constexpr int NP = kPlanes<DT>;
-    constexpr int ND = Sh::ND, KP = Sh::KP, KS = Sh::KS, W = Sh::W, VS = Sh::VS;
-    constexpr int kKPlane = Sh::kKPlane, kSPlane = Sh::kSPlane, kTPlane = Sh::kTPlane, kOPlane = kC * VS;
-    constexpr int kWide = 3 * (kSPlane > 2 * kTPlane ? kSPlane : 2 * kTPlane);
-    // fp32 tiles of K and Q together pass the LDS from 65 rows on: Q then takes K's place
-    constexpr bool kShare = DT == DT_F32 && RT >= 2;
+    constexpr int ND = 4 * RT, KP = 64 * RT, KS = KP + 8, VS = 16 * NC + 8;
+    constexpr int kKPlane = kC * KS, kVPlane = kC * VS;
+    // fp32: Q follows K in one place, the inverse P in another
+    constexpr bool kShare = DT == DT_F32;
     __shared__ __attribute__((aligned(16))) uint16_t kt[NP * kKPlane];
     __shared__ __attribute__((aligned(16))) uint16_t qt_[kShare ? 8 : NP * kKPlane];
-    __shared__ __attribute__((aligned(16))) uint16_t wide[kWide];  // dS, then what goes into K^T and Q^T
-    __shared__ __attribute__((aligned(16))) uint16_t rt[3 * kTPlane];
-    __shared__ __attribute__((aligned(16))) uint16_t ot[NP * kOPlane];  // dO [token][column]
-    __shared__ __attribute__((aligned(16))) char gt[kC * VS * Elem<DT>::bytes];  // dV, as stored
+    __shared__ __attribute__((aligned(16))) uint16_t at[3 * kTPlane];
+    __shared__ __attribute__((aligned(16))) uint16_t it_[kShare ? 8 : 3 * kTPlane];
+    __shared__ __attribute__((aligned(16))) uint16_t ot[NP * kVPlane];  // dO [token][column]
     __shared__ __attribute__((aligned(16))) float gates[3 * kC];
-    uint16_t *const lt = wide, *const et = wide + 3 * kTPlane;
-    uint16_t* const qt = kShare ? kt : qt_;
+    uint16_t *const qt = kShare ? kt : qt_, *const it = kShare ? at : it_;
 
     int64_t bh;
     int group;
@@ -397,189 +376,139 @@ delta_walk_back(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaBwd p, 
     const int64_t b = bh / s.H;
     const int h = (int)(bh % s.H), hk = h / (s.H / s.HK);
     const int lane = threadIdx.x & 63, w = wave_number(), ln = lane & 15, lg = lane >> 4;
-    const int v0 = group * W, wr = w & 3;
-    const int row0 = wr * 16, r0 = row0 + lg * 4;
+    const int v0 = group * waves * 16, col = v0 + w * 16 + ln, kw = kept_width(s.V);
+    const bool works = w < waves;
     const int64_t slots = state_slots(s.T);
+
+    f32x4 S[ND];
+    each_state<ND>(s, bh, col, lane, [&](int i, int r, bool ok, int64_t at) {
+        S[i][r] = works && p.grad_last && ok ? p.grad_last[at] : 0.0f;
+    });
+
+    Tile<DT, KP, true> kn, qn;
+    Tile<DT, NC * 16, false> on;
+    Rows64<3> tn, an;
+    Gates gn;
+    auto load = [&](int start, int len) {
+        gn.load(prep, bh * s.T + start, len);
+        kn.load(block_rows(in.k, b, hk, start, len), in.k.st, 0, KP, wd.k);
+        on.load(block_rows(go, b, h, start, len), go.st, v0, waves * 16, wd.v);
+        an.load(prep.att_t, bh * s.T + start, len);
+        tn.load(prep.inv_t, bh * s.T + start, len);
+        qn.load(block_rows(in.q, b, hk, start, len), in.q.st, 0, KP, wd.k);
+    };
     const int n = blocks.count(b);
     int start, len;
     bool first;  // whether a segment starts with the block
     blocks.at(b, n - 1, start, len, first);
+    load(start, len);
+    // what leaves a block enters the one behind it, unless a segment starts there
+    bool cut = false;
+    for (int c = n - 1; c >= 0; --c) {
+        const int behind = start + len;
+        int prev = 0, plen = 0;
+        bool pfirst = false;
+        if (c > 0) blocks.at(b, c - 1, prev, plen, pfirst);
+        gn.store(gates);
+        kn.store(kt, kKPlane, KS);
+        on.store(ot, kVPlane, VS);
+        an.store(at);
+        if (!kShare) {
+            tn.store(it);
+            qn.store(qt, kKPlane, KS);
+        }
+        __syncthreads();
+        if (!kShare) load(prev, plen);
 
-    if (w < 4) {
-        const int d0 = wr * ND * 16, kw = kept_width(s.V);
-        f32x4 S[ND][CT];
-        each_state<ND, CT>(s, bh, d0, v0, lane, [&](int i, int j, int r, bool ok, int64_t at) {
-            S[i][j][r] = p.grad_last && ok ? p.grad_last[at] : 0.0f;
-        });
-        Frag<3> ti[2], at[2];  // columns of the inverse and of the weights: tokens from a row's own on
-        auto load_cols = [&](Frag<3> (&f)[2], const uint16_t* p, int start, int len) {
-            const Buffer rows = plane_rows<3>(p, bh * s.T + start, len);
-            if (wr < 2) f[0] = plane_frag<3>(rows, row0 + ln, lg * 8);
-            f[1] = plane_frag<3>(rows, row0 + ln, 32 + lg * 8);
-        };
-        load_cols(at, prep.att_t, start, len);
-        load_cols(ti, prep.inv_t, start, len);
-        // what leaves a block enters the one behind it, unless a segment starts there
-        bool cut = false;
-        for (int c = n - 1; c >= 0; --c) {
-            const int behind = start + len;
-            int prev = 0, plen = 0;
-            bool pfirst = false;
-            if (c > 0) blocks.at(b, c - 1, prev, plen, pfirst);
+        f32x4 x[4], po[4], en[4];
+        Frag<NP> o0, o1;
+        float end = 0.0f;
+        if (works) {
             if (cut) {
 #pragma unroll
-                for (int i = 0; i < ND; ++i)
-#pragma unroll
-                    for (int j = 0; j < CT; ++j) S[i][j] = f32x4{0, 0, 0, 0};
+                for (int i = 0; i < ND; ++i) S[i] = f32x4{0, 0, 0, 0};
             } else {
-                keep_state<ND, CT>(keep.ds + (bh * slots + (behind < s.T ? behind / kC : slots - 1)) * s.K * kw, s, kw, d0,
-                                   v0, lane, S);
+                keep_state<ND>(keep.ds + (bh * slots + (behind < s.T ? behind / kC : slots - 1)) * s.K * kw, s.K, kw, col,
+                               lane, S);
+            }
+            end = gates[len - 1];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[i] = po[i] = f32x4{0, 0, 0, 0};
+                en[i] = *reinterpret_cast<const f32x4*>(gates + i * 16 + lg * 4);
+            }
+            o0 = rows_frag<NP>(ot, kVPlane, VS, 0, w * 16, 4, lane);
+            o1 = rows_frag<NP>(ot, kVPlane, VS, 32, w * 16, 4, lane);
+            triangle<3, false>(po, at, o0, o1, lane);
+#pragma unroll
+            for (int g = 0; g < KP / 32; ++g) {
+                const Frag<3> sf = split8(S[2 * g], S[2 * g + 1]);
+                Frag<NP> a[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) a[i] = row_frag<NP>(kt, kKPlane, KS, i * 16, g * 32, lane);
+                mma(x, a, sf);
             }
 #pragma unroll
-            for (int i = 0; i < ND; ++i)
+            for (int i = 0; i < 4; ++i) {
+                const f32x4 le = *reinterpret_cast<const f32x4*>(gates + kC + i * 16 + lg * 4);
 #pragma unroll
-                for (int j = 0; j < CT; ++j)
-                    store_planes(wide + (j * 16 + ln) * KS + d0 + i * 16 + lg * 4, kSPlane, S[i][j]);
-            __syncthreads();  // the operands and dS are in LDS
-
-            f32x4 kd[CT], po[CT];
-            Frag<NP> of[CT];
-#pragma unroll
-            for (int j = 0; j < CT; ++j) kd[j] = po[j] = f32x4{0, 0, 0, 0};
-            if (wr < 2) {
-#pragma unroll
-                for (int j = 0; j < CT; ++j) of[j] = col_frag<NP>(ot, kOPlane, VS, 0, j * 16, lane);
-                mma(po, at[0], of);
+                for (int r = 0; r < 4; ++r) po[i][r] = fmaf(le[r], x[i][r], in.scale * po[i][r]);
             }
+        }
+        if (kShare) {
+            __syncthreads();  // the weights are read
+            tn.store(it);
+            __syncthreads();
+        }
+        if (works) {
 #pragma unroll
-            for (int j = 0; j < CT; ++j) of[j] = col_frag<NP>(ot, kOPlane, VS, 32, j * 16, lane);
-            mma(po, at[1], of);
-            load_cols(at, prep.att_t, prev, plen);
-            Frag<3> f[CT];
+            for (int i = 0; i < 4; ++i) x[i] = f32x4{0, 0, 0, 0};
+            triangle<3, false>(x, it, split8(po[0], po[1]), split8(po[2], po[3]), lane);
+            keep_tokens(keep.r + (bh * s.T + start) * kw, kw, len, col, lane, x);
 #pragma unroll
-            for (int k = 0; k < KP; k += 32) {
-#pragma unroll
-                for (int j = 0; j < CT; ++j) f[j] = row_frag<3>(wide, kSPlane, KS, j * 16, k, lane);
-                mma(kd, row_frag<NP>(kt, kKPlane, KS, row0, k, lane), f);
-            }
-            const f32x4 en = *reinterpret_cast<const f32x4*>(gates + r0);
-            const f32x4 le = *reinterpret_cast<const f32x4*>(gates + kC + r0);
-            const f32x4 be = *reinterpret_cast<const f32x4*>(gates + 2 * kC + r0);
-            const float end = gates[len - 1];
-#pragma unroll
-            for (int j = 0; j < CT; ++j) {
-                f32x4 y;
-#pragma unroll
-                for (int r = 0; r < 4; ++r) y[r] = fmaf(le[r], kd[j][r], in.scale * po[j][r]);
-                store_planes(rt + (j * 16 + ln) * kTS + r0, kTPlane, y);
-            }
-            __syncthreads();  // dU is
-
-            f32x4 x[CT];
-#pragma unroll
-            for (int j = 0; j < CT; ++j) x[j] = f32x4{0, 0, 0, 0};
-            if (wr < 2) {
-#pragma unroll
-                for (int j = 0; j < CT; ++j) f[j] = row_frag<3>(rt, kTPlane, kTS, j * 16, 0, lane);
-                mma(x, ti[0], f);
-            }
-#pragma unroll
-            for (int j = 0; j < CT; ++j) f[j] = row_frag<3>(rt, kTPlane, kTS, j * 16, 32, lane);
-            mma(x, ti[1], f);
-            load_cols(ti, prep.inv_t, prev, plen);
-            f32x4 dv[CT];
-#pragma unroll
-            for (int j = 0; j < CT; ++j) {
-                f32x4 l;
+            for (int i = 0; i < 4; ++i) {
+                const f32x4 be = *reinterpret_cast<const f32x4*>(gates + 2 * kC + i * 16 + lg * 4);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    dv[j][r] = be[r] * x[j][r];
-                    l[r] = -en[r] * dv[j][r];
+                    x[i][r] *= be[r];
+                    po[i][r] = -en[i][r] * x[i][r];
                 }
-                store_planes(lt + (j * 16 + ln) * kTS + r0, kTPlane, l);
             }
-            __syncthreads();  // what goes into K^T and Q^T is
-
-            keep_tokens<CT>(keep.r + (bh * s.T + start) * kw, kw, len, row0, v0, lane, x);
-            store_rows<DT, CT, WHOLE>(p.grad_v, gt + row0 * VS * Elem<DT>::bytes, s, b, h, start, len, row0, v0, dv);
+            store_tokens<DT>(p.grad_v, s, b * s.T + start, len, h, col, lane, x);
 #pragma unroll
             for (int i = 0; i < ND; ++i)
 #pragma unroll
-                for (int j = 0; j < CT; ++j)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) S[i][j][r] *= end;
-#pragma unroll
-            for (int k = 0; k < kC; k += 32) {
-#pragma unroll
-                for (int j = 0; j < CT; ++j) f[j] = row_frag<3>(lt, kTPlane, kTS, j * 16, k, lane);
-#pragma unroll
-                for (int i = 0; i < ND; ++i) mma(S[i], col_frag<NP>(kt, kKPlane, KS, k, d0 + i * 16, lane), f);
-            }
-            if (kShare) {
-                __syncthreads();  // K is read
-                __syncthreads();  // Q is in its place
-            }
-#pragma unroll
-            for (int k = 0; k < kC; k += 32) {
-#pragma unroll
-                for (int j = 0; j < CT; ++j) f[j] = row_frag<3>(et, kTPlane, kTS, j * 16, k, lane);
-#pragma unroll
-                for (int i = 0; i < ND; ++i) mma(S[i], col_frag<NP>(qt, kKPlane, KS, k, d0 + i * 16, lane), f);
-            }
-            __syncthreads();  // and all of it is read
-            start = prev, len = plen, cut = first, first = pfirst;
+                for (int r = 0; r < 4; ++r) S[i][r] *= end;
+            add_tokens<NP>(S, kt, kKPlane, KS, split8(po[0], po[1]), split8(po[2], po[3]), lane);
         }
-        if (p.grad_h0)
-            each_state<ND, CT>(s, bh, d0, v0, lane, [&](int i, int j, int r, bool ok, int64_t at) {
-                if (ok) p.grad_h0[at] = cut ? 0.0f : S[i][j][r];
-            });
-        return;
-    }
-
-    Tile<DT, KP> kn, qn;
-    Tile<DT, W> on;
-    Gates gn;
-    auto load = [&](int start, int len) {
-        kn.load(block_rows(in.k, b, hk, start, len), in.k.st, 0, wd.k);
-        if (!kShare) qn.load(block_rows(in.q, b, hk, start, len), in.q.st, 0, wd.k);
-        on.load(block_rows(go, b, h, start, len), go.st, v0, wd.v);
-        gn.load(prep, bh * s.T + start, len);
-    };
-    load(start, len);
-    for (int c = n - 1; c >= 0; --c) {
-        int prev = 0, plen = 0;
-        if (c > 0) blocks.at(b, c - 1, prev, plen, first);
-        kn.store(kt, kKPlane, KS);
-        if (!kShare) qn.store(qt, kKPlane, KS);
-        on.store(ot, kOPlane, VS);
-        gn.store(gates);
-        __syncthreads();
-        if (kShare) qn.load(block_rows(in.q, b, hk, start, len), in.q.st, 0, wd.k);
-        load(prev, plen);
-        const f32x4 en = *reinterpret_cast<const f32x4*>(gates + r0);
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < CT; ++j) {
-            f32x4 e;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) e[r] = in.scale * en[r] * element<NP>(ot + (r0 + r) * VS + j * 16 + ln, kOPlane);
-            store_planes(et + (j * 16 + ln) * kTS + r0, kTPlane, e);
-        }
-        __syncthreads();
         if (kShare) {
-            __syncthreads();
+            __syncthreads();  // K is read
             qn.store(qt, kKPlane, KS);
             __syncthreads();
+            load(prev, plen);
         }
-        __syncthreads();
-        start = prev, len = plen;
+        if (works) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const f32x4 o = read_values<NP>(ot, kVPlane, VS, i * 16, w * 16, lane);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) x[i][r] = in.scale * en[i][r] * o[r];
+            }
+            add_tokens<NP>(S, qt, kKPlane, KS, split8(x[0], x[1]), split8(x[2], x[3]), lane);
+        }
+        __syncthreads();  // all of the block is read
+        start = prev, len = plen, cut = first, first = pfirst;
     }
+    if (p.grad_h0 && works)
+        each_state<ND>(s, bh, col, lane, [&](int i, int r, bool ok, int64_t at) {
+            if (ok) p.grad_h0[at] = cut ? 0.0f : S[i][r];
+        });
 }
 
-// Columns of a workgroup: 32, or 16 where fp32 tiles of K leave no room for
-// more, or where V has no more.
+// Wavefronts with columns that a workgroup has room for: fp32 tiles of more than
+// 192 rows leave LDS for four.
 template <int DT, int RT>
-constexpr int kMaxCT = DT == DT_F32 && RT >= 3 ? 1 : 2;
+constexpr int kMaxWaves = DT == DT_F32 && RT == 4 ? 4 : 8;
 
 template <class F>
 hipError_t by_rows(const DeltaShape& s, F f) {
@@ -591,50 +520,47 @@ hipError_t by_rows(const DeltaShape& s, F f) {
     }
 }
 
-// Whether rows of a [B, T, H, V] output are whole aligned vectors.
-bool whole(const DeltaShape& s, const void* p, int dtype) {
-    return (reinterpret_cast<uintptr_t>(p) | (uintptr_t)(s.V * (dtype == DT_F32 ? 4 : 2))) % 16 == 0;
+struct Spread {
+    int waves, groups;
+    dim3 grid;
+};
+
+// Columns are spread evenly over the workgroups of a head.
+Spread spread(const DeltaShape& s, int most) {
+    const int tiles = (s.V + 15) / 16, groups = (tiles + most - 1) / most, waves = (tiles + groups - 1) / groups;
+    return Spread{waves, groups, dim3((unsigned)((s.B * s.H + 7) / 8 * 8 * groups))};
 }
 
-dim3 walk_grid(const DeltaShape& s, int groups) { return dim3((unsigned)((s.B * s.H + 7) / 8 * 8 * groups)); }
-
-template <int DT, bool KEEP>
+template <int DT, bool KEEP, int NS>
 hipError_t walk(const DeltaShape& s, const DeltaIn& in, const Blocks& blocks, const Prep& prep, const DeltaFwd& out,
                 const Kept& keep, hipStream_t st) {
     const Widths wd{row_width(s.K, DT), row_width(s.V, DT)};
-    const bool rows = whole(s, out.out, DT);
     return by_rows(s, [&](auto rt) {
-        constexpr int RT = decltype(rt)::value, CT = kMaxCT<DT, RT>;
-        const int groups = (s.V + CT * 16 - 1) / (CT * 16);
-        if (KEEP || rows)
-            delta_walk<DT, RT, CT, KEEP, true><<<walk_grid(s, groups), kWalkThreads, 0, st>>>(s, in, blocks, prep, out, keep, groups, wd);
-        else
-            delta_walk<DT, RT, CT, KEEP, KEEP><<<walk_grid(s, groups), kWalkThreads, 0, st>>>(s, in, blocks, prep, out, keep, groups, wd);
+        constexpr int RT = decltype(rt)::value, NC = kMaxWaves<DT, RT>;
+        const Spread x = spread(s, NC);
+        delta_walk<DT, RT, NC, KEEP, NS><<<x.grid, kWalkThreads, 0, st>>>(s, in, blocks, prep, out, keep, x.groups, x.waves, wd);
         return hipGetLastError();
     });
 }
 
 hipError_t run_walk(const DeltaShape& s, const DeltaIn& in, const Blocks& blocks, const Prep& prep,
-                    const DeltaFwd& out, const Kept* keep, hipStream_t st) {
-    if (s.dtype == DT_BF16)
-        return keep ? walk<DT_BF16, true>(s, in, blocks, prep, out, *keep, st)
-                    : walk<DT_BF16, false>(s, in, blocks, prep, out, Kept{}, st);
-    return keep ? walk<DT_F32, true>(s, in, blocks, prep, out, *keep, st)
-                : walk<DT_F32, false>(s, in, blocks, prep, out, Kept{}, st);
+                    const DeltaFwd& out, const Kept* keep, int planes, hipStream_t st) {
+    if (s.dtype == DT_F32)
+        return keep ? walk<DT_F32, true, 3>(s, in, blocks, prep, out, *keep, st)
+                    : walk<DT_F32, false, 3>(s, in, blocks, prep, out, Kept{}, st);
+    if (keep) return walk<DT_BF16, true, 3>(s, in, blocks, prep, out, *keep, st);
+    return planes == 2 ? walk<DT_BF16, false, 2>(s, in, blocks, prep, out, Kept{}, st)
+                       : walk<DT_BF16, false, 3>(s, in, blocks, prep, out, Kept{}, st);
 }
 
 template <int DT>
 hipError_t walk_back(const DeltaShape& s, const DeltaIn& in, const Blocks& blocks, const Prep& prep, const DeltaBwd& p,
                      const HeadRows& go, const Kept& keep, hipStream_t st) {
     const Widths wd{row_width(s.K, DT), row_width(s.V, DT)};
-    const bool rows = whole(s, p.grad_v, DT);
     return by_rows(s, [&](auto rt) {
-        constexpr int RT = decltype(rt)::value, CT = kMaxCT<DT, RT>;
-        const int groups = (s.V + CT * 16 - 1) / (CT * 16);
-        if (rows)
-            delta_walk_back<DT, RT, CT, true><<<walk_grid(s, groups), kWalkThreads, 0, st>>>(s, in, blocks, prep, p, go, keep, groups, wd);
-        else
-            delta_walk_back<DT, RT, CT, false><<<walk_grid(s, groups), kWalkThreads, 0, st>>>(s, in, blocks, prep, p, go, keep, groups, wd);
+        constexpr int RT = decltype(rt)::value, NC = kMaxWaves<DT, RT>;
+        const Spread x = spread(s, NC);
+        delta_walk_back<DT, RT, NC><<<x.grid, kWalkThreads, 0, st>>>(s, in, blocks, prep, p, go, keep, x.groups, x.waves, wd);
         return hipGetLastError();
     });
 }
