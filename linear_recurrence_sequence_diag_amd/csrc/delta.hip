@@ -61,7 +61,7 @@ hipError_t begin(const DeltaShape& s, const DeltaIn& in, const void* grad_out, i
     pass->blocks = Blocks{starts, counts, (int)s.T};
     pass->prep = Prep{reinterpret_cast<f32x4*>(base + l.gates), f(l.gl), planes(l.inv), planes(l.att), planes(l.att_t),
                       planes(l.inv_t)};
-    pass->keep = Kept{f(l.x), f(l.r), f(l.s), f(l.ds), f(l.pq), f(l.pk)};
+    pass->keep = Kept{f(l.x), f(l.r), f(l.s), f(l.ds), reinterpret_cast<f32x4*>(base + l.sums)};
     auto whole = [&](HeadRows* rows, bool wanted, size_t o, int64_t heads, int n) {
         if (!wanted) return hipSuccess;
         const hipError_t e = run_copy(*rows, base + o, s.B, s.T, heads, n, s.dtype, st);

@@ -14,6 +14,12 @@
 // (q_i and the later k_i come with exp(G_i) everywhere, the earlier k with
 // exp(-G_j), which gives dG from the three sums.)  A workgroup takes the heads
 // that share its query/key head in turn, so their sums have a fixed order.
+//
+// A wavefront has 16 columns of q and k, and with them 16 rows of S and dS, which
+// are operands as they lie in memory; what all of them need (dO, R and X, 64
+// columns at a time, then PD, LD, K and Q) lies in LDS.  The products of tokens
+// with tokens are spread over the wavefronts a tile of 16x16 at a time while the
+// same columns are there.
 #include "delta_tile.hpp"
 #include "delta_ws.hpp"
 
@@ -21,30 +27,50 @@ namespace lrscan {
 namespace delta {
 
 constexpr int kWide = 512;    // threads of a workgroup
-constexpr int kVS = 32 + 8;   // elements of an LDS row of 32 columns
-constexpr int kGS = kC + 8;   // of 64
+constexpr int kGS = kC + 8;   // elements of an LDS row of 64
+constexpr int kGPlane = kC * kGS;
 
-// A wavefront has 16 of the block's tokens (wt) and half of the other side's tiles of 16 (wh).
-template <int DT>
-__global__ void __launch_bounds__(kWide) delta_grads(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaBwd p,
-                                                     HeadRows go, Kept keep, int wk, int wv, int slots) {
+template <int NA, int NB>
+__device__ __forceinline__ void mma_pair(f32x4& c0, f32x4& c1, const Frag<NA> (&a)[2], const Frag<NB>& b) {
+    f32x4 c[2] = {c0, c1};
+    mma(c, a, b);
+    c0 = c[0], c1 = c[1];
+}
+
+// TT: tiles of 16 tokens of a wavefront, 4, or 2 where K leaves half of the
+// wavefronts without columns.
+template <int DT, int TT>
+__global__ void __launch_bounds__(kWide, 2) delta_grads(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaBwd p,
+                                                        HeadRows go, Kept keep, int wk, int wv, int slots) {
     constexpr int NP = kPlanes<DT>;
-    constexpr int kVPlane = kC * kVS, kTPlane = kC * kGS;
-    // S (or X) and dS, 32 columns of 64 rows; in their place then 64 columns of K and Q
-    constexpr int kOperands = 2 * (3 * kVPlane > NP * kTPlane ? 3 * kVPlane : NP * kTPlane);
-    __shared__ __attribute__((aligned(16))) uint16_t ops[kOperands];
-    __shared__ __attribute__((aligned(16))) uint16_t pt[3 * kTPlane], lt[3 * kTPlane];  // PD, LD [j][i]
-    __shared__ __attribute__((aligned(16))) float enter[kC], leave[kC], beta[kC], gh[kC], gl[kC], dg[2 * kC];
+    constexpr int DN = 2 * TT;                       // tiles of columns of a workgroup
+    constexpr int kKS = DN * 16 + 8, kKPlane = kC * kKS;
+    constexpr int kRows = (6 + NP) * kGPlane;        // X, R, dO
+    constexpr int kTiles = 2 * NP * kKPlane;         // then K and Q
+    __shared__ __attribute__((aligned(16))) uint16_t ops[kRows > kTiles ? kRows : kTiles];
+    __shared__ __attribute__((aligned(16))) uint16_t pt[3 * kGPlane], lt[3 * kGPlane];  // PD, LD [j][i]
+    __shared__ __attribute__((aligned(16))) float gates[5 * kC];  // enter, leave, beta, G in two
+    __shared__ __attribute__((aligned(16))) float dg[DN * kC];
     __shared__ float ends[kWide / 64];
-    uint16_t *const st = ops, *const dt = ops + 3 * kVPlane, *const kb = ops, *const qb = ops + NP * kTPlane;
+    uint16_t *const xt = ops, *const rt = ops + 3 * kGPlane, *const ot = ops + 6 * kGPlane;
+    uint16_t *const kb = ops, *const qb = ops + NP * kKPlane;
+    const float *const enter = gates, *const leave = gates + kC, *const beta = gates + 2 * kC, *const gh = gates + 3 * kC,
+                *const gl = gates + 4 * kC;
     const int lane = threadIdx.x & 63, w = wave_number(), ln = lane & 15, lg = lane >> 4;
-    const int wt = w & 3, wh = w >> 2;
+    const int dt = w % DN, t0_ = w / DN * TT;  // the wavefront's tile of columns, and its first of tokens
     const int64_t bk = blockIdx.x / slots, b = bk / s.HK;
     const int hk = (int)(bk % s.HK), share = s.H / s.HK;
     const int n = blocks.count(b);
-    const int row = wt * 16 + ln;
     const int kw = kept_width(s.V);
-    const int sr = threadIdx.x >> 3, sc = (threadIdx.x & 7) * 4;  // four columns of a staged row
+    const int sr = threadIdx.x >> 3, sc = (threadIdx.x & 7) * 8;  // eight columns of a staged row
+    // tiles (i, j), j <= i, of the products of tokens with tokens: number w, and w + 8 of ten
+    int ti[2], tj[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int x = w + 8 * q;
+        ti[q] = x < 1 ? 0 : x < 3 ? 1 : x < 6 ? 2 : 3;
+        tj[q] = x - ti[q] * (ti[q] + 1) / 2;
+    }
 
     for (int c = blockIdx.x % slots; c < n; c += slots) {
         int start, len;
@@ -60,223 +86,239 @@ __global__ void __launch_bounds__(kWide) delta_grads(DeltaShape s, DeltaIn in, B
         const bool has_ds = next < s.T ? !cut : p.grad_last != nullptr;
         const int64_t nslots = state_slots(s.T);
         const Buffer krows = block_rows(in.k, b, hk, start, len), qrows = block_rows(in.q, b, hk, start, len);
-        for (int hh = 0; hh < share; ++hh) {
-            const int h = hk * share + hh;
-            const int64_t bh = b * s.H + h, t0 = bh * s.T + start;
-            const int64_t state = (int64_t)s.K * kw;
-            const Buffer S = buffer(keep.s + (bh * nslots + start / kC) * state, has_s ? state * 4 : 0);
-            const Buffer dS = buffer(keep.ds + (bh * nslots + (next < s.T ? next / kC : nslots - 1)) * state,
-                                     has_ds ? state * 4 : 0);
-            const Buffer orows = block_rows(go, b, h, start, len);
-            const Buffer xrows = buffer(keep.x + t0 * kw, (int64_t)len * kw * 4);
-            const Buffer rrows = buffer(keep.r + t0 * kw, (int64_t)len * kw * 4);
-
-            // ---- products of tokens with tokens ----
-            f32x4 dp[2], dl[2];  // tiles 2 i + wh of the other tokens
-#pragma unroll
-            for (int i = 0; i < 2; ++i) dp[i] = dl[i] = f32x4{0, 0, 0, 0};
-            f32x4 xs = __builtin_bit_cast(f32x4, load16(xrows, sc < kw ? (sr * kw + sc) * 4 : kNowhere));
-            Raw8<DT> o;
-            Raw8<DT_F32> r;
-            o.load(orows, row * (int)go.st, lg * 8, wv);
-            r.load(rrows, row * kw * 4, lg * 8, kw);
-            __syncthreads();
-            if (threadIdx.x < kC) {
-                const f32x4 g = __builtin_bit_cast(f32x4, load16(buffer(prep.gates + t0, len * 16), threadIdx.x * 16));
-                enter[threadIdx.x] = g[0], leave[threadIdx.x] = g[1], beta[threadIdx.x] = g[2], gh[threadIdx.x] = g[3];
-                gl[threadIdx.x] = load4(buffer(prep.gl + t0, len * 4), threadIdx.x * 4);
-            }
-            for (int v0 = 0; v0 < s.V; v0 += 32) {
-                store_planes(st + sr * kVS + sc, kVPlane, xs);
-                __syncthreads();
-                const Frag<NP> of = o.frag();
-                const Frag<3> rf = r.frag();
-                const int v1 = v0 + 32;
-                xs = __builtin_bit_cast(f32x4, load16(xrows, v1 + sc < kw ? (sr * kw + v1 + sc) * 4 : kNowhere));
-                o.load(orows, row * (int)go.st, v1 + lg * 8, wv);
-                r.load(rrows, row * kw * 4, v1 + lg * 8, kw);
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    if (2 * i + wh <= wt) {
-                        const Frag<3> xf = row_frag<3>(st, kVPlane, kVS, (2 * i + wh) * 16, 0, lane);
-                        mma(dp[i], of, xf);
-                        mma(dl[i], rf, xf);
-                    }
-                __syncthreads();
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int j = 2 * i + wh, col = j * 16 + ln;
-                f32x4 pd = {0, 0, 0, 0}, ld = {0, 0, 0, 0};
-                if (j <= wt) {
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int t = wt * 16 + lg * 4 + r;
-                        if (col > t) continue;
-                        const float d = beta[col] * expf((gh[t] - gh[col]) + (gl[t] - gl[col]));
-                        pd[r] = in.scale * d * dp[i][r];
-                        if (col < t)
-                            ld[r] = -beta[t] * d * dl[i][r];
-                        else if (t < len)
-                            p.grad_beta[(b * s.T + start + t) * s.H + h] = dl[i][r];  // R_t . X_t
-                    }
-                }
-                uint16_t* at = pt + col * kGS + wt * 16 + lg * 4;
-                store_planes(at, kTPlane, pd);
-                store_planes(lt + (at - pt), kTPlane, ld);
-            }
-
-            // ---- 64 columns of q and k at a time ----
-            float dgi[4] = {0, 0, 0, 0}, end = 0.0f;
-            for (int d0 = 0; d0 < s.K; d0 += 64) {
-                Raw8<DT> kn, qn;
-                {
-                    const int r = threadIdx.x >> 3, q = d0 + (threadIdx.x & 7) * 8;
-                    kn.load(krows, r * (int)in.k.st, q, wk);
-                    qn.load(qrows, r * (int)in.q.st, q, wk);
-                }
-                f32x4 dq[2], kl[2], kr[2], kd[2];  // tiles 2 wh + j of the columns
-#pragma unroll
-                for (int j = 0; j < 2; ++j) dq[j] = kl[j] = kr[j] = kd[j] = f32x4{0, 0, 0, 0};
-                f32x4 ss, ds;
-                Raw8<DT_F32> x;
+        for (int d0 = 0; d0 < s.K; d0 += 16 * DN) {
+            const int col = d0 + dt * 16 + ln;
+            const bool works = d0 + dt * 16 < s.K;
+            // sums over the heads that share this q and k, this thread's own
+            f32x4* const sums = keep.sums + (int64_t)blockIdx.x * 8 * kWide + threadIdx.x;
+            for (int hh = 0; hh < share; ++hh) {
+                const int h = hk * share + hh;
+                const int64_t bh = b * s.H + h, t0 = bh * s.T + start;
+                const int64_t state = (int64_t)s.K * kw;
+                const Buffer S = buffer(keep.s + (bh * nslots + start / kC) * state, has_s ? state * 4 : 0);
+                const Buffer dS = buffer(keep.ds + (bh * nslots + (next < s.T ? next / kC : nslots - 1)) * state,
+                                         has_ds ? state * 4 : 0);
+                const Buffer orows = block_rows(go, b, h, start, len);
+                const Buffer xrows = buffer(keep.x + t0 * kw, (int64_t)len * kw * 4);
+                const Buffer rrows = buffer(keep.r + t0 * kw, (int64_t)len * kw * 4);
+                Raw8<DT> o;
+                Raw8<DT_F32> r, x;
                 auto load = [&](int v0) {
-                    const uint32_t at = v0 + sc < kw ? ((d0 + sr) * kw + v0 + sc) * 4 : kNowhere;
-                    ss = __builtin_bit_cast(f32x4, load16(S, at));
-                    ds = __builtin_bit_cast(f32x4, load16(dS, at));
-                    o.load(orows, row * (int)go.st, v0 + lg * 8, wv);
-                    r.load(rrows, row * kw * 4, v0 + lg * 8, kw);
-                    x.load(xrows, row * kw * 4, v0 + lg * 8, kw);
+                    o.load(orows, sr * (int)go.st, v0 + sc, wv);
+                    r.load(rrows, sr * kw * 4, v0 + sc, kw);
+                    x.load(xrows, sr * kw * 4, v0 + sc, kw);
                 };
-                if (has_s || has_ds) {
-                    load(0);
-                    for (int v0 = 0; v0 < s.V; v0 += 32) {
-                        __syncthreads();
-                        float dot = 0.0f;
+                const f32x4 g = __builtin_bit_cast(f32x4, load16(buffer(prep.gates + t0, len * 16),
+                                                                 threadIdx.x < kC ? threadIdx.x * 16 : kNowhere));
+                const float gll = load4(buffer(prep.gl + t0, len * 4), threadIdx.x < kC ? threadIdx.x * 4 : kNowhere);
+                load(0);
+
+                f32x4 dp[2], dl[2], dq[TT], kl[TT], kr[TT];
+                float end = 0.0f;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) dot = fmaf(ss[i], ds[i], dot);
-                        end = fmaf(dot, enter[len - 1], end);
-                        store_planes(st + sr * kVS + sc, kVPlane, ss);
-                        store_planes(dt + sr * kVS + sc, kVPlane, ds);
-                        __syncthreads();
-                        const Frag<NP> of = o.frag();
-                        const Frag<3> rf = r.frag(), xf = x.frag();
-                        load(v0 + 32);
+                for (int i = 0; i < 2; ++i) dp[i] = dl[i] = f32x4{0, 0, 0, 0};
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const Frag<3> sf = row_frag<3>(st, kVPlane, kVS, (2 * wh + j) * 16, 0, lane);
-                            mma(dq[j], of, sf);
-                            mma(kl[j], rf, sf);
-                            mma(kd[j], xf, row_frag<3>(dt, kVPlane, kVS, (2 * wh + j) * 16, 0, lane));
+                for (int i = 0; i < TT; ++i) dq[i] = kl[i] = kr[i] = f32x4{0, 0, 0, 0};
+                for (int v0 = 0; v0 < s.V; v0 += 64) {
+                    Raw8<DT_F32> ss[2], es[2];  // this wavefront's rows of the states
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        ss[k].load(S, col * kw * 4, v0 + k * 32 + lg * 8, kw);
+                        es[k].load(dS, col * kw * 4, v0 + k * 32 + lg * 8, kw);
+                    }
+                    __syncthreads();  // what stood there is read
+                    if (v0 == 0 && threadIdx.x < kC) {
+                        const int i = threadIdx.x;
+                        gates[i] = g[0], gates[kC + i] = g[1], gates[2 * kC + i] = g[2], gates[3 * kC + i] = g[3];
+                        gates[4 * kC + i] = gll;
+                    }
+                    store_frag(ot + sr * kGS + sc, kGPlane, o.frag());
+                    store_frag(rt + sr * kGS + sc, kGPlane, r.frag());
+                    store_frag(xt + sr * kGS + sc, kGPlane, x.frag());
+                    __syncthreads();
+                    load(v0 + 64);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+                        if (q == 0 || w < 2) {
+#pragma unroll
+                            for (int k = 0; k < 64; k += 32) {
+                                const Frag<3> f = row_frag<3>(xt, kGPlane, kGS, tj[q] * 16, k, lane);
+                                mma(dp[q], row_frag<NP>(ot, kGPlane, kGS, ti[q] * 16, k, lane), f);
+                                mma(dl[q], row_frag<3>(rt, kGPlane, kGS, ti[q] * 16, k, lane), f);
+                            }
+                        }
+                    if (works && (has_s || has_ds)) {
+                        const float whole = enter[len - 1];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            float dot = 0.0f;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) dot = fmaf(ss[k].a[i], es[k].a[i], fmaf(ss[k].b[i], es[k].b[i], dot));
+                            // wavefronts that share columns count them once
+                            if (t0_ == 0) end = fmaf(dot, whole, end);
+                            const Frag<3> sf = ss[k].frag(), ef = es[k].frag();
+#pragma unroll
+                            for (int i = 0; i < TT; i += 2) {
+                                Frag<3> a[2];
+                                Frag<NP> e[2];
+#pragma unroll
+                                for (int j = 0; j < 2; ++j) {
+                                    a[j] = row_frag<3>(rt, kGPlane, kGS, (t0_ + i + j) * 16, k * 32, lane);
+                                    e[j] = row_frag<NP>(ot, kGPlane, kGS, (t0_ + i + j) * 16, k * 32, lane);
+                                }
+                                mma_pair(kl[i], kl[i + 1], a, sf);
+                                mma_pair(dq[i], dq[i + 1], e, sf);
+#pragma unroll
+                                for (int j = 0; j < 2; ++j)
+                                    a[j] = row_frag<3>(xt, kGPlane, kGS, (t0_ + i + j) * 16, k * 32, lane);
+                                mma_pair(kr[i], kr[i + 1], a, ef);
+                            }
                         }
                     }
+                }
+                Raw8<DT> kn[DN / 4], qn[DN / 4];
+#pragma unroll
+                for (int i = 0; i < DN / 4; ++i) {
+                    const int at = i * kWide + threadIdx.x, row = at / (DN * 2), q = at % (DN * 2) * 8;
+                    kn[i].load(krows, row * (int)in.k.st, d0 + q, wk);
+                    qn[i].load(qrows, row * (int)in.q.st, d0 + q, wk);
+                }
+                // PD and LD, columns of the earlier token; the tiles above the diagonal are not read
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+                    if (q == 0 || w < 2) {
+                        const int j = tj[q] * 16 + ln;
+                        f32x4 pd, ld;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int t = ti[q] * 16 + lg * 4 + e;
+                            const float d = beta[j] * expf((gh[t] - gh[j]) + (gl[t] - gl[j]));
+                            pd[e] = j <= t ? in.scale * d * dp[q][e] : 0.0f;
+                            ld[e] = j < t ? -beta[t] * d * dl[q][e] : 0.0f;
+                            if (j == t && t < len && d0 == 0) p.grad_beta[(b * s.T + start + t) * s.H + h] = dl[q][e];  // R_t . X_t
+                        }
+                        uint16_t* at = pt + j * kGS + ti[q] * 16 + lg * 4;
+                        store_planes(at, kGPlane, pd);
+                        store_planes(lt + (at - pt), kGPlane, ld);
+                        // of the two tiles that an operand of 32 spans, the one above the diagonal
+                        if (ti[q] == tj[q] && (ti[q] & 1)) {
+                            at -= 16;
+#pragma unroll
+                            for (int e = 0; e < 3; ++e)
+                                *reinterpret_cast<u32x2*>(at + e * kGPlane) = *reinterpret_cast<u32x2*>(lt + (at - pt) + e * kGPlane) =
+                                    u32x2{0, 0};
+                        }
+                    }
+                __syncthreads();
+#pragma unroll
+                for (int i = 0; i < DN / 4; ++i) {
+                    const int at = i * kWide + threadIdx.x, row = at / (DN * 2), q = at % (DN * 2) * 8;
+                    store_frag(kb + row * kKS + q, kKPlane, kn[i].frag());
+                    store_frag(qb + row * kKS + q, kKPlane, qn[i].frag());
                 }
                 __syncthreads();
-                {
-                    const int at = (threadIdx.x >> 3) * kGS + (threadIdx.x & 7) * 8;
-                    store_frag(kb + at, kTPlane, kn.frag());
-                    store_frag(qb + at, kTPlane, qn.frag());
+                f32x4 dgi[TT], tq[TT], tk[TT];
+#pragma unroll
+                for (int i = 0; i < TT; ++i) {
+                    dgi[i] = tq[i] = tk[i] = f32x4{0, 0, 0, 0};
+                    if (hh) tq[i] = sums[2 * i * kWide], tk[i] = sums[(2 * i + 1) * kWide];
                 }
+                if (works) {
+#pragma unroll
+                    for (int i = 0; i < TT; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int t = (t0_ + i) * 16 + lg * 4 + e;
+                            dq[i][e] *= in.scale * enter[t];
+                            kl[i][e] *= -beta[t] * enter[t];
+                            kr[i][e] *= leave[t] * beta[t];
+                            end = fmaf(element<NP>(kb + t * kKS + dt * 16 + ln, kKPlane), kr[i][e], end);
+                        }
+#pragma unroll
+                    for (int ks = 0; ks < 2; ++ks) {
+                        const Frag<NP> kf = col_frag<NP>(kb, kKPlane, kKS, ks * 32, dt * 16, lane);
+                        const Frag<NP> qf = col_frag<NP>(qb, kKPlane, kKS, ks * 32, dt * 16, lane);
+#pragma unroll
+                        for (int i = 0; i < TT; ++i) {
+                            const int t = t0_ + i;
+                            if (ks == 0 || t >= 2) {
+                                mma(dq[i], col_frag<3>(pt, kGPlane, kGS, ks * 32, t * 16, lane), kf);
+                                mma(kl[i], col_frag<3>(lt, kGPlane, kGS, ks * 32, t * 16, lane), kf);
+                            }
+                            if (ks == 1 || t < 2) {
+                                mma(kr[i], row_frag<3>(pt, kGPlane, kGS, t * 16, ks * 32, lane), qf);
+                                mma(kr[i], row_frag<3>(lt, kGPlane, kGS, t * 16, ks * 32, lane), kf);
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < TT; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int at = ((t0_ + i) * 16 + lg * 4 + e) * kKS + dt * 16 + ln;
+                            const float k = element<NP>(kb + at, kKPlane), q = element<NP>(qb + at, kKPlane);
+                            dgi[i][e] = fmaf(q, dq[i][e], k * (kl[i][e] - kr[i][e]));
+                            tq[i][e] += dq[i][e];
+                            tk[i][e] += kl[i][e] + kr[i][e];
+                        }
+                    if (hh + 1 < share) {
+#pragma unroll
+                        for (int i = 0; i < TT; ++i) sums[2 * i * kWide] = tq[i], sums[(2 * i + 1) * kWide] = tk[i];
+                    } else {
+                        store_tokens<DT, TT>(p.grad_q, b * s.T + start, len, s.HK, hk, s.K, t0_ * 16, col, lane, tq);
+                        store_tokens<DT, TT>(p.grad_k, b * s.T + start, len, s.HK, hk, s.K, t0_ * 16, col, lane, tk);
+                    }
+                }
+#pragma unroll
+                for (int m = 1; m < 16; m *= 2)
+#pragma unroll
+                    for (int i = 0; i < TT; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) dgi[i][e] += __shfl_xor(dgi[i][e], m);
+#pragma unroll
+                for (int m = 1; m < 64; m *= 2) end += __shfl_xor(end, m);
+#pragma unroll
+                for (int i = 0; i < TT; ++i)
+                    if (ln == 0) *reinterpret_cast<f32x4*>(dg + dt * kC + (t0_ + i) * 16 + lg * 4) = dgi[i];
+                if (lane == 0) ends[w] = end;
                 __syncthreads();
+                if (w == 0) {
+                    float x = 0.0f;
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                    for (int i = 0; i < DN; ++i) x += dg[i * kC + lane];
+                    if (lane >= len) x = 0.0f;
+                    if (lane == len - 1)
+                        x += ((ends[0] + ends[1]) + (ends[2] + ends[3])) + ((ends[4] + ends[5]) + (ends[6] + ends[7]));
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int t = wt * 16 + lg * 4 + r;
-                        dq[j][r] *= in.scale * enter[t];
-                        kl[j][r] *= -beta[t] * enter[t];
-                        kd[j][r] *= leave[t] * beta[t];
+                    for (int m = 1; m < 64; m *= 2) {
+                        const float y = __shfl_down(x, m);
+                        if (lane + m < 64) x += y;
                     }
-#pragma unroll
-                for (int ks = 0; ks < 2; ++ks) {
-                    const bool low = ks == 0 || wt >= 2, high = ks == 1 || wt < 2;
-                    Frag<NP> kf[2], qf[2];
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        kf[j] = col_frag<NP>(kb, kTPlane, kGS, ks * 32, (2 * wh + j) * 16, lane);
-                        qf[j] = col_frag<NP>(qb, kTPlane, kGS, ks * 32, (2 * wh + j) * 16, lane);
-                    }
-                    if (low) {
-                        const Frag<3> a = col_frag<3>(pt, kTPlane, kGS, ks * 32, wt * 16, lane);
-                        const Frag<3> l = col_frag<3>(lt, kTPlane, kGS, ks * 32, wt * 16, lane);
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            mma(dq[j], a, kf[j]);
-                            mma(kl[j], l, kf[j]);
-                        }
-                    }
-                    if (high) {
-                        const Frag<3> a = row_frag<3>(pt, kTPlane, kGS, wt * 16, ks * 32, lane);
-                        const Frag<3> l = row_frag<3>(lt, kTPlane, kGS, wt * 16, ks * 32, lane);
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            mma(kr[j], a, qf[j]);
-                            mma(kr[j], l, kf[j]);
-                        }
-                    }
+                    if (!has_s && lane == 0) x = 0.0f;  // nothing entered for it to decay
+                    float* to = p.grad_g + (b * s.T + start + lane) * s.H + h;
+                    if (lane < len) *to = d0 ? *to + x : x;  // of the columns before
                 }
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int lc = (2 * wh + j) * 16 + ln, col = d0 + lc;
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int t = wt * 16 + lg * 4 + r;
-                        const float k = element<NP>(kb + t * kGS + lc, kTPlane), q = element<NP>(qb + t * kGS + lc, kTPlane);
-                        dgi[r] = fmaf(q, dq[j][r], dgi[r]);
-                        dgi[r] = fmaf(k, kl[j][r] - (kr[j][r] + kd[j][r]), dgi[r]);
-                        end = fmaf(k, kd[j][r], end);
-                        if (t >= len || col >= s.K) continue;
-                        const int64_t at = ((b * s.T + start + t) * s.HK + hk) * s.K + col;
-                        float gq = dq[j][r], gk = kl[j][r] + (kr[j][r] + kd[j][r]);
-                        if (hh) gq += keep.pq[at], gk += keep.pk[at];
-                        if (hh + 1 < share) {
-                            keep.pq[at] = gq, keep.pk[at] = gk;
-                        } else {
-                            put1<DT>(p.grad_q, at, gq);
-                            put1<DT>(p.grad_k, at, gk);
-                        }
-                    }
-                }
-                __syncthreads();
-            }
-#pragma unroll
-            for (int m = 1; m < 16; m *= 2)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) dgi[r] += __shfl_xor(dgi[r], m);
-#pragma unroll
-            for (int m = 1; m < 64; m *= 2) end += __shfl_xor(end, m);
-            if (ln == 0) *reinterpret_cast<f32x4*>(dg + wh * kC + wt * 16 + lg * 4) = f32x4{dgi[0], dgi[1], dgi[2], dgi[3]};
-            if (lane == 0) ends[w] = end;
-            __syncthreads();
-            if (w == 0) {
-                float x = lane < len ? dg[lane] + dg[kC + lane] : 0.0f;
-                if (lane == len - 1)
-                    x += ((ends[0] + ends[1]) + (ends[2] + ends[3])) + ((ends[4] + ends[5]) + (ends[6] + ends[7]));
-#pragma unroll
-                for (int m = 1; m < 64; m *= 2) {
-                    const float y = __shfl_down(x, m);
-                    if (lane + m < 64) x += y;
-                }
-                if (!has_s && lane == 0) x = 0.0f;  // nothing entered for it to decay
-                if (lane < len) p.grad_g[(b * s.T + start + lane) * s.H + h] = x;
             }
         }
     }
 }
 
-template <int DT>
+template <int DT, int TT>
 hipError_t grads(const DeltaShape& s, const DeltaIn& in, const Blocks& blocks, const Prep& prep, const DeltaBwd& p,
                  const HeadRows& go, const Kept& keep, hipStream_t st) {
     const int slots = (int)((s.T + kC - 1) / kC);
-    delta_grads<DT><<<dim3((unsigned)(s.B * s.HK * slots)), kWide, 0, st>>>(
+    delta_grads<DT, TT><<<dim3((unsigned)(s.B * s.HK * slots)), kWide, 0, st>>>(
         s, in, blocks, prep, p, go, keep, row_width(s.K, DT), row_width(s.V, DT), slots);
     return hipGetLastError();
 }
 
 hipError_t run_grads(const DeltaShape& s, const DeltaIn& in, const Blocks& blocks, const Prep& prep,
                      const DeltaBwd& p, const HeadRows& go, const Kept& keep, hipStream_t st) {
-    return s.dtype == DT_BF16 ? grads<DT_BF16>(s, in, blocks, prep, p, go, keep, st)
-                              : grads<DT_F32>(s, in, blocks, prep, p, go, keep, st);
+    if (s.K <= 64)
+        return s.dtype == DT_BF16 ? grads<DT_BF16, 2>(s, in, blocks, prep, p, go, keep, st)
+                                  : grads<DT_F32, 2>(s, in, blocks, prep, p, go, keep, st);
+    return s.dtype == DT_BF16 ? grads<DT_BF16, 4>(s, in, blocks, prep, p, go, keep, st)
+                              : grads<DT_F32, 4>(s, in, blocks, prep, p, go, keep, st);
 }
 
 }  // namespace delta

@@ -280,6 +280,27 @@ __device__ __forceinline__ float element(const uint16_t* at, int plane) {
     return x;
 }
 
+// A lane's column of N tiles of tokens, from the block's token row0 on, of a
+// contiguous [tokens, heads, width] output; what lies past the block's len tokens
+// or the row's columns is left out.
+template <int DT, int N>
+__device__ __forceinline__ void store_tokens(void* out, int64_t t0, int len, int heads, int h, int width, int row0, int col,
+                                             int lane, const f32x4 (&x)[N]) {
+    constexpr int E = Elem<DT>::bytes;
+    const int64_t step = (int64_t)heads * width * E;
+    const Buffer rows = buffer(static_cast<char*>(out) + t0 * step + (int64_t)h * width * E, len * step);
+    const uint32_t at = col < width ? (row0 + (lane >> 4) * 4) * (int)step + col * E : kNowhere;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            if constexpr (DT == DT_F32)
+                store4(rows, at, (i * 16 + r) * (int)step, x[i][r]);
+            else
+                __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16_bits(x[i][r]), rows, at, (i * 16 + r) * (int)step, 0);
+        }
+}
+
 // ---- the blocks of a batch row ----
 // Every block of up to kC tokens lies within one segment, so no product reaches
 // from one segment into another.  Without resets they start at multiples of kC.

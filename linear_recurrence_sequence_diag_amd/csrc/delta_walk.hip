@@ -95,9 +95,8 @@ struct Rows64 {
     }
 };
 
-// A lane's tokens of a column of a token scratch (rows of kw columns), of a state
-// scratch, and of a [tokens, heads, V] output; what lies past rows or columns is
-// left out.
+// A lane's tokens of a column of a token scratch (rows of kw columns) and of a state
+// scratch; what lies past rows or columns is left out.
 __device__ __forceinline__ void keep_tokens(float* to, int kw, int len, int col, int lane, const f32x4 (&x)[4]) {
     const Buffer rows = buffer(to, (int64_t)len * kw * 4);
     const uint32_t at = col < kw ? (uint32_t)(((lane >> 4) * 4 * kw + col) * 4) : kNowhere;
@@ -115,24 +114,6 @@ __device__ __forceinline__ void keep_state(float* to, int K, int kw, int col, in
 #pragma unroll
         for (int r = 0; r < 4; ++r) store4(rows, at, (i * 16 + r) * kw * 4, x[i][r]);
 }
-template <int DT>
-__device__ __forceinline__ void store_tokens(void* out, const DeltaShape& s, int64_t t0, int len, int h, int col, int lane,
-                                             const f32x4 (&x)[4]) {
-    constexpr int E = Elem<DT>::bytes;
-    const int64_t step = (int64_t)s.H * s.V * E;
-    const Buffer rows = buffer(static_cast<char*>(out) + t0 * step + (int64_t)h * s.V * E, len * step);
-    const uint32_t at = col < s.V ? (lane >> 4) * 4 * (int)step + col * E : kNowhere;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            if constexpr (DT == DT_F32)
-                store4(rows, at, (i * 16 + r) * (int)step, x[i][r]);
-            else
-                __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16_bits(x[i][r]), rows, at, (i * 16 + r) * (int)step, 0);
-        }
-}
-
 // A column of a state [K, V] in or out of accumulators.
 template <int ND, class F>
 __device__ __forceinline__ void each_state(const DeltaShape& s, int64_t bh, int col, int lane, F f) {
@@ -331,7 +312,7 @@ delta_walk(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaFwd p, Kept 
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) qs[i][r] *= in.scale;
-                store_tokens<DT>(p.out, s, b * s.T + start, len, h, col, lane, qs);
+                store_tokens<DT, 4>(p.out, b * s.T + start, len, s.H, h, s.V, 0, col, lane, qs);
             }
 #pragma unroll
             for (int i = 0; i < ND; ++i)
@@ -474,7 +455,7 @@ delta_walk_back(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaBwd p, 
                     po[i][r] = -en[i][r] * x[i][r];
                 }
             }
-            store_tokens<DT>(p.grad_v, s, b * s.T + start, len, h, col, lane, x);
+            store_tokens<DT, 4>(p.grad_v, b * s.T + start, len, s.H, h, s.V, 0, col, lane, x);
 #pragma unroll
             for (int i = 0; i < ND; ++i)
 #pragma unroll

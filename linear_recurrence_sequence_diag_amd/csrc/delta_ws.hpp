@@ -33,7 +33,7 @@ inline bool rows_whole(const HeadRows& r, int width, int bytes) {
 
 // Byte offsets into a call's workspace.
 struct Layout {
-    size_t starts, counts, gates, gl, inv, att, att_t, inv_t, x, r, s, ds, pq, pk, q, k, v, go, total;
+    size_t starts, counts, gates, gl, inv, att, att_t, inv_t, x, r, s, ds, sums, q, k, v, go, total;
     Layout(const DeltaShape& d, bool backward, int planes, bool reset, const Copies& copy) {
         const size_t tokens = (size_t)d.B * d.H * d.T, bytes = d.dtype == DT_F32 ? 4 : 2;
         size_t at = 0;
@@ -54,9 +54,7 @@ struct Layout {
         const size_t state = (size_t)d.B * d.H * state_slots(d.T) * d.K * kept_width(d.V) * 4;
         take(s, state, backward);
         take(ds, state, backward);
-        const size_t part = (size_t)d.B * d.T * d.HK * d.K * 4;
-        take(pq, part, backward && d.H > d.HK);
-        take(pk, part, backward && d.H > d.HK);
+        take(sums, (size_t)d.B * d.HK * ((d.T + kC - 1) / kC) * 512 * 8 * 16, backward && d.H > d.HK);
         const size_t kr = (size_t)d.B * d.T * d.HK * row_width(d.K, d.dtype) * bytes, vr = tokens * row_width(d.V, d.dtype) * bytes;
         take(q, kr, copy.q);
         take(k, kr, copy.k);
@@ -68,9 +66,9 @@ struct Layout {
 
 // What the backward keeps between its passes, in fp32, in rows of kept_width(V).
 struct Kept {
-    float *x, *r;    // [B, H, T]: x of the forward, and the gradient of beta (x's right side)
-    float *s, *ds;   // [B, H, slots, K]: states that enter blocks, gradients that leave them
-    float *pq, *pk;  // [B, T, HK, K]: sums over the heads that share a query/key head so far
+    float *x, *r;   // [B, H, T]: x of the forward, and the gradient of beta (x's right side)
+    float *s, *ds;  // [B, H, slots, K]: states that enter blocks, gradients that leave them
+    f32x4* sums;    // a workgroup's 512 x 8: of q's and k's gradients over the heads that share a q and k so far
 };
 
 // Copies rows [B, T, heads, n] into contiguous ones of row_width(n), zeros behind.
