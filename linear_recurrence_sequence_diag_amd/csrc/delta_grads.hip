@@ -72,7 +72,8 @@ __global__ void __launch_bounds__(kWide, 2) delta_grads(DeltaShape s, DeltaIn in
         tj[q] = x - ti[q] * (ti[q] + 1) / 2;
     }
 
-    for (int c = blockIdx.x % slots; c < n; c += slots) {
+    // rows with more blocks than slots begin again at a slot of their own, so no XCD gets all of those
+    for (int c = (int)((blockIdx.x + bk) % slots); c < n; c += slots) {
         int start, len;
         bool first;
         blocks.at(b, c, start, len, first);
@@ -224,16 +225,21 @@ __global__ void __launch_bounds__(kWide, 2) delta_grads(DeltaShape s, DeltaIn in
                     if (hh) tq[i] = sums[2 * i * kWide], tk[i] = sums[(2 * i + 1) * kWide];
                 }
                 if (works) {
+                    f32x4 kv[TT];
 #pragma unroll
-                    for (int i = 0; i < TT; ++i)
+                    for (int i = 0; i < TT; ++i) {
+                        const int t = (t0_ + i) * 16 + lg * 4;
+                        const f32x4 en = *reinterpret_cast<const f32x4*>(enter + t), le = *reinterpret_cast<const f32x4*>(leave + t),
+                                    be = *reinterpret_cast<const f32x4*>(beta + t);
+                        kv[i] = read_values<NP>(kb, kKPlane, kKS, (t0_ + i) * 16, dt * 16, lane);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const int t = (t0_ + i) * 16 + lg * 4 + e;
-                            dq[i][e] *= in.scale * enter[t];
-                            kl[i][e] *= -beta[t] * enter[t];
-                            kr[i][e] *= leave[t] * beta[t];
-                            end = fmaf(element<NP>(kb + t * kKS + dt * 16 + ln, kKPlane), kr[i][e], end);
+                            dq[i][e] *= in.scale * en[e];
+                            kl[i][e] *= -be[e] * en[e];
+                            kr[i][e] *= le[e] * be[e];
+                            end = fmaf(kv[i][e], kr[i][e], end);
                         }
+                    }
 #pragma unroll
                     for (int ks = 0; ks < 2; ++ks) {
                         const Frag<NP> kf = col_frag<NP>(kb, kKPlane, kKS, ks * 32, dt * 16, lane);
@@ -252,15 +258,15 @@ __global__ void __launch_bounds__(kWide, 2) delta_grads(DeltaShape s, DeltaIn in
                         }
                     }
 #pragma unroll
-                    for (int i = 0; i < TT; ++i)
+                    for (int i = 0; i < TT; ++i) {
+                        const f32x4 qv = read_values<NP>(qb, kKPlane, kKS, (t0_ + i) * 16, dt * 16, lane);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const int at = ((t0_ + i) * 16 + lg * 4 + e) * kKS + dt * 16 + ln;
-                            const float k = element<NP>(kb + at, kKPlane), q = element<NP>(qb + at, kKPlane);
-                            dgi[i][e] = fmaf(q, dq[i][e], k * (kl[i][e] - kr[i][e]));
+                            dgi[i][e] = sum16(fmaf(qv[e], dq[i][e], kv[i][e] * (kl[i][e] - kr[i][e])));
                             tq[i][e] += dq[i][e];
                             tk[i][e] += kl[i][e] + kr[i][e];
                         }
+                    }
                     if (hh + 1 < share) {
 #pragma unroll
                         for (int i = 0; i < TT; ++i) sums[2 * i * kWide] = tq[i], sums[(2 * i + 1) * kWide] = tk[i];
@@ -269,12 +275,6 @@ __global__ void __launch_bounds__(kWide, 2) delta_grads(DeltaShape s, DeltaIn in
                         store_tokens<DT, TT>(p.grad_k, b * s.T + start, len, s.HK, hk, s.K, t0_ * 16, col, lane, tk);
                     }
                 }
-#pragma unroll
-                for (int m = 1; m < 16; m *= 2)
-#pragma unroll
-                    for (int i = 0; i < TT; ++i)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) dgi[i][e] += __shfl_xor(dgi[i][e], m);
 #pragma unroll
                 for (int m = 1; m < 64; m *= 2) end += __shfl_xor(end, m);
 #pragma unroll

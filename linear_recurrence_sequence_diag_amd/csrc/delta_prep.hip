@@ -102,7 +102,8 @@ __global__ void __launch_bounds__(kThreads) delta_prep(DeltaShape s, DeltaIn in,
     const int64_t bh = blockIdx.x / slots, b = bh / s.H;
     const int h = (int)(bh % s.H), hk = h / (s.H / s.HK);
     const int n = blocks.count(b);
-    for (int c = blockIdx.x % slots; c < n; c += slots) {
+    // rows with more blocks than slots begin again at a slot of their own, so no XCD gets all of those
+    for (int c = (int)((blockIdx.x + bh) % slots); c < n; c += slots) {
         int start, len;
         bool cut;
         blocks.at(b, c, start, len, cut);

@@ -301,6 +301,15 @@ __device__ __forceinline__ void store_tokens(void* out, int64_t t0, int len, int
         }
 }
 
+// The sum of a value over the 16 lanes of a column tile, in all of them.
+__device__ __forceinline__ float sum16(float x) {
+    x += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), 0x128, 0xf, 0xf, true));  // row_ror 8
+    x += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), 0x124, 0xf, 0xf, true));
+    x += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), 0x122, 0xf, 0xf, true));
+    x += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), 0x121, 0xf, 0xf, true));
+    return x;
+}
+
 // ---- the blocks of a batch row ----
 // Every block of up to kC tokens lies within one segment, so no product reaches
 // from one segment into another.  Without resets they start at multiples of kC.
