@@ -29,6 +29,7 @@ bool delta_fits(const DeltaShape& s) {
     if ((int64_t)s.H * s.V > (1 << 22) || (int64_t)s.HK * s.K > (1 << 22)) return false;  // 32-bit offsets in a block's rows
     const int64_t slots = (s.T + kC - 1) / kC, groups = (s.V + 15) / 16;
     const int64_t heads = s.B * s.H;  // B * T * H * V is within 2^40
+    // (parts are formed only of few heads: at most 256 in all)
     return heads <= ((int64_t)1 << 30) / groups && heads <= ((int64_t)1 << 30) / slots;
 }
 
@@ -45,6 +46,7 @@ struct Pass {
     Blocks blocks;
     Prep prep;
     Kept keep;
+    Parts parts;
 };
 
 hipError_t begin(const DeltaShape& s, const DeltaIn& in, const void* grad_out, int operands, void* ws, hipStream_t st,
@@ -62,6 +64,7 @@ hipError_t begin(const DeltaShape& s, const DeltaIn& in, const void* grad_out, i
     pass->prep = Prep{reinterpret_cast<f32x4*>(base + l.gates), f(l.gl), planes(l.inv), planes(l.att), planes(l.att_t),
                       planes(l.inv_t)};
     pass->keep = Kept{f(l.x), f(l.r), f(l.s), f(l.ds), reinterpret_cast<f32x4*>(base + l.sums)};
+    pass->parts = Parts{sequence_parts(s), f(l.between), f(l.behind), f(l.map), backward ? f(l.map_t) : nullptr};
     auto whole = [&](HeadRows* rows, bool wanted, size_t o, int64_t heads, int n) {
         if (!wanted) return hipSuccess;
         const hipError_t e = run_copy(*rows, base + o, s.B, s.T, heads, n, s.dtype, st);
@@ -87,16 +90,16 @@ hipError_t launch_delta_fwd(const DeltaShape& s, const DeltaIn& in, const DeltaF
     const int planes = operand_planes(s, p.last != nullptr);
     const hipError_t e = begin(s, in, nullptr, planes, ws, st, &pass);
     if (e != hipSuccess) return e;
-    return run_walk(s, pass.in, pass.blocks, pass.prep, p, nullptr, planes, st);
+    return run_walk(s, pass.in, pass.blocks, pass.prep, p, nullptr, pass.parts, planes, st);
 }
 
 hipError_t launch_delta_bwd(const DeltaShape& s, const DeltaIn& in, const DeltaBwd& p, void* ws, hipStream_t st) {
     Pass pass;
     hipError_t e = begin(s, in, p.grad_out, 3, ws, st, &pass);
     if (e != hipSuccess) return e;
-    e = run_walk(s, pass.in, pass.blocks, pass.prep, DeltaFwd{nullptr, nullptr}, &pass.keep, 3, st);
+    e = run_walk(s, pass.in, pass.blocks, pass.prep, DeltaFwd{nullptr, nullptr}, &pass.keep, pass.parts, 3, st);
     if (e != hipSuccess) return e;
-    e = run_walk_back(s, pass.in, pass.blocks, pass.prep, p, pass.go, pass.keep, st);
+    e = run_walk_back(s, pass.in, pass.blocks, pass.prep, p, pass.go, pass.keep, pass.parts, st);
     if (e != hipSuccess) return e;
     return run_grads(s, pass.in, pass.blocks, pass.prep, p, pass.go, pass.keep, st);
 }

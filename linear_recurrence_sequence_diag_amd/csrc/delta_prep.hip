@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(kScanThreads) delta_blocks(const uint8_t* rese
 constexpr int kS = kC + 4;  // floats of an LDS row
 
 template <int DT, bool BWD, int NS>
-__global__ void __launch_bounds__(kThreads) delta_prep(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, int slots,
+__global__ void __launch_bounds__(kThreads, DT == DT_BF16 ? 3 : 2) delta_prep(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, int slots,
                                                        int width) {
     constexpr int NP = kPlanes<DT>;
     // 128 columns (fp32: 64) of K and Q at a time, then the block's matrices

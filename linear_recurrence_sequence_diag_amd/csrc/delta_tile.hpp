@@ -135,18 +135,26 @@ constexpr uint32_t kNowhere = 0x80000000u;
 __device__ __forceinline__ Buffer buffer(const void* p, int64_t bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00020000);
 }
-__device__ __forceinline__ u32x4 load16(Buffer r, uint32_t at, uint32_t more = 0) {
-    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, at, more, 0));
+// The whole offset goes where the bounds check looks at it.
+__device__ __forceinline__ u32x4 load16(Buffer r, uint32_t at) {
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0));
 }
-__device__ __forceinline__ float load4(Buffer r, uint32_t at, uint32_t more = 0) {
-    return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, at, more, 0));
+__device__ __forceinline__ float load4(Buffer r, uint32_t at) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0));
 }
-__device__ __forceinline__ void store4(Buffer r, uint32_t at, uint32_t more, float x) {
-    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, x), r, at, more, 0);
+__device__ __forceinline__ void store4(Buffer r, uint32_t at, float x) {
+    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, x), r, at, 0, 0);
 }
 
 // The wavefront's number in its workgroup, as a scalar.
 __device__ __forceinline__ int wave_number() { return __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)); }
+
+// An offset formed anew for each block (`with`: something of the block's): sums of
+// it would otherwise stay in registers through a walk's loop, 16 and more of them.
+__device__ __forceinline__ uint32_t anew(uint32_t x, int64_t with) {
+    asm("" : "+v"(x) : "s"((uint32_t)with));
+    return x;
+}
 
 // The rows of one head of an operand that belong to a block.  Rows are whole
 // aligned vectors of 16 bytes (others were copied into such).
@@ -289,15 +297,15 @@ __device__ __forceinline__ void store_tokens(void* out, int64_t t0, int len, int
     constexpr int E = Elem<DT>::bytes;
     const int64_t step = (int64_t)heads * width * E;
     const Buffer rows = buffer(static_cast<char*>(out) + t0 * step + (int64_t)h * width * E, len * step);
-    const uint32_t at = col < width ? (row0 + (lane >> 4) * 4) * (int)step + col * E : kNowhere;
+    const uint32_t at = anew(col < width ? (row0 + (lane >> 4) * 4) * (int)step + col * E : kNowhere, t0);
 #pragma unroll
     for (int i = 0; i < N; ++i)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             if constexpr (DT == DT_F32)
-                store4(rows, at, (i * 16 + r) * (int)step, x[i][r]);
+                store4(rows, at + (i * 16 + r) * (int)step, x[i][r]);
             else
-                __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16_bits(x[i][r]), rows, at, (i * 16 + r) * (int)step, 0);
+                __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16_bits(x[i][r]), rows, at + (i * 16 + r) * (int)step, 0, 0);
         }
 }
 

@@ -24,13 +24,20 @@ constexpr int kWalkThreads = 512;
 constexpr int kTS = kC + 8;          // elements of an LDS row of 64
 constexpr int kTPlane = kC * kTS;
 
-// Workgroups of one head lie on one XCD, so its operands are read from memory
-// once: bh % 8 is the workgroup's number % 8.
-__device__ __forceinline__ bool my_head(const DeltaShape& s, int groups, int64_t& bh, int& group) {
-    const int64_t r = blockIdx.x >> 3;
+// Workgroups of one head and part lie on one XCD, so its operands are read from
+// memory once: the number of the two is the workgroup's number modulo 8.
+__device__ __forceinline__ bool my_part(const DeltaShape& s, int groups, int parts, int64_t& bh, int& part, int& group) {
+    const int64_t r = blockIdx.x >> 3, x = r / groups * 8 + (blockIdx.x & 7);
     group = (int)(r % groups);
-    bh = r / groups * 8 + (blockIdx.x & 7);
+    part = (int)(x % parts);
+    bh = x / parts;
     return bh < s.B * s.H;
+}
+
+// The blocks of a part: [first, end).
+__device__ __forceinline__ void part_blocks(int n, int part, int parts, int& first, int& end) {
+    first = (int)((int64_t)n * part / parts);
+    end = (int)((int64_t)n * (part + 1) / parts);
 }
 
 // A block's gates, [3][kC] in LDS.
@@ -99,21 +106,32 @@ struct Rows64 {
 // scratch; what lies past rows or columns is left out.
 __device__ __forceinline__ void keep_tokens(float* to, int kw, int len, int col, int lane, const f32x4 (&x)[4]) {
     const Buffer rows = buffer(to, (int64_t)len * kw * 4);
-    const uint32_t at = col < kw ? (uint32_t)(((lane >> 4) * 4 * kw + col) * 4) : kNowhere;
+    const uint32_t at = anew(col < kw ? (uint32_t)(((lane >> 4) * 4 * kw + col) * 4) : kNowhere, reinterpret_cast<intptr_t>(to));
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) store4(rows, at, (i * 16 + r) * kw * 4, x[i][r]);
+        for (int r = 0; r < 4; ++r) store4(rows, at + (i * 16 + r) * kw * 4, x[i][r]);
 }
 template <int ND>
 __device__ __forceinline__ void keep_state(float* to, int K, int kw, int col, int lane, const f32x4 (&x)[ND]) {
     const Buffer rows = buffer(to, (int64_t)K * kw * 4);
-    const uint32_t at = col < kw ? (uint32_t)(((lane >> 4) * 4 * kw + col) * 4) : kNowhere;
+    const uint32_t at = anew(col < kw ? (uint32_t)(((lane >> 4) * 4 * kw + col) * 4) : kNowhere, reinterpret_cast<intptr_t>(to));
 #pragma unroll
     for (int i = 0; i < ND; ++i)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) store4(rows, at, (i * 16 + r) * kw * 4, x[i][r]);
+        for (int r = 0; r < 4; ++r) store4(rows, at + (i * 16 + r) * kw * 4, x[i][r]);
 }
+// The same of a state scratch, into accumulators.
+template <int ND>
+__device__ __forceinline__ void take_state(const float* from, int K, int kw, int col, int lane, f32x4 (&x)[ND]) {
+    const Buffer rows = buffer(from, (int64_t)K * kw * 4);
+    const uint32_t at = anew(col < kw ? (uint32_t)(((lane >> 4) * 4 * kw + col) * 4) : kNowhere, reinterpret_cast<intptr_t>(from));
+#pragma unroll
+    for (int i = 0; i < ND; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[i][r] = load4(rows, at + (i * 16 + r) * kw * 4);
+}
+
 // A column of a state [K, V] in or out of accumulators.
 template <int ND, class F>
 __device__ __forceinline__ void each_state(const DeltaShape& s, int64_t bh, int col, int lane, F f) {
@@ -167,11 +185,17 @@ struct Widths {
     int k, v;
 };
 
+// What a walk leaves: outputs and the last state; x and the states that enter
+// blocks; or, of a part, the map from the state that enters it to the one that
+// leaves: columns of V from zero, then K columns of the identity with values of 0.
+enum Leaves { kOutputs, kKept, kSpan };
+
 // NC: wavefronts with columns, at most; the launch says how many.  NS: planes of
 // fp32 operands.
-template <int DT, int RT, int NC, bool KEEP, int NS>
+template <int DT, int RT, int NC, int LEAVES, int NS>
 __global__ void __launch_bounds__(kWalkThreads, 2)
-delta_walk(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaFwd p, Kept keep, int groups, int waves, Widths wd) {
+delta_walk(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaFwd p, Kept keep, Parts parts, int groups, int waves, Widths wd) {
+    constexpr bool KEEP = LEAVES != kOutputs;
     constexpr int NP = kPlanes<DT>;
     constexpr int ND = 4 * RT, KP = 64 * RT, KS = KP + 8, VS = 16 * NC + 8;
     constexpr int kKPlane = kC * KS, kVPlane = kC * VS;
@@ -186,16 +210,23 @@ delta_walk(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaFwd p, Kept 
     uint16_t *const qt = kShare ? kt : qt_, *const at = kShare ? it : at_;
 
     int64_t bh;
-    int group;
-    if (!my_head(s, groups, bh, group)) return;
+    int group, part;
+    // of the last part nothing needs the map, and of the first only where the initial state leads
+    if (!my_part(s, groups, LEAVES == kSpan ? parts.n - 1 : parts.n, bh, part, group)) return;
     const int64_t b = bh / s.H;
     const int h = (int)(bh % s.H), hk = h / (s.H / s.HK);
     const int lane = threadIdx.x & 63, w = wave_number(), ln = lane & 15, lg = lane >> 4;
     const int v0 = group * waves * 16, col = v0 + w * 16 + ln, kw = kept_width(s.V);
     const bool works = w < waves;
+    const int one = LEAVES == kSpan ? col - (s.V + 15) / 16 * 16 : -1;  // the column of the identity
 
     f32x4 S[ND];
-    each_state<ND>(s, bh, col, lane, [&](int i, int r, bool ok, int64_t at) { S[i][r] = works && in.h0 && ok ? in.h0[at] : 0.0f; });
+    if (LEAVES != kSpan && part > 0)
+        take_state<ND>(parts.enter + (bh * parts.n + part) * s.K * kw, s.K, kw, works ? col : kw, lane, S);
+    else
+        each_state<ND>(s, bh, col, lane, [&](int i, int r, bool ok, int64_t at) {
+            S[i][r] = works && part == 0 && in.h0 && ok ? in.h0[at] : i * 16 + lg * 4 + r == one ? 1.0f : 0.0f;
+        });
 
     Tile<DT, KP, true> kn, qn;
     Tile<DT, NC * 16, false> vn;
@@ -209,12 +240,13 @@ delta_walk(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaFwd p, Kept 
         tn.load(prep.inv, bh * s.T + start, len);
         if (!KEEP) an.load(prep.att, bh * s.T + start, len);
     };
-    const int n = blocks.count(b);
+    int from, n;
+    part_blocks(blocks.count(b), part, parts.n, from, n);
     int start, len;
     bool cut;
-    blocks.at(b, 0, start, len, cut);
+    blocks.at(b, from, start, len, cut);
     load(start, len);
-    for (int c = 0; c < n; ++c) {
+    for (int c = from; c < n; ++c) {
         // the next block; past the last one, one without tokens
         int next = s.T, nlen = 0;
         bool ncut = false;
@@ -235,7 +267,7 @@ delta_walk(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaFwd p, Kept 
             if (cut) {
 #pragma unroll
                 for (int i = 0; i < ND; ++i) S[i] = f32x4{0, 0, 0, 0};
-            } else if (KEEP) {
+            } else if (LEAVES == kKept) {
                 keep_state<ND>(keep.s + (bh * state_slots(s.T) + start / kC) * s.K * kw, s.K, kw, col, lane, S);
             }
         }
@@ -280,7 +312,7 @@ delta_walk(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaFwd p, Kept 
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[i] = f32x4{0, 0, 0, 0};
             triangle<NS, true>(x, it, split8<NS>(ks[0], ks[1]), split8<NS>(ks[2], ks[3]), lane);
-            if (KEEP) keep_tokens(keep.x + (bh * s.T + start) * kw, kw, len, col, lane, x);
+            if (LEAVES == kKept) keep_tokens(keep.x + (bh * s.T + start) * kw, kw, len, col, lane, x);
             f32x4 l[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -323,7 +355,24 @@ delta_walk(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaFwd p, Kept 
         __syncthreads();  // all of the block is read
         start = next, len = nlen, cut = ncut;
     }
-    if (!KEEP && p.last && works)
+    if (LEAVES == kSpan && works) {
+        if (one < 0) {
+            keep_state<ND>(parts.enter + (bh * parts.n + part + 1) * s.K * kw, s.K, kw, col, lane, S);
+        } else if (part > 0) {
+            const int64_t at = (bh * parts.n + part) * s.K * kept_width(s.K);
+            keep_state<ND>(parts.map + at, s.K, kept_width(s.K), one, lane, S);
+            if (parts.map_t) {
+                const Buffer rows = buffer(parts.map_t + at, (int64_t)s.K * kept_width(s.K) * 4);
+#pragma unroll
+                for (int i = 0; i < ND; ++i) {
+                    const int d = i * 16 + lg * 4;
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, S[i]), rows,
+                                                           d < kept_width(s.K) ? (one * kept_width(s.K) + d) * 4 : kNowhere, 0, 0);
+                }
+            }
+        }
+    }
+    if (!KEEP && p.last && works && part + 1 == parts.n)
         each_state<ND>(s, bh, col, lane, [&](int i, int r, bool ok, int64_t at) {
             if (ok) p.last[at] = S[i][r];
         });
@@ -334,10 +383,12 @@ delta_walk(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaFwd p, Kept 
 //   dU = scale P^T dO + leave K dS,  R = (I + diag(beta) M)^-T dU  (the gradient
 //   of beta (V - enter K S)),  dV = beta R,
 //   dS' = end dS + Q^T (scale enter dO) - K^T (beta enter R).
-template <int DT, int RT, int NC>
+// SPAN: of a part only the gradient that reaches the state entering it, from
+// nothing behind it (of the last part, from grad_last).
+template <int DT, int RT, int NC, bool SPAN>
 __global__ void __launch_bounds__(kWalkThreads, 2)
-delta_walk_back(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaBwd p, HeadRows go, Kept keep, int groups,
-                int waves, Widths wd) {
+delta_walk_back(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaBwd p, HeadRows go, Kept keep, Parts parts,
+                int groups, int waves, Widths wd) {
     constexpr int NP = kPlanes<DT>;
     constexpr int ND = 4 * RT, KP = 64 * RT, KS = KP + 8, VS = 16 * NC + 8;
     constexpr int kKPlane = kC * KS, kVPlane = kC * VS;
@@ -352,8 +403,9 @@ delta_walk_back(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaBwd p, 
     uint16_t *const qt = kShare ? kt : qt_, *const it = kShare ? at : it_;
 
     int64_t bh;
-    int group;
-    if (!my_head(s, groups, bh, group)) return;
+    int group, part;
+    if (!my_part(s, groups, SPAN ? parts.n - 1 : parts.n, bh, part, group)) return;
+    if (SPAN) ++part;  // nothing needs it of the first
     const int64_t b = bh / s.H;
     const int h = (int)(bh % s.H), hk = h / (s.H / s.HK);
     const int lane = threadIdx.x & 63, w = wave_number(), ln = lane & 15, lg = lane >> 4;
@@ -362,9 +414,12 @@ delta_walk_back(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaBwd p, 
     const int64_t slots = state_slots(s.T);
 
     f32x4 S[ND];
-    each_state<ND>(s, bh, col, lane, [&](int i, int r, bool ok, int64_t at) {
-        S[i][r] = works && p.grad_last && ok ? p.grad_last[at] : 0.0f;
-    });
+    if (!SPAN && part + 1 < parts.n)
+        take_state<ND>(parts.leave + (bh * parts.n + part) * s.K * kw, s.K, kw, works ? col : kw, lane, S);
+    else
+        each_state<ND>(s, bh, col, lane, [&](int i, int r, bool ok, int64_t at) {
+            S[i][r] = works && part + 1 == parts.n && p.grad_last && ok ? p.grad_last[at] : 0.0f;
+        });
 
     Tile<DT, KP, true> kn, qn;
     Tile<DT, NC * 16, false> on;
@@ -378,18 +433,19 @@ delta_walk_back(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaBwd p, 
         tn.load(prep.inv_t, bh * s.T + start, len);
         qn.load(block_rows(in.q, b, hk, start, len), in.q.st, 0, KP, wd.k);
     };
-    const int n = blocks.count(b);
+    int to, n;
+    part_blocks(blocks.count(b), part, parts.n, to, n);
     int start, len;
     bool first;  // whether a segment starts with the block
     blocks.at(b, n - 1, start, len, first);
     load(start, len);
     // what leaves a block enters the one behind it, unless a segment starts there
     bool cut = false;
-    for (int c = n - 1; c >= 0; --c) {
+    for (int c = n - 1; c >= to; --c) {
         const int behind = start + len;
         int prev = 0, plen = 0;
         bool pfirst = false;
-        if (c > 0) blocks.at(b, c - 1, prev, plen, pfirst);
+        if (c > to) blocks.at(b, c - 1, prev, plen, pfirst);
         gn.store(gates);
         kn.store(kt, kKPlane, KS);
         on.store(ot, kVPlane, VS);
@@ -408,7 +464,7 @@ delta_walk_back(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaBwd p, 
             if (cut) {
 #pragma unroll
                 for (int i = 0; i < ND; ++i) S[i] = f32x4{0, 0, 0, 0};
-            } else {
+            } else if (!SPAN) {
                 keep_state<ND>(keep.ds + (bh * slots + (behind < s.T ? behind / kC : slots - 1)) * s.K * kw, s.K, kw, col,
                                lane, S);
             }
@@ -445,7 +501,7 @@ delta_walk_back(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaBwd p, 
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[i] = f32x4{0, 0, 0, 0};
             triangle<3, false>(x, it, split8(po[0], po[1]), split8(po[2], po[3]), lane);
-            keep_tokens(keep.r + (bh * s.T + start) * kw, kw, len, col, lane, x);
+            if (!SPAN) keep_tokens(keep.r + (bh * s.T + start) * kw, kw, len, col, lane, x);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const f32x4 be = *reinterpret_cast<const f32x4*>(gates + 2 * kC + i * 16 + lg * 4);
@@ -455,7 +511,7 @@ delta_walk_back(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaBwd p, 
                     po[i][r] = -en[i][r] * x[i][r];
                 }
             }
-            store_tokens<DT, 4>(p.grad_v, b * s.T + start, len, s.H, h, s.V, 0, col, lane, x);
+            if (!SPAN) store_tokens<DT, 4>(p.grad_v, b * s.T + start, len, s.H, h, s.V, 0, col, lane, x);
 #pragma unroll
             for (int i = 0; i < ND; ++i)
 #pragma unroll
@@ -480,10 +536,84 @@ delta_walk_back(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaBwd p, 
         __syncthreads();  // all of the block is read
         start = prev, len = plen, cut = first, first = pfirst;
     }
-    if (p.grad_h0 && works)
+    if (SPAN && works) {
+        if (cut)
+#pragma unroll
+            for (int i = 0; i < ND; ++i) S[i] = f32x4{0, 0, 0, 0};
+        keep_state<ND>(parts.leave + (bh * parts.n + part - 1) * s.K * kw, s.K, kw, col, lane, S);
+    }
+    if (!SPAN && p.grad_h0 && works && part == 0)
         each_state<ND>(s, bh, col, lane, [&](int i, int r, bool ok, int64_t at) {
             if (ok) p.grad_h0[at] = cut ? 0.0f : S[i][r];
         });
+}
+
+// ---- parts of a long sequence ----
+//
+// A sequence over few heads is walked in parts at the same time: first every part's
+// map S -> A S + B is formed, then the states between parts, one after the other,
+// then each part is walked from its own.  The gradients' maps are the transposed
+// ones.  Here the states between: x[p + 1] += A_p x[p], forward, for p from 1 on,
+// or x[p - 1] += A_p^T x[p] back, for p from parts - 2 on; a workgroup has 16
+// columns of a head, its wavefronts tiles of 16 rows.
+constexpr int kJoinS = kDeltaMaxK + 8;
+
+template <bool BACK>
+__global__ void __launch_bounds__(kWalkThreads) delta_join(DeltaShape s, Parts parts, int tiles) {
+    __shared__ __attribute__((aligned(16))) uint16_t xs[2][3 * 16 * kJoinS];
+    const int64_t bh = blockIdx.x / tiles;
+    const int lane = threadIdx.x & 63, w = wave_number(), ln = lane & 15, lg = lane >> 4;
+    const int col = (int)(blockIdx.x % tiles) * 16 + ln, kw = kept_width(s.V), ka = kept_width(s.K);
+    const int64_t state = (int64_t)s.K * kw;
+    float* const x = (BACK ? parts.leave : parts.enter) + bh * parts.n * state;
+    const float* const map = (BACK ? parts.map_t : parts.map) + bh * parts.n * s.K * ka;
+    const int row_tiles = (s.K + 15) / 16;
+    auto tile_at = [&](int i) { return col < kw ? (uint32_t)(((i * 16 + lg * 4) * kw + col) * 4) : kNowhere; };
+    const int first = BACK ? parts.n - 2 : 1;
+    for (int i = w; i < kDeltaMaxK / 16; i += 8) {  // past the rows: zeros
+        f32x4 v = {0, 0, 0, 0};
+        if (i < row_tiles)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] = load4(buffer(x + first * state, state * 4), tile_at(i) + r * kw * 4);
+        store_planes(xs[0] + ln * kJoinS + i * 16 + lg * 4, 16 * kJoinS, v);
+        store_planes(xs[1] + ln * kJoinS + i * 16 + lg * 4, 16 * kJoinS, f32x4{0, 0, 0, 0});
+    }
+    __syncthreads();
+    for (int step = 0; step + 2 < parts.n; ++step) {
+        const int p = BACK ? parts.n - 2 - step : 1 + step, to = BACK ? p - 1 : p + 1;
+        const Buffer rows = buffer(map + (int64_t)p * s.K * ka, (int64_t)s.K * ka * 4), out = buffer(x + to * state, state * 4);
+        const uint16_t* now = xs[step & 1];
+        uint16_t* then = xs[1 - (step & 1)];
+        for (int i = w; i < row_tiles; i += 8) {
+            f32x4 c[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+#pragma unroll
+            for (int r = 0; r < 4; ++r) c[0][r] = load4(out, tile_at(i) + r * kw * 4);
+            for (int k = 0; k < s.K; k += 64)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    Raw8<DT_F32> a;
+                    a.load(rows, (i * 16 + ln) * ka * 4, k + j * 32 + lg * 8, ka);
+                    mma(c[j], a.frag(), row_frag<3>(now, 16 * kJoinS, kJoinS, 0, k + j * 32, lane));
+                }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                c[0][r] += c[1][r];
+                store4(out, tile_at(i) + r * kw * 4, c[0][r]);
+            }
+            store_planes(then + ln * kJoinS + i * 16 + lg * 4, 16 * kJoinS, c[0]);
+        }
+        __syncthreads();
+    }
+}
+
+hipError_t run_join(const DeltaShape& s, const Parts& parts, bool back, hipStream_t st) {
+    const int tiles = (s.V + 15) / 16;
+    if (parts.n < 3) return hipSuccess;
+    if (back)
+        delta_join<true><<<dim3((unsigned)(s.B * s.H * tiles)), kWalkThreads, 0, st>>>(s, parts, tiles);
+    else
+        delta_join<false><<<dim3((unsigned)(s.B * s.H * tiles)), kWalkThreads, 0, st>>>(s, parts, tiles);
+    return hipGetLastError();
 }
 
 // Wavefronts with columns that a workgroup has room for: fp32 tiles of more than
@@ -506,50 +636,76 @@ struct Spread {
     dim3 grid;
 };
 
-// Columns are spread evenly over the workgroups of a head.
-Spread spread(const DeltaShape& s, int most) {
-    const int tiles = (s.V + 15) / 16, groups = (tiles + most - 1) / most, waves = (tiles + groups - 1) / groups;
-    return Spread{waves, groups, dim3((unsigned)((s.B * s.H + 7) / 8 * 8 * groups))};
+// Columns are spread evenly over the workgroups of a head, on more of them than
+// need be where that leaves compute units idle: a block then takes less time
+// (us of a call, 8, 4, 2 and 1 wavefronts a workgroup: bf16 [1, 32768, 8 heads of
+// 128] 2505, 1718, 1611, 1583; fp32 [4, 1023, 16 heads of 64] reverse 282, 282,
+// 267, 264; but of 160 heads bf16 [8, 2048] 292, 342, 438, 660).
+Spread spread(const DeltaShape& s, int tiles, int parts, int most) {
+    const int64_t heads = s.B * s.H * parts, spare = kComputeUnits / heads;
+    int groups = (tiles + most - 1) / most;
+    if (spare > groups) groups = spare < tiles ? (int)spare : tiles;
+    const int waves = (tiles + groups - 1) / groups;
+    groups = (tiles + waves - 1) / waves;
+    return Spread{waves, groups, dim3((unsigned)((heads + 7) / 8 * 8 * groups))};
 }
 
-template <int DT, bool KEEP, int NS>
+template <int DT, int LEAVES, int NS>
 hipError_t walk(const DeltaShape& s, const DeltaIn& in, const Blocks& blocks, const Prep& prep, const DeltaFwd& out,
-                const Kept& keep, hipStream_t st) {
+                const Kept& keep, const Parts& parts, hipStream_t st) {
     const Widths wd{row_width(s.K, DT), row_width(s.V, DT)};
+    const int tiles = (s.V + 15) / 16 + (LEAVES == kSpan ? (s.K + 15) / 16 : 0);
     return by_rows(s, [&](auto rt) {
         constexpr int RT = decltype(rt)::value, NC = kMaxWaves<DT, RT>;
-        const Spread x = spread(s, NC);
-        delta_walk<DT, RT, NC, KEEP, NS><<<x.grid, kWalkThreads, 0, st>>>(s, in, blocks, prep, out, keep, x.groups, x.waves, wd);
+        const Spread x = spread(s, tiles, LEAVES == kSpan ? parts.n - 1 : parts.n, NC);
+        delta_walk<DT, RT, NC, LEAVES, NS>
+            <<<x.grid, kWalkThreads, 0, st>>>(s, in, blocks, prep, out, keep, parts, x.groups, x.waves, wd);
         return hipGetLastError();
     });
 }
 
 hipError_t run_walk(const DeltaShape& s, const DeltaIn& in, const Blocks& blocks, const Prep& prep,
-                    const DeltaFwd& out, const Kept* keep, int planes, hipStream_t st) {
+                    const DeltaFwd& out, const Kept* keep, const Parts& parts, int planes, hipStream_t st) {
+    if (parts.n > 1) {
+        const hipError_t e = s.dtype == DT_F32 ? walk<DT_F32, kSpan, 3>(s, in, blocks, prep, out, Kept{}, parts, st)
+                             : planes == 2     ? walk<DT_BF16, kSpan, 2>(s, in, blocks, prep, out, Kept{}, parts, st)
+                                               : walk<DT_BF16, kSpan, 3>(s, in, blocks, prep, out, Kept{}, parts, st);
+        if (e != hipSuccess) return e;
+        const hipError_t f = run_join(s, parts, false, st);
+        if (f != hipSuccess) return f;
+    }
     if (s.dtype == DT_F32)
-        return keep ? walk<DT_F32, true, 3>(s, in, blocks, prep, out, *keep, st)
-                    : walk<DT_F32, false, 3>(s, in, blocks, prep, out, Kept{}, st);
-    if (keep) return walk<DT_BF16, true, 3>(s, in, blocks, prep, out, *keep, st);
-    return planes == 2 ? walk<DT_BF16, false, 2>(s, in, blocks, prep, out, Kept{}, st)
-                       : walk<DT_BF16, false, 3>(s, in, blocks, prep, out, Kept{}, st);
+        return keep ? walk<DT_F32, kKept, 3>(s, in, blocks, prep, out, *keep, parts, st)
+                    : walk<DT_F32, kOutputs, 3>(s, in, blocks, prep, out, Kept{}, parts, st);
+    if (keep) return walk<DT_BF16, kKept, 3>(s, in, blocks, prep, out, *keep, parts, st);
+    return planes == 2 ? walk<DT_BF16, kOutputs, 2>(s, in, blocks, prep, out, Kept{}, parts, st)
+                       : walk<DT_BF16, kOutputs, 3>(s, in, blocks, prep, out, Kept{}, parts, st);
 }
 
-template <int DT>
+template <int DT, bool SPAN>
 hipError_t walk_back(const DeltaShape& s, const DeltaIn& in, const Blocks& blocks, const Prep& prep, const DeltaBwd& p,
-                     const HeadRows& go, const Kept& keep, hipStream_t st) {
+                     const HeadRows& go, const Kept& keep, const Parts& parts, hipStream_t st) {
     const Widths wd{row_width(s.K, DT), row_width(s.V, DT)};
     return by_rows(s, [&](auto rt) {
         constexpr int RT = decltype(rt)::value, NC = kMaxWaves<DT, RT>;
-        const Spread x = spread(s, NC);
-        delta_walk_back<DT, RT, NC><<<x.grid, kWalkThreads, 0, st>>>(s, in, blocks, prep, p, go, keep, x.groups, x.waves, wd);
+        const Spread x = spread(s, (s.V + 15) / 16, SPAN ? parts.n - 1 : parts.n, NC);
+        delta_walk_back<DT, RT, NC, SPAN>
+            <<<x.grid, kWalkThreads, 0, st>>>(s, in, blocks, prep, p, go, keep, parts, x.groups, x.waves, wd);
         return hipGetLastError();
     });
 }
 
 hipError_t run_walk_back(const DeltaShape& s, const DeltaIn& in, const Blocks& blocks, const Prep& prep,
-                         const DeltaBwd& p, const HeadRows& go, const Kept& keep, hipStream_t st) {
-    return s.dtype == DT_BF16 ? walk_back<DT_BF16>(s, in, blocks, prep, p, go, keep, st)
-                              : walk_back<DT_F32>(s, in, blocks, prep, p, go, keep, st);
+                         const DeltaBwd& p, const HeadRows& go, const Kept& keep, const Parts& parts, hipStream_t st) {
+    const bool wide = s.dtype == DT_F32;
+    if (parts.n > 1) {
+        hipError_t e = wide ? walk_back<DT_F32, true>(s, in, blocks, prep, p, go, keep, parts, st)
+                            : walk_back<DT_BF16, true>(s, in, blocks, prep, p, go, keep, parts, st);
+        if (e == hipSuccess) e = run_join(s, parts, true, st);
+        if (e != hipSuccess) return e;
+    }
+    return wide ? walk_back<DT_F32, false>(s, in, blocks, prep, p, go, keep, parts, st)
+                : walk_back<DT_BF16, false>(s, in, blocks, prep, p, go, keep, parts, st);
 }
 
 }  // namespace delta

@@ -20,6 +20,17 @@ inline int row_width(int n, int dtype) {
 // Columns of the scratch rows that the backward keeps.
 __host__ __device__ __forceinline__ int kept_width(int V) { return (V + 7) / 8 * 8; }
 
+constexpr int kComputeUnits = 256;
+
+// Parts of a sequence that are walked at the same time, where its heads leave most
+// compute units idle.  Forming the parts' maps takes about as long as the walk
+// itself, so it pays from three parts on, each of at least eight blocks.
+inline int sequence_parts(const DeltaShape& d) {
+    const int64_t units = d.B * d.H * ((d.V + 127) / 128), blocks = (d.T + kC - 1) / kC;
+    const int64_t parts = kComputeUnits / units < blocks / 8 ? kComputeUnits / units : blocks / 8;
+    return parts < 3 ? 1 : (int)parts;
+}
+
 // Operands whose rows are not whole aligned vectors, or lie too far apart for
 // 32-bit offsets within a block, are copied into rows that are.
 struct Copies {
@@ -33,7 +44,7 @@ inline bool rows_whole(const HeadRows& r, int width, int bytes) {
 
 // Byte offsets into a call's workspace.
 struct Layout {
-    size_t starts, counts, gates, gl, inv, att, att_t, inv_t, x, r, s, ds, sums, q, k, v, go, total;
+    size_t starts, counts, gates, gl, inv, att, att_t, inv_t, x, r, s, ds, sums, between, behind, map, map_t, q, k, v, go, total;
     Layout(const DeltaShape& d, bool backward, int planes, bool reset, const Copies& copy) {
         const size_t tokens = (size_t)d.B * d.H * d.T, bytes = d.dtype == DT_F32 ? 4 : 2;
         size_t at = 0;
@@ -55,6 +66,12 @@ struct Layout {
         take(s, state, backward);
         take(ds, state, backward);
         take(sums, (size_t)d.B * d.HK * ((d.T + kC - 1) / kC) * 512 * 8 * 16, backward && d.H > d.HK);
+        const int64_t parts = sequence_parts(d);
+        const size_t heads = (size_t)d.B * d.H * parts;
+        take(between, heads * d.K * kept_width(d.V) * 4, parts > 1);
+        take(behind, heads * d.K * kept_width(d.V) * 4, parts > 1 && backward);
+        take(map, heads * d.K * kept_width(d.K) * 4, parts > 1);
+        take(map_t, heads * d.K * kept_width(d.K) * 4, parts > 1 && backward);
         const size_t kr = (size_t)d.B * d.T * d.HK * row_width(d.K, d.dtype) * bytes, vr = tokens * row_width(d.V, d.dtype) * bytes;
         take(q, kr, copy.q);
         take(k, kr, copy.k);
@@ -71,6 +88,14 @@ struct Kept {
     f32x4* sums;    // a workgroup's 512 x 8: of q's and k's gradients over the heads that share a q and k so far
 };
 
+// Between the parts of a sequence, in fp32, [B, H, parts]: the state that enters a
+// part and the gradient of the one that leaves it (rows of kept_width(V)); the
+// parts' maps, and transposed (rows of kept_width(K)).
+struct Parts {
+    int n;
+    float *enter, *leave, *map, *map_t;
+};
+
 // Copies rows [B, T, heads, n] into contiguous ones of row_width(n), zeros behind.
 hipError_t run_copy(const HeadRows& from, void* to, int64_t B, int64_t T, int64_t heads, int n, int dtype, hipStream_t st);
 hipError_t run_blocks(const DeltaShape& s, const uint8_t* reset, int* starts, int* counts, hipStream_t st);
@@ -78,10 +103,10 @@ hipError_t run_prep(const DeltaShape& s, const DeltaIn& in, const Blocks& blocks
                     int planes, hipStream_t st);
 // The walk over the blocks: outputs and the last state, or (keep) x and the entering states.
 hipError_t run_walk(const DeltaShape& s, const DeltaIn& in, const Blocks& blocks, const Prep& prep,
-                    const DeltaFwd& out, const Kept* keep, int planes, hipStream_t st);
+                    const DeltaFwd& out, const Kept* keep, const Parts& parts, int planes, hipStream_t st);
 // The walk back: r, grad_v, the gradients that leave blocks, and grad_h0.
 hipError_t run_walk_back(const DeltaShape& s, const DeltaIn& in, const Blocks& blocks, const Prep& prep,
-                         const DeltaBwd& p, const HeadRows& go, const Kept& keep, hipStream_t st);
+                         const DeltaBwd& p, const HeadRows& go, const Kept& keep, const Parts& parts, hipStream_t st);
 // The other gradients, every block by itself.
 hipError_t run_grads(const DeltaShape& s, const DeltaIn& in, const Blocks& blocks, const Prep& prep,
                      const DeltaBwd& p, const HeadRows& go, const Kept& keep, hipStream_t st);
