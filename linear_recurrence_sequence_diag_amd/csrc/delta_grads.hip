@@ -58,8 +58,8 @@ __global__ void __launch_bounds__(kWide, 2) delta_grads(DeltaShape s, DeltaIn in
                 *const gl = gates + 4 * kC;
     const int lane = threadIdx.x & 63, w = wave_number(), ln = lane & 15, lg = lane >> 4;
     const int dt = w % DN, t0_ = w / DN * TT;  // the wavefront's tile of columns, and its first of tokens
-    const int64_t bk = blockIdx.x / slots, b = bk / s.HK;
-    const int hk = (int)(bk % s.HK), share = s.H / s.HK;
+    const int64_t bk = scalar((int)blockIdx.x / slots), b = scalar((int)bk / s.HK);
+    const int hk = scalar((int)bk % s.HK), share = scalar(s.H / s.HK);
     const int n = blocks.count(b);
     const int kw = kept_width(s.V);
     const int sr = threadIdx.x >> 3, sc = (threadIdx.x & 7) * 8;  // eight columns of a staged row
@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kWide, 2) delta_grads(DeltaShape s, DeltaIn in
     }
 
     // rows with more blocks than slots begin again at a slot of their own, so no XCD gets all of those
-    for (int c = (int)((blockIdx.x + bk) % slots); c < n; c += slots) {
+    for (int c = scalar((int)((blockIdx.x + bk) % slots)); c < n; c += slots) {
         int start, len;
         bool first;
         blocks.at(b, c, start, len, first);

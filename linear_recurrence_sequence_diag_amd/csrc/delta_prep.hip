@@ -99,11 +99,11 @@ __global__ void __launch_bounds__(kThreads, DT == DT_BF16 ? 3 : 2) delta_prep(De
     float *const M = N + kC * kS, *const Ti = M + kC * kS;  // M: the outputs' weights, forward
     float* const tmp = Ti + 32;  // the inverse's upper right quarter, which nothing reads
     const int lane = threadIdx.x & 63, w = wave_number(), ln = lane & 15, lg = lane >> 4;
-    const int64_t bh = blockIdx.x / slots, b = bh / s.H;
-    const int h = (int)(bh % s.H), hk = h / (s.H / s.HK);
+    const int64_t bh = scalar((int)blockIdx.x / slots), b = scalar((int)bh / s.H);
+    const int h = scalar((int)bh % s.H), hk = scalar(h / (s.H / s.HK));
     const int n = blocks.count(b);
     // rows with more blocks than slots begin again at a slot of their own, so no XCD gets all of those
-    for (int c = (int)((blockIdx.x + bh) % slots); c < n; c += slots) {
+    for (int c = scalar((int)((blockIdx.x + bh) % slots)); c < n; c += slots) {
         int start, len;
         bool cut;
         blocks.at(b, c, start, len, cut);

@@ -146,8 +146,12 @@ __device__ __forceinline__ void store4(Buffer r, uint32_t at, float x) {
     __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, x), r, at, 0, 0);
 }
 
-// The wavefront's number in its workgroup, as a scalar.
-__device__ __forceinline__ int wave_number() { return __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)); }
+// A value that is the same in all lanes, as a scalar (a division leaves it in
+// vector registers, and a buffer descriptor made from those takes a loop over the
+// lanes for every access).
+__device__ __forceinline__ int scalar(int x) { return __builtin_amdgcn_readfirstlane(x); }
+// The wavefront's number in its workgroup.
+__device__ __forceinline__ int wave_number() { return scalar((int)(threadIdx.x >> 6)); }
 
 // An offset formed anew for each block (`with`: something of the block's): sums of
 // it would otherwise stay in registers through a walk's loop, 16 and more of them.

@@ -27,17 +27,17 @@ constexpr int kTPlane = kC * kTS;
 // Workgroups of one head and part lie on one XCD, so its operands are read from
 // memory once: the number of the two is the workgroup's number modulo 8.
 __device__ __forceinline__ bool my_part(const DeltaShape& s, int groups, int parts, int64_t& bh, int& part, int& group) {
-    const int64_t r = blockIdx.x >> 3, x = r / groups * 8 + (blockIdx.x & 7);
-    group = (int)(r % groups);
-    part = (int)(x % parts);
-    bh = x / parts;
+    const int r = (int)(blockIdx.x >> 3), x = scalar(r / groups) * 8 + (int)(blockIdx.x & 7);
+    group = scalar(r % groups);
+    part = scalar(x % parts);
+    bh = scalar(x / parts);
     return bh < s.B * s.H;
 }
 
 // The blocks of a part: [first, end).
 __device__ __forceinline__ void part_blocks(int n, int part, int parts, int& first, int& end) {
-    first = (int)((int64_t)n * part / parts);
-    end = (int)((int64_t)n * (part + 1) / parts);
+    first = scalar((int)((int64_t)n * part / parts));
+    end = scalar((int)((int64_t)n * (part + 1) / parts));
 }
 
 // A block's gates, [3][kC] in LDS.
@@ -213,8 +213,8 @@ delta_walk(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaFwd p, Kept 
     int group, part;
     // of the last part nothing needs the map, and of the first only where the initial state leads
     if (!my_part(s, groups, LEAVES == kSpan ? parts.n - 1 : parts.n, bh, part, group)) return;
-    const int64_t b = bh / s.H;
-    const int h = (int)(bh % s.H), hk = h / (s.H / s.HK);
+    const int64_t b = scalar((int)bh / s.H);
+    const int h = scalar((int)bh % s.H), hk = scalar(h / (s.H / s.HK));
     const int lane = threadIdx.x & 63, w = wave_number(), ln = lane & 15, lg = lane >> 4;
     const int v0 = group * waves * 16, col = v0 + w * 16 + ln, kw = kept_width(s.V);
     const bool works = w < waves;
@@ -406,8 +406,8 @@ delta_walk_back(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaBwd p, 
     int group, part;
     if (!my_part(s, groups, SPAN ? parts.n - 1 : parts.n, bh, part, group)) return;
     if (SPAN) ++part;  // nothing needs it of the first
-    const int64_t b = bh / s.H;
-    const int h = (int)(bh % s.H), hk = h / (s.H / s.HK);
+    const int64_t b = scalar((int)bh / s.H);
+    const int h = scalar((int)bh % s.H), hk = scalar(h / (s.H / s.HK));
     const int lane = threadIdx.x & 63, w = wave_number(), ln = lane & 15, lg = lane >> 4;
     const int v0 = group * waves * 16, col = v0 + w * 16 + ln, kw = kept_width(s.V);
     const bool works = w < waves;
@@ -561,7 +561,7 @@ constexpr int kJoinS = kDeltaMaxK + 8;
 template <bool BACK>
 __global__ void __launch_bounds__(kWalkThreads) delta_join(DeltaShape s, Parts parts, int tiles) {
     __shared__ __attribute__((aligned(16))) uint16_t xs[2][3 * 16 * kJoinS];
-    const int64_t bh = blockIdx.x / tiles;
+    const int64_t bh = scalar((int)blockIdx.x / tiles);
     const int lane = threadIdx.x & 63, w = wave_number(), ln = lane & 15, lg = lane >> 4;
     const int col = (int)(blockIdx.x % tiles) * 16 + ln, kw = kept_width(s.V), ka = kept_width(s.K);
     const int64_t state = (int64_t)s.K * kw;
