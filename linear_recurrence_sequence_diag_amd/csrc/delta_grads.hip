@@ -194,8 +194,9 @@ __global__ void __launch_bounds__(kWide, 2) delta_grads(DeltaShape s, DeltaIn in
                         for (int e = 0; e < 4; ++e) {
                             const int t = ti[q] * 16 + lg * 4 + e;
                             const float d = beta[j] * expf((gh[t] - gh[j]) + (gl[t] - gl[j]));
-                            pd[e] = j <= t ? in.scale * d * dp[q][e] : 0.0f;
-                            ld[e] = j < t ? -beta[t] * d * dl[q][e] : 0.0f;
+                            // a token past the block has no gates, so its d may be infinite
+                            pd[e] = j <= t && t < len ? in.scale * d * dp[q][e] : 0.0f;
+                            ld[e] = j < t && t < len ? -beta[t] * d * dl[q][e] : 0.0f;
                             if (j == t && t < len && d0 == 0) p.grad_beta[(b * s.T + start + t) * s.H + h] = dl[q][e];  // R_t . X_t
                         }
                         uint16_t* at = pt + j * kGS + ti[q] * 16 + lg * 4;
