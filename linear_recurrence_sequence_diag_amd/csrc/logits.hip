@@ -33,97 +33,141 @@ __device__ __forceinline__ RowVec<DT> load_vec(const char* p) {
     return r;
 }
 
+// A sum as it stands in `named`: never the word that means none.
+__device__ __forceinline__ uint32_t bias_bits(float sum) {
+    const uint32_t w = __float_as_uint(sum);
+    return w == kNone ? 0x7fc00000u : w;
+}
+
 template <int DT, class I, bool COUNT, bool BIAS>
 __global__ void __launch_bounds__(kThreads) logits(LogitsArgs a, int slices) {
-    constexpr int N = Elem<DT>::V;
-    __shared__ uint32_t count[COUNT ? kSlice : 1];
-    __shared__ uint32_t named[BIAS ? kSlice : 1];
+    constexpr int N = Elem<DT>::V, PER = kSlice / N / kThreads;  // vectors of a thread
+    __shared__ __attribute__((aligned(16))) uint32_t count[COUNT ? kSlice : 4];
+    __shared__ __attribute__((aligned(16))) uint32_t named[BIAS ? kSlice : 4];
     __shared__ int twice;
     const int64_t b = blockIdx.x / slices;
     const int64_t v0 = (int64_t)(blockIdx.x % slices) * kSlice;
     const int n = (int)(a.V - v0 < kSlice ? a.V - v0 : kSlice);
+    const char* in = static_cast<const char*>(a.in) + (b * a.in_stride + v0) * Elem<DT>::bytes;
+    char* out = static_cast<char*>(a.out) + (b * a.out_stride + v0) * Elem<DT>::bytes;
+    const uint32_t* allowed = a.allowed ? a.allowed + b * ((a.V + 31) / 32) : nullptr;
+
+    // the slice's logits and mask are on their way while the history is counted
+    RowVec<DT> x[PER];
+    uint32_t open[PER];
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        const int i = (k * kThreads + threadIdx.x) * N;
+        if (i + N <= n) x[k] = load_vec<DT>(in + (int64_t)i * Elem<DT>::bytes);
+        // N entries share a word of the mask: v0 and i are multiples of N
+        open[k] = kNone;
+        if (allowed && i < n) open[k] = allowed[(v0 + i) >> 5] >> ((v0 + i) & 31);
+    }
+
+    const float rep = COUNT && a.repetition ? a.repetition[b] : 1.0f;
+    const float pres = COUNT && a.presence ? a.presence[b] : 0.0f;
+    const float freq = COUNT && a.frequency ? a.frequency[b] : 0.0f;
 
     if (COUNT || BIAS) {
-        for (int i = threadIdx.x; i < kSlice; i += kThreads) {
-            if (COUNT) count[i] = 0;
-            if (BIAS) named[i] = kNone;
+        // so are the first tokens of the history and the first entries of the list
+        const I* ids = static_cast<const I*>(a.bias_ids) + b * a.K;
+        const float* bias = a.bias + b * a.K;
+        const int64_t length = COUNT ? clamped<I>(a.lengths, b, a.L, a.L) : 0;
+        const int64_t prompt = COUNT ? clamped<I>(a.prompts, b, 0, a.L) : 0;
+        const I* t = static_cast<const I*>(a.tokens) + b * a.token_stride;
+        I id[4];
+        auto tokens = [&](int64_t i0) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) id[j] = i0 + j * kThreads < length ? t[i0 + j * kThreads] : I(-1);
+        };
+        tokens(threadIdx.x);
+        I mine = -1;
+        float value = 0.0f;
+        if (BIAS && threadIdx.x < a.K) mine = ids[threadIdx.x], value = bias[threadIdx.x];
+        for (int i = threadIdx.x * 4; i < kSlice; i += kThreads * 4) {
+            if (COUNT) *reinterpret_cast<uint4*>(count + i) = make_uint4(0, 0, 0, 0);
+            if (BIAS) *reinterpret_cast<uint4*>(named + i) = make_uint4(kNone, kNone, kNone, kNone);
         }
         if (threadIdx.x == 0) twice = 0;
         __syncthreads();
-        if (COUNT) {
-            const int64_t length = clamped<I>(a.lengths, b, a.L, a.L), prompt = clamped<I>(a.prompts, b, 0, a.L);
-            const I* t = static_cast<const I*>(a.tokens) + b * a.token_stride;
-            for (int64_t i = threadIdx.x; i < length; i += kThreads) {
-                const int64_t x = (int64_t)t[i] - v0;
-                if (x < 0 || x >= n) continue;
-                if (i < prompt)
-                    atomicOr(&count[x], kSeen);
-                else
-                    atomicAdd(&count[x], 1u);
+        if (COUNT)
+            for (int64_t i0 = threadIdx.x; i0 < length; i0 += 4 * kThreads) {
+                if (i0 >= kThreads) tokens(i0);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int64_t at = (int64_t)id[j] - v0;
+                    if (id[j] < 0 || at < 0 || at >= n) continue;
+                    if (i0 + j * kThreads < prompt)
+                        atomicOr(&count[at], kSeen);
+                    else
+                        atomicAdd(&count[at], 1u);
+                }
             }
-        }
-        const I* ids = static_cast<const I*>(a.bias_ids) + b * a.K;
-        const float* bias = a.bias + b * a.K;
+        // an entry's list position stands at its token, the first one's where there are several
         if (BIAS)
             for (int64_t i = threadIdx.x; i < a.K; i += kThreads) {
-                const int64_t x = (int64_t)ids[i] - v0;
-                if (x >= 0 && x < n) atomicMin(&named[x], (uint32_t)i);
+                const int64_t at = (int64_t)(i < kThreads ? mine : ids[i]) - v0;
+                if (at >= 0 && at < n && atomicMin(&named[at], (uint32_t)i) != kNone) twice = 1;
             }
         __syncthreads();
         if (BIAS) {
-            for (int64_t i = threadIdx.x; i < a.K; i += kThreads) {
-                const int64_t x = (int64_t)ids[i] - v0;
-                if (x >= 0 && x < n && named[x] != (uint32_t)i) twice = 1;
-            }
-            __syncthreads();
-            const bool again = twice != 0;
-            // an owner replaces its number by the sum; the others' test against it is behind them
-            for (int64_t i = threadIdx.x; i < a.K; i += kThreads) {
-                const int64_t x = (int64_t)ids[i] - v0;
-                if (x < 0 || x >= n) continue;
-                bool first = true;
-                if (again)
+            if (twice) {
+                // the first position's entry replaces it by the sum, once all have seen whose it is
+                for (int64_t i0 = 0; i0 < a.K; i0 += kThreads) {
+                    const int64_t i = i0 + threadIdx.x;
+                    const int64_t at = i < a.K ? (int64_t)ids[i] - v0 : -1;
+                    bool first = at >= 0 && at < n;
                     for (int64_t j = 0; j < i && first; ++j) first = ids[j] != ids[i];
-                if (!first) continue;
-                float sum = bias[i];
-                if (again)
+                    if (!first) continue;
+                    float sum = bias[i];
                     for (int64_t j = i + 1; j < a.K; ++j)
                         if (ids[j] == ids[i]) sum += bias[j];
-                const uint32_t bits = __float_as_uint(sum);
-                named[x] = bits == kNone ? 0x7fc00000u : bits;
+                    named[at] = bias_bits(sum);
+                }
+            } else {
+                for (int64_t i = threadIdx.x; i < a.K; i += kThreads) {
+                    const int64_t at = (int64_t)(i < kThreads ? mine : ids[i]) - v0;
+                    if (at >= 0 && at < n) named[at] = bias_bits(i < kThreads ? value : bias[i]);
+                }
             }
             __syncthreads();
         }
     }
-    const float rep = COUNT && a.repetition ? a.repetition[b] : 1.0f;
-    const float pres = COUNT && a.presence ? a.presence[b] : 0.0f;
-    const float freq = COUNT && a.frequency ? a.frequency[b] : 0.0f;
-    const uint32_t* allowed = a.allowed ? a.allowed + b * ((a.V + 31) / 32) : nullptr;
-    auto adjust = [&](float z, int i, bool open) {
-        if (COUNT) {
-            const uint32_t c = count[i];
-            if (c) {
-                if (a.repetition) z = z > 0.0f ? z / rep : z * rep;
-                const uint32_t times = c & ~kSeen;
-                if (times) {
-                    z -= freq * (float)times;
-                    z -= pres;
-                }
+    auto adjust = [&](float z, uint32_t c, uint32_t name) {
+        if (c) {
+            if (a.repetition) z = z > 0.0f ? z / rep : z * rep;
+            const uint32_t times = c & ~kSeen;
+            if (times) {
+                z -= freq * (float)times;
+                z -= pres;
             }
         }
-        if (BIAS && named[i] != kNone) z += __uint_as_float(named[i]);
-        return open ? z : -__builtin_inff();
+        return name != kNone ? z + __uint_as_float(name) : z;
     };
-    const char* in = static_cast<const char*>(a.in) + (b * a.in_stride + v0) * Elem<DT>::bytes;
-    char* out = static_cast<char*>(a.out) + (b * a.out_stride + v0) * Elem<DT>::bytes;
-    for (int i = threadIdx.x * N; i < n; i += kThreads * N) {
-        // N entries share a word of the mask: v0 and i are multiples of N
-        const uint32_t word = allowed ? allowed[(v0 + i) >> 5] >> ((v0 + i) & 31) : kNone;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        const int i = (k * kThreads + threadIdx.x) * N;
         if (i + N <= n) {
-            RowVec<DT> x = load_vec<DT>(in + (int64_t)i * Elem<DT>::bytes);
             float y[N];
 #pragma unroll
-            for (int j = 0; j < N; ++j) y[j] = adjust(x.get(j), i + j, word >> j & 1);
+            for (int j = 0; j < N; ++j) y[j] = x[k].get(j);
+            // whole words of the tables at a time; few entries stand in any of them
+            uint32_t c[N], name[N], any = 0, least = kNone;
+#pragma unroll
+            for (int j = 0; j < N; j += 4) {
+                uint4 u = make_uint4(0, 0, 0, 0), v = make_uint4(kNone, kNone, kNone, kNone);
+                if (COUNT) u = *reinterpret_cast<const uint4*>(count + i + j);
+                if (BIAS) v = *reinterpret_cast<const uint4*>(named + i + j);
+                c[j] = u.x, c[j + 1] = u.y, c[j + 2] = u.z, c[j + 3] = u.w;
+                name[j] = v.x, name[j + 1] = v.y, name[j + 2] = v.z, name[j + 3] = v.w;
+                any |= u.x | u.y | u.z | u.w;
+                least &= v.x & v.y & v.z & v.w;
+            }
+            if (any != 0 || least != kNone)
+#pragma unroll
+                for (int j = 0; j < N; ++j) y[j] = adjust(y[j], c[j], name[j]);
+#pragma unroll
+            for (int j = 0; j < N; ++j) y[j] = open[k] >> j & 1 ? y[j] : -__builtin_inff();
             uint32_t w[4];
             if constexpr (DT == DT_F32) {
 #pragma unroll
@@ -135,7 +179,9 @@ __global__ void __launch_bounds__(kThreads) logits(LogitsArgs a, int slices) {
             __builtin_memcpy(out + (int64_t)i * Elem<DT>::bytes, w, 16);
         } else {
             for (int j = 0; i + j < n; ++j) {
-                const float y = adjust(Elem<DT>::load1(in, i + j), i + j, word >> j & 1);
+                float y = Elem<DT>::load1(in, i + j);
+                y = adjust(y, COUNT ? count[i + j] : 0, BIAS ? named[i + j] : kNone);
+                y = open[k] >> j & 1 ? y : -__builtin_inff();
                 if constexpr (DT == DT_F32)
                     reinterpret_cast<float*>(out)[i + j] = y;
                 else
