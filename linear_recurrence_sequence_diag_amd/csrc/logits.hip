@@ -44,6 +44,8 @@ __global__ void __launch_bounds__(kThreads) logits(LogitsArgs a, int slices) {
     constexpr int N = Elem<DT>::V, PER = kSlice / N / kThreads;  // vectors of a thread
     __shared__ __attribute__((aligned(16))) uint32_t count[COUNT ? kSlice : 4];
     __shared__ __attribute__((aligned(16))) uint32_t named[BIAS ? kSlice : 4];
+    __shared__ int listed[BIAS ? kThreads : 1];
+    __shared__ float values[BIAS ? kThreads : 1];
     __shared__ int twice;
     const int64_t b = blockIdx.x / slices;
     const int64_t v0 = (int64_t)(blockIdx.x % slices) * kSlice;
@@ -111,7 +113,20 @@ __global__ void __launch_bounds__(kThreads) logits(LogitsArgs a, int slices) {
             }
         __syncthreads();
         if (BIAS) {
-            if (twice) {
+            if (twice && a.K <= kThreads) {
+                // the first position's entry adds those behind it in order, from LDS
+                const int64_t at = threadIdx.x < a.K ? (int64_t)mine - v0 : -1;
+                const bool first = at >= 0 && at < n && named[at] == threadIdx.x;
+                listed[threadIdx.x] = at >= 0 && at < n ? (int)at : -1;
+                values[threadIdx.x] = value;
+                __syncthreads();
+                if (first) {
+                    float sum = value;
+#pragma unroll 4
+                    for (int j = threadIdx.x + 1; j < (int)a.K; ++j) sum = listed[j] == (int)at ? sum + values[j] : sum;
+                    named[at] = bias_bits(sum);
+                }
+            } else if (twice) {
                 // the first position's entry replaces it by the sum, once all have seen whose it is
                 for (int64_t i0 = 0; i0 < a.K; i0 += kThreads) {
                     const int64_t i = i0 + threadIdx.x;
