@@ -1199,7 +1199,9 @@ def _adamw_class():
         """AdamW (decoupled weight decay) whose step is ``adamw_update`` on all params of
         a group that have a gradient.  ``state_bits`` 8 holds the states as e4m3 codes
         with a scale for each ADAMW_GROUP elements; ``master`` holds float32 weights
-        beside bfloat16 params.  ``step(grad_scale=...)`` multiplies the gradients."""
+        beside bfloat16 params.  ``step(grad_scale=...)`` multiplies the gradients.  The
+        count of steps is the host's, so a step is not captured into a graph (adamw_update
+        with ``step`` on the device is)."""
 
         def __init__(self, params, rate=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2,
                      state_bits=32, master=False):
@@ -1226,6 +1228,9 @@ def _adamw_class():
 
         @torch.no_grad()
         def step(self, closure=None, grad_scale=None):
+            if torch.cuda.is_available() and torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("a captured step would keep its number: capture adamw_update with "
+                                   "step on the device")
             loss = None
             if closure is not None:
                 with torch.enable_grad():
