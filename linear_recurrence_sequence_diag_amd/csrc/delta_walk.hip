@@ -199,8 +199,10 @@ delta_walk(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaFwd p, Kept 
     constexpr int NP = kPlanes<DT>;
     constexpr int ND = 4 * RT, KP = 64 * RT, KS = KP + 8, VS = 16 * NC + 8;
     constexpr int kKPlane = kC * KS, kVPlane = kC * VS;
-    // fp32 tiles take three planes each: Q lies where K will, the inverse where P will
-    constexpr bool kShare = DT == DT_F32;
+    // fp32 tiles take three planes each: of more than 64 rows Q lies where K will, the
+    // inverse where P will (of 64 with room for all, fp32 [4, 1023, 16 heads of 64]
+    // reverse 241 us a call for 248)
+    constexpr bool kShare = DT == DT_F32 && RT > 1;
     __shared__ __attribute__((aligned(16))) uint16_t kt[NP * kKPlane];
     __shared__ __attribute__((aligned(16))) uint16_t qt_[KEEP || kShare ? 8 : NP * kKPlane];
     __shared__ __attribute__((aligned(16))) uint16_t it[NS * kTPlane];
@@ -392,8 +394,8 @@ delta_walk_back(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaBwd p, 
     constexpr int NP = kPlanes<DT>;
     constexpr int ND = 4 * RT, KP = 64 * RT, KS = KP + 8, VS = 16 * NC + 8;
     constexpr int kKPlane = kC * KS, kVPlane = kC * VS;
-    // fp32: Q follows K in one place, the inverse P in another
-    constexpr bool kShare = DT == DT_F32;
+    // fp32 of more than 64 rows: Q follows K in one place, the inverse P in another
+    constexpr bool kShare = DT == DT_F32 && RT > 1;
     __shared__ __attribute__((aligned(16))) uint16_t kt[NP * kKPlane];
     __shared__ __attribute__((aligned(16))) uint16_t qt_[kShare ? 8 : NP * kKPlane];
     __shared__ __attribute__((aligned(16))) uint16_t at[3 * kTPlane];
@@ -555,65 +557,100 @@ delta_walk_back(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaBwd p, 
 // then each part is walked from its own.  The gradients' maps are the transposed
 // ones.  Here the states between: x[p + 1] += A_p x[p], forward, for p from 1 on,
 // or x[p - 1] += A_p^T x[p] back, for p from parts - 2 on; a workgroup has 16
-// columns of a head, its wavefronts tiles of 16 rows.
+// columns of a head, its wavefronts tiles of 16 rows.  A part that a segment starts
+// in passes nothing on, which no product says: what it is handed, and its map past
+// the start, may be infinite.
+// A step waits for the one before it, so its map is loaded while that one is at
+// work, where the registers hold both (bf16, 8 heads of 128: 2.5 us a step, 3.1
+// when loaded within it; what bounds it is a compute unit's 64 KB of map a step).
 constexpr int kJoinS = kDeltaMaxK + 8;
 
-template <bool BACK>
-__global__ void __launch_bounds__(kWalkThreads) delta_join(DeltaShape s, Parts parts, int tiles) {
+template <bool BACK, int RT>
+__global__ void __launch_bounds__(kWalkThreads, 2) delta_join(DeltaShape s, Blocks blocks, Parts parts, int tiles) {
+    constexpr int NT = RT > 2 ? 2 : 1, NK = 2 * RT;  // a wavefront's tiles, and their operands of 32
+    constexpr bool kAhead = RT <= 2;                 // registers hold two steps' maps
     __shared__ __attribute__((aligned(16))) uint16_t xs[2][3 * 16 * kJoinS];
-    const int64_t bh = scalar((int)blockIdx.x / tiles);
+    __shared__ bool barred[kComputeUnits];  // parts that a segment starts in
+    static_assert(kComputeUnits <= kWalkThreads, "a thread for each part");
+    // workgroups of a head lie on one XCD and read its maps once
+    const int r8 = (int)(blockIdx.x >> 3);
+    const int64_t bh = scalar(r8 / tiles * 8 + (int)(blockIdx.x & 7));
+    if (bh >= s.B * s.H) return;
     const int lane = threadIdx.x & 63, w = wave_number(), ln = lane & 15, lg = lane >> 4;
-    const int col = (int)(blockIdx.x % tiles) * 16 + ln, kw = kept_width(s.V), ka = kept_width(s.K);
+    const int col = r8 % tiles * 16 + ln, kw = kept_width(s.V), ka = kept_width(s.K);
     const int64_t state = (int64_t)s.K * kw;
     float* const x = (BACK ? parts.leave : parts.enter) + bh * parts.n * state;
     const float* const map = (BACK ? parts.map_t : parts.map) + bh * parts.n * s.K * ka;
-    const int row_tiles = (s.K + 15) / 16;
     auto tile_at = [&](int i) { return col < kw ? (uint32_t)(((i * 16 + lg * 4) * kw + col) * 4) : kNowhere; };
-    const int first = BACK ? parts.n - 2 : 1;
+    const int first = BACK ? parts.n - 2 : 1, by = BACK ? -1 : 1, steps = parts.n - 2;
+    if (threadIdx.x < parts.n) {
+        const int64_t b = bh / s.H, n = blocks.count(b);
+        bool any = false;
+        for (int64_t c = n * threadIdx.x / parts.n; c < n * (threadIdx.x + 1) / parts.n; ++c) {
+            int start, len;
+            bool cut;
+            blocks.at(b, (int)c, start, len, cut);
+            any = any || cut;
+        }
+        barred[threadIdx.x] = any;
+    }
     for (int i = w; i < kDeltaMaxK / 16; i += 8) {  // past the rows: zeros
-        f32x4 v = {0, 0, 0, 0};
-        if (i < row_tiles)
+        f32x4 v;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) v[r] = load4(buffer(x + first * state, state * 4), tile_at(i) + r * kw * 4);
+        for (int r = 0; r < 4; ++r) v[r] = load4(buffer(x + first * state, state * 4), tile_at(i) + r * kw * 4);
         store_planes(xs[0] + ln * kJoinS + i * 16 + lg * 4, 16 * kJoinS, v);
         store_planes(xs[1] + ln * kJoinS + i * 16 + lg * 4, 16 * kJoinS, f32x4{0, 0, 0, 0});
     }
-    __syncthreads();
-    for (int step = 0; step + 2 < parts.n; ++step) {
-        const int p = BACK ? parts.n - 2 - step : 1 + step, to = BACK ? p - 1 : p + 1;
-        const Buffer rows = buffer(map + (int64_t)p * s.K * ka, (int64_t)s.K * ka * 4), out = buffer(x + to * state, state * 4);
+    struct Operands {
+        Raw8<DT_F32> a[NT][NK];
+        f32x4 own[NT];
+    } x0, x1;
+    auto state_of = [&](int step) {  // nothing past the last step
+        return buffer(x + (first + by * (step + 1)) * state, step < steps ? state * 4 : 0);
+    };
+    auto load = [&](Operands& o, int step) {
+        const Buffer rows = buffer(map + (int64_t)(first + by * step) * s.K * ka, step < steps ? (int64_t)s.K * ka * 4 : 0);
+        const Buffer own = state_of(step);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+#pragma unroll
+            for (int j = 0; j < NK; ++j) o.a[t][j].load(rows, ((w + 8 * t) * 16 + ln) * ka * 4, j * 32 + lg * 8, ka);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) o.own[t][r] = load4(own, tile_at(w + 8 * t) + r * kw * 4);
+        }
+    };
+    auto join = [&](int step, Operands& o, Operands& next) {
+        const Buffer out = state_of(step);
+        const bool through = !barred[first + by * step];
         const uint16_t* now = xs[step & 1];
         uint16_t* then = xs[1 - (step & 1)];
-        for (int i = w; i < row_tiles; i += 8) {
+        if (kAhead) {
+            load(next, step + 1);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
             f32x4 c[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
 #pragma unroll
-            for (int r = 0; r < 4; ++r) c[0][r] = load4(out, tile_at(i) + r * kw * 4);
-            for (int k = 0; k < s.K; k += 64)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    Raw8<DT_F32> a;
-                    a.load(rows, (i * 16 + ln) * ka * 4, k + j * 32 + lg * 8, ka);
-                    mma(c[j], a.frag(), row_frag<3>(now, 16 * kJoinS, kJoinS, 0, k + j * 32, lane));
-                }
+            for (int j = 0; j < NK; ++j)
+                mma(c[j & 1], o.a[t][j].frag(), row_frag<3>(now, 16 * kJoinS, kJoinS, 0, j * 32, lane));
+            const int i = w + 8 * t;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                c[0][r] += c[1][r];
+                c[0][r] = o.own[t][r] + (through ? c[0][r] + c[1][r] : 0.0f);
                 store4(out, tile_at(i) + r * kw * 4, c[0][r]);
             }
             store_planes(then + ln * kJoinS + i * 16 + lg * 4, 16 * kJoinS, c[0]);
         }
+        if (!kAhead) load(o, step + 1);
         __syncthreads();
+    };
+    load(x0, 0);
+    __syncthreads();
+    for (int step = 0; step < steps; step += kAhead ? 2 : 1) {
+        join(step, x0, x1);
+        if (kAhead && step + 1 < steps) join(step + 1, x1, x0);
     }
-}
-
-hipError_t run_join(const DeltaShape& s, const Parts& parts, bool back, hipStream_t st) {
-    const int tiles = (s.V + 15) / 16;
-    if (parts.n < 3) return hipSuccess;
-    if (back)
-        delta_join<true><<<dim3((unsigned)(s.B * s.H * tiles)), kWalkThreads, 0, st>>>(s, parts, tiles);
-    else
-        delta_join<false><<<dim3((unsigned)(s.B * s.H * tiles)), kWalkThreads, 0, st>>>(s, parts, tiles);
-    return hipGetLastError();
 }
 
 // Wavefronts with columns that a workgroup has room for: fp32 tiles of more than
@@ -629,6 +666,20 @@ hipError_t by_rows(const DeltaShape& s, F f) {
         case 3: return f(std::integral_constant<int, 3>{});
         default: return f(std::integral_constant<int, 4>{});
     }
+}
+
+hipError_t run_join(const DeltaShape& s, const Blocks& blocks, const Parts& parts, bool back, hipStream_t st) {
+    if (parts.n < 3) return hipSuccess;
+    const int tiles = (s.V + 15) / 16;
+    const dim3 grid((unsigned)((s.B * s.H + 7) / 8 * 8 * tiles));
+    return by_rows(s, [&](auto rt) {
+        constexpr int RT = decltype(rt)::value;
+        if (back)
+            delta_join<true, RT><<<grid, kWalkThreads, 0, st>>>(s, blocks, parts, tiles);
+        else
+            delta_join<false, RT><<<grid, kWalkThreads, 0, st>>>(s, blocks, parts, tiles);
+        return hipGetLastError();
+    });
 }
 
 struct Spread {
@@ -671,7 +722,7 @@ hipError_t run_walk(const DeltaShape& s, const DeltaIn& in, const Blocks& blocks
                              : planes == 2     ? walk<DT_BF16, kSpan, 2>(s, in, blocks, prep, out, Kept{}, parts, st)
                                                : walk<DT_BF16, kSpan, 3>(s, in, blocks, prep, out, Kept{}, parts, st);
         if (e != hipSuccess) return e;
-        const hipError_t f = run_join(s, parts, false, st);
+        const hipError_t f = run_join(s, blocks, parts, false, st);
         if (f != hipSuccess) return f;
     }
     if (s.dtype == DT_F32)
@@ -701,7 +752,7 @@ hipError_t run_walk_back(const DeltaShape& s, const DeltaIn& in, const Blocks& b
     if (parts.n > 1) {
         hipError_t e = wide ? walk_back<DT_F32, true>(s, in, blocks, prep, p, go, keep, parts, st)
                             : walk_back<DT_BF16, true>(s, in, blocks, prep, p, go, keep, parts, st);
-        if (e == hipSuccess) e = run_join(s, parts, true, st);
+        if (e == hipSuccess) e = run_join(s, blocks, parts, true, st);
         if (e != hipSuccess) return e;
     }
     return wide ? walk_back<DT_F32, false>(s, in, blocks, prep, p, go, keep, parts, st)

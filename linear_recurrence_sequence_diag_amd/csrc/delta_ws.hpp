@@ -23,11 +23,20 @@ __host__ __device__ __forceinline__ int kept_width(int V) { return (V + 7) / 8 *
 constexpr int kComputeUnits = 256;
 
 // Parts of a sequence that are walked at the same time, where its heads leave most
-// compute units idle.  Forming the parts' maps takes about as long as the walk
-// itself, so it pays from three parts on, each of at least eight blocks.
+// compute units idle.  Forming the parts' maps, of K + V columns, takes as long as
+// the walk itself or longer, so it pays from three parts on whose maps find room at
+// once, of three blocks or more each; joining them takes a step for each part, so
+// there are no more than twice the root of the blocks.  us of a forward and of a
+// reverse call without parts and with them, B = 1, K = V = 128, bf16:
+//   8 heads, T = 800      54, 157     49, 141
+//   8 heads, T = 2048    111, 305     71, 191
+//   8 heads, T = 32768  1577, 5126   331, 1375
+//  32 heads, T = 1024     66, 219     64, 215
+//  43 heads, T = 2048    130, 560    151, 569 (in five parts, whose maps find no room at once)
 inline int sequence_parts(const DeltaShape& d) {
-    const int64_t units = d.B * d.H * ((d.V + 127) / 128), blocks = (d.T + kC - 1) / kC;
-    const int64_t parts = kComputeUnits / units < blocks / 8 ? kComputeUnits / units : blocks / 8;
+    const int64_t units = d.B * d.H * ((d.K + d.V + 127) / 128), blocks = (d.T + kC - 1) / kC;
+    int64_t parts = kComputeUnits / units < blocks / 3 ? kComputeUnits / units : blocks / 3;
+    while (parts * parts > 4 * blocks) --parts;
     return parts < 3 ? 1 : (int)parts;
 }
 

@@ -203,6 +203,30 @@ def test_segments_do_not_reach_each_other(dt, T):
     assert not torch.isfinite(lr.delta_scan(*args, h0=h0)[0]).any()
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_segments_that_end_in_any_part_do_not_reach_the_next(dt):
+    """A long row is walked in parts; segments with infinities and NaN end in, before and behind parts' ends."""
+    T = 2100
+    x, _, _, _ = _case(1, T, 2, 1, 64, 32, dt, seed=6)
+    cuts = list(range(0, 1000, 37)) + [1024, 1200, 1408, 1500, 1900]
+    reset = torch.zeros(1, T, dtype=torch.bool)
+    reset[:, cuts] = True
+    args = [x[n].cuda() for n in NAMES]
+    go, r = x["grad_out"].cuda(), reset.cuda()
+    want = lr.delta_scan(*args, reset=r)[:1] + lr.delta_scan_backward(*args, go, reset=r)[:5]
+    for odd in (0, 1):  # every other segment, the last ones among them
+        bad, g = [t.clone() for t in args], go.clone()
+        fine = torch.ones(T, dtype=torch.bool)
+        for lo, hi in list(zip(cuts, cuts[1:] + [T]))[odd::2]:
+            bad[1][:, lo:hi] = float("inf")
+            bad[2][:, hi - 1] = float("nan")
+            g[:, lo] = float("nan")
+            fine[lo:hi] = False
+        got = lr.delta_scan(*bad, reset=r)[:1] + lr.delta_scan_backward(*bad, g, reset=r)[:5]
+        for a, b in zip(want, got):
+            assert torch.equal(a[:, fine], b[:, fine])
+
+
 def test_gates_at_their_ends():
     """Decays of 0 and 1, of the type's lowest value and minus infinity, strengths of 0 and 1, against the walk."""
     x, _, _, _ = _case(2, 200, 2, 2, 32, 16, "f32", seed=7)
