@@ -137,7 +137,6 @@ __global__ void __launch_bounds__(kWide, 2) delta_grads(DeltaShape s, DeltaIn in
                     store_frag(rt + sr * kGS + sc, kGPlane, r.frag());
                     store_frag(xt + sr * kGS + sc, kGPlane, x.frag());
                     __syncthreads();
-                    load(v0 + 64);
 #pragma unroll
                     for (int q = 0; q < 2; ++q)
                         if (q == 0 || w < 2) {
@@ -176,6 +175,7 @@ __global__ void __launch_bounds__(kWide, 2) delta_grads(DeltaShape s, DeltaIn in
                             }
                         }
                     }
+                    load(v0 + 64);
                 }
                 Raw8<DT> kn[DN / 4], qn[DN / 4];
 #pragma unroll
