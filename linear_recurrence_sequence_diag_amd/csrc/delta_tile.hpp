@@ -108,14 +108,6 @@ __device__ __forceinline__ Frag<N> split8(f32x4 a, f32x4 b) {
     return f;
 }
 
-template <int N>
-__device__ __forceinline__ Frag<N> planes(const Frag<3>& f) {
-    Frag<N> x;
-#pragma unroll
-    for (int i = 0; i < N; ++i) x.p[i] = f.p[i];
-    return x;
-}
-
 // Four consecutive k of a column, into N planes `step` elements apart.
 template <int N = 3>
 __device__ __forceinline__ void store_planes(uint16_t* at, int step, f32x4 v) {
@@ -282,14 +274,6 @@ template <int NP>
 __device__ __forceinline__ void store_frag(uint16_t* at, int plane, const Frag<NP>& f) {
 #pragma unroll
     for (int i = 0; i < NP; ++i) *reinterpret_cast<u32x4*>(at + i * plane) = f.p[i];
-}
-
-// one element of a tile
-template <int NP>
-__device__ __forceinline__ float element(const uint16_t* at, int plane) {
-    float x = bf16_bits_to_f32(at[0]);
-    if constexpr (NP == 3) x += bf16_bits_to_f32(at[plane]) + bf16_bits_to_f32(at[2 * plane]);
-    return x;
 }
 
 // A lane's column of N tiles of tokens, from the block's token row0 on, of a

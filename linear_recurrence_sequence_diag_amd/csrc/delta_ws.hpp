@@ -105,8 +105,17 @@ struct Parts {
     float *enter, *leave, *map, *map_t;
 };
 
-// Copies rows [B, T, heads, n] into contiguous ones of row_width(n), zeros behind.
-hipError_t run_copy(const HeadRows& from, void* to, int64_t B, int64_t T, int64_t heads, int n, int dtype, hipStream_t st);
+// Copies of rows [B, T, heads, n] into contiguous ones of `width`, zeros behind.
+struct RowCopies {
+    struct One {
+        HeadRows from;
+        void* to;
+        int64_t heads, rows;
+        int n, width;
+    } of[4];
+    int count;
+};
+hipError_t run_copies(const RowCopies& copies, int64_t T, int dtype, hipStream_t st);
 hipError_t run_blocks(const DeltaShape& s, const uint8_t* reset, int* starts, int* counts, hipStream_t st);
 hipError_t run_prep(const DeltaShape& s, const DeltaIn& in, const Blocks& blocks, const Prep& prep, bool backward,
                     int planes, hipStream_t st);
