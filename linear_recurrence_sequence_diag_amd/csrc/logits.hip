@@ -127,17 +127,23 @@ __global__ void __launch_bounds__(kThreads) logits(LogitsArgs a, int slices) {
                     named[at] = bias_bits(sum);
                 }
             } else if (twice) {
-                // the first position's entry replaces it by the sum, once all have seen whose it is
+                // a longer list in pieces, each token's sum so far standing in `named`
+                for (int i = threadIdx.x; i < kSlice; i += kThreads) named[i] = kNone;
                 for (int64_t i0 = 0; i0 < a.K; i0 += kThreads) {
-                    const int64_t i = i0 + threadIdx.x;
-                    const int64_t at = i < a.K ? (int64_t)ids[i] - v0 : -1;
-                    bool first = at >= 0 && at < n;
-                    for (int64_t j = 0; j < i && first; ++j) first = ids[j] != ids[i];
-                    if (!first) continue;
-                    float sum = bias[i];
-                    for (int64_t j = i + 1; j < a.K; ++j)
-                        if (ids[j] == ids[i]) sum += bias[j];
-                    named[at] = bias_bits(sum);
+                    const int64_t i = i0 + threadIdx.x, at = i < a.K ? (int64_t)ids[i] - v0 : -1;
+                    const int here = at >= 0 && at < n ? (int)at : -1;
+                    const float own = i < a.K ? bias[i] : 0.0f;
+                    __syncthreads();  // the piece before is read
+                    listed[threadIdx.x] = here;
+                    values[threadIdx.x] = own;
+                    __syncthreads();
+                    bool first = here >= 0;
+                    for (int j = 0; j < (int)threadIdx.x && first; ++j) first = listed[j] != here;
+                    if (first) {
+                        float sum = named[here] == kNone ? own : __uint_as_float(named[here]) + own;
+                        for (int j = threadIdx.x + 1; j < kThreads; ++j) sum = listed[j] == here ? sum + values[j] : sum;
+                        named[here] = bias_bits(sum);
+                    }
                 }
             } else {
                 for (int64_t i = threadIdx.x; i < a.K; i += kThreads) {

@@ -432,3 +432,28 @@ def test_refusals():
     with pytest.raises(lr.LRScanError) as e:
         lr.delta_scan(*args, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
     assert e.value.status == -5
+
+
+def test_offsets_past_32_bits():
+    """A long row of many heads, over 2^31 values: behind its last reset it gives what a short call gives."""
+    T, H, K, V, tail = 560000, 32, 64, 128, 200
+    gen = torch.Generator(device="cuda").manual_seed(11)
+
+    def normal(*s):
+        return torch.randn(s, generator=gen, device="cuda", dtype=torch.bfloat16)
+
+    q, k = (torch.nn.functional.normalize(normal(1, T, 1, K), dim=-1) for _ in range(2))
+    v, go = normal(1, T, H, V), normal(1, T, H, V)
+    g = -0.1 * torch.rand(1, T, H, generator=gen, device="cuda")
+    beta = torch.rand(1, T, H, generator=gen, device="cuda")
+    reset = torch.zeros(1, T, dtype=torch.bool, device="cuda")
+    reset[:, [0, 1000, T - tail]] = True
+    args = (q, k, v, g, beta)
+    out = lr.delta_scan(*args, reset=reset, with_last=False)[0][:, T - tail:].clone()
+    grads = [t[:, T - tail:].clone() for t in lr.delta_scan_backward(*args, go, reset=reset)[:5]]
+    short = [t[:, T - tail:].contiguous() for t in args]
+    assert torch.equal(out, lr.delta_scan(*short, with_last=False)[0])
+    first = torch.zeros(1, tail, dtype=torch.bool, device="cuda")
+    first[:, 0] = True
+    want = lr.delta_scan_backward(*short, go[:, T - tail:].contiguous(), reset=first)[:5]
+    assert all(torch.equal(a, b) for a, b in zip(grads, want))

@@ -137,6 +137,20 @@ def test_the_same_token_many_times():
     assert torch.equal(y, lr.adjust_logits(x, **r))
 
 
+@pytest.mark.parametrize("K,V", [(512, 300), (513, 300), (1500, 900), (5000, 4200), (30000, 20000)])
+def test_long_lists_that_name_tokens_twice(K, V):
+    """Lists of one piece and of several, tokens named in some of them; of few names none stands more than 32 times."""
+    gen = torch.Generator().manual_seed(K)
+    x = torch.randn(3, V, generator=gen).cuda()
+    ids = torch.randint(-3, V + 3, (3, K), generator=gen)
+    assert torch.bincount(ids.clamp(0, V - 1).flatten(), minlength=V).max() <= 32 * 3
+    ids[0, 0] = ids[0, K - 1] = V - 1
+    rules = {"bias_ids": ids.cuda(), "bias": torch.randn(3, K, generator=gen).cuda()}
+    check(x, rules)
+    again = [lr.adjust_logits(x, **rules) for _ in range(3)]
+    assert all(torch.equal(again[0], y) for y in again[1:])
+
+
 def test_masks_that_leave_a_row_empty_and_logits_that_are_not_finite():
     x, r = make(3, 700, 50, 5, "f32", seed=3)
     r["allowed"][1] = 0
