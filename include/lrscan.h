@@ -410,16 +410,19 @@ LRSCAN_API size_t scan_embed_workspace_bytes(int64_t N, int64_t V, int64_t D, in
  *   out_t = scale S_t^T q_t.
  * q, k [B,T,HK,K] and v [B,T,H,V] of `dtype`; log_decay and beta [B,T,H] fp32;
  * value head h reads query/key head h / (H / HK) (H a multiple of HK).  K is at
- * most 256.  Queries and keys are taken as they are: with keys of norm 1 and
+ * most 256, H and V at most 65536, H V and HK K at most 2^22, T at most 2^30
+ * (LRSCAN_ERR_DIM).  Queries and keys are taken as they are: with keys of norm 1 and
  * beta in [0, 1] the state stays bounded.  A log_decay below -200 counts as
  * -200 (a decay of 0 in fp32).
  * At a reset step (opts->reset, [B,T]) the state that enters is dropped,
  * whatever it holds, and log_decay is not used; nothing of one segment reaches
  * another, be it an infinity or a NaN.  Within a segment an infinity may come
  * out as a NaN.
- * Tokens are taken in blocks of 64, whose products run on the matrix cores with
- * the accuracy of fp32 (every operand as the exact sum of bf16 parts); all sums
- * and states are fp32.
+ * Tokens are taken in blocks of 64, whose products run on the matrix cores; all
+ * sums and states are fp32.  A fp32 operand goes there as the sum of three bf16
+ * parts, which has the accuracy of fp32; of a bf16 forward without last, whose
+ * results are bf16 alone, as the sum of two (2^-18 of the value, below a hundredth
+ * of that rounding).  Calls repeat bit for bit.
  * `strides` (a host array, or NULL for contiguous) holds three numbers for each
  * operand, in elements: from one batch row, one step and one head to the next
  * (q, k and v may be parts of one projection).  None is negative; one may be 0.
