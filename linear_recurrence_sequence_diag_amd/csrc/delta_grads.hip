@@ -20,6 +20,12 @@
 // columns at a time, then PD, LD, K and Q) lies in LDS.  The products of tokens
 // with tokens are spread over the wavefronts a tile of 16x16 at a time while the
 // same columns are there.
+//
+// bf16 [8, 2048], 20 heads of 128 over 10 keys: 595 us, of which the matrix cores
+// are busy for 103 and the 1.5 GB read and 0.44 written take 380 at a copy's rate.
+// One workgroup a compute unit (LDS and registers allow no second one), whose two
+// wavefronts a SIMD wait half of the time.  The next head's operands loaded ahead
+// cost registers that spill (786 us), as K and Q kept in LDS for all heads (670).
 #include "delta_tile.hpp"
 #include "delta_ws.hpp"
 

@@ -8,7 +8,9 @@
 // biased entry's word holds the number of the first list entry that names it;
 // that one alone adds, later entries of the same token behind it in their order.
 // Then one pass over the slice.  Bytes of the logits bound large vocabularies,
-// the walk along a long history small ones.
+// the walk along a long history small ones: bf16 [32, 262144] takes 16.2 us with all
+// rules, 2048 tokens and 64 entries a row (8.8 with none, a copy 6.1), of which the
+// tables' clearing and the history are what is more; fp32 [5, 4001] 6.4 us.
 #include "device.hpp"
 #include "logits.hpp"
 
