@@ -21,11 +21,12 @@
 // with tokens are spread over the wavefronts a tile of 16x16 at a time while the
 // same columns are there.
 //
-// bf16 [8, 2048], 20 heads of 128 over 10 keys: 595 us, of which the matrix cores
-// are busy for 103 and the 1.5 GB read and 0.44 written take 380 at a copy's rate.
-// One workgroup a compute unit (LDS and registers allow no second one), whose two
-// wavefronts a SIMD wait half of the time.  The next head's operands loaded ahead
-// cost registers that spill (786 us), as K and Q kept in LDS for all heads (670).
+// bf16 [8, 2048], 20 heads of 128 over 10 keys: 577 us, of which the matrix cores
+// are busy for 103 (592 with both sums over heads in memory, 420 MB more to write
+// and read).  One workgroup a compute unit (LDS and registers allow no second one),
+// whose two wavefronts a SIMD wait half of the time.  The next head's operands
+// loaded ahead cost registers that spill (786 us), as K and Q kept in LDS for all
+// heads (670).
 #include "delta_tile.hpp"
 #include "delta_ws.hpp"
 
@@ -58,6 +59,9 @@ __global__ void __launch_bounds__(kWide, 2) delta_grads(DeltaShape s, DeltaIn in
     __shared__ __attribute__((aligned(16))) float gates[5 * kC];  // enter, leave, beta, G in two
     __shared__ __attribute__((aligned(16))) float dg[DN * kC];
     __shared__ float ends[kWide / 64];
+    // sums over the heads that share a q and k: as many of the two as there is room for here
+    constexpr int kHeld = DT == DT_BF16 ? (TT == 2 ? 2 : 1) : TT == 2 ? 1 : 0;
+    __shared__ f32x4 held[kHeld ? kHeld * TT * kWide : 1];
     uint16_t *const xt = ops, *const rt = ops + 3 * kGPlane, *const ot = ops + 6 * kGPlane;
     uint16_t *const kb = ops, *const qb = ops + NP * kKPlane;
     const float *const enter = gates, *const leave = gates + kC, *const beta = gates + 2 * kC, *const gh = gates + 3 * kC,
@@ -96,8 +100,11 @@ __global__ void __launch_bounds__(kWide, 2) delta_grads(DeltaShape s, DeltaIn in
         for (int d0 = 0; d0 < s.K; d0 += 16 * DN) {
             const int col = d0 + dt * 16 + ln;
             const bool works = d0 + dt * 16 < s.K;
-            // sums over the heads that share this q and k, this thread's own
-            f32x4* const sums = keep.sums + (int64_t)blockIdx.x * 8 * kWide + threadIdx.x;
+            // this thread's sums of q (n = 0) and k (1)
+            auto sum = [&](int n, int i) -> f32x4& {
+                return n < kHeld ? held[(n * TT + i) * kWide + threadIdx.x]
+                                 : keep.sums[((int64_t)blockIdx.x * 8 + n * TT + i) * kWide + threadIdx.x];
+            };
             for (int hh = 0; hh < share; ++hh) {
                 const int h = hk * share + hh;
                 const int64_t bh = b * s.H + h, t0 = bh * s.T + start;
@@ -229,7 +236,7 @@ __global__ void __launch_bounds__(kWide, 2) delta_grads(DeltaShape s, DeltaIn in
 #pragma unroll
                 for (int i = 0; i < TT; ++i) {
                     dgi[i] = tq[i] = tk[i] = f32x4{0, 0, 0, 0};
-                    if (hh) tq[i] = sums[2 * i * kWide], tk[i] = sums[(2 * i + 1) * kWide];
+                    if (hh) tq[i] = sum(0, i), tk[i] = sum(1, i);
                 }
                 if (works) {
                     f32x4 kv[TT];
@@ -276,7 +283,7 @@ __global__ void __launch_bounds__(kWide, 2) delta_grads(DeltaShape s, DeltaIn in
                     }
                     if (hh + 1 < share) {
 #pragma unroll
-                        for (int i = 0; i < TT; ++i) sums[2 * i * kWide] = tq[i], sums[(2 * i + 1) * kWide] = tk[i];
+                        for (int i = 0; i < TT; ++i) sum(0, i) = tq[i], sum(1, i) = tk[i];
                     } else {
                         store_tokens<DT, TT>(p.grad_q, b * s.T + start, len, s.HK, hk, s.K, t0_ * 16, col, lane, tq);
                         store_tokens<DT, TT>(p.grad_k, b * s.T + start, len, s.HK, hk, s.K, t0_ * 16, col, lane, tk);
