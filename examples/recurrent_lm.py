@@ -32,6 +32,8 @@ HEAD = 32  # width of a head of the delta rule: its state is HEAD x HEAD
 class RecurrentLM(torch.nn.Module):
     def __init__(self, vocab=97, width=128, dtype=torch.float32, seed=0, mixer="gated"):
         super().__init__()
+        if mixer not in ("gated", "delta") or (mixer == "delta" and width % HEAD):
+            raise ValueError(f"mixer must be gated, or delta of a width in heads of {HEAD}")
         gen = torch.Generator().manual_seed(seed)
 
         def param(*shape, sd, kind=dtype):

@@ -1199,7 +1199,8 @@ def _adamw_class():
         """AdamW (decoupled weight decay) whose step is ``adamw_update`` on all params of
         a group that have a gradient.  ``state_bits`` 8 holds the states as e4m3 codes
         with a scale for each ADAMW_GROUP elements; ``master`` holds float32 weights
-        beside bfloat16 params.  ``step(grad_scale=...)`` multiplies the gradients.  The
+        beside bfloat16 params (from the first step on; params set later from outside
+        are overwritten by them).  ``step(grad_scale=...)`` multiplies the gradients.  The
         count of steps is the host's, so a step is not captured into a graph (adamw_update
         with ``step`` on the device is)."""
 

@@ -593,11 +593,10 @@ __global__ void __launch_bounds__(kWalkThreads, 2) delta_join(DeltaShape s, Bloc
     if (threadIdx.x < parts.n) {
         const int64_t b = bh / s.H, n = blocks.count(b);
         bool any = false;
-        for (int64_t c = n * threadIdx.x / parts.n; c < n * (threadIdx.x + 1) / parts.n; ++c) {
+        const int64_t end = n * (threadIdx.x + 1) / parts.n;
+        for (int64_t c = n * threadIdx.x / parts.n; c < end && !any; ++c) {
             int start, len;
-            bool cut;
-            blocks.at(b, (int)c, start, len, cut);
-            any = any || cut;
+            blocks.at(b, (int)c, start, len, any);
         }
         barred[threadIdx.x] = any;
     }

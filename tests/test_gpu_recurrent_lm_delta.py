@@ -246,3 +246,9 @@ def test_the_optimizer_refuses_capture(lm):
         with pytest.raises(RuntimeError, match="captured"):
             opt.step()
     assert kept.numel() == 8
+
+
+def test_the_model_refuses_other_mixers_and_widths(lm):
+    for more in (dict(mixer="other"), dict(mixer="delta", width=72)):
+        with pytest.raises(ValueError, match="mixer"):
+            lm.RecurrentLM(**more)
