@@ -28,6 +28,7 @@ namespace lrscan {
 namespace delta {
 
 constexpr int kWalkThreads = 512;
+constexpr int kMaxWaves = 8;         // wavefronts with columns, at most; the launch says how many
 constexpr int kTS = kC + 8;          // elements of an LDS row of 64
 constexpr int kTPlane = kC * kTS;
 
@@ -88,6 +89,42 @@ struct Tile {
                 store_frag(row + q, plane, f);
             }
         }
+    }
+};
+
+// V or dO of a block in LDS, [token][column], as they are stored: fp32 in one plane
+// leaves room for eight wavefronts' columns beside K's 256 in three (fp32 [14, 513],
+// 16 heads of 256: 693 us a forward call, 929 with four and V in three planes).
+template <int DT, int COLS>
+struct Values {
+    static constexpr int kStride = DT == DT_F32 ? 2 * (COLS + 4) : COLS + 8, kSize = kC * kStride;
+    static __device__ __forceinline__ void store(uint16_t* tile, const Tile<DT, COLS, false>& t) {
+        if constexpr (DT == DT_F32) {
+#pragma unroll
+            for (int i = 0; i < t.PER; ++i) {
+                const int o = i * kWalkThreads + threadIdx.x;
+                f32x4* row = reinterpret_cast<f32x4*>(tile + o / (COLS / 8) * kStride + o % (COLS / 8) * 16);
+                row[0] = t.x[i].a, row[1] = t.x[i].b;
+            }
+        } else {
+            t.store(tile, 0, kStride);
+        }
+    }
+    // a lane's four tokens of a column
+    static __device__ __forceinline__ f32x4 four(const uint16_t* tile, int row0, int col0, int lane) {
+        if constexpr (DT == DT_F32) {
+            const float* at = reinterpret_cast<const float*>(tile) + (row0 + (lane >> 4) * 4) * (COLS + 4) + col0 + (lane & 15);
+            return f32x4{at[0], at[COLS + 4], at[2 * (COLS + 4)], at[3 * (COLS + 4)]};
+        } else {
+            return read_values<1>(tile, 0, kStride, row0, col0, lane);
+        }
+    }
+    // an operand with 32 tokens as k
+    static __device__ __forceinline__ Frag<kPlanes<DT>> frag(const uint16_t* tile, int row0, int col0, int lane) {
+        if constexpr (DT == DT_F32)
+            return split8(four(tile, row0, col0, lane), four(tile, row0 + 16, col0, lane));
+        else
+            return rows_frag<1>(tile, 0, kStride, row0, col0, 4, lane);
     }
 };
 
@@ -197,15 +234,14 @@ struct Widths {
 // leaves: columns of V from zero, then K columns of the identity with values of 0.
 enum Leaves { kOutputs, kKept, kSpan };
 
-// NC: wavefronts with columns, at most; the launch says how many.  NS: planes of
-// fp32 operands.
-template <int DT, int RT, int NC, int LEAVES, int NS>
+// NS: planes of fp32 operands.
+template <int DT, int RT, int LEAVES, int NS>
 __global__ void __launch_bounds__(kWalkThreads, 2)
 delta_walk(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaFwd p, Kept keep, Parts parts, int groups, int waves, Widths wd) {
     constexpr bool KEEP = LEAVES != kOutputs;
     constexpr int NP = kPlanes<DT>;
-    constexpr int ND = 4 * RT, KP = 64 * RT, KS = KP + 8, VS = 16 * NC + 8;
-    constexpr int kKPlane = kC * KS, kVPlane = kC * VS;
+    constexpr int ND = 4 * RT, KP = 64 * RT, KS = KP + 8, kKPlane = kC * KS;
+    using Columns = Values<DT, 16 * kMaxWaves>;
     // fp32 tiles take three planes each: of more than 64 rows Q lies where K will, the
     // inverse where P will (of 64 with room for all, fp32 [4, 1023, 16 heads of 64]
     // reverse 241 us a call for 248)
@@ -214,7 +250,7 @@ delta_walk(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaFwd p, Kept 
     __shared__ __attribute__((aligned(16))) uint16_t qt_[KEEP || kShare ? 8 : NP * kKPlane];
     __shared__ __attribute__((aligned(16))) uint16_t it[NS * kTPlane];
     __shared__ __attribute__((aligned(16))) uint16_t at_[KEEP || kShare ? 8 : NS * kTPlane];
-    __shared__ __attribute__((aligned(16))) uint16_t vt[NP * kVPlane];  // V [token][column]
+    __shared__ __attribute__((aligned(16))) uint16_t vt[Columns::kSize];  // V [token][column]
     __shared__ __attribute__((aligned(16))) float gates[3 * kC];
     uint16_t *const qt = kShare ? kt : qt_, *const at = kShare ? it : at_;
 
@@ -238,7 +274,7 @@ delta_walk(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaFwd p, Kept 
         });
 
     Tile<DT, KP, true> kn, qn;
-    Tile<DT, NC * 16, false> vn;
+    Tile<DT, 16 * kMaxWaves, false> vn;
     Rows64<NS> tn, an;
     Gates gn;
     auto load = [&](int start, int len) {
@@ -263,7 +299,7 @@ delta_walk(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaFwd p, Kept 
         gn.store(gates);
         if (!KEEP) qn.store(qt, kKPlane, KS);
         if (KEEP || !kShare) kn.store(kt, kKPlane, KS);
-        vn.store(vt, kVPlane, VS);
+        Columns::store(vt, vn);
         tn.store(it);
         if (!KEEP && !kShare) an.store(at);
         __syncthreads();
@@ -313,7 +349,7 @@ delta_walk(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaFwd p, Kept 
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 en[i] = *reinterpret_cast<const f32x4*>(gates + i * 16 + lg * 4);
-                const f32x4 v = read_values<NP>(vt, kVPlane, VS, i * 16, w * 16, lane);
+                const f32x4 v = Columns::four(vt, i * 16, w * 16, lane);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) ks[i][r] = fmaf(-en[i][r], ks[i][r], v[r]);
             }
@@ -394,20 +430,20 @@ delta_walk(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaFwd p, Kept 
 //   dS' = end dS + Q^T (scale enter dO) - K^T (beta enter R).
 // SPAN: of a part only the gradient that reaches the state entering it, from
 // nothing behind it (of the last part, from grad_last).
-template <int DT, int RT, int NC, bool SPAN>
+template <int DT, int RT, bool SPAN>
 __global__ void __launch_bounds__(kWalkThreads, 2)
 delta_walk_back(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaBwd p, HeadRows go, Kept keep, Parts parts,
                 int groups, int waves, Widths wd) {
     constexpr int NP = kPlanes<DT>;
-    constexpr int ND = 4 * RT, KP = 64 * RT, KS = KP + 8, VS = 16 * NC + 8;
-    constexpr int kKPlane = kC * KS, kVPlane = kC * VS;
+    constexpr int ND = 4 * RT, KP = 64 * RT, KS = KP + 8, kKPlane = kC * KS;
+    using Columns = Values<DT, 16 * kMaxWaves>;
     // fp32 of more than 64 rows: Q follows K in one place, the inverse P in another
     constexpr bool kShare = DT == DT_F32 && RT > 1;
     __shared__ __attribute__((aligned(16))) uint16_t kt[NP * kKPlane];
     __shared__ __attribute__((aligned(16))) uint16_t qt_[kShare ? 8 : NP * kKPlane];
     __shared__ __attribute__((aligned(16))) uint16_t at[3 * kTPlane];
     __shared__ __attribute__((aligned(16))) uint16_t it_[kShare ? 8 : 3 * kTPlane];
-    __shared__ __attribute__((aligned(16))) uint16_t ot[NP * kVPlane];  // dO [token][column]
+    __shared__ __attribute__((aligned(16))) uint16_t ot[Columns::kSize];  // dO [token][column]
     __shared__ __attribute__((aligned(16))) float gates[3 * kC];
     uint16_t *const qt = kShare ? kt : qt_, *const it = kShare ? at : it_;
 
@@ -431,7 +467,7 @@ delta_walk_back(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaBwd p, 
         });
 
     Tile<DT, KP, true> kn, qn;
-    Tile<DT, NC * 16, false> on;
+    Tile<DT, 16 * kMaxWaves, false> on;
     Rows64<3> tn, an;
     Gates gn;
     auto load = [&](int start, int len) {
@@ -457,7 +493,7 @@ delta_walk_back(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaBwd p, 
         if (c > to) blocks.at(b, c - 1, prev, plen, pfirst);
         gn.store(gates);
         kn.store(kt, kKPlane, KS);
-        on.store(ot, kVPlane, VS);
+        Columns::store(ot, on);
         an.store(at);
         if (!kShare) {
             tn.store(it);
@@ -483,8 +519,8 @@ delta_walk_back(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaBwd p, 
                 x[i] = po[i] = f32x4{0, 0, 0, 0};
                 en[i] = *reinterpret_cast<const f32x4*>(gates + i * 16 + lg * 4);
             }
-            o0 = rows_frag<NP>(ot, kVPlane, VS, 0, w * 16, 4, lane);
-            o1 = rows_frag<NP>(ot, kVPlane, VS, 32, w * 16, 4, lane);
+            o0 = Columns::frag(ot, 0, w * 16, lane);
+            o1 = Columns::frag(ot, 32, w * 16, lane);
             triangle<3, false>(po, at, o0, o1, lane);
 #pragma unroll
             for (int g = 0; g < KP / 32; ++g) {
@@ -536,7 +572,7 @@ delta_walk_back(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaBwd p, 
         if (works) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const f32x4 o = read_values<NP>(ot, kVPlane, VS, i * 16, w * 16, lane);
+                const f32x4 o = Columns::four(ot, i * 16, w * 16, lane);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) x[i][r] = in.scale * en[i][r] * o[r];
             }
@@ -659,11 +695,6 @@ __global__ void __launch_bounds__(kWalkThreads, 2) delta_join(DeltaShape s, Bloc
     }
 }
 
-// Wavefronts with columns that a workgroup has room for: fp32 tiles of more than
-// 192 rows leave LDS for four.
-template <int DT, int RT>
-constexpr int kMaxWaves = DT == DT_F32 && RT == 4 ? 4 : 8;
-
 template <class F>
 hipError_t by_rows(const DeltaShape& s, F f) {
     switch ((s.K + 63) / 64) {
@@ -713,9 +744,9 @@ hipError_t walk(const DeltaShape& s, const DeltaIn& in, const Blocks& blocks, co
     const Widths wd{row_width(s.K, DT), row_width(s.V, DT)};
     const int tiles = (s.V + 15) / 16 + (LEAVES == kSpan ? (s.K + 15) / 16 : 0);
     return by_rows(s, [&](auto rt) {
-        constexpr int RT = decltype(rt)::value, NC = kMaxWaves<DT, RT>;
-        const Spread x = spread(s, tiles, LEAVES == kSpan ? parts.n - 1 : parts.n, NC);
-        delta_walk<DT, RT, NC, LEAVES, NS>
+        constexpr int RT = decltype(rt)::value;
+        const Spread x = spread(s, tiles, LEAVES == kSpan ? parts.n - 1 : parts.n, kMaxWaves);
+        delta_walk<DT, RT, LEAVES, NS>
             <<<x.grid, kWalkThreads, 0, st>>>(s, in, blocks, prep, out, keep, parts, x.groups, x.waves, wd);
         return hipGetLastError();
     });
@@ -744,9 +775,9 @@ hipError_t walk_back(const DeltaShape& s, const DeltaIn& in, const Blocks& block
                      const HeadRows& go, const Kept& keep, const Parts& parts, hipStream_t st) {
     const Widths wd{row_width(s.K, DT), row_width(s.V, DT)};
     return by_rows(s, [&](auto rt) {
-        constexpr int RT = decltype(rt)::value, NC = kMaxWaves<DT, RT>;
-        const Spread x = spread(s, (s.V + 15) / 16, SPAN ? parts.n - 1 : parts.n, NC);
-        delta_walk_back<DT, RT, NC, SPAN>
+        constexpr int RT = decltype(rt)::value;
+        const Spread x = spread(s, (s.V + 15) / 16, SPAN ? parts.n - 1 : parts.n, kMaxWaves);
+        delta_walk_back<DT, RT, SPAN>
             <<<x.grid, kWalkThreads, 0, st>>>(s, in, blocks, prep, p, go, keep, parts, x.groups, x.waves, wd);
         return hipGetLastError();
     });
