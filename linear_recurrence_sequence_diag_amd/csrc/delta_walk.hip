@@ -277,13 +277,20 @@ delta_walk(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaFwd p, Kept 
     Tile<DT, 16 * kMaxWaves, false> vn;
     Rows64<NS> tn, an;
     Gates gn;
+    // what shares a place follows later, so that not all of a block is in registers
+    // (fp32 forward calls: [8, 1024], 16 heads of 128, 197 us for 215; [14, 513], 16
+    // heads of 192, 403 for 454; but of 256, where they spill all the same, 763 for 693)
+    constexpr bool kLater = !KEEP && kShare && RT < 4;
+    auto load_later = [&](int start, int len) {
+        kn.load(block_rows(in.k, b, hk, start, len), in.k.st, 0, KP, wd.k);
+        if (!KEEP) an.load(prep.att, bh * s.T + start, len);
+    };
     auto load = [&](int start, int len) {
         gn.load(prep, bh * s.T + start, len);
         if (!KEEP) qn.load(block_rows(in.q, b, hk, start, len), in.q.st, 0, KP, wd.k);
-        kn.load(block_rows(in.k, b, hk, start, len), in.k.st, 0, KP, wd.k);
         vn.load(block_rows(in.v, b, h, start, len), in.v.st, v0, waves * 16, wd.v);
         tn.load(prep.inv, bh * s.T + start, len);
-        if (!KEEP) an.load(prep.att, bh * s.T + start, len);
+        if (!kLater) load_later(start, len);
     };
     int from, n;
     part_blocks(blocks.count(b), part, parts.n, from, n);
@@ -303,7 +310,10 @@ delta_walk(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaFwd p, Kept 
         tn.store(it);
         if (!KEEP && !kShare) an.store(at);
         __syncthreads();
-        if (KEEP || !kShare) load(next, nlen);
+        if (kLater)
+            load_later(start, len);
+        else if (KEEP || !kShare)
+            load(next, nlen);
 
         f32x4 qs[4], ks[4];
 #pragma unroll
@@ -335,6 +345,7 @@ delta_walk(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaFwd p, Kept 
             __syncthreads();  // Q is read
             kn.store(kt, kKPlane, KS);
             __syncthreads();
+            if (kLater) load(next, nlen);
             if (works)
 #pragma unroll
                 for (int g = 0; g < KP / 32; ++g) {
@@ -376,7 +387,7 @@ delta_walk(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaFwd p, Kept 
             __syncthreads();  // the inverse is read
             an.store(at);
             __syncthreads();
-            load(next, nlen);
+            if (!kLater) load(next, nlen);
         }
         if (works) {
             if (!KEEP && p.out) {
@@ -470,13 +481,19 @@ delta_walk_back(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaBwd p, 
     Tile<DT, 16 * kMaxWaves, false> on;
     Rows64<3> tn, an;
     Gates gn;
+    // what shares a place follows later (of 192, reverse: 1178 us for 1194; of 256 1989
+    // for 1737)
+    constexpr bool kLater = kShare && RT < 4;
+    auto load_later = [&](int start, int len) {
+        tn.load(prep.inv_t, bh * s.T + start, len);
+        qn.load(block_rows(in.q, b, hk, start, len), in.q.st, 0, KP, wd.k);
+    };
     auto load = [&](int start, int len) {
         gn.load(prep, bh * s.T + start, len);
         kn.load(block_rows(in.k, b, hk, start, len), in.k.st, 0, KP, wd.k);
         on.load(block_rows(go, b, h, start, len), go.st, v0, waves * 16, wd.v);
         an.load(prep.att_t, bh * s.T + start, len);
-        tn.load(prep.inv_t, bh * s.T + start, len);
-        qn.load(block_rows(in.q, b, hk, start, len), in.q.st, 0, KP, wd.k);
+        if (!kLater) load_later(start, len);
     };
     int to, n;
     part_blocks(blocks.count(b), part, parts.n, to, n);
@@ -500,7 +517,10 @@ delta_walk_back(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaBwd p, 
             qn.store(qt, kKPlane, KS);
         }
         __syncthreads();
-        if (!kShare) load(prev, plen);
+        if (kLater)
+            load_later(start, len);
+        else if (!kShare)
+            load(prev, plen);
 
         f32x4 x[4], po[4], en[4];
         Frag<NP> o0, o1;
