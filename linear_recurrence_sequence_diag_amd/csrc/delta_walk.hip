@@ -14,8 +14,8 @@
 // beyond the columns only load.
 //
 // What bounds it is the length of a block's chain of products: bf16 [8, 2048], 20
-// heads of 128 with resets, are 160 workgroups that take 12.5 thousand cycles a
-// block, 209 us, 38 of them matrix instructions with two wavefronts a SIMD; LDS
+// heads of 128 with resets, are 160 workgroups that take 12.3 thousand cycles a
+// block, 205 us, 38 of them matrix instructions with two wavefronts a SIMD; LDS
 // reads and the cutting into planes hardly overlap with these.  The kept walk of the
 // backward pass takes 270 us (485 MB of states and x written), the walk back 358
 // (579 MB).
