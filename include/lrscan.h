@@ -420,9 +420,8 @@ LRSCAN_API size_t scan_embed_workspace_bytes(int64_t N, int64_t V, int64_t D, in
  * out as a NaN.
  * Tokens are taken in blocks of 64, whose products run on the matrix cores; all
  * sums and states are fp32.  A fp32 operand goes there as the sum of three bf16
- * parts, which has the accuracy of fp32; of a bf16 forward without last, whose
- * results are bf16 alone, as the sum of two (2^-18 of the value, below a hundredth
- * of that rounding).  Calls repeat bit for bit.
+ * parts, which has the accuracy of fp32.  Calls repeat bit for bit, and out is the
+ * same whether last is asked for or not.
  * `strides` (a host array, or NULL for contiguous) holds three numbers for each
  * operand, in elements: from one batch row, one step and one head to the next
  * (q, k and v may be parts of one projection).  None is negative; one may be 0.

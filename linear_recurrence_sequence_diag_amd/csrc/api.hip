@@ -1202,7 +1202,7 @@ LRSCAN_API int scan_delta_fwd(const void* q, const void* k, const void* v, const
     hipStream_t hs = static_cast<hipStream_t>(stream);
     const DeltaIn in = delta_in(s, q, k, v, log_decay, beta, scale, opts ? opts->h0 : nullptr, reset, strides);
     void* ws = nullptr;
-    rc = plain_workspace(delta_ws_bytes(s, &in, nullptr, last != nullptr, false), opts, hs, &ws);
+    rc = plain_workspace(delta_ws_bytes(s, &in, nullptr, false), opts, hs, &ws);
     if (rc != LRSCAN_OK) return rc;
     return hip_status(launch_delta_fwd(s, in, DeltaFwd{out, last}, ws, hs));
 }
@@ -1224,7 +1224,7 @@ LRSCAN_API int scan_delta_bwd(const void* q, const void* k, const void* v, const
     hipStream_t hs = static_cast<hipStream_t>(stream);
     const DeltaIn in = delta_in(s, q, k, v, log_decay, beta, scale, opts ? opts->h0 : nullptr, reset, strides);
     void* ws = nullptr;
-    rc = plain_workspace(delta_ws_bytes(s, &in, grad_out, true, true), opts, hs, &ws);
+    rc = plain_workspace(delta_ws_bytes(s, &in, grad_out, true), opts, hs, &ws);
     if (rc != LRSCAN_OK) return rc;
     const DeltaBwd p{grad_out, grad_last, grad_q, grad_k, grad_v, grad_log_decay, grad_beta,
                      opts ? opts->grad_h0 : nullptr};
@@ -1255,7 +1255,7 @@ LRSCAN_API size_t scan_delta_workspace_bytes(int64_t B, int64_t T, int64_t H, in
                                              int dtype, int backward) {
     DeltaShape s;
     if (delta_shape(B, T, H, HK, K, V, dtype, &s) != LRSCAN_OK) return 0;
-    return delta_ws_bytes(s, nullptr, nullptr, true, backward != 0);
+    return delta_ws_bytes(s, nullptr, nullptr, backward != 0);
 }
 
 // ---- AdamW ------------------------------------------------------------------------------

@@ -33,9 +33,9 @@ bool delta_fits(const DeltaShape& s) {
     return heads <= ((int64_t)1 << 30) / groups && heads <= ((int64_t)1 << 30) / slots;
 }
 
-size_t delta_ws_bytes(const DeltaShape& s, const DeltaIn* in, const void* grad_out, bool fp32_results, bool backward) {
-    if (!in) return Layout(s, backward, 3, true, Copies{true, true, true, true}).total;
-    return Layout(s, backward, operand_planes(s, fp32_results), in->reset != nullptr, copies(s, *in, grad_out)).total;
+size_t delta_ws_bytes(const DeltaShape& s, const DeltaIn* in, const void* grad_out, bool backward) {
+    if (!in) return Layout(s, backward, true, Copies{true, true, true, true}).total;
+    return Layout(s, backward, in->reset != nullptr, copies(s, *in, grad_out)).total;
 }
 
 namespace {
@@ -49,11 +49,10 @@ struct Pass {
     Parts parts;
 };
 
-hipError_t begin(const DeltaShape& s, const DeltaIn& in, const void* grad_out, int operands, void* ws, hipStream_t st,
-                 Pass* pass) {
+hipError_t begin(const DeltaShape& s, const DeltaIn& in, const void* grad_out, void* ws, hipStream_t st, Pass* pass) {
     const bool backward = grad_out != nullptr;
     const Copies copy = copies(s, in, grad_out);
-    const Layout l(s, backward, operands, in.reset != nullptr, copy);
+    const Layout l(s, backward, in.reset != nullptr, copy);
     char* base = static_cast<char*>(ws);
     auto f = [&](size_t o) { return reinterpret_cast<float*>(base + o); };
     auto planes = [&](size_t o) { return reinterpret_cast<uint16_t*>(base + o); };
@@ -82,24 +81,23 @@ hipError_t begin(const DeltaShape& s, const DeltaIn& in, const void* grad_out, i
     hipError_t e = run_copies(c, s.T, s.dtype, st);
     if (e == hipSuccess && in.reset) e = run_blocks(s, in.reset, starts, counts, st);
     if (e != hipSuccess) return e;
-    return run_prep(s, pass->in, pass->blocks, pass->prep, backward, operands, st);
+    return run_prep(s, pass->in, pass->blocks, pass->prep, backward, st);
 }
 
 }  // namespace
 
 hipError_t launch_delta_fwd(const DeltaShape& s, const DeltaIn& in, const DeltaFwd& p, void* ws, hipStream_t st) {
     Pass pass;
-    const int planes = operand_planes(s, p.last != nullptr);
-    const hipError_t e = begin(s, in, nullptr, planes, ws, st, &pass);
+    const hipError_t e = begin(s, in, nullptr, ws, st, &pass);
     if (e != hipSuccess) return e;
-    return run_walk(s, pass.in, pass.blocks, pass.prep, p, nullptr, pass.parts, planes, st);
+    return run_walk(s, pass.in, pass.blocks, pass.prep, p, nullptr, pass.parts, st);
 }
 
 hipError_t launch_delta_bwd(const DeltaShape& s, const DeltaIn& in, const DeltaBwd& p, void* ws, hipStream_t st) {
     Pass pass;
-    hipError_t e = begin(s, in, p.grad_out, 3, ws, st, &pass);
+    hipError_t e = begin(s, in, p.grad_out, ws, st, &pass);
     if (e != hipSuccess) return e;
-    e = run_walk(s, pass.in, pass.blocks, pass.prep, DeltaFwd{nullptr, nullptr}, &pass.keep, pass.parts, 3, st);
+    e = run_walk(s, pass.in, pass.blocks, pass.prep, DeltaFwd{nullptr, nullptr}, &pass.keep, pass.parts, st);
     if (e != hipSuccess) return e;
     e = run_walk_back(s, pass.in, pass.blocks, pass.prep, p, pass.go, pass.keep, pass.parts, st);
     if (e != hipSuccess) return e;

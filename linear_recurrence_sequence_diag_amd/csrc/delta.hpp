@@ -49,9 +49,8 @@ constexpr int kDeltaMaxK = 256;
 // Whether the shape's launches and offsets fit what the kernels count with.
 bool delta_fits(const DeltaShape& s);
 // Scratch of a call (256-byte aligned; rewritten before it is read), or (in NULL)
-// of the call with the largest of any operands of these sizes; grad_out: of a backward;
-// fp32_results: whether a state or gradients in fp32 come out.
-size_t delta_ws_bytes(const DeltaShape& s, const DeltaIn* in, const void* grad_out, bool fp32_results, bool backward);
+// of the call with the largest of any operands of these sizes; grad_out: of a backward.
+size_t delta_ws_bytes(const DeltaShape& s, const DeltaIn* in, const void* grad_out, bool backward);
 hipError_t launch_delta_fwd(const DeltaShape& s, const DeltaIn& in, const DeltaFwd& p, void* ws, hipStream_t st);
 hipError_t launch_delta_bwd(const DeltaShape& s, const DeltaIn& in, const DeltaBwd& p, void* ws, hipStream_t st);
 // One token: in.h0 is the state that enters, in.reset [B].  `last` may be in.h0.

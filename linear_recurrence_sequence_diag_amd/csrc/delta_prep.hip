@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kScanThreads) delta_blocks(const uint8_t* rese
 
 constexpr int kS = kC + 4;  // floats of an LDS row
 
-template <int DT, bool BWD, int NS>
+template <int DT, bool BWD>
 __global__ void __launch_bounds__(kThreads, DT == DT_BF16 ? 3 : 2) delta_prep(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, int slots,
                                                        int width) {
     constexpr int NP = kPlanes<DT>;
@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, DT == DT_BF16 ? 3 : 2) delta_prep(De
             // rows (columns of the transposed ones) 0 .. 31 have nothing to read beyond (before) 32
             if (BWD) {
                 if (col < len && (j < 2 || w >= 2))
-                    store_planes<3>(prep.att_t + ((bh * s.T + start + col) * 3) * kC + place(w * 16 + lg * 4), kC, back);
+                    store_planes(prep.att_t + ((bh * s.T + start + col) * 3) * kC + place(w * 16 + lg * 4), kC, back);
             } else {
 #pragma unroll
                 for (int r = 0; r < 4; ++r) M[(w * 16 + lg * 4 + r) * kS + col] = back[r];
@@ -249,12 +249,12 @@ __global__ void __launch_bounds__(kThreads, DT == DT_BF16 ? 3 : 2) delta_prep(De
             if (r < len && (r >= 32 || q < 32)) {
                 // the eight elements that stand at q .. q + 7
                 const int e = r * kS + (q & 32) + (q & 24) / 2;
-                const int64_t to = (bh * s.T + start + r) * NS * kC + q;
+                const int64_t to = (bh * s.T + start + r) * 3 * kC + q;
                 store_frag(prep.inv + to, kC,
-                           split8<NS>(*reinterpret_cast<const f32x4*>(Ti + e), *reinterpret_cast<const f32x4*>(Ti + e + 16)));
+                           split8(*reinterpret_cast<const f32x4*>(Ti + e), *reinterpret_cast<const f32x4*>(Ti + e + 16)));
                 if (!BWD)
                     store_frag(prep.att + to, kC,
-                               split8<NS>(*reinterpret_cast<const f32x4*>(M + e), *reinterpret_cast<const f32x4*>(M + e + 16)));
+                               split8(*reinterpret_cast<const f32x4*>(M + e), *reinterpret_cast<const f32x4*>(M + e + 16)));
             }
         }
         if (BWD) {
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, DT == DT_BF16 ? 3 : 2) delta_prep(De
                     y[r] = (i == col ? 1.0f : 0.0f) - bt[i] * y[r];
                 }
                 if (col < len && (j < 2 || w >= 2))
-                    store_planes<3>(prep.inv_t + (bh * s.T + start + col) * 3 * kC + place(w * 16 + lg * 4), kC, y);
+                    store_planes(prep.inv_t + (bh * s.T + start + col) * 3 * kC + place(w * 16 + lg * 4), kC, y);
             }
         }
     }
@@ -281,21 +281,19 @@ hipError_t run_blocks(const DeltaShape& s, const uint8_t* reset, int* starts, in
     return hipGetLastError();
 }
 
-template <int DT, bool BWD, int NS>
+template <int DT, bool BWD>
 hipError_t prep_of(const DeltaShape& s, const DeltaIn& in, const Blocks& blocks, const Prep& prep, hipStream_t st) {
     const int slots = (int)((s.T + kC - 1) / kC);
-    delta_prep<DT, BWD, NS><<<dim3((unsigned)(s.B * s.H * slots)), kThreads, 0, st>>>(s, in, blocks, prep, slots,
+    delta_prep<DT, BWD><<<dim3((unsigned)(s.B * s.H * slots)), kThreads, 0, st>>>(s, in, blocks, prep, slots,
                                                                                    row_width(s.K, DT));
     return hipGetLastError();
 }
 
 hipError_t run_prep(const DeltaShape& s, const DeltaIn& in, const Blocks& blocks, const Prep& prep, bool backward,
-                    int planes, hipStream_t st) {
+                    hipStream_t st) {
     if (s.dtype == DT_F32)
-        return backward ? prep_of<DT_F32, true, 3>(s, in, blocks, prep, st) : prep_of<DT_F32, false, 3>(s, in, blocks, prep, st);
-    if (backward) return prep_of<DT_BF16, true, 3>(s, in, blocks, prep, st);
-    return planes == 2 ? prep_of<DT_BF16, false, 2>(s, in, blocks, prep, st)
-                       : prep_of<DT_BF16, false, 3>(s, in, blocks, prep, st);
+        return backward ? prep_of<DT_F32, true>(s, in, blocks, prep, st) : prep_of<DT_F32, false>(s, in, blocks, prep, st);
+    return backward ? prep_of<DT_BF16, true>(s, in, blocks, prep, st) : prep_of<DT_BF16, false>(s, in, blocks, prep, st);
 }
 
 }  // namespace delta

@@ -6,9 +6,7 @@
 // product of two fp32 operands is six bf16 products of 16x16x32 with fp32 sums
 // (those left out are below 2^-26 of it), and a product with a bf16 operand is
 // three.  The fp32 matrix instruction has a sixteenth of the bf16 rate, so six
-// are 2.7 times as fast, three 5.3 times.  Two values hold 17 bits (what is left
-// is at most 2^-18): enough for what ends in a bf16 output, whose rounding is 512
-// times as large.  An infinity or NaN gives NaN.
+// are 2.7 times as fast, three 5.3 times.  An infinity or NaN gives NaN.
 //
 // Layouts of v_mfma_f32_16x16x32_bf16, lane l, ln = l & 15, lg = l >> 4:
 //   A: row ln, k = 8 lg .. 8 lg + 7      B: column ln, the same k
@@ -55,15 +53,11 @@ __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
                                                    0, 0, 0);
 }
 
-// the products of parts i and j with i + j up to this are taken
-template <int NA, int NB>
-constexpr int kLast = NA == 3 || NB == 3 ? 2 : 1;
-
-// c += a b, the small parts first
+// c += a b, the small parts first: the products of parts i and j with i + j <= 2
 template <int NA, int NB>
 __device__ __forceinline__ void mma(f32x4& c, const Frag<NA>& a, const Frag<NB>& b) {
 #pragma unroll
-    for (int s = kLast<NA, NB>; s >= 0; --s)
+    for (int s = 2; s >= 0; --s)
 #pragma unroll
         for (int i = 0; i <= s; ++i)
             if (i < NA && s - i < NB) c = mfma(a.p[i], b.p[s - i], c);
@@ -73,7 +67,7 @@ __device__ __forceinline__ void mma(f32x4& c, const Frag<NA>& a, const Frag<NB>&
 template <int NA, int NB, int M>
 __device__ __forceinline__ void mma(f32x4 (&c)[M], const Frag<NA> (&a)[M], const Frag<NB>& b) {
 #pragma unroll
-    for (int s = kLast<NA, NB>; s >= 0; --s)
+    for (int s = 2; s >= 0; --s)
 #pragma unroll
         for (int i = 0; i <= s; ++i)
             if (i < NA && s - i < NB)
@@ -81,41 +75,38 @@ __device__ __forceinline__ void mma(f32x4 (&c)[M], const Frag<NA> (&a)[M], const
                 for (int j = 0; j < M; ++j) c[j] = mfma(a[j].p[i], b.p[s - i], c[j]);
 }
 
-// two floats as N pairs of bf16, each the rounded rest of those before it
-template <int N>
-__device__ __forceinline__ void split2(float x0, float x1, uint32_t (&p)[N]) {
+// two floats as three pairs of bf16, each the rounded rest of those before it
+__device__ __forceinline__ void split2(float x0, float x1, uint32_t (&p)[3]) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
+    for (int i = 0; i < 3; ++i) {
         p[i] = pack_bf16x2(x0, x1);
-        if (i + 1 < N) {
+        if (i < 2) {
             x0 -= __uint_as_float(p[i] << 16);
             x1 -= __uint_as_float(p[i] & 0xffff0000u);
         }
     }
 }
 
-template <int N = 3>
-__device__ __forceinline__ Frag<N> split8(f32x4 a, f32x4 b) {
-    Frag<N> f;
+__device__ __forceinline__ Frag<3> split8(f32x4 a, f32x4 b) {
+    Frag<3> f;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        uint32_t p[N], q[N];
-        split2<N>(a[2 * j], a[2 * j + 1], p);
-        split2<N>(b[2 * j], b[2 * j + 1], q);
+        uint32_t p[3], q[3];
+        split2(a[2 * j], a[2 * j + 1], p);
+        split2(b[2 * j], b[2 * j + 1], q);
 #pragma unroll
-        for (int i = 0; i < N; ++i) f.p[i][j] = p[i], f.p[i][2 + j] = q[i];
+        for (int i = 0; i < 3; ++i) f.p[i][j] = p[i], f.p[i][2 + j] = q[i];
     }
     return f;
 }
 
-// Four consecutive k of a column, into N planes `step` elements apart.
-template <int N = 3>
+// Four consecutive k of a column, into three planes `step` elements apart.
 __device__ __forceinline__ void store_planes(uint16_t* at, int step, f32x4 v) {
-    uint32_t p[N], q[N];
-    split2<N>(v[0], v[1], p);
-    split2<N>(v[2], v[3], q);
+    uint32_t p[3], q[3];
+    split2(v[0], v[1], p);
+    split2(v[2], v[3], q);
 #pragma unroll
-    for (int i = 0; i < N; ++i) *reinterpret_cast<u32x2*>(at + i * step) = u32x2{p[i], q[i]};
+    for (int i = 0; i < 3; ++i) *reinterpret_cast<u32x2*>(at + i * step) = u32x2{p[i], q[i]};
 }
 
 // ---- rows in memory ----
@@ -335,14 +326,10 @@ struct Prep {
     // the upper float of G; the lower one (backward)
     f32x4* gates;
     float* gl;
-    // rows of kC as bf16 planes, [B, H, T][plane][kC], their columns in place():
+    // rows of kC in three bf16 planes, [B, H, T][plane][kC], their columns in place():
     uint16_t *inv, *att;      // (I + N)^-1, N_ij = decay_ij k_i.k_j beta_j (i > j); decay_ij q_i.k_j
     uint16_t *att_t, *inv_t;  // backward: columns of decay_ij q_i.k_j, and of (I + diag(beta) M)^-1, M = N / beta_j
 };
-
-// Planes of a call's fp32 operands: two where all that it gives are bf16 outputs;
-// three where a state or gradient in fp32 leaves it.
-inline int operand_planes(const DeltaShape& s, bool fp32_results) { return s.dtype == DT_F32 || fp32_results ? 3 : 2; }
 
 // the matrix-core product of two small fp32 LDS matrices: one 16x16 tile of A B, depth k
 __device__ __forceinline__ f32x4 mm16(const float* A, int sa, const float* B, int sb, int k, int lane) {

@@ -128,19 +128,18 @@ struct Values {
     }
 };
 
-// A block's rows of kC in NP planes.
-template <int NP>
+// A block's rows of kC in three planes.
 struct Rows64 {
-    u32x4 x[NP];
+    u32x4 x[3];
     __device__ __forceinline__ void load(const uint16_t* p, int64_t t0, int len) {
-        const Buffer rows = buffer(p + t0 * (NP * kC), len * (NP * kC * 2));
+        const Buffer rows = buffer(p + t0 * (3 * kC), len * (3 * kC * 2));
 #pragma unroll
-        for (int i = 0; i < NP; ++i) x[i] = load16(rows, (i * kWalkThreads + threadIdx.x) * 16);
+        for (int i = 0; i < 3; ++i) x[i] = load16(rows, (i * kWalkThreads + threadIdx.x) * 16);
     }
     __device__ __forceinline__ void store(uint16_t* tile) const {
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-            const int o = i * kWalkThreads + threadIdx.x, r = o / (8 * NP), q = o % (8 * NP);
+        for (int i = 0; i < 3; ++i) {
+            const int o = i * kWalkThreads + threadIdx.x, r = o / 24, q = o % 24;
             *reinterpret_cast<u32x4*>(tile + q / 8 * kTPlane + r * kTS + q % 8 * 8) = x[i];
         }
     }
@@ -189,9 +188,9 @@ __device__ __forceinline__ void each_state(const DeltaShape& s, int64_t bh, int 
 }
 
 // S = end S + K^T l (or Q^T l), l the tokens' two operands of 32.
-template <int NP, int ND, int NS>
-__device__ __forceinline__ void add_tokens(f32x4 (&S)[ND], const uint16_t* tile, int plane, int stride, const Frag<NS>& l0,
-                                           const Frag<NS>& l1, int lane) {
+template <int NP, int ND>
+__device__ __forceinline__ void add_tokens(f32x4 (&S)[ND], const uint16_t* tile, int plane, int stride, const Frag<3>& l0,
+                                           const Frag<3>& l1, int lane) {
 #pragma unroll
     for (int i = 0; i < ND; i += 2) {
         f32x4 c[2] = {S[i], S[i + 1]};
@@ -205,19 +204,19 @@ __device__ __forceinline__ void add_tokens(f32x4 (&S)[ND], const uint16_t* tile,
     }
 }
 
-// x += A y over a block's tokens, A's rows in NA planes in LDS, y the tokens' two
+// x += A y over a block's tokens, A's rows in LDS, y the tokens' two
 // operands of 32; LOWER: rows reach the tokens up to their own, else from there on.
-template <int NA, bool LOWER, int NB>
+template <bool LOWER, int NB>
 __device__ __forceinline__ void triangle(f32x4 (&x)[4], const uint16_t* rows, const Frag<NB>& y0, const Frag<NB>& y1,
                                          int lane) {
     f32x4 c[2] = {x[LOWER ? 2 : 0], x[LOWER ? 3 : 1]}, d[2] = {x[LOWER ? 0 : 2], x[LOWER ? 1 : 3]};
     const int full = LOWER ? 2 : 0, half = LOWER ? 0 : 2;  // tiles of rows with both operands, and with one
-    const Frag<NA> a[2] = {row_frag<NA>(rows, kTPlane, kTS, full * 16, 0, lane),
-                           row_frag<NA>(rows, kTPlane, kTS, (full + 1) * 16, 0, lane)};
-    const Frag<NA> b[2] = {row_frag<NA>(rows, kTPlane, kTS, full * 16, 32, lane),
-                           row_frag<NA>(rows, kTPlane, kTS, (full + 1) * 16, 32, lane)};
-    const Frag<NA> e[2] = {row_frag<NA>(rows, kTPlane, kTS, half * 16, LOWER ? 0 : 32, lane),
-                           row_frag<NA>(rows, kTPlane, kTS, (half + 1) * 16, LOWER ? 0 : 32, lane)};
+    const Frag<3> a[2] = {row_frag<3>(rows, kTPlane, kTS, full * 16, 0, lane),
+                           row_frag<3>(rows, kTPlane, kTS, (full + 1) * 16, 0, lane)};
+    const Frag<3> b[2] = {row_frag<3>(rows, kTPlane, kTS, full * 16, 32, lane),
+                           row_frag<3>(rows, kTPlane, kTS, (full + 1) * 16, 32, lane)};
+    const Frag<3> e[2] = {row_frag<3>(rows, kTPlane, kTS, half * 16, LOWER ? 0 : 32, lane),
+                           row_frag<3>(rows, kTPlane, kTS, (half + 1) * 16, LOWER ? 0 : 32, lane)};
     mma(d, e, LOWER ? y0 : y1);
     mma(c, a, y0);
     mma(c, b, y1);
@@ -234,8 +233,7 @@ struct Widths {
 // leaves: columns of V from zero, then K columns of the identity with values of 0.
 enum Leaves { kOutputs, kKept, kSpan };
 
-// NS: planes of fp32 operands.
-template <int DT, int RT, int LEAVES, int NS>
+template <int DT, int RT, int LEAVES>
 __global__ void __launch_bounds__(kWalkThreads, 2)
 delta_walk(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaFwd p, Kept keep, Parts parts, int groups, int waves, Widths wd) {
     constexpr bool KEEP = LEAVES != kOutputs;
@@ -248,8 +246,8 @@ delta_walk(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaFwd p, Kept 
     constexpr bool kShare = DT == DT_F32 && RT > 1;
     __shared__ __attribute__((aligned(16))) uint16_t kt[NP * kKPlane];
     __shared__ __attribute__((aligned(16))) uint16_t qt_[KEEP || kShare ? 8 : NP * kKPlane];
-    __shared__ __attribute__((aligned(16))) uint16_t it[NS * kTPlane];
-    __shared__ __attribute__((aligned(16))) uint16_t at_[KEEP || kShare ? 8 : NS * kTPlane];
+    __shared__ __attribute__((aligned(16))) uint16_t it[3 * kTPlane];
+    __shared__ __attribute__((aligned(16))) uint16_t at_[KEEP || kShare ? 8 : 3 * kTPlane];
     __shared__ __attribute__((aligned(16))) uint16_t vt[Columns::kSize];  // V [token][column]
     __shared__ __attribute__((aligned(16))) float gates[3 * kC];
     uint16_t *const qt = kShare ? kt : qt_, *const at = kShare ? it : at_;
@@ -275,7 +273,7 @@ delta_walk(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaFwd p, Kept 
 
     Tile<DT, KP, true> kn, qn;
     Tile<DT, 16 * kMaxWaves, false> vn;
-    Rows64<NS> tn, an;
+    Rows64 tn, an;
     Gates gn;
     // what shares a place follows later, so that not all of a block is in registers
     // (fp32 forward calls: [8, 1024], 16 heads of 128, 197 us for 215; [14, 513], 16
@@ -336,7 +334,7 @@ delta_walk(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaFwd p, Kept 
         if (works) {
 #pragma unroll
             for (int g = 0; g < KP / 32; ++g) {
-                const Frag<NS> sf = split8<NS>(S[2 * g], S[2 * g + 1]);
+                const Frag<3> sf = split8(S[2 * g], S[2 * g + 1]);
                 if (!KEEP) times_state(qs, qt, sf, g);
                 if (KEEP || !kShare) times_state(ks, kt, sf, g);
             }
@@ -349,11 +347,11 @@ delta_walk(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaFwd p, Kept 
             if (works)
 #pragma unroll
                 for (int g = 0; g < KP / 32; ++g) {
-                    times_state(ks, kt, split8<NS>(S[2 * g], S[2 * g + 1]), g);
+                    times_state(ks, kt, split8(S[2 * g], S[2 * g + 1]), g);
                 }
         }
         f32x4 en[4];
-        Frag<NS> l0, l1, u0, u1;
+        Frag<3> l0, l1, u0, u1;
         float end = 0.0f;
         if (works) {
             end = gates[len - 1];
@@ -367,7 +365,7 @@ delta_walk(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaFwd p, Kept 
             f32x4 x[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[i] = f32x4{0, 0, 0, 0};
-            triangle<NS, true>(x, it, split8<NS>(ks[0], ks[1]), split8<NS>(ks[2], ks[3]), lane);
+            triangle<true>(x, it, split8(ks[0], ks[1]), split8(ks[2], ks[3]), lane);
             if (LEAVES == kKept) keep_tokens(keep.x + (bh * s.T + start) * kw, kw, len, col, lane, x);
             f32x4 l[4];
 #pragma unroll
@@ -380,8 +378,8 @@ delta_walk(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaFwd p, Kept 
                     l[i][r] = le[r] * x[i][r];
                 }
             }
-            u0 = split8<NS>(x[0], x[1]), u1 = split8<NS>(x[2], x[3]);
-            l0 = split8<NS>(l[0], l[1]), l1 = split8<NS>(l[2], l[3]);
+            u0 = split8(x[0], x[1]), u1 = split8(x[2], x[3]);
+            l0 = split8(l[0], l[1]), l1 = split8(l[2], l[3]);
         }
         if (!KEEP && kShare) {
             __syncthreads();  // the inverse is read
@@ -395,7 +393,7 @@ delta_walk(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaFwd p, Kept 
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) qs[i][r] *= en[i][r];
-                triangle<NS, true>(qs, at, u0, u1, lane);
+                triangle<true>(qs, at, u0, u1, lane);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -479,7 +477,7 @@ delta_walk_back(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaBwd p, 
 
     Tile<DT, KP, true> kn, qn;
     Tile<DT, 16 * kMaxWaves, false> on;
-    Rows64<3> tn, an;
+    Rows64 tn, an;
     Gates gn;
     // what shares a place follows later (of 192, reverse: 1178 us for 1194; of 256 1989
     // for 1737)
@@ -541,7 +539,7 @@ delta_walk_back(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaBwd p, 
             }
             o0 = Columns::frag(ot, 0, w * 16, lane);
             o1 = Columns::frag(ot, 32, w * 16, lane);
-            triangle<3, false>(po, at, o0, o1, lane);
+            triangle<false>(po, at, o0, o1, lane);
 #pragma unroll
             for (int g = 0; g < KP / 32; ++g) {
                 const Frag<3> sf = split8(S[2 * g], S[2 * g + 1]);
@@ -565,7 +563,7 @@ delta_walk_back(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaBwd p, 
         if (works) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[i] = f32x4{0, 0, 0, 0};
-            triangle<3, false>(x, it, split8(po[0], po[1]), split8(po[2], po[3]), lane);
+            triangle<false>(x, it, split8(po[0], po[1]), split8(po[2], po[3]), lane);
             if (!SPAN) keep_tokens(keep.r + (bh * s.T + start) * kw, kw, len, col, lane, x);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -758,7 +756,7 @@ Spread spread(const DeltaShape& s, int tiles, int parts, int most) {
     return Spread{waves, groups, dim3((unsigned)((heads + 7) / 8 * 8 * groups))};
 }
 
-template <int DT, int LEAVES, int NS>
+template <int DT, int LEAVES>
 hipError_t walk(const DeltaShape& s, const DeltaIn& in, const Blocks& blocks, const Prep& prep, const DeltaFwd& out,
                 const Kept& keep, const Parts& parts, hipStream_t st) {
     const Widths wd{row_width(s.K, DT), row_width(s.V, DT)};
@@ -766,28 +764,26 @@ hipError_t walk(const DeltaShape& s, const DeltaIn& in, const Blocks& blocks, co
     return by_rows(s, [&](auto rt) {
         constexpr int RT = decltype(rt)::value;
         const Spread x = spread(s, tiles, LEAVES == kSpan ? parts.n - 1 : parts.n, kMaxWaves);
-        delta_walk<DT, RT, LEAVES, NS>
+        delta_walk<DT, RT, LEAVES>
             <<<x.grid, kWalkThreads, 0, st>>>(s, in, blocks, prep, out, keep, parts, x.groups, x.waves, wd);
         return hipGetLastError();
     });
 }
 
 hipError_t run_walk(const DeltaShape& s, const DeltaIn& in, const Blocks& blocks, const Prep& prep,
-                    const DeltaFwd& out, const Kept* keep, const Parts& parts, int planes, hipStream_t st) {
+                    const DeltaFwd& out, const Kept* keep, const Parts& parts, hipStream_t st) {
     if (parts.n > 1) {
-        const hipError_t e = s.dtype == DT_F32 ? walk<DT_F32, kSpan, 3>(s, in, blocks, prep, out, Kept{}, parts, st)
-                             : planes == 2     ? walk<DT_BF16, kSpan, 2>(s, in, blocks, prep, out, Kept{}, parts, st)
-                                               : walk<DT_BF16, kSpan, 3>(s, in, blocks, prep, out, Kept{}, parts, st);
+        const hipError_t e = s.dtype == DT_F32 ? walk<DT_F32, kSpan>(s, in, blocks, prep, out, Kept{}, parts, st)
+                                               : walk<DT_BF16, kSpan>(s, in, blocks, prep, out, Kept{}, parts, st);
         if (e != hipSuccess) return e;
         const hipError_t f = run_join(s, blocks, parts, false, st);
         if (f != hipSuccess) return f;
     }
     if (s.dtype == DT_F32)
-        return keep ? walk<DT_F32, kKept, 3>(s, in, blocks, prep, out, *keep, parts, st)
-                    : walk<DT_F32, kOutputs, 3>(s, in, blocks, prep, out, Kept{}, parts, st);
-    if (keep) return walk<DT_BF16, kKept, 3>(s, in, blocks, prep, out, *keep, parts, st);
-    return planes == 2 ? walk<DT_BF16, kOutputs, 2>(s, in, blocks, prep, out, Kept{}, parts, st)
-                       : walk<DT_BF16, kOutputs, 3>(s, in, blocks, prep, out, Kept{}, parts, st);
+        return keep ? walk<DT_F32, kKept>(s, in, blocks, prep, out, *keep, parts, st)
+                    : walk<DT_F32, kOutputs>(s, in, blocks, prep, out, Kept{}, parts, st);
+    return keep ? walk<DT_BF16, kKept>(s, in, blocks, prep, out, *keep, parts, st)
+                : walk<DT_BF16, kOutputs>(s, in, blocks, prep, out, Kept{}, parts, st);
 }
 
 template <int DT, bool SPAN>

@@ -54,7 +54,7 @@ inline bool rows_whole(const HeadRows& r, int width, int bytes) {
 // Byte offsets into a call's workspace.
 struct Layout {
     size_t starts, counts, gates, gl, inv, att, att_t, inv_t, x, r, s, ds, sums, between, behind, map, map_t, q, k, v, go, total;
-    Layout(const DeltaShape& d, bool backward, int planes, bool reset, const Copies& copy) {
+    Layout(const DeltaShape& d, bool backward, bool reset, const Copies& copy) {
         const size_t tokens = (size_t)d.B * d.H * d.T, bytes = d.dtype == DT_F32 ? 4 : 2;
         size_t at = 0;
         auto take = [&](size_t& o, size_t n, bool wanted) {
@@ -65,8 +65,8 @@ struct Layout {
         take(counts, (size_t)d.B * 4, reset);
         take(gates, tokens * 16, true);
         take(gl, tokens * 4, backward);
-        take(inv, tokens * kC * 2 * planes, true);
-        take(att, tokens * kC * 2 * planes, !backward);
+        take(inv, tokens * kC * 6, true);
+        take(att, tokens * kC * 6, !backward);
         take(att_t, tokens * kC * 6, backward);
         take(inv_t, tokens * kC * 6, backward);
         take(x, tokens * kept_width(d.V) * 4, backward);
@@ -118,10 +118,10 @@ struct RowCopies {
 hipError_t run_copies(const RowCopies& copies, int64_t T, int dtype, hipStream_t st);
 hipError_t run_blocks(const DeltaShape& s, const uint8_t* reset, int* starts, int* counts, hipStream_t st);
 hipError_t run_prep(const DeltaShape& s, const DeltaIn& in, const Blocks& blocks, const Prep& prep, bool backward,
-                    int planes, hipStream_t st);
+                    hipStream_t st);
 // The walk over the blocks: outputs and the last state, or (keep) x and the entering states.
 hipError_t run_walk(const DeltaShape& s, const DeltaIn& in, const Blocks& blocks, const Prep& prep,
-                    const DeltaFwd& out, const Kept* keep, const Parts& parts, int planes, hipStream_t st);
+                    const DeltaFwd& out, const Kept* keep, const Parts& parts, hipStream_t st);
 // The walk back: r, grad_v, the gradients that leave blocks, and grad_h0.
 hipError_t run_walk_back(const DeltaShape& s, const DeltaIn& in, const Blocks& blocks, const Prep& prep,
                          const DeltaBwd& p, const HeadRows& go, const Kept& keep, const Parts& parts, hipStream_t st);
