@@ -89,12 +89,7 @@ __global__ void __launch_bounds__(kWide, 2) delta_grads(DeltaShape s, DeltaIn in
         blocks.at(b, c, start, len, first);
         const int next = start + len;
         const bool has_s = !first && (start > 0 || in.h0);
-        bool cut = false;
-        if (c + 1 < n) {
-            int x, y;
-            blocks.at(b, c + 1, x, y, cut);
-        }
-        const bool has_ds = next < s.T ? !cut : p.grad_last != nullptr;
+        const bool has_ds = next < s.T ? !blocks.cut_behind(b, c) : p.grad_last != nullptr;
         const int64_t nslots = state_slots(s.T);
         const Buffer krows = block_rows(in.k, b, hk, start, len), qrows = block_rows(in.q, b, hk, start, len);
         for (int d0 = 0; d0 < s.K; d0 += 16 * DN) {
@@ -109,8 +104,8 @@ __global__ void __launch_bounds__(kWide, 2) delta_grads(DeltaShape s, DeltaIn in
                 const int h = hk * share + hh;
                 const int64_t bh = b * s.H + h, t0 = bh * s.T + start;
                 const int64_t state = (int64_t)s.K * kw;
-                const Buffer S = buffer(keep.s + (bh * nslots + start / kC) * state, has_s ? state * 4 : 0);
-                const Buffer dS = buffer(keep.ds + (bh * nslots + (next < s.T ? next / kC : nslots - 1)) * state,
+                const Buffer S = buffer(keep.s + (bh * nslots + entering_slot(start)) * state, has_s ? state * 4 : 0);
+                const Buffer dS = buffer(keep.ds + (bh * nslots + leaving_slot(s.T, next)) * state,
                                          has_ds ? state * 4 : 0);
                 const Buffer orows = block_rows(go, b, h, start, len);
                 const Buffer xrows = buffer(keep.x + t0 * kw, (int64_t)len * kw * 4);

@@ -20,13 +20,12 @@
 
 #include "device.hpp"
 #include "delta.hpp"
+#include "delta_blocks.hpp"
 
 namespace lrscan {
 namespace delta {
 
-constexpr int kC = 64;       // tokens of a block
 constexpr int kThreads = 256;
-constexpr int kCut = (int)0x80000000;
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -296,29 +295,6 @@ __device__ __forceinline__ float sum16(float x) {
     x += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), 0x121, 0xf, 0xf, true));
     return x;
 }
-
-// ---- the blocks of a batch row ----
-// Every block of up to kC tokens lies within one segment, so no product reaches
-// from one segment into another.  Without resets they start at multiples of kC.
-struct Blocks {
-    const int* starts;  // [B][T + 1], kCut set where a segment starts, the last one T; NULL without resets
-    const int* counts;  // [B]
-    int T;
-    __device__ __forceinline__ int count(int64_t b) const { return starts ? counts[b] : (T + kC - 1) / kC; }
-    // block c, and whether a reset starts it
-    __device__ __forceinline__ void at(int64_t b, int c, int& start, int& len, bool& cut) const {
-        if (starts) {
-            const int* p = starts + b * ((int64_t)T + 1) + c;
-            cut = p[0] < 0;
-            start = p[0] & ~kCut;
-            len = (p[1] & ~kCut) - start;
-        } else {
-            start = c * kC;
-            len = min(kC, T - start);
-            cut = false;
-        }
-    }
-};
 
 // What prepares the blocks for the walk over them, by token: [B, H, T] and rows of kC.
 struct Prep {

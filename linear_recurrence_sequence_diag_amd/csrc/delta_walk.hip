@@ -44,8 +44,8 @@ __device__ __forceinline__ bool my_part(const DeltaShape& s, int groups, int par
 
 // The blocks of a part: [first, end).
 __device__ __forceinline__ void part_blocks(int n, int part, int parts, int& first, int& end) {
-    first = scalar((int)((int64_t)n * part / parts));
-    end = scalar((int)((int64_t)n * (part + 1) / parts));
+    first = scalar(part_start(n, part, parts));
+    end = scalar(part_start(n, part + 1, parts));
 }
 
 // A block's gates, [3][kC] in LDS.
@@ -321,7 +321,7 @@ delta_walk(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaFwd p, Kept 
 #pragma unroll
                 for (int i = 0; i < ND; ++i) S[i] = f32x4{0, 0, 0, 0};
             } else if (LEAVES == kKept) {
-                keep_state<ND>(keep.s + (bh * state_slots(s.T) + start / kC) * s.K * kw, s.K, kw, col, lane, S);
+                keep_state<ND>(keep.s + (bh * state_slots(s.T) + entering_slot(start)) * s.K * kw, s.K, kw, col, lane, S);
             }
         }
         // x += A S for rows A in LDS
@@ -499,8 +499,9 @@ delta_walk_back(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaBwd p, 
     bool first;  // whether a segment starts with the block
     blocks.at(b, n - 1, start, len, first);
     load(start, len);
-    // what leaves a block enters the one behind it, unless a segment starts there
-    bool cut = false;
+    // what leaves a block enters the one behind it, unless a segment starts there: then
+    // it is kept nowhere, as its place may be that of a block in another part
+    bool cut = blocks.cut_behind(b, n - 1);
     for (int c = n - 1; c >= to; --c) {
         const int behind = start + len;
         int prev = 0, plen = 0;
@@ -528,8 +529,7 @@ delta_walk_back(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaBwd p, 
 #pragma unroll
                 for (int i = 0; i < ND; ++i) S[i] = f32x4{0, 0, 0, 0};
             } else if (!SPAN) {
-                keep_state<ND>(keep.ds + (bh * slots + (behind < s.T ? behind / kC : slots - 1)) * s.K * kw, s.K, kw, col,
-                               lane, S);
+                keep_state<ND>(keep.ds + (bh * slots + leaving_slot(s.T, behind)) * s.K * kw, s.K, kw, col, lane, S);
             }
             end = gates[len - 1];
 #pragma unroll
@@ -645,12 +645,12 @@ __global__ void __launch_bounds__(kWalkThreads, 2) delta_join(DeltaShape s, Bloc
     auto tile_at = [&](int i) { return col < kw ? (uint32_t)(((i * 16 + lg * 4) * kw + col) * 4) : kNowhere; };
     const int first = BACK ? parts.n - 2 : 1, by = BACK ? -1 : 1, steps = parts.n - 2;
     if (threadIdx.x < parts.n) {
-        const int64_t b = bh / s.H, n = blocks.count(b);
+        const int64_t b = bh / s.H;
+        const int n = blocks.count(b), part = (int)threadIdx.x, end = part_start(n, part + 1, parts.n);
         bool any = false;
-        const int64_t end = n * (threadIdx.x + 1) / parts.n;
-        for (int64_t c = n * threadIdx.x / parts.n; c < end && !any; ++c) {
+        for (int c = part_start(n, part, parts.n); c < end && !any; ++c) {
             int start, len;
-            blocks.at(b, (int)c, start, len, any);
+            blocks.at(b, c, start, len, any);
         }
         barred[threadIdx.x] = any;
     }

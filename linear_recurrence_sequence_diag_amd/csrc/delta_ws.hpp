@@ -7,11 +7,6 @@
 namespace lrscan {
 namespace delta {
 
-// States at the blocks' starts: a block that a segment does not start begins 64
-// tokens behind another of its segment, so start / 64 is its own slot; one more
-// for the sequence's end.
-__host__ __device__ __forceinline__ int64_t state_slots(int64_t T) { return T / kC + 2; }
-
 // Elements of a row of n that is whole vectors of 16 bytes.
 inline int row_width(int n, int dtype) {
     const int per = dtype == DT_F32 ? 4 : 8;
