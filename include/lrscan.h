@@ -415,7 +415,8 @@ LRSCAN_API size_t scan_embed_workspace_bytes(int64_t N, int64_t V, int64_t D, in
  * beta in [0, 1] the state stays bounded.  A log_decay below -200 counts as
  * -200 (a decay of 0 in fp32).
  * At a reset step (opts->reset, [B,T]) the state that enters is dropped,
- * whatever it holds, and log_decay is not used; nothing of one segment reaches
+ * whatever it holds, and log_decay is not used (nor is the first step's where
+ * there is no initial state to decay); nothing of one segment reaches
  * another, be it an infinity or a NaN.  Within a segment an infinity may come
  * out as a NaN.
  * Tokens are taken in blocks of 64, whose products run on the matrix cores; all

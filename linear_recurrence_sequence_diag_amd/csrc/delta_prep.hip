@@ -116,7 +116,9 @@ __global__ void __launch_bounds__(kThreads, DT == DT_BF16 ? 3 : 2) delta_prep(De
         __syncthreads();  // the last block's LDS is read
         if (w == 0) {
             const bool ok = lane < len;
-            float g = ok ? *reinterpret_cast<const float*>(in.g.row(b, start + lane, h)) : 0.0f;
+            // nothing enters a segment's first token that its decay could act on, so that decay is 1
+            const bool first = lane == 0 && (cut || (start == 0 && !in.h0));
+            float g = ok && !first ? *reinterpret_cast<const float*>(in.g.row(b, start + lane, h)) : 0.0f;
             g = g < -200.0f ? -200.0f : g;  // exp is 0 there in fp32; no infinity enters a difference
             const float beta = ok ? *reinterpret_cast<const float*>(in.beta.row(b, start + lane, h)) : 0.0f;
             double G = g;

@@ -605,10 +605,13 @@ delta_walk_back(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaBwd p, 
             for (int i = 0; i < ND; ++i) S[i] = f32x4{0, 0, 0, 0};
         keep_state<ND>(parts.leave + (bh * parts.n + part - 1) * s.K * kw, s.K, kw, col, lane, S);
     }
-    if (!SPAN && p.grad_h0 && works && part == 0)
+    if (!SPAN && p.grad_h0 && works && part == 0) {
+        // without an initial state the blocks leave its decay out
+        const float decay = in.h0 ? 1.0f : expf(*reinterpret_cast<const float*>(in.g.row(b, 0, h)));
         each_state<ND>(s, bh, col, lane, [&](int i, int r, bool ok, int64_t at) {
-            if (ok) p.grad_h0[at] = cut ? 0.0f : S[i][r];
+            if (ok) p.grad_h0[at] = cut ? 0.0f : decay * S[i][r];
         });
+    }
 }
 
 // ---- parts of a long sequence ----

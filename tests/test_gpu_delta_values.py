@@ -59,3 +59,58 @@ def test_gradients_of_rows_in_parts_where_segments_start_densely(T, dense, dt):
             assert all(torch.equal(a, b) for a, b in zip(first, got))
         else:
             first = got
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), 100.0, 1000.0, float("-inf")])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [150, 1700])
+def test_a_segments_first_decay_is_not_used(T, dt, value):
+    """No value of log_decay where a segment starts changes a bit of any result, in the segment or outside."""
+    _, args, go = _inputs(1, T, 2, 1, 64, 32, dt, 3)
+    reset = torch.zeros(1, T, dtype=torch.bool, device="cuda")
+    cuts = [5, 64, 100, 101, T - 40]
+    reset[:, cuts] = True
+
+    def results(log_decay, r):
+        x = (*args[:3], log_decay, args[4])
+        return lr.delta_scan(*x, reset=r) + lr.delta_scan_backward(*x, go, reset=r)[:5]
+
+    bad, zero = args[3].clone(), args[3].clone()
+    at = [0] + cuts  # the row's first token has no state to decay either
+    bad[:, at], zero[:, at] = value, 0.0
+    for a, b in zip(results(zero, reset), results(bad, reset)):
+        assert torch.isfinite(a).all() and torch.equal(a, b)
+    bad[:, cuts] = zero[:, cuts]
+    for a, b in zip(results(zero, None), results(bad, None)):
+        assert torch.isfinite(a).all() and torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T", [40, 1300])
+def test_the_initial_states_gradient_where_there_is_none(T):
+    """grad_h0 of a call without h0 is that of a call from zeros, the first step's decay in it."""
+    _, args, go = _inputs(2, T, 2, 1, 64, 32, "f32", 4)
+    zeros = torch.zeros(2, 2, 64, 32, device="cuda")
+    got = lr.delta_scan_backward(*args, go, need_grad_h0=True)
+    want = lr.delta_scan_backward(*args, go, h0=zeros, need_grad_h0=True)
+    for a, b in zip(got, want):  # both keep the bounds of fp32 blocks, 64 u of the largest each
+        assert (a - b).abs().max() <= 2 * 64 * D.U * b.abs().max()
+    assert all(torch.equal(a, b) for a, b in zip(got, lr.delta_scan_backward(*args, go)[:5]))
+
+
+def test_a_prompt_and_its_tokens_one_by_one_agree_at_segment_starts():
+    """The steps drop the same decays as the blocks."""
+    T = 70
+    x, args, _ = _inputs(2, T, 2, 1, 32, 16, "f32", 5)
+    reset = torch.zeros(2, T, dtype=torch.bool)
+    reset[0, [3, 64]] = reset[1, [20, 66]] = True
+    x["log_decay"][reset] = float("nan")
+    args[3] = x["log_decay"].cuda()
+    ref = D.forward(*[x[n].double() for n in NAMES], 0.25, reset)
+    f32 = D.forward(*[x[n] for n in NAMES], 0.25, reset)
+    out, last = lr.delta_scan(*args, scale=0.25, reset=reset.cuda())
+    state = None
+    for t in range(T):
+        step, state = lr.delta_step(*[a[:, t] for a in args], state, scale=0.25, reset=reset[:, t].contiguous().cuda())
+        D.check("out", step, ref[0][:, t], f32[0][:, t], torch.float32)
+    for name, got, a, b in (("out", out, ref[0], f32[0]), ("last", last, ref[1], f32[1]), ("last", state, ref[1], f32[1])):
+        D.check(name, got, a, b, torch.float32)
