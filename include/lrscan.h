@@ -417,8 +417,13 @@ LRSCAN_API size_t scan_embed_workspace_bytes(int64_t N, int64_t V, int64_t D, in
  * At a reset step (opts->reset, [B,T]) the state that enters is dropped,
  * whatever it holds, and log_decay is not used (nor is the first step's where
  * there is no initial state to decay); nothing of one segment reaches
- * another, be it an infinity or a NaN.  Within a segment an infinity may come
- * out as a NaN.
+ * another, be it an infinity or a NaN.  Within a segment a value that is not
+ * finite (or that bf16 rounds to an infinity, above 3.39e38) reaches what depends
+ * on it, where it may come out as a NaN: of q its own step's output, of the others
+ * the outputs from its step on; of grad_out the gradients up to its step, of q its
+ * own step's alone.  The other gradients of a segment whose inputs are not all
+ * finite may be NaN throughout.  So are results where the sum of positive
+ * log_decay within 64 steps leaves the range of exp.
  * Tokens are taken in blocks of 64, whose products run on the matrix cores; all
  * sums and states are fp32.  A fp32 operand goes there as the sum of three bf16
  * parts, which has the accuracy of fp32.  Calls repeat bit for bit, and out is the

@@ -244,6 +244,23 @@ __global__ void __launch_bounds__(kThreads, DT == DT_BF16 ? 3 : 2) delta_prep(De
         }
         __syncthreads();
 
+        // A product of 16 or 32 rows brings a value that is not finite to the rows before its
+        // own too, as zero times it; what stands anywhere in the inverse stands in its last
+        // row.  Then a column a lane, every row from those before it alone.
+        if (__any(!(fabsf(Ti[(kC - 1) * kS + lane]) < INFINITY))) {
+            __syncthreads();
+            if (w == 0)
+                for (int r = 0; r < kC; ++r) {
+                    float y = r == lane ? 1.0f : 0.0f;
+                    for (int q = 0; q < r; ++q) {
+                        const float z = fmaf(-N[r * kS + q], Ti[q * kS + lane], y);
+                        y = q >= lane ? z : y;  // the rows before the column's own are zeros
+                    }
+                    Ti[r * kS + lane] = y;
+                }
+            __syncthreads();
+        }
+
         // rows of the inverse and of the outputs' weights
 #pragma unroll
         for (int i = 0; i < 2; ++i) {

@@ -223,6 +223,55 @@ __device__ __forceinline__ void triangle(f32x4 (&x)[4], const uint16_t* rows, co
     x[full] = c[0], x[full + 1] = c[1], x[half] = d[0], x[half + 1] = d[1];
 }
 
+// A triangle's rows do not take all of the 32 tokens that a product spans: the others'
+// weights are zeros, which leave a value out unless it is not finite.  So from a
+// column's first such token on (of the triangle that reaches back, up to its last
+// one) an operand is zeros, and the rows that do take it are made NaN afterwards.
+// What rounds to an infinity in bf16 counts as one.  Looking for such tokens is 1 to
+// 3% of a call (bf16 [8, 2048], 20 heads of 128: 367 -> 370 us, reverse 1338 -> 1355),
+// which without the branches marked as rare is 12%: spills.
+constexpr float kOver = 0x1.ffp127f;
+template <bool LOWER>
+__device__ __forceinline__ int mute(f32x4 (&y)[4], int lane) {
+    float most = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) most = __builtin_elementwise_maximum(most, fabsf(y[i][r]));  // NaN where there is one
+    int at = LOWER ? kC : -1;
+    if (__builtin_expect(__any(!(most < kOver)), 0)) {
+        auto each = [&](auto f) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) f(i * 16 + (lane >> 4) * 4 + r, i, r);
+        };
+        each([&](int t, int i, int r) {
+            if (!(fabsf(y[i][r]) < kOver)) at = LOWER ? min(at, t) : max(at, t);
+        });
+#pragma unroll
+        for (int m = 16; m < 64; m *= 2) {
+            const int other = __shfl_xor(at, m);
+            at = LOWER ? min(at, other) : max(at, other);
+        }
+        each([&](int t, int i, int r) {
+            if (LOWER ? t >= at : t <= at) y[i][r] = 0.0f;
+        });
+    }
+    return at;
+}
+template <bool LOWER>
+__device__ __forceinline__ void spoil(f32x4 (&x)[4], int at, int lane) {
+    if (__builtin_expect(!__any(LOWER ? at < kC : at >= 0), 1)) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int t = i * 16 + (lane >> 4) * 4 + r;
+            if (LOWER ? t >= at : t <= at) x[i][r] = __builtin_nanf("");
+        }
+}
+
 // Elements of the operands' rows of K and of V.
 struct Widths {
     int k, v;
@@ -353,6 +402,7 @@ delta_walk(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaFwd p, Kept 
         f32x4 en[4];
         Frag<3> l0, l1, u0, u1;
         float end = 0.0f;
+        int bad = kC;  // the column's first token whose value is not finite
         if (works) {
             end = gates[len - 1];
 #pragma unroll
@@ -365,7 +415,9 @@ delta_walk(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaFwd p, Kept 
             f32x4 x[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[i] = f32x4{0, 0, 0, 0};
+            bad = mute<true>(ks, lane);
             triangle<true>(x, it, split8(ks[0], ks[1]), split8(ks[2], ks[3]), lane);
+            spoil<true>(x, bad, lane);
             if (LEAVES == kKept) keep_tokens(keep.x + (bh * s.T + start) * kw, kw, len, col, lane, x);
             f32x4 l[4];
 #pragma unroll
@@ -378,6 +430,7 @@ delta_walk(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaFwd p, Kept 
                     l[i][r] = le[r] * x[i][r];
                 }
             }
+            if (!KEEP) bad = mute<true>(x, lane);
             u0 = split8(x[0], x[1]), u1 = split8(x[2], x[3]);
             l0 = split8(l[0], l[1]), l1 = split8(l[2], l[3]);
         }
@@ -394,6 +447,7 @@ delta_walk(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaFwd p, Kept 
 #pragma unroll
                     for (int r = 0; r < 4; ++r) qs[i][r] *= en[i][r];
                 triangle<true>(qs, at, u0, u1, lane);
+                spoil<true>(qs, bad, lane);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -540,6 +594,18 @@ delta_walk_back(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaBwd p, 
             o0 = Columns::frag(ot, 0, w * 16, lane);
             o1 = Columns::frag(ot, 32, w * 16, lane);
             triangle<false>(po, at, o0, o1, lane);
+            // a gradient that is not finite stands in every row of the first tile
+            if (__builtin_expect(__any(!(fabsf(po[0][0]) < INFINITY)), 0)) {
+                f32x4 o[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    o[i] = Columns::four(ot, i * 16, w * 16, lane);
+                    po[i] = f32x4{0, 0, 0, 0};
+                }
+                const int bad = mute<false>(o, lane);
+                triangle<false>(po, at, split8(o[0], o[1]), split8(o[2], o[3]), lane);
+                spoil<false>(po, bad, lane);
+            }
 #pragma unroll
             for (int g = 0; g < KP / 32; ++g) {
                 const Frag<3> sf = split8(S[2 * g], S[2 * g + 1]);
@@ -563,7 +629,9 @@ delta_walk_back(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaBwd p, 
         if (works) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[i] = f32x4{0, 0, 0, 0};
+            const int bad = mute<false>(po, lane);
             triangle<false>(x, it, split8(po[0], po[1]), split8(po[2], po[3]), lane);
+            spoil<false>(x, bad, lane);
             if (!SPAN) keep_tokens(keep.r + (bh * s.T + start) * kw, kw, len, col, lane, x);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {

@@ -114,3 +114,66 @@ def test_a_prompt_and_its_tokens_one_by_one_agree_at_segment_starts():
         D.check("out", step, ref[0][:, t], f32[0][:, t], torch.float32)
     for name, got, a, b in (("out", out, ref[0], f32[0]), ("last", last, ref[1], f32[1]), ("last", state, ref[1], f32[1])):
         D.check(name, got, a, b, torch.float32)
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(1, 300, 2, 1, 64, 40), (1, 1300, 2, 2, 128, 33), (1, 140, 1, 1, 200, 20)], ids=str)
+def test_outputs_before_a_value_that_is_not_finite(shape, dt, value):
+    """The recurrence is causal: a row's outputs in front of such a value, as of padding behind a sequence, are what
+    they are without it; from it on, and in the last state, they are not finite where they depend on it."""
+    T, V = shape[1], shape[-1]
+    x, args, _ = _inputs(*shape, dt, 6)
+    ref, f32 = ([t for t in D.forward(*[x[n].to(kind) for n in NAMES], 0.25)[:1]] for kind in (torch.float64, torch.float32))
+    clean, last = lr.delta_scan(*args, scale=0.25)
+    for t in sorted({0, 1, 15, 16, 40, 63, 64, 97, T - 1}):
+        for i, name in enumerate(NAMES):
+            bad = [a.clone() for a in args]
+            bad[i][:, t] = value
+            out, state = lr.delta_scan(*bad, scale=0.25)
+            if name in ("q", "v"):  # no rounding before it differs
+                assert torch.equal(out[:, :t], clean[:, :t]), (name, t)
+            elif t > 0:
+                D.check("out", out[:, :t], ref[0][:, :t], f32[0][:, :t], DT[dt])
+            if name == "q":
+                assert torch.equal(out[:, t + 1:], clean[:, t + 1:]) and torch.equal(state, last)
+                assert not torch.isfinite(out[:, t]).any()
+            elif name != "log_decay" or t > 0:  # the first one is not used
+                assert not torch.isfinite(out[:, t:]).all(-1).any() and not torch.isfinite(state).all(-1).any(), (name, t)
+        # one value of one head reaches its column alone
+        bad = args[2].clone()
+        bad[0, t, 0, V // 2] = value
+        out, state = lr.delta_scan(*args[:2], bad, *args[3:], scale=0.25)
+        mine = torch.zeros_like(out, dtype=torch.bool)
+        mine[:, t:, 0, V // 2] = True
+        assert torch.equal(out[~mine], clean[~mine]) and not torch.isfinite(out[mine]).any()
+        column = torch.zeros_like(state, dtype=torch.bool)
+        column[:, 0, :, V // 2] = True
+        assert torch.equal(state[~column], last[~column]) and not torch.isfinite(state[column]).any()
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("-inf")])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(1, 300, 2, 1, 64, 40), (1, 1300, 2, 2, 128, 33), (1, 140, 1, 1, 200, 20)], ids=str)
+def test_gradients_behind_an_outputs_gradient_that_is_not_finite(shape, dt, value):
+    """An output does not depend on the steps behind it, so neither do their gradients on its own."""
+    T = shape[1]
+    _, args, go = _inputs(*shape, dt, 7)
+    clean = lr.delta_scan_backward(*args, go)[:5]
+    for t in sorted({0, 15, 16, 40, 63, 64, 97, T - 1}):
+        bad = go.clone()
+        bad[:, t] = value
+        for a, b in zip(clean, lr.delta_scan_backward(*args, bad)[:5]):
+            assert torch.equal(a[:, t + 1:], b[:, t + 1:]), t
+        # and of the queries' gradients, the step's own alone
+        assert torch.equal(clean[0][:, :t], lr.delta_scan_backward(*args, bad)[0][:, :t])
+
+
+def test_values_past_the_type_of_the_products():
+    """A finite value that no bf16 holds counts as an infinity, from its own step on."""
+    _, args, _ = _inputs(1, 100, 1, 1, 32, 16, "f32", 8)
+    clean = lr.delta_scan(*args)[0]
+    args[2] = args[2].clone()
+    args[2][:, 50] = torch.finfo(torch.float32).max
+    out = lr.delta_scan(*args)[0]
+    assert torch.equal(out[:, :50], clean[:, :50])
