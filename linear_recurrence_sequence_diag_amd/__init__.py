@@ -13,6 +13,7 @@ calls raise.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
 
@@ -1147,6 +1148,14 @@ def adamw_update(params, grads, exp_avgs, exp_avg_sqs, step, rate=1e-3, betas=(0
     ``exp_avg_sq_scales`` (float32, one for each ADAMW_GROUP elements); the second
     then holds the root of the mean square.  ``grad_scale``: a float32 CUDA tensor
     of one element that multiplies the gradients."""
+    _enqueue(*_adamw_call(params, grads, exp_avgs, exp_avg_sqs, step, rate, betas, eps,
+                          weight_decay, masters, exp_avg_scales, exp_avg_sq_scales, grad_scale))
+
+
+def _adamw_call(params, grads, exp_avgs, exp_avg_sqs, step, rate, betas, eps, weight_decay,
+                masters, exp_avg_scales, exp_avg_sq_scales, grad_scale):
+    """What _enqueue takes for an update whose tensors are as they have to be; the
+    caller keeps them."""
     torch = _torch()
     count = len(params)
     small = exp_avg_scales is not None
@@ -1187,9 +1196,9 @@ def adamw_update(params, grads, exp_avgs, exp_avg_sqs, step, rate=1e-3, betas=(0
     if grad_scale is not None and not isinstance(grad_scale, torch.Tensor):
         raise ValueError("grad_scale must be a float32 CUDA (HIP) tensor of one element")
     table = (_I64 * len(flat))(*flat)
-    _enqueue(ref, scan_adamw, ctypes.addressof(table), count, 8 if small else 32, rate, betas[0],
-             betas[1], eps, weight_decay, 0 if on_device else step,
-             step.data_ptr() if on_device else None, _ptr(grad_scale), dtype_code(dtype))
+    return (ref, scan_adamw, table, count, 8 if small else 32, rate, betas[0], betas[1], eps,
+            weight_decay, 0 if on_device else step, step.data_ptr() if on_device else None,
+            _ptr(grad_scale), dtype_code(dtype))
 
 
 def _adamw_class():
@@ -1200,9 +1209,10 @@ def _adamw_class():
         a group that have a gradient.  ``state_bits`` 8 holds the states as e4m3 codes
         with a scale for each ADAMW_GROUP elements; ``master`` holds float32 weights
         beside bfloat16 params (from the first step on; params set later from outside
-        are overwritten by them).  ``step(grad_scale=...)`` multiplies the gradients.  The
-        count of steps is the host's, so a step is not captured into a graph (adamw_update
-        with ``step`` on the device is)."""
+        are overwritten by them).  ``step(grad_scale=...)`` multiplies the gradients; where
+        it refuses a tensor or a number, of whatever group, no weight, state or count has
+        changed.  The count of steps is the host's, so a step is not captured into a graph
+        (adamw_update with ``step`` on the device is)."""
 
         def __init__(self, params, rate=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2,
                      state_bits=32, master=False):
@@ -1212,9 +1222,8 @@ def _adamw_class():
                                           weight_decay=weight_decay, state_bits=state_bits,
                                           master=bool(master)))
 
-        def _begin(self, p, group):
-            s = self.state[p]
-            s["step"] = 0
+        def _first(self, p, group):
+            s = {"step": 0}
             if group["state_bits"] == 8:
                 groups = -(-p.numel() // ADAMW_GROUP)
                 for name in ("exp_avg", "exp_avg_sq"):
@@ -1226,6 +1235,7 @@ def _adamw_class():
                     s[name] = torch.zeros(p.shape, dtype=torch.float32, device=p.device)
             if group["master"] and p.dtype != torch.float32:
                 s["master"] = p.detach().float()
+            return s
 
         @torch.no_grad()
         def step(self, closure=None, grad_scale=None):
@@ -1236,30 +1246,37 @@ def _adamw_class():
             if closure is not None:
                 with torch.enable_grad():
                     loss = closure()
+            calls = []  # all of them are checked before the first one runs
             for group in self.param_groups:
+                rate, (b1, b2), eps, decay = (float(group["lr"]), group["betas"], group["eps"],
+                                              group["weight_decay"])
+                if not (math.isfinite(rate) and math.isfinite(decay) and 0.0 <= eps < math.inf
+                        and 0.0 <= b1 < 1.0 and 0.0 <= b2 < 1.0):
+                    raise LRScanError(-10, "AdamW.step")
                 alike = {}  # one update takes tensors of one device, dtype and step
                 for p in group["params"]:
                     if p.grad is None or p.numel() == 0:
                         continue
                     if not p.is_contiguous() or p.grad.is_sparse:
                         raise ValueError("params must be contiguous and their gradients dense")
-                    if not self.state[p]:
-                        self._begin(p, group)
-                    s = self.state[p]
-                    s["step"] += 1
-                    alike.setdefault((p.device, p.dtype, s["step"]), []).append(p)
-                for (_, _, at), ps in alike.items():
-                    states = [self.state[p] for p in ps]
+                    s = self.state.get(p) or self._first(p, group)
+                    alike.setdefault((p.device, p.dtype, s["step"] + 1), []).append((p, s))
+                for (_, _, at), rows in alike.items():
+                    ps, states = zip(*rows)
 
                     def kept(name):
                         return [s[name] for s in states] if name in states[0] else None
 
-                    adamw_update([p.detach() for p in ps], [p.grad.contiguous() for p in ps],
-                                 kept("exp_avg"), kept("exp_avg_sq"), at, rate=group["lr"],
-                                 betas=group["betas"], eps=group["eps"],
-                                 weight_decay=group["weight_decay"], masters=kept("master"),
-                                 exp_avg_scales=kept("exp_avg_scale"),
-                                 exp_avg_sq_scales=kept("exp_avg_sq_scale"), grad_scale=grad_scale)
+                    grads = [p.grad.contiguous() for p in ps]
+                    calls.append((_adamw_call([p.detach() for p in ps], grads, kept("exp_avg"),
+                                              kept("exp_avg_sq"), at, rate, (b1, b2), eps, decay,
+                                              kept("master"), kept("exp_avg_scale"),
+                                              kept("exp_avg_sq_scale"), grad_scale), rows, grads, at))
+            for call, rows, _, at in calls:
+                _enqueue(*call)
+                for p, s in rows:
+                    s["step"] = at
+                    self.state[p] = s
             return loss
 
         def load_state_dict(self, state_dict):
