@@ -706,6 +706,12 @@ def _enqueue(ref, call, *args):
         return call(*args, stream)
 
 
+def _written(*tensors):
+    """Tells autograd that a call has written tensors in place, so that a graph which
+    saved one of them refuses to go back through it."""
+    _torch().autograd.graph.increment_version(tensors)
+
+
 def _check_rows(name, t, ref, dims):
     """An operand whose rows may be strided: contiguous along the last dimension."""
     if not isinstance(t, _torch().Tensor) or not t.is_cuda:
@@ -1129,6 +1135,8 @@ def delta_step(q, k, v, log_decay, beta, state=None, scale=None, reset=None, wit
              beta.data_ptr(), K ** -0.5 if scale is None else scale, _ptr(state), _ptr(reset),
              _ptr(out), new.data_ptr(), B, H, HK, K, V, dtype_code(q.dtype),
              _head_strides(q, k, v, log_decay, beta))
+    if out_state is not None:
+        _written(out_state)
     return out, new
 
 
@@ -1150,6 +1158,7 @@ def adamw_update(params, grads, exp_avgs, exp_avg_sqs, step, rate=1e-3, betas=(0
     of one element that multiplies the gradients."""
     _enqueue(*_adamw_call(params, grads, exp_avgs, exp_avg_sqs, step, rate, betas, eps,
                           weight_decay, masters, exp_avg_scales, exp_avg_sq_scales, grad_scale))
+    _written(*params, *(masters or ()))
 
 
 def _adamw_call(params, grads, exp_avgs, exp_avg_sqs, step, rate, betas, eps, weight_decay,
@@ -1274,6 +1283,7 @@ def _adamw_class():
                                               kept("exp_avg_sq_scale"), grad_scale), rows, grads, at))
             for call, rows, _, at in calls:
                 _enqueue(*call)
+                _written(*(p for p, _ in rows), *(s["master"] for _, s in rows if "master" in s))
                 for p, s in rows:
                     s["step"] = at
                     self.state[p] = s
@@ -1352,7 +1362,8 @@ def adjust_logits(logits, tokens=None, lengths=None, prompt_lengths=None, repeti
     for name, t in (("repetition", repetition), ("presence", presence), ("frequency", frequency)):
         check(name, t, (B,), (torch.float32,))
     check("allowed", allowed, (B, -(-V // 32)), (torch.int32,))
-    if out is None:
+    given = out is not None
+    if not given:
         out = torch.empty((B, V), device=logits.device, dtype=logits.dtype)
     else:
         check("out", out, (B, V), (logits.dtype,), rows=True)
@@ -1369,6 +1380,8 @@ def adjust_logits(logits, tokens=None, lengths=None, prompt_lengths=None, repeti
              _ptr(prompt_lengths), _ptr(repetition), _ptr(presence), _ptr(frequency),
              _ptr(bias_ids), _ptr(bias), K, _ptr(allowed), 4 if kind == torch.int32 else 8, B, V,
              dtype_code(logits.dtype))
+    if given:
+        _written(out)
     return out
 
 

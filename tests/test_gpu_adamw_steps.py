@@ -87,3 +87,49 @@ def test_a_refused_step_changes_nothing(steps, bits, master):
     opt.step()
     other.step()
     _same(_held(other), _held(opt))
+
+
+@pytest.mark.parametrize("dtype,master", [(torch.float32, False), (torch.bfloat16, True)])
+def test_a_graph_from_before_an_update_is_refused(dtype, master):
+    """As with torch's optimizers: a backward through weights that a step has changed since raises."""
+    (w,) = _params(40, dtype=dtype)
+    opt = lr.AdamW([w], master=master)
+    loss = (w * w).sum()
+    loss.backward(retain_graph=True)
+    opt.step()
+    with pytest.raises(RuntimeError, match="modified by an inplace"):
+        loss.backward()
+    (w * w).sum().backward()  # a graph of the weights as they are now
+    # the update of lists tells it too
+    loss = (w * w).sum()
+    states = [torch.zeros(40, device="cuda") for _ in range(2)]
+    masters = [w.detach().float()]
+    seen = masters[0]._version
+    lr.adamw_update([w.detach()], [w.grad], [states[0]], [states[1]], 1, masters=masters)
+    assert masters[0]._version > seen
+    with pytest.raises(RuntimeError, match="modified by an inplace"):
+        loss.backward()
+
+
+def test_other_results_in_place_are_seen_too():
+    z = torch.randn(2, 50, device="cuda", requires_grad=True)
+    y = z.exp()
+    loss = (y * y).sum()
+    lr.adjust_logits(y.detach(), bias_ids=torch.zeros(2, 1, dtype=torch.int64, device="cuda"),
+                     bias=torch.ones(2, 1, device="cuda"), out=y.detach())
+    with pytest.raises(RuntimeError, match="modified by an inplace"):
+        loss.backward()
+    state = torch.randn(1, 1, 8, 8, device="cuda", requires_grad=True)
+    kept = state * 1.0
+    loss = (kept * kept).sum()
+    rows = [torch.randn(1, 1, 8, device="cuda") for _ in range(3)] + [torch.zeros(1, 1, device="cuda")] * 2
+    lr.delta_step(*rows, kept.detach(), out_state=kept.detach())
+    with pytest.raises(RuntimeError, match="modified by an inplace"):
+        loss.backward()
+    with torch.inference_mode():  # tensors without a version
+        held = torch.zeros(1, 1, 8, 8, device="cuda")
+        lr.delta_step(*rows, held, out_state=held)
+        x = torch.randn(2, 50, device="cuda")
+        lr.adjust_logits(x, out=x)
+        p, g, m, v = (torch.ones(9, device="cuda") for _ in range(4))
+        lr.adamw_update([p], [g], [m], [v], 1)
