@@ -410,7 +410,10 @@ LRSCAN_API size_t scan_embed_workspace_bytes(int64_t N, int64_t V, int64_t D, in
  *   out_t = scale S_t^T q_t.
  * q, k [B,T,HK,K] and v [B,T,H,V] of `dtype`; log_decay and beta [B,T,H] fp32;
  * value head h reads query/key head h / (H / HK) (H a multiple of HK).  K is at
- * most 256, H and V at most 65536, H V and HK K at most 2^22, T at most 2^30
+ * most 256, H and V at most 65536, H V and HK K at most 2^22; for launches of fewer
+ * than 2^32 work-items, B H rounded up to 8 times ceil(V / 128) is below 2^23,
+ * B H ceil(T / 64) below 2^24, in the backward B HK ceil(T / 64) below 2^23, B with
+ * resets below 2^22, and of a step B H ceil(V / 64) below 2^24
  * (LRSCAN_ERR_DIM).  Queries and keys are taken as they are: with keys of norm 1 and
  * beta in [0, 1] the state stays bounded.  A log_decay below -200 counts as
  * -200 (a decay of 0 in fp32).
@@ -479,7 +482,8 @@ LRSCAN_API size_t scan_delta_workspace_bytes(int64_t B, int64_t T, int64_t H, in
  * that takes the largest magnitude to 448; a root above zero is held as at least
  * the smallest code above zero.  All zero is a valid first state.  A gradient
  * that is not finite makes states of its group of 256 not finite.
- * Tensors lie 16-byte aligned for the fast path, and do not overlap.
+ * Tensors lie 16-byte aligned for the fast path, and do not overlap; each holds at
+ * most 2^36 - 4096 elements (LRSCAN_ERR_DIM).
  * ------------------------------------------------------------------------ */
 typedef struct {
     void* param;
@@ -512,7 +516,8 @@ LRSCAN_API int scan_adamw(const lrscan_adamw_tensor* tensors, int64_t count, int
  * Tokens and list entries outside [0, V) name nothing.
  * tokens, lengths, prompts and bias_ids are whole numbers of id_bytes (4 or 8).
  * repetition, presence, frequency [B], bias [B,K] fp32.  Each of the rules may
- * be NULL.  in_stride, out_stride, token_stride: elements between rows.  out may
+ * be NULL.  B ceil(V / 4096) is below 2^23, and L and K below 2^31, V up to 2^31 - 32
+ * (LRSCAN_ERR_DIM).  in_stride, out_stride, token_stride: elements between rows.  out may
  * be logits itself (with the same stride).
  * ------------------------------------------------------------------------ */
 LRSCAN_API int scan_logits(const void* logits, int64_t in_stride, void* out, int64_t out_stride,

@@ -29,8 +29,7 @@
 namespace lrscan {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kPerBlock = 4096;  // elements of a workgroup, all of them loaded first
+constexpr int kThreads = kAdamwThreads, kPerBlock = kAdamwPerBlock;
 constexpr int kTensors = 56;
 constexpr float kTop = 448.0f, kBottom = 0x1p-9f;  // of e4m3
 
@@ -273,7 +272,7 @@ hipError_t launch_adamw(const lrscan_adamw_tensor* tensors, int64_t count, int d
         while (list.n < kTensors && from < count) {
             const lrscan_adamw_tensor& t = tensors[from];
             const int64_t blocks = (t.n + kPerBlock - 1) / kPerBlock;
-            if (list.n && list.first[list.n] + blocks > ((int64_t)1 << 30)) break;
+            if (list.first[list.n] + blocks > kAdamwMaxBlocks) break;
             list.t[list.n] = t;
             list.first[list.n + 1] = list.first[list.n] + (uint32_t)blocks;
             ++list.n;

@@ -16,6 +16,10 @@ struct AdamwArgs {
 };
 
 constexpr int kAdamwGroup = 256;  // elements that share the scale of an 8-bit state
+constexpr int kAdamwThreads = 256, kAdamwPerBlock = 4096;  // of a workgroup; its elements, all of them loaded first
+// Workgroups whose work-items stay in 32 bits, and what a tensor may hold.
+constexpr int64_t kAdamwMaxBlocks = ((int64_t)1 << 32) / kAdamwThreads - 1;
+constexpr int64_t kAdamwMaxElems = kAdamwMaxBlocks * kAdamwPerBlock;
 
 hipError_t launch_adamw(const lrscan_adamw_tensor* tensors, int64_t count, int dtype, int state_bits, bool masters,
                         const AdamwArgs& a, hipStream_t st);

@@ -491,14 +491,15 @@ bool head_strides_ok(const int64_t* strides, const DeltaShape& s) {
     return true;
 }
 
-int delta_shape(int64_t B, int64_t T, int64_t H, int64_t HK, int64_t K, int64_t V, int dtype, DeltaShape* s) {
+int delta_shape(int64_t B, int64_t T, int64_t H, int64_t HK, int64_t K, int64_t V, int dtype, DeltaPass pass, bool reset,
+                DeltaShape* s) {
     if (B < 1 || T < 1 || H < 1 || HK < 1 || K < 1 || V < 1) return LRSCAN_ERR_DIM;
     if (H > kMaxElems || HK > H || H % HK != 0 || K > kDeltaMaxK || V > kMaxElems) return LRSCAN_ERR_DIM;
     if (!dims_ok(B, T, H) || H * B * T > kMaxElems / (V > K ? V : K)) return LRSCAN_ERR_DIM;
     if (!dtype_ok(dtype)) return LRSCAN_ERR_DTYPE;
     if (H > 65536 || V > 65536) return LRSCAN_ERR_DIM;
     *s = DeltaShape{B, T, (int)H, (int)HK, (int)K, (int)V, dtype};
-    return delta_fits(*s) ? LRSCAN_OK : LRSCAN_ERR_DIM;
+    return delta_fits(*s, pass, reset) ? LRSCAN_OK : LRSCAN_ERR_DIM;
 }
 
 int delta_opts_ok(const lrscan_opts* o) {
@@ -1194,11 +1195,11 @@ LRSCAN_API int scan_delta_fwd(const void* q, const void* k, const void* v, const
                               const lrscan_opts* opts) {
     if (!q || !k || !v || !log_decay || !beta || (!out && !last)) return LRSCAN_ERR_NULL;
     DeltaShape s;
-    int rc = delta_shape(B, T, H, HK, K, V, dtype, &s);
+    const uint8_t* reset = opts ? opts->reset : nullptr;
+    int rc = delta_shape(B, T, H, HK, K, V, dtype, kDeltaForward, reset != nullptr, &s);
     if (rc != LRSCAN_OK) return rc;
     if (!std::isfinite(scale) || !head_strides_ok(strides, s)) return LRSCAN_ERR_ARG;
     if ((rc = delta_opts_ok(opts)) != LRSCAN_OK) return rc;
-    const uint8_t* reset = opts ? opts->reset : nullptr;
     hipStream_t hs = static_cast<hipStream_t>(stream);
     const DeltaIn in = delta_in(s, q, k, v, log_decay, beta, scale, opts ? opts->h0 : nullptr, reset, strides);
     void* ws = nullptr;
@@ -1216,11 +1217,11 @@ LRSCAN_API int scan_delta_bwd(const void* q, const void* k, const void* v, const
         !grad_beta)
         return LRSCAN_ERR_NULL;
     DeltaShape s;
-    int rc = delta_shape(B, T, H, HK, K, V, dtype, &s);
+    const uint8_t* reset = opts ? opts->reset : nullptr;
+    int rc = delta_shape(B, T, H, HK, K, V, dtype, kDeltaBackward, reset != nullptr, &s);
     if (rc != LRSCAN_OK) return rc;
     if (!std::isfinite(scale) || !head_strides_ok(strides, s)) return LRSCAN_ERR_ARG;
     if ((rc = delta_opts_ok(opts)) != LRSCAN_OK) return rc;
-    const uint8_t* reset = opts ? opts->reset : nullptr;
     hipStream_t hs = static_cast<hipStream_t>(stream);
     const DeltaIn in = delta_in(s, q, k, v, log_decay, beta, scale, opts ? opts->h0 : nullptr, reset, strides);
     void* ws = nullptr;
@@ -1237,7 +1238,7 @@ LRSCAN_API int scan_delta_step(const void* q, const void* k, const void* v, cons
                                const int64_t* strides, void* stream) {
     if (!q || !k || !v || !log_decay || !beta || (!out && !state_out)) return LRSCAN_ERR_NULL;
     DeltaShape s;
-    const int rc = delta_shape(B, 1, H, HK, K, V, dtype, &s);
+    const int rc = delta_shape(B, 1, H, HK, K, V, dtype, kDeltaStep, false, &s);
     if (rc != LRSCAN_OK) return rc;
     int64_t rows[15];
     for (int i = 0; strides && i < 5; ++i) {
@@ -1254,7 +1255,7 @@ LRSCAN_API int scan_delta_step(const void* q, const void* k, const void* v, cons
 LRSCAN_API size_t scan_delta_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t HK, int64_t K, int64_t V,
                                              int dtype, int backward) {
     DeltaShape s;
-    if (delta_shape(B, T, H, HK, K, V, dtype, &s) != LRSCAN_OK) return 0;
+    if (delta_shape(B, T, H, HK, K, V, dtype, backward ? kDeltaBackward : kDeltaForward, false, &s) != LRSCAN_OK) return 0;
     return delta_ws_bytes(s, nullptr, nullptr, backward != 0);
 }
 
@@ -1273,7 +1274,7 @@ LRSCAN_API int scan_adamw(const lrscan_adamw_tensor* tensors, int64_t count, int
         if (!t.param || !t.grad || !t.exp_avg || !t.exp_avg_sq || (t.master != nullptr) != masters)
             return LRSCAN_ERR_NULL;
         if (state_bits == 8 && (!t.exp_avg_scale || !t.exp_avg_sq_scale)) return LRSCAN_ERR_NULL;
-        if (t.n < 1 || t.n > kMaxElems) return LRSCAN_ERR_DIM;
+        if (t.n < 1 || t.n > kAdamwMaxElems) return LRSCAN_ERR_DIM;
     }
     if (!std::isfinite(rate) || !std::isfinite(weight_decay) || !(eps >= 0.0) || !std::isfinite(eps) ||
         !(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || (!step_dev && step < 1))

@@ -16,6 +16,9 @@ HeadRows contiguous(const DeltaShape& s, const void* p, int64_t heads, int width
     return HeadRows{static_cast<char*>(const_cast<void*>(p)), s.T * heads * sh, heads * sh, sh};
 }
 
+constexpr int kStepColumns = 64;  // of a workgroup of the step
+int step_groups(const DeltaShape& s) { return (s.V + kStepColumns - 1) / kStepColumns; }
+
 Copies copies(const DeltaShape& s, const DeltaIn& in, const void* grad_out) {
     const int e = s.dtype == DT_F32 ? 4 : 2;
     return Copies{!rows_whole(in.q, s.K, e), !rows_whole(in.k, s.K, e), !rows_whole(in.v, s.V, e),
@@ -24,13 +27,18 @@ Copies copies(const DeltaShape& s, const DeltaIn& in, const void* grad_out) {
 
 }  // namespace
 
-bool delta_fits(const DeltaShape& s) {
+bool delta_fits(const DeltaShape& s, DeltaPass pass, bool reset) {
     if (s.K > kDeltaMaxK || s.V > 65536 || s.H > 65536 || s.T > ((int64_t)1 << 30)) return false;
     if ((int64_t)s.H * s.V > (1 << 22) || (int64_t)s.HK * s.K > (1 << 22)) return false;  // 32-bit offsets in a block's rows
-    const int64_t slots = (s.T + kC - 1) / kC, groups = (s.V + 15) / 16;
-    const int64_t heads = s.B * s.H;  // B * T * H * V is within 2^40
-    // (parts are formed only of few heads: at most 256 in all)
-    return heads <= ((int64_t)1 << 30) / groups && heads <= ((int64_t)1 << 30) / slots;
+    // work-items of a grid in 32 bits (B * T * H * V is within 2^40)
+    auto grid_fits = [](int64_t workgroups, int64_t threads) { return workgroups < ((int64_t)1 << 32) / threads; };
+    const int64_t slots = (s.T + kC - 1) / kC, heads = s.B * s.H;
+    if (pass == kDeltaStep) return grid_fits(heads * step_groups(s), kThreads);
+    // the walks (of few heads, which is where parts are formed and columns spread, they are far smaller)
+    if (!grid_fits((heads + 7) / 8 * 8 * ((s.V + 127) / 128), kWalkThreads)) return false;
+    if (reset && !grid_fits(s.B, kScanThreads)) return false;
+    if (pass == kDeltaBackward && !grid_fits(s.B * s.HK * slots, kGradThreads)) return false;
+    return grid_fits(heads * slots, kThreads);
 }
 
 size_t delta_ws_bytes(const DeltaShape& s, const DeltaIn* in, const void* grad_out, bool backward) {
@@ -223,7 +231,7 @@ __global__ void __launch_bounds__(kThreads) delta_step(DeltaShape s, DeltaIn in,
 
 template <int DT, int COLS, int CV>
 hipError_t step(const DeltaShape& s, const DeltaIn& in, const DeltaFwd& p, hipStream_t st) {
-    const int groups = (s.V + COLS - 1) / COLS;
+    const int groups = step_groups(s);
     delta_step<DT, COLS, CV><<<dim3((unsigned)(s.B * s.H * groups)), kThreads, 0, st>>>(s, in, p, groups);
     return hipGetLastError();
 }
@@ -232,8 +240,8 @@ template <int DT>
 hipError_t step_of(const DeltaShape& s, const DeltaIn& in, const DeltaFwd& p, hipStream_t st) {
     const bool vec = (reinterpret_cast<uintptr_t>(in.h0) | reinterpret_cast<uintptr_t>(p.last) |
                       (uintptr_t)(s.V * 4)) % 16 == 0;
-    if (!vec) return step<DT, 64, 1>(s, in, p, st);
-    return step<DT, 64, 4>(s, in, p, st);
+    if (!vec) return step<DT, kStepColumns, 1>(s, in, p, st);
+    return step<DT, kStepColumns, 4>(s, in, p, st);
 }
 
 }  // namespace delta

@@ -47,7 +47,8 @@ struct DeltaBwd {
 constexpr int kDeltaMaxK = 256;
 
 // Whether the shape's launches and offsets fit what the kernels count with.
-bool delta_fits(const DeltaShape& s);
+enum DeltaPass { kDeltaForward, kDeltaBackward, kDeltaStep };
+bool delta_fits(const DeltaShape& s, DeltaPass pass, bool reset);
 // Scratch of a call (256-byte aligned; rewritten before it is read), or (in NULL)
 // of the call with the largest of any operands of these sizes; grad_out: of a backward.
 size_t delta_ws_bytes(const DeltaShape& s, const DeltaIn* in, const void* grad_out, bool backward);

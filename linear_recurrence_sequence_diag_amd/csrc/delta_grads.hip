@@ -33,7 +33,6 @@
 namespace lrscan {
 namespace delta {
 
-constexpr int kWide = 512;    // threads of a workgroup
 constexpr int kGS = kC + 8;   // elements of an LDS row of 64
 constexpr int kGPlane = kC * kGS;
 
@@ -47,7 +46,7 @@ __device__ __forceinline__ void mma_pair(f32x4& c0, f32x4& c1, const Frag<NA> (&
 // TT: tiles of 16 tokens of a wavefront, 4, or 2 where K leaves half of the
 // wavefronts without columns.
 template <int DT, int TT>
-__global__ void __launch_bounds__(kWide, 2) delta_grads(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaBwd p,
+__global__ void __launch_bounds__(kGradThreads, 2) delta_grads(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaBwd p,
                                                         HeadRows go, Kept keep, int wk, int wv, int slots) {
     constexpr int NP = kPlanes<DT>;
     constexpr int DN = 2 * TT;                       // tiles of columns of a workgroup
@@ -58,10 +57,10 @@ __global__ void __launch_bounds__(kWide, 2) delta_grads(DeltaShape s, DeltaIn in
     __shared__ __attribute__((aligned(16))) uint16_t pt[3 * kGPlane], lt[3 * kGPlane];  // PD, LD [j][i]
     __shared__ __attribute__((aligned(16))) float gates[5 * kC];  // enter, leave, beta, G in two
     __shared__ __attribute__((aligned(16))) float dg[DN * kC];
-    __shared__ float ends[kWide / 64];
+    __shared__ float ends[kGradThreads / 64];
     // sums over the heads that share a q and k: as many of the two as there is room for here
     constexpr int kHeld = DT == DT_BF16 ? (TT == 2 ? 2 : 1) : TT == 2 ? 1 : 0;
-    __shared__ f32x4 held[kHeld ? kHeld * TT * kWide : 1];
+    __shared__ f32x4 held[kHeld ? kHeld * TT * kGradThreads : 1];
     uint16_t *const xt = ops, *const rt = ops + 3 * kGPlane, *const ot = ops + 6 * kGPlane;
     uint16_t *const kb = ops, *const qb = ops + NP * kKPlane;
     const float *const enter = gates, *const leave = gates + kC, *const beta = gates + 2 * kC, *const gh = gates + 3 * kC,
@@ -97,8 +96,8 @@ __global__ void __launch_bounds__(kWide, 2) delta_grads(DeltaShape s, DeltaIn in
             const bool works = d0 + dt * 16 < s.K;
             // this thread's sums of q (n = 0) and k (1)
             auto sum = [&](int n, int i) -> f32x4& {
-                return n < kHeld ? held[(n * TT + i) * kWide + threadIdx.x]
-                                 : keep.sums[((int64_t)blockIdx.x * 8 + n * TT + i) * kWide + threadIdx.x];
+                return n < kHeld ? held[(n * TT + i) * kGradThreads + threadIdx.x]
+                                 : keep.sums[((int64_t)blockIdx.x * 8 + n * TT + i) * kGradThreads + threadIdx.x];
             };
             for (int hh = 0; hh < share; ++hh) {
                 const int h = hk * share + hh;
@@ -188,7 +187,7 @@ __global__ void __launch_bounds__(kWide, 2) delta_grads(DeltaShape s, DeltaIn in
                 Raw8<DT> kn[DN / 4], qn[DN / 4];
 #pragma unroll
                 for (int i = 0; i < DN / 4; ++i) {
-                    const int at = i * kWide + threadIdx.x, row = at / (DN * 2), q = at % (DN * 2) * 8;
+                    const int at = i * kGradThreads + threadIdx.x, row = at / (DN * 2), q = at % (DN * 2) * 8;
                     kn[i].load(krows, row * (int)in.k.st, d0 + q, wk);
                     qn[i].load(qrows, row * (int)in.q.st, d0 + q, wk);
                 }
@@ -222,7 +221,7 @@ __global__ void __launch_bounds__(kWide, 2) delta_grads(DeltaShape s, DeltaIn in
                 __syncthreads();
 #pragma unroll
                 for (int i = 0; i < DN / 4; ++i) {
-                    const int at = i * kWide + threadIdx.x, row = at / (DN * 2), q = at % (DN * 2) * 8;
+                    const int at = i * kGradThreads + threadIdx.x, row = at / (DN * 2), q = at % (DN * 2) * 8;
                     store_frag(kb + row * kKS + q, kKPlane, kn[i].frag());
                     store_frag(qb + row * kKS + q, kKPlane, qn[i].frag());
                 }
@@ -316,7 +315,7 @@ template <int DT, int TT>
 hipError_t grads(const DeltaShape& s, const DeltaIn& in, const Blocks& blocks, const Prep& prep, const DeltaBwd& p,
                  const HeadRows& go, const Kept& keep, hipStream_t st) {
     const int slots = (int)((s.T + kC - 1) / kC);
-    delta_grads<DT, TT><<<dim3((unsigned)(s.B * s.HK * slots)), kWide, 0, st>>>(
+    delta_grads<DT, TT><<<dim3((unsigned)(s.B * s.HK * slots)), kGradThreads, 0, st>>>(
         s, in, blocks, prep, p, go, keep, row_width(s.K, DT), row_width(s.V, DT), slots);
     return hipGetLastError();
 }

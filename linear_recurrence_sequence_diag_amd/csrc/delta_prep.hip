@@ -22,7 +22,6 @@ namespace lrscan {
 namespace delta {
 
 // ---- blocks between resets ----
-constexpr int kScanThreads = 1024;
 constexpr int kScanTokens = 16;  // of one thread
 
 // Inclusive scan of one int a thread over the workgroup (max or sum).

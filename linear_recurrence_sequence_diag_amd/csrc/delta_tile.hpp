@@ -25,7 +25,10 @@
 namespace lrscan {
 namespace delta {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;       // of a workgroup of blocks' operands, and of the step
+constexpr int kWalkThreads = 512;   // of the walks
+constexpr int kGradThreads = 512;   // of the gradients
+constexpr int kScanThreads = 1024;  // of the search for segment starts
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));

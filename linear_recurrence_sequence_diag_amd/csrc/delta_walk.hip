@@ -27,7 +27,6 @@
 namespace lrscan {
 namespace delta {
 
-constexpr int kWalkThreads = 512;
 constexpr int kMaxWaves = 8;         // wavefronts with columns, at most; the launch says how many
 constexpr int kTS = kC + 8;          // elements of an LDS row of 64
 constexpr int kTPlane = kC * kTS;

@@ -69,7 +69,7 @@ struct Layout {
         const size_t state = (size_t)d.B * d.H * state_slots(d.T) * d.K * kept_width(d.V) * 4;
         take(s, state, backward);
         take(ds, state, backward);
-        take(sums, (size_t)d.B * d.HK * ((d.T + kC - 1) / kC) * 512 * 8 * 16, backward && d.H > d.HK);
+        take(sums, (size_t)d.B * d.HK * ((d.T + kC - 1) / kC) * kGradThreads * 8 * 16, backward && d.H > d.HK);
         const int64_t parts = sequence_parts(d);
         const size_t heads = (size_t)d.B * d.H * parts;
         take(between, heads * d.K * kept_width(d.V) * 4, parts > 1);

@@ -239,7 +239,7 @@ void by_ids(const LogitsArgs& a, hipStream_t st) {
 
 bool logits_fits(const LogitsArgs& a) {
     return a.V <= ((int64_t)1 << 31) - 32 && a.L <= ((int64_t)1 << 31) - 1 && a.K <= ((int64_t)1 << 31) - 1 &&
-           a.B <= ((int64_t)1 << 31) / ((a.V + kSlice - 1) / kSlice) - 1;
+           a.B <= (((int64_t)1 << 32) / kThreads - 1) / ((a.V + kSlice - 1) / kSlice);  // work-items of the grid in 32 bits
 }
 
 hipError_t launch_logits(const LogitsArgs& a, hipStream_t st) {
