@@ -1231,6 +1231,17 @@ def _adamw_class():
                                           weight_decay=weight_decay, state_bits=state_bits,
                                           master=bool(master)))
 
+        def add_param_group(self, param_group):
+            # a group's options have the constructor's names; torch keeps the rate as lr
+            if isinstance(param_group, dict) and "rate" in param_group:
+                if "lr" in param_group:
+                    raise ValueError("a group's rate and lr are one option")
+                param_group = dict(param_group)
+                param_group["lr"] = param_group.pop("rate")
+            if isinstance(param_group, dict) and param_group.get("state_bits", 8) not in (8, 32):
+                raise ValueError("state_bits must be 8 or 32")
+            super().add_param_group(param_group)
+
         def _first(self, p, group):
             s = {"step": 0}
             if group["state_bits"] == 8:
