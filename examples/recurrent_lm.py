@@ -146,8 +146,8 @@ def generate(model, prompt, n, repetition=1.0, presence=0.0, frequency=0.0):
     repetition on tokens of the prompt and the answer, presence and frequency on the answer's."""
     B, P = prompt.shape
     logits, states = model.prefill(prompt)
-    out = torch.cat([prompt, prompt.new_zeros(B, n)], 1)
-    said, asked = (prompt.new_full((B,), P) for _ in range(2))
+    out = torch.cat([prompt, prompt.new_zeros(B, n, dtype=torch.int64)], 1)  # of argmax's type
+    said, asked = (out.new_full((B,), P) for _ in range(2))
     rules = {}
     if (repetition, presence, frequency) != (1.0, 0.0, 0.0):
         rules = {name: logits.new_full((B,), x, dtype=torch.float32)
