@@ -32,10 +32,12 @@ struct Blocks {
             cut = false;
         }
     }
-    // whether a reset starts the block behind c (nothing does where c is the last one)
-    __host__ __device__ __forceinline__ bool cut_behind(int64_t b, int c) const {
-        if (!starts || c + 1 >= counts[b]) return false;
-        return starts[b * ((int64_t)T + 1) + c + 1] < 0;
+    // whether a reset starts the block behind c, of n
+    __host__ __device__ __forceinline__ bool cut_behind(int64_t b, int c, int n) const {
+        bool cut = false;
+        int start, len;
+        if (c + 1 < n) at(b, c + 1, start, len, cut);
+        return cut;
     }
 };
 

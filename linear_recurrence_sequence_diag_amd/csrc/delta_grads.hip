@@ -88,7 +88,8 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads(DeltaShape s, Del
         blocks.at(b, c, start, len, first);
         const int next = start + len;
         const bool has_s = !first && (start > 0 || in.h0);
-        const bool has_ds = next < s.T ? !blocks.cut_behind(b, c) : p.grad_last != nullptr;
+        const bool cut = blocks.cut_behind(b, c, n);
+        const bool has_ds = next < s.T ? !cut : p.grad_last != nullptr;
         const int64_t nslots = state_slots(s.T);
         const Buffer krows = block_rows(in.k, b, hk, start, len), qrows = block_rows(in.q, b, hk, start, len);
         for (int d0 = 0; d0 < s.K; d0 += 16 * DN) {

@@ -546,15 +546,16 @@ delta_walk_back(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaBwd p, 
         an.load(prep.att_t, bh * s.T + start, len);
         if (!kLater) load_later(start, len);
     };
+    const int count = blocks.count(b);
     int to, n;
-    part_blocks(blocks.count(b), part, parts.n, to, n);
+    part_blocks(count, part, parts.n, to, n);
     int start, len;
     bool first;  // whether a segment starts with the block
     blocks.at(b, n - 1, start, len, first);
     load(start, len);
     // what leaves a block enters the one behind it, unless a segment starts there: then
     // it is kept nowhere, as its place may be that of a block in another part
-    bool cut = blocks.cut_behind(b, n - 1);
+    bool cut = blocks.cut_behind(b, n - 1, count);
     for (int c = n - 1; c >= to; --c) {
         const int behind = start + len;
         int prev = 0, plen = 0;

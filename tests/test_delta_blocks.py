@@ -60,7 +60,7 @@ void replay(const std::vector<char>& reset, int parts) {
             else if (by[0] != c) ++wrong;
         };
         if (!cut && start > 0) check(enters[entering_slot(start)]);
-        if (!blocks.cut_behind(0, c)) check(leaves[leaving_slot(T, start + len)]);
+        if (!blocks.cut_behind(0, c, n)) check(leaves[leaving_slot(T, start + len)]);
     }
 }
 
@@ -95,7 +95,7 @@ def _replay(tmp_path, behind):
 
 def test_what_the_gradients_read_has_one_writer(tmp_path):
     """As the walk back does: whether a segment starts behind a part's last block is the next block's to say."""
-    rows, read, shared, wrong = _replay(tmp_path, "blocks.cut_behind(0, end - 1)")
+    rows, read, shared, wrong = _replay(tmp_path, "blocks.cut_behind(0, end - 1, n)")
     assert rows > 1000 and read > 10 ** 4 and (shared, wrong) == (0, 0)
 
 
