@@ -324,9 +324,9 @@ delta_walk(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaFwd p, Kept 
     Rows64 tn, an;
     Gates gn;
     // what shares a place follows later, so that not all of a block is in registers
-    // (fp32 forward calls: [8, 1024], 16 heads of 128, 197 us for 215; [14, 513], 16
-    // heads of 192, 403 for 454; but of 256, where they spill all the same, 763 for 693)
-    constexpr bool kLater = !KEEP && kShare && RT < 4;
+    // (fp32 forward calls: [8, 1024], 16 heads of 128, 224 us for 234; [14, 513], 16
+    // heads of 192, 384 for 436, of 256 668 for 674)
+    constexpr bool kLater = !KEEP && kShare;
     auto load_later = [&](int start, int len) {
         kn.load(block_rows(in.k, b, hk, start, len), in.k.st, 0, KP, wd.k);
         if (!KEEP) an.load(prep.att, bh * s.T + start, len);
@@ -358,7 +358,7 @@ delta_walk(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaFwd p, Kept 
         __syncthreads();
         if (kLater)
             load_later(start, len);
-        else if (KEEP || !kShare)
+        else
             load(next, nlen);
 
         f32x4 qs[4], ks[4];
@@ -391,7 +391,7 @@ delta_walk(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaFwd p, Kept 
             __syncthreads();  // Q is read
             kn.store(kt, kKPlane, KS);
             __syncthreads();
-            if (kLater) load(next, nlen);
+            load(next, nlen);
             if (works)
 #pragma unroll
                 for (int g = 0; g < KP / 32; ++g) {
@@ -437,7 +437,6 @@ delta_walk(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaFwd p, Kept 
             __syncthreads();  // the inverse is read
             an.store(at);
             __syncthreads();
-            if (!kLater) load(next, nlen);
         }
         if (works) {
             if (!KEEP && p.out) {
@@ -532,9 +531,8 @@ delta_walk_back(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaBwd p, 
     Tile<DT, 16 * kMaxWaves, false> on;
     Rows64 tn, an;
     Gates gn;
-    // what shares a place follows later (of 192, reverse: 1178 us for 1194; of 256 1989
-    // for 1737)
-    constexpr bool kLater = kShare && RT < 4;
+    // what shares a place follows later (fp32 [14, 513], 16 heads of 192, reverse: 1165 us
+    // for 1210; of 256 1712 for 1744)
     auto load_later = [&](int start, int len) {
         tn.load(prep.inv_t, bh * s.T + start, len);
         qn.load(block_rows(in.q, b, hk, start, len), in.q.st, 0, KP, wd.k);
@@ -544,7 +542,7 @@ delta_walk_back(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaBwd p, 
         kn.load(block_rows(in.k, b, hk, start, len), in.k.st, 0, KP, wd.k);
         on.load(block_rows(go, b, h, start, len), go.st, v0, waves * 16, wd.v);
         an.load(prep.att_t, bh * s.T + start, len);
-        if (!kLater) load_later(start, len);
+        if (!kShare) load_later(start, len);
     };
     const int count = blocks.count(b);
     int to, n;
@@ -570,9 +568,9 @@ delta_walk_back(DeltaShape s, DeltaIn in, Blocks blocks, Prep prep, DeltaBwd p, 
             qn.store(qt, kKPlane, KS);
         }
         __syncthreads();
-        if (kLater)
+        if (kShare)
             load_later(start, len);
-        else if (!kShare)
+        else
             load(prev, plen);
 
         f32x4 x[4], po[4], en[4];
