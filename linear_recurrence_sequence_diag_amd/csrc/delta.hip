@@ -149,7 +149,7 @@ hipError_t run_copies(const RowCopies& c, int64_t T, int dtype, hipStream_t st) 
 // A workgroup has COLS columns of a head; its threads hold CV columns of every
 // RG-th row in registers between the sums and the update.  Bytes of the state
 // bound it (bf16, 32 rows of 20 heads of 128 by 128: 20.5 us for 84 MB, 4.1 TB/s;
-// fp32, one row of 8 heads of 64 by 64: 6.2 us, a launch and one round of loads).
+// fp32, one row of 8 heads of 64 by 64: 6.1 us, a launch and one round of loads).
 // Every thread writes the elements that it read, so the new state may replace the
 // old one.
 namespace delta {

@@ -21,9 +21,9 @@
 // with tokens are spread over the wavefronts a tile of 16x16 at a time while the
 // same columns are there.
 //
-// bf16 [8, 2048], 20 heads of 128 over 10 keys: 577 us, of which the matrix cores
-// are busy for 103 (592 with both sums over heads in memory, 420 MB more to write
-// and read).  One workgroup a compute unit (LDS and registers allow no second one),
+// bf16 [8, 2048], 20 heads of 128 over 10 keys: 566 us, of which the matrix cores
+// are busy for 103 (with both sums over heads in memory, 210 MB more to write and
+// read, it takes 15 us more).  One workgroup a compute unit (LDS and registers allow no second one),
 // whose two wavefronts a SIMD wait half of the time.  The next head's operands
 // loaded ahead cost registers that spill (786 us), as K and Q kept in LDS for all
 // heads (670).

@@ -11,10 +11,10 @@
 // floats, so a difference of two large sums keeps its small decays.
 //
 // Blocks are independent, three workgroups a compute unit (bf16), and what bounds
-// them is memory: bf16 [8, 2048], 20 heads of 128 with resets, 100 us for 192 MB
-// read and 129 MB written; for the backward pass, which takes the transposed
-// operands too and in three planes, 196 us, 275 MB read and 465 MB written (a
-// unit's wavefronts wait for loads two thirds of the time).
+// them is memory: bf16 [8, 2048], 20 heads of 128 with resets, 110 us for 194 MB
+// read and 191 MB written; for the backward pass, which takes the transposed
+// operands too, 200 us, 284 MB read and 460 MB written (a unit's wavefronts wait
+// for loads 70% of the time).
 #include "delta_tile.hpp"
 #include "delta_ws.hpp"
 

@@ -14,10 +14,10 @@
 // beyond the columns only load.
 //
 // What bounds it is the length of a block's chain of products: bf16 [8, 2048], 20
-// heads of 128 with resets, are 160 workgroups that take 12.3 thousand cycles a
-// block, 205 us, 38 of them matrix instructions with two wavefronts a SIMD; LDS
+// heads of 128 with resets, are 160 workgroups that take 17.3 thousand cycles a
+// block, 288 us, 63 of them matrix instructions with two wavefronts a SIMD; LDS
 // reads and the cutting into planes hardly overlap with these.  The kept walk of the
-// backward pass takes 270 us (485 MB of states and x written), the walk back 358
+// backward pass takes 269 us (485 MB of states and x written), the walk back 365
 // (579 MB).
 #include "delta_tile.hpp"
 #include "delta_ws.hpp"
@@ -93,7 +93,8 @@ struct Tile {
 
 // V or dO of a block in LDS, [token][column], as they are stored: fp32 in one plane
 // leaves room for eight wavefronts' columns beside K's 256 in three (fp32 [14, 513],
-// 16 heads of 256: 693 us a forward call, 929 with four and V in three planes).
+// 16 heads of 256: a forward call of 929 us, with four and V in three planes, took 693
+// with them, and takes 670 now).
 template <int DT, int COLS>
 struct Values {
     static constexpr int kStride = DT == DT_F32 ? 2 * (COLS + 4) : COLS + 8, kSize = kC * kStride;
@@ -227,7 +228,7 @@ __device__ __forceinline__ void triangle(f32x4 (&x)[4], const uint16_t* rows, co
 // column's first such token on (of the triangle that reaches back, up to its last
 // one) an operand is zeros, and the rows that do take it are made NaN afterwards.
 // What rounds to an infinity in bf16 counts as one.  Looking for such tokens is 1 to
-// 3% of a call (bf16 [8, 2048], 20 heads of 128: 367 -> 370 us, reverse 1338 -> 1355),
+// 3% of a call (bf16 [8, 2048], 20 heads of 128: 3 us of 370, reverse 17 of 1320),
 // which without the branches marked as rare is 12%: spills.
 constexpr float kOver = 0x1.ffp127f;
 template <bool LOWER>
@@ -813,9 +814,9 @@ struct Spread {
 
 // Columns are spread evenly over the workgroups of a head, on more of them than
 // need be where that leaves compute units idle: a block then takes less time
-// (us of a call, 8, 4, 2 and 1 wavefronts a workgroup: bf16 [1, 32768, 8 heads of
-// 128] 2505, 1718, 1611, 1583; fp32 [4, 1023, 16 heads of 64] reverse 282, 282,
-// 267, 264; but of 160 heads bf16 [8, 2048] 292, 342, 438, 660).
+// (us of a call without parts, 8, 4, 2 and 1 wavefronts a workgroup: bf16 [1, 32768,
+// 8 heads of 128] 3438, 2252, 2218, 2217; fp32 [4, 1023, 16 heads of 64] reverse 276,
+// 276, 270, 269; but of 160 heads bf16 [8, 2048] 336, 394, 529, 809).
 Spread spread(const DeltaShape& s, int tiles, int parts, int most) {
     const int64_t heads = s.B * s.H * parts, spare = kComputeUnits / heads;
     int groups = (tiles + most - 1) / most;

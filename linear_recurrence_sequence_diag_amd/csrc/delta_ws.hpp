@@ -23,11 +23,11 @@ constexpr int kComputeUnits = 256;
 // once, of three blocks or more each; joining them takes a step for each part, so
 // there are no more than twice the root of the blocks.  us of a forward and of a
 // reverse call without parts and with them, B = 1, K = V = 128, bf16:
-//   8 heads, T = 800      54, 157     49, 141
-//   8 heads, T = 2048    111, 305     71, 191
-//   8 heads, T = 32768  1577, 5126   331, 1375
-//  32 heads, T = 1024     66, 219     64, 215
-//  43 heads, T = 2048    130, 560    151, 569 (in five parts, whose maps find no room at once)
+//   8 heads, T = 800      70, 160     57, 142
+//   8 heads, T = 2048    150, 314     80, 188
+//   8 heads, T = 32768  2216, 5232   409, 1325
+//  32 heads, T = 1024     87, 221     71, 207
+//  43 heads, T = 2048    169, 548    177, 520 (in five parts, whose maps find no room at once)
 inline int sequence_parts(const DeltaShape& d) {
     const int64_t units = d.B * d.H * ((d.K + d.V + 127) / 128), blocks = (d.T + kC - 1) / kC;
     int64_t parts = kComputeUnits / units < blocks / 3 ? kComputeUnits / units : blocks / 3;
@@ -89,7 +89,7 @@ struct Layout {
 struct Kept {
     float *x, *r;   // [B, H, T]: x of the forward, and the gradient of beta (x's right side)
     float *s, *ds;  // [B, H, slots, K]: states that enter blocks, gradients that leave them
-    f32x4* sums;    // a workgroup's 512 x 8: of q's and k's gradients over the heads that share a q and k so far
+    f32x4* sums;    // a workgroup's kGradThreads x 8: of q's and k's gradients over the heads that share a q and k so far
 };
 
 // Between the parts of a sequence, in fp32, [B, H, parts]: the state that enters a
