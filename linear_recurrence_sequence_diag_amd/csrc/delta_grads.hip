@@ -23,10 +23,10 @@
 //
 // bf16 [8, 2048], 20 heads of 128 over 10 keys: 566 us, of which the matrix cores
 // are busy for 103 (with both sums over heads in memory, 210 MB more to write and
-// read, it takes 15 us more).  One workgroup a compute unit (LDS and registers allow no second one),
-// whose two wavefronts a SIMD wait half of the time.  The next head's operands
-// loaded ahead cost registers that spill (786 us), as K and Q kept in LDS for all
-// heads (670).
+// read, it takes 15 us more).  One workgroup a compute unit (LDS and registers allow
+// no second one), whose two wavefronts a SIMD wait half of the time.  The next head's
+// operands loaded ahead cost registers that spill (786 us), as K and Q kept in LDS for
+// all heads (670).
 #include "delta_tile.hpp"
 #include "delta_ws.hpp"
 

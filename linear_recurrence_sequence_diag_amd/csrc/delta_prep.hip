@@ -256,6 +256,10 @@ __global__ void __launch_bounds__(kThreads, DT == DT_BF16 ? 3 : 2) delta_prep(De
                         y = q >= lane ? z : y;  // the rows before the column's own are zeros
                     }
                     Ti[r * kS + lane] = y;
+                    if (__any(!(fabsf(y) < INFINITY))) {  // then no row behind it is finite
+                        for (int i = r + 1; i < kC; ++i) Ti[i * kS + lane] = lane <= i ? __builtin_nanf("") : 0.0f;
+                        break;
+                    }
                 }
             __syncthreads();
         }
